@@ -1,5 +1,7 @@
 """vcoll: virtual-rank collectives (reduce-scatter, allgather, allreduce,
-tensor-fusion pack/unpack) on one GB300 GPU.
+tensor-fusion pack/unpack) on one GB300 GPU, and the layer operators of a
+rank whose gradients they reduce (embedding, layer norm, 8-bit activations:
+``layers.py``).
 
 This module is a thin ctypes binding over ``libvcoll.so`` (C ABI in
 ``include/vcoll.h``).  It only marshals arguments -- device pointers from
@@ -586,3 +588,25 @@ def fusion_allreduce(tensors, outs, fused, op="avg", ring_order=False,
     the same tensors: FusionBufferPlan marshals the pointers once.)"""
     FusionBufferPlan(tensors, outs, fused, op, ring_order, threshold_bytes)(stream)
     return outs
+
+
+# ---------------------------------------------------------- layer operators
+# (bound on first use: this module itself does not import torch)
+
+_LAYERS = {"Checkpoint8", "checkpoint8", "checkpoint8_restore", "embedding", "embedding_backward",
+           "embedding_workspace_bytes", "layer_norm", "layer_norm_backward",
+           "layer_norm_backward_checkpoint8", "layer_norm_checkpoint8",
+           "layer_norm_workspace_bytes", "vcoll_checkpoint8", "vcoll_checkpoint8_restore",
+           "vcoll_embedding", "vcoll_embedding_backward",
+           "vcoll_embedding_backward_workspace_bytes", "vcoll_layer_norm",
+           "vcoll_layer_norm_backward", "vcoll_layer_norm_backward_checkpoint8",
+           "vcoll_layer_norm_checkpoint8", "vcoll_layer_norm_workspace_bytes", "I32", "I64",
+           "CHECKPOINT8_BLOCK"}
+
+
+def __getattr__(name):
+    if name not in _LAYERS:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import layers
+    value = globals()[name] = getattr(layers, name)
+    return value

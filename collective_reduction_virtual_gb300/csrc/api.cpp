@@ -1269,6 +1269,27 @@ namespace vcoll {
 // lets entry points defined in other translation units report a failure
 // through vcoll_last_error()
 int report_error(int status, const char* message) { return fail(status, "%s", message); }
+
+int device_sms(int* sms) {
+  int dev = 0;
+  return current_device(&dev, sms);
+}
+
+int launch_grid(const void* fn, int64_t gx, int64_t gy, int threads, size_t smem, void* params,
+                void* stream) {
+  void* args[] = {params};
+  if (smem > 48 * 1024) {
+    int rc = allow_dynamic_smem(fn, smem);
+    if (rc) return rc;
+  }
+  const cudaError_t e = launch_pdl(fn, dim3((unsigned)gx, (unsigned)gy), dim3((unsigned)threads),
+                                   args, smem, (cudaStream_t)stream);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return cuda_fail(e, "kernel launch");
+  }
+  return VCOLL_OK;
+}
 }  // namespace vcoll
 
 extern "C" {

@@ -1,0 +1,433 @@
+// Host side of the layer operators declared in include/vcoll.h: argument
+// checks, choice of kernel and launches.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdarg>
+#include <cstdio>
+
+#include "layers_internal.h"
+
+using namespace vcoll;
+
+namespace {
+
+int fail(int status, const char* fmt, ...) {
+  char msg[256];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(msg, sizeof(msg), fmt, ap);
+  va_end(ap);
+  return report_error(status, msg);
+}
+
+#define VCOLL_TRY(expr)   \
+  do {                    \
+    const int rc_ = expr; \
+    if (rc_) return rc_;  \
+  } while (0)
+
+constexpr int64_t kMaxExtent = 0x7FFFFFFE;
+
+int elem_size(int dtype) { return dtype == VCOLL_F32 ? 4 : dtype == VCOLL_BF16 ? 2 : 0; }
+
+int check_type(int dtype, const char* what) {
+  if (!elem_size(dtype)) return fail(VCOLL_ERR_INVALID_TYPE, "unknown %s %d", what, dtype);
+  return VCOLL_OK;
+}
+
+int check_extent(int64_t v, const char* what) {
+  if (v < 0) return fail(VCOLL_ERR_INVALID_ARG, "%s = %lld < 0", what, (long long)v);
+  if (v > kMaxExtent)
+    return fail(VCOLL_ERR_UNSUPPORTED, "%s = %lld is above %lld", what, (long long)v,
+                (long long)kMaxExtent);
+  return VCOLL_OK;
+}
+
+// One operand of a call: rows x cols elements of es bytes, ld elements apart.
+struct Operand {
+  const char* name;
+  const void* ptr;
+  int64_t rows, cols, ld;
+  int es;
+  bool out;
+  const void* alias;  // the operand that it may coincide with, or NULL
+};
+
+int check_operand(const Operand& o) {
+  if (o.rows == 0 || o.cols == 0) return VCOLL_OK;
+  if (!o.ptr) return fail(VCOLL_ERR_INVALID_ARG, "%s is NULL", o.name);
+  if ((uint64_t)o.ptr % o.es)
+    return fail(VCOLL_ERR_INVALID_ARG, "%s is not aligned to the element size", o.name);
+  if (o.ld < o.cols)
+    return fail(VCOLL_ERR_INVALID_ARG, "%s: row stride %lld < %lld columns", o.name,
+                (long long)o.ld, (long long)o.cols);
+  if (o.ld > (INT64_MAX / 8 - o.cols) / o.rows)  // the byte extent must fit 64 bits
+    return fail(VCOLL_ERR_INVALID_ARG, "%s: row stride %lld is out of range", o.name,
+                (long long)o.ld);
+  return VCOLL_OK;
+}
+
+bool overlap(const Operand& a, const Operand& b) {
+  const uint64_t pa = (uint64_t)a.ptr, pb = (uint64_t)b.ptr;
+  const uint64_t wa = (uint64_t)a.cols * a.es, wb = (uint64_t)b.cols * b.es;
+  const uint64_t sa = (uint64_t)a.ld * a.es, sb = (uint64_t)b.ld * b.es;
+  const uint64_t ea = pa + (uint64_t)(a.rows - 1) * sa + wa;
+  const uint64_t eb = pb + (uint64_t)(b.rows - 1) * sb + wb;
+  if (ea <= pb || eb <= pa) return false;
+  if (sa == sb && a.rows > 1 && b.rows > 1) {  // column ranges of the same wider rows
+    const uint64_t d = pb >= pa ? (pb - pa) % sa : (sa - (pa - pb) % sa) % sa;
+    return d < wa || d + wb > sa;
+  }
+  return true;
+}
+
+// Pointers, strides, and that no output overlaps another operand.
+int check_operands(const Operand* ops, int n) {
+  for (int i = 0; i < n; ++i) VCOLL_TRY(check_operand(ops[i]));
+  for (int i = 0; i < n; ++i)
+    for (int k = i + 1; k < n; ++k) {
+      const Operand &a = ops[i], &b = ops[k];
+      if (!a.ptr || !b.ptr || !a.rows || !b.rows || !a.cols || !b.cols) continue;
+      if (!a.out && !b.out) continue;
+      if (a.ptr == b.ptr && a.ld == b.ld && a.es == b.es && (a.alias == b.ptr || b.alias == a.ptr))
+        continue;
+      if (overlap(a, b))
+        return fail(VCOLL_ERR_INVALID_ARG, "%s overlaps %s", a.name, b.name);
+    }
+  return VCOLL_OK;
+}
+
+int check_workspace(const void* workspace, size_t bytes, size_t need) {
+  if (!need) return VCOLL_OK;
+  if (!workspace || bytes < need)
+    return fail(VCOLL_ERR_INVALID_ARG, "the workspace holds %zu bytes, %zu are needed",
+                workspace ? bytes : (size_t)0, need);
+  if ((uint64_t)workspace % 256)
+    return fail(VCOLL_ERR_INVALID_ARG, "the workspace is not 256-byte aligned");
+  return VCOLL_OK;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// CTAs for `items` pieces of work of which a CTA does `per` at a time: all of
+// them at once, at most `waves` CTAs per SM, each looping over its share.
+int grid_for(int64_t items, int64_t per, int waves, int64_t* grid) {
+  int sms = 0;
+  VCOLL_TRY(device_sms(&sms));
+  *grid = std::max<int64_t>(1, std::min<int64_t>(ceil_div(items, per), (int64_t)sms * waves));
+  return VCOLL_OK;
+}
+
+constexpr int kWarps = kRowThreads / 32;
+
+size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+}  // namespace
+
+extern "C" {
+
+int vcoll_embedding(const void* tokens, int index_type, int64_t N, const void* table,
+                    int64_t table_ld, int64_t V, int64_t D, float scale, void* out,
+                    int64_t out_ld, int dtype, void* stream) {
+  VCOLL_TRY(check_type(dtype, "dtype"));
+  if (index_type != VCOLL_I32 && index_type != VCOLL_I64)
+    return fail(VCOLL_ERR_INVALID_TYPE, "unknown index type %d", index_type);
+  VCOLL_TRY(check_extent(N, "N"));
+  VCOLL_TRY(check_extent(V, "V"));
+  VCOLL_TRY(check_extent(D, "D"));
+  const int es = elem_size(dtype);
+  const Operand ops[] = {
+      {"tokens", tokens, D ? N : 0, 1, 1, index_type == VCOLL_I64 ? 8 : 4, false, nullptr},
+      {"table", table, N ? V : 0, D, table_ld, es, false, nullptr},
+      {"out", out, N, D, out_ld, es, true, nullptr}};
+  VCOLL_TRY(check_operands(ops, 3));
+  if (!N || !D) return VCOLL_OK;
+  EmbedParams p = {};
+  p.tokens = tokens;
+  p.table = table;
+  p.out = out;
+  p.N = N;
+  p.V = V;
+  p.D = D;
+  p.table_ld = table_ld;
+  p.out_ld = out_ld;
+  p.scale = scale;
+  p.idx64 = index_type == VCOLL_I64;
+  int64_t grid;
+  VCOLL_TRY(grid_for(N, kWarps, 32, &grid));
+  return launch_grid(embed_kernel(dtype), grid, 1, kRowThreads, 0, &p, stream);
+}
+
+size_t vcoll_embedding_backward_workspace_bytes(int64_t N, int64_t V, int64_t D) {
+  if (N <= 0 || V <= 0 || D <= 0) return 0;
+  return 4 * align256((size_t)N * sizeof(uint32_t));
+}
+
+int vcoll_embedding_backward(const void* grad, int64_t grad_ld, int dtype, const void* tokens,
+                             int index_type, int64_t N, int64_t V, int64_t D, float scale,
+                             const void* base, int64_t base_ld, void* table_grad,
+                             int64_t table_ld, int table_dtype, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  VCOLL_TRY(check_type(dtype, "dtype"));
+  VCOLL_TRY(check_type(table_dtype, "table dtype"));
+  if (index_type != VCOLL_I32 && index_type != VCOLL_I64)
+    return fail(VCOLL_ERR_INVALID_TYPE, "unknown index type %d", index_type);
+  VCOLL_TRY(check_extent(N, "N"));
+  VCOLL_TRY(check_extent(V, "V"));
+  VCOLL_TRY(check_extent(D, "D"));
+  const int es = elem_size(dtype), ts = elem_size(table_dtype);
+  const size_t need = vcoll_embedding_backward_workspace_bytes(N, V, D);
+  const Operand ops[] = {
+      {"tokens", tokens, V && D ? N : 0, 1, 1, index_type == VCOLL_I64 ? 8 : 4, false, nullptr},
+      {"grad", grad, V ? N : 0, D, grad_ld, es, false, nullptr},
+      {"base", base, base ? V : 0, D, base_ld, ts, false, nullptr},
+      {"table_grad", table_grad, V, D, table_ld, ts, true, base},
+      {"workspace", workspace, need ? 1 : 0, (int64_t)need, (int64_t)need, 1, true, nullptr}};
+  VCOLL_TRY(check_operands(ops, 4));
+  VCOLL_TRY(check_workspace(workspace, workspace_bytes, need));
+  VCOLL_TRY(check_operands(ops, 5));
+  if (!V || !D) return VCOLL_OK;
+  const bool in_place = base && base == table_grad;
+  if (!N && in_place) return VCOLL_OK;
+  EmbedGradParams p = {};
+  p.tokens = tokens;
+  p.grad = grad;
+  p.base = base;
+  p.out = table_grad;
+  const size_t part = align256((size_t)N * sizeof(uint32_t));
+  for (int k = 0; k < 2 && N; ++k) {
+    p.key[k] = (uint32_t*)((char*)workspace + (size_t)(2 * k) * part);
+    p.pos[k] = (uint32_t*)((char*)workspace + (size_t)(2 * k + 1) * part);
+  }
+  p.N = N;
+  p.V = V;
+  p.D = D;
+  p.grad_ld = grad_ld;
+  p.base_ld = base_ld;
+  p.out_ld = table_ld;
+  p.scale = scale;
+  p.idx64 = index_type == VCOLL_I64;
+  p.in_place = in_place;
+  int bits = 1;  // of keys 0 .. V
+  while (bits < 31 && (V >> bits)) ++bits;
+  p.passes = (int)ceil_div(bits, kSortMaxBits);
+  p.bits = std::max(5, (int)ceil_div(bits, p.passes));
+  if (N) {
+    const size_t smem = ((size_t)1 << kSortMaxBits) * (kSortThreads / 32) * sizeof(uint32_t);
+    VCOLL_TRY(launch_grid(embed_sort_kernel(), 1, 1, kSortThreads, smem, &p, stream));
+  }
+  int64_t grid;
+  VCOLL_TRY(grid_for(V, kWarps, 32, &grid));
+  return launch_grid(embed_grad_kernel(dtype, table_dtype), grid, 1, kRowThreads, 0, &p, stream);
+}
+
+// x, y (or grad, dx) and the 8-bit operands of the layer norm entry points
+static int norm_checks(int64_t N, int64_t D, int dtype, int weight_dtype) {
+  VCOLL_TRY(check_type(dtype, "dtype"));
+  VCOLL_TRY(check_type(weight_dtype, "weight dtype"));
+  VCOLL_TRY(check_extent(N, "N"));
+  return check_extent(D, "D");
+}
+
+static int check_codes(const void* codes, int64_t codes_ld, int64_t N, int64_t D) {
+  if (!N || !D) return VCOLL_OK;
+  if ((uint64_t)codes % 16 || codes_ld % 16)
+    return fail(VCOLL_ERR_INVALID_ARG, "codes and their row stride must be multiples of 16 bytes");
+  return VCOLL_OK;
+}
+
+// columns of a row of codes that are written
+static int64_t codes_cols(int64_t D) { return (D + 15) / 16 * 16; }
+static int64_t blocks_of(int64_t D) { return ceil_div(D, VCOLL_CHECKPOINT8_BLOCK); }
+
+static int norm_forward(const void* x, int64_t x_ld, const void* weight, const void* bias,
+                        int weight_dtype, int64_t N, int64_t D, float eps, void* y, int64_t y_ld,
+                        float* mean, float* rstd, bool keep, int8_t* codes, int64_t codes_ld,
+                        float* scales, int dtype, void* stream) {
+  VCOLL_TRY(norm_checks(N, D, dtype, weight_dtype));
+  const int es = elem_size(dtype), ws = elem_size(weight_dtype);
+  const int64_t K = keep ? N : 0, B = blocks_of(D);
+  const Operand ops[] = {{"x", x, N, D, x_ld, es, false, nullptr},
+                         {"weight", weight, weight && N ? 1 : 0, D, D, ws, false, nullptr},
+                         {"bias", bias, bias && N ? 1 : 0, D, D, ws, false, nullptr},
+                         {"y", y, N, D, y_ld, es, true, x},
+                         {"mean", mean, mean && D ? 1 : 0, N, N, 4, true, nullptr},
+                         {"rstd", rstd, rstd && D ? 1 : 0, N, N, 4, true, nullptr},
+                         {"codes", codes, K, codes_cols(D), codes_ld, 1, true, nullptr},
+                         {"scales", scales, K, B, B, 4, true, nullptr}};
+  if (keep) VCOLL_TRY(check_codes(codes, codes_ld, N, D));
+  VCOLL_TRY(check_operands(ops, 8));
+  if (!N || !D) return VCOLL_OK;
+  NormParams p = {};
+  p.x = x;
+  p.weight = weight;
+  p.bias = bias;
+  p.y = y;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.codes = keep ? codes : nullptr;
+  p.scales = scales;
+  p.N = N;
+  p.D = D;
+  p.x_ld = x_ld;
+  p.y_ld = y_ld;
+  p.codes_ld = codes_ld;
+  p.eps = eps;
+  p.wbf16 = weight_dtype == VCOLL_BF16;
+  int64_t grid;
+  VCOLL_TRY(grid_for(N, 1, 32, &grid));
+  return launch_grid(norm_kernel(dtype), grid, 1, kRowThreads, 0, &p, stream);
+}
+
+static int norm_backward(const void* grad, int64_t grad_ld, const void* x, int64_t x_ld,
+                         const int8_t* codes, int64_t codes_ld, const float* scales,
+                         const float* mean, const float* rstd, const void* weight,
+                         int weight_dtype, int64_t N, int64_t D, void* dx, int64_t dx_ld,
+                         void* dweight, void* dbias, bool kept, int dtype, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  VCOLL_TRY(norm_checks(N, D, dtype, weight_dtype));
+  const int es = elem_size(dtype), ws = elem_size(weight_dtype);
+  const int64_t K = kept ? N : 0, X = kept ? 0 : N, B = blocks_of(D);
+  const bool alias_grad = dx == grad;
+  const size_t need = vcoll_layer_norm_workspace_bytes(N, D);
+  const Operand ops[] = {
+      {"grad", grad, N, D, grad_ld, es, false, nullptr},
+      {"x", x, X, D, x_ld, es, false, nullptr},
+      {"mean", mean, X && D ? 1 : 0, N, N, 4, false, nullptr},
+      {"rstd", rstd, N && D ? 1 : 0, N, N, 4, false, nullptr},
+      {"codes", codes, K, D, codes_ld, 1, false, nullptr},
+      {"scales", scales, K, B, B, 4, false, nullptr},
+      {"weight", weight, weight && N ? 1 : 0, D, D, ws, false, nullptr},
+      {"dx", dx, dx ? N : 0, D, dx_ld, es, true, alias_grad ? grad : x},
+      {"dweight", dweight, dweight ? 1 : 0, D, D, ws, true, nullptr},
+      {"dbias", dbias, dbias ? 1 : 0, D, D, ws, true, nullptr},
+      {"workspace", workspace, need ? 1 : 0, (int64_t)need, (int64_t)need, 1, true, nullptr}};
+  if (kept) VCOLL_TRY(check_codes(codes, codes_ld, N, D));
+  VCOLL_TRY(check_operands(ops, 10));
+  VCOLL_TRY(check_workspace(workspace, workspace_bytes, need));
+  VCOLL_TRY(check_operands(ops, 11));
+  if (!D) return VCOLL_OK;
+  NormParams p = {};
+  p.x = kept ? nullptr : x;
+  p.grad = grad;
+  p.weight = weight;
+  p.y = dx;
+  p.mean = const_cast<float*>(mean);
+  p.rstd = const_cast<float*>(rstd);
+  p.codes = const_cast<int8_t*>(codes);
+  p.scales = const_cast<float*>(scales);
+  p.dweight = dweight;
+  p.dbias = dbias;
+  p.part = (float*)workspace;
+  p.N = N;
+  p.D = D;
+  p.x_ld = x_ld;
+  p.grad_ld = grad_ld;
+  p.y_ld = dx_ld;
+  p.codes_ld = codes_ld;
+  p.wbf16 = weight_dtype == VCOLL_BF16;
+  if (dweight || dbias)
+    VCOLL_TRY(launch_grid(norm_wgrad_kernel(dtype), ceil_div(D, 32), 1, kRowThreads, 0, &p, stream));
+  if (!dx || !N) return VCOLL_OK;
+  int64_t grid;
+  VCOLL_TRY(grid_for(N, 1, 32, &grid));
+  return launch_grid(norm_grad_kernel(dtype), grid, 1, kRowThreads, 0, &p, stream);
+}
+
+int vcoll_layer_norm(const void* x, int64_t x_ld, const void* weight, const void* bias,
+                     int weight_dtype, int64_t N, int64_t D, float eps, void* y, int64_t y_ld,
+                     float* mean, float* rstd, int dtype, void* stream) {
+  return norm_forward(x, x_ld, weight, bias, weight_dtype, N, D, eps, y, y_ld, mean, rstd, false,
+                      nullptr, 0, nullptr, dtype, stream);
+}
+
+int vcoll_layer_norm_checkpoint8(const void* x, int64_t x_ld, const void* weight,
+                                 const void* bias, int weight_dtype, int64_t N, int64_t D,
+                                 float eps, void* y, int64_t y_ld, float* rstd, int8_t* codes,
+                                 int64_t codes_ld, float* scales, int dtype, void* stream) {
+  return norm_forward(x, x_ld, weight, bias, weight_dtype, N, D, eps, y, y_ld, nullptr, rstd, true,
+                      codes, codes_ld, scales, dtype, stream);
+}
+
+size_t vcoll_layer_norm_workspace_bytes(int64_t N, int64_t D) {
+  (void)N;
+  (void)D;
+  return 0;
+}
+
+int vcoll_layer_norm_backward(const void* grad, int64_t grad_ld, const void* x, int64_t x_ld,
+                              const float* mean, const float* rstd, const void* weight,
+                              int weight_dtype, int64_t N, int64_t D, void* dx, int64_t dx_ld,
+                              void* dweight, void* dbias, int dtype, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  return norm_backward(grad, grad_ld, x, x_ld, nullptr, 0, nullptr, mean, rstd, weight,
+                       weight_dtype, N, D, dx, dx_ld, dweight, dbias, false, dtype, workspace,
+                       workspace_bytes, stream);
+}
+
+int vcoll_layer_norm_backward_checkpoint8(const void* grad, int64_t grad_ld, const int8_t* codes,
+                                          int64_t codes_ld, const float* scales,
+                                          const float* rstd, const void* weight, int weight_dtype,
+                                          int64_t N, int64_t D, void* dx, int64_t dx_ld,
+                                          void* dweight, void* dbias, int dtype, void* workspace,
+                                          size_t workspace_bytes, void* stream) {
+  return norm_backward(grad, grad_ld, nullptr, 0, codes, codes_ld, scales, nullptr, rstd, weight,
+                       weight_dtype, N, D, dx, dx_ld, dweight, dbias, true, dtype, workspace,
+                       workspace_bytes, stream);
+}
+
+int vcoll_checkpoint8(const void* x, int64_t x_ld, int64_t N, int64_t D, int8_t* codes,
+                      int64_t codes_ld, float* scales, int dtype, void* stream) {
+  VCOLL_TRY(norm_checks(N, D, dtype, VCOLL_F32));
+  const int64_t B = blocks_of(D);
+  const Operand ops[] = {{"x", x, N, D, x_ld, elem_size(dtype), false, nullptr},
+                         {"codes", codes, N, codes_cols(D), codes_ld, 1, true, nullptr},
+                         {"scales", scales, N, B, B, 4, true, nullptr}};
+  VCOLL_TRY(check_codes(codes, codes_ld, N, D));
+  VCOLL_TRY(check_operands(ops, 3));
+  if (!N || !D) return VCOLL_OK;
+  PackParams p = {};
+  p.x = x;
+  p.codes = codes;
+  p.scales = scales;
+  p.N = N;
+  p.D = D;
+  p.x_ld = x_ld;
+  p.codes_ld = codes_ld;
+  int64_t grid;
+  VCOLL_TRY(grid_for(N * B, kWarps, 32, &grid));
+  return launch_grid(pack8_kernel(dtype), grid, 1, kRowThreads, 0, &p, stream);
+}
+
+int vcoll_checkpoint8_restore(const int8_t* codes, int64_t codes_ld, const float* scales,
+                              const void* weight, const void* bias, int weight_dtype, int64_t N,
+                              int64_t D, void* out, int64_t out_ld, int dtype, void* stream) {
+  VCOLL_TRY(norm_checks(N, D, dtype, weight_dtype));
+  const int ws = elem_size(weight_dtype);
+  const int64_t B = blocks_of(D);
+  const Operand ops[] = {{"codes", codes, N, D, codes_ld, 1, false, nullptr},
+                         {"scales", scales, N, B, B, 4, false, nullptr},
+                         {"weight", weight, weight && N ? 1 : 0, D, D, ws, false, nullptr},
+                         {"bias", bias, bias && N ? 1 : 0, D, D, ws, false, nullptr},
+                         {"out", out, N, D, out_ld, elem_size(dtype), true, nullptr}};
+  VCOLL_TRY(check_codes(codes, codes_ld, N, D));
+  VCOLL_TRY(check_operands(ops, 5));
+  if (!N || !D) return VCOLL_OK;
+  PackParams p = {};
+  p.out = out;
+  p.weight = weight;
+  p.bias = bias;
+  p.codes = const_cast<int8_t*>(codes);
+  p.scales = const_cast<float*>(scales);
+  p.N = N;
+  p.D = D;
+  p.x_ld = out_ld;
+  p.codes_ld = codes_ld;
+  p.wbf16 = weight_dtype == VCOLL_BF16;
+  int64_t grid;
+  VCOLL_TRY(grid_for(N, 1, 32, &grid));
+  return launch_grid(unpack8_kernel(dtype), grid, 1, kRowThreads, 0, &p, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,84 @@
+// Parameters and kernel selectors of the layer operators (embedding, layer
+// norm, 8-bit activations), shared by their host entry points (layers.cpp)
+// and kernels.  Not part of the public ABI.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include "vcoll_internal.h"
+
+namespace vcoll {
+
+constexpr int kRowThreads = 256;  // threads of a CTA that works on rows
+
+struct EmbedParams {
+  const void* tokens;
+  const void* table;
+  void* out;
+  int64_t N, V, D;
+  int64_t table_ld, out_ld;
+  float scale;
+  int idx64;
+};
+
+// The gradient's tokens are sorted by (token, position) with a stable LSD
+// radix sort; tokens outside [0, V) sort as V, behind all others.
+constexpr int kSortThreads = 1024;
+constexpr int kSortMaxBits = 9;  // digit width
+struct EmbedGradParams {
+  const void* tokens;
+  const void* grad;
+  const void* base;  // NULL: zeros
+  void* out;
+  uint32_t* key[2];  // ping-pong of the sort: N keys and N positions each
+  uint32_t* pos[2];
+  int64_t N, V, D;
+  int64_t grad_ld, base_ld, out_ld;
+  float scale;
+  int idx64;
+  int in_place;  // base is out
+  int passes, bits;
+};
+
+struct NormParams {
+  const void* x;       // N x D, or NULL: h comes from codes and scales
+  const void* grad;    // backward only
+  const void* weight;  // NULL: ones
+  const void* bias;    // NULL: zeros
+  void* y;             // forward: y; backward: dx (may be NULL)
+  float* mean;
+  float* rstd;
+  int8_t* codes;  // forward: kept 8-bit h (or NULL); backward: where h comes from
+  float* scales;
+  void* dweight;
+  void* dbias;
+  float* part;  // backward workspace
+  int64_t N, D;
+  int64_t x_ld, grad_ld, y_ld, codes_ld;
+  float eps;
+  int wbf16;  // weight, bias, dweight, dbias are bf16
+};
+
+struct PackParams {
+  const void* x;
+  void* out;
+  const void* weight;
+  const void* bias;
+  int8_t* codes;
+  float* scales;
+  int64_t N, D;
+  int64_t x_ld, codes_ld;  // x_ld: of x or out
+  int wbf16;
+};
+
+const void* embed_kernel(int dtype);
+const void* embed_sort_kernel();
+const void* embed_grad_kernel(int dtype, int table_dtype);
+const void* norm_kernel(int dtype);
+const void* norm_grad_kernel(int dtype);
+const void* norm_wgrad_kernel(int dtype);
+const void* pack8_kernel(int dtype);
+const void* unpack8_kernel(int dtype);
+
+}  // namespace vcoll

@@ -240,6 +240,15 @@ const void* selftest_timeout_kernel();
 // Sets the thread-local message vcoll_last_error() returns; returns status.
 int report_error(int status, const char* message);
 
+// Launch of one kernel whose only parameter is the struct at `params`, with
+// programmatic stream serialization (the kernel starts with pdl_enter).
+// smem: dynamic shared memory, always the same for one kernel when it is
+// above 48 KB.  Returns a status with its message set.
+int launch_grid(const void* fn, int64_t gx, int64_t gy, int threads, size_t smem, void* params,
+                void* stream);
+// SM count of the current device.
+int device_sms(int* sms);
+
 // Kernel selection (function pointers for cudaLaunchKernel).  W_t is the
 // compile-time rank count (2, 4, 8, 16) or 0 for the runtime-W kernels; vec
 // selects the 16-byte vector path.

@@ -333,6 +333,133 @@ int vcoll_sparse_allreduce_noalloc(const void* const* in, void* const* out, void
                                    int W, int64_t n, float threshold, int topk, int64_t* nnz,
                                    void* stream);
 
+/*
+ * Layer operators: the memory-bound ends of a rank's training step, whose
+ * weight gradients are what the collectives above reduce.  Each call is one
+ * rank's; every gradient output may be a slice of that rank's fusion buffer
+ * (any alignment to the element).  The conventions at the top of this file
+ * hold, and in addition:
+ *  - A matrix of N rows and D columns is a pointer and a row stride `*_ld`
+ *    in elements (>= D; rows may be parts of wider rows); its columns are
+ *    adjacent.  N, D, V up to 2^31 - 2 each; offsets are 64-bit.
+ *  - Buffers of one call may not overlap, except where a call names an
+ *    in-place form; matrices that are different column ranges of the same
+ *    wider rows (equal row strides in bytes) do not overlap.
+ *  - Sums, means and statistics are fp32; a bf16 output is rounded once.
+ *    The order of every sum is fixed by the sizes and the GPU alone, so a
+ *    call repeated on the same inputs gives the same bits.
+ *  - `workspace`: device memory of the size the *_workspace_bytes function
+ *    gives, 256-byte aligned, contents neither expected nor kept; calls that
+ *    share one must not overlap.
+ *  - An empty input (N == 0) still writes what its outputs then are (the
+ *    gradient of no rows is zero); D == 0 enqueues nothing.
+ * The pages have no counterpart of these entry points.
+ */
+
+/* Type of a token index. */
+typedef enum { VCOLL_I32 = 0, VCOLL_I64 = 1 } vcoll_index_t;
+
+/*
+ * Embedding lookup: out[i] = scale * table[tokens[i]] (one fp32 multiply,
+ * rounded to dtype), i < N.  table: V x D, out: N x D, both of dtype.  A token
+ * outside [0, V) -- padding -- gives a row of zeros.
+ */
+int vcoll_embedding(const void* tokens, int index_type, int64_t N, const void* table,
+                    int64_t table_ld, int64_t V, int64_t D, float scale, void* out,
+                    int64_t out_ld, int dtype, void* stream);
+
+/*
+ * Its gradient: table_grad[v] = base[v] + scale * (the sum of grad[i] over the
+ * i with tokens[i] == v).  Every row of table_grad (V x D, of table_dtype) is
+ * written, rows of tokens that do not occur as base or zeros.  base (V x D, of
+ * table_dtype) may be NULL (zeros), or table_grad itself with the same row
+ * stride: then only the rows of tokens that occur are read and written.
+ * Tokens outside [0, V) contribute nothing.  grad: N x D of dtype.  The tokens
+ * are sorted (stably), so each row is summed in the order of i, cut into
+ * parts at places that depend on the sizes alone.
+ */
+size_t vcoll_embedding_backward_workspace_bytes(int64_t N, int64_t V, int64_t D);
+int vcoll_embedding_backward(const void* grad, int64_t grad_ld, int dtype, const void* tokens,
+                             int index_type, int64_t N, int64_t V, int64_t D, float scale,
+                             const void* base, int64_t base_ld, void* table_grad,
+                             int64_t table_ld, int table_dtype, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * Layer norm over the D columns of each row: mean = sum(x) / D,
+ * rstd = 1 / sqrt(sum((x - mean)^2) / D + eps), y = (x - mean) * rstd * weight
+ * + bias.  x, y: N x D of dtype; in place: y == x with the same row stride.
+ * weight, bias: D of weight_dtype, either may be NULL (ones, zeros).  mean,
+ * rstd: N fp32 each, kept for the backward pass; either may be NULL.  A row
+ * holding an infinity or a NaN is NaN throughout, other rows are not touched
+ * by it.
+ */
+int vcoll_layer_norm(const void* x, int64_t x_ld, const void* weight, const void* bias,
+                     int weight_dtype, int64_t N, int64_t D, float eps, void* y, int64_t y_ld,
+                     float* mean, float* rstd, int dtype, void* stream);
+
+/*
+ * Its gradient.  With h = (x - mean) * rstd and g = grad * weight:
+ * dx = rstd * (g - sum(g) / D - h * sum(g * h) / D), dweight = the sum of
+ * grad * h over the rows, dbias = the sum of grad over the rows.  grad, x, dx:
+ * N x D of dtype; in place: dx == grad or dx == x with the same row stride.
+ * weight (NULL: ones), dweight, dbias: D of weight_dtype; dx, dweight and
+ * dbias may each be NULL (not wanted).
+ */
+size_t vcoll_layer_norm_workspace_bytes(int64_t N, int64_t D);
+int vcoll_layer_norm_backward(const void* grad, int64_t grad_ld, const void* x, int64_t x_ld,
+                              const float* mean, const float* rstd, const void* weight,
+                              int weight_dtype, int64_t N, int64_t D, void* dx, int64_t dx_ld,
+                              void* dweight, void* dbias, int dtype, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * Activations kept in 8 bits between the forward and the backward pass.  Each
+ * VCOLL_CHECKPOINT8_BLOCK columns of a row share a scale: with a the block's
+ * largest magnitude, scale = a / 127 and code = x * (127 / a) rounded to the
+ * nearest integer, ties to even (fp32 divisions and product, each rounded
+ * once), standing for code * scale.  A block with a < 2^-100 is kept as zeros
+ * (scale 0); one with an infinity or a NaN has scale NaN, so that it reads
+ * back as NaN.  codes: N x D int8 at a row stride of codes_ld >= D bytes, a
+ * multiple of 16, from a 16-byte aligned address; what lies between D and the
+ * next multiple of 16 is written as zeros.  scales: N x
+ * ceil(D / VCOLL_CHECKPOINT8_BLOCK) fp32, rows adjacent.  x: N x D of dtype.
+ */
+#define VCOLL_CHECKPOINT8_BLOCK 128
+int vcoll_checkpoint8(const void* x, int64_t x_ld, int64_t N, int64_t D, int8_t* codes,
+                      int64_t codes_ld, float* scales, int dtype, void* stream);
+
+/*
+ * What the codes stand for: out = code * scale, or code * scale * weight +
+ * bias where those are given (D of weight_dtype, either may be NULL).  out:
+ * N x D of dtype.
+ */
+int vcoll_checkpoint8_restore(const int8_t* codes, int64_t codes_ld, const float* scales,
+                              const void* weight, const void* bias, int weight_dtype, int64_t N,
+                              int64_t D, void* out, int64_t out_ld, int dtype, void* stream);
+
+/*
+ * Layer norm that keeps its normalised input h = (x - mean) * rstd in 8 bits
+ * on the way (the codes and scales of vcoll_checkpoint8 of h): neither x nor y
+ * has to be kept, vcoll_checkpoint8_restore with the weight and bias gives y
+ * back.  y is computed from the unrounded h.  Other arguments as
+ * vcoll_layer_norm.
+ */
+int vcoll_layer_norm_checkpoint8(const void* x, int64_t x_ld, const void* weight,
+                                 const void* bias, int weight_dtype, int64_t N, int64_t D,
+                                 float eps, void* y, int64_t y_ld, float* rstd, int8_t* codes,
+                                 int64_t codes_ld, float* scales, int dtype, void* stream);
+
+/* The gradient of vcoll_layer_norm from what vcoll_layer_norm_checkpoint8
+ * kept: h is code * scale.  Other arguments as vcoll_layer_norm_backward; in
+ * place: dx == grad with the same row stride. */
+int vcoll_layer_norm_backward_checkpoint8(const void* grad, int64_t grad_ld, const int8_t* codes,
+                                          int64_t codes_ld, const float* scales,
+                                          const float* rstd, const void* weight, int weight_dtype,
+                                          int64_t N, int64_t D, void* dx, int64_t dx_ld,
+                                          void* dweight, void* dbias, int dtype, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+
 /* Device-side error bits, OR-ed into one word per device by the kernels.
  * The staged kernels bound every wait on their shared-memory barriers (2 s of
  * wall-clock time); a wait that gives up records VCOLL_DEVICE_ERR_TIMEOUT and
