@@ -1,161 +1,487 @@
 // Embedding lookup and its gradient.
 #include "device_common.cuh"
 #include "layers_internal.h"
+#include "row_access.cuh"
 
 namespace vcoll {
 
+// A row is taken by p.row_warps adjacent warps of a CTA (a power of two), each
+// with kLookup accesses of 16 bytes per lane in flight at a time: the table's
+// rows arrive in pieces of 2 KB.
+template <typename T, int A>
+__global__ void __launch_bounds__(kRowThreads) vc_embed(const __grid_constant__ EmbedParams p) {
+  pdl_enter();
+  constexpr int E = kLane<T>, G = E / A * kLookup;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t i = (int64_t)blockIdx.x * ((kRowThreads / 32) >> p.row_shift) + (warp >> p.row_shift);
+  if (i >= p.N) return;
+  const int64_t t = token_at(p.tokens, p.idx64, i);
+  const bool inside = t >= 0 && t < p.V;
+  const char* from = elem_at<T>(p.table, inside ? t * p.table_ld : 0);
+  char* to = elem_at<T>(p.out, i * p.out_ld);
+  const int64_t step = (int64_t)(kLookup * 32 * E) << p.row_shift;
+  for (int64_t c0 = (warp & ((1 << p.row_shift) - 1)) * (kLookup * 32 * E) + lane * A; c0 < p.D; c0 += step) {
+    Raw<T, A> r[G];
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      if (inside && c0 + j * 32 * A < p.D) r[j].load(elem_at<T>(from, c0 + j * 32 * A));
+      else r[j].zero();
+    }
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      if (c0 + j * 32 * A >= p.D) break;
+      float f[A];
+      r[j].widen(f);
+#pragma unroll
+      for (int a = 0; a < A; ++a) f[a] = __fmul_rn(f[a], p.scale);
+      Raw<T, A> o;
+      o.narrow(f);
+      o.store_stream(elem_at<T>(to, c0 + j * 32 * A));
+    }
+  }
+}
+
+// ------------------------------------------------------ sorting the tokens
+// Stable LSD radix sort of the tokens' (key, position) pairs.  A CTA sorts a
+// tile of the array by one digit: each warp owns a contiguous part of the
+// tile and counts its digits; the counts, scanned over warps and digits, give
+// each warp its places; and it walks its part again in order, the lanes of one
+// digit taking the next places (match) in lane order.
+
 namespace {
 
-__device__ __forceinline__ int64_t token_at(const void* tokens, int idx64, int64_t i) {
-  return idx64 ? static_cast<const int64_t*>(tokens)[i] : static_cast<const int32_t*>(tokens)[i];
+constexpr int kSortWarps = kSortThreads / 32;
+
+__device__ __forceinline__ uint32_t sort_key(const EmbedGradParams& p, int pass, int64_t i) {
+  if (pass) return p.key[(pass + 1) & 1][i];
+  const int64_t t = token_at(p.tokens, p.idx64, i);
+  return t >= 0 && t < p.V ? (uint32_t)t : (uint32_t)p.V;
 }
 
-template <typename T>
-__device__ __forceinline__ float load1(const void* base, int64_t i) {
-  return Elem<T>::widen1(static_cast<const typename Elem<T>::Bits*>(base)[i]);
+// The part of [lo, hi) that this warp owns.
+struct WarpPart {
+  int64_t lo, hi;
+};
+__device__ __forceinline__ WarpPart warp_part(int64_t lo, int64_t hi) {
+  const int64_t per = ((hi - lo + kSortWarps - 1) / kSortWarps + 31) & ~(int64_t)31;
+  WarpPart w;
+  w.lo = lo + (threadIdx.x >> 5) * per;
+  w.lo = w.lo < hi ? w.lo : hi;
+  w.hi = w.lo + per < hi ? w.lo + per : hi;
+  return w;
 }
-template <typename T>
-__device__ __forceinline__ void store1(void* base, int64_t i, float f) {
-  static_cast<typename Elem<T>::Bits*>(base)[i] = Elem<T>::narrow1(f);
+
+// count[warp][digit] of the warps' parts.
+__device__ __forceinline__ void count_digits(const EmbedGradParams& p, int pass, int64_t lo,
+                                             int64_t hi, uint32_t* count) {
+  const int bins = 1 << p.bits, shift = pass * p.bits;
+  for (int b = threadIdx.x; b < bins * kSortWarps; b += kSortThreads) count[b] = 0;
+  __syncthreads();
+  const WarpPart w = warp_part(lo, hi);
+  uint32_t* mine = count + (threadIdx.x >> 5) * bins;
+  for (int64_t i = w.lo + (threadIdx.x & 31); i < w.hi; i += 32)
+    atomicAdd(&mine[(sort_key(p, pass, i) >> shift) & (bins - 1)], 1u);
+  __syncthreads();
+}
+
+// Exclusive sum over the threads of the CTA.
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* wsum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t inc = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t u = __shfl_up_sync(~0u, inc, d);
+    if (lane >= d) inc += u;
+  }
+  if (lane == 31) wsum[warp] = inc;
+  __syncthreads();
+  uint32_t before = lane < warp ? wsum[lane] : 0u;
+  before = __reduce_add_sync(~0u, before);
+  __syncthreads();
+  return before + inc - v;
+}
+
+// Turns count[warp][digit] into each warp's first place for each digit;
+// thread d holds `first`, the tile's first place for digit d.
+__device__ __forceinline__ void place_warps(int bins, uint32_t first, uint32_t* count) {
+  if ((int)threadIdx.x < bins)
+    for (int w = 0; w < kSortWarps; ++w) {
+      const uint32_t c = count[w * bins + threadIdx.x];
+      count[w * bins + threadIdx.x] = first;
+      first += c;
+    }
+  __syncthreads();
+}
+
+// Writes the tile's pairs to their places; each(key, place) sees every one.
+template <typename F>
+__device__ __forceinline__ void scatter_tile(const EmbedGradParams& p, int pass, int64_t lo,
+                                             int64_t hi, uint32_t* count, F each) {
+  const int bins = 1 << p.bits, shift = pass * p.bits, lane = threadIdx.x & 31;
+  const uint32_t* pos = p.pos[(pass + 1) & 1];
+  uint32_t* okey = p.key[pass & 1];
+  uint32_t* opos = p.pos[pass & 1];
+  uint32_t* next = count + (threadIdx.x >> 5) * bins;
+  const WarpPart w = warp_part(lo, hi);
+  for (int64_t i0 = w.lo; i0 < w.hi; i0 += 32) {
+    const int64_t i = i0 + lane;
+    const bool in = i < w.hi;
+    const uint32_t k = in ? sort_key(p, pass, i) : 0u;
+    const uint32_t from = in ? (pass ? pos[i] : (uint32_t)i) : 0u;
+    const uint32_t digit = (k >> shift) & (bins - 1);
+    const uint32_t same = __match_any_sync(~0u, in ? digit : 0xFFFFFFFFu);
+    const uint32_t before = __popc(same & ((1u << lane) - 1));
+    const uint32_t at = in ? next[digit] + before : 0u;
+    __syncwarp();
+    if (in && before == 0) next[digit] += __popc(same);
+    __syncwarp();
+    if (in) {
+      okey[at] = k;
+      opos[at] = from;
+      each(k, at);
+    }
+  }
 }
 
 }  // namespace
 
-// One warp per row.
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads) vc_embed(const __grid_constant__ EmbedParams p) {
-  pdl_enter();
-  const int lane = threadIdx.x & 31;
-  const int64_t step = (int64_t)gridDim.x * (kRowThreads / 32);
-  for (int64_t i = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); i < p.N; i += step) {
-    const int64_t t = token_at(p.tokens, p.idx64, i);
-    const bool inside = t >= 0 && t < p.V;
-    for (int64_t c = lane; c < p.D; c += 32)
-      store1<T>(p.out, i * p.out_ld + c,
-                inside ? __fmul_rn(load1<T>(p.table, t * p.table_ld + c), p.scale) : 0.0f);
-  }
-}
-
-// Stable LSD radix sort of the tokens' (key, position) pairs by one CTA.  Each
-// warp owns a contiguous part of the array: it counts its digits, the counts
-// are scanned over (digit, warp), and it walks its part again in order, the
-// lanes of one digit taking the next places (match) in lane order.
+// The whole sort in one CTA.
 __global__ void __launch_bounds__(kSortThreads) vc_embed_sort(const __grid_constant__ EmbedGradParams p) {
   pdl_enter();
-  constexpr int NW = kSortThreads / 32;
-  extern __shared__ uint32_t cnt[];  // [digit][warp]
-  __shared__ uint32_t wsum[NW];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  extern __shared__ uint32_t count[];  // [warp][digit]
+  __shared__ uint32_t wsum[kSortWarps];
   const int bins = 1 << p.bits;
-  const int64_t per = ((p.N + NW - 1) / NW + 31) / 32 * 32;
-  const int64_t lo = warp * per < p.N ? warp * per : p.N;
-  const int64_t hi = lo + per < p.N ? lo + per : p.N;
   for (int pass = 0; pass < p.passes; ++pass) {
-    const uint32_t* key = p.key[(pass + 1) & 1];
-    const uint32_t* pos = p.pos[(pass + 1) & 1];
-    uint32_t* okey = p.key[pass & 1];
-    uint32_t* opos = p.pos[pass & 1];
-    const int shift = pass * p.bits;
-    auto read = [&](int64_t i) -> uint32_t {
-      if (pass) return key[i];
-      const int64_t t = token_at(p.tokens, p.idx64, i);
-      return t >= 0 && t < p.V ? (uint32_t)t : (uint32_t)p.V;
-    };
-    for (int b = threadIdx.x; b < bins * NW; b += kSortThreads) cnt[b] = 0;
-    __syncthreads();
-    for (int64_t i = lo + lane; i < hi; i += 32)
-      atomicAdd(&cnt[((read(i) >> shift) & (bins - 1)) * NW + warp], 1u);
-    __syncthreads();
-    // exclusive scan over [digit][warp]: bins / NW' entries per thread
-    const int each = bins * NW / kSortThreads;  // bins >= 32, so at least one
-    uint32_t sum = 0;
-    for (int k = 0; k < each; ++k) sum += cnt[threadIdx.x * each + k];
-    uint32_t inc = sum;
-    for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t v = __shfl_up_sync(~0u, inc, d);
-      if (lane >= d) inc += v;
-    }
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    if (warp == 0) {
-      uint32_t v = wsum[lane];
-      for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t u = __shfl_up_sync(~0u, v, d);
-        if (lane >= d) v += u;
-      }
-      wsum[lane] = v;
-    }
-    __syncthreads();
-    uint32_t run = inc - sum + (warp ? wsum[warp - 1] : 0u);
-    for (int k = 0; k < each; ++k) {
-      const uint32_t c = cnt[threadIdx.x * each + k];
-      cnt[threadIdx.x * each + k] = run;
-      run += c;
-    }
-    __syncthreads();
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-      const int64_t i = i0 + lane;
-      const bool in = i < hi;
-      const uint32_t k = in ? read(i) : 0u;
-      const uint32_t digit = (k >> shift) & (bins - 1);
-      const uint32_t same = __match_any_sync(~0u, in ? digit : 0xFFFFFFFFu);
-      const uint32_t before = __popc(same & ((1u << lane) - 1));
-      uint32_t at = 0;
-      if (in) at = cnt[digit * NW + warp] + before;
-      __syncwarp();
-      if (in && before == 0) cnt[digit * NW + warp] += __popc(same);
-      __syncwarp();
-      if (in) {
-        okey[at] = k;
-        opos[at] = pass ? pos[i] : (uint32_t)i;
-      }
-    }
+    count_digits(p, pass, 0, p.N, count);
+    uint32_t total = 0;
+    if ((int)threadIdx.x < bins)
+      for (int w = 0; w < kSortWarps; ++w) total += count[w * bins + threadIdx.x];
+    place_warps(bins, block_scan(total, wsum), count);
+    scatter_tile(p, pass, 0, p.N, count, [](uint32_t, uint32_t) {});
     __syncthreads();
   }
 }
 
-// One warp per row of the table: its tokens' places in the sorted list by
-// bisection, then the sum of their rows in order.
-template <typename T, typename TO>
+// The sort in one launch per pass, a CTA per tile, after one that counts the
+// first digit.  cnt[pass][tile][digit] are the tiles' counts.
+__global__ void __launch_bounds__(kSortThreads) vc_embed_count(const __grid_constant__ EmbedGradParams p) {
+  pdl_enter();
+  extern __shared__ uint32_t count[];
+  const int bins = 1 << p.bits;
+  const int64_t lo = (int64_t)blockIdx.x * p.sort_tile;
+  const int64_t hi = lo + p.sort_tile < p.N ? lo + p.sort_tile : p.N;
+  const size_t matrix = (size_t)gridDim.x * bins;
+  for (int b = threadIdx.x; b < bins * (p.passes - 1); b += kSortThreads)
+    p.cnt[(size_t)(1 + b / bins) * matrix + (size_t)blockIdx.x * bins + b % bins] = 0;
+  count_digits(p, 0, lo, hi, count);
+  if ((int)threadIdx.x < bins) {
+    uint32_t total = 0;
+    for (int w = 0; w < kSortWarps; ++w) total += count[w * bins + threadIdx.x];
+    p.cnt[(size_t)blockIdx.x * bins + threadIdx.x] = total;
+  }
+}
+
+// One pass: the tile's first place for digit d is what all tiles have below d
+// and the tiles before it have at d.  Every CTA sums the matrix of counts for
+// itself (it is read from L2), which saves a launch; the next pass's counts
+// are collected on the way, each pair's at the tile where it lands.
+__global__ void __launch_bounds__(kSortThreads)
+    vc_embed_scatter(const __grid_constant__ EmbedGradParams p) {
+  pdl_enter();
+  extern __shared__ uint32_t count[];
+  __shared__ uint32_t wsum[kSortWarps];
+  __shared__ uint32_t sall[kSortThreads], sbefore[kSortThreads];
+  const int pass = p.pass, bins = 1 << p.bits, tiles = gridDim.x;
+  const uint32_t* cnt = p.cnt + (size_t)pass * tiles * bins;
+  const int64_t lo = (int64_t)blockIdx.x * p.sort_tile;
+  const int64_t hi = lo + p.sort_tile < p.N ? lo + p.sort_tile : p.N;
+  // kSortThreads / bins groups of threads share the tiles
+  const int digit = threadIdx.x & (bins - 1), group = threadIdx.x >> p.bits;
+  const int groups = kSortThreads >> p.bits;
+  uint32_t all = 0, before = 0;
+#pragma unroll 4
+  for (int t = group; t < tiles; t += groups) {
+    const uint32_t c = cnt[(size_t)t * bins + digit];
+    all += c;
+    before += t < (int)blockIdx.x ? c : 0u;
+  }
+  sall[threadIdx.x] = all;
+  sbefore[threadIdx.x] = before;
+  count_digits(p, pass, lo, hi, count);
+  all = before = 0;
+  if ((int)threadIdx.x < bins)
+    for (int g = 0; g < groups; ++g) {
+      all += sall[g * bins + threadIdx.x];
+      before += sbefore[g * bins + threadIdx.x];
+    }
+  place_warps(bins, block_scan(all, wsum) + before, count);
+  if (pass + 1 < p.passes) {
+    uint32_t* next = p.cnt + (size_t)(pass + 1) * tiles * bins;
+    const int shift = (pass + 1) * p.bits;
+    scatter_tile(p, pass, lo, hi, count, [&](uint32_t k, uint32_t at) {
+      atomicAdd(&next[(size_t)(at / (uint32_t)p.sort_tile) * bins + ((k >> shift) & (bins - 1))], 1u);
+    });
+  } else {
+    scatter_tile(p, pass, lo, hi, count, [](uint32_t, uint32_t) {});
+  }
+}
+
+// --------------------------------------------------- summing the sorted rows
+// The sorted list is cut into chunks of p.chunk places, and a warp sums one
+// chunk's rows over one tile of 32 * E columns, eight rows' loads in flight.
+// A token whose places lie inside the chunk is written at once; the sum of one
+// that began in an earlier chunk goes to the chunk's first partial row (fp32),
+// of one that goes on in the next to its second, and vc_embed_join adds these
+// up in order.  The work is even however the tokens are spread.
+
+namespace {
+
+template <typename T, typename TO, int A>
+struct GradTile {
+  static constexpr int E = kLane<T>;
+  const EmbedGradParams& p;
+  int lane;
+  int64_t col0;  // first column of the tile
+
+  __device__ __forceinline__ int64_t col(int j) const { return col0 + (j * 32 + lane) * A; }
+
+  // table_grad[v] = base[v] + scale * sum
+  __device__ __forceinline__ void finish(int64_t v, const float (&sum)[E]) const {
+#pragma unroll
+    for (int j = 0; j < E / A; ++j) {
+      const int64_t c = col(j);
+      if (c >= p.D) continue;
+      float f[A];
+      if (p.base) {
+        Raw<TO, A> b;
+        b.load_stream(elem_at<TO>(p.base, v * p.base_ld + c));
+        b.widen(f);
+      }
+#pragma unroll
+      for (int a = 0; a < A; ++a)
+        f[a] = p.base ? fmaf(sum[j * A + a], p.scale, f[a]) : __fmul_rn(sum[j * A + a], p.scale);
+      Raw<TO, A> o;
+      o.narrow(f);
+      o.store_stream(elem_at<TO>(p.out, v * p.out_ld + c));
+    }
+  }
+
+  __device__ __forceinline__ float4* partial(int64_t chunk, int slot, int64_t tile) const {
+    return reinterpret_cast<float4*>(p.part) + ((chunk * 2 + slot) * p.tiles + tile) * (32 * E / 4) + lane;
+  }
+  __device__ __forceinline__ void put(float4* at, const float (&sum)[E]) const {
+#pragma unroll
+    for (int k = 0; k < E; k += 4) at[k * 8] = make_float4(sum[k], sum[k + 1], sum[k + 2], sum[k + 3]);
+  }
+  __device__ __forceinline__ void add(const float4* at, float (&sum)[E]) const {
+#pragma unroll
+    for (int k = 0; k < E; k += 4) {
+      const float4 v = at[k * 8];
+      sum[k] += v.x;
+      sum[k + 1] += v.y;
+      sum[k + 2] += v.z;
+      sum[k + 3] += v.w;
+    }
+  }
+};
+
+__device__ __forceinline__ int64_t lower_bound(const uint32_t* key, int64_t a, int64_t b, uint32_t v) {
+  while (a < b) {
+    const int64_t m = (a + b) >> 1;
+    if (key[m] < v) a = m + 1;
+    else b = m;
+  }
+  return a;
+}
+
+// Rows of 32 adjacent tokens, those that do not occur: base or zeros.
+template <typename TO, int A>
+__device__ __forceinline__ void fill_rows(const EmbedGradParams& p, const uint32_t* key, int64_t group) {
+  __shared__ uint32_t absent;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp == 0) {
+    const int64_t v = group * 32 + lane;
+    bool gone = v < p.V;
+    if (gone) {
+      const int64_t k = lower_bound(key, 0, p.N, (uint32_t)v);
+      gone = k == p.N || key[k] != (uint32_t)v;
+    }
+    const uint32_t m = __ballot_sync(~0u, gone);
+    if (lane == 0) absent = m;
+  }
+  __syncthreads();
+  for (uint32_t m = absent; m; m &= m - 1) {
+    const int64_t v = group * 32 + __ffs(m) - 1;
+    for (int64_t c = (int64_t)threadIdx.x * A; c < p.D; c += kRowThreads * A) {
+      Raw<TO, A> o;
+      if (p.base) o.load_stream(elem_at<TO>(p.base, v * p.base_ld + c));
+      else o.zero();
+      o.store_stream(elem_at<TO>(p.out, v * p.out_ld + c));
+    }
+  }
+}
+
+}  // namespace
+
+template <typename T, typename TO, int A>
 __global__ void __launch_bounds__(kRowThreads) vc_embed_grad(const __grid_constant__ EmbedGradParams p) {
   pdl_enter();
-  const int lane = threadIdx.x & 31;
-  const int64_t step = (int64_t)gridDim.x * (kRowThreads / 32);
+  constexpr int E = kLane<T>;
+  constexpr int U = A == 1 && E == 8 ? 4 : 8;  // rows in flight: 32 registers' worth
   const uint32_t* key = p.key[(p.passes + 1) & 1];
   const uint32_t* pos = p.pos[(p.passes + 1) & 1];
-  auto lower = [&](int64_t v) {
-    int64_t a = 0, b = p.N;
-    while (a < b) {
-      const int64_t m = (a + b) >> 1;
-      if ((int64_t)key[m] < v) a = m + 1;
-      else b = m;
+  if ((int64_t)blockIdx.x >= p.sum_ctas) {
+    fill_rows<TO, A>(p, key, (int64_t)blockIdx.x - p.sum_ctas);
+    return;
+  }
+  const int64_t unit = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+  const int64_t chunk = unit / p.tiles, tile = unit % p.tiles;
+  const int64_t lo = chunk * p.chunk;
+  if (lo >= p.N) return;
+  const int64_t hi = lo + p.chunk < p.N ? lo + p.chunk : p.N;
+  const GradTile<T, TO, A> g{p, (int)(threadIdx.x & 31), tile * 32 * E};
+  const uint32_t none = (uint32_t)p.V;
+  uint32_t cur = key[lo];
+  if (cur >= none) return;  // tokens outside the table sort last
+  bool began = lo > 0 && key[lo - 1] == cur;  // the current token began before this chunk
+  float sum[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) sum[e] = 0.0f;
+  for (int64_t k0 = lo; k0 < hi; k0 += U) {
+    uint32_t k[U];
+    Raw<T, A> r[U][E / A];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      k[u] = k0 + u < hi ? key[k0 + u] : none;
+      if (k[u] < none) {
+        const int64_t row = (int64_t)pos[k0 + u] * p.grad_ld;
+#pragma unroll
+        for (int j = 0; j < E / A; ++j) {
+          if (g.col(j) < p.D) r[u][j].load_stream(elem_at<T>(p.grad, row + g.col(j)));
+          else r[u][j].zero();
+        }
+      }
     }
-    return a;
-  };
-  for (int64_t v = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); v < p.V; v += step) {
-    const int64_t a = lower(v), b = lower(v + 1);
-    if (a == b && p.in_place) continue;
-    for (int64_t c = lane; c < p.D; c += 32) {
-      float sum = 0.0f;
-      for (int64_t k = a; k < b; ++k) sum += load1<T>(p.grad, (int64_t)pos[k] * p.grad_ld + c);
-      sum *= p.scale;
-      if (p.base) sum = load1<TO>(p.base, v * p.base_ld + c) + sum;
-      store1<TO>(p.out, v * p.out_ld + c, sum);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k[u] >= none) break;
+      if (k[u] != cur) {
+        if (began) g.put(g.partial(chunk, 0, tile), sum);
+        else g.finish(cur, sum);
+        began = false;
+        cur = k[u];
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum[e] = 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < E / A; ++j) {
+        float f[A];
+        r[u][j].widen(f);
+#pragma unroll
+        for (int a = 0; a < A; ++a) sum[j * A + a] += f[a];
+      }
     }
+  }
+  if (began) g.put(g.partial(chunk, 0, tile), sum);
+  else if (hi < p.N && key[hi] == cur) g.put(g.partial(chunk, 1, tile), sum);
+  else g.finish(cur, sum);
+}
+
+// A warp per (chunk, tile): if a token begins in the chunk and goes on after
+// it, its sum is the chunk's second partial row and the first ones of the
+// chunks that it reaches.  Tokens over more than kJoinAlone of them are added
+// up by all warps of the CTA, each a contiguous part, then in warp order.
+template <typename T, typename TO, int A>
+__global__ void __launch_bounds__(kRowThreads) vc_embed_join(const __grid_constant__ EmbedGradParams p) {
+  pdl_enter();
+  constexpr int E = kLane<T>, NW = kRowThreads / 32;
+  __shared__ int64_t last_of[NW];  // the last chunk of the warp's token, -1: nothing to do
+  __shared__ float part[NW][32 * E];
+  const uint32_t* key = p.key[(p.passes + 1) & 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t unit = (int64_t)blockIdx.x * NW + warp;
+  const int64_t chunk = unit / p.tiles, tile = unit % p.tiles;
+  const int64_t lo = chunk * p.chunk, hi = lo + p.chunk;
+  int64_t last = -1;
+  uint32_t v = 0;
+  if (hi < p.N) {
+    v = key[hi - 1];
+    if (v < (uint32_t)p.V && key[hi] == v && !(lo > 0 && key[lo - 1] == v))
+      last = (lower_bound(key, hi, p.N, v + 1) - 1) / p.chunk;
+  }
+  const GradTile<T, TO, A> g{p, lane, tile * 32 * E};
+  if (last >= 0 && last - chunk <= kJoinAlone) {
+    float sum[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[e] = 0.0f;
+    g.add(g.partial(chunk, 1, tile), sum);
+    for (int64_t c = chunk + 1; c <= last; ++c) g.add(g.partial(c, 0, tile), sum);
+    g.finish(v, sum);
+    last = -1;
+  }
+  if (lane == 0) last_of[warp] = last;
+  __syncthreads();
+  for (int w = 0; w < NW; ++w) {
+    const int64_t end = last_of[w];
+    if (end < 0) continue;  // the same for the whole CTA
+    const int64_t u = (int64_t)blockIdx.x * NW + w, from = u / p.tiles, t = u % p.tiles;
+    const GradTile<T, TO, A> gw{p, lane, t * 32 * E};
+    const int64_t per = (end - from + NW - 1) / NW;
+    const int64_t a = from + 1 + warp * per, b = a + per < end + 1 ? a + per : end + 1;
+    float sum[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[e] = 0.0f;
+    if (warp == 0) gw.add(gw.partial(from, 1, t), sum);
+#pragma unroll 4
+    for (int64_t c = a; c < b; ++c) gw.add(gw.partial(c, 0, t), sum);
+#pragma unroll
+    for (int e = 0; e < E; ++e) part[warp][e * 32 + lane] = sum[e];
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        float s = part[0][e * 32 + lane];
+        for (int k = 1; k < NW; ++k) s += part[k][e * 32 + lane];
+        sum[e] = s;
+      }
+      gw.finish(key[(from + 1) * p.chunk - 1], sum);
+    }
+    __syncthreads();
   }
 }
 
-const void* embed_kernel(int dtype) {
-  return dtype == VCOLL_F32 ? (const void*)&vc_embed<float> : (const void*)&vc_embed<__nv_bfloat16>;
+namespace {
+template <typename T>
+const void* lookup_kernel(int access) {
+  return access == kLane<T> ? (const void*)&vc_embed<T, kLane<T>>
+         : access == 2      ? (const void*)&vc_embed<T, 2>
+                            : (const void*)&vc_embed<T, 1>;
+}
+}  // namespace
+const void* embed_kernel(int dtype, int access) {
+  return dtype == VCOLL_F32 ? lookup_kernel<float>(access) : lookup_kernel<__nv_bfloat16>(access);
 }
 const void* embed_sort_kernel() { return (const void*)&vc_embed_sort; }
-const void* embed_grad_kernel(int dtype, int table_dtype) {
+const void* embed_count_kernel() { return (const void*)&vc_embed_count; }
+const void* embed_scatter_kernel() { return (const void*)&vc_embed_scatter; }
+
+namespace {
+template <typename T, typename TO>
+const void* grad_kernel(int access, int join) {
+  constexpr int E = kLane<T>;
+  if (access == E) return join ? (const void*)&vc_embed_join<T, TO, E> : (const void*)&vc_embed_grad<T, TO, E>;
+  if (access == 2) return join ? (const void*)&vc_embed_join<T, TO, 2> : (const void*)&vc_embed_grad<T, TO, 2>;
+  return join ? (const void*)&vc_embed_join<T, TO, 1> : (const void*)&vc_embed_grad<T, TO, 1>;
+}
+}  // namespace
+
+const void* embed_grad_kernel(int dtype, int table_dtype, int access, int join) {
   using B = __nv_bfloat16;
   if (dtype == VCOLL_F32)
-    return table_dtype == VCOLL_F32 ? (const void*)&vc_embed_grad<float, float>
-                                    : (const void*)&vc_embed_grad<float, B>;
-  return table_dtype == VCOLL_F32 ? (const void*)&vc_embed_grad<B, float>
-                                  : (const void*)&vc_embed_grad<B, B>;
+    return table_dtype == VCOLL_F32 ? grad_kernel<float, float>(access, join)
+                                    : grad_kernel<float, B>(access, join);
+  return table_dtype == VCOLL_F32 ? grad_kernel<B, float>(access, join)
+                                  : grad_kernel<B, B>(access, join);
 }
 
 }  // namespace vcoll

@@ -123,6 +123,47 @@ constexpr int kWarps = kRowThreads / 32;
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
+// The widest access, of `most`, 2 or 1 elements, that every row of an operand
+// allows (row_access.cuh).  An absent operand allows any.
+int access_of(const Operand& o, int most) {
+  if (!o.ptr || !o.rows || !o.cols) return most;
+  for (int a : {most, 2})
+    if ((uint64_t)o.ptr % std::min(16, a * o.es) == 0 && o.cols % a == 0 &&
+        (o.rows == 1 || o.ld % a == 0))
+      return a;
+  return 1;
+}
+
+// Up to this many tokens one CTA sorts.
+constexpr int64_t kSortOneCta = 4096;
+
+// The workspace of the embedding's gradient.
+struct GradLayout {
+  int passes, bits;            // of the sort
+  int64_t sort_tile, chunk;
+  size_t list, cnt, part, bytes;  // bytes of one list; offsets; all
+};
+GradLayout grad_layout(int64_t N, int64_t V, int64_t D) {
+  GradLayout L;
+  int bits = 1;  // of keys 0 .. V
+  while (bits < 31 && (V >> bits)) ++bits;
+  L.passes = (int)ceil_div(bits, kSortMaxBits);
+  L.bits = (int)ceil_div(bits, L.passes);
+  L.sort_tile = std::max(kSortMinTile, ceil_div(ceil_div(N, kSortMaxTiles), 32) * 32);
+  // Places per warp: enough chunks for two waves of 32 warps on 152 SMs, each
+  // of 32 places at least (partial rows are traffic) and 256 at most.
+  const int64_t tiles = ceil_div(D, 256);
+  L.chunk = std::min<int64_t>(256, std::max<int64_t>(1, ceil_div(N * tiles, 2 * 32 * 152 * 32)) * 32);
+  L.list = align256((size_t)N * sizeof(uint32_t));
+  L.cnt = 4 * L.list;
+  L.part = L.cnt;
+  if (N > kSortOneCta)
+    L.part += align256((size_t)L.passes * (size_t)ceil_div(N, L.sort_tile) * sizeof(uint32_t) << L.bits);
+  // rows of partial sums are padded to whole tiles, of 256 columns at most
+  L.bytes = L.part + align256((size_t)ceil_div(N, L.chunk) * 2 * (size_t)tiles * 256 * sizeof(float));
+  return L;
+}
+
 }  // namespace
 
 extern "C" {
@@ -154,14 +195,16 @@ int vcoll_embedding(const void* tokens, int index_type, int64_t N, const void* t
   p.out_ld = out_ld;
   p.scale = scale;
   p.idx64 = index_type == VCOLL_I64;
-  int64_t grid;
-  VCOLL_TRY(grid_for(N, kWarps, 32, &grid));
-  return launch_grid(embed_kernel(dtype), grid, 1, kRowThreads, 0, &p, stream);
+  const int E = 16 / es, access = std::min(access_of(ops[1], E), access_of(ops[2], E));
+  while ((1 << p.row_shift) < kWarps && ((int64_t)(kLookup * 32 * E) << p.row_shift) < D)
+    ++p.row_shift;
+  return launch_grid(embed_kernel(dtype, access), ceil_div(N, kWarps >> p.row_shift), 1,
+                     kRowThreads, 0, &p, stream);
 }
 
 size_t vcoll_embedding_backward_workspace_bytes(int64_t N, int64_t V, int64_t D) {
-  if (N <= 0 || V <= 0 || D <= 0) return 0;
-  return 4 * align256((size_t)N * sizeof(uint32_t));
+  if (N <= 0 || V <= 0 || D <= 0 || N > kMaxExtent || V > kMaxExtent || D > kMaxExtent) return 0;
+  return grad_layout(N, V, D).bytes;
 }
 
 int vcoll_embedding_backward(const void* grad, int64_t grad_ld, int dtype, const void* tokens,
@@ -195,11 +238,6 @@ int vcoll_embedding_backward(const void* grad, int64_t grad_ld, int dtype, const
   p.grad = grad;
   p.base = base;
   p.out = table_grad;
-  const size_t part = align256((size_t)N * sizeof(uint32_t));
-  for (int k = 0; k < 2 && N; ++k) {
-    p.key[k] = (uint32_t*)((char*)workspace + (size_t)(2 * k) * part);
-    p.pos[k] = (uint32_t*)((char*)workspace + (size_t)(2 * k + 1) * part);
-  }
   p.N = N;
   p.V = V;
   p.D = D;
@@ -208,18 +246,43 @@ int vcoll_embedding_backward(const void* grad, int64_t grad_ld, int dtype, const
   p.out_ld = table_ld;
   p.scale = scale;
   p.idx64 = index_type == VCOLL_I64;
-  p.in_place = in_place;
-  int bits = 1;  // of keys 0 .. V
-  while (bits < 31 && (V >> bits)) ++bits;
-  p.passes = (int)ceil_div(bits, kSortMaxBits);
-  p.bits = std::max(5, (int)ceil_div(bits, p.passes));
   if (N) {
+    const GradLayout L = grad_layout(N, V, D);
+    char* ws = (char*)workspace;
+    for (int k = 0; k < 2; ++k) {
+      p.key[k] = (uint32_t*)(ws + (size_t)(2 * k) * L.list);
+      p.pos[k] = (uint32_t*)(ws + (size_t)(2 * k + 1) * L.list);
+    }
+    p.cnt = (uint32_t*)(ws + L.cnt);
+    p.part = (float*)(ws + L.part);
+    p.passes = L.passes;
+    p.bits = L.bits;
+    p.sort_tile = L.sort_tile;
+    p.chunk = L.chunk;
     const size_t smem = ((size_t)1 << kSortMaxBits) * (kSortThreads / 32) * sizeof(uint32_t);
-    VCOLL_TRY(launch_grid(embed_sort_kernel(), 1, 1, kSortThreads, smem, &p, stream));
+    if (N <= kSortOneCta) {
+      VCOLL_TRY(launch_grid(embed_sort_kernel(), 1, 1, kSortThreads, smem, &p, stream));
+    } else {
+      const int64_t tiles = ceil_div(N, L.sort_tile);
+      VCOLL_TRY(launch_grid(embed_count_kernel(), tiles, 1, kSortThreads, smem, &p, stream));
+      for (p.pass = 0; p.pass < p.passes; ++p.pass)
+        VCOLL_TRY(launch_grid(embed_scatter_kernel(), tiles, 1, kSortThreads, smem, &p, stream));
+    }
   }
-  int64_t grid;
-  VCOLL_TRY(grid_for(V, kWarps, 32, &grid));
-  return launch_grid(embed_grad_kernel(dtype, table_dtype), grid, 1, kRowThreads, 0, &p, stream);
+  const int E = 16 / es;
+  int access = E;
+  for (const Operand* o = ops + 1; o < ops + 4; ++o) access = std::min(access, access_of(*o, E));
+  p.tiles = ceil_div(D, 32 * E);
+  p.sum_ctas = N ? ceil_div(ceil_div(N, p.chunk) * p.tiles, kWarps) : 0;
+  const int64_t fill = in_place ? 0 : ceil_div(V, 32);
+  if (p.sum_ctas + fill > 0x7FFFFFFF)
+    return fail(VCOLL_ERR_UNSUPPORTED, "a table of %lld x %lld is too large", (long long)V,
+                (long long)D);
+  VCOLL_TRY(launch_grid(embed_grad_kernel(dtype, table_dtype, access, 0), p.sum_ctas + fill, 1,
+                        kRowThreads, 0, &p, stream));
+  if (N <= p.chunk) return VCOLL_OK;  // no token reaches a second chunk
+  return launch_grid(embed_grad_kernel(dtype, table_dtype, access, 1), p.sum_ctas, 1, kRowThreads,
+                     0, &p, stream);
 }
 
 // x, y (or grad, dx) and the 8-bit operands of the layer norm entry points

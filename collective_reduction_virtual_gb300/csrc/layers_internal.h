@@ -12,6 +12,7 @@ namespace vcoll {
 
 constexpr int kRowThreads = 256;  // threads of a CTA that works on rows
 
+constexpr int kLookup = 4;  // 16-byte accesses per lane in flight in the lookup
 struct EmbedParams {
   const void* tokens;
   const void* table;
@@ -20,12 +21,17 @@ struct EmbedParams {
   int64_t table_ld, out_ld;
   float scale;
   int idx64;
+  int row_shift;  // log2 of the warps that take a row
 };
 
 // The gradient's tokens are sorted by (token, position) with a stable LSD
 // radix sort; tokens outside [0, V) sort as V, behind all others.
 constexpr int kSortThreads = 1024;
 constexpr int kSortMaxBits = 9;  // digit width
+constexpr int kSortMaxPasses = 4;
+constexpr int64_t kSortMinTile = 2048;  // keys of a CTA where several sort
+constexpr int kSortMaxTiles = 128;
+constexpr int64_t kJoinAlone = 16;  // partial rows that one warp adds up alone
 struct EmbedGradParams {
   const void* tokens;
   const void* grad;
@@ -33,12 +39,17 @@ struct EmbedGradParams {
   void* out;
   uint32_t* key[2];  // ping-pong of the sort: N keys and N positions each
   uint32_t* pos[2];
+  uint32_t* cnt;     // digit counts: passes x tiles x 2^bits
+  float* part;       // partial rows: chunks x 2 x tiles x (32 * E)
   int64_t N, V, D;
   int64_t grad_ld, base_ld, out_ld;
+  int64_t sort_tile;  // keys of a tile of the sort
+  int64_t chunk;      // places of the sorted list that a warp sums
+  int64_t tiles;      // column tiles
+  int64_t sum_ctas;   // CTAs that sum; the ones behind them fill absent rows
   float scale;
   int idx64;
-  int in_place;  // base is out
-  int passes, bits;
+  int passes, bits, pass;
 };
 
 struct NormParams {
@@ -72,9 +83,12 @@ struct PackParams {
   int wbf16;
 };
 
-const void* embed_kernel(int dtype);
+// access: elements of an access (a whole 16 bytes of dtype, 2 or 1)
+const void* embed_kernel(int dtype, int access);
 const void* embed_sort_kernel();
-const void* embed_grad_kernel(int dtype, int table_dtype);
+const void* embed_count_kernel();
+const void* embed_scatter_kernel();
+const void* embed_grad_kernel(int dtype, int table_dtype, int access, int join);
 const void* norm_kernel(int dtype);
 const void* norm_grad_kernel(int dtype);
 const void* norm_wgrad_kernel(int dtype);
