@@ -41,6 +41,72 @@ __global__ void __launch_bounds__(kRowThreads) vc_embed(const __grid_constant__ 
   }
 }
 
+// --------------------------------------------------- rows of absent tokens
+// Every token of the list leaves its position in stamp[token] (one of them
+// stays, whichever).  A row's token occurs if and only if the position that
+// its stamp names holds it, so the stamps need no clearing beforehand: what an
+// older call or nobody wrote there does not pass.
+
+namespace {
+
+__device__ __forceinline__ void put_stamp(const EmbedGradParams& p, uint32_t key, uint32_t i) {
+  if (key < (uint32_t)p.V) p.stamp[key] = i;
+}
+
+// One warp writes base or zeros to those of kFillRows adjacent rows whose
+// tokens do not occur, eight accesses per lane in flight.  BYTES: of an access.
+template <int BYTES>
+__device__ __forceinline__ void fill_pieces(const EmbedGradParams& p, int64_t v) {
+  using P = Raw<float, BYTES / 4>;
+  const char* from = static_cast<const char*>(p.base) + v * p.base_ld * p.table_es;
+  char* to = static_cast<char*>(p.out) + v * p.out_ld * p.table_es;
+  const int64_t end = p.D * p.table_es;
+  for (int64_t c0 = (threadIdx.x & 31) * BYTES; c0 < end; c0 += 8 * 32 * BYTES) {
+    P r[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (p.base && c0 + k * 32 * BYTES < end) r[k].load_stream(from + c0 + k * 32 * BYTES);
+      else r[k].zero();
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (c0 + k * 32 * BYTES < end) r[k].store_stream(to + c0 + k * 32 * BYTES);
+  }
+}
+// two-byte pieces: rows of bf16 at odd places
+__device__ __forceinline__ void fill_halves(const EmbedGradParams& p, int64_t v) {
+  using P = Raw<__nv_bfloat16, 1>;
+  const char* from = elem_at<__nv_bfloat16>(p.base, v * p.base_ld);
+  char* to = elem_at<__nv_bfloat16>(p.out, v * p.out_ld);
+  for (int64_t c0 = threadIdx.x & 31; c0 < p.D; c0 += 8 * 32) {
+    P r[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (p.base && c0 + k * 32 < p.D) r[k].load_stream(from + (c0 + k * 32) * 2);
+      else r[k].zero();
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (c0 + k * 32 < p.D) r[k].store_stream(to + (c0 + k * 32) * 2);
+  }
+}
+
+__device__ __forceinline__ void fill_rows(const EmbedGradParams& p, int64_t first) {
+  const int lane = threadIdx.x & 31;
+  const int64_t v = first + lane;
+  bool gone = lane < kFillRows && v < p.fill_end;
+  if (gone && p.N) {
+    const uint32_t i = p.stamp[v];
+    gone = (int64_t)i >= p.N || token_at(p.tokens, p.idx64, i) != v;
+  }
+  for (uint32_t m = __ballot_sync(~0u, gone); m; m &= m - 1) {
+    const int64_t row = first + __ffs(m) - 1;
+    if (p.fill_bytes == 16) fill_pieces<16>(p, row);
+    else if (p.fill_bytes == 4) fill_pieces<4>(p, row);
+    else fill_halves(p, row);
+  }
+}
+
+}  // namespace
+
 // ------------------------------------------------------ sorting the tokens
 // Stable LSD radix sort of the tokens' (key, position) pairs.  A CTA sorts a
 // tile of the array by one digit: each warp owns a contiguous part of the
@@ -51,6 +117,8 @@ __global__ void __launch_bounds__(kRowThreads) vc_embed(const __grid_constant__ 
 namespace {
 
 constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kStampPiece = 2048, kStampSlots = 8192;
+static_assert((kStampPiece + kStampSlots) * 4 <= (1 << kSortMaxBits) * kSortWarps * 4, "shared memory");
 
 __device__ __forceinline__ uint32_t sort_key(const EmbedGradParams& p, int pass, int64_t i) {
   if (pass) return p.key[(pass + 1) & 1][i];
@@ -138,7 +206,7 @@ __device__ __forceinline__ void scatter_tile(const EmbedGradParams& p, int pass,
     if (in) {
       okey[at] = k;
       opos[at] = from;
-      each(k, at);
+      each(k, at, from);
     }
   }
 }
@@ -157,7 +225,9 @@ __global__ void __launch_bounds__(kSortThreads) vc_embed_sort(const __grid_const
     if ((int)threadIdx.x < bins)
       for (int w = 0; w < kSortWarps; ++w) total += count[w * bins + threadIdx.x];
     place_warps(bins, block_scan(total, wsum), count);
-    scatter_tile(p, pass, 0, p.N, count, [](uint32_t, uint32_t) {});
+    scatter_tile(p, pass, 0, p.N, count, [&](uint32_t k, uint32_t, uint32_t i) {
+      if (pass == 0) put_stamp(p, k, i);
+    });
     __syncthreads();
   }
 }
@@ -173,6 +243,25 @@ __global__ void __launch_bounds__(kSortThreads) vc_embed_count(const __grid_cons
   const size_t matrix = (size_t)gridDim.x * bins;
   for (int b = threadIdx.x; b < bins * (p.passes - 1); b += kSortThreads)
     p.cnt[(size_t)(1 + b / bins) * matrix + (size_t)blockIdx.x * bins + b % bins] = 0;
+  // one stamp for each token of a tile's piece: as many stores to a frequent
+  // token's stamp as it has places would wait for one another (21 us instead
+  // of 6 at 262144 tokens spread as in text)
+  uint32_t* skey = count;
+  uint32_t* slot = count + kStampPiece;
+  for (int64_t i0 = lo; i0 < hi; i0 += kStampPiece) {
+    const int n = (int)(hi - i0 < kStampPiece ? hi - i0 : kStampPiece);
+    for (int i = threadIdx.x; i < n; i += kSortThreads) {
+      const uint32_t k = sort_key(p, 0, i0 + i);
+      skey[i] = k;
+      slot[k & (kStampSlots - 1)] = i;  // one of those that share the slot stays
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kSortThreads) {
+      const uint32_t k = skey[i], in = slot[k & (kStampSlots - 1)];
+      if ((int)in == i || skey[in] != k) put_stamp(p, k, (uint32_t)(i0 + i));
+    }
+    __syncthreads();
+  }
   count_digits(p, 0, lo, hi, count);
   if ((int)threadIdx.x < bins) {
     uint32_t total = 0;
@@ -184,14 +273,20 @@ __global__ void __launch_bounds__(kSortThreads) vc_embed_count(const __grid_cons
 // One pass: the tile's first place for digit d is what all tiles have below d
 // and the tiles before it have at d.  Every CTA sums the matrix of counts for
 // itself (it is read from L2), which saves a launch; the next pass's counts
-// are collected on the way, each pair's at the tile where it lands.
+// are collected on the way, each pair's at the tile where it lands.  A pass
+// takes a few microseconds and hardly any bandwidth, so CTAs behind the tiles'
+// fill rows of absent tokens meanwhile.
 __global__ void __launch_bounds__(kSortThreads)
     vc_embed_scatter(const __grid_constant__ EmbedGradParams p) {
   pdl_enter();
   extern __shared__ uint32_t count[];
   __shared__ uint32_t wsum[kSortWarps];
   __shared__ uint32_t sall[kSortThreads], sbefore[kSortThreads];
-  const int pass = p.pass, bins = 1 << p.bits, tiles = gridDim.x;
+  const int pass = p.pass, bins = 1 << p.bits, tiles = p.sort_tiles;
+  if ((int)blockIdx.x >= tiles) {
+    fill_rows(p, p.fill_begin + ((int64_t)(blockIdx.x - tiles) * kSortWarps + (threadIdx.x >> 5)) * kFillRows);
+    return;
+  }
   const uint32_t* cnt = p.cnt + (size_t)pass * tiles * bins;
   const int64_t lo = (int64_t)blockIdx.x * p.sort_tile;
   const int64_t hi = lo + p.sort_tile < p.N ? lo + p.sort_tile : p.N;
@@ -199,7 +294,7 @@ __global__ void __launch_bounds__(kSortThreads)
   const int digit = threadIdx.x & (bins - 1), group = threadIdx.x >> p.bits;
   const int groups = kSortThreads >> p.bits;
   uint32_t all = 0, before = 0;
-#pragma unroll 4
+#pragma unroll 16
   for (int t = group; t < tiles; t += groups) {
     const uint32_t c = cnt[(size_t)t * bins + digit];
     all += c;
@@ -218,11 +313,11 @@ __global__ void __launch_bounds__(kSortThreads)
   if (pass + 1 < p.passes) {
     uint32_t* next = p.cnt + (size_t)(pass + 1) * tiles * bins;
     const int shift = (pass + 1) * p.bits;
-    scatter_tile(p, pass, lo, hi, count, [&](uint32_t k, uint32_t at) {
+    scatter_tile(p, pass, lo, hi, count, [&](uint32_t k, uint32_t at, uint32_t) {
       atomicAdd(&next[(size_t)(at / (uint32_t)p.sort_tile) * bins + ((k >> shift) & (bins - 1))], 1u);
     });
   } else {
-    scatter_tile(p, pass, lo, hi, count, [](uint32_t, uint32_t) {});
+    scatter_tile(p, pass, lo, hi, count, [](uint32_t, uint32_t, uint32_t) {});
   }
 }
 
@@ -285,102 +380,81 @@ struct GradTile {
   }
 };
 
-__device__ __forceinline__ int64_t lower_bound(const uint32_t* key, int64_t a, int64_t b, uint32_t v) {
-  while (a < b) {
-    const int64_t m = (a + b) >> 1;
-    if (key[m] < v) a = m + 1;
-    else b = m;
-  }
-  return a;
-}
-
-// Rows of 32 adjacent tokens, those that do not occur: base or zeros.
-template <typename TO, int A>
-__device__ __forceinline__ void fill_rows(const EmbedGradParams& p, const uint32_t* key, int64_t group) {
-  __shared__ uint32_t absent;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (warp == 0) {
-    const int64_t v = group * 32 + lane;
-    bool gone = v < p.V;
-    if (gone) {
-      const int64_t k = lower_bound(key, 0, p.N, (uint32_t)v);
-      gone = k == p.N || key[k] != (uint32_t)v;
-    }
-    const uint32_t m = __ballot_sync(~0u, gone);
-    if (lane == 0) absent = m;
-  }
-  __syncthreads();
-  for (uint32_t m = absent; m; m &= m - 1) {
-    const int64_t v = group * 32 + __ffs(m) - 1;
-    for (int64_t c = (int64_t)threadIdx.x * A; c < p.D; c += kRowThreads * A) {
-      Raw<TO, A> o;
-      if (p.base) o.load_stream(elem_at<TO>(p.base, v * p.base_ld + c));
-      else o.zero();
-      o.store_stream(elem_at<TO>(p.out, v * p.out_ld + c));
-    }
-  }
-}
-
 }  // namespace
 
 template <typename T, typename TO, int A>
-__global__ void __launch_bounds__(kRowThreads) vc_embed_grad(const __grid_constant__ EmbedGradParams p) {
+__global__ void __launch_bounds__(kRowThreads, A == kLane<T> ? 3 : 4)
+    vc_embed_grad(const __grid_constant__ EmbedGradParams p) {
   pdl_enter();
   constexpr int E = kLane<T>;
   constexpr int U = A == 1 && E == 8 ? 4 : 8;  // rows in flight: 32 registers' worth
   const uint32_t* key = p.key[(p.passes + 1) & 1];
   const uint32_t* pos = p.pos[(p.passes + 1) & 1];
-  if ((int64_t)blockIdx.x >= p.sum_ctas) {
-    fill_rows<TO, A>(p, key, (int64_t)blockIdx.x - p.sum_ctas);
+  // the CTAs that fill are spread evenly among those that sum, so that reads
+  // and writes mix
+  const int64_t fills = (int64_t)gridDim.x - p.sum_ctas;
+  const int64_t fill = (int64_t)blockIdx.x * fills / gridDim.x;
+  if (((int64_t)blockIdx.x + 1) * fills / gridDim.x != fill) {
+    fill_rows(p, p.fill_begin + (fill * (kRowThreads / 32) + (threadIdx.x >> 5)) * kFillRows);
     return;
   }
-  const int64_t unit = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+  const int64_t unit = ((int64_t)blockIdx.x - fill) * (kRowThreads / 32) + (threadIdx.x >> 5);
   const int64_t chunk = unit / p.tiles, tile = unit % p.tiles;
   const int64_t lo = chunk * p.chunk;
   if (lo >= p.N) return;
   const int64_t hi = lo + p.chunk < p.N ? lo + p.chunk : p.N;
   const GradTile<T, TO, A> g{p, (int)(threadIdx.x & 31), tile * 32 * E};
   const uint32_t none = (uint32_t)p.V;
-  uint32_t cur = key[lo];
-  if (cur >= none) return;  // tokens outside the table sort last
+  // 32 places at a time, one per lane, the next ones loaded ahead; tokens
+  // outside the table sort last, so the valid lanes are the first ones
+  int64_t at = lo + g.lane;
+  uint32_t key_next = at < hi ? key[at] : none, pos_next = at < hi ? pos[at] : 0u;
+  uint32_t cur = __shfl_sync(~0u, key_next, 0);
+  if (cur >= none) return;
   bool began = lo > 0 && key[lo - 1] == cur;  // the current token began before this chunk
   float sum[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) sum[e] = 0.0f;
-  for (int64_t k0 = lo; k0 < hi; k0 += U) {
-    uint32_t k[U];
-    Raw<T, A> r[U][E / A];
+  for (int64_t k0 = lo; k0 < hi; k0 += 32) {
+    const uint32_t k = key_next, from = pos_next;
+    at += 32;
+    key_next = at < hi ? key[at] : none;
+    pos_next = at < hi ? pos[at] : 0u;
+    const int n = __popc(__ballot_sync(~0u, k < none));
+    const uint32_t prev = __shfl_up_sync(~0u, k, 1);
+    const uint32_t starts = __ballot_sync(~0u, k != (g.lane ? prev : cur));
+#pragma unroll 1
+    for (int s = 0; s < n; s += U) {
+      Raw<T, A> r[U][E / A];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      k[u] = k0 + u < hi ? key[k0 + u] : none;
-      if (k[u] < none) {
-        const int64_t row = (int64_t)pos[k0 + u] * p.grad_ld;
+      for (int u = 0; u < U; ++u) {
+        const int64_t row = (int64_t)__shfl_sync(~0u, from, s + u) * p.grad_ld;
 #pragma unroll
         for (int j = 0; j < E / A; ++j) {
-          if (g.col(j) < p.D) r[u][j].load_stream(elem_at<T>(p.grad, row + g.col(j)));
+          if (s + u < n && g.col(j) < p.D) r[u][j].load_stream(elem_at<T>(p.grad, row + g.col(j)));
           else r[u][j].zero();
         }
       }
-    }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (k[u] >= none) break;
-      if (k[u] != cur) {
-        if (began) g.put(g.partial(chunk, 0, tile), sum);
-        else g.finish(cur, sum);
-        began = false;
-        cur = k[u];
+      for (int u = 0; u < U; ++u) {
+        if (s + u < n && (starts >> (s + u) & 1)) {
+          if (began) g.put(g.partial(chunk, 0, tile), sum);
+          else g.finish(cur, sum);
+          began = false;
+          cur = __shfl_sync(~0u, k, s + u);
 #pragma unroll
-        for (int e = 0; e < E; ++e) sum[e] = 0.0f;
+          for (int e = 0; e < E; ++e) sum[e] = 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < E / A; ++j) {
+          float f[A];
+          r[u][j].widen(f);
+#pragma unroll
+          for (int a = 0; a < A; ++a) sum[j * A + a] += f[a];
+        }
       }
-#pragma unroll
-      for (int j = 0; j < E / A; ++j) {
-        float f[A];
-        r[u][j].widen(f);
-#pragma unroll
-        for (int a = 0; a < A; ++a) sum[j * A + a] += f[a];
-      }
     }
+    if (n < 32) break;
   }
   if (began) g.put(g.partial(chunk, 0, tile), sum);
   else if (hi < p.N && key[hi] == cur) g.put(g.partial(chunk, 1, tile), sum);
@@ -399,15 +473,25 @@ __global__ void __launch_bounds__(kRowThreads) vc_embed_join(const __grid_consta
   __shared__ float part[NW][32 * E];
   const uint32_t* key = p.key[(p.passes + 1) & 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t unit = (int64_t)blockIdx.x * NW + warp;
+  // units a CTA apart: those of one chunk, which a long token makes long, go to
+  // different CTAs
+  const int64_t unit = (int64_t)warp * gridDim.x + blockIdx.x;
   const int64_t chunk = unit / p.tiles, tile = unit % p.tiles;
   const int64_t lo = chunk * p.chunk, hi = lo + p.chunk;
   int64_t last = -1;
   uint32_t v = 0;
   if (hi < p.N) {
     v = key[hi - 1];
-    if (v < (uint32_t)p.V && key[hi] == v && !(lo > 0 && key[lo - 1] == v))
-      last = (lower_bound(key, hi, p.N, v + 1) - 1) / p.chunk;
+    if (v < (uint32_t)p.V && key[hi] == v && !(lo > 0 && key[lo - 1] == v)) {
+      // the last chunk that begins inside the token, 32 at a time
+      uint32_t reach;
+      last = chunk;
+      do {
+        const int64_t first = (last + 1 + lane) * p.chunk;
+        reach = __popc(__ballot_sync(~0u, first < p.N && key[first] == v));
+        last += reach;
+      } while (reach == 32);
+    }
   }
   const GradTile<T, TO, A> g{p, lane, tile * 32 * E};
   if (last >= 0 && last - chunk <= kJoinAlone) {
@@ -424,7 +508,7 @@ __global__ void __launch_bounds__(kRowThreads) vc_embed_join(const __grid_consta
   for (int w = 0; w < NW; ++w) {
     const int64_t end = last_of[w];
     if (end < 0) continue;  // the same for the whole CTA
-    const int64_t u = (int64_t)blockIdx.x * NW + w, from = u / p.tiles, t = u % p.tiles;
+    const int64_t u = (int64_t)w * gridDim.x + blockIdx.x, from = u / p.tiles, t = u % p.tiles;
     const GradTile<T, TO, A> gw{p, lane, t * 32 * E};
     const int64_t per = (end - from + NW - 1) / NW;
     const int64_t a = from + 1 + warp * per, b = a + per < end + 1 ? a + per : end + 1;

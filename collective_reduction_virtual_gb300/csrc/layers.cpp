@@ -137,11 +137,15 @@ int access_of(const Operand& o, int most) {
 // Up to this many tokens one CTA sorts.
 constexpr int64_t kSortOneCta = 4096;
 
+// Bytes of absent rows that are filled beside each pass of the sort, about
+// what is written in the time that a pass takes.
+constexpr int64_t kFillPassBytes = 48 << 20;
+
 // The workspace of the embedding's gradient.
 struct GradLayout {
   int passes, bits;            // of the sort
   int64_t sort_tile, chunk;
-  size_t list, cnt, part, bytes;  // bytes of one list; offsets; all
+  size_t list, cnt, stamp, part, bytes;  // bytes of one list; offsets; all
 };
 GradLayout grad_layout(int64_t N, int64_t V, int64_t D) {
   GradLayout L;
@@ -156,9 +160,10 @@ GradLayout grad_layout(int64_t N, int64_t V, int64_t D) {
   L.chunk = std::min<int64_t>(256, std::max<int64_t>(1, ceil_div(N * tiles, 2 * 32 * 152 * 32)) * 32);
   L.list = align256((size_t)N * sizeof(uint32_t));
   L.cnt = 4 * L.list;
-  L.part = L.cnt;
+  L.stamp = L.cnt;
   if (N > kSortOneCta)
-    L.part += align256((size_t)L.passes * (size_t)ceil_div(N, L.sort_tile) * sizeof(uint32_t) << L.bits);
+    L.stamp += align256((size_t)L.passes * (size_t)ceil_div(N, L.sort_tile) * sizeof(uint32_t) << L.bits);
+  L.part = L.stamp + align256((size_t)V * sizeof(uint32_t));
   // rows of partial sums are padded to whole tiles, of 256 columns at most
   L.bytes = L.part + align256((size_t)ceil_div(N, L.chunk) * 2 * (size_t)tiles * 256 * sizeof(float));
   return L;
@@ -246,6 +251,11 @@ int vcoll_embedding_backward(const void* grad, int64_t grad_ld, int dtype, const
   p.out_ld = table_ld;
   p.scale = scale;
   p.idx64 = index_type == VCOLL_I64;
+  p.table_es = ts;
+  // the fill copies bytes: rows of base and table_grad in pieces of 16, 4 or 2
+  p.fill_bytes = std::min(access_of(ops[2], 16 / ts), access_of(ops[3], 16 / ts)) * ts;
+  if (p.fill_bytes == 8) p.fill_bytes = 4;
+  p.fill_end = in_place ? V : 0;  // rows filled so far: none is, or all stay as they are
   if (N) {
     const GradLayout L = grad_layout(N, V, D);
     char* ws = (char*)workspace;
@@ -254,6 +264,7 @@ int vcoll_embedding_backward(const void* grad, int64_t grad_ld, int dtype, const
       p.pos[k] = (uint32_t*)(ws + (size_t)(2 * k + 1) * L.list);
     }
     p.cnt = (uint32_t*)(ws + L.cnt);
+    p.stamp = (uint32_t*)(ws + L.stamp);
     p.part = (float*)(ws + L.part);
     p.passes = L.passes;
     p.bits = L.bits;
@@ -263,10 +274,17 @@ int vcoll_embedding_backward(const void* grad, int64_t grad_ld, int dtype, const
     if (N <= kSortOneCta) {
       VCOLL_TRY(launch_grid(embed_sort_kernel(), 1, 1, kSortThreads, smem, &p, stream));
     } else {
-      const int64_t tiles = ceil_div(N, L.sort_tile);
-      VCOLL_TRY(launch_grid(embed_count_kernel(), tiles, 1, kSortThreads, smem, &p, stream));
-      for (p.pass = 0; p.pass < p.passes; ++p.pass)
-        VCOLL_TRY(launch_grid(embed_scatter_kernel(), tiles, 1, kSortThreads, smem, &p, stream));
+      p.sort_tiles = (int)ceil_div(N, L.sort_tile);
+      VCOLL_TRY(launch_grid(embed_count_kernel(), p.sort_tiles, 1, kSortThreads, smem, &p, stream));
+      constexpr int64_t kCtaRows = kSortThreads / 32 * kFillRows;
+      const int64_t fill = ceil_div(std::max<int64_t>(1, kFillPassBytes / (D * ts)), kCtaRows);
+      for (p.pass = 0; p.pass < p.passes; ++p.pass) {
+        p.fill_begin = p.fill_end;
+        p.fill_end = std::min(V, p.fill_begin + fill * kCtaRows);
+        VCOLL_TRY(launch_grid(embed_scatter_kernel(),
+                              p.sort_tiles + ceil_div(p.fill_end - p.fill_begin, kCtaRows), 1,
+                              kSortThreads, smem, &p, stream));
+      }
     }
   }
   const int E = 16 / es;
@@ -274,12 +292,15 @@ int vcoll_embedding_backward(const void* grad, int64_t grad_ld, int dtype, const
   for (const Operand* o = ops + 1; o < ops + 4; ++o) access = std::min(access, access_of(*o, E));
   p.tiles = ceil_div(D, 32 * E);
   p.sum_ctas = N ? ceil_div(ceil_div(N, p.chunk) * p.tiles, kWarps) : 0;
-  const int64_t fill = in_place ? 0 : ceil_div(V, 32);
-  if (p.sum_ctas + fill > 0x7FFFFFFF)
-    return fail(VCOLL_ERR_UNSUPPORTED, "a table of %lld x %lld is too large", (long long)V,
+  p.fill_begin = p.fill_end;
+  p.fill_end = V;
+  const int64_t grid = p.sum_ctas + ceil_div(V - p.fill_begin, kWarps * kFillRows);
+  if (grid > 0x7FFFFFFF)
+    return fail(VCOLL_ERR_UNSUPPORTED, "%lld rows of %lld columns are too many", (long long)N,
                 (long long)D);
-  VCOLL_TRY(launch_grid(embed_grad_kernel(dtype, table_dtype, access, 0), p.sum_ctas + fill, 1,
-                        kRowThreads, 0, &p, stream));
+  if (grid)
+    VCOLL_TRY(launch_grid(embed_grad_kernel(dtype, table_dtype, access, 0), grid, 1, kRowThreads, 0,
+                          &p, stream));
   if (N <= p.chunk) return VCOLL_OK;  // no token reaches a second chunk
   return launch_grid(embed_grad_kernel(dtype, table_dtype, access, 1), p.sum_ctas, 1, kRowThreads,
                      0, &p, stream);

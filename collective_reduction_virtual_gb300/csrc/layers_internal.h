@@ -31,6 +31,7 @@ constexpr int kSortMaxBits = 9;  // digit width
 constexpr int kSortMaxPasses = 4;
 constexpr int64_t kSortMinTile = 2048;  // keys of a CTA where several sort
 constexpr int kSortMaxTiles = 128;
+constexpr int64_t kFillRows = 2;  // adjacent rows that a warp fills
 constexpr int64_t kJoinAlone = 16;  // partial rows that one warp adds up alone
 struct EmbedGradParams {
   const void* tokens;
@@ -41,12 +42,17 @@ struct EmbedGradParams {
   uint32_t* pos[2];
   uint32_t* cnt;     // digit counts: passes x tiles x 2^bits
   float* part;       // partial rows: chunks x 2 x tiles x (32 * E)
+  uint32_t* stamp;   // V positions (vc_embed_count)
   int64_t N, V, D;
   int64_t grad_ld, base_ld, out_ld;
   int64_t sort_tile;  // keys of a tile of the sort
   int64_t chunk;      // places of the sorted list that a warp sums
   int64_t tiles;      // column tiles
-  int64_t sum_ctas;   // CTAs that sum; the ones behind them fill absent rows
+  int64_t sum_ctas;   // CTAs that sum
+  int64_t fill_begin, fill_end;  // rows that a launch fills where their tokens are absent
+  int fill_bytes;     // of an access of these: 16, 4 or 2
+  int table_es;       // bytes of an element of the table
+  int sort_tiles;
   float scale;
   int idx64;
   int passes, bits, pass;
