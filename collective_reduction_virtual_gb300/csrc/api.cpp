@@ -88,14 +88,16 @@ int allow_dynamic_smem(const void* fn, size_t bytes) {
   return VCOLL_OK;
 }
 
-int resident_blocks(int dev, const void* fn, int threads, size_t smem, int* blocks) {
+// smem_allowed: allow_dynamic_smem has been called for fn with `smem` or more.
+int resident_blocks(int dev, const void* fn, int threads, size_t smem, int* blocks,
+                    bool smem_allowed = false) {
   std::lock_guard<std::mutex> lk(g_mu);
   for (const OccEntry& o : g_occ)
     if (o.dev == dev && o.fn == fn && o.threads == threads && o.smem == smem) {
       *blocks = o.blocks;
       return VCOLL_OK;
     }
-  if (smem > 48 * 1024) {
+  if (smem > 48 * 1024 && !smem_allowed) {
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
   }
@@ -1275,11 +1277,19 @@ int device_sms(int* sms) {
   return current_device(&dev, sms);
 }
 
+int device_residency(const void* fn, int threads, size_t smem, int* blocks) {
+  int dev = 0, sms = 0;
+  int rc = current_device(&dev, &sms);
+  if (rc) return rc;
+  if (smem > 48 * 1024 && (rc = allow_dynamic_smem(fn, kLaunchMaxSmem))) return rc;
+  return resident_blocks(dev, fn, threads, smem, blocks, true);
+}
+
 int launch_grid(const void* fn, int64_t gx, int64_t gy, int threads, size_t smem, void* params,
                 void* stream) {
   void* args[] = {params};
   if (smem > 48 * 1024) {
-    int rc = allow_dynamic_smem(fn, smem);
+    int rc = allow_dynamic_smem(fn, kLaunchMaxSmem);
     if (rc) return rc;
   }
   const cudaError_t e = launch_pdl(fn, dim3((unsigned)gx, (unsigned)gy), dim3((unsigned)threads),

@@ -134,6 +134,44 @@ int access_of(const Operand& o, int most) {
   return 1;
 }
 
+// How a team of warps takes a row of D columns (norm_rows.cuh): two chunks a
+// warp, more where 16 warps do not suffice; 0 chunks: too wide for that.
+struct NormShape {
+  int warps, chunks, threads;
+};
+NormShape norm_shape(int64_t D, int E, bool grad) {
+  const int64_t all = ceil_div(D, 32 * E);
+  NormShape s = {1, 0, kNormCtaWarps * 32};
+  if (all > (int64_t)kNormMaxWarps * norm_max_chunks(E, grad)) return s;
+  s.chunks = all == 1 ? 1 : 2;
+  while (ceil_div(all, s.chunks) > kNormMaxWarps) s.chunks *= 2;
+  s.warps = (int)ceil_div(all, s.chunks);
+  if (s.warps > kNormCtaWarps / 2) {
+    s.threads = s.warps * 32;  // one team
+  } else {
+    while (s.warps & (s.warps - 1)) ++s.warps;  // a power of two of teams
+  }
+  return s;
+}
+
+// Launch of a norm_rows.cuh kernel: as many CTAs as stay resident, at most
+// `most`.  *ctas: how many.
+int launch_norm_rows(const void* fn, const NormShape& s, size_t smem, int64_t most, NormParams* p,
+                     void* stream, int* ctas) {
+  int sms = 0, fit = 0;
+  VCOLL_TRY(device_sms(&sms));
+  VCOLL_TRY(device_residency(fn, s.threads, smem, &fit));
+  const int64_t need = ceil_div(p->N, s.threads / 32 / s.warps);
+  *ctas = (int)std::min(most, std::min<int64_t>(need, (int64_t)sms * fit));
+  return launch_grid(fn, *ctas, 1, s.threads, smem, p, stream);
+}
+
+// Access of two matrices: fp32 rows are taken in 16 or 4 bytes, bf16 in 16, 4 or 2.
+int row_access(int a, int b, int dtype) {
+  const int both = std::min(a, b);
+  return dtype == VCOLL_F32 && both == 2 ? 1 : both;
+}
+
 // Up to this many tokens one CTA sorts.
 constexpr int64_t kSortOneCta = 4096;
 
@@ -359,9 +397,23 @@ static int norm_forward(const void* x, int64_t x_ld, const void* weight, const v
   p.codes_ld = codes_ld;
   p.eps = eps;
   p.wbf16 = weight_dtype == VCOLL_BF16;
-  int64_t grid;
-  VCOLL_TRY(grid_for(N, 1, 32, &grid));
-  return launch_grid(norm_kernel(dtype), grid, 1, kRowThreads, 0, &p, stream);
+  const int E = 16 / es;
+  const NormShape s = norm_shape(D, E, false);
+  if (!s.chunks) {
+    int64_t grid;
+    VCOLL_TRY(grid_for(N, 1, 32, &grid));
+    return launch_grid(norm_wide_kernel(dtype), grid, 1, kRowThreads, 0, &p, stream);
+  }
+  p.warps = s.warps;
+  const int access = row_access(access_of(ops[0], E), access_of(ops[3], E), dtype);
+  const void* fn = dtype == VCOLL_F32 ? norm_rows_kernel_f32(access, s.chunks, false, keep)
+                                      : norm_rows_kernel_bf16(access, s.chunks, false, keep);
+  // the ring, weight and bias, and two partial sums of 8 bytes a warp
+  const size_t smem = (size_t)s.threads * 16 * s.chunks *
+                          (norm_stages(s.chunks, false) + (norm_keeps_weight(s.chunks) ? 2 * E / 4 : 0)) +
+                      s.threads / 2;
+  int ctas;
+  return launch_norm_rows(fn, s, smem, kMaxExtent, &p, stream, &ctas);
 }
 
 static int norm_backward(const void* grad, int64_t grad_ld, const void* x, int64_t x_ld,
@@ -411,12 +463,32 @@ static int norm_backward(const void* grad, int64_t grad_ld, const void* x, int64
   p.y_ld = dx_ld;
   p.codes_ld = codes_ld;
   p.wbf16 = weight_dtype == VCOLL_BF16;
-  if (dweight || dbias)
-    VCOLL_TRY(launch_grid(norm_wgrad_kernel(dtype), ceil_div(D, 32), 1, kRowThreads, 0, &p, stream));
-  if (!dx || !N) return VCOLL_OK;
-  int64_t grid;
-  VCOLL_TRY(grid_for(N, 1, 32, &grid));
-  return launch_grid(norm_grad_kernel(dtype), grid, 1, kRowThreads, 0, &p, stream);
+  const int E = 16 / es;
+  const NormShape s = norm_shape(D, E, true);
+  if (!s.chunks) {
+    if (dweight || dbias)
+      VCOLL_TRY(launch_grid(norm_wgrad_wide_kernel(dtype), ceil_div(D, 32), 1, kRowThreads, 0, &p, stream));
+    if (!dx || !N) return VCOLL_OK;
+    int64_t grid;
+    VCOLL_TRY(grid_for(N, 1, 32, &grid));
+    return launch_grid(norm_grad_wide_kernel(dtype), grid, 1, kRowThreads, 0, &p, stream);
+  }
+  if (!dx && !dweight && !dbias) return VCOLL_OK;
+  if (N) {
+    p.warps = s.warps;
+    p.part = dweight || dbias ? (float*)workspace : nullptr;
+    int access = row_access(access_of(ops[0], E), access_of(ops[7], E), dtype);
+    if (!kept) access = row_access(access, access_of(ops[1], E), dtype);
+    const void* fn = dtype == VCOLL_F32 ? norm_rows_kernel_f32(access, s.chunks, true, kept)
+                                        : norm_rows_kernel_bf16(access, s.chunks, true, kept);
+    const size_t smem = (size_t)s.threads *
+                            (norm_stages(s.chunks, true) * norm_grad_slot_bytes(s.chunks, E, kept) +
+                             (norm_keeps_weight(s.chunks) ? s.chunks * E * 4 : 0)) +
+                        s.threads / 2;
+    VCOLL_TRY(launch_norm_rows(fn, s, smem, kNormMaxCtas, &p, stream, &p.parts));
+  }
+  if (!dweight && !dbias) return VCOLL_OK;
+  return launch_grid(norm_wsum_kernel(), ceil_div(D, 32), 2, 1024, 0, &p, stream);
 }
 
 int vcoll_layer_norm(const void* x, int64_t x_ld, const void* weight, const void* bias,
@@ -435,9 +507,9 @@ int vcoll_layer_norm_checkpoint8(const void* x, int64_t x_ld, const void* weight
 }
 
 size_t vcoll_layer_norm_workspace_bytes(int64_t N, int64_t D) {
-  (void)N;
-  (void)D;
-  return 0;
+  // partial rows of the CTAs, for rows that a team holds (in either type)
+  if (N <= 0 || D <= 0 || D > kNormMaxWarps * 32 * 32) return 0;
+  return (size_t)std::min<int64_t>(N, kNormMaxCtas) * 2 * (size_t)D * sizeof(float);
 }
 
 int vcoll_layer_norm_backward(const void* grad, int64_t grad_ld, const void* x, int64_t x_ld,
@@ -461,6 +533,12 @@ int vcoll_layer_norm_backward_checkpoint8(const void* grad, int64_t grad_ld, con
                        workspace_bytes, stream);
 }
 
+static int launch_pack(const void* fn, int E, PackParams* p, void* stream) {
+  while ((1 << p->row_shift) < kWarps && ((int64_t)(kPackChunks * 32 * E) << p->row_shift) < p->D)
+    ++p->row_shift;
+  return launch_grid(fn, ceil_div(p->N, kWarps >> p->row_shift), 1, kRowThreads, 0, p, stream);
+}
+
 int vcoll_checkpoint8(const void* x, int64_t x_ld, int64_t N, int64_t D, int8_t* codes,
                       int64_t codes_ld, float* scales, int dtype, void* stream) {
   VCOLL_TRY(norm_checks(N, D, dtype, VCOLL_F32));
@@ -471,6 +549,7 @@ int vcoll_checkpoint8(const void* x, int64_t x_ld, int64_t N, int64_t D, int8_t*
   VCOLL_TRY(check_codes(codes, codes_ld, N, D));
   VCOLL_TRY(check_operands(ops, 3));
   if (!N || !D) return VCOLL_OK;
+  const int E = 16 / elem_size(dtype);
   PackParams p = {};
   p.x = x;
   p.codes = codes;
@@ -479,9 +558,7 @@ int vcoll_checkpoint8(const void* x, int64_t x_ld, int64_t N, int64_t D, int8_t*
   p.D = D;
   p.x_ld = x_ld;
   p.codes_ld = codes_ld;
-  int64_t grid;
-  VCOLL_TRY(grid_for(N * B, kWarps, 32, &grid));
-  return launch_grid(pack8_kernel(dtype), grid, 1, kRowThreads, 0, &p, stream);
+  return launch_pack(pack8_kernel(dtype, row_access(access_of(ops[0], E), E, dtype)), E, &p, stream);
 }
 
 int vcoll_checkpoint8_restore(const int8_t* codes, int64_t codes_ld, const float* scales,
@@ -498,6 +575,7 @@ int vcoll_checkpoint8_restore(const int8_t* codes, int64_t codes_ld, const float
   VCOLL_TRY(check_codes(codes, codes_ld, N, D));
   VCOLL_TRY(check_operands(ops, 5));
   if (!N || !D) return VCOLL_OK;
+  const int E = 16 / elem_size(dtype);
   PackParams p = {};
   p.out = out;
   p.weight = weight;
@@ -509,9 +587,7 @@ int vcoll_checkpoint8_restore(const int8_t* codes, int64_t codes_ld, const float
   p.x_ld = out_ld;
   p.codes_ld = codes_ld;
   p.wbf16 = weight_dtype == VCOLL_BF16;
-  int64_t grid;
-  VCOLL_TRY(grid_for(N, 1, 32, &grid));
-  return launch_grid(unpack8_kernel(dtype), grid, 1, kRowThreads, 0, &p, stream);
+  return launch_pack(unpack8_kernel(dtype, row_access(access_of(ops[4], E), E, dtype)), E, &p, stream);
 }
 
 }  // extern "C"

@@ -75,7 +75,28 @@ struct NormParams {
   int64_t x_ld, grad_ld, y_ld, codes_ld;
   float eps;
   int wbf16;  // weight, bias, dweight, dbias are bf16
+  int warps;  // that take a row
+  int parts;  // partial rows of the gradient (CTAs)
 };
+
+// norm_rows.cuh: slots of the ring of rows on their way, warps of a CTA of
+// several teams, and of the largest team.
+VCOLL_HD constexpr int norm_stages(int R, bool grad) { return R <= 2 ? 4 : grad && R == 8 ? 1 : 2; }
+// weight and bias stay in shared memory
+VCOLL_HD constexpr bool norm_keeps_weight(int R) { return R <= 2; }
+constexpr int kNormCtaWarps = 8;
+constexpr int kNormMaxWarps = 16;
+// CTAs of the gradient at most: its partial rows' room in the workspace.
+constexpr int kNormMaxCtas = 608;
+// columns up to which a team's registers hold a row, forward and backward:
+// kNormMaxWarps warps of 8 chunks, or of 4 where 8 values a lane and chunk
+// are summed over the rows too
+VCOLL_HD constexpr int norm_max_chunks(int E, bool grad) { return grad && E == 8 ? 4 : 8; }
+// bytes of a thread's slots of one stage of the backward ring
+VCOLL_HD constexpr int norm_grad_slot_bytes(int R, int E, bool kept) {
+  return R * 16 + (kept ? R * E + R * 8 : R * 16) + 8;
+}
+
 
 struct PackParams {
   const void* x;
@@ -87,7 +108,9 @@ struct PackParams {
   int64_t N, D;
   int64_t x_ld, codes_ld;  // x_ld: of x or out
   int wbf16;
+  int row_shift;  // log2 of the warps that take a row
 };
+constexpr int kPackChunks = 4;  // chunks that a warp has in flight
 
 // access: elements of an access (a whole 16 bytes of dtype, 2 or 1)
 const void* embed_kernel(int dtype, int access);
@@ -95,10 +118,13 @@ const void* embed_sort_kernel();
 const void* embed_count_kernel();
 const void* embed_scatter_kernel();
 const void* embed_grad_kernel(int dtype, int table_dtype, int access, int join);
-const void* norm_kernel(int dtype);
-const void* norm_grad_kernel(int dtype);
-const void* norm_wgrad_kernel(int dtype);
-const void* pack8_kernel(int dtype);
-const void* unpack8_kernel(int dtype);
+const void* norm_rows_kernel_f32(int access, int chunks, bool grad, bool kept);
+const void* norm_rows_kernel_bf16(int access, int chunks, bool grad, bool kept);
+const void* norm_wsum_kernel();
+const void* norm_wide_kernel(int dtype);
+const void* norm_grad_wide_kernel(int dtype);
+const void* norm_wgrad_wide_kernel(int dtype);
+const void* pack8_kernel(int dtype, int access);
+const void* unpack8_kernel(int dtype, int access);
 
 }  // namespace vcoll

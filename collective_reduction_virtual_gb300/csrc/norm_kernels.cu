@@ -1,33 +1,15 @@
-// Layer norm, its gradient, and activations kept in 8 bits.
-#include "device_common.cuh"
-#include "layers_internal.h"
+// Layer norm and its gradient for rows of any width, the gradient's last sum,
+// and 8-bit activations.
+#include "norm_common.cuh"
 
 namespace vcoll {
 
+// ------------------------------------------------------ rows of any width
+// For rows wider than a team of warps holds (norm_rows.cuh): a CTA per row
+// that reads it again for each step, from L2 after the first; element by
+// element, since such rows are rare and long enough to hide it.
+
 namespace {
-
-constexpr int kBlock8 = VCOLL_CHECKPOINT8_BLOCK;
-constexpr float kTiny8 = 7.888609052210118e-31f;  // 2^-100
-
-template <typename T>
-__device__ __forceinline__ float load1(const void* base, int64_t i) {
-  return Elem<T>::widen1(static_cast<const typename Elem<T>::Bits*>(base)[i]);
-}
-template <typename T>
-__device__ __forceinline__ void store1(void* base, int64_t i, float f) {
-  static_cast<typename Elem<T>::Bits*>(base)[i] = Elem<T>::narrow1(f);
-}
-// weights and biases, in either type; `none` where there is no such buffer
-__device__ __forceinline__ float loadw(const void* w, int bf16, int64_t i, float none) {
-  if (!w) return none;
-  return bf16 ? load1<__nv_bfloat16>(w, i) : load1<float>(w, i);
-}
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
-  return v;
-}
 
 // Sum over the CTA, the same in every thread.
 __device__ __forceinline__ float block_sum(float v, float* red) {
@@ -39,64 +21,25 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return warp_sum(lane < (int)(blockDim.x >> 5) ? red[lane] : 0.0f);
 }
 
-// The largest magnitude over a warp, NaN if any value is NaN.
-__device__ __forceinline__ float warp_top(float a) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    const float b = __shfl_xor_sync(~0u, a, d);
-    a = (b > a || b != b) ? b : a;
-  }
-  return a;
-}
-struct Scale8 {
-  float scale, unit;
-};
-__device__ __forceinline__ Scale8 scale8(float top) {
-  Scale8 s;
-  if (!(top <= 3.402823466e38f)) {  // infinity or NaN
-    s.scale = __uint_as_float(0x7FC00000u);
-    s.unit = 0.0f;
-  } else if (top < kTiny8) {
-    s.scale = s.unit = 0.0f;
-  } else {
-    s.scale = __fdiv_rn(top, 127.0f);
-    s.unit = __fdiv_rn(127.0f, top);
-  }
-  return s;
-}
-__device__ __forceinline__ int8_t code8(float x, const Scale8& s) {
-  // a zero unit (zeros, or a block with a NaN or an infinity) gives code 0
-  return s.unit == 0.0f ? (int8_t)0 : (int8_t)__float2int_rn(__fmul_rn(x, s.unit));
-}
-
 // One warp keeps one block of 128 columns; value(c) gives column c's value.
 template <typename F>
 __device__ __forceinline__ void keep_block(int64_t b, int64_t D, int8_t* codes, float* scale,
                                            F value) {
-  const int lane = threadIdx.x & 31;
-  float v[4], top = 0.0f;
+  float v[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int64_t c = b * kBlock8 + k * 32 + lane;
+    const int64_t c = b * kBlock8 + k * 32 + (threadIdx.x & 31);
     v[k] = c < D ? value(c) : 0.0f;
-    const float a = fabsf(v[k]);
-    top = (a > top || a != a) ? a : top;
   }
-  const Scale8 s = scale8(warp_top(top));
-  const int64_t end = (D + 15) / 16 * 16;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int64_t c = b * kBlock8 + k * 32 + lane;
-    if (c < end) codes[c] = c < D ? code8(v[k], s) : (int8_t)0;
-  }
-  if (lane == 0) *scale = s.scale;
+  // as fp32 in single elements: 4 groups of 32 columns, one block
+  keep8<float, 1>(v, b * kBlock8 + (threadIdx.x & 31), 0, D, codes, scale);
 }
 
 }  // namespace
 
 // One CTA per row: the mean, the deviations' squares, then the outputs.
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) vc_norm(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kRowThreads) vc_norm_wide(const __grid_constant__ NormParams p) {
   pdl_enter();
   __shared__ float red[kRowThreads / 32];
   for (int64_t i = blockIdx.x; i < p.N; i += gridDim.x) {
@@ -120,7 +63,7 @@ __global__ void __launch_bounds__(kRowThreads) vc_norm(const __grid_constant__ N
     for (int64_t c = threadIdx.x; c < p.D; c += kRowThreads) {
       const float h = (load1<T>(p.x, at + c) - mean) * rstd;
       store1<T>(p.y, i * p.y_ld + c,
-                h * loadw(p.weight, p.wbf16, c, 1.0f) + loadw(p.bias, p.wbf16, c, 0.0f));
+                h * load_weight(p.weight, p.wbf16, c, 1.0f) + load_weight(p.bias, p.wbf16, c, 0.0f));
     }
     if (threadIdx.x == 0) {
       if (p.mean) p.mean[i] = mean;
@@ -142,30 +85,30 @@ __device__ __forceinline__ float normal_at(const NormParams& p, int64_t i, int64
 
 // One CTA per row: the two sums of the row, then dx.
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) vc_norm_grad(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kRowThreads) vc_norm_grad_wide(const __grid_constant__ NormParams p) {
   pdl_enter();
   __shared__ float red[kRowThreads / 32];
   for (int64_t i = blockIdx.x; i < p.N; i += gridDim.x) {
     const float mean = p.x ? p.mean[i] : 0.0f, rstd = p.rstd[i];
     float s1 = 0.0f, s2 = 0.0f;
     for (int64_t c = threadIdx.x; c < p.D; c += kRowThreads) {
-      const float g = load1<T>(p.grad, i * p.grad_ld + c) * loadw(p.weight, p.wbf16, c, 1.0f);
+      const float g = load1<T>(p.grad, i * p.grad_ld + c) * load_weight(p.weight, p.wbf16, c, 1.0f);
       s1 += g;
       s2 += g * normal_at<T>(p, i, c, mean, rstd);
     }
     s1 = block_sum(s1, red) / (float)p.D;
     s2 = block_sum(s2, red) / (float)p.D;
     for (int64_t c = threadIdx.x; c < p.D; c += kRowThreads) {
-      const float g = load1<T>(p.grad, i * p.grad_ld + c) * loadw(p.weight, p.wbf16, c, 1.0f);
+      const float g = load1<T>(p.grad, i * p.grad_ld + c) * load_weight(p.weight, p.wbf16, c, 1.0f);
       store1<T>(p.y, i * p.y_ld + c, (g - s1 - normal_at<T>(p, i, c, mean, rstd) * s2) * rstd);
     }
   }
 }
 
 // One CTA per 32 columns: its warps sum every eighth row, then their sums.
-// It runs before vc_norm_grad, which may write dx over grad or x.
+// It runs before vc_norm_grad_wide, which may write dx over grad or x.
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) vc_norm_wgrad(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kRowThreads) vc_norm_wgrad_wide(const __grid_constant__ NormParams p) {
   pdl_enter();
   constexpr int NW = kRowThreads / 32;
   __shared__ float sw[NW][32], sb[NW][32];
@@ -196,39 +139,135 @@ __global__ void __launch_bounds__(kRowThreads) vc_norm_wgrad(const __grid_consta
   }
 }
 
-// One warp per block of 128 columns.
-template <typename T>
+// ------------------------------------------ the gradient's sum over the CTAs
+
+// part[cta][2][D] summed over the CTAs: a CTA per 32 columns of one of the
+// two; its warps take every 32nd row, and the first one adds up their sums.
+__global__ void __launch_bounds__(1024) vc_norm_wsum(const __grid_constant__ NormParams p) {
+  pdl_enter();
+  __shared__ float sum[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  void* out = blockIdx.y ? p.dbias : p.dweight;
+  if (!out) return;
+  float s = 0.0f;
+  if (c < p.D) {
+    const float* from = p.part + blockIdx.y * p.D + c;
+#pragma unroll 8
+    for (int k = warp; k < p.parts; k += 32) s += from[(int64_t)k * 2 * p.D];
+  }
+  sum[warp][lane] = s;
+  __syncthreads();
+  s = warp_sum(sum[lane][warp]);  // column `warp` of this CTA's
+  const int64_t col = (int64_t)blockIdx.x * 32 + warp;
+  if (lane || col >= p.D) return;
+  if (p.wbf16) store1<__nv_bfloat16>(out, col, s);
+  else store1<float>(out, col, s);
+}
+
+// ------------------------------------------------------- 8-bit activations
+// A row is taken by 2^row_shift adjacent warps of a CTA, kPackChunks chunks of
+// 32 * E columns at a time, all of their loads in flight.
+
+template <typename T, int A>
 __global__ void __launch_bounds__(kRowThreads) vc_pack8(const __grid_constant__ PackParams p) {
   pdl_enter();
-  const int64_t blocks = (p.D + kBlock8 - 1) / kBlock8;
-  const int64_t step = (int64_t)gridDim.x * (kRowThreads / 32);
-  for (int64_t k = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); k < p.N * blocks;
-       k += step) {
-    const int64_t i = k / blocks, b = k % blocks;
-    keep_block(b, p.D, p.codes + i * p.codes_ld, p.scales + k,
-               [&](int64_t c) { return load1<T>(p.x, i * p.x_ld + c); });
+  using P = Pieces<T, A>;
+  constexpr int E = P::E;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t i = (int64_t)blockIdx.x * ((kRowThreads / 32) >> p.row_shift) + (warp >> p.row_shift);
+  if (i >= p.N) return;
+  const char* x = elem_at<T>(p.x, i * p.x_ld);
+  int8_t* codes = p.codes + i * p.codes_ld;
+  float* scales = p.scales + i * ((p.D + kBlock8 - 1) / kBlock8);
+  const int64_t step = (int64_t)(kPackChunks * 32 * E) << p.row_shift;
+  for (int64_t c0 = (int64_t)(warp & ((1 << p.row_shift) - 1)) * (kPackChunks * 32 * E); c0 < p.D; c0 += step) {
+    Raw<T, A> raw[kPackChunks][E / A];
+#pragma unroll
+    for (int k = 0; k < kPackChunks; ++k) P::load(raw[k], x, c0 + k * 32 * E + lane * A, p.D);
+#pragma unroll
+    for (int k = 0; k < kPackChunks; ++k) {
+      const int64_t base = c0 + k * 32 * E;
+      if (base >= p.D) break;
+      float f[E];
+      P::widen(raw[k], f);
+      keep8<T, A>(f, base + lane * A, base / kBlock8, p.D, codes, scales);
+    }
   }
 }
 
-template <typename T>
+template <typename T, int A>
 __global__ void __launch_bounds__(kRowThreads) vc_unpack8(const __grid_constant__ PackParams p) {
   pdl_enter();
-  const int64_t blocks = (p.D + kBlock8 - 1) / kBlock8;
-  for (int64_t i = blockIdx.x; i < p.N; i += gridDim.x)
-    for (int64_t c = threadIdx.x; c < p.D; c += kRowThreads) {
-      const float h = (float)p.codes[i * p.codes_ld + c] * p.scales[i * blocks + c / kBlock8];
-      store1<T>(p.out, i * p.x_ld + c,
-                h * loadw(p.weight, p.wbf16, c, 1.0f) + loadw(p.bias, p.wbf16, c, 0.0f));
+  using P = Pieces<T, A>;
+  constexpr int E = P::E;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t i = (int64_t)blockIdx.x * ((kRowThreads / 32) >> p.row_shift) + (warp >> p.row_shift);
+  if (i >= p.N) return;
+  char* out = elem_at<T>(p.out, i * p.x_ld);
+  const int8_t* codes = p.codes + i * p.codes_ld;
+  const float* scales = p.scales + i * ((p.D + kBlock8 - 1) / kBlock8);
+  const int64_t step = (int64_t)(kPackChunks * 32 * E) << p.row_shift;
+  for (int64_t c0 = (int64_t)(warp & ((1 << p.row_shift) - 1)) * (kPackChunks * 32 * E); c0 < p.D; c0 += step) {
+    uint32_t word[kPackChunks][E / 4];
+    float scale[kPackChunks][E / A];
+#pragma unroll
+    for (int k = 0; k < kPackChunks; ++k) {
+      const int64_t c = c0 + k * 32 * E + lane * A;
+#pragma unroll
+      for (int w = 0; w < E / 4; ++w) word[k][w] = 0u;
+#pragma unroll
+      for (int j = 0; j < E / A; ++j) {
+        const int64_t at = c + j * 32 * A;
+        if (at >= p.D) {
+          scale[k][j] = 0.0f;
+          continue;
+        }
+        scale[k][j] = scales[at / kBlock8];
+        if constexpr (A == 8) {
+          const uint2 v = *reinterpret_cast<const uint2*>(codes + at);
+          word[k][0] = v.x;
+          word[k][1] = v.y;
+        } else if constexpr (A == 4) {
+          word[k][j] = *reinterpret_cast<const uint32_t*>(codes + at);
+        } else {
+#pragma unroll
+          for (int a = 0; a < A; ++a)
+            word[k][(j * A + a) / 4] |= (uint32_t)(uint8_t)codes[at + a] << (8 * ((j * A + a) % 4));
+        }
+      }
     }
+#pragma unroll
+    for (int k = 0; k < kPackChunks; ++k) {
+      const int64_t c = c0 + k * 32 * E + lane * A;
+      if (c0 + k * 32 * E >= p.D) break;
+      float f[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        f[e] = code_value(word[k][e / 4], e % 4) * scale[k][e / A];
+        const int64_t at = c + P::offset(e);
+        if ((p.weight || p.bias) && at < p.D)
+          f[e] = fmaf(f[e], load_weight(p.weight, p.wbf16, at, 1.0f), load_weight(p.bias, p.wbf16, at, 0.0f));
+      }
+      P::store(out, c, p.D, f);
+    }
+  }
 }
 
 #define VCOLL_BY_TYPE(fn) \
   (dtype == VCOLL_F32 ? (const void*)&fn<float> : (const void*)&fn<__nv_bfloat16>)
-const void* norm_kernel(int dtype) { return VCOLL_BY_TYPE(vc_norm); }
-const void* norm_grad_kernel(int dtype) { return VCOLL_BY_TYPE(vc_norm_grad); }
-const void* norm_wgrad_kernel(int dtype) { return VCOLL_BY_TYPE(vc_norm_wgrad); }
-const void* pack8_kernel(int dtype) { return VCOLL_BY_TYPE(vc_pack8); }
-const void* unpack8_kernel(int dtype) { return VCOLL_BY_TYPE(vc_unpack8); }
+#define VCOLL_BY_ACCESS(fn)                                                                \
+  (dtype == VCOLL_F32 ? access == 4 ? (const void*)&fn<float, 4> : (const void*)&fn<float, 1> \
+   : access == 8      ? (const void*)&fn<__nv_bfloat16, 8>                                 \
+   : access == 2      ? (const void*)&fn<__nv_bfloat16, 2>                                 \
+                      : (const void*)&fn<__nv_bfloat16, 1>)
+const void* norm_wide_kernel(int dtype) { return VCOLL_BY_TYPE(vc_norm_wide); }
+const void* norm_grad_wide_kernel(int dtype) { return VCOLL_BY_TYPE(vc_norm_grad_wide); }
+const void* norm_wgrad_wide_kernel(int dtype) { return VCOLL_BY_TYPE(vc_norm_wgrad_wide); }
+const void* norm_wsum_kernel() { return (const void*)&vc_norm_wsum; }
+const void* pack8_kernel(int dtype, int access) { return VCOLL_BY_ACCESS(vc_pack8); }
+const void* unpack8_kernel(int dtype, int access) { return VCOLL_BY_ACCESS(vc_unpack8); }
 #undef VCOLL_BY_TYPE
+#undef VCOLL_BY_ACCESS
 
 }  // namespace vcoll

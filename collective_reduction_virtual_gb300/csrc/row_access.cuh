@@ -89,15 +89,20 @@ struct Raw {
       for (int a = 0; a < A; a += 2) Elem<__nv_bfloat16>::widen2(w[a / 2], f[a], f[a + 1]);
     }
   }
+  // computed values: a NaN becomes the canonical one
   __device__ __forceinline__ void narrow(const float (&f)[A]) {
     if constexpr (Elem<T>::kBytes == 4) {
 #pragma unroll
       for (int a = 0; a < A; ++a) w[a] = __float_as_uint(f[a]);
     } else if constexpr (A == 1) {
-      w[0] = Elem<__nv_bfloat16>::narrow1(f[0]);
+      const __nv_bfloat16 h = __float2bfloat16_rn(f[0]);
+      w[0] = *reinterpret_cast<const uint16_t*>(&h);
     } else {
 #pragma unroll
-      for (int a = 0; a < A; a += 2) w[a / 2] = Elem<__nv_bfloat16>::narrow2(f[a], f[a + 1]);
+      for (int a = 0; a < A; a += 2) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[a], f[a + 1]);
+        w[a / 2] = *reinterpret_cast<const uint32_t*>(&h);
+      }
     }
   }
 };
@@ -113,6 +118,29 @@ __device__ __forceinline__ char* elem_at(void* base, int64_t i) {
 
 __device__ __forceinline__ int64_t token_at(const void* tokens, int idx64, int64_t i) {
   return idx64 ? static_cast<const int64_t*>(tokens)[i] : static_cast<const int32_t*>(tokens)[i];
+}
+
+// cp.async: each thread fetches its own pieces into its own slots of shared
+// memory and waits for them alone, so a ring of such slots keeps several rows
+// in flight without registers and without a barrier between threads.
+template <int BYTES>
+__device__ __forceinline__ void fetch_async(void* slot, const void* from) {
+  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(slot));
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+  else if constexpr (BYTES == 8)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at), "l"(from) : "memory");
+  else if constexpr (BYTES == 4)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at), "l"(from) : "memory");
+  else if constexpr (BYTES == 2)  // below the smallest asynchronous copy
+    *static_cast<uint16_t*>(slot) = *static_cast<const uint16_t*>(from);
+  else
+    *static_cast<uint8_t*>(slot) = *static_cast<const uint8_t*>(from);
+}
+__device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void fetch_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 }  // namespace vcoll

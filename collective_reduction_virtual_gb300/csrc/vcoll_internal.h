@@ -242,10 +242,13 @@ int report_error(int status, const char* message);
 
 // Launch of one kernel whose only parameter is the struct at `params`, with
 // programmatic stream serialization (the kernel starts with pdl_enter).
-// smem: dynamic shared memory, always the same for one kernel when it is
-// above 48 KB.  Returns a status with its message set.
+// smem: dynamic shared memory, up to kLaunchMaxSmem.  Returns a status with
+// its message set.
+constexpr size_t kLaunchMaxSmem = 208 * 1024;
 int launch_grid(const void* fn, int64_t gx, int64_t gy, int threads, size_t smem, void* params,
                 void* stream);
+// CTAs of that launch that fit on an SM of the current device at once.
+int device_residency(const void* fn, int threads, size_t smem, int* blocks);
 // SM count of the current device.
 int device_sms(int* sms);
 

@@ -345,7 +345,8 @@ int vcoll_sparse_allreduce_noalloc(const void* const* in, void* const* out, void
  *  - Buffers of one call may not overlap, except where a call names an
  *    in-place form; matrices that are different column ranges of the same
  *    wider rows (equal row strides in bytes) do not overlap.
- *  - Sums, means and statistics are fp32; a bf16 output is rounded once.
+ *  - Sums, means and statistics are fp32; a bf16 output is rounded once (a
+ *    computed NaN is the canonical one of the conversion).
  *    The order of every sum is fixed by the sizes and the GPU alone, so a
  *    call repeated on the same inputs gives the same bits.
  *  - `workspace`: device memory of the size the *_workspace_bytes function
