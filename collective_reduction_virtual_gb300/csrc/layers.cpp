@@ -405,13 +405,13 @@ static int norm_forward(const void* x, int64_t x_ld, const void* weight, const v
     return launch_grid(norm_wide_kernel(dtype), grid, 1, kRowThreads, 0, &p, stream);
   }
   p.warps = s.warps;
-  const int access = row_access(access_of(ops[0], E), access_of(ops[3], E), dtype);
+  int access = E;
+  for (int k = 0; k < 4; ++k) access = row_access(access, access_of(ops[k], E), dtype);
   const void* fn = dtype == VCOLL_F32 ? norm_rows_kernel_f32(access, s.chunks, false, keep)
                                       : norm_rows_kernel_bf16(access, s.chunks, false, keep);
-  // the ring, weight and bias, and two partial sums of 8 bytes a warp
-  const size_t smem = (size_t)s.threads * 16 * s.chunks *
-                          (norm_stages(s.chunks, false) + (norm_keeps_weight(s.chunks) ? 2 * E / 4 : 0)) +
-                      s.threads / 2;
+  // the ring, and two partial sums of 8 bytes a warp
+  const size_t smem =
+      (size_t)s.threads * 16 * s.chunks * norm_stages(s.chunks, false) + s.threads / 2;
   int ctas;
   return launch_norm_rows(fn, s, smem, kMaxExtent, &p, stream, &ctas);
 }
@@ -477,14 +477,12 @@ static int norm_backward(const void* grad, int64_t grad_ld, const void* x, int64
   if (N) {
     p.warps = s.warps;
     p.part = dweight || dbias ? (float*)workspace : nullptr;
-    int access = row_access(access_of(ops[0], E), access_of(ops[7], E), dtype);
-    if (!kept) access = row_access(access, access_of(ops[1], E), dtype);
+    int access = E;
+    for (int k : {0, 1, 6, 7}) access = row_access(access, access_of(ops[k], E), dtype);
     const void* fn = dtype == VCOLL_F32 ? norm_rows_kernel_f32(access, s.chunks, true, kept)
                                         : norm_rows_kernel_bf16(access, s.chunks, true, kept);
-    const size_t smem = (size_t)s.threads *
-                            (norm_stages(s.chunks, true) * norm_grad_slot_bytes(s.chunks, E, kept) +
-                             (norm_keeps_weight(s.chunks) ? s.chunks * E * 4 : 0)) +
-                        s.threads / 2;
+    const size_t smem = (size_t)s.threads * norm_stages(s.chunks, true) *
+                            norm_grad_slot_bytes(s.chunks, E, kept) + s.threads / 2;
     VCOLL_TRY(launch_norm_rows(fn, s, smem, kNormMaxCtas, &p, stream, &p.parts));
   }
   if (!dweight && !dbias) return VCOLL_OK;

@@ -82,8 +82,6 @@ struct NormParams {
 // norm_rows.cuh: slots of the ring of rows on their way, warps of a CTA of
 // several teams, and of the largest team.
 VCOLL_HD constexpr int norm_stages(int R, bool grad) { return R <= 2 ? 4 : grad && R == 8 ? 1 : 2; }
-// weight and bias stay in shared memory
-VCOLL_HD constexpr bool norm_keeps_weight(int R) { return R <= 2; }
 constexpr int kNormCtaWarps = 8;
 constexpr int kNormMaxWarps = 16;
 // CTAs of the gradient at most: its partial rows' room in the workspace.

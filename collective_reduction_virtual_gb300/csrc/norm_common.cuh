@@ -45,6 +45,31 @@ struct Pieces {
       if (c + j * 32 * A < D)
         fetch_async<BYTES>(static_cast<char*>(slot) + j * BYTES, elem_at<T>(row, c + j * 32 * A));
   }
+  // The weight (or bias) of the thread's columns, in either type, from a place
+  // that allows accesses of A elements; ones or zeros where there is none.
+  static __device__ __forceinline__ void weights(const void* w, int bf16, int c, int D, float none,
+                                                 float (&f)[E]) {
+#pragma unroll
+    for (int j = 0; j < E / A; ++j) {
+      float g[A];
+#pragma unroll
+      for (int a = 0; a < A; ++a) g[a] = none;
+      const int at = c + j * 32 * A;
+      if (w && at < D) {
+        if (bf16) {
+          Raw<__nv_bfloat16, A> v;
+          v.load(elem_at<__nv_bfloat16>(w, at));
+          v.widen(g);
+        } else {
+          Raw<float, A> v;
+          v.load(elem_at<float>(w, at));
+          v.widen(g);
+        }
+      }
+#pragma unroll
+      for (int a = 0; a < A; ++a) f[j * A + a] = g[a];
+    }
+  }
   static __device__ __forceinline__ void load(Raw<T, A> (&v)[E / A], const void* row, int64_t c, int64_t D) {
 #pragma unroll
     for (int j = 0; j < E / A; ++j) {
@@ -109,7 +134,8 @@ __device__ __forceinline__ float code_value(uint32_t word, int k) {
 }
 
 // Keeps a lane's E values of a chunk: its codes and, from one lane, the
-// chunk's scales.  c: the lane's first column; block: the chunk's first block.
+// chunk's scales.  Values past the row's end are 0.  c: the lane's first
+// column; block: the chunk's first block.
 template <typename T, int A>
 __device__ __forceinline__ void keep8(const float (&f)[kLane<T>], int64_t c, int64_t block, int64_t D,
                                       int8_t* codes, float* scales) {
@@ -123,7 +149,7 @@ __device__ __forceinline__ void keep8(const float (&f)[kLane<T>], int64_t c, int
   for (int b = 0; b < B; ++b) top[b] = 0u;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const uint32_t m = c + offset(e) < D ? magnitude_bits(f[e]) : 0u;
+    const uint32_t m = magnitude_bits(f[e]);
 #pragma unroll
     for (int b = 0; b < B; ++b)
       if (block_of(e) == b) top[b] = max(top[b], m);
@@ -140,7 +166,7 @@ __device__ __forceinline__ void keep8(const float (&f)[kLane<T>], int64_t c, int
       const int in = block_of(k + e);
       const float unit = B == 1 || in == 0 ? s[0].unit : s[B - 1].unit;
       mask = B == 1 || in == 0 ? s[0].mask : s[B - 1].mask;
-      q[e] = c + offset(k + e) < D ? code_bits(f[k + e], unit) : 0u;
+      q[e] = code_bits(f[k + e], unit);
     }
     word[k / 4] = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410) & mask;
   }

@@ -47,50 +47,29 @@ __device__ __forceinline__ int team_col(const Team& t, int r) {
   return (t.warp + t.warps * r) * 32 * kLane<T> + t.lane * A;
 }
 
-// fp32 values of a thread's E elements lie 16 bytes apart per thread.
-template <int E>
-__device__ __forceinline__ void read_slots(const float* base, int threads, float (&f)[E]) {
-#pragma unroll
-  for (int k = 0; k < E; k += 4) {
-    const float4 v = *reinterpret_cast<const float4*>(base + (size_t)(k / 4) * threads * 4);
-    f[k] = v.x;
-    f[k + 1] = v.y;
-    f[k + 2] = v.z;
-    f[k + 3] = v.w;
-  }
-}
-
-// The weight (or bias) of a thread's columns of a chunk, past the end 0.
-template <typename T, int A>
-__device__ __forceinline__ void read_weight(const void* w, int bf16, int c, int D, float none,
-                                            float (&f)[kLane<T>]) {
-#pragma unroll
-  for (int e = 0; e < kLane<T>; ++e) {
-    const int at = c + Pieces<T, A>::offset(e);
-    f[e] = at < D ? load_weight(w, bf16, at, none) : 0.0f;
-  }
-}
-
 }  // namespace
 
-// Shared memory: the ring [stage][r][thread] of 16 bytes, weight and bias
-// [r][k][thread] of 4 fp32 (wide rows read them again each time: they would
-// take the whole of it), and the teams' partial sums.
+// The ring starts as zeros: columns past a row's end are never fetched and
+// stay so.
+__device__ __forceinline__ void clear_ring(char* smem, int bytes) {
+  for (int k = threadIdx.x * 16; k < bytes; k += blockDim.x * 16)
+    *reinterpret_cast<uint4*>(smem + k) = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+}
+
+// Shared memory: the ring [stage][r][thread] of 16 bytes and the teams'
+// partial sums.  Weight and bias are read for each row, from L1.
 template <typename T, int A, int R, bool KEEP>
-__global__ void __launch_bounds__(512, R == 8 ? 1 : 2) vc_norm_rows(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(512, R >= 4 ? 1 : 2) vc_norm_rows(const __grid_constant__ NormParams p) {
   pdl_enter();
   using P = Pieces<T, A>;
   constexpr int E = P::E, S = norm_stages(R, false);
-  constexpr bool WS = norm_keeps_weight(R);
   extern __shared__ __align__(16) char smem[];
-  const int threads = blockDim.x, tid = threadIdx.x, D = (int)p.D;
+  const int threads = blockDim.x, D = (int)p.D;
   const Team t(p.warps);
-  char* ring = smem + tid * 16;
+  char* ring = smem + threadIdx.x * 16;
   const int slot = threads * 16;  // from one slot of a thread to its next
-  float* weight = reinterpret_cast<float*>(smem + S * R * slot) + tid * 4;
-  float* bias = weight + (size_t)R * E * threads;
-  float2* red = reinterpret_cast<float2*>(smem + (S * R + (WS ? 2 * R * E / 4 : 0)) * slot) +
-                t.index * 2 * t.warps;
+  float2* red = reinterpret_cast<float2*>(smem + S * R * slot) + t.index * 2 * t.warps;
 
   const int64_t teams = (int64_t)gridDim.x * (threads / 32 / p.warps);
   const int64_t first = (int64_t)blockIdx.x * (threads / 32 / p.warps) + t.index;
@@ -101,55 +80,48 @@ __global__ void __launch_bounds__(512, R == 8 ? 1 : 2) vc_norm_rows(const __grid
         P::fetch(ring + (s * R + r) * slot, elem_at<T>(p.x, i * p.x_ld), team_col<T, A>(t, r), D);
     fetch_commit();
   };
+  clear_ring(smem, S * R * slot);
 #pragma unroll
   for (int s = 0; s < S; ++s) fetch(first + s * teams, s);
-  int mine = 0;  // columns of this thread
+  // columns of a warp
+  auto columns = [&](int warp) {
+    int n = 0;
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int c = team_col<T, A>(t, r);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const bool in = c + P::offset(e) < D;
-      mine += in;
-      if constexpr (!WS) continue;
-      const size_t at = (size_t)(r * E / 4 + e / 4) * threads * 4 + e % 4;
-      weight[at] = in ? load_weight(p.weight, p.wbf16, c + P::offset(e), 1.0f) : 0.0f;
-      bias[at] = in ? load_weight(p.bias, p.wbf16, c + P::offset(e), 0.0f) : 0.0f;
-    }
-  }
-  const float cols = (float)__reduce_add_sync(~0u, mine);  // of this warp
+    for (int r = 0; r < R; ++r) n += min(max(D - (warp + t.warps * r) * 32 * E, 0), 32 * E);
+    return n;
+  };
+  const bool full = columns(t.warp) == R * 32 * E;
+  const float cols = (float)max(columns(t.warp), 1), cols_of = (float)columns(t.lane);
   int s = 0, parity = 0;
   for (int64_t i = first; i < p.N; i += teams) {
     fetch_wait<S - 1>();
-    uint4 raw[R];
-    float sum = 0.0f;
+    float f[R][E], sx = 0.0f, sy = 0.0f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      raw[r] = *reinterpret_cast<const uint4*>(ring + (s * R + r) * slot);
-      float f[E];
-      Elem<T>::widen(raw[r], f);
-      const int c = team_col<T, A>(t, r);
+      Elem<T>::widen(*reinterpret_cast<const uint4*>(ring + (s * R + r) * slot), f[r]);
 #pragma unroll
-      for (int e = 0; e < E; ++e) sum += c + P::offset(e) < D ? f[e] : 0.0f;
+      for (int e = 0; e < E; e += 2) add2(sx, sy, sx, sy, f[r][e], f[r][e + 1]);
     }
-    sum = warp_sum(sum);
+    const float sum = warp_sum(sx + sy);
     fetch(i + S * teams, s);  // the slot has been read
     s = s + 1 == S ? 0 : s + 1;
-    const float local = cols > 0.0f ? sum / cols : 0.0f;
-    float sq = 0.0f;
+    const float local = sum / cols;
+    if (!full)
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float f[E];
-      Elem<T>::widen(raw[r], f);
-      const int c = team_col<T, A>(t, r);
+      for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float d = c + P::offset(e) < D ? f[e] - local : 0.0f;
-        sq = fmaf(d, d, sq);
+        for (int e = 0; e < E; ++e)
+          if (team_col<T, A>(t, r) + P::offset(e) >= D) f[r][e] = local;
+    float qx = 0.0f, qy = 0.0f;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        float dx, dy;
+        add2(dx, dy, f[r][e], f[r][e + 1], -local, -local);
+        fma2(qx, qy, dx, dy, dx, dy, qx, qy);
       }
-    }
-    sq = warp_sum(sq);
-    float mean = local;
+    float sq = warp_sum(qx + qy), mean = local;
     if (t.warps > 1) {
       float2* now = red + parity * t.warps;
       parity ^= 1;
@@ -157,38 +129,34 @@ __global__ void __launch_bounds__(512, R == 8 ? 1 : 2) vc_norm_rows(const __grid
       t.meet();
       const float2 o = t.lane < t.warps ? now[t.lane] : make_float2(0.0f, 0.0f);
       mean = warp_sum(o.x) / (float)D;
-      // the columns of warp t.lane
-      int n = 0;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int left = D - (t.lane + t.warps * r) * 32 * E;
-        n += left <= 0 ? 0 : left < 32 * E ? left : 32 * E;
-      }
-      const float d = t.lane < t.warps && n ? o.x / (float)n - mean : 0.0f;
-      sq = warp_sum(fmaf((float)n * d, d, o.y));
+      const float d = t.lane < t.warps && cols_of > 0.0f ? o.x / cols_of - mean : 0.0f;
+      sq = warp_sum(fmaf(cols_of * d, d, o.y));
     }
     const float rstd = rsqrtf(sq / (float)D + p.eps);
     char* y = elem_at<T>(p.y, i * p.y_ld);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float f[E], w[E], b[E];
-      Elem<T>::widen(raw[r], f);
       const int c = team_col<T, A>(t, r);
 #pragma unroll
-      for (int e = 0; e < E; ++e) f[e] = (f[e] - mean) * rstd;
-      if constexpr (KEEP)
-        keep8<T, A>(f, c, (t.warp + t.warps * r) * (32 * E / kBlock8), D,
-                    p.codes + i * p.codes_ld, p.scales + i * ((D + kBlock8 - 1) / kBlock8));
-      if constexpr (WS) {
-        read_slots<E>(weight + (size_t)r * E * threads, threads, w);
-        read_slots<E>(bias + (size_t)r * E * threads, threads, b);
-      } else {
-        read_weight<T, A>(p.weight, p.wbf16, c, D, 1.0f, w);
-        read_weight<T, A>(p.bias, p.wbf16, c, D, 0.0f, b);
+      for (int e = 0; e < E; e += 2) {
+        add2(f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], -mean, -mean);
+        mul2(f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], rstd, rstd);
       }
+      if constexpr (KEEP) {
+        if (!full)
 #pragma unroll
-      for (int e = 0; e < E; ++e) f[e] = fmaf(f[e], w[e], b[e]);
-      P::store(y, c, D, f);
+          for (int e = 0; e < E; ++e)
+            if (c + P::offset(e) >= D) f[r][e] = 0.0f;
+        keep8<T, A>(f[r], c, (t.warp + t.warps * r) * (32 * E / kBlock8), D, p.codes + i * p.codes_ld,
+                    p.scales + i * ((D + kBlock8 - 1) / kBlock8));
+      }
+      float w[E], b[E];
+      P::weights(p.weight, p.wbf16, c, D, 1.0f, w);
+      P::weights(p.bias, p.wbf16, c, D, 0.0f, b);
+#pragma unroll
+      for (int e = 0; e < E; e += 2)
+        fma2(f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], w[e], w[e + 1], b[e], b[e + 1]);
+      P::store(y, c, D, f[r]);
     }
     if (t.warp == 0 && t.lane == 0) {
       if (p.mean) p.mean[i] = mean;
@@ -200,14 +168,12 @@ __global__ void __launch_bounds__(512, R == 8 ? 1 : 2) vc_norm_rows(const __grid
 // Shared memory: the ring [stage] of gradient and x [r][thread] of 16 bytes
 // each (KEPT: instead of x the codes [r][warp] of 32 * E bytes, in the order of
 // the columns, and the scales [r][thread] of 2 fp32), the row's statistics
-// [thread] of 2 fp32; the weight [r][k][thread] of 4 fp32; and the teams'
-// partial sums.
+// [thread] of 2 fp32; and the teams' partial sums.
 template <typename T, int A, int R, bool KEPT>
 __global__ void __launch_bounds__(512, 1) vc_norm_grad_rows(const __grid_constant__ NormParams p) {
   pdl_enter();
   using P = Pieces<T, A>;
   constexpr int E = P::E, S = norm_stages(R, true);
-  constexpr bool WS = norm_keeps_weight(R);
   // scales that a thread's pieces of a chunk need: their blocks of 128 columns
   constexpr int SC = 32 * E / kBlock8 == 2 && A < E ? 2 : 1;
   extern __shared__ __align__(16) char smem[];
@@ -219,9 +185,7 @@ __global__ void __launch_bounds__(512, 1) vc_norm_grad_rows(const __grid_constan
   char* xslot = smem + R * threads * 16 + tid * (KEPT ? E : 16);
   char* cslot = smem + R * threads * (16 + E) + tid * 8;  // KEPT: scales
   char* sslot = smem + stage - threads * 8 + tid * 8;
-  float* weight = reinterpret_cast<float*>(smem + S * stage) + tid * 4;
-  float2* red = reinterpret_cast<float2*>(smem + S * stage + (WS ? R * E * 4 * threads : 0)) +
-                t.index * 2 * t.warps;
+  float2* red = reinterpret_cast<float2*>(smem + S * stage) + t.index * 2 * t.warps;
 
   const int64_t teams = (int64_t)gridDim.x * (threads / 32 / p.warps);
   const int64_t first = (int64_t)blockIdx.x * (threads / 32 / p.warps) + t.index;
@@ -251,20 +215,9 @@ __global__ void __launch_bounds__(512, 1) vc_norm_grad_rows(const __grid_constan
     }
     fetch_commit();
   };
-  // columns past the row's end are never fetched: their gradient stays 0
-  for (int k = 0; k < S * stage; k += threads * 16)
-    if (k + tid * 16 < S * stage) *reinterpret_cast<uint4*>(smem + k + tid * 16) = make_uint4(0, 0, 0, 0);
-  __syncthreads();
+  clear_ring(smem, S * stage);
 #pragma unroll
   for (int s = 0; s < S; ++s) fetch(first + s * teams, s);
-#pragma unroll
-  for (int r = 0; r < (WS ? R : 0); ++r) {
-    const int c = team_col<T, A>(t, r);
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      weight[(size_t)(r * E / 4 + e / 4) * threads * 4 + e % 4] =
-          c + P::offset(e) < D ? load_weight(p.weight, p.wbf16, c + P::offset(e), 1.0f) : 0.0f;
-  }
   float dw[R][E], db[R][E];
 #pragma unroll
   for (int r = 0; r < R; ++r)
@@ -277,67 +230,51 @@ __global__ void __launch_bounds__(512, 1) vc_norm_grad_rows(const __grid_constan
     if constexpr (KEPT && A < E) __syncwarp();  // codes that other lanes fetched
     const int at = s * stage;
     const float2 stat = *reinterpret_cast<const float2*>(sslot + at);
-    const float mean = stat.x, rstd = stat.y;
-    uint4 graw[R], xraw[R];
-    float2 scale[R];
+    const float rstd = stat.y;
+    // columns past the row's end have a gradient of 0, so they add nothing
+    float f[R][E], h[R][E], s1x = 0.0f, s1y = 0.0f, s2x = 0.0f, s2y = 0.0f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      graw[r] = *reinterpret_cast<const uint4*>(gslot + at + r * threads * 16);
+      Elem<T>::widen(*reinterpret_cast<const uint4*>(gslot + at + r * threads * 16), f[r]);
       if constexpr (KEPT) {
         const char* from = xslot + at + r * threads * E;
+        const float2 scale = *reinterpret_cast<const float2*>(cslot + at + r * threads * 8);
+        uint32_t word[2] = {0u, 0u};
         if constexpr (A < E) {
           from -= t.lane * (E - A);  // this lane's first column
-          uint32_t word[2] = {0u, 0u};
 #pragma unroll
           for (int e = 0; e < E; ++e)
             word[e / 4] |= (uint32_t)(uint8_t)from[P::offset(e)] << (8 * (e % 4));
-          xraw[r].x = word[0];
-          xraw[r].y = word[1];
         } else if constexpr (E == 8) {
           const uint2 v = *reinterpret_cast<const uint2*>(from);
-          xraw[r].x = v.x;
-          xraw[r].y = v.y;
+          word[0] = v.x;
+          word[1] = v.y;
         } else {
-          xraw[r].x = *reinterpret_cast<const uint32_t*>(from);
+          word[0] = *reinterpret_cast<const uint32_t*>(from);
         }
-        scale[r] = *reinterpret_cast<const float2*>(cslot + at + r * threads * 8);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          h[r][e] = code_value(word[e / 4], e % 4) * (SC == 2 && P::offset(e) >= kBlock8 ? scale.y : scale.x);
       } else {
-        xraw[r] = *reinterpret_cast<const uint4*>(xslot + at + r * threads * 16);
+        Elem<T>::widen(*reinterpret_cast<const uint4*>(xslot + at + r * threads * 16), h[r]);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          add2(h[r][e], h[r][e + 1], h[r][e], h[r][e + 1], -stat.x, -stat.x);
+          mul2(h[r][e], h[r][e + 1], h[r][e], h[r][e + 1], rstd, rstd);
+        }
+      }
+      float w[E];
+      P::weights(p.weight, p.wbf16, team_col<T, A>(t, r), D, 1.0f, w);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        fma2(dw[r][e], dw[r][e + 1], f[r][e], f[r][e + 1], h[r][e], h[r][e + 1], dw[r][e], dw[r][e + 1]);
+        add2(db[r][e], db[r][e + 1], db[r][e], db[r][e + 1], f[r][e], f[r][e + 1]);
+        mul2(f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], w[e], w[e + 1]);  // g from here on
+        add2(s1x, s1y, s1x, s1y, f[r][e], f[r][e + 1]);
+        fma2(s2x, s2y, f[r][e], f[r][e + 1], h[r][e], h[r][e + 1], s2x, s2y);
       }
     }
-    auto normal = [&](int r, float (&h)[E]) {
-      if constexpr (KEPT) {
-        const uint32_t word[2] = {xraw[r].x, xraw[r].y};
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float sc = SC == 2 && P::offset(e) >= kBlock8 ? scale[r].y : scale[r].x;
-          h[e] = code_value(word[e / 4], e % 4) * sc;
-        }
-      } else {
-        Elem<T>::widen(xraw[r], h);
-#pragma unroll
-        for (int e = 0; e < E; ++e) h[e] = (h[e] - mean) * rstd;
-      }
-    };
-    float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float f[E], h[E], w[E];
-      Elem<T>::widen(graw[r], f);
-      normal(r, h);
-      if constexpr (WS) read_slots<E>(weight + (size_t)r * E * threads, threads, w);
-      else read_weight<T, A>(p.weight, p.wbf16, team_col<T, A>(t, r), D, 1.0f, w);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        dw[r][e] = fmaf(f[e], h[e], dw[r][e]);
-        db[r][e] += f[e];
-        const float g = f[e] * w[e];
-        s1 += g;
-        s2 = fmaf(g, h[e], s2);
-      }
-    }
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
+    float s1 = warp_sum(s1x + s1y), s2 = warp_sum(s2x + s2y);
     fetch(i + S * teams, s);  // the slot has been read
     s = s + 1 == S ? 0 : s + 1;
     if (!p.y) continue;
@@ -350,19 +287,18 @@ __global__ void __launch_bounds__(512, 1) vc_norm_grad_rows(const __grid_constan
       s1 = warp_sum(o.x);
       s2 = warp_sum(o.y);
     }
-    s1 /= (float)D;
-    s2 /= (float)D;
+    s1 /= -(float)D;
+    s2 /= -(float)D;
     char* dx = elem_at<T>(p.y, i * p.y_ld);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float f[E], h[E], w[E];
-      Elem<T>::widen(graw[r], f);
-      normal(r, h);
-      if constexpr (WS) read_slots<E>(weight + (size_t)r * E * threads, threads, w);
-      else read_weight<T, A>(p.weight, p.wbf16, team_col<T, A>(t, r), D, 1.0f, w);
 #pragma unroll
-      for (int e = 0; e < E; ++e) f[e] = (fmaf(f[e], w[e], -s1) - h[e] * s2) * rstd;
-      P::store(dx, team_col<T, A>(t, r), D, f);
+      for (int e = 0; e < E; e += 2) {
+        add2(f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], s1, s1);
+        fma2(f[r][e], f[r][e + 1], h[r][e], h[r][e + 1], s2, s2, f[r][e], f[r][e + 1]);
+        mul2(f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], rstd, rstd);
+      }
+      P::store(dx, team_col<T, A>(t, r), D, f[r]);
     }
   }
   if (!p.part) return;
