@@ -134,8 +134,8 @@ int access_of(const Operand& o, int most) {
   return 1;
 }
 
-// How a team of warps takes a row of D columns (norm_rows.cuh): two chunks a
-// warp, more where 16 warps do not suffice; 0 chunks: too wide for that.
+// How a team of warps takes a row of D columns (norm_rows.cuh); 0 chunks: too
+// wide for that.
 struct NormShape {
   int warps, chunks, threads;
 };
@@ -143,14 +143,11 @@ NormShape norm_shape(int64_t D, int E, bool grad) {
   const int64_t all = ceil_div(D, 32 * E);
   NormShape s = {1, 0, kNormCtaWarps * 32};
   if (all > (int64_t)kNormMaxWarps * norm_max_chunks(E, grad)) return s;
-  s.chunks = all == 1 ? 1 : 2;
+  s.chunks = 1;
+  while (s.chunks < norm_chunks(E, grad) && s.chunks < all) s.chunks *= 2;
   while (ceil_div(all, s.chunks) > kNormMaxWarps) s.chunks *= 2;
   s.warps = (int)ceil_div(all, s.chunks);
-  if (s.warps > kNormCtaWarps / 2) {
-    s.threads = s.warps * 32;  // one team
-  } else {
-    while (s.warps & (s.warps - 1)) ++s.warps;  // a power of two of teams
-  }
+  s.threads = s.warps * std::max(1, kNormCtaWarps / s.warps) * 32;
   return s;
 }
 
@@ -407,8 +404,8 @@ static int norm_forward(const void* x, int64_t x_ld, const void* weight, const v
   p.warps = s.warps;
   int access = E;
   for (int k = 0; k < 4; ++k) access = row_access(access, access_of(ops[k], E), dtype);
-  const void* fn = dtype == VCOLL_F32 ? norm_rows_kernel_f32(access, s.chunks, false, keep)
-                                      : norm_rows_kernel_bf16(access, s.chunks, false, keep);
+  const void* fn = dtype == VCOLL_F32 ? norm_rows_kernel_f32(access, s.chunks, s.threads, false, keep)
+                                      : norm_rows_kernel_bf16(access, s.chunks, s.threads, false, keep);
   // the ring, and two partial sums of 8 bytes a warp
   const size_t smem =
       (size_t)s.threads * 16 * s.chunks * norm_stages(s.chunks, false) + s.threads / 2;
@@ -479,8 +476,8 @@ static int norm_backward(const void* grad, int64_t grad_ld, const void* x, int64
     p.part = dweight || dbias ? (float*)workspace : nullptr;
     int access = E;
     for (int k : {0, 1, 6, 7}) access = row_access(access, access_of(ops[k], E), dtype);
-    const void* fn = dtype == VCOLL_F32 ? norm_rows_kernel_f32(access, s.chunks, true, kept)
-                                        : norm_rows_kernel_bf16(access, s.chunks, true, kept);
+    const void* fn = dtype == VCOLL_F32 ? norm_rows_kernel_f32(access, s.chunks, s.threads, true, kept)
+                                        : norm_rows_kernel_bf16(access, s.chunks, s.threads, true, kept);
     const size_t smem = (size_t)s.threads * norm_stages(s.chunks, true) *
                             norm_grad_slot_bytes(s.chunks, E, kept) + s.threads / 2;
     VCOLL_TRY(launch_norm_rows(fn, s, smem, kNormMaxCtas, &p, stream, &p.parts));

@@ -79,22 +79,23 @@ struct NormParams {
   int parts;  // partial rows of the gradient (CTAs)
 };
 
-// norm_rows.cuh: slots of the ring of rows on their way, warps of a CTA of
-// several teams, and of the largest team.
-VCOLL_HD constexpr int norm_stages(int R, bool grad) { return R <= 2 ? 4 : grad && R == 8 ? 1 : 2; }
+// norm_rows.cuh: warps of a CTA of several teams, and of the largest team.
 constexpr int kNormCtaWarps = 8;
 constexpr int kNormMaxWarps = 16;
 // CTAs of the gradient at most: its partial rows' room in the workspace.
 constexpr int kNormMaxCtas = 608;
-// columns up to which a team's registers hold a row, forward and backward:
-// kNormMaxWarps warps of 8 chunks, or of 4 where 8 values a lane and chunk
-// are summed over the rows too
+// Chunks of 32 * E columns that a warp takes: 32 values a lane forward, 16
+// backward, where the sums over the rows are in registers too; and at most.
+VCOLL_HD constexpr int norm_chunks(int E, bool grad) { return (grad ? 16 : 32) / E; }
 VCOLL_HD constexpr int norm_max_chunks(int E, bool grad) { return grad && E == 8 ? 4 : 8; }
+// slots of the ring of rows on their way: 256 bytes a thread or so
+VCOLL_HD constexpr int norm_stages(int R, bool grad) {
+  return grad ? (R <= 2 ? 4 : R == 4 ? 2 : 1) : (R <= 4 ? 4 : 2);
+}
 // bytes of a thread's slots of one stage of the backward ring
 VCOLL_HD constexpr int norm_grad_slot_bytes(int R, int E, bool kept) {
   return R * 16 + (kept ? R * E + R * 8 : R * 16) + 8;
 }
-
 
 struct PackParams {
   const void* x;
@@ -116,8 +117,8 @@ const void* embed_sort_kernel();
 const void* embed_count_kernel();
 const void* embed_scatter_kernel();
 const void* embed_grad_kernel(int dtype, int table_dtype, int access, int join);
-const void* norm_rows_kernel_f32(int access, int chunks, bool grad, bool kept);
-const void* norm_rows_kernel_bf16(int access, int chunks, bool grad, bool kept);
+const void* norm_rows_kernel_f32(int access, int chunks, int threads, bool grad, bool kept);
+const void* norm_rows_kernel_bf16(int access, int chunks, int threads, bool grad, bool kept);
 const void* norm_wsum_kernel();
 const void* norm_wide_kernel(int dtype);
 const void* norm_grad_wide_kernel(int dtype);

@@ -6,34 +6,32 @@ namespace vcoll {
 namespace {
 
 template <int A, bool KEEP>
-const void* forward(int chunks) {
-  switch (chunks) {
-    case 1: return (const void*)&vc_norm_rows<__nv_bfloat16, A, 1, KEEP>;
-    case 2: return (const void*)&vc_norm_rows<__nv_bfloat16, A, 2, KEEP>;
-    case 4: return (const void*)&vc_norm_rows<__nv_bfloat16, A, 4, KEEP>;
-    default: return (const void*)&vc_norm_rows<__nv_bfloat16, A, 8, KEEP>;
-  }
+const void* forward(int chunks, int threads) {
+  if (chunks == 1 && threads <= 256) return (const void*)&vc_norm_rows<__nv_bfloat16, A, 1, 256, KEEP>;
+  if (chunks == 2 && threads <= 256) return (const void*)&vc_norm_rows<__nv_bfloat16, A, 2, 256, KEEP>;
+  if (chunks == 4 && threads <= 256) return (const void*)&vc_norm_rows<__nv_bfloat16, A, 4, 256, KEEP>;
+  if (chunks == 4 && threads <= 512) return (const void*)&vc_norm_rows<__nv_bfloat16, A, 4, 512, KEEP>;
+  return (const void*)&vc_norm_rows<__nv_bfloat16, A, 8, 512, KEEP>;
 }
 template <int A, bool KEPT>
-const void* backward(int chunks) {
-  switch (chunks) {
-    case 1: return (const void*)&vc_norm_grad_rows<__nv_bfloat16, A, 1, KEPT>;
-    case 2: return (const void*)&vc_norm_grad_rows<__nv_bfloat16, A, 2, KEPT>;
-    default: return (const void*)&vc_norm_grad_rows<__nv_bfloat16, A, 4, KEPT>;
-  }
+const void* backward(int chunks, int threads) {
+  if (chunks == 1 && threads <= 256) return (const void*)&vc_norm_grad_rows<__nv_bfloat16, A, 1, 256, KEPT>;
+  if (chunks == 2 && threads <= 256) return (const void*)&vc_norm_grad_rows<__nv_bfloat16, A, 2, 256, KEPT>;
+  if (chunks == 2 && threads <= 512) return (const void*)&vc_norm_grad_rows<__nv_bfloat16, A, 2, 512, KEPT>;
+  return (const void*)&vc_norm_grad_rows<__nv_bfloat16, A, 4, 512, KEPT>;
 }
 template <int A>
-const void* by_pass(int chunks, bool grad, bool kept) {
-  if (grad) return kept ? backward<A, true>(chunks) : backward<A, false>(chunks);
-  return kept ? forward<A, true>(chunks) : forward<A, false>(chunks);
+const void* by_pass(int chunks, int threads, bool grad, bool kept) {
+  if (grad) return kept ? backward<A, true>(chunks, threads) : backward<A, false>(chunks, threads);
+  return kept ? forward<A, true>(chunks, threads) : forward<A, false>(chunks, threads);
 }
 
 }  // namespace
 
-const void* norm_rows_kernel_bf16(int access, int chunks, bool grad, bool kept) {
-  if (access == 8) return by_pass<8>(chunks, grad, kept);
-  if (access == 2) return by_pass<2>(chunks, grad, kept);
-  return by_pass<1>(chunks, grad, kept);
+const void* norm_rows_kernel_bf16(int access, int chunks, int threads, bool grad, bool kept) {
+  if (access == 8) return by_pass<8>(chunks, threads, grad, kept);
+  if (access == 2) return by_pass<2>(chunks, threads, grad, kept);
+  return by_pass<1>(chunks, threads, grad, kept);
 }
 
 }  // namespace vcoll

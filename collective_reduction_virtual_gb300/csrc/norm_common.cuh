@@ -32,70 +32,101 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// A thread's pieces of one chunk of a row, A elements each; c: its first column.
-template <typename T, int A>
-struct Pieces {
+// The columns of a lane in a warp's group of R chunks (R * 32 * E columns).
+// Plainly, chunk r is 32 * E adjacent columns.  With BLOCKS, and whole accesses
+// (A == E), each block of 128 columns belongs to LANES lanes, all R accesses of
+// a lane lying in one block: its scale is then computed, or fetched, once for
+// R * E values, and an access of the warp is pieces of LANES * 16 bytes.
+template <typename T, int A, int R, bool BLOCKS>
+struct Lanes {
   static constexpr int E = kLane<T>, BYTES = A * Elem<T>::kBytes;
-  // element e of the thread's E is column c + offset(e)
-  static __device__ __forceinline__ constexpr int offset(int e) { return e / A * 32 * A + e % A; }
+  static constexpr int kColumns = R * 32 * E;
+  static constexpr bool kBlocks = BLOCKS && A == E;
+  static constexpr int LANES = 128 / (R * E) < 32 ? 128 / (R * E) : 32;
+  // first column of lane in the group, and column of element e of access r from there
+  static __device__ __forceinline__ int first(int lane) {
+    return kBlocks ? lane / LANES * kBlock8 + lane % LANES * E : lane * A;
+  }
+  static __device__ __forceinline__ constexpr int offset(int r, int e) {
+    return kBlocks ? r * LANES * E + e : r * 32 * E + e / A * 32 * A + e % A;
+  }
 
-  static __device__ __forceinline__ void fetch(void* slot, const void* row, int c, int D) {
-#pragma unroll
-    for (int j = 0; j < E / A; ++j)
-      if (c + j * 32 * A < D)
-        fetch_async<BYTES>(static_cast<char*>(slot) + j * BYTES, elem_at<T>(row, c + j * 32 * A));
+  // In what follows c is the lane's first column in the row of D columns;
+  // full: the warp's whole group lies inside the row.
+  static __device__ __forceinline__ bool inside(int r, int e, int c, int D, bool full) {
+    return full || c + offset(r, e) < D;
   }
-  // The weight (or bias) of the thread's columns, in either type, from a place
-  // that allows accesses of A elements; ones or zeros where there is none.
-  static __device__ __forceinline__ void weights(const void* w, int bf16, int c, int D, float none,
-                                                 float (&f)[E]) {
+  // slots: one of 16 bytes for each r, `step` bytes apart
+  static __device__ __forceinline__ void fetch(char* slots, int step, const char* row, int c, int D,
+                                               bool full) {
+    const char* from = row + (int64_t)c * Elem<T>::kBytes;
 #pragma unroll
-    for (int j = 0; j < E / A; ++j) {
-      float g[A];
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int a = 0; a < A; ++a) g[a] = none;
-      const int at = c + j * 32 * A;
-      if (w && at < D) {
-        if (bf16) {
-          Raw<__nv_bfloat16, A> v;
-          v.load(elem_at<__nv_bfloat16>(w, at));
-          v.widen(g);
-        } else {
-          Raw<float, A> v;
-          v.load(elem_at<float>(w, at));
-          v.widen(g);
-        }
+      for (int e = 0; e < E; e += A)
+        if (inside(r, e, c, D, full))
+          fetch_async<BYTES>(slots + r * step + e * Elem<T>::kBytes, from + offset(r, e) * Elem<T>::kBytes);
+  }
+  static __device__ __forceinline__ void load(uint4 (&raw)[R], const char* row, int c, int D, bool full) {
+    const char* from = row + (int64_t)c * Elem<T>::kBytes;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      uint32_t word[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int e = 0; e < E; e += A) {
+        Raw<T, A> v;
+        if (inside(r, e, c, D, full)) v.load_stream(from + offset(r, e) * Elem<T>::kBytes);
+        else v.zero();
+        v.into(word, e);
       }
-#pragma unroll
-      for (int a = 0; a < A; ++a) f[j * A + a] = g[a];
+      raw[r] = make_uint4(word[0], word[1], word[2], word[3]);
     }
   }
-  static __device__ __forceinline__ void load(Raw<T, A> (&v)[E / A], const void* row, int64_t c, int64_t D) {
+  static __device__ __forceinline__ void store(char* row, int c, int D, bool full, const float (&f)[R][E]) {
+    char* to = row + (int64_t)c * Elem<T>::kBytes;
 #pragma unroll
-    for (int j = 0; j < E / A; ++j) {
-      if (c + j * 32 * A < D) v[j].load_stream(elem_at<T>(row, c + j * 32 * A));
-      else v[j].zero();
-    }
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < E; e += A) {
+        float g[A];
+#pragma unroll
+        for (int a = 0; a < A; ++a) g[a] = f[r][e + a];
+        Raw<T, A> o;
+        o.narrow(g);
+        if (inside(r, e, c, D, full)) o.store_stream(to + offset(r, e) * Elem<T>::kBytes);
+      }
   }
-  static __device__ __forceinline__ void widen(const Raw<T, A> (&v)[E / A], float (&f)[E]) {
+  // The weight (or bias) of access r's columns, in either type, from a place
+  // that allows accesses of A elements; `none` where there is none.
+  static __device__ __forceinline__ void weights(const void* w, int bf16, int r, int c, int D, bool full,
+                                                 float none, float (&f)[E]) {
 #pragma unroll
-    for (int j = 0; j < E / A; ++j) {
-      float g[A];
-      v[j].widen(g);
+    for (int e = 0; e < E; ++e) f[e] = none;
+    if (!w) return;
+    if (bf16) {
+      const char* from = elem_at<__nv_bfloat16>(w, c);
 #pragma unroll
-      for (int a = 0; a < A; ++a) f[j * A + a] = g[a];
-    }
-  }
-  static __device__ __forceinline__ void store(void* row, int64_t c, int64_t D, const float (&f)[E]) {
+      for (int e = 0; e < E; e += A)
+        if (inside(r, e, c, D, full)) {
+          float g[A];
+          Raw<__nv_bfloat16, A> v;
+          v.load(from + offset(r, e) * 2);
+          v.widen(g);
 #pragma unroll
-    for (int j = 0; j < E / A; ++j) {
-      if (c + j * 32 * A >= D) break;
-      float g[A];
+          for (int a = 0; a < A; ++a) f[e + a] = g[a];
+        }
+    } else {
+      const char* from = elem_at<float>(w, c);
 #pragma unroll
-      for (int a = 0; a < A; ++a) g[a] = f[j * A + a];
-      Raw<T, A> o;
-      o.narrow(g);
-      o.store_stream(elem_at<T>(row, c + j * 32 * A));
+      for (int e = 0; e < E; e += A)
+        if (inside(r, e, c, D, full)) {
+          float g[A];
+          Raw<float, A> v;
+          v.load(from + offset(r, e) * 4);
+          v.widen(g);
+#pragma unroll
+          for (int a = 0; a < A; ++a) f[e + a] = g[a];
+        }
     }
   }
 };
@@ -133,57 +164,68 @@ __device__ __forceinline__ float code_value(uint32_t word, int k) {
   return __uint_as_float(__byte_perm(up, 0x4B000000u, 0x7540 | k)) - 8388736.0f;
 }
 
-// Keeps a lane's E values of a chunk: its codes and, from one lane, the
-// chunk's scales.  Values past the row's end are 0.  c: the lane's first
-// column; block: the chunk's first block.
-template <typename T, int A>
-__device__ __forceinline__ void keep8(const float (&f)[kLane<T>], int64_t c, int64_t block, int64_t D,
-                                      int8_t* codes, float* scales) {
-  constexpr int E = kLane<T>, B = 32 * E / kBlock8;  // blocks of a chunk
-  const int lane = threadIdx.x & 31;
-  // offset of element e from the lane's first column, and its block
-  auto offset = [](int e) { return Pieces<T, A>::offset(e); };
-  auto block_of = [&](int e) { return B == 1 ? 0 : A == E ? lane >> 4 : offset(e) / kBlock8; };
-  uint32_t top[B];
+// The four codes of 4 values.
+__device__ __forceinline__ uint32_t code_word(const float* f, const Scale8& s) {
+  return __byte_perm(__byte_perm(code_bits(f[0], s.unit), code_bits(f[1], s.unit), 0x0040),
+                     __byte_perm(code_bits(f[2], s.unit), code_bits(f[3], s.unit), 0x0040), 0x5410) &
+         s.mask;
+}
+
+// Keeps a warp's group of values: the codes and the scales of its blocks.
+// Values past the row's end are 0.  col: the group's first column, a multiple
+// of 128; c = col + Lanes::first(lane).
+template <typename T, int A, int R>
+__device__ __forceinline__ void keep8(const float (&f)[R][kLane<T>], int col, int c, int D, int8_t* codes,
+                                      float* scales) {
+  using P = Lanes<T, A, R, true>;
+  constexpr int E = P::E;
+  const int lane = threadIdx.x & 31, end = (D + 15) & ~15;
+  if constexpr (P::kBlocks) {
+    uint32_t top = 0u;
 #pragma unroll
-  for (int b = 0; b < B; ++b) top[b] = 0u;
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const uint32_t m = magnitude_bits(f[e]);
+      for (int e = 0; e < E; ++e) top = max(top, magnitude_bits(f[r][e]));
+    if constexpr (P::LANES == 32) {
+      top = __reduce_max_sync(~0u, top);
+    } else {
 #pragma unroll
-    for (int b = 0; b < B; ++b)
-      if (block_of(e) == b) top[b] = max(top[b], m);
-  }
-  Scale8 s[B];
-#pragma unroll
-  for (int b = 0; b < B; ++b) s[b] = scale8(__reduce_max_sync(~0u, top[b]));
-  uint32_t word[E / 4];
-#pragma unroll
-  for (int k = 0; k < E; k += 4) {
-    uint32_t q[4], mask = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int in = block_of(k + e);
-      const float unit = B == 1 || in == 0 ? s[0].unit : s[B - 1].unit;
-      mask = B == 1 || in == 0 ? s[0].mask : s[B - 1].mask;
-      q[e] = code_bits(f[k + e], unit);
+      for (int d = P::LANES / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
     }
-    word[k / 4] = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410) & mask;
-  }
-  const int64_t end = (D + 15) & ~(int64_t)15;
+    const Scale8 s = scale8(top);
 #pragma unroll
-  for (int j = 0; j < E / A; ++j) {
-    const int64_t at = c + j * 32 * A;
-    if (at >= end) break;
-    if constexpr (A == 8) *reinterpret_cast<uint2*>(codes + at) = make_uint2(word[0], word[1]);
-    else if constexpr (A == 4) *reinterpret_cast<uint32_t*>(codes + at) = word[j];
-    else if constexpr (A == 2)
-      *reinterpret_cast<uint16_t*>(codes + at) = (uint16_t)(word[j / 2] >> (16 * (j % 2)));
-    else codes[at] = (int8_t)(word[j / 4] >> (8 * (j % 4)));
+    for (int r = 0; r < R; ++r) {
+      if (c + P::offset(r, 0) >= end) break;
+      int8_t* at = codes + c + P::offset(r, 0);
+      if constexpr (E == 8)
+        *reinterpret_cast<uint2*>(at) = make_uint2(code_word(f[r], s), code_word(f[r] + 4, s));
+      else *reinterpret_cast<uint32_t*>(at) = code_word(f[r], s);
+    }
+    if (lane % P::LANES == 0 && c < D) scales[c / kBlock8] = s.scale;
+  } else {
+    constexpr int B = 32 * E / kBlock8;  // blocks of a chunk, 4 elements of a lane in each
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int first = col + r * 32 * E + b * kBlock8;
+        if (first >= D) break;
+        const float* v = f[r] + 4 * b;
+        uint32_t top = 0u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, magnitude_bits(v[e]));
+        const Scale8 s = scale8(__reduce_max_sync(~0u, top));
+        const uint32_t word = code_word(v, s);
+#pragma unroll
+        for (int e = 0; e < 4; e += A) {
+          const int at = c + P::offset(r, 4 * b + e);
+          if (at >= end) break;
+          if constexpr (A == 2) *reinterpret_cast<uint16_t*>(codes + at) = (uint16_t)(word >> (8 * e));
+          else codes[at] = (int8_t)(word >> (8 * e));
+        }
+        if (lane == 0) scales[first / kBlock8] = s.scale;
+      }
   }
-  const int64_t blocks = (D + kBlock8 - 1) / kBlock8;
-  if (lane == 0 && block < blocks) scales[block] = s[0].scale;
-  if (B == 2 && lane == 16 && block + 1 < blocks) scales[block + 1] = s[B - 1].scale;
 }
 
 }  // namespace

@@ -25,14 +25,16 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 template <typename F>
 __device__ __forceinline__ void keep_block(int64_t b, int64_t D, int8_t* codes, float* scale,
                                            F value) {
-  float v[4];
+  const int lane = threadIdx.x & 31;
+  float v[1][4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int64_t c = b * kBlock8 + k * 32 + (threadIdx.x & 31);
-    v[k] = c < D ? value(c) : 0.0f;
+    const int64_t c = b * kBlock8 + k * 32 + lane;
+    v[0][k] = c < D ? value(c) : 0.0f;
   }
   // as fp32 in single elements: 4 groups of 32 columns, one block
-  keep8<float, 1>(v, b * kBlock8 + (threadIdx.x & 31), 0, D, codes, scale);
+  const int64_t left = D - b * kBlock8;
+  keep8<float, 1, 1>(v, 0, lane, left < kBlock8 ? (int)left : kBlock8, codes + b * kBlock8, scale);
 }
 
 }  // namespace
@@ -167,90 +169,89 @@ __global__ void __launch_bounds__(1024) vc_norm_wsum(const __grid_constant__ Nor
 
 // ------------------------------------------------------- 8-bit activations
 // A row is taken by 2^row_shift adjacent warps of a CTA, kPackChunks chunks of
-// 32 * E columns at a time, all of their loads in flight.
+// 32 * E columns a warp at a time, all of their loads in flight.
 
 template <typename T, int A>
 __global__ void __launch_bounds__(kRowThreads) vc_pack8(const __grid_constant__ PackParams p) {
   pdl_enter();
-  using P = Pieces<T, A>;
+  constexpr int R = kPackChunks;
+  using P = Lanes<T, A, R, true>;
   constexpr int E = P::E;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = (int)p.D;
   const int64_t i = (int64_t)blockIdx.x * ((kRowThreads / 32) >> p.row_shift) + (warp >> p.row_shift);
   if (i >= p.N) return;
   const char* x = elem_at<T>(p.x, i * p.x_ld);
   int8_t* codes = p.codes + i * p.codes_ld;
-  float* scales = p.scales + i * ((p.D + kBlock8 - 1) / kBlock8);
-  const int64_t step = (int64_t)(kPackChunks * 32 * E) << p.row_shift;
-  for (int64_t c0 = (int64_t)(warp & ((1 << p.row_shift) - 1)) * (kPackChunks * 32 * E); c0 < p.D; c0 += step) {
-    Raw<T, A> raw[kPackChunks][E / A];
+  float* scales = p.scales + i * ((D + kBlock8 - 1) / kBlock8);
+  // 64-bit: the step past the last group may pass 2^31
+  for (int64_t g = (warp & ((1 << p.row_shift) - 1)) * P::kColumns; g < D; g += (int64_t)P::kColumns << p.row_shift) {
+    const int col = (int)g, c = col + P::first(lane);
+    uint4 raw[R];
+    P::load(raw, x, c, D, g + P::kColumns <= D);
+    float f[R][E];
 #pragma unroll
-    for (int k = 0; k < kPackChunks; ++k) P::load(raw[k], x, c0 + k * 32 * E + lane * A, p.D);
-#pragma unroll
-    for (int k = 0; k < kPackChunks; ++k) {
-      const int64_t base = c0 + k * 32 * E;
-      if (base >= p.D) break;
-      float f[E];
-      P::widen(raw[k], f);
-      keep8<T, A>(f, base + lane * A, base / kBlock8, p.D, codes, scales);
-    }
+    for (int r = 0; r < R; ++r) Elem<T>::widen(raw[r], f[r]);
+    keep8<T, A, R>(f, col, c, D, codes, scales);
   }
 }
 
 template <typename T, int A>
 __global__ void __launch_bounds__(kRowThreads) vc_unpack8(const __grid_constant__ PackParams p) {
   pdl_enter();
-  using P = Pieces<T, A>;
+  constexpr int R = kPackChunks;
+  using P = Lanes<T, A, R, true>;
   constexpr int E = P::E;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = (int)p.D;
   const int64_t i = (int64_t)blockIdx.x * ((kRowThreads / 32) >> p.row_shift) + (warp >> p.row_shift);
   if (i >= p.N) return;
   char* out = elem_at<T>(p.out, i * p.x_ld);
   const int8_t* codes = p.codes + i * p.codes_ld;
-  const float* scales = p.scales + i * ((p.D + kBlock8 - 1) / kBlock8);
-  const int64_t step = (int64_t)(kPackChunks * 32 * E) << p.row_shift;
-  for (int64_t c0 = (int64_t)(warp & ((1 << p.row_shift) - 1)) * (kPackChunks * 32 * E); c0 < p.D; c0 += step) {
-    uint32_t word[kPackChunks][E / 4];
-    float scale[kPackChunks][E / A];
+  const float* scales = p.scales + i * ((D + kBlock8 - 1) / kBlock8);
+  for (int64_t g = (warp & ((1 << p.row_shift) - 1)) * P::kColumns; g < D; g += (int64_t)P::kColumns << p.row_shift) {
+    const int c = (int)g + P::first(lane);
+    const bool full = g + P::kColumns <= D;
+    uint32_t word[R][2];
+    float scale[R][E / 4];  // of each four elements
 #pragma unroll
-    for (int k = 0; k < kPackChunks; ++k) {
-      const int64_t c = c0 + k * 32 * E + lane * A;
-#pragma unroll
-      for (int w = 0; w < E / 4; ++w) word[k][w] = 0u;
-#pragma unroll
-      for (int j = 0; j < E / A; ++j) {
-        const int64_t at = c + j * 32 * A;
-        if (at >= p.D) {
-          scale[k][j] = 0.0f;
-          continue;
+    for (int r = 0; r < R; ++r) {
+      word[r][0] = word[r][1] = 0u;
+      if constexpr (P::kBlocks) {
+        if (r == 0) scale[0][0] = c < D ? scales[c / kBlock8] : 0.0f;
+        if (P::inside(r, 0, c, D, full)) {
+          const int8_t* at = codes + c + P::offset(r, 0);
+          if constexpr (E == 8) {
+            const uint2 v = __ldcs(reinterpret_cast<const uint2*>(at));
+            word[r][0] = v.x;
+            word[r][1] = v.y;
+          } else {
+            word[r][0] = __ldcs(reinterpret_cast<const uint32_t*>(at));
+          }
         }
-        scale[k][j] = scales[at / kBlock8];
-        if constexpr (A == 8) {
-          const uint2 v = *reinterpret_cast<const uint2*>(codes + at);
-          word[k][0] = v.x;
-          word[k][1] = v.y;
-        } else if constexpr (A == 4) {
-          word[k][j] = *reinterpret_cast<const uint32_t*>(codes + at);
-        } else {
+      } else {
 #pragma unroll
-          for (int a = 0; a < A; ++a)
-            word[k][(j * A + a) / 4] |= (uint32_t)(uint8_t)codes[at + a] << (8 * ((j * A + a) % 4));
+        for (int e = 0; e < E; ++e) {
+          const bool in = P::inside(r, e, c, D, full);
+          if (in) word[r][e / 4] |= (uint32_t)(uint8_t)codes[c + P::offset(r, e)] << (8 * (e % 4));
+          if (e % 4 == 0) scale[r][e / 4] = in ? scales[(c + P::offset(r, e)) / kBlock8] : 0.0f;
         }
       }
     }
+    float f[R][E];
 #pragma unroll
-    for (int k = 0; k < kPackChunks; ++k) {
-      const int64_t c = c0 + k * 32 * E + lane * A;
-      if (c0 + k * 32 * E >= p.D) break;
-      float f[E];
+    for (int r = 0; r < R; ++r) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        f[e] = code_value(word[k][e / 4], e % 4) * scale[k][e / A];
-        const int64_t at = c + P::offset(e);
-        if ((p.weight || p.bias) && at < p.D)
-          f[e] = fmaf(f[e], load_weight(p.weight, p.wbf16, at, 1.0f), load_weight(p.bias, p.wbf16, at, 0.0f));
+      for (int e = 0; e < E; ++e)
+        f[r][e] = code_value(word[r][e / 4], e % 4) * (P::kBlocks ? scale[0][0] : scale[r][e / 4]);
+      if (p.weight || p.bias) {
+        float w[E], b[E];
+        P::weights(p.weight, p.wbf16, r, c, D, full, 1.0f, w);
+        P::weights(p.bias, p.wbf16, r, c, D, full, 0.0f, b);
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+          fma2(f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], w[e], w[e + 1], b[e], b[e + 1]);
       }
-      P::store(out, c, p.D, f);
     }
+    P::store(out, c, D, full, f);
   }
 }
 

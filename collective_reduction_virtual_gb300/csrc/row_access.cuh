@@ -89,6 +89,16 @@ struct Raw {
       for (int a = 0; a < A; a += 2) Elem<__nv_bfloat16>::widen2(w[a / 2], f[a], f[a + 1]);
     }
   }
+  // Puts the bits in their place among the words of 16 bytes, first: the first
+  // element's number there (words are zero so far where A * kBytes == 2).
+  __device__ __forceinline__ void into(uint32_t (&word)[4], int first) const {
+    if constexpr (kBytes == 2) {
+      word[first / 2] |= w[0] << (16 * (first % 2));
+    } else {
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) word[first * Elem<T>::kBytes / 4 + k] = w[k];
+    }
+  }
   // computed values: a NaN becomes the canonical one
   __device__ __forceinline__ void narrow(const float (&f)[A]) {
     if constexpr (Elem<T>::kBytes == 4) {
