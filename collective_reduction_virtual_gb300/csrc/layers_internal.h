@@ -88,13 +88,13 @@ constexpr int kNormMaxCtas = 608;
 // backward, where the sums over the rows are in registers too; and at most.
 VCOLL_HD constexpr int norm_chunks(int E, bool grad) { return (grad ? 16 : 32) / E; }
 VCOLL_HD constexpr int norm_max_chunks(int E, bool grad) { return grad && E == 8 ? 4 : 8; }
-// slots of the ring of rows on their way: 256 bytes a thread or so
+// slots of the ring of rows on their way: 128 to 256 bytes a thread
 VCOLL_HD constexpr int norm_stages(int R, bool grad) {
-  return grad ? (R <= 2 ? 4 : R == 4 ? 2 : 1) : (R <= 4 ? 4 : 2);
+  return grad ? (R <= 2 ? 4 : R == 4 ? 2 : 1) : (R <= 2 ? 4 : 2);
 }
 // bytes of a thread's slots of one stage of the backward ring
 VCOLL_HD constexpr int norm_grad_slot_bytes(int R, int E, bool kept) {
-  return R * 16 + (kept ? R * E + R * 8 : R * 16) + 8;
+  return R * 16 + (kept ? R * E : R * 16);
 }
 
 struct PackParams {

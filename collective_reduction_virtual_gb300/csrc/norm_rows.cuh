@@ -159,9 +159,11 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 3 : 1)
 }
 
 // Shared memory: the ring [stage] of gradient and x [r][thread] of 16 bytes
-// each (KEPT: instead of x the codes, E bytes, and the scales [r][thread] of 2
-// fp32), the row's statistics [thread] of 2 fp32; and the teams' partial sums.
-// Where A < E a warp's codes lie in the order of the columns.
+// each (KEPT: instead of x the codes, E bytes), and the teams' partial sums.
+// Where A < E a warp's codes lie in the order of the columns.  The row's
+// statistics and scales, which many lanes share, are loaded into registers one
+// row ahead: as asynchronous copies to each lane's slot they would take more of
+// the load/store unit's time than the rows themselves.
 template <typename T, int A, int R, int MT, bool KEPT>
 __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
     vc_norm_grad_rows(const __grid_constant__ NormParams p) {
@@ -180,8 +182,6 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
   const int stage = norm_grad_slot_bytes(R, E, KEPT) * threads;
   char* gslot = smem + tid * 16;
   char* xslot = smem + R * threads * 16 + tid * (KEPT ? E : 16);
-  char* cslot = smem + R * threads * (16 + E) + tid * 8;  // KEPT: scales
-  char* sslot = smem + stage - threads * 8 + tid * 8;
   float* red = reinterpret_cast<float*>(smem + S * stage) + t.index * 4 * t.warps;
 
   const int64_t teams = (int64_t)gridDim.x * (threads / 32 / p.warps);
@@ -205,29 +205,36 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
           const int from = P::kBlocks ? c + P::offset(r, 0) : col + (r * 32 + t.lane) * E;
           if (full || from < D) fetch_async<E>(xslot + at + r * threads * E, x + from);
         }
-        const float* scales = p.scales + ahead * blocks;
-#pragma unroll
-        for (int r = 0; r < SR; ++r)
-#pragma unroll
-          for (int k = 0; k < SC; ++k) {
-            const int at_col = c + (P::kBlocks ? 0 : r * 32 * E + k * kBlock8);
-            if (full || at_col < D)
-              fetch_async<4>(cslot + at + r * threads * 8 + k * 4, scales + at_col / kBlock8);
-          }
       } else {
         P::fetch(xslot + at, threads * 16, x, c, D, full);
-        fetch_async<4>(sslot + at, p.mean + ahead);
       }
-      fetch_async<4>(sslot + at + 4, p.rstd + ahead);
     }
     fetch_commit();
     ahead += teams;
     grad += gstep;
     x += xstep;
   };
+  float mean_next = 0.0f, rstd_next = 0.0f, scale_next[SR][SC];
+  auto look_ahead = [&](int64_t row) {
+    if (row >= p.N) return;
+    rstd_next = p.rstd[row];
+    if constexpr (KEPT) {
+      const float* scales = p.scales + row * blocks;
+#pragma unroll
+      for (int r = 0; r < SR; ++r)
+#pragma unroll
+        for (int k = 0; k < SC; ++k) {
+          const int at = c + (P::kBlocks ? 0 : r * 32 * E + k * kBlock8);
+          scale_next[r][k] = full || at < D ? scales[at / kBlock8] : 0.0f;
+        }
+    } else {
+      mean_next = p.mean[row];
+    }
+  };
   clear_ring(smem, S * stage);
 #pragma unroll
   for (int s = 0; s < S; ++s) fetch(s);
+  look_ahead(i);
   float dw[R][E], db[R][E];
 #pragma unroll
   for (int r = 0; r < R; ++r)
@@ -239,8 +246,13 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
     fetch_wait<S - 1>();
     if constexpr (KEPT && !P::kBlocks) __syncwarp();  // codes that other lanes fetched
     const int at = s * stage;
-    const float2 stat = *reinterpret_cast<const float2*>(sslot + at);
-    const float rstd = stat.y;
+    const float mean = mean_next, rstd = rstd_next;
+    float scale[SR][SC];
+#pragma unroll
+    for (int r = 0; r < SR; ++r)
+#pragma unroll
+      for (int k = 0; k < SC; ++k) scale[r][k] = KEPT ? scale_next[r][k] : 0.0f;
+    look_ahead(i + teams);
     // columns past the row's end have a gradient of 0, so they add nothing
     float f[R][E], h[R][E], s1x = 0.0f, s1y = 0.0f, s2x = 0.0f, s2y = 0.0f;
 #pragma unroll
@@ -248,8 +260,6 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
       Elem<T>::widen(*reinterpret_cast<const uint4*>(gslot + at + r * threads * 16), f[r]);
       if constexpr (KEPT) {
         const char* from = xslot + at + r * threads * E;
-        const float2 scale =
-            *reinterpret_cast<const float2*>(cslot + at + (P::kBlocks ? 0 : r) * threads * 8);
         uint32_t word[2] = {0u, 0u};
         if constexpr (!P::kBlocks) {
           from -= t.lane * (E - A);  // this lane's first column
@@ -265,14 +275,14 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
         }
 #pragma unroll
         for (int e = 0; e < E; e += 2) {
-          const float sc = SC == 2 && e >= 4 ? scale.y : scale.x;
+          const float sc = scale[P::kBlocks ? 0 : r][SC == 2 && e >= 4 ? 1 : 0];
           mul2(h[r][e], h[r][e + 1], code_value(word[e / 4], e % 4), code_value(word[e / 4], e % 4 + 1), sc, sc);
         }
       } else {
         Elem<T>::widen(*reinterpret_cast<const uint4*>(xslot + at + r * threads * 16), h[r]);
 #pragma unroll
         for (int e = 0; e < E; e += 2) {
-          add2(h[r][e], h[r][e + 1], h[r][e], h[r][e + 1], -stat.x, -stat.x);
+          add2(h[r][e], h[r][e + 1], h[r][e], h[r][e + 1], -mean, -mean);
           mul2(h[r][e], h[r][e + 1], h[r][e], h[r][e + 1], rstd, rstd);
         }
       }
