@@ -32,42 +32,40 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// The columns of a lane in a warp's group of R chunks (R * 32 * E columns).
-// Plainly, chunk r is 32 * E adjacent columns.  With BLOCKS, and whole accesses
-// (A == E), each block of 128 columns belongs to LANES lanes, all R accesses of
-// a lane lying in one block: its scale is then computed, or fetched, once for
-// R * E values, and an access of the warp is pieces of LANES * 16 bytes.
-template <typename T, int A, int R, bool BLOCKS>
+template <bool V>
+struct Bool {
+  static constexpr bool value = V;
+};
+
+// The columns of a lane in a warp's group of R chunks of 32 * E adjacent
+// columns.  In what follows c is the lane's first column in the row of D
+// columns; FULL: the warp's whole group lies inside the row.
+template <typename T, int A, int R>
 struct Lanes {
   static constexpr int E = kLane<T>, BYTES = A * Elem<T>::kBytes;
   static constexpr int kColumns = R * 32 * E;
-  static constexpr bool kBlocks = BLOCKS && A == E;
-  static constexpr int LANES = 128 / (R * E) < 32 ? 128 / (R * E) : 32;
-  // first column of lane in the group, and column of element e of access r from there
-  static __device__ __forceinline__ int first(int lane) {
-    return kBlocks ? lane / LANES * kBlock8 + lane % LANES * E : lane * A;
-  }
+  static __device__ __forceinline__ int first(int lane) { return lane * A; }
+  // column of element e of chunk r, from the first one
   static __device__ __forceinline__ constexpr int offset(int r, int e) {
-    return kBlocks ? r * LANES * E + e : r * 32 * E + e / A * 32 * A + e % A;
+    return r * 32 * E + e / A * 32 * A + e % A;
   }
-
-  // In what follows c is the lane's first column in the row of D columns;
-  // full: the warp's whole group lies inside the row.
-  static __device__ __forceinline__ bool inside(int r, int e, int c, int D, bool full) {
-    return full || c + offset(r, e) < D;
+  template <bool FULL>
+  static __device__ __forceinline__ bool inside(int r, int e, int c, int D) {
+    return FULL || c + offset(r, e) < D;
   }
   // slots: one of 16 bytes for each r, `step` bytes apart
-  static __device__ __forceinline__ void fetch(char* slots, int step, const char* row, int c, int D,
-                                               bool full) {
+  template <bool FULL>
+  static __device__ __forceinline__ void fetch(char* slots, int step, const char* row, int c, int D) {
     const char* from = row + (int64_t)c * Elem<T>::kBytes;
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int e = 0; e < E; e += A)
-        if (inside(r, e, c, D, full))
+        if (inside<FULL>(r, e, c, D))
           fetch_async<BYTES>(slots + r * step + e * Elem<T>::kBytes, from + offset(r, e) * Elem<T>::kBytes);
   }
-  static __device__ __forceinline__ void load(uint4 (&raw)[R], const char* row, int c, int D, bool full) {
+  template <bool FULL>
+  static __device__ __forceinline__ void load(uint4 (&raw)[R], const char* row, int c, int D) {
     const char* from = row + (int64_t)c * Elem<T>::kBytes;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -75,14 +73,15 @@ struct Lanes {
 #pragma unroll
       for (int e = 0; e < E; e += A) {
         Raw<T, A> v;
-        if (inside(r, e, c, D, full)) v.load_stream(from + offset(r, e) * Elem<T>::kBytes);
+        if (inside<FULL>(r, e, c, D)) v.load_stream(from + offset(r, e) * Elem<T>::kBytes);
         else v.zero();
         v.into(word, e);
       }
       raw[r] = make_uint4(word[0], word[1], word[2], word[3]);
     }
   }
-  static __device__ __forceinline__ void store(char* row, int c, int D, bool full, const float (&f)[R][E]) {
+  template <bool FULL>
+  static __device__ __forceinline__ void store(char* row, int c, int D, const float (&f)[R][E]) {
     char* to = row + (int64_t)c * Elem<T>::kBytes;
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -93,41 +92,66 @@ struct Lanes {
         for (int a = 0; a < A; ++a) g[a] = f[r][e + a];
         Raw<T, A> o;
         o.narrow(g);
-        if (inside(r, e, c, D, full)) o.store_stream(to + offset(r, e) * Elem<T>::kBytes);
+        if (inside<FULL>(r, e, c, D)) o.store_stream(to + offset(r, e) * Elem<T>::kBytes);
       }
   }
-  // The weight (or bias) of access r's columns, in either type, from a place
-  // that allows accesses of A elements; `none` where there is none.
-  static __device__ __forceinline__ void weights(const void* w, int bf16, int r, int c, int D, bool full,
-                                                 float none, float (&f)[E]) {
+  // The weight (or bias), of type TW, of chunk r's columns, from a place that
+  // allows accesses of A elements.
+  template <typename TW, bool FULL>
+  static __device__ __forceinline__ void weights(const void* w, int r, int c, int D, float (&f)[E]) {
+    const char* from = elem_at<TW>(w, c);
 #pragma unroll
-    for (int e = 0; e < E; ++e) f[e] = none;
-    if (!w) return;
-    if (bf16) {
-      const char* from = elem_at<__nv_bfloat16>(w, c);
+    for (int e = 0; e < E; e += A) {
+      float g[A];
+      Raw<TW, A> v;
+      if (inside<FULL>(r, e, c, D)) v.load(from + offset(r, e) * Elem<TW>::kBytes);
+      else v.zero();
+      v.widen(g);
 #pragma unroll
-      for (int e = 0; e < E; e += A)
-        if (inside(r, e, c, D, full)) {
-          float g[A];
-          Raw<__nv_bfloat16, A> v;
-          v.load(from + offset(r, e) * 2);
-          v.widen(g);
-#pragma unroll
-          for (int a = 0; a < A; ++a) f[e + a] = g[a];
-        }
-    } else {
-      const char* from = elem_at<float>(w, c);
-#pragma unroll
-      for (int e = 0; e < E; e += A)
-        if (inside(r, e, c, D, full)) {
-          float g[A];
-          Raw<float, A> v;
-          v.load(from + offset(r, e) * 4);
-          v.widen(g);
-#pragma unroll
-          for (int a = 0; a < A; ++a) f[e + a] = g[a];
-        }
+      for (int a = 0; a < A; ++a) f[e + a] = g[a];
     }
+  }
+  template <typename TW, bool FULL>
+  static __device__ __forceinline__ void scale_by(const void* w, int c, int D, float (&f)[R][E]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float v[E];
+      weights<TW, FULL>(w, r, c, D, v);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) mul2(f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], v[e], v[e + 1]);
+    }
+  }
+  template <typename TW, bool FULL>
+  static __device__ __forceinline__ void affine_by(const void* w, const void* b, int c, int D,
+                                                   float (&f)[R][E]) {
+    if (w && b) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float v[E], u[E];
+        weights<TW, FULL>(w, r, c, D, v);
+        weights<TW, FULL>(b, r, c, D, u);
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+          fma2(f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], v[e], v[e + 1], u[e], u[e + 1]);
+      }
+    } else if (w) {
+      scale_by<TW, FULL>(w, c, D, f);
+    } else if (b) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float u[E];
+        weights<TW, FULL>(b, r, c, D, u);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) add2(f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], u[e], u[e + 1]);
+      }
+    }
+  }
+  // f * weight + bias, each of which may be absent
+  template <bool FULL>
+  static __device__ __forceinline__ void affine(const void* w, const void* b, int bf16, int c, int D,
+                                                float (&f)[R][E]) {
+    if (bf16) affine_by<__nv_bfloat16, FULL>(w, b, c, D, f);
+    else affine_by<float, FULL>(w, b, c, D, f);
   }
 };
 
@@ -171,37 +195,69 @@ __device__ __forceinline__ uint32_t code_word(const float* f, const Scale8& s) {
          s.mask;
 }
 
+// The largest of R values over each LB adjacent lanes.  Halves of the values
+// change hands first, so that R values take little more shuffles than one: the
+// lane ends with the one of value group_of(lane).
+template <int R, int LB>
+struct GroupTop {
+  static constexpr int kEach = LB / R;  // adjacent lanes that end with the same value
+  static __device__ __forceinline__ int group_of(int lane) { return lane / kEach % R; }
+  static __device__ __forceinline__ uint32_t top(uint32_t (&v)[R]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int d = LB / 2, n = R; d; d >>= 1) {
+      if (n > 1) {
+        n /= 2;
+#pragma unroll
+        for (int k = 0; k < R / 2; ++k)
+          if (k < n) {
+            const uint32_t mine = lane & d ? v[k + n] : v[k], other = lane & d ? v[k] : v[k + n];
+            v[k] = max(mine, __shfl_xor_sync(~0u, other, d));
+          }
+      } else {
+        v[0] = max(v[0], __shfl_xor_sync(~0u, v[0], d));
+      }
+    }
+    return v[0];
+  }
+};
+
 // Keeps a warp's group of values: the codes and the scales of its blocks.
 // Values past the row's end are 0.  col: the group's first column, a multiple
 // of 128; c = col + Lanes::first(lane).
 template <typename T, int A, int R>
 __device__ __forceinline__ void keep8(const float (&f)[R][kLane<T>], int col, int c, int D, int8_t* codes,
                                       float* scales) {
-  using P = Lanes<T, A, R, true>;
+  using P = Lanes<T, A, R>;
   constexpr int E = P::E;
   const int lane = threadIdx.x & 31, end = (D + 15) & ~15;
-  if constexpr (P::kBlocks) {
-    uint32_t top = 0u;
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int e = 0; e < E; ++e) top = max(top, magnitude_bits(f[r][e]));
-    if constexpr (P::LANES == 32) {
-      top = __reduce_max_sync(~0u, top);
-    } else {
-#pragma unroll
-      for (int d = P::LANES / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
-    }
-    const Scale8 s = scale8(top);
+  if constexpr (A == E) {
+    // a block is LB adjacent lanes' access: each lane computes the scale of one
+    // of its R blocks
+    constexpr int LB = kBlock8 / E;
+    using G = GroupTop<R, LB>;
+    uint32_t top[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (c + P::offset(r, 0) >= end) break;
+      top[r] = 0u;
+#pragma unroll
+      for (int e = 0; e < E; ++e) top[r] = max(top[r], magnitude_bits(f[r][e]));
+    }
+    const Scale8 mine = scale8(G::top(top));
+    const int first = lane & ~(LB - 1);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      Scale8 s;
+      s.unit = __shfl_sync(~0u, mine.unit, first + r * G::kEach);
+      s.mask = s.unit != 0.0f ? 0xFFFFFFFFu : 0u;
+      if (c + P::offset(r, 0) >= end) continue;
       int8_t* at = codes + c + P::offset(r, 0);
       if constexpr (E == 8)
         *reinterpret_cast<uint2*>(at) = make_uint2(code_word(f[r], s), code_word(f[r] + 4, s));
       else *reinterpret_cast<uint32_t*>(at) = code_word(f[r], s);
     }
-    if (lane % P::LANES == 0 && c < D) scales[c / kBlock8] = s.scale;
+    const int at = col + G::group_of(lane) * 32 * E + first * E;  // the block's first column
+    if (lane % G::kEach == 0 && at < D) scales[at / kBlock8] = mine.scale;
   } else {
     constexpr int B = 32 * E / kBlock8;  // blocks of a chunk, 4 elements of a lane in each
 #pragma unroll

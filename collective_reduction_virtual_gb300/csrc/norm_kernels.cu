@@ -175,7 +175,7 @@ template <typename T, int A>
 __global__ void __launch_bounds__(kRowThreads) vc_pack8(const __grid_constant__ PackParams p) {
   pdl_enter();
   constexpr int R = kPackChunks;
-  using P = Lanes<T, A, R, true>;
+  using P = Lanes<T, A, R>;
   constexpr int E = P::E;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = (int)p.D;
   const int64_t i = (int64_t)blockIdx.x * ((kRowThreads / 32) >> p.row_shift) + (warp >> p.row_shift);
@@ -187,7 +187,8 @@ __global__ void __launch_bounds__(kRowThreads) vc_pack8(const __grid_constant__ 
   for (int64_t g = (warp & ((1 << p.row_shift) - 1)) * P::kColumns; g < D; g += (int64_t)P::kColumns << p.row_shift) {
     const int col = (int)g, c = col + P::first(lane);
     uint4 raw[R];
-    P::load(raw, x, c, D, g + P::kColumns <= D);
+    if (g + P::kColumns <= D) P::template load<true>(raw, x, c, D);
+    else P::template load<false>(raw, x, c, D);
     float f[R][E];
 #pragma unroll
     for (int r = 0; r < R; ++r) Elem<T>::widen(raw[r], f[r]);
@@ -199,7 +200,7 @@ template <typename T, int A>
 __global__ void __launch_bounds__(kRowThreads) vc_unpack8(const __grid_constant__ PackParams p) {
   pdl_enter();
   constexpr int R = kPackChunks;
-  using P = Lanes<T, A, R, true>;
+  using P = Lanes<T, A, R>;
   constexpr int E = P::E;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = (int)p.D;
   const int64_t i = (int64_t)blockIdx.x * ((kRowThreads / 32) >> p.row_shift) + (warp >> p.row_shift);
@@ -209,49 +210,48 @@ __global__ void __launch_bounds__(kRowThreads) vc_unpack8(const __grid_constant_
   const float* scales = p.scales + i * ((D + kBlock8 - 1) / kBlock8);
   for (int64_t g = (warp & ((1 << p.row_shift) - 1)) * P::kColumns; g < D; g += (int64_t)P::kColumns << p.row_shift) {
     const int c = (int)g + P::first(lane);
-    const bool full = g + P::kColumns <= D;
-    uint32_t word[R][2];
-    float scale[R][E / 4];  // of each four elements
+    auto group = [&](auto full) {
+      constexpr bool FULL = decltype(full)::value;
+      uint32_t word[R][2];
+      float scale[R][E / 4];  // of each four elements
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      word[r][0] = word[r][1] = 0u;
-      if constexpr (P::kBlocks) {
-        if (r == 0) scale[0][0] = c < D ? scales[c / kBlock8] : 0.0f;
-        if (P::inside(r, 0, c, D, full)) {
-          const int8_t* at = codes + c + P::offset(r, 0);
-          if constexpr (E == 8) {
-            const uint2 v = __ldcs(reinterpret_cast<const uint2*>(at));
-            word[r][0] = v.x;
-            word[r][1] = v.y;
-          } else {
-            word[r][0] = __ldcs(reinterpret_cast<const uint32_t*>(at));
+      for (int r = 0; r < R; ++r) {
+        word[r][0] = word[r][1] = 0u;
+        if constexpr (A == E) {
+          scale[r][0] = 0.0f;
+          if (P::template inside<FULL>(r, 0, c, D)) {
+            const int at = c + P::offset(r, 0);
+            scale[r][0] = scales[at / kBlock8];
+            if constexpr (E == 8) {
+              const uint2 v = __ldcs(reinterpret_cast<const uint2*>(codes + at));
+              word[r][0] = v.x;
+              word[r][1] = v.y;
+            } else {
+              word[r][0] = __ldcs(reinterpret_cast<const uint32_t*>(codes + at));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const bool in = P::template inside<FULL>(r, e, c, D);
+            if (in) word[r][e / 4] |= (uint32_t)(uint8_t)codes[c + P::offset(r, e)] << (8 * (e % 4));
+            if (e % 4 == 0) scale[r][e / 4] = in ? scales[(c + P::offset(r, e)) / kBlock8] : 0.0f;
           }
         }
-      } else {
+      }
+      float f[R][E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const bool in = P::inside(r, e, c, D, full);
-          if (in) word[r][e / 4] |= (uint32_t)(uint8_t)codes[c + P::offset(r, e)] << (8 * (e % 4));
-          if (e % 4 == 0) scale[r][e / 4] = in ? scales[(c + P::offset(r, e)) / kBlock8] : 0.0f;
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float s = scale[r][A == E ? 0 : e / 4];
+          mul2(f[r][e], f[r][e + 1], code_value(word[r][e / 4], e % 4), code_value(word[r][e / 4], e % 4 + 1), s, s);
         }
-      }
-    }
-    float f[R][E];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        f[r][e] = code_value(word[r][e / 4], e % 4) * (P::kBlocks ? scale[0][0] : scale[r][e / 4]);
-      if (p.weight || p.bias) {
-        float w[E], b[E];
-        P::weights(p.weight, p.wbf16, r, c, D, full, 1.0f, w);
-        P::weights(p.bias, p.wbf16, r, c, D, full, 0.0f, b);
-#pragma unroll
-        for (int e = 0; e < E; e += 2)
-          fma2(f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], w[e], w[e + 1], b[e], b[e + 1]);
-      }
-    }
-    P::store(out, c, D, full, f);
+      P::template affine<FULL>(p.weight, p.bias, p.wbf16, c, D, f);
+      P::template store<FULL>(out, c, D, f);
+    };
+    if (g + P::kColumns <= D) group(Bool<true>());
+    else group(Bool<false>());
   }
 }
 

@@ -73,89 +73,79 @@ template <typename T, int A, int R, int MT, bool KEEP>
 __global__ void __launch_bounds__(MT, MT == 256 ? 3 : 1)
     vc_norm_rows(const __grid_constant__ NormParams p) {
   pdl_enter();
-  // the same lanes whether h is kept or not: the same order of sums, so the same y
-  using P = Lanes<T, A, R, true>;
+  using P = Lanes<T, A, R>;
   constexpr int E = P::E, S = norm_stages(R, false);
   extern __shared__ __align__(16) char smem[];
   const int threads = blockDim.x, D = (int)p.D;
   const Team t(p.warps);
   const int col = t.warp * P::kColumns, c = col + P::first(t.lane);
-  const bool full = col + P::kColumns <= D;
   char* ring = smem + threadIdx.x * 16;
   const int slot = threads * 16;  // from one slot of a thread to its next
   float* red = reinterpret_cast<float*>(smem + S * R * slot) + t.index * 4 * t.warps;
 
-  const int64_t teams = (int64_t)gridDim.x * (threads / 32 / p.warps);
-  int64_t i = (int64_t)blockIdx.x * (threads / 32 / p.warps) + t.index;
-  int64_t ahead = i;  // next row to fetch
-  const char* x = elem_at<T>(p.x, i * p.x_ld);
-  const int64_t xstep = teams * p.x_ld * Elem<T>::kBytes, ystep = teams * p.y_ld * Elem<T>::kBytes;
-  char* y = elem_at<T>(p.y, i * p.y_ld);
-  auto fetch = [&](int s) {
-    if (ahead < p.N) P::fetch(ring + s * R * slot, slot, x, c, D, full);
-    fetch_commit();
-    ahead += teams;
-    x += xstep;
-  };
+  const uint32_t rows = (uint32_t)p.N, teams = gridDim.x * (threads / 32 / p.warps);
+  const uint32_t begin = blockIdx.x * (threads / 32 / p.warps) + t.index;
   clear_ring(smem, S * R * slot);
+  // a warp whose columns all lie inside the row needs no guards
+  auto work = [&](auto full) {
+    constexpr bool FULL = decltype(full)::value;
+    const char* x = elem_at<T>(p.x, begin * p.x_ld);
+    char* y = elem_at<T>(p.y, begin * p.y_ld);
+    const int64_t xstep = teams * p.x_ld * Elem<T>::kBytes, ystep = teams * p.y_ld * Elem<T>::kBytes;
+    uint32_t ahead = begin;  // next row to fetch
+    auto fetch = [&](int s) {
+      if (ahead < rows) P::template fetch<FULL>(ring + s * R * slot, slot, x, c, D);
+      fetch_commit();
+      ahead += teams;
+      x += xstep;
+    };
 #pragma unroll
-  for (int s = 0; s < S; ++s) fetch(s);
-  int s = 0;
-  for (; i < p.N; i += teams, y += ystep) {
-    fetch_wait<S - 1>();
-    float f[R][E], sx = 0.0f, sy = 0.0f;
+    for (int s = 0; s < S; ++s) fetch(s);
+    int s = 0;
+    for (uint32_t i = begin; i < rows; i += teams, y += ystep) {
+      fetch_wait<S - 1>();
+      float f[R][E], sx = 0.0f, sy = 0.0f;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      Elem<T>::widen(*reinterpret_cast<const uint4*>(ring + (s * R + r) * slot), f[r]);
+      for (int r = 0; r < R; ++r) {
+        Elem<T>::widen(*reinterpret_cast<const uint4*>(ring + (s * R + r) * slot), f[r]);
 #pragma unroll
-      for (int e = 0; e < E; e += 2) add2(sx, sy, sx, sy, f[r][e], f[r][e + 1]);
-    }
-    float mean = warp_sum(sx + sy);
-    fetch(s);  // the slot has been read
-    s = s + 1 == S ? 0 : s + 1;
-    if (t.warps > 1) mean = t.sum(mean, red);
-    mean /= (float)D;
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int e = 0; e < E; e += 2)
-        add2(f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], -mean, -mean);
-    if (!full)
+        for (int e = 0; e < E; e += 2) add2(sx, sy, sx, sy, f[r][e], f[r][e + 1]);
+      }
+      float mean = warp_sum(sx + sy);
+      fetch(s);  // the slot has been read
+      s = s + 1 == S ? 0 : s + 1;
+      if (t.warps > 1) mean = t.sum(mean, red);
+      mean /= (float)D;
+      float qx = 0.0f, qy = 0.0f;
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (c + P::offset(r, e) >= D) f[r][e] = 0.0f;
-    float qx = 0.0f, qy = 0.0f;
+        for (int e = 0; e < E; e += 2) {
+          add2(f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], -mean, -mean);
+          if (!P::template inside<FULL>(r, e, c, D)) f[r][e] = 0.0f;
+          if (!P::template inside<FULL>(r, e + 1, c, D)) f[r][e + 1] = 0.0f;
+          fma2(qx, qy, f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], qx, qy);
+        }
+      float var = warp_sum(qx + qy);
+      if (t.warps > 1) var = t.sum(var, red + 2 * t.warps);
+      const float rstd = rsqrtf(var / (float)D + p.eps);
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+      for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int e = 0; e < E; e += 2)
-        fma2(qx, qy, f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], qx, qy);
-    float var = warp_sum(qx + qy);
-    if (t.warps > 1) var = t.sum(var, red + 2 * t.warps);
-    const float rstd = rsqrtf(var / (float)D + p.eps);
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int e = 0; e < E; e += 2) mul2(f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], rstd, rstd);
-    if constexpr (KEEP)
-      keep8<T, A, R>(f, col, c, D, p.codes + i * p.codes_ld, p.scales + i * ((D + kBlock8 - 1) / kBlock8));
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float w[E], b[E];
-      P::weights(p.weight, p.wbf16, r, c, D, full, 1.0f, w);
-      P::weights(p.bias, p.wbf16, r, c, D, full, 0.0f, b);
-#pragma unroll
-      for (int e = 0; e < E; e += 2)
-        fma2(f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], w[e], w[e + 1], b[e], b[e + 1]);
+        for (int e = 0; e < E; e += 2) mul2(f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], rstd, rstd);
+      if constexpr (KEEP)
+        keep8<T, A, R>(f, col, c, D, p.codes + i * p.codes_ld,
+                       p.scales + (int64_t)i * ((D + kBlock8 - 1) / kBlock8));
+      P::template affine<FULL>(p.weight, p.bias, p.wbf16, c, D, f);
+      P::template store<FULL>(y, c, D, f);
+      if (t.warp == 0 && t.lane == 0) {
+        if (p.mean) p.mean[i] = mean;
+        if (p.rstd) p.rstd[i] = rstd;
+      }
     }
-    P::store(y, c, D, full, f);
-    if (t.warp == 0 && t.lane == 0) {
-      if (p.mean) p.mean[i] = mean;
-      if (p.rstd) p.rstd[i] = rstd;
-    }
-  }
+  };
+  if (col + P::kColumns <= D) work(Bool<true>());
+  else work(Bool<false>());
 }
 
 // Shared memory: the ring [stage] of gradient and x [r][thread] of 16 bytes
@@ -168,160 +158,168 @@ template <typename T, int A, int R, int MT, bool KEPT>
 __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
     vc_norm_grad_rows(const __grid_constant__ NormParams p) {
   pdl_enter();
-  using P = Lanes<T, A, R, KEPT>;
+  using P = Lanes<T, A, R>;
   constexpr int E = P::E, S = norm_stages(R, true);
-  // scales that a lane needs for an access: all accesses share one, or the
-  // blocks of a chunk have one each
-  constexpr int SR = P::kBlocks ? 1 : R, SC = P::kBlocks ? 1 : 32 * E / kBlock8;
+  // scales that a lane needs for a chunk: of its access's block, or of all
+  constexpr int SC = A == E ? 1 : 32 * E / kBlock8;
   extern __shared__ __align__(16) char smem[];
   const int threads = blockDim.x, tid = threadIdx.x, D = (int)p.D;
   const int blocks = (D + kBlock8 - 1) / kBlock8;
   const Team t(p.warps);
   const int col = t.warp * P::kColumns, c = col + P::first(t.lane);
-  const bool full = col + P::kColumns <= D;
   const int stage = norm_grad_slot_bytes(R, E, KEPT) * threads;
   char* gslot = smem + tid * 16;
   char* xslot = smem + R * threads * 16 + tid * (KEPT ? E : 16);
   float* red = reinterpret_cast<float*>(smem + S * stage) + t.index * 4 * t.warps;
 
-  const int64_t teams = (int64_t)gridDim.x * (threads / 32 / p.warps);
-  int64_t i = (int64_t)blockIdx.x * (threads / 32 / p.warps) + t.index;
-  int64_t ahead = i;  // next row to fetch
-  const char* grad = elem_at<T>(p.grad, i * p.grad_ld);
-  const char* x = KEPT ? reinterpret_cast<const char*>(p.codes) + i * p.codes_ld : elem_at<T>(p.x, i * p.x_ld);
-  char* dx = p.y ? elem_at<T>(p.y, i * p.y_ld) : nullptr;
-  const int64_t gstep = teams * p.grad_ld * Elem<T>::kBytes;
-  const int64_t xstep = KEPT ? teams * p.codes_ld : teams * p.x_ld * Elem<T>::kBytes;
-  const int64_t dstep = p.y ? teams * p.y_ld * Elem<T>::kBytes : 0;
-  auto fetch = [&](int s) {
-    if (ahead < p.N) {
-      const int at = s * stage;
-      P::fetch(gslot + at, threads * 16, grad, c, D, full);
-      if constexpr (KEPT) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          // pieces of E bytes whatever A is: rows of codes are 16-byte aligned
-          // and padded
-          const int from = P::kBlocks ? c + P::offset(r, 0) : col + (r * 32 + t.lane) * E;
-          if (full || from < D) fetch_async<E>(xslot + at + r * threads * E, x + from);
-        }
-      } else {
-        P::fetch(xslot + at, threads * 16, x, c, D, full);
-      }
-    }
-    fetch_commit();
-    ahead += teams;
-    grad += gstep;
-    x += xstep;
-  };
-  float mean_next = 0.0f, rstd_next = 0.0f, scale_next[SR][SC];
-  auto look_ahead = [&](int64_t row) {
-    if (row >= p.N) return;
-    rstd_next = p.rstd[row];
-    if constexpr (KEPT) {
-      const float* scales = p.scales + row * blocks;
-#pragma unroll
-      for (int r = 0; r < SR; ++r)
-#pragma unroll
-        for (int k = 0; k < SC; ++k) {
-          const int at = c + (P::kBlocks ? 0 : r * 32 * E + k * kBlock8);
-          scale_next[r][k] = full || at < D ? scales[at / kBlock8] : 0.0f;
-        }
-    } else {
-      mean_next = p.mean[row];
-    }
-  };
-  clear_ring(smem, S * stage);
-#pragma unroll
-  for (int s = 0; s < S; ++s) fetch(s);
-  look_ahead(i);
+  const uint32_t rows = (uint32_t)p.N, teams = gridDim.x * (threads / 32 / p.warps);
+  const uint32_t begin = blockIdx.x * (threads / 32 / p.warps) + t.index;
   float dw[R][E], db[R][E];
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int e = 0; e < E; ++e) dw[r][e] = db[r][e] = 0.0f;
-
-  int s = 0, place = 0;
-  for (; i < p.N; i += teams, dx += dstep) {
-    fetch_wait<S - 1>();
-    if constexpr (KEPT && !P::kBlocks) __syncwarp();  // codes that other lanes fetched
-    const int at = s * stage;
-    const float mean = mean_next, rstd = rstd_next;
-    float scale[SR][SC];
+  clear_ring(smem, S * stage);
+  auto work = [&](auto full) {
+    constexpr bool FULL = decltype(full)::value;
+    const char* grad = elem_at<T>(p.grad, begin * p.grad_ld);
+    const char* x = KEPT ? reinterpret_cast<const char*>(p.codes) + begin * p.codes_ld
+                         : elem_at<T>(p.x, begin * p.x_ld);
+    char* dx = p.y ? elem_at<T>(p.y, begin * p.y_ld) : nullptr;
+    const int64_t gstep = teams * p.grad_ld * Elem<T>::kBytes;
+    const int64_t xstep = KEPT ? teams * p.codes_ld : teams * p.x_ld * Elem<T>::kBytes;
+    const int64_t dstep = p.y ? teams * p.y_ld * Elem<T>::kBytes : 0;
+    uint32_t ahead = begin;  // next row to fetch
+    auto fetch = [&](int s) {
+      if (ahead < rows) {
+        const int at = s * stage;
+        P::template fetch<FULL>(gslot + at, threads * 16, grad, c, D);
+        if constexpr (KEPT) {
 #pragma unroll
-    for (int r = 0; r < SR; ++r)
-#pragma unroll
-      for (int k = 0; k < SC; ++k) scale[r][k] = KEPT ? scale_next[r][k] : 0.0f;
-    look_ahead(i + teams);
-    // columns past the row's end have a gradient of 0, so they add nothing
-    float f[R][E], h[R][E], s1x = 0.0f, s1y = 0.0f, s2x = 0.0f, s2y = 0.0f;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      Elem<T>::widen(*reinterpret_cast<const uint4*>(gslot + at + r * threads * 16), f[r]);
-      if constexpr (KEPT) {
-        const char* from = xslot + at + r * threads * E;
-        uint32_t word[2] = {0u, 0u};
-        if constexpr (!P::kBlocks) {
-          from -= t.lane * (E - A);  // this lane's first column
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            word[e / 4] |= (uint32_t)(uint8_t)from[P::offset(0, e)] << (8 * (e % 4));
-        } else if constexpr (E == 8) {
-          const uint2 v = *reinterpret_cast<const uint2*>(from);
-          word[0] = v.x;
-          word[1] = v.y;
+          for (int r = 0; r < R; ++r) {
+            // pieces of E bytes whatever A is: rows of codes are 16-byte aligned
+            // and padded
+            const int from = col + (r * 32 + t.lane) * E;
+            if (FULL || from < D) fetch_async<E>(xslot + at + r * threads * E, x + from);
+          }
         } else {
-          word[0] = *reinterpret_cast<const uint32_t*>(from);
+          P::template fetch<FULL>(xslot + at, threads * 16, x, c, D);
         }
+      }
+      fetch_commit();
+      ahead += teams;
+      grad += gstep;
+      x += xstep;
+    };
+    float mean_next = 0.0f, rstd_next = 0.0f, scale_next[R][SC];
+    auto look_ahead = [&](uint32_t row) {
+      if (row >= rows) return;
+      rstd_next = p.rstd[row];
+      if constexpr (KEPT) {
+        const float* scales = p.scales + (int64_t)row * blocks;
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float sc = scale[P::kBlocks ? 0 : r][SC == 2 && e >= 4 ? 1 : 0];
-          mul2(h[r][e], h[r][e + 1], code_value(word[e / 4], e % 4), code_value(word[e / 4], e % 4 + 1), sc, sc);
-        }
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int k = 0; k < SC; ++k) {
+            const int at = c + r * 32 * E + k * kBlock8;
+            scale_next[r][k] = FULL || at < D ? scales[at / kBlock8] : 0.0f;
+          }
       } else {
-        Elem<T>::widen(*reinterpret_cast<const uint4*>(xslot + at + r * threads * 16), h[r]);
+        mean_next = p.mean[row];
+      }
+    };
+#pragma unroll
+    for (int s = 0; s < S; ++s) fetch(s);
+    look_ahead(begin);
+    int s = 0, place = 0;
+    for (uint32_t i = begin; i < rows; i += teams, dx += dstep) {
+      fetch_wait<S - 1>();
+      if constexpr (KEPT && A < E) __syncwarp();  // codes that other lanes fetched
+      const int at = s * stage;
+      [[maybe_unused]] const float mean = mean_next;
+      const float rstd = rstd_next;
+      float scale[R][SC];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int k = 0; k < SC; ++k) scale[r][k] = KEPT ? scale_next[r][k] : 0.0f;
+      look_ahead(i + teams);
+      // columns past the row's end have a gradient of 0, so they add nothing
+      float f[R][E], h[R][E];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        Elem<T>::widen(*reinterpret_cast<const uint4*>(gslot + at + r * threads * 16), f[r]);
+        if constexpr (KEPT) {
+          const char* from = xslot + at + r * threads * E;
+          uint32_t word[2] = {0u, 0u};
+          if constexpr (A < E) {
+            from -= t.lane * (E - A);  // this lane's first column
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              word[e / 4] |= (uint32_t)(uint8_t)from[P::offset(0, e)] << (8 * (e % 4));
+          } else if constexpr (E == 8) {
+            const uint2 v = *reinterpret_cast<const uint2*>(from);
+            word[0] = v.x;
+            word[1] = v.y;
+          } else {
+            word[0] = *reinterpret_cast<const uint32_t*>(from);
+          }
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const float sc = scale[r][SC == 2 && e >= 4 ? 1 : 0];
+            mul2(h[r][e], h[r][e + 1], code_value(word[e / 4], e % 4), code_value(word[e / 4], e % 4 + 1), sc, sc);
+          }
+        } else {
+          Elem<T>::widen(*reinterpret_cast<const uint4*>(xslot + at + r * threads * 16), h[r]);
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            add2(h[r][e], h[r][e + 1], h[r][e], h[r][e + 1], -mean, -mean);
+            mul2(h[r][e], h[r][e + 1], h[r][e], h[r][e + 1], rstd, rstd);
+          }
+        }
 #pragma unroll
         for (int e = 0; e < E; e += 2) {
-          add2(h[r][e], h[r][e + 1], h[r][e], h[r][e + 1], -mean, -mean);
-          mul2(h[r][e], h[r][e + 1], h[r][e], h[r][e + 1], rstd, rstd);
+          fma2(dw[r][e], dw[r][e + 1], f[r][e], f[r][e + 1], h[r][e], h[r][e + 1], dw[r][e], dw[r][e + 1]);
+          add2(db[r][e], db[r][e + 1], db[r][e], db[r][e + 1], f[r][e], f[r][e + 1]);
         }
       }
-      float w[E];
-      P::weights(p.weight, p.wbf16, r, c, D, full, 1.0f, w);
+      P::template affine<FULL>(p.weight, nullptr, p.wbf16, c, D, f);  // g
+      float s1x = 0.0f, s1y = 0.0f, s2x = 0.0f, s2y = 0.0f;
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        fma2(dw[r][e], dw[r][e + 1], f[r][e], f[r][e + 1], h[r][e], h[r][e + 1], dw[r][e], dw[r][e + 1]);
-        add2(db[r][e], db[r][e + 1], db[r][e], db[r][e + 1], f[r][e], f[r][e + 1]);
-        mul2(f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], w[e], w[e + 1]);  // g from here on
-        add2(s1x, s1y, s1x, s1y, f[r][e], f[r][e + 1]);
-        fma2(s2x, s2y, f[r][e], f[r][e + 1], h[r][e], h[r][e + 1], s2x, s2y);
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          add2(s1x, s1y, s1x, s1y, f[r][e], f[r][e + 1]);
+          fma2(s2x, s2y, f[r][e], f[r][e + 1], h[r][e], h[r][e + 1], s2x, s2y);
+        }
+      float s1 = warp_sum(s1x + s1y), s2 = warp_sum(s2x + s2y);
+      fetch(s);  // the slot has been read
+      s = s + 1 == S ? 0 : s + 1;
+      if (!p.y) continue;
+      if (t.warps > 1) {
+        t.sum2(s1, s2, red + place);
+        place ^= 2 * t.warps;
       }
-    }
-    float s1 = warp_sum(s1x + s1y), s2 = warp_sum(s2x + s2y);
-    fetch(s);  // the slot has been read
-    s = s + 1 == S ? 0 : s + 1;
-    if (!p.y) continue;
-    if (t.warps > 1) {
-      t.sum2(s1, s2, red + place);
-      place ^= 2 * t.warps;
-    }
-    s1 /= -(float)D;
-    s2 /= -(float)D;
+      s1 /= -(float)D;
+      s2 /= -(float)D;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+      for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        add2(f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], s1, s1);
-        fma2(f[r][e], f[r][e + 1], h[r][e], h[r][e + 1], s2, s2, f[r][e], f[r][e + 1]);
-        mul2(f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], rstd, rstd);
-      }
-    P::store(dx, c, D, full, f);
-  }
+        for (int e = 0; e < E; e += 2) {
+          add2(f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], s1, s1);
+          fma2(f[r][e], f[r][e + 1], h[r][e], h[r][e + 1], s2, s2, f[r][e], f[r][e + 1]);
+          mul2(f[r][e], f[r][e + 1], f[r][e], f[r][e + 1], rstd, rstd);
+        }
+      P::template store<FULL>(dx, c, D, f);
+    }
+  };
+  if (col + P::kColumns <= D) work(Bool<true>());
+  else work(Bool<false>());
   if (!p.part) return;
   // the CTA's sums: its teams add theirs up in the ring's memory, in order
   fetch_wait<0>();
   const int count = threads / 32 / p.warps;
-  float* rows = reinterpret_cast<float*>(smem);  // [2][E * R][team's thread]
+  float* sums = reinterpret_cast<float*>(smem);  // [2][E * R][team's thread]
   const int width = p.warps * 32, own = t.warp * 32 + t.lane;
   for (int k = 0; k < count; ++k) {
     __syncthreads();
@@ -330,7 +328,7 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        float* a = rows + (r * E + e) * width + own;
+        float* a = sums + (r * E + e) * width + own;
         float* b = a + R * E * width;
         if (k) {
           dw[r][e] = *a + dw[r][e];
