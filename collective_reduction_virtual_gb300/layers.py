@@ -120,13 +120,33 @@ def vcoll_layer_norm_backward_checkpoint8(grad, grad_ld, codes, codes_ld, scales
 
 
 # -------------------------------------------------------------- tensor layer
+# A call on a few rows takes the GPU a few microseconds, so these functions
+# keep the host's work short: the raw handle of the current stream, checks of
+# the common case first, and one pass over each argument.
 
 _TYPES = {torch.float32: F32, torch.bfloat16: BF16}
 _INDEX = {torch.int32: I32, torch.int64: I64}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _refuse(message, status=ERR_INVALID_ARG):
     raise VcollError(status, message)
+
+
+def _handle(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(device)
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _empty(shape, dtype, stream):
+    """A tensor allocated on the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device="cuda")
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device="cuda")
 
 
 def _dtype(t, what):
@@ -136,26 +156,25 @@ def _dtype(t, what):
     return code
 
 
-def _place(t, what):
-    """The tensor lies where the kernels of the current device may reach it."""
+def _place(t, what, device):
+    """Refuses a tensor that the kernels of the current device cannot reach."""
     if t.is_cuda:
-        if t.get_device() != torch.cuda.current_device():
-            _refuse(f"{what} is on device {t.get_device()}, the current device is "
-                    f"{torch.cuda.current_device()}")
-    elif not t.is_pinned():
+        _refuse(f"{what} is on device {t.get_device()}, the current device is {device}")
+    if not t.is_pinned():
         _refuse(f"{what} is neither a CUDA tensor nor pinned host memory")
 
 
-def _rows(t, what, width=None, rows=None):
-    """(rows, row stride in elements) of a tensor taken as a matrix."""
-    _place(t, what)
-    if t.dim() == 0:
+def _rows(t, what, device, width=None, rows=None):
+    """(rows, columns, row stride in elements) of a tensor taken as a matrix."""
+    if t.get_device() != device:
+        _place(t, what, device)
+    shape = t.shape
+    if not shape:
         _refuse(f"{what} has no axes")
-    d = t.shape[-1]
-    if width is not None and d != width:
-        _refuse(f"{what} has {d} columns, {width} are expected")
+    d = shape[-1]
     if t.is_contiguous():
-        n, ld = (t.numel() // d if d else t.shape[:-1].numel()), d
+        n = shape[0] if len(shape) == 2 else shape[:-1].numel()
+        ld = d
     else:
         try:
             m = t.view(-1, d) if d else t
@@ -165,76 +184,68 @@ def _rows(t, what, width=None, rows=None):
             _refuse(f"{what} is not a matrix of rows with adjacent columns (not contiguous)")
         n = m.shape[0]
         ld = m.stride(0) if n > 1 else d
+    if width is not None and d != width:
+        _refuse(f"{what} has {d} columns, {width} are expected")
     if rows is not None and n != rows:
         _refuse(f"{what} has {n} rows, {rows} are expected")
-    return n, ld
+    return n, d, ld
 
 
-def _vector(t, what, length, dtype=None):
-    _place(t, what)
+def _vector(t, what, device, length, dtype):
+    if t.get_device() != device:
+        _place(t, what, device)
     if t.numel() != length or not t.is_contiguous():
         _refuse(f"{what} is not a contiguous tensor of {length} elements")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype != dtype:
         _refuse(f"{what} is {t.dtype}, {dtype} is expected", ERR_INVALID_TYPE)
     return t.data_ptr()
 
 
-class _Call:
-    """The stream of one call, and the tensors that it allocates there."""
-
-    __slots__ = ("stream", "handle")
-
-    def __init__(self, stream):
-        self.stream = stream
-        self.handle = (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
-
-    def empty(self, shape, dtype):
-        if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device="cuda")
-        with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device="cuda")
-
-    def workspace(self, given, need):
-        """(pointer, bytes, the tensor to hold on to)."""
-        if given is None:
-            if not need:
-                return 0, 0, None
-            given = self.empty(need, torch.uint8)
-        _place(given, "workspace")
-        return given.data_ptr(), given.numel() * given.element_size(), given
-
-
-def _tokens(tokens):
+def _tokens(tokens, device):
     code = _INDEX.get(tokens.dtype)
     if code is None:
         _refuse(f"tokens: unsupported dtype {tokens.dtype}", ERR_INVALID_TYPE)
-    _place(tokens, "tokens")
+    if tokens.get_device() != device:
+        _place(tokens, "tokens", device)
     if not tokens.is_contiguous():
         _refuse("tokens is not contiguous")
     return code
+
+
+def _workspace(given, need, device, stream):
+    """(pointer, bytes, the tensor to hold on to)."""
+    if given is None:
+        if not need:
+            return 0, 0, None
+        given = _empty(need, torch.uint8, stream)
+        return given.data_ptr(), need, given
+    if given.get_device() != device:
+        _place(given, "workspace", device)
+    return given.data_ptr(), given.numel() * given.element_size(), given
 
 
 def embedding(tokens, table, scale=1.0, out=None, stream=None):
     """scale * table[tokens]: tokens (int32 or int64) of any shape, table
     [V, D].  A token outside [0, V) gives zeros.  Returns out, [*tokens.shape,
     D] of table's type."""
-    index = _tokens(tokens)
+    device = torch.cuda.current_device()
+    index = _tokens(tokens, device)
     dtype = _dtype(table, "table")
     if table.dim() != 2:
         _refuse("table is not a matrix")
-    V, D = table.shape
-    _, table_ld = _rows(table, "table")
+    V, D, table_ld = _rows(table, "table", device)
     N = tokens.numel()
-    call = _Call(stream)
     if out is None:
-        out = call.empty((*tokens.shape, D), table.dtype)
+        out = _empty((*tokens.shape, D), table.dtype, stream)
         out_ld = D
     else:
-        _, out_ld = _rows(out, "out", D, N)
+        _, _, out_ld = _rows(out, "out", device, D, N)
         if out.dtype != table.dtype:
             _refuse(f"out is {out.dtype}, table {table.dtype}", ERR_INVALID_TYPE)
-    _check(vcoll_embedding(tokens.data_ptr(), index, N, table.data_ptr(), table_ld, V, D, scale,
-                           out.data_ptr(), out_ld, dtype, call.handle))
+    rc = _fn("vcoll_embedding")(tokens.data_ptr(), index, N, table.data_ptr(), table_ld, V, D,
+                                scale, out.data_ptr(), out_ld, dtype, _handle(stream, device))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -251,50 +262,52 @@ def embedding_backward(grad, tokens, vocab, scale=1.0, base=None, out=None, dtyp
     only the rows of tokens that occur.  dtype: out's type (base's, or
     grad's).  workspace: a uint8 CUDA tensor of embedding_workspace_bytes(N,
     vocab, D) bytes, allocated here when omitted."""
-    index = _tokens(tokens)
-    N = tokens.numel()
+    device = torch.cuda.current_device()
+    index = _tokens(tokens, device)
     code = _dtype(grad, "grad")
-    _, grad_ld = _rows(grad, "grad", None, N)
-    D = grad.shape[-1]
-    call = _Call(stream)
+    N, D, grad_ld = _rows(grad, "grad", device, None, tokens.numel())
     base_ptr, base_ld = 0, D
     if base is not None:
-        _, base_ld = _rows(base, "base", D, vocab)
+        _, _, base_ld = _rows(base, "base", device, D, vocab)
         base_ptr = base.data_ptr()
     if out is None:
-        want = dtype or (base if base is not None else grad).dtype
-        out = call.empty((vocab, D), want)
+        if vocab < 0:
+            _refuse(f"vocab = {vocab} < 0")
+        out = _empty((vocab, D), dtype or (base if base is not None else grad).dtype, stream)
         out_ld = D
     else:
-        _, out_ld = _rows(out, "out", D, vocab)
+        _, _, out_ld = _rows(out, "out", device, D, vocab)
         if dtype is not None and out.dtype != dtype:
             _refuse(f"out is {out.dtype}, {dtype} is asked for", ERR_INVALID_TYPE)
     table_code = _dtype(out, "out")
     if base is not None and base.dtype != out.dtype:
         _refuse(f"base is {base.dtype}, out {out.dtype}", ERR_INVALID_TYPE)
-    ws, ws_bytes, _hold = call.workspace(
-        workspace, vcoll_embedding_backward_workspace_bytes(N, vocab, D))
-    _check(vcoll_embedding_backward(grad.data_ptr(), grad_ld, code, tokens.data_ptr(), index, N,
-                                    vocab, D, scale, base_ptr, base_ld, out.data_ptr(), out_ld,
-                                    table_code, ws, ws_bytes, call.handle))
+    need = _fn("vcoll_embedding_backward_workspace_bytes")(N, vocab, D)
+    ws, ws_bytes, _hold = _workspace(workspace, need, device, stream)
+    rc = _fn("vcoll_embedding_backward")(grad.data_ptr(), grad_ld, code, tokens.data_ptr(), index,
+                                         N, vocab, D, scale, base_ptr, base_ld, out.data_ptr(),
+                                         out_ld, table_code, ws, ws_bytes,
+                                         _handle(stream, device))
+    if rc:
+        _check(rc)
     return out
 
 
-def _weights(weight, bias, D):
+def _weights(weight, bias, D, device):
     """(weight pointer, bias pointer, their type)."""
     w = weight if weight is not None else bias
     if w is None:
         return 0, 0, F32
     code = _dtype(w, "weight")
-    return (_vector(weight, "weight", D) if weight is not None else 0,
-            _vector(bias, "bias", D, w.dtype) if bias is not None else 0, code)
+    return (_vector(weight, "weight", device, D, w.dtype) if weight is not None else 0,
+            _vector(bias, "bias", device, D, w.dtype) if bias is not None else 0, code)
 
 
-def _matrix_out(call, out, like, what, N, D):
+def _matrix_out(out, like, what, N, D, device, stream):
     """(tensor, row stride) of an output shaped and typed as `like`."""
     if out is None:
-        return call.empty(like.shape, like.dtype), D
-    _, ld = _rows(out, what, D, N)
+        return _empty(like.shape, like.dtype, stream), D
+    _, _, ld = _rows(out, what, device, D, N)
     if out.dtype != like.dtype:
         _refuse(f"{what} is {out.dtype}, {like.dtype} is expected", ERR_INVALID_TYPE)
     return out, ld
@@ -303,17 +316,18 @@ def _matrix_out(call, out, like, what, N, D):
 def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
     """Layer norm over the last axis: (y, mean, rstd), y in x's type (in place
     with ``out=x``), mean and rstd fp32 of x's shape without its last axis."""
+    device = torch.cuda.current_device()
     code = _dtype(x, "x")
-    N, x_ld = _rows(x, "x")
-    D = x.shape[-1]
-    w, b, wcode = _weights(weight, bias, D)
-    call = _Call(stream)
-    y, y_ld = _matrix_out(call, out, x, "out", N, D)
-    stats = call.empty((2, *x.shape[:-1]), torch.float32)
-    mean, rstd = stats.unbind(0)
-    at = stats.data_ptr()
-    _check(vcoll_layer_norm(x.data_ptr(), x_ld, w, b, wcode, N, D, eps, y.data_ptr(), y_ld, at,
-                            at + 4 * N, code, call.handle))
+    N, D, x_ld = _rows(x, "x", device)
+    w, b, wcode = _weights(weight, bias, D, device)
+    y, y_ld = _matrix_out(out, x, "out", N, D, device, stream)
+    lead = x.shape[:-1]
+    mean = _empty(lead, torch.float32, stream)
+    rstd = _empty(lead, torch.float32, stream)
+    rc = _fn("vcoll_layer_norm")(x.data_ptr(), x_ld, w, b, wcode, N, D, eps, y.data_ptr(), y_ld,
+                                 mean.data_ptr(), rstd.data_ptr(), code, _handle(stream, device))
+    if rc:
+        _check(rc)
     return y, mean, rstd
 
 
@@ -321,17 +335,22 @@ def layer_norm_workspace_bytes(N, width) -> int:
     return vcoll_layer_norm_workspace_bytes(N, width)
 
 
-def _gradients(call, grad, weight, dx, dweight, dbias, weight_grads, N, D):
+def _gradients(grad, weight, dx, dweight, dbias, weight_grads, N, D, device, stream):
     """Output tensors and pointers of a layer norm's gradient."""
-    w, _, wcode = _weights(weight, None, D)
-    dx, dx_ld = _matrix_out(call, dx, grad, "dx", N, D)
+    w, _, wcode = _weights(weight, None, D, device)
+    dx, dx_ld = _matrix_out(dx, grad, "dx", N, D, device, stream)
     wtype = weight.dtype if weight is not None else torch.float32
-    if dweight is None and weight_grads:
-        dweight = call.empty(D, wtype)
-    if dbias is None and weight_grads:
-        dbias = call.empty(D, wtype)
-    pw = _vector(dweight, "dweight", D, wtype) if dweight is not None else 0
-    pb = _vector(dbias, "dbias", D, wtype) if dbias is not None else 0
+    pw = pb = 0
+    if dweight is not None:
+        pw = _vector(dweight, "dweight", device, D, wtype)
+    elif weight_grads:
+        dweight = _empty(D, wtype, stream)
+        pw = dweight.data_ptr()
+    if dbias is not None:
+        pb = _vector(dbias, "dbias", device, D, wtype)
+    elif weight_grads:
+        dbias = _empty(D, wtype, stream)
+        pb = dbias.data_ptr()
     return w, wcode, dx, dx_ld, dweight, dbias, pw, pb
 
 
@@ -342,21 +361,23 @@ def layer_norm_backward(grad, x, mean, rstd, weight=None, dx=None, dweight=None,
     x (in place); dweight and dbias are of weight's type (fp32 without a
     weight) and may be slices of a fusion buffer; weight_grads=False leaves out
     (returns None for) those that are not given."""
+    device = torch.cuda.current_device()
     code = _dtype(grad, "grad")
-    N, grad_ld = _rows(grad, "grad")
-    D = grad.shape[-1]
-    _, x_ld = _rows(x, "x", D, N)
+    N, D, grad_ld = _rows(grad, "grad", device)
+    _, _, x_ld = _rows(x, "x", device, D, N)
     if x.dtype != grad.dtype:
         _refuse(f"x is {x.dtype}, grad {grad.dtype}", ERR_INVALID_TYPE)
-    pm = _vector(mean, "mean", N, torch.float32)
-    pr = _vector(rstd, "rstd", N, torch.float32)
-    call = _Call(stream)
-    w, wcode, dx, dx_ld, dweight, dbias, pw, pb = _gradients(call, grad, weight, dx, dweight,
-                                                             dbias, weight_grads, N, D)
-    ws, ws_bytes, _hold = call.workspace(workspace, vcoll_layer_norm_workspace_bytes(N, D))
-    _check(vcoll_layer_norm_backward(grad.data_ptr(), grad_ld, x.data_ptr(), x_ld, pm, pr, w,
-                                     wcode, N, D, dx.data_ptr(), dx_ld, pw, pb, code, ws, ws_bytes,
-                                     call.handle))
+    pm = _vector(mean, "mean", device, N, torch.float32)
+    pr = _vector(rstd, "rstd", device, N, torch.float32)
+    w, wcode, dx, dx_ld, dweight, dbias, pw, pb = _gradients(
+        grad, weight, dx, dweight, dbias, weight_grads, N, D, device, stream)
+    need = _fn("vcoll_layer_norm_workspace_bytes")(N, D)
+    ws, ws_bytes, _hold = _workspace(workspace, need, device, stream)
+    rc = _fn("vcoll_layer_norm_backward")(grad.data_ptr(), grad_ld, x.data_ptr(), x_ld, pm, pr, w,
+                                          wcode, N, D, dx.data_ptr(), dx_ld, pw, pb, code, ws,
+                                          ws_bytes, _handle(stream, device))
+    if rc:
+        _check(rc)
     return dx, dweight, dbias
 
 
@@ -373,50 +394,58 @@ class Checkpoint8(NamedTuple):
         return self.codes.numel() + 4 * self.scales.numel()
 
 
-def _kept_empty(call, shape):
-    D = shape[-1]
-    codes = call.empty((*shape[:-1], (D + 15) // 16 * 16), torch.int8)
-    scales = call.empty((*shape[:-1], -(-D // CHECKPOINT8_BLOCK)), torch.float32)
-    return Checkpoint8(codes, scales, shape)
+def _kept_empty(shape, stream):
+    """(codes, their row stride, scales) for an activation of that shape."""
+    lead, D = shape[:-1], shape[-1]
+    ld = (D + 15) // 16 * 16
+    return (_empty((*lead, ld), torch.int8, stream), ld,
+            _empty((*lead, -(-D // CHECKPOINT8_BLOCK)), torch.float32, stream))
 
 
-def _kept(kept, D=None, N=None):
+def _kept(kept, device, D=None, N=None):
     """(rows, columns, codes pointer, their row stride, scales pointer)."""
-    width = kept.shape[-1]
-    rows = kept.shape[:-1].numel()
+    codes, scales, shape = kept
+    width = shape[-1]
+    rows = shape[0] if len(shape) == 2 else shape[:-1].numel()
     if (D is not None and width != D) or (N is not None and rows != N):
-        _refuse(f"the kept activation has the shape {tuple(kept.shape)}")
-    ld = kept.codes.shape[-1]
-    if kept.codes.dtype != torch.int8 or ld < width:
-        _refuse("codes are not int8 rows of the kept activation", ERR_INVALID_TYPE)
-    return (rows, width, _vector(kept.codes, "codes", rows * ld), ld,
-            _vector(kept.scales, "scales", rows * -(-width // CHECKPOINT8_BLOCK), torch.float32))
+        _refuse(f"the kept activation has the shape {tuple(shape)}")
+    ld = codes.shape[-1]
+    if ld < width:
+        _refuse("codes are not rows of the kept activation")
+    return (rows, width, _vector(codes, "codes", device, rows * ld, torch.int8), ld,
+            _vector(scales, "scales", device, rows * -(-width // CHECKPOINT8_BLOCK),
+                    torch.float32))
 
 
 def checkpoint8(x, stream=None) -> Checkpoint8:
     """x kept in 8 bits, with one scale for each 128 columns of a row."""
+    device = torch.cuda.current_device()
     code = _dtype(x, "x")
-    N, x_ld = _rows(x, "x")
-    call = _Call(stream)
-    kept = _kept_empty(call, x.shape)
-    _check(vcoll_checkpoint8(x.data_ptr(), x_ld, N, x.shape[-1], kept.codes.data_ptr(),
-                             kept.codes.shape[-1], kept.scales.data_ptr(), code, call.handle))
-    return kept
+    N, D, x_ld = _rows(x, "x", device)
+    codes, ld, scales = _kept_empty(x.shape, stream)
+    rc = _fn("vcoll_checkpoint8")(x.data_ptr(), x_ld, N, D, codes.data_ptr(), ld,
+                                  scales.data_ptr(), code, _handle(stream, device))
+    if rc:
+        _check(rc)
+    return Checkpoint8(codes, scales, x.shape)
 
 
 def checkpoint8_restore(kept, weight=None, bias=None, dtype=torch.float32, out=None, stream=None):
     """What a Checkpoint8 stands for, times weight plus bias where given (the
     output of the layer norm that kept it).  dtype: of the result, unless out
     is given."""
-    N, D, codes, codes_ld, scales = _kept(kept)
-    w, b, wcode = _weights(weight, bias, D)
-    call = _Call(stream)
+    device = torch.cuda.current_device()
+    N, D, codes, codes_ld, scales = _kept(kept, device)
+    w, b, wcode = _weights(weight, bias, D, device)
     if out is None:
-        out, out_ld = call.empty(kept.shape, dtype), D
+        out, out_ld = _empty(kept.shape, dtype, stream), D
     else:
-        _, out_ld = _rows(out, "out", D, N)
-    _check(vcoll_checkpoint8_restore(codes, codes_ld, scales, w, b, wcode, N, D, out.data_ptr(),
-                                     out_ld, _dtype(out, "out"), call.handle))
+        _, _, out_ld = _rows(out, "out", device, D, N)
+    rc = _fn("vcoll_checkpoint8_restore")(codes, codes_ld, scales, w, b, wcode, N, D,
+                                          out.data_ptr(), out_ld, _dtype(out, "out"),
+                                          _handle(stream, device))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -425,34 +454,37 @@ def layer_norm_checkpoint8(x, weight=None, bias=None, eps=1e-5, out=None, stream
     (y, rstd, kept).  Neither x nor y is needed for the backward pass then:
     ``checkpoint8_restore(kept, weight, bias)`` gives y back, and
     ``layer_norm_backward_checkpoint8`` the gradients."""
+    device = torch.cuda.current_device()
     code = _dtype(x, "x")
-    N, x_ld = _rows(x, "x")
-    D = x.shape[-1]
-    w, b, wcode = _weights(weight, bias, D)
-    call = _Call(stream)
-    y, y_ld = _matrix_out(call, out, x, "out", N, D)
-    rstd = call.empty(x.shape[:-1], torch.float32)
-    kept = _kept_empty(call, x.shape)
-    _check(vcoll_layer_norm_checkpoint8(x.data_ptr(), x_ld, w, b, wcode, N, D, eps, y.data_ptr(),
-                                        y_ld, rstd.data_ptr(), kept.codes.data_ptr(),
-                                        kept.codes.shape[-1], kept.scales.data_ptr(), code,
-                                        call.handle))
-    return y, rstd, kept
+    N, D, x_ld = _rows(x, "x", device)
+    w, b, wcode = _weights(weight, bias, D, device)
+    y, y_ld = _matrix_out(out, x, "out", N, D, device, stream)
+    rstd = _empty(x.shape[:-1], torch.float32, stream)
+    codes, ld, scales = _kept_empty(x.shape, stream)
+    rc = _fn("vcoll_layer_norm_checkpoint8")(x.data_ptr(), x_ld, w, b, wcode, N, D, eps,
+                                             y.data_ptr(), y_ld, rstd.data_ptr(),
+                                             codes.data_ptr(), ld, scales.data_ptr(), code,
+                                             _handle(stream, device))
+    if rc:
+        _check(rc)
+    return y, rstd, Checkpoint8(codes, scales, x.shape)
 
 
 def layer_norm_backward_checkpoint8(grad, kept, rstd, weight=None, dx=None, dweight=None,
                                     dbias=None, weight_grads=True, workspace=None, stream=None):
     """``layer_norm_backward`` from what ``layer_norm_checkpoint8`` kept."""
+    device = torch.cuda.current_device()
     code = _dtype(grad, "grad")
-    N, grad_ld = _rows(grad, "grad")
-    D = grad.shape[-1]
-    _, _, codes, codes_ld, scales = _kept(kept, D, N)
-    pr = _vector(rstd, "rstd", N, torch.float32)
-    call = _Call(stream)
-    w, wcode, dx, dx_ld, dweight, dbias, pw, pb = _gradients(call, grad, weight, dx, dweight,
-                                                             dbias, weight_grads, N, D)
-    ws, ws_bytes, _hold = call.workspace(workspace, vcoll_layer_norm_workspace_bytes(N, D))
-    _check(vcoll_layer_norm_backward_checkpoint8(grad.data_ptr(), grad_ld, codes, codes_ld, scales,
-                                                 pr, w, wcode, N, D, dx.data_ptr(), dx_ld, pw, pb,
-                                                 code, ws, ws_bytes, call.handle))
+    N, D, grad_ld = _rows(grad, "grad", device)
+    _, _, codes, codes_ld, scales = _kept(kept, device, D, N)
+    pr = _vector(rstd, "rstd", device, N, torch.float32)
+    w, wcode, dx, dx_ld, dweight, dbias, pw, pb = _gradients(
+        grad, weight, dx, dweight, dbias, weight_grads, N, D, device, stream)
+    need = _fn("vcoll_layer_norm_workspace_bytes")(N, D)
+    ws, ws_bytes, _hold = _workspace(workspace, need, device, stream)
+    rc = _fn("vcoll_layer_norm_backward_checkpoint8")(
+        grad.data_ptr(), grad_ld, codes, codes_ld, scales, pr, w, wcode, N, D, dx.data_ptr(),
+        dx_ld, pw, pb, code, ws, ws_bytes, _handle(stream, device))
+    if rc:
+        _check(rc)
     return dx, dweight, dbias
