@@ -89,6 +89,12 @@ __device__ __forceinline__ void fill_halves(const EmbedGradParams& p, int64_t v)
   }
 }
 
+__device__ __forceinline__ void fill_row(const EmbedGradParams& p, int64_t row) {
+  if (p.fill_bytes == 16) fill_pieces<16>(p, row);
+  else if (p.fill_bytes == 4) fill_pieces<4>(p, row);
+  else fill_halves(p, row);
+}
+
 __device__ __forceinline__ void fill_rows(const EmbedGradParams& p, int64_t first) {
   const int lane = threadIdx.x & 31;
   const int64_t v = first + lane;
@@ -97,12 +103,7 @@ __device__ __forceinline__ void fill_rows(const EmbedGradParams& p, int64_t firs
     const uint32_t i = p.stamp[v];
     gone = (int64_t)i >= p.N || token_at(p.tokens, p.idx64, i) != v;
   }
-  for (uint32_t m = __ballot_sync(~0u, gone); m; m &= m - 1) {
-    const int64_t row = first + __ffs(m) - 1;
-    if (p.fill_bytes == 16) fill_pieces<16>(p, row);
-    else if (p.fill_bytes == 4) fill_pieces<4>(p, row);
-    else fill_halves(p, row);
-  }
+  for (uint32_t m = __ballot_sync(~0u, gone); m; m &= m - 1) fill_row(p, first + __ffs(m) - 1);
 }
 
 }  // namespace
@@ -340,24 +341,27 @@ struct GradTile {
 
   __device__ __forceinline__ int64_t col(int j) const { return col0 + (j * 32 + lane) * A; }
 
-  // table_grad[v] = base[v] + scale * sum
-  __device__ __forceinline__ void finish(int64_t v, const float (&sum)[E]) const {
+  // base[v] of the lane's columns, zeros where there is no base
+  __device__ __forceinline__ void load_base(int64_t v, Raw<TO, A> (&b)[E / A]) const {
 #pragma unroll
     for (int j = 0; j < E / A; ++j) {
-      const int64_t c = col(j);
-      if (c >= p.D) continue;
+      if (p.base && col(j) < p.D) b[j].load_stream(elem_at<TO>(p.base, v * p.base_ld + col(j)));
+      else b[j].zero();
+    }
+  }
+  // table_grad[v] = base[v] + scale * sum
+  __device__ __forceinline__ void finish(int64_t v, const float (&sum)[E], const Raw<TO, A> (&b)[E / A]) const {
+#pragma unroll
+    for (int j = 0; j < E / A; ++j) {
+      if (col(j) >= p.D) continue;
       float f[A];
-      if (p.base) {
-        Raw<TO, A> b;
-        b.load_stream(elem_at<TO>(p.base, v * p.base_ld + c));
-        b.widen(f);
-      }
+      b[j].widen(f);
 #pragma unroll
       for (int a = 0; a < A; ++a)
         f[a] = p.base ? fmaf(sum[j * A + a], p.scale, f[a]) : __fmul_rn(sum[j * A + a], p.scale);
       Raw<TO, A> o;
       o.narrow(f);
-      o.store_stream(elem_at<TO>(p.out, v * p.out_ld + c));
+      o.store_stream(elem_at<TO>(p.out, v * p.out_ld + col(j)));
     }
   }
 
@@ -382,12 +386,14 @@ struct GradTile {
 
 }  // namespace
 
-template <typename T, typename TO, int A>
+// BASE: there is a base, whose rows are fetched with the rows that end a
+// token's sum; half as many rows are in flight then.
+template <typename T, typename TO, int A, bool BASE>
 __global__ void __launch_bounds__(kRowThreads, A == kLane<T> ? 3 : 4)
     vc_embed_grad(const __grid_constant__ EmbedGradParams p) {
   pdl_enter();
   constexpr int E = kLane<T>;
-  constexpr int U = A == 1 && E == 8 ? 4 : 8;  // rows in flight: 32 registers' worth
+  constexpr int U = BASE || (A == 1 && E == 8) ? 4 : 8;  // rows in flight
   const uint32_t* key = p.key[(p.passes + 1) & 1];
   const uint32_t* pos = p.pos[(p.passes + 1) & 1];
   // the CTAs that fill are spread evenly among those that sum, so that reads
@@ -409,9 +415,10 @@ __global__ void __launch_bounds__(kRowThreads, A == kLane<T> ? 3 : 4)
   // outside the table sort last, so the valid lanes are the first ones
   int64_t at = lo + g.lane;
   uint32_t key_next = at < hi ? key[at] : none, pos_next = at < hi ? pos[at] : 0u;
-  uint32_t cur = __shfl_sync(~0u, key_next, 0);
-  if (cur >= none) return;
-  bool began = lo > 0 && key[lo - 1] == cur;  // the current token began before this chunk
+  const uint32_t first = __shfl_sync(~0u, key_next, 0);
+  if (first >= none) return;
+  bool began = lo > 0 && key[lo - 1] == first;  // the first token began before this chunk
+  const uint32_t after = hi < p.N ? key[hi] : none;  // a token that goes on after it
   float sum[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) sum[e] = 0.0f;
@@ -421,11 +428,15 @@ __global__ void __launch_bounds__(kRowThreads, A == kLane<T> ? 3 : 4)
     key_next = at < hi ? key[at] : none;
     pos_next = at < hi ? pos[at] : 0u;
     const int n = __popc(__ballot_sync(~0u, k < none));
-    const uint32_t prev = __shfl_up_sync(~0u, k, 1);
-    const uint32_t starts = __ballot_sync(~0u, k != (g.lane ? prev : cur));
+    uint32_t next = __shfl_down_sync(~0u, k, 1);
+    const uint32_t next32 = __shfl_sync(~0u, key_next, 0);
+    if (g.lane == 31) next = next32;
+    // places that end a token's sum in this chunk
+    const uint32_t ends = __ballot_sync(~0u, k < none && next != k);
 #pragma unroll 1
     for (int s = 0; s < n; s += U) {
       Raw<T, A> r[U][E / A];
+      Raw<TO, A> b[BASE ? U : 1][E / A];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t row = (int64_t)__shfl_sync(~0u, from, s + u) * p.grad_ld;
@@ -435,16 +446,18 @@ __global__ void __launch_bounds__(kRowThreads, A == kLane<T> ? 3 : 4)
           else r[u][j].zero();
         }
       }
+      if constexpr (BASE) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const uint32_t v = __shfl_sync(~0u, k, s + u);
+          if (ends >> (s + u) & 1) g.load_base(v, b[u]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < E / A; ++j) b[0][j].zero();
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (s + u < n && (starts >> (s + u) & 1)) {
-          if (began) g.put(g.partial(chunk, 0, tile), sum);
-          else g.finish(cur, sum);
-          began = false;
-          cur = __shfl_sync(~0u, k, s + u);
-#pragma unroll
-          for (int e = 0; e < E; ++e) sum[e] = 0.0f;
-        }
 #pragma unroll
         for (int j = 0; j < E / A; ++j) {
           float f[A];
@@ -452,13 +465,19 @@ __global__ void __launch_bounds__(kRowThreads, A == kLane<T> ? 3 : 4)
 #pragma unroll
           for (int a = 0; a < A; ++a) sum[j * A + a] += f[a];
         }
+        if (ends >> (s + u) & 1) {
+          const uint32_t v = __shfl_sync(~0u, k, s + u);
+          if (began) g.put(g.partial(chunk, 0, tile), sum);
+          else if (v == after) g.put(g.partial(chunk, 1, tile), sum);
+          else g.finish(v, sum, b[BASE ? u : 0]);
+          began = false;
+#pragma unroll
+          for (int e = 0; e < E; ++e) sum[e] = 0.0f;
+        }
       }
     }
     if (n < 32) break;
   }
-  if (began) g.put(g.partial(chunk, 0, tile), sum);
-  else if (hi < p.N && key[hi] == cur) g.put(g.partial(chunk, 1, tile), sum);
-  else g.finish(cur, sum);
 }
 
 // A warp per (chunk, tile): if a token begins in the chunk and goes on after
@@ -473,9 +492,13 @@ __global__ void __launch_bounds__(kRowThreads) vc_embed_join(const __grid_consta
   __shared__ float part[NW][32 * E];
   const uint32_t* key = p.key[(p.passes + 1) & 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if ((int64_t)blockIdx.x >= p.sum_ctas) {  // hardly any bandwidth is used here either
+    fill_rows(p, p.fill_begin + (((int64_t)blockIdx.x - p.sum_ctas) * NW + warp) * kFillRows);
+    return;
+  }
   // units a CTA apart: those of one chunk, which a long token makes long, go to
   // different CTAs
-  const int64_t unit = (int64_t)warp * gridDim.x + blockIdx.x;
+  const int64_t unit = (int64_t)warp * p.sum_ctas + blockIdx.x;
   const int64_t chunk = unit / p.tiles, tile = unit % p.tiles;
   const int64_t lo = chunk * p.chunk, hi = lo + p.chunk;
   int64_t last = -1;
@@ -500,7 +523,9 @@ __global__ void __launch_bounds__(kRowThreads) vc_embed_join(const __grid_consta
     for (int e = 0; e < E; ++e) sum[e] = 0.0f;
     g.add(g.partial(chunk, 1, tile), sum);
     for (int64_t c = chunk + 1; c <= last; ++c) g.add(g.partial(c, 0, tile), sum);
-    g.finish(v, sum);
+    Raw<TO, A> b[E / A];
+    g.load_base(v, b);
+    g.finish(v, sum, b);
     last = -1;
   }
   if (lane == 0) last_of[warp] = last;
@@ -508,7 +533,7 @@ __global__ void __launch_bounds__(kRowThreads) vc_embed_join(const __grid_consta
   for (int w = 0; w < NW; ++w) {
     const int64_t end = last_of[w];
     if (end < 0) continue;  // the same for the whole CTA
-    const int64_t u = (int64_t)w * gridDim.x + blockIdx.x, from = u / p.tiles, t = u % p.tiles;
+    const int64_t u = (int64_t)w * p.sum_ctas + blockIdx.x, from = u / p.tiles, t = u % p.tiles;
     const GradTile<T, TO, A> gw{p, lane, t * 32 * E};
     const int64_t per = (end - from + NW - 1) / NW;
     const int64_t a = from + 1 + warp * per, b = a + per < end + 1 ? a + per : end + 1;
@@ -528,10 +553,82 @@ __global__ void __launch_bounds__(kRowThreads) vc_embed_join(const __grid_consta
         for (int k = 1; k < NW; ++k) s += part[k][e * 32 + lane];
         sum[e] = s;
       }
-      gw.finish(key[(from + 1) * p.chunk - 1], sum);
+      const uint32_t token = key[(from + 1) * p.chunk - 1];
+      Raw<TO, A> base[E / A];
+      gw.load_base(token, base);
+      gw.finish(token, sum, base);
     }
     __syncthreads();
   }
+}
+
+// ------------------------------------------------------------- short lists
+// Up to kSmallTokens tokens one launch does all, without a sort.  A warp per
+// (place, tile of columns) reads the list: if an earlier place holds its token
+// it has nothing to do, else it sums the rows of the places that hold it, in
+// order.  CTAs behind these fill the rows of absent tokens, 64 a CTA.
+
+template <typename T, typename TO, int A>
+__global__ void __launch_bounds__(kRowThreads) vc_embed_grad_small(const __grid_constant__ EmbedGradParams p) {
+  pdl_enter();
+  constexpr int E = kLane<T>, U = A == 1 && E == 8 ? 4 : 8;
+  __shared__ int32_t list[kSmallTokens];  // -1: outside the table
+  __shared__ uint32_t met[2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = (int)p.N;
+  const bool fills = (int64_t)blockIdx.x >= p.sum_ctas;
+  const int64_t first = ((int64_t)blockIdx.x - p.sum_ctas) * 64;
+  if (threadIdx.x < 2) met[threadIdx.x] = 0u;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kRowThreads) {
+    const int64_t t = token_at(p.tokens, p.idx64, i);
+    list[i] = t >= 0 && t < p.V ? (int32_t)t : -1;
+    if (fills && t >= first && t < first + 64) atomicOr(&met[(t - first) >> 5], 1u << ((t - first) & 31));
+  }
+  __syncthreads();
+  if (fills) {
+    for (int r = warp; r < 64 && first + r < p.V; r += kRowThreads / 32)
+      if (!(met[r >> 5] >> (r & 31) & 1)) fill_row(p, first + r);
+    return;
+  }
+  const int64_t unit = (int64_t)blockIdx.x * (kRowThreads / 32) + warp;
+  const int64_t place = unit / p.tiles;
+  if (place >= n) return;
+  const int32_t v = list[place];
+  if (v < 0) return;
+  for (int i = 0; i < place; i += 32)
+    if (__ballot_sync(~0u, i + lane < place && list[i + lane] == v)) return;
+  const GradTile<T, TO, A> g{p, lane, unit % p.tiles * 32 * E};
+  float sum[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) sum[e] = 0.0f;
+  Raw<TO, A> base[E / A];
+  g.load_base(v, base);
+  for (int i = (int)place & ~31; i < n; i += 32) {
+    uint32_t same = __ballot_sync(~0u, i + lane < n && list[i + lane] == v);
+    while (same) {
+      Raw<T, A> r[U][E / A];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t row = (int64_t)(i + __ffs(same) - 1) * p.grad_ld;
+#pragma unroll
+        for (int j = 0; j < E / A; ++j) {
+          if (same && g.col(j) < p.D) r[u][j].load_stream(elem_at<T>(p.grad, row + g.col(j)));
+          else r[u][j].zero();
+        }
+        same &= same - 1;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < E / A; ++j) {
+          float f[A];
+          r[u][j].widen(f);
+#pragma unroll
+          for (int a = 0; a < A; ++a) sum[j * A + a] += f[a];
+        }
+    }
+  }
+  g.finish(v, sum, base);
 }
 
 namespace {
@@ -550,22 +647,30 @@ const void* embed_count_kernel() { return (const void*)&vc_embed_count; }
 const void* embed_scatter_kernel() { return (const void*)&vc_embed_scatter; }
 
 namespace {
+template <typename T, typename TO, int A>
+const void* grad_kernel(GradPart part) {
+  switch (part) {
+    case GRAD_SMALL: return (const void*)&vc_embed_grad_small<T, TO, A>;
+    case GRAD_SUM: return (const void*)&vc_embed_grad<T, TO, A, false>;
+    case GRAD_SUM_BASE: return (const void*)&vc_embed_grad<T, TO, A, true>;
+    default: return (const void*)&vc_embed_join<T, TO, A>;
+  }
+}
 template <typename T, typename TO>
-const void* grad_kernel(int access, int join) {
-  constexpr int E = kLane<T>;
-  if (access == E) return join ? (const void*)&vc_embed_join<T, TO, E> : (const void*)&vc_embed_grad<T, TO, E>;
-  if (access == 2) return join ? (const void*)&vc_embed_join<T, TO, 2> : (const void*)&vc_embed_grad<T, TO, 2>;
-  return join ? (const void*)&vc_embed_join<T, TO, 1> : (const void*)&vc_embed_grad<T, TO, 1>;
+const void* grad_kernel(int access, GradPart part) {
+  return access == kLane<T> ? grad_kernel<T, TO, kLane<T>>(part)
+         : access == 2      ? grad_kernel<T, TO, 2>(part)
+                            : grad_kernel<T, TO, 1>(part);
 }
 }  // namespace
 
-const void* embed_grad_kernel(int dtype, int table_dtype, int access, int join) {
+const void* embed_grad_kernel(int dtype, int table_dtype, int access, GradPart part) {
   using B = __nv_bfloat16;
   if (dtype == VCOLL_F32)
-    return table_dtype == VCOLL_F32 ? grad_kernel<float, float>(access, join)
-                                    : grad_kernel<float, B>(access, join);
-  return table_dtype == VCOLL_F32 ? grad_kernel<B, float>(access, join)
-                                  : grad_kernel<B, B>(access, join);
+    return table_dtype == VCOLL_F32 ? grad_kernel<float, float>(access, part)
+                                    : grad_kernel<float, B>(access, part);
+  return table_dtype == VCOLL_F32 ? grad_kernel<B, float>(access, part)
+                                  : grad_kernel<B, B>(access, part);
 }
 
 }  // namespace vcoll

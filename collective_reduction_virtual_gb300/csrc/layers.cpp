@@ -243,7 +243,8 @@ int vcoll_embedding(const void* tokens, int index_type, int64_t N, const void* t
 }
 
 size_t vcoll_embedding_backward_workspace_bytes(int64_t N, int64_t V, int64_t D) {
-  if (N <= 0 || V <= 0 || D <= 0 || N > kMaxExtent || V > kMaxExtent || D > kMaxExtent) return 0;
+  if (N <= kSmallTokens || V <= 0 || D <= 0 || N > kMaxExtent || V > kMaxExtent || D > kMaxExtent)
+    return 0;
   return grad_layout(N, V, D).bytes;
 }
 
@@ -290,55 +291,65 @@ int vcoll_embedding_backward(const void* grad, int64_t grad_ld, int dtype, const
   // the fill copies bytes: rows of base and table_grad in pieces of 16, 4 or 2
   p.fill_bytes = std::min(access_of(ops[2], 16 / ts), access_of(ops[3], 16 / ts)) * ts;
   if (p.fill_bytes == 8) p.fill_bytes = 4;
-  p.fill_end = in_place ? V : 0;  // rows filled so far: none is, or all stay as they are
-  if (N) {
-    const GradLayout L = grad_layout(N, V, D);
-    char* ws = (char*)workspace;
-    for (int k = 0; k < 2; ++k) {
-      p.key[k] = (uint32_t*)(ws + (size_t)(2 * k) * L.list);
-      p.pos[k] = (uint32_t*)(ws + (size_t)(2 * k + 1) * L.list);
-    }
-    p.cnt = (uint32_t*)(ws + L.cnt);
-    p.stamp = (uint32_t*)(ws + L.stamp);
-    p.part = (float*)(ws + L.part);
-    p.passes = L.passes;
-    p.bits = L.bits;
-    p.sort_tile = L.sort_tile;
-    p.chunk = L.chunk;
-    const size_t smem = ((size_t)1 << kSortMaxBits) * (kSortThreads / 32) * sizeof(uint32_t);
-    if (N <= kSortOneCta) {
-      VCOLL_TRY(launch_grid(embed_sort_kernel(), 1, 1, kSortThreads, smem, &p, stream));
-    } else {
-      p.sort_tiles = (int)ceil_div(N, L.sort_tile);
-      VCOLL_TRY(launch_grid(embed_count_kernel(), p.sort_tiles, 1, kSortThreads, smem, &p, stream));
-      constexpr int64_t kCtaRows = kSortThreads / 32 * kFillRows;
-      const int64_t fill = ceil_div(std::max<int64_t>(1, kFillPassBytes / (D * ts)), kCtaRows);
-      for (p.pass = 0; p.pass < p.passes; ++p.pass) {
-        p.fill_begin = p.fill_end;
-        p.fill_end = std::min(V, p.fill_begin + fill * kCtaRows);
-        VCOLL_TRY(launch_grid(embed_scatter_kernel(),
-                              p.sort_tiles + ceil_div(p.fill_end - p.fill_begin, kCtaRows), 1,
-                              kSortThreads, smem, &p, stream));
-      }
-    }
-  }
   const int E = 16 / es;
   int access = E;
   for (const Operand* o = ops + 1; o < ops + 4; ++o) access = std::min(access, access_of(*o, E));
   p.tiles = ceil_div(D, 32 * E);
-  p.sum_ctas = N ? ceil_div(ceil_div(N, p.chunk) * p.tiles, kWarps) : 0;
-  p.fill_begin = p.fill_end;
-  p.fill_end = V;
-  const int64_t grid = p.sum_ctas + ceil_div(V - p.fill_begin, kWarps * kFillRows);
-  if (grid > 0x7FFFFFFF)
+  auto kernel = [&](GradPart part) { return embed_grad_kernel(dtype, table_dtype, access, part); };
+  if (N <= kSmallTokens) {
+    p.sum_ctas = ceil_div(N * p.tiles, kWarps);
+    return launch_grid(kernel(GRAD_SMALL), p.sum_ctas + (in_place ? 0 : ceil_div(V, 64)), 1,
+                       kRowThreads, 0, &p, stream);
+  }
+  const GradLayout L = grad_layout(N, V, D);
+  char* ws = (char*)workspace;
+  for (int k = 0; k < 2; ++k) {
+    p.key[k] = (uint32_t*)(ws + (size_t)(2 * k) * L.list);
+    p.pos[k] = (uint32_t*)(ws + (size_t)(2 * k + 1) * L.list);
+  }
+  p.cnt = (uint32_t*)(ws + L.cnt);
+  p.stamp = (uint32_t*)(ws + L.stamp);
+  p.part = (float*)(ws + L.part);
+  p.passes = L.passes;
+  p.bits = L.bits;
+  p.sort_tile = L.sort_tile;
+  p.chunk = L.chunk;
+  p.sum_ctas = ceil_div(ceil_div(N, p.chunk) * p.tiles, kWarps);
+  if (p.sum_ctas + ceil_div(V, kWarps * kFillRows) > 0x7FFFFFFF)
     return fail(VCOLL_ERR_UNSUPPORTED, "%lld rows of %lld columns are too many", (long long)N,
                 (long long)D);
-  if (grid)
-    VCOLL_TRY(launch_grid(embed_grad_kernel(dtype, table_dtype, access, 0), grid, 1, kRowThreads, 0,
-                          &p, stream));
-  if (N <= p.chunk) return VCOLL_OK;  // no token reaches a second chunk
-  return launch_grid(embed_grad_kernel(dtype, table_dtype, access, 1), p.sum_ctas, 1, kRowThreads,
-                     0, &p, stream);
+  // Rows of absent tokens are filled beside the sort's passes, kFillPassBytes
+  // each, and beside the join, half as many; the others beside the sums.  In
+  // place all of them stay.
+  const bool join = N > p.chunk;  // a token may reach a second chunk
+  const int64_t share = std::max<int64_t>(1, kFillPassBytes / (D * ts));
+  const int64_t early = N <= kSortOneCta ? 0 : std::min(V, p.passes * share);
+  const int64_t last = in_place || !join ? V : V - std::min(V - early, share / 2);  // the join's first
+  p.fill_end = in_place ? V : 0;  // rows filled so far
+  // the next `count` rows, and CTAs of `warps` warps for them
+  auto take = [&](int64_t count, int64_t end, int64_t warps) {
+    p.fill_begin = p.fill_end;
+    p.fill_end = std::min(end, p.fill_begin + count);
+    return ceil_div(p.fill_end - p.fill_begin, warps * kFillRows);
+  };
+  const size_t smem = ((size_t)1 << kSortMaxBits) * (kSortThreads / 32) * sizeof(uint32_t);
+  if (N <= kSortOneCta) {
+    VCOLL_TRY(launch_grid(embed_sort_kernel(), 1, 1, kSortThreads, smem, &p, stream));
+  } else {
+    p.sort_tiles = (int)ceil_div(N, L.sort_tile);
+    VCOLL_TRY(launch_grid(embed_count_kernel(), p.sort_tiles, 1, kSortThreads, smem, &p, stream));
+    for (p.pass = 0; p.pass < p.passes; ++p.pass) {
+      const int64_t fill = take(share, last, kSortThreads / 32);
+      VCOLL_TRY(launch_grid(embed_scatter_kernel(), p.sort_tiles + fill, 1, kSortThreads, smem, &p,
+                            stream));
+    }
+  }
+  const int64_t fill = take(V, last, kWarps);
+  VCOLL_TRY(launch_grid(kernel(base ? GRAD_SUM_BASE : GRAD_SUM), p.sum_ctas + fill, 1, kRowThreads,
+                        0, &p, stream));
+  if (!join) return VCOLL_OK;
+  const int64_t rest = take(V, V, kWarps);
+  return launch_grid(kernel(GRAD_JOIN), p.sum_ctas + rest, 1, kRowThreads, 0, &p, stream);
 }
 
 // x, y (or grad, dx) and the 8-bit operands of the layer norm entry points

@@ -32,6 +32,7 @@ constexpr int kSortMaxPasses = 4;
 constexpr int64_t kSortMinTile = 2048;  // keys of a CTA where several sort
 constexpr int kSortMaxTiles = 128;
 constexpr int64_t kFillRows = 2;  // adjacent rows that a warp fills
+constexpr int kSmallTokens = 512;  // up to which the list is not sorted
 constexpr int64_t kJoinAlone = 16;  // partial rows that one warp adds up alone
 struct EmbedGradParams {
   const void* tokens;
@@ -116,7 +117,8 @@ const void* embed_kernel(int dtype, int access);
 const void* embed_sort_kernel();
 const void* embed_count_kernel();
 const void* embed_scatter_kernel();
-const void* embed_grad_kernel(int dtype, int table_dtype, int access, int join);
+enum GradPart { GRAD_SMALL, GRAD_SUM, GRAD_SUM_BASE, GRAD_JOIN };
+const void* embed_grad_kernel(int dtype, int table_dtype, int access, GradPart part);
 const void* norm_rows_kernel_f32(int access, int chunks, int threads, bool grad, bool kept);
 const void* norm_rows_kernel_bf16(int access, int chunks, int threads, bool grad, bool kept);
 const void* norm_wsum_kernel();

@@ -113,6 +113,9 @@ def test_embedding_shapes_extreme_tokens_and_an_empty_table(v):
     (700, 30, 515, "one", "dense"), (300, 20, 64, "none", "dense"), (0, 9, 64, "any", "dense"),
     (9000, 70000, 16, "skewed", "dense"), (20000, 17, 8, "skewed", "dense"),
     (513, 600000, 2, "any", "dense"), (200, 50, 2500, "skewed", "slice"),
+    (512, 300, 72, "one", "odd"), (512, 2000, 258, "skewed", "dense"), (513, 2000, 258, "one", "dense"),
+    (4096, 9000, 24, "skewed", "dense"), (4097, 65, 24, "any", "slice"), (6000, 3, 1000, "any", "dense"),
+    (5000, 40, 129, "none", "dense"), (70000, 513, 16, "skewed", "dense"),
 ])
 def test_embedding_backward(v, dtype, table_dtype, n, V, d, kind, layout):
     g = gen(n + V + d)
@@ -513,7 +516,8 @@ def test_tensor_layer_refusals(v):
         lambda: v.embedding_backward(x, t[:4], 10), lambda: v.embedding_backward(x, t, 10, out=x),
         lambda: v.embedding_backward(x, t, 10, base=torch.zeros(9, 64, device="cuda")),
         lambda: v.embedding_backward(x, t, 10, base=torch.zeros(10, 64, device="cuda"), dtype=torch.bfloat16),
-        lambda: v.embedding_backward(x, t, 10, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
+        lambda: v.embedding_backward(x.repeat(500, 1), t.repeat(500), 10,
+                                     workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
         lambda: v.embedding_backward(x, t, -1),
     ]
     for i, f in enumerate(bad):
@@ -549,9 +553,10 @@ def test_embedding_refusals(v):
 
 def test_embedding_backward_refusals(v):
     f = v.vcoll_embedding_backward
-    need = v.vcoll_embedding_backward_workspace_bytes(4, 10, 64)
+    assert v.vcoll_embedding_backward_workspace_bytes(4, 10, 64) == 0  # short lists take none
+    need = v.vcoll_embedding_backward_workspace_bytes(4000, 10, 64)
     assert need > 0
-    ok = [A, 64, v.F32, B, v.I64, 4, 10, 64, 1.0, 0, 64, C, 64, v.F32, D_, need]
+    ok = [A, 64, v.F32, B, v.I64, 4000, 10, 64, 1.0, 0, 64, C, 64, v.F32, D_, need]
     for at, value, want in [(2, 2, v.ERR_INVALID_TYPE), (13, 5, v.ERR_INVALID_TYPE),
                             (4, 2, v.ERR_INVALID_TYPE), (5, -1, v.ERR_INVALID_ARG),
                             (6, -1, v.ERR_INVALID_ARG), (7, 1 << 31, v.ERR_UNSUPPORTED),
