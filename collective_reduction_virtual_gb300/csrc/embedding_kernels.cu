@@ -566,53 +566,29 @@ __global__ void __launch_bounds__(kRowThreads) vc_embed_join(const __grid_consta
 // Up to kSmallTokens tokens one launch does all, without a sort.  A warp per
 // (place, tile of columns) reads the list: if an earlier place holds its token
 // it has nothing to do, else it sums the rows of the places that hold it, in
-// order.  CTAs behind these fill the rows of absent tokens, 64 a CTA.
+// order.  Tokens of more than kSmallAlone places are summed by all warps of the
+// CTA, an eighth of the list each, and joined in order.  CTAs behind these fill
+// the rows of absent tokens, a row a warp.
 
+namespace {
+
+// Adds up the rows of the places lo .. hi - 1 (lo a multiple of 32) that hold v.
 template <typename T, typename TO, int A>
-__global__ void __launch_bounds__(kRowThreads) vc_embed_grad_small(const __grid_constant__ EmbedGradParams p) {
-  pdl_enter();
+__device__ __forceinline__ void sum_places(const GradTile<T, TO, A>& g, const int32_t* list, int lo, int hi,
+                                           int32_t v, float (&sum)[kLane<T>]) {
   constexpr int E = kLane<T>, U = A == 1 && E == 8 ? 4 : 8;
-  __shared__ int32_t list[kSmallTokens];  // -1: outside the table
-  __shared__ uint32_t met[2];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = (int)p.N;
-  const bool fills = (int64_t)blockIdx.x >= p.sum_ctas;
-  const int64_t first = ((int64_t)blockIdx.x - p.sum_ctas) * 64;
-  if (threadIdx.x < 2) met[threadIdx.x] = 0u;
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kRowThreads) {
-    const int64_t t = token_at(p.tokens, p.idx64, i);
-    list[i] = t >= 0 && t < p.V ? (int32_t)t : -1;
-    if (fills && t >= first && t < first + 64) atomicOr(&met[(t - first) >> 5], 1u << ((t - first) & 31));
-  }
-  __syncthreads();
-  if (fills) {
-    for (int r = warp; r < 64 && first + r < p.V; r += kRowThreads / 32)
-      if (!(met[r >> 5] >> (r & 31) & 1)) fill_row(p, first + r);
-    return;
-  }
-  const int64_t unit = (int64_t)blockIdx.x * (kRowThreads / 32) + warp;
-  const int64_t place = unit / p.tiles;
-  if (place >= n) return;
-  const int32_t v = list[place];
-  if (v < 0) return;
-  for (int i = 0; i < place; i += 32)
-    if (__ballot_sync(~0u, i + lane < place && list[i + lane] == v)) return;
-  const GradTile<T, TO, A> g{p, lane, unit % p.tiles * 32 * E};
-  float sum[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) sum[e] = 0.0f;
-  Raw<TO, A> base[E / A];
-  g.load_base(v, base);
-  for (int i = (int)place & ~31; i < n; i += 32) {
-    uint32_t same = __ballot_sync(~0u, i + lane < n && list[i + lane] == v);
+  for (int i = lo; i < hi; i += 32) {
+    uint32_t same = __ballot_sync(~0u, i + g.lane < hi && list[i + g.lane] == v);
     while (same) {
       Raw<T, A> r[U][E / A];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t row = (int64_t)(i + __ffs(same) - 1) * p.grad_ld;
+        const int64_t row = (int64_t)(i + __ffs(same) - 1) * g.p.grad_ld;
 #pragma unroll
         for (int j = 0; j < E / A; ++j) {
-          if (same && g.col(j) < p.D) r[u][j].load_stream(elem_at<T>(p.grad, row + g.col(j)));
+          if (same && g.col(j) < g.p.D) r[u][j].load_stream(elem_at<T>(g.p.grad, row + g.col(j)));
           else r[u][j].zero();
         }
         same &= same - 1;
@@ -628,7 +604,76 @@ __global__ void __launch_bounds__(kRowThreads) vc_embed_grad_small(const __grid_
         }
     }
   }
-  g.finish(v, sum, base);
+}
+
+}  // namespace
+
+template <typename T, typename TO, int A>
+__global__ void __launch_bounds__(kRowThreads) vc_embed_grad_small(const __grid_constant__ EmbedGradParams p) {
+  pdl_enter();
+  constexpr int E = kLane<T>, NW = kRowThreads / 32;
+  __shared__ int32_t list[kSmallTokens];  // -1: outside the table
+  __shared__ uint32_t met;  // of the CTA's rows, those whose tokens occur
+  __shared__ int32_t shared_token[NW];  // -1: nothing left for the CTA to do
+  __shared__ float part[NW][32 * E];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = (int)p.N;
+  const bool fills = (int64_t)blockIdx.x >= p.sum_ctas;
+  const int64_t first = ((int64_t)blockIdx.x - p.sum_ctas) * NW;
+  if (threadIdx.x == 0) met = 0u;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kRowThreads) {
+    const int64_t t = token_at(p.tokens, p.idx64, i);
+    list[i] = t >= 0 && t < p.V ? (int32_t)t : -1;
+    if (fills && t >= first && t < first + NW) atomicOr(&met, 1u << (t - first));
+  }
+  __syncthreads();
+  if (fills) {
+    if (first + warp < p.V && !(met >> warp & 1)) fill_row(p, first + warp);
+    return;
+  }
+  // units a CTA apart: the tiles of a frequent token's place go to different
+  // CTAs (512 places of one token, 4096 bf16 columns: 10 us; 56 us when a CTA
+  // has eight of its tiles to add up in turn)
+  auto unit_of = [&](int w) { return (int64_t)w * p.sum_ctas + blockIdx.x; };
+  auto tile_of = [&](int w) { return GradTile<T, TO, A>{p, lane, unit_of(w) % p.tiles * 32 * E}; };
+  const int64_t place = unit_of(warp) / p.tiles;
+  int32_t v = place < n ? list[place] : -1;
+  for (int i = 0; i < place && v >= 0; i += 32)
+    if (__ballot_sync(~0u, i + lane < place && list[i + lane] == v)) v = -1;  // an earlier place holds it
+  int count = 0;
+  if (v >= 0)
+    for (int i = (int)place & ~31; i < n; i += 32)
+      count += __popc(__ballot_sync(~0u, i + lane < n && list[i + lane] == v));
+  float sum[E];
+  if (v >= 0 && count <= kSmallAlone) {
+    const GradTile<T, TO, A> g = tile_of(warp);
+    Raw<TO, A> base[E / A];
+    g.load_base(v, base);
+    sum_places(g, list, (int)place & ~31, n, v, sum);
+    g.finish(v, sum, base);
+    v = -1;
+  }
+  if (lane == 0) shared_token[warp] = v;
+  __syncthreads();
+  for (int w = 0; w < NW; ++w) {
+    v = shared_token[w];
+    if (v < 0) continue;  // the same for the whole CTA
+    const GradTile<T, TO, A> g = tile_of(w);
+    const int per = ((n + NW - 1) / NW + 31) & ~31;
+    sum_places(g, list, warp * per, min(n, (warp + 1) * per), v, sum);
+#pragma unroll
+    for (int e = 0; e < E; ++e) part[warp][e * 32 + lane] = sum[e];
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        for (int k = 1; k < NW; ++k) sum[e] += part[k][e * 32 + lane];
+      Raw<TO, A> base[E / A];
+      g.load_base(v, base);
+      g.finish(v, sum, base);
+    }
+    __syncthreads();
+  }
 }
 
 namespace {

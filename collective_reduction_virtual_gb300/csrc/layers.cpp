@@ -298,7 +298,7 @@ int vcoll_embedding_backward(const void* grad, int64_t grad_ld, int dtype, const
   auto kernel = [&](GradPart part) { return embed_grad_kernel(dtype, table_dtype, access, part); };
   if (N <= kSmallTokens) {
     p.sum_ctas = ceil_div(N * p.tiles, kWarps);
-    return launch_grid(kernel(GRAD_SMALL), p.sum_ctas + (in_place ? 0 : ceil_div(V, 64)), 1,
+    return launch_grid(kernel(GRAD_SMALL), p.sum_ctas + (in_place ? 0 : ceil_div(V, kWarps)), 1,
                        kRowThreads, 0, &p, stream);
   }
   const GradLayout L = grad_layout(N, V, D);

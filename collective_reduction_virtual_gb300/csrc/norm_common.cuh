@@ -181,11 +181,13 @@ __device__ __forceinline__ uint32_t magnitude_bits(float x) { return __float_as_
 __device__ __forceinline__ uint32_t code_bits(float x, float unit) {
   return __float_as_uint(__fadd_rn(__fmul_rn(x, unit), 12582912.0f));
 }
-// code k of a word as fp32: the byte plus 128 as the end of 2^23's bits, less
-// 2^23 + 128; both steps exact.
-__device__ __forceinline__ float code_value(uint32_t word, int k) {
+// Codes k and k + 1 of a word times a scale: a byte plus 128 as the end of
+// 2^23's bits, less 2^23 + 128 (both steps exact), times the scale.
+__device__ __forceinline__ void code_values(uint32_t word, int k, float scale, float& x, float& y) {
   const uint32_t up = word ^ 0x80808080u;
-  return __uint_as_float(__byte_perm(up, 0x4B000000u, 0x7540 | k)) - 8388736.0f;
+  add2(x, y, __uint_as_float(__byte_perm(up, 0x4B000000u, 0x7540 | k)),
+       __uint_as_float(__byte_perm(up, 0x4B000000u, 0x7540 | (k + 1))), -8388736.0f, -8388736.0f);
+  mul2(x, y, x, y, scale, scale);
 }
 
 // The four codes of 4 values.

@@ -243,10 +243,8 @@ __global__ void __launch_bounds__(kRowThreads) vc_unpack8(const __grid_constant_
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float s = scale[r][A == E ? 0 : e / 4];
-          mul2(f[r][e], f[r][e + 1], code_value(word[r][e / 4], e % 4), code_value(word[r][e / 4], e % 4 + 1), s, s);
-        }
+        for (int e = 0; e < E; e += 2)
+          code_values(word[r][e / 4], e % 4, scale[r][A == E ? 0 : e / 4], f[r][e], f[r][e + 1]);
       P::template affine<FULL>(p.weight, p.bias, p.wbf16, c, D, f);
       P::template store<FULL>(out, c, D, f);
     };

@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
 #pragma unroll
           for (int e = 0; e < E; e += 2) {
             const float sc = scale[r][SC == 2 && e >= 4 ? 1 : 0];
-            mul2(h[r][e], h[r][e + 1], code_value(word[e / 4], e % 4), code_value(word[e / 4], e % 4 + 1), sc, sc);
+            code_values(word[e / 4], e % 4, sc, h[r][e], h[r][e + 1]);
           }
         } else {
           Elem<T>::widen(*reinterpret_cast<const uint4*>(xslot + at + r * threads * 16), h[r]);

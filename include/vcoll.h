@@ -347,8 +347,8 @@ int vcoll_sparse_allreduce_noalloc(const void* const* in, void* const* out, void
  *    wider rows (equal row strides in bytes) do not overlap.
  *  - Sums, means and statistics are fp32; a bf16 output is rounded once (a
  *    computed NaN is the canonical one of the conversion).
- *    The order of every sum is fixed by the sizes and the GPU alone, so a
- *    call repeated on the same inputs gives the same bits.
+ *    The order of every sum is fixed by the sizes, the tokens and the GPU, so
+ *    a call repeated on the same inputs gives the same bits.
  *  - `workspace`: device memory of the size the *_workspace_bytes function
  *    gives, 256-byte aligned, contents neither expected nor kept; calls that
  *    share one must not overlap.
@@ -376,8 +376,8 @@ int vcoll_embedding(const void* tokens, int index_type, int64_t N, const void* t
  * table_dtype) may be NULL (zeros), or table_grad itself with the same row
  * stride: then only the rows of tokens that occur are read and written.
  * Tokens outside [0, V) contribute nothing.  grad: N x D of dtype.  The tokens
- * are sorted (stably), so each row is summed in the order of i, cut into
- * parts at places that depend on the sizes alone.
+ * are brought into order (stably), so each row is summed in the order of i,
+ * cut into parts at places that the tokens and the sizes determine.
  */
 size_t vcoll_embedding_backward_workspace_bytes(int64_t N, int64_t V, int64_t D);
 int vcoll_embedding_backward(const void* grad, int64_t grad_ld, int dtype, const void* tokens,
