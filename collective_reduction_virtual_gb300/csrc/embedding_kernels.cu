@@ -5,39 +5,35 @@
 
 namespace vcoll {
 
-// A row is taken by p.row_warps adjacent warps of a CTA (a power of two), each
-// with kLookup accesses of 16 bytes per lane in flight at a time: the table's
-// rows arrive in pieces of 2 KB.
+// A warp takes kLookup accesses of 16 bytes per lane of a row, all in flight:
+// the table's rows arrive in pieces of 2 KB.
 template <typename T, int A>
 __global__ void __launch_bounds__(kRowThreads) vc_embed(const __grid_constant__ EmbedParams p) {
   pdl_enter();
   constexpr int E = kLane<T>, G = E / A * kLookup;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t i = (int64_t)blockIdx.x * ((kRowThreads / 32) >> p.row_shift) + (warp >> p.row_shift);
-  if (i >= p.N) return;
-  const int64_t t = token_at(p.tokens, p.idx64, i);
+  const RowPiece piece((int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5), p.pieces);
+  if (piece.row >= p.N) return;
+  const int64_t t = token_at(p.tokens, p.idx64, piece.row);
   const bool inside = t >= 0 && t < p.V;
-  const char* from = elem_at<T>(p.table, inside ? t * p.table_ld : 0);
-  char* to = elem_at<T>(p.out, i * p.out_ld);
-  const int64_t step = (int64_t)(kLookup * 32 * E) << p.row_shift;
-  for (int64_t c0 = (warp & ((1 << p.row_shift) - 1)) * (kLookup * 32 * E) + lane * A; c0 < p.D; c0 += step) {
-    Raw<T, A> r[G];
+  const int64_t c0 = piece.piece * (kLookup * 32 * E) + (threadIdx.x & 31) * A;
+  const char* from = elem_at<T>(p.table, (inside ? t * p.table_ld : 0) + c0);
+  char* to = elem_at<T>(p.out, piece.row * p.out_ld + c0);
+  Raw<T, A> r[G];
 #pragma unroll
-    for (int j = 0; j < G; ++j) {
-      if (inside && c0 + j * 32 * A < p.D) r[j].load(elem_at<T>(from, c0 + j * 32 * A));
-      else r[j].zero();
-    }
+  for (int j = 0; j < G; ++j) {
+    if (inside && c0 + j * 32 * A < p.D) r[j].load(elem_at<T>(from, j * 32 * A));
+    else r[j].zero();
+  }
 #pragma unroll
-    for (int j = 0; j < G; ++j) {
-      if (c0 + j * 32 * A >= p.D) break;
-      float f[A];
-      r[j].widen(f);
+  for (int j = 0; j < G; ++j) {
+    if (c0 + j * 32 * A >= p.D) break;
+    float f[A];
+    r[j].widen(f);
 #pragma unroll
-      for (int a = 0; a < A; ++a) f[a] = __fmul_rn(f[a], p.scale);
-      Raw<T, A> o;
-      o.narrow(f);
-      o.store_stream(elem_at<T>(to, c0 + j * 32 * A));
-    }
+    for (int a = 0; a < A; ++a) f[a] = __fmul_rn(f[a], p.scale);
+    Raw<T, A> o;
+    o.narrow(f);
+    o.store_stream(elem_at<T>(to, j * 32 * A));
   }
 }
 

@@ -121,6 +121,15 @@ int grid_for(int64_t items, int64_t per, int waves, int64_t* grid) {
 
 constexpr int kWarps = kRowThreads / 32;
 
+// A warp for each piece of each of N rows.
+int launch_pieces(const void* fn, int64_t N, int64_t pieces, void* params, void* stream) {
+  const int64_t grid = ceil_div(N, kWarps) > 0x7FFFFFFF / pieces ? 0 : ceil_div(N * pieces, kWarps);
+  if (!grid || grid > 0x7FFFFFFF)
+    return fail(VCOLL_ERR_UNSUPPORTED, "%lld rows of %lld pieces are too many", (long long)N,
+                (long long)pieces);
+  return launch_grid(fn, grid, 1, kRowThreads, 0, params, stream);
+}
+
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // The widest access, of `most`, 2 or 1 elements, that every row of an operand
@@ -236,10 +245,8 @@ int vcoll_embedding(const void* tokens, int index_type, int64_t N, const void* t
   p.scale = scale;
   p.idx64 = index_type == VCOLL_I64;
   const int E = 16 / es, access = std::min(access_of(ops[1], E), access_of(ops[2], E));
-  while ((1 << p.row_shift) < kWarps && ((int64_t)(kLookup * 32 * E) << p.row_shift) < D)
-    ++p.row_shift;
-  return launch_grid(embed_kernel(dtype, access), ceil_div(N, kWarps >> p.row_shift), 1,
-                     kRowThreads, 0, &p, stream);
+  p.pieces = ceil_div(D, kLookup * 32 * E);
+  return launch_pieces(embed_kernel(dtype, access), N, p.pieces, &p, stream);
 }
 
 size_t vcoll_embedding_backward_workspace_bytes(int64_t N, int64_t V, int64_t D) {
@@ -539,12 +546,6 @@ int vcoll_layer_norm_backward_checkpoint8(const void* grad, int64_t grad_ld, con
                        workspace_bytes, stream);
 }
 
-static int launch_pack(const void* fn, int E, PackParams* p, void* stream) {
-  while ((1 << p->row_shift) < kWarps && ((int64_t)(kPackChunks * 32 * E) << p->row_shift) < p->D)
-    ++p->row_shift;
-  return launch_grid(fn, ceil_div(p->N, kWarps >> p->row_shift), 1, kRowThreads, 0, p, stream);
-}
-
 int vcoll_checkpoint8(const void* x, int64_t x_ld, int64_t N, int64_t D, int8_t* codes,
                       int64_t codes_ld, float* scales, int dtype, void* stream) {
   VCOLL_TRY(norm_checks(N, D, dtype, VCOLL_F32));
@@ -564,7 +565,9 @@ int vcoll_checkpoint8(const void* x, int64_t x_ld, int64_t N, int64_t D, int8_t*
   p.D = D;
   p.x_ld = x_ld;
   p.codes_ld = codes_ld;
-  return launch_pack(pack8_kernel(dtype, row_access(access_of(ops[0], E), E, dtype)), E, &p, stream);
+  p.pieces = ceil_div(D, kPackChunks * 32 * E);
+  return launch_pieces(pack8_kernel(dtype, row_access(access_of(ops[0], E), E, dtype)), N, p.pieces,
+                       &p, stream);
 }
 
 int vcoll_checkpoint8_restore(const int8_t* codes, int64_t codes_ld, const float* scales,
@@ -593,7 +596,10 @@ int vcoll_checkpoint8_restore(const int8_t* codes, int64_t codes_ld, const float
   p.x_ld = out_ld;
   p.codes_ld = codes_ld;
   p.wbf16 = weight_dtype == VCOLL_BF16;
-  return launch_pack(unpack8_kernel(dtype, row_access(access_of(ops[4], E), E, dtype)), E, &p, stream);
+  p.pieces = ceil_div(D, kPackChunks * 32 * E);
+  int access = E;
+  for (int k : {2, 3, 4}) access = row_access(access, access_of(ops[k], E), dtype);
+  return launch_pieces(unpack8_kernel(dtype, access), N, p.pieces, &p, stream);
 }
 
 }  // extern "C"

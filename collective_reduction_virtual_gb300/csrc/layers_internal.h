@@ -21,7 +21,7 @@ struct EmbedParams {
   int64_t table_ld, out_ld;
   float scale;
   int idx64;
-  int row_shift;  // log2 of the warps that take a row
+  int64_t pieces;  // of a row, a warp each
 };
 
 // The gradient's tokens are sorted by (token, position) with a stable LSD
@@ -111,8 +111,8 @@ struct PackParams {
   float* scales;
   int64_t N, D;
   int64_t x_ld, codes_ld;  // x_ld: of x or out
+  int64_t pieces;  // of a row, a warp each
   int wbf16;
-  int row_shift;  // log2 of the warps that take a row
 };
 constexpr int kPackChunks = 4;  // chunks that a warp has in flight
 

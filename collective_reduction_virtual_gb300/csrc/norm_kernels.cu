@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(1024) vc_norm_wsum(const __grid_constant__ Nor
 }
 
 // ------------------------------------------------------- 8-bit activations
-// A row is taken by 2^row_shift adjacent warps of a CTA, kPackChunks chunks of
-// 32 * E columns a warp at a time, all of their loads in flight.
+// A warp takes kPackChunks chunks of 32 * E columns of a row, all of their
+// loads in flight.
 
 template <typename T, int A>
 __global__ void __launch_bounds__(kRowThreads) vc_pack8(const __grid_constant__ PackParams p) {
@@ -177,23 +177,18 @@ __global__ void __launch_bounds__(kRowThreads) vc_pack8(const __grid_constant__ 
   constexpr int R = kPackChunks;
   using P = Lanes<T, A, R>;
   constexpr int E = P::E;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = (int)p.D;
-  const int64_t i = (int64_t)blockIdx.x * ((kRowThreads / 32) >> p.row_shift) + (warp >> p.row_shift);
+  const int D = (int)p.D;
+  const RowPiece piece((int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5), p.pieces);
+  const int64_t i = piece.row;
   if (i >= p.N) return;
-  const char* x = elem_at<T>(p.x, i * p.x_ld);
-  int8_t* codes = p.codes + i * p.codes_ld;
-  float* scales = p.scales + i * ((D + kBlock8 - 1) / kBlock8);
-  // 64-bit: the step past the last group may pass 2^31
-  for (int64_t g = (warp & ((1 << p.row_shift) - 1)) * P::kColumns; g < D; g += (int64_t)P::kColumns << p.row_shift) {
-    const int col = (int)g, c = col + P::first(lane);
-    uint4 raw[R];
-    if (g + P::kColumns <= D) P::template load<true>(raw, x, c, D);
-    else P::template load<false>(raw, x, c, D);
-    float f[R][E];
+  const int col = (int)piece.piece * P::kColumns, c = col + P::first(threadIdx.x & 31);
+  uint4 raw[R];
+  if (D - col >= P::kColumns) P::template load<true>(raw, elem_at<T>(p.x, i * p.x_ld), c, D);
+  else P::template load<false>(raw, elem_at<T>(p.x, i * p.x_ld), c, D);
+  float f[R][E];
 #pragma unroll
-    for (int r = 0; r < R; ++r) Elem<T>::widen(raw[r], f[r]);
-    keep8<T, A, R>(f, col, c, D, codes, scales);
-  }
+  for (int r = 0; r < R; ++r) Elem<T>::widen(raw[r], f[r]);
+  keep8<T, A, R>(f, col, c, D, p.codes + i * p.codes_ld, p.scales + i * ((D + kBlock8 - 1) / kBlock8));
 }
 
 template <typename T, int A>
@@ -201,56 +196,58 @@ __global__ void __launch_bounds__(kRowThreads) vc_unpack8(const __grid_constant_
   pdl_enter();
   constexpr int R = kPackChunks;
   using P = Lanes<T, A, R>;
+  using Q = Lanes<T, A, 1>;  // one chunk
   constexpr int E = P::E;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = (int)p.D;
-  const int64_t i = (int64_t)blockIdx.x * ((kRowThreads / 32) >> p.row_shift) + (warp >> p.row_shift);
+  const int D = (int)p.D;
+  const RowPiece piece((int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5), p.pieces);
+  const int64_t i = piece.row;
   if (i >= p.N) return;
   char* out = elem_at<T>(p.out, i * p.x_ld);
   const int8_t* codes = p.codes + i * p.codes_ld;
   const float* scales = p.scales + i * ((D + kBlock8 - 1) / kBlock8);
-  for (int64_t g = (warp & ((1 << p.row_shift) - 1)) * P::kColumns; g < D; g += (int64_t)P::kColumns << p.row_shift) {
-    const int c = (int)g + P::first(lane);
-    auto group = [&](auto full) {
-      constexpr bool FULL = decltype(full)::value;
-      uint32_t word[R][2];
-      float scale[R][E / 4];  // of each four elements
+  const int col = (int)piece.piece * P::kColumns, c = col + P::first(threadIdx.x & 31);
+  auto group = [&](auto full) {
+    constexpr bool FULL = decltype(full)::value;
+    uint32_t word[R][2];
+    float scale[R][E / 4];  // of each four elements
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        word[r][0] = word[r][1] = 0u;
-        if constexpr (A == E) {
-          scale[r][0] = 0.0f;
-          if (P::template inside<FULL>(r, 0, c, D)) {
-            const int at = c + P::offset(r, 0);
-            scale[r][0] = scales[at / kBlock8];
-            if constexpr (E == 8) {
-              const uint2 v = __ldcs(reinterpret_cast<const uint2*>(codes + at));
-              word[r][0] = v.x;
-              word[r][1] = v.y;
-            } else {
-              word[r][0] = __ldcs(reinterpret_cast<const uint32_t*>(codes + at));
-            }
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const bool in = P::template inside<FULL>(r, e, c, D);
-            if (in) word[r][e / 4] |= (uint32_t)(uint8_t)codes[c + P::offset(r, e)] << (8 * (e % 4));
-            if (e % 4 == 0) scale[r][e / 4] = in ? scales[(c + P::offset(r, e)) / kBlock8] : 0.0f;
+    for (int r = 0; r < R; ++r) {
+      word[r][0] = word[r][1] = 0u;
+      if constexpr (A == E) {
+        scale[r][0] = 0.0f;
+        if (P::template inside<FULL>(r, 0, c, D)) {
+          const int at = c + P::offset(r, 0);
+          scale[r][0] = scales[at / kBlock8];
+          if constexpr (E == 8) {
+            const uint2 v = __ldcs(reinterpret_cast<const uint2*>(codes + at));
+            word[r][0] = v.x;
+            word[r][1] = v.y;
+          } else {
+            word[r][0] = __ldcs(reinterpret_cast<const uint32_t*>(codes + at));
           }
         }
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const bool in = P::template inside<FULL>(r, e, c, D);
+          if (in) word[r][e / 4] |= (uint32_t)(uint8_t)codes[c + P::offset(r, e)] << (8 * (e % 4));
+          if (e % 4 == 0) scale[r][e / 4] = in ? scales[(c + P::offset(r, e)) / kBlock8] : 0.0f;
+        }
       }
-      float f[R][E];
+    }
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r) {
+      const int cr = c + r * 32 * E;
+      float f[1][E];
 #pragma unroll
-        for (int e = 0; e < E; e += 2)
-          code_values(word[r][e / 4], e % 4, scale[r][A == E ? 0 : e / 4], f[r][e], f[r][e + 1]);
-      P::template affine<FULL>(p.weight, p.bias, p.wbf16, c, D, f);
-      P::template store<FULL>(out, c, D, f);
-    };
-    if (g + P::kColumns <= D) group(Bool<true>());
-    else group(Bool<false>());
-  }
+      for (int e = 0; e < E; e += 2)
+        code_values(word[r][e / 4], e % 4, scale[r][A == E ? 0 : e / 4], f[0][e], f[0][e + 1]);
+      Q::template affine<FULL>(p.weight, p.bias, p.wbf16, cr, D, f);
+      Q::template store<FULL>(out, cr, D, f);
+    }
+  };
+  if (D - col >= P::kColumns) group(Bool<true>());
+  else group(Bool<false>());
 }
 
 #define VCOLL_BY_TYPE(fn) \

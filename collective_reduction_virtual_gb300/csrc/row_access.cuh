@@ -126,6 +126,19 @@ __device__ __forceinline__ char* elem_at(void* base, int64_t i) {
   return static_cast<char*>(base) + i * Elem<T>::kBytes;
 }
 
+// Which piece of which row a warp takes, where a row has `pieces` of them.
+struct RowPiece {
+  int64_t row, piece;
+  __device__ __forceinline__ RowPiece(int64_t unit, int64_t pieces) {
+    if ((unit | pieces) >> 32) {
+      row = unit / pieces;
+    } else {  // a quarter of the instructions
+      row = (uint32_t)unit / (uint32_t)pieces;
+    }
+    piece = unit - row * pieces;
+  }
+};
+
 __device__ __forceinline__ int64_t token_at(const void* tokens, int idx64, int64_t i) {
   return idx64 ? static_cast<const int64_t*>(tokens)[i] : static_cast<const int32_t*>(tokens)[i];
 }

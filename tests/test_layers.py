@@ -221,6 +221,42 @@ def test_layer_norm(v, dtype, n, d, layout):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,wtype", [(a, b) for a in TYPES for b in TYPES])
+@pytest.mark.parametrize("at", [1, 2, 4])
+def test_weights_at_any_alignment(v, dtype, wtype, at):
+    # weight and bias off the 16-byte boundary beside aligned rows
+    g = gen(at)
+    n, d = 70, 1024
+    x, grad = matrix(g, n, d, dtype), matrix(g, n, d, dtype)
+    aligned = weights(g, d, wtype)
+    flat = torch.empty(2 * d + 16, dtype=wtype, device="cuda")
+    w, b = flat[at:at + d].copy_(aligned[0]), flat[d + 8 + at:2 * d + 8 + at].copy_(aligned[1])
+    wy, _, _, _, _, _, _, by = R.norm(R.f64(x), *host_weights(w, b, d), float(np.float32(1e-5)))
+    y, mean, rstd = v.layer_norm(x, w, b)
+    near(y, wy, by, dtype)
+    wy, _, _, _, _, _, _, by = R.norm(R.f64(x), np.ones(d), R.f64(b), float(np.float32(1e-5)))
+    near(v.layer_norm(x, None, b)[0], wy, by, dtype)
+    h = (R.f64(x) - R.f64(mean)[:, None]) * R.f64(rstd)[:, None]
+    wx, ww, wb, bx, bw, bb = R.norm_grad(R.f64(grad), h, R.f64(rstd), R.f64(w))
+    dx, dw, db = v.layer_norm_backward(grad, x, mean, rstd, w)
+    near(dx, wx, bx, dtype)
+    near(dw, ww, bw, wtype)
+    y2, rstd, k = v.layer_norm_checkpoint8(x, w, b)
+    assert torch.equal(y2, y)
+    # no sums: the same bits whatever the alignment
+    assert torch.equal(v.checkpoint8_restore(k, w, b, dtype=dtype),
+                       v.checkpoint8_restore(k, *aligned, dtype=dtype))
+    assert torch.equal(v.checkpoint8_restore(k, None, b, dtype=dtype),
+                       v.checkpoint8_restore(k, None, aligned[1], dtype=dtype))
+    kept = R.unpack8(k.codes.cpu().numpy(), k.scales.cpu().numpy())
+    wx, ww, wb, bx, bw, bb = R.norm_grad(R.f64(grad), kept, R.f64(rstd), R.f64(w))
+    dx, dw, db = v.layer_norm_backward_checkpoint8(grad, k, rstd, w)
+    near(dx, wx, bx, dtype)
+    near(dw, ww, bw, wtype)
+    near(db, wb, bb, wtype)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", TYPES)
 def test_layer_norm_constant_rows_offsets_and_special_values(v, dtype):
     g = gen(3)
