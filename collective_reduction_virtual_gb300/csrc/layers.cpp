@@ -164,6 +164,8 @@ NormShape norm_shape(int64_t D, int E, bool grad) {
 // `most`.  *ctas: how many.
 int launch_norm_rows(const void* fn, const NormShape& s, size_t smem, int64_t most, NormParams* p,
                      void* stream, int* ctas) {
+  if (!fn)
+    return fail(VCOLL_ERR_UNSUPPORTED, "no kernel for %d chunks and %d threads", s.chunks, s.threads);
   int sms = 0, fit = 0;
   VCOLL_TRY(device_sms(&sms));
   VCOLL_TRY(device_residency(fn, s.threads, smem, &fit));

@@ -11,14 +11,16 @@ const void* forward(int chunks, int threads) {
   if (chunks == 2 && threads <= 256) return (const void*)&vc_norm_rows<__nv_bfloat16, A, 2, 256, KEEP>;
   if (chunks == 4 && threads <= 256) return (const void*)&vc_norm_rows<__nv_bfloat16, A, 4, 256, KEEP>;
   if (chunks == 4 && threads <= 512) return (const void*)&vc_norm_rows<__nv_bfloat16, A, 4, 512, KEEP>;
-  return (const void*)&vc_norm_rows<__nv_bfloat16, A, 8, 512, KEEP>;
+  if (chunks == 8 && threads <= 512) return (const void*)&vc_norm_rows<__nv_bfloat16, A, 8, 512, KEEP>;
+  return nullptr;
 }
 template <int A, bool KEPT>
 const void* backward(int chunks, int threads) {
   if (chunks == 1 && threads <= 256) return (const void*)&vc_norm_grad_rows<__nv_bfloat16, A, 1, 256, KEPT>;
   if (chunks == 2 && threads <= 256) return (const void*)&vc_norm_grad_rows<__nv_bfloat16, A, 2, 256, KEPT>;
   if (chunks == 2 && threads <= 512) return (const void*)&vc_norm_grad_rows<__nv_bfloat16, A, 2, 512, KEPT>;
-  return (const void*)&vc_norm_grad_rows<__nv_bfloat16, A, 4, 512, KEPT>;
+  if (chunks == 4 && threads <= 512) return (const void*)&vc_norm_grad_rows<__nv_bfloat16, A, 4, 512, KEPT>;
+  return nullptr;
 }
 template <int A>
 const void* by_pass(int chunks, int threads, bool grad, bool kept) {

@@ -11,7 +11,8 @@ const void* forward(int chunks, int threads) {
   if (chunks == 2 && threads <= 256) return (const void*)&vc_norm_rows<float, A, 2, 256, KEEP>;
   if (chunks == 4 && threads <= 256) return (const void*)&vc_norm_rows<float, A, 4, 256, KEEP>;
   if (chunks == 8 && threads <= 256) return (const void*)&vc_norm_rows<float, A, 8, 256, KEEP>;
-  return (const void*)&vc_norm_rows<float, A, 8, 512, KEEP>;
+  if (chunks == 8 && threads <= 512) return (const void*)&vc_norm_rows<float, A, 8, 512, KEEP>;
+  return nullptr;
 }
 template <int A, bool KEPT>
 const void* backward(int chunks, int threads) {
@@ -19,7 +20,8 @@ const void* backward(int chunks, int threads) {
   if (chunks == 2 && threads <= 256) return (const void*)&vc_norm_grad_rows<float, A, 2, 256, KEPT>;
   if (chunks == 4 && threads <= 256) return (const void*)&vc_norm_grad_rows<float, A, 4, 256, KEPT>;
   if (chunks == 4 && threads <= 512) return (const void*)&vc_norm_grad_rows<float, A, 4, 512, KEPT>;
-  return (const void*)&vc_norm_grad_rows<float, A, 8, 512, KEPT>;
+  if (chunks == 8 && threads <= 512) return (const void*)&vc_norm_grad_rows<float, A, 8, 512, KEPT>;
+  return nullptr;
 }
 template <int A>
 const void* by_pass(int chunks, int threads, bool grad, bool kept) {

@@ -70,7 +70,7 @@ __device__ __forceinline__ void clear_ring(char* smem, int bytes) {
 // partial sums.  Weight and bias are read for each row, from L1.  MT: threads
 // of a CTA at most.
 template <typename T, int A, int R, int MT, bool KEEP>
-__global__ void __launch_bounds__(MT, MT == 256 ? 3 : 1)
+__global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
     vc_norm_rows(const __grid_constant__ NormParams p) {
   pdl_enter();
   using P = Lanes<T, A, R>;
