@@ -5,17 +5,18 @@
 
 namespace vcoll {
 
-// A warp takes kLookup accesses of 16 bytes per lane of a row, all in flight:
-// the table's rows arrive in pieces of 2 KB.
+// A warp takes a piece of a row, all of its accesses in flight: 2 KB in accesses
+// of 16 bytes, fewer in narrower ones, so that no lane waits for columns that a
+// narrow row does not have.
 template <typename T, int A>
 __global__ void __launch_bounds__(kRowThreads) vc_embed(const __grid_constant__ EmbedParams p) {
   pdl_enter();
-  constexpr int E = kLane<T>, G = E / A * kLookup;
+  constexpr int G = lookup_accesses(A, kLane<T>);
   const RowPiece piece((int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5), p.pieces);
   if (piece.row >= p.N) return;
   const int64_t t = token_at(p.tokens, p.idx64, piece.row);
   const bool inside = t >= 0 && t < p.V;
-  const int64_t c0 = piece.piece * (kLookup * 32 * E) + (threadIdx.x & 31) * A;
+  const int64_t c0 = piece.piece * (G * 32 * A) + (threadIdx.x & 31) * A;
   const char* from = elem_at<T>(p.table, (inside ? t * p.table_ld : 0) + c0);
   char* to = elem_at<T>(p.out, piece.row * p.out_ld + c0);
   Raw<T, A> r[G];
