@@ -430,7 +430,7 @@ static int norm_forward(const void* x, int64_t x_ld, const void* weight, const v
                                       : norm_rows_kernel_bf16(access, s.chunks, s.threads, false, keep);
   // the ring, and two partial sums of 8 bytes a warp
   const size_t smem =
-      (size_t)s.threads * 16 * s.chunks * norm_stages(s.chunks, false) + s.threads / 2;
+      (size_t)s.threads * 16 * s.chunks * norm_stages(s.chunks, E, false) + s.threads / 2;
   int ctas;
   return launch_norm_rows(fn, s, smem, kMaxExtent, &p, stream, &ctas);
 }
@@ -500,8 +500,10 @@ static int norm_backward(const void* grad, int64_t grad_ld, const void* x, int64
     for (int k : {0, 1, 6, 7}) access = row_access(access, access_of(ops[k], E), dtype);
     const void* fn = dtype == VCOLL_F32 ? norm_rows_kernel_f32(access, s.chunks, s.threads, true, kept)
                                         : norm_rows_kernel_bf16(access, s.chunks, s.threads, true, kept);
-    const size_t smem = (size_t)s.threads * norm_stages(s.chunks, true) *
-                            norm_grad_slot_bytes(s.chunks, E, kept) + s.threads / 2;
+    const size_t smem =
+        (size_t)s.threads * (norm_stages(s.chunks, E, true) * norm_grad_slot_bytes(s.chunks, E, kept) +
+                             norm_grad_smem_sums(s.chunks, E) * s.chunks * E * 4) +
+        s.threads / 2;
     VCOLL_TRY(launch_norm_rows(fn, s, smem, kNormMaxCtas, &p, stream, &p.parts));
   }
   if (!dweight && !dbias) return VCOLL_OK;

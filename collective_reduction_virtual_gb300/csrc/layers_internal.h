@@ -100,9 +100,13 @@ constexpr int kNormMaxCtas = 608;
 // backward, where the sums over the rows are in registers too; and at most.
 VCOLL_HD constexpr int norm_chunks(int E, bool grad) { return (grad ? 16 : 32) / E; }
 VCOLL_HD constexpr int norm_max_chunks(int E, bool grad) { return grad && E == 8 ? 4 : 8; }
+// Backward, how many of the two sums over the rows are in shared memory: with
+// 32 values a lane registers do not hold them (they spilled: 16384 columns of
+// bf16 ran at 2.9 TB/s).
+VCOLL_HD constexpr int norm_grad_smem_sums(int R, int E) { return R * E <= 16 ? 0 : E == 8 ? 2 : 1; }
 // slots of the ring of rows on their way: 128 to 256 bytes a thread
-VCOLL_HD constexpr int norm_stages(int R, bool grad) {
-  return grad ? (R <= 2 ? 4 : R == 4 ? 2 : 1) : (R <= 2 ? 4 : 2);
+VCOLL_HD constexpr int norm_stages(int R, int E, bool grad) {
+  return grad ? (R <= 2 ? 4 : R * E <= 16 ? 2 : 1) : (R <= 2 ? 4 : 2);
 }
 // bytes of a thread's slots of one stage of the backward ring
 VCOLL_HD constexpr int norm_grad_slot_bytes(int R, int E, bool kept) {

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
     vc_norm_rows(const __grid_constant__ NormParams p) {
   pdl_enter();
   using P = Lanes<T, A, R>;
-  constexpr int E = P::E, S = norm_stages(R, false);
+  constexpr int E = P::E, S = norm_stages(R, E, false);
   extern __shared__ __align__(16) char smem[];
   const int threads = blockDim.x, D = (int)p.D;
   const Team t(p.warps);
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
     vc_norm_grad_rows(const __grid_constant__ NormParams p) {
   pdl_enter();
   using P = Lanes<T, A, R>;
-  constexpr int E = P::E, S = norm_stages(R, true);
+  constexpr int E = P::E, S = norm_stages(R, E, true);
   // scales that a lane needs for a chunk: of its access's block, or of all
   constexpr int SC = A == E ? 1 : 32 * E / kBlock8;
   extern __shared__ __align__(16) char smem[];
@@ -170,7 +170,13 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
   const int stage = norm_grad_slot_bytes(R, E, KEPT) * threads;
   char* gslot = smem + tid * 16;
   char* xslot = smem + R * threads * 16 + tid * (KEPT ? E : 16);
-  float* red = reinterpret_cast<float*>(smem + S * stage) + t.index * 4 * t.warps;
+  // the sums over the rows: in registers, or beside the ring, where they start
+  // as zeros, too: [dw, db][r][k][thread] of 4 fp32 (fp32 rows leave room there
+  // for the one alone)
+  constexpr bool SUMS = norm_grad_smem_sums(R, E) > 0, BOTH = norm_grad_smem_sums(R, E) > 1;
+  const int sums_bytes = norm_grad_smem_sums(R, E) * R * E * 4 * threads;
+  float4* sums = reinterpret_cast<float4*>(smem + S * stage) + tid;
+  float* red = reinterpret_cast<float*>(smem + S * stage + sums_bytes) + t.index * 4 * t.warps;
 
   const uint32_t rows = (uint32_t)p.N, teams = gridDim.x * (threads / 32 / p.warps);
   const uint32_t begin = blockIdx.x * (threads / 32 / p.warps) + t.index;
@@ -179,7 +185,7 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int e = 0; e < E; ++e) dw[r][e] = db[r][e] = 0.0f;
-  clear_ring(smem, S * stage);
+  clear_ring(smem, S * stage + sums_bytes);
   auto work = [&](auto full) {
     constexpr bool FULL = decltype(full)::value;
     const char* grad = elem_at<T>(p.grad, begin * p.grad_ld);
@@ -200,7 +206,15 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
             // pieces of E bytes whatever A is: rows of codes are 16-byte aligned
             // and padded
             const int from = col + (r * 32 + t.lane) * E;
-            if (FULL || from < D) fetch_async<E>(xslot + at + r * threads * E, x + from);
+            if (FULL || from < D) {
+              // beside rows of single bf16 elements, which are copied at once, the
+              // codes are, too: an asynchronous copy behind those copies was lost
+              // in one build of this kernel
+              if constexpr (P::BYTES < 4)
+                *reinterpret_cast<uint2*>(xslot + at + r * threads * E) =
+                    *reinterpret_cast<const uint2*>(x + from);
+              else fetch_async<E>(xslot + at + r * threads * E, x + from);
+            }
           }
         } else {
           P::template fetch<FULL>(xslot + at, threads * 16, x, c, D);
@@ -277,10 +291,32 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
             mul2(h[r][e], h[r][e + 1], h[r][e], h[r][e + 1], rstd, rstd);
           }
         }
+        if constexpr (SUMS) {
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          fma2(dw[r][e], dw[r][e + 1], f[r][e], f[r][e + 1], h[r][e], h[r][e + 1], dw[r][e], dw[r][e + 1]);
-          add2(db[r][e], db[r][e + 1], db[r][e], db[r][e + 1], f[r][e], f[r][e + 1]);
+          for (int k = 0; k < E; k += 4) {
+            float4* at = sums + (r * E + k) / 4 * threads;
+            float4 w = *at;
+            fma2(w.x, w.y, f[r][k], f[r][k + 1], h[r][k], h[r][k + 1], w.x, w.y);
+            fma2(w.z, w.w, f[r][k + 2], f[r][k + 3], h[r][k + 2], h[r][k + 3], w.z, w.w);
+            *at = w;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; e += 2)
+            fma2(dw[r][e], dw[r][e + 1], f[r][e], f[r][e + 1], h[r][e], h[r][e + 1], dw[r][e], dw[r][e + 1]);
+        }
+        if constexpr (BOTH) {
+#pragma unroll
+          for (int k = 0; k < E; k += 4) {
+            float4* at = sums + (R * E + r * E + k) / 4 * threads;
+            float4 b = *at;
+            add2(b.x, b.y, b.x, b.y, f[r][k], f[r][k + 1]);
+            add2(b.z, b.w, b.z, b.w, f[r][k + 2], f[r][k + 3]);
+            *at = b;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; e += 2) add2(db[r][e], db[r][e + 1], db[r][e], db[r][e + 1], f[r][e], f[r][e + 1]);
         }
       }
       P::template affine<FULL>(p.weight, nullptr, p.wbf16, c, D, f);  // g
@@ -316,10 +352,24 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
   if (col + P::kColumns <= D) work(Bool<true>());
   else work(Bool<false>());
   if (!p.part) return;
+  if constexpr (SUMS) {  // one team, each thread its own columns
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int at = c + P::offset(r, e);
+        const float* own = reinterpret_cast<const float*>(sums + (r * E + e) / 4 * threads) + e % 4;
+        if (at < D) {
+          p.part[(size_t)blockIdx.x * 2 * D + at] = *own;
+          p.part[(size_t)(blockIdx.x * 2 + 1) * D + at] = BOTH ? own[R * E * threads] : db[r][e];
+        }
+      }
+    return;
+  } else {
   // the CTA's sums: its teams add theirs up in the ring's memory, in order
   fetch_wait<0>();
   const int count = threads / 32 / p.warps;
-  float* sums = reinterpret_cast<float*>(smem);  // [2][E * R][team's thread]
+  float* place = reinterpret_cast<float*>(smem);  // [2][E * R][team's thread]
   const int width = p.warps * 32, own = t.warp * 32 + t.lane;
   for (int k = 0; k < count; ++k) {
     __syncthreads();
@@ -328,7 +378,7 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        float* a = sums + (r * E + e) * width + own;
+        float* a = place + (r * E + e) * width + own;
         float* b = a + R * E * width;
         if (k) {
           dw[r][e] = *a + dw[r][e];
@@ -345,6 +395,7 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
           }
         }
       }
+  }
   }
 }
 

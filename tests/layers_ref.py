@@ -43,21 +43,22 @@ def lookup_grad(grad, tokens, V, scale, base):
 
 
 def norm(x, w, b, eps):
-    """(y, mean, rstd, h, and the bounds of mean, rstd relative, h, y)"""
+    """(y, mean, rstd, h, and the bounds of mean, rstd relative, h, y); arrays
+    or tensors of 64 bits"""
     D = x.shape[1]
     mean = x.mean(1)
     dev = x - mean[:, None]
     var = (dev * dev).mean(1)
-    rstd = 1.0 / np.sqrt(var + eps)
+    rstd = (var + eps) ** -0.5
     h = dev * rstd[:, None]
     c = chain(D) * U
-    dmean = (c + U) * np.abs(x).mean(1)
+    dmean = (c + U) * abs(x).mean(1)
     # deviations are taken from the computed mean: dmean enters the variance squared
     dvar = (c + 4 * U) * (var + dmean ** 2) + dmean ** 2
     drel = 0.5 * dvar / (var + eps) + 2.0 ** -22 + 2 * U
-    dh = rstd[:, None] * (dmean[:, None] + U * np.abs(dev)) + np.abs(h) * (drel[:, None] + 3 * U)
+    dh = rstd[:, None] * (dmean[:, None] + U * abs(dev)) + abs(h) * (drel[:, None] + 3 * U)
     y = h * w + b
-    dy = dh * np.abs(w) + 3 * U * (np.abs(h * w) + np.abs(b))
+    dy = dh * abs(w) + 3 * U * (abs(h * w) + abs(b))
     return y, mean, rstd, h, dmean, drel, dh, dy
 
 
@@ -68,12 +69,12 @@ def norm_grad(grad, h, rstd, w):
     m1, m2 = g.mean(1, keepdims=True), (g * h).mean(1, keepdims=True)
     dx = (g - m1 - h * m2) * rstd[:, None]
     c = (chain(D) + 8) * U
-    size = np.abs(g) + np.abs(m1) + np.abs(h * m2)
-    bx = rstd[:, None] * (c * (np.abs(g).mean(1, keepdims=True) +
-                               np.abs(h) * np.abs(g * h).mean(1, keepdims=True)) + 10 * U * size)
+    size = abs(g) + abs(m1) + abs(h * m2)
+    bx = rstd[:, None] * (c * (abs(g).mean(1, keepdims=True) +
+                               abs(h) * abs(g * h).mean(1, keepdims=True)) + 10 * U * size)
     dw, db = (grad * h).sum(0), grad.sum(0)
-    bw = (N + 8) * U * np.abs(grad * h).sum(0)
-    bb = (N + 4) * U * np.abs(grad).sum(0)
+    bw = (N + 8) * U * abs(grad * h).sum(0)
+    bb = (N + 4) * U * abs(grad).sum(0)
     return dx, dw, db, bx, bw, bb
 
 

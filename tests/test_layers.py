@@ -187,7 +187,8 @@ def test_embedding_is_the_adjoint_of_its_gradient(v):
 # --------------------------------------------------------------- layer norm
 
 SHAPES = [(1, 1), (3, 2), (2, 31), (5, 128), (17, 129), (9, 1000), (130, 256), (4, 1001), (33, 4096),
-          (2, 8200), (3, 16384), (2, 70001), (1200, 72)]
+          (2, 8200), (3, 16384), (2, 70001), (1200, 72), (7, 130), (6, 514), (5, 1026), (4, 4098),
+          (3, 8202), (2, 16382)]
 
 
 def weights(g, d, wtype, which="both"):
@@ -307,6 +308,53 @@ def test_layer_norm_backward(v, dtype, n, d, layout):
     assert a is None and torch.equal(b, db)
     v.layer_norm_backward(grad, x, mean, rstd, w, dx=grad, weight_grads=False)
     assert torch.equal(grad, dx)
+
+
+def close(got, want, bound, dtype):
+    """near(), on the GPU"""
+    tol = bound * 1.01 + R.out_unit(dtype) * (want.abs() + bound)
+    bad = (got.double() - want).abs() > tol
+    assert not bad.any(), (bad.nonzero()[:4].tolist(), got[bad][:4].tolist(), want[bad][:4].tolist())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,d", [(5000, 128), (5000, 256), (5000, 512), (3000, 1024), (2500, 1536),
+                                 (1500, 4096), (700, 8192), (700, 12288), (700, 16384), (100, 32768)])
+@pytest.mark.parametrize("at", [0, 2, 1])
+def test_layer_norm_every_width_and_alignment_over_many_rows(v, dtype, n, d, at):
+    # rows enough for every CTA to take several, and the accesses that 16-, 4- and 2- (4-) byte
+    # alignment allow, at widths on each side of how a row is shared out
+    g = gen(n + d + at)
+
+    def place(t):
+        return torch.empty(t.numel() + at, dtype=t.dtype, device="cuda")[at:].view(t.shape).copy_(t)
+
+    x, grad = (place(matrix(g, n, d, dtype, "dense", 2.0, 0.3)) for _ in range(2))
+    w, b = (place(t) for t in weights(g, d, dtype))
+    w64, b64, g64 = w.double(), b.double(), grad.double()
+    wy, wm, wr, h, bm, br, dh, by = R.norm(x.double(), w64, b64, float(np.float32(1e-5)))
+    y, mean, rstd = v.layer_norm(x, w, b, out=place(x))
+    close(mean, wm, bm + R.U * wm.abs(), torch.float32)
+    close(rstd, wr, wr * br, torch.float32)
+    close(y, wy, by, dtype)
+    y2, rstd, k = v.layer_norm_checkpoint8(x, w, b, out=place(x))
+    assert torch.equal(y, y2)
+    kept = (k.codes.view(n, -1, 128).double() * k.scales.double()[:, :, None]).view(n, d)
+    step = k.scales.double().repeat_interleave(128, 1)
+    assert ((kept - h).abs() <= 0.5 * step * (1 + 300 * R.U) + dh).all()
+    back = v.checkpoint8_restore(k, w, b, dtype=dtype, out=place(x))
+    close(back, kept * w64 + b64, 3 * R.U * ((kept * w64).abs() + b64.abs()), dtype)
+    h = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    for form, hh in ((0, h), (1, kept)):
+        wx, ww, wb, bx, bw, bb = R.norm_grad(g64, hh, rstd.double(), w64)
+        if form:
+            dx, dw, db = v.layer_norm_backward_checkpoint8(grad, k, rstd, w, dx=place(x))
+        else:
+            dx, dw, db = v.layer_norm_backward(grad, x, mean, rstd, w, dx=place(x))
+        close(dx, wx, bx, dtype)
+        close(dw, ww, bw, dtype)
+        close(db, wb, bb, dtype)
 
 
 @pytest.mark.gpu
@@ -699,3 +747,55 @@ def test_column_ranges_of_the_same_rows_do_not_overlap(v):
     assert "overlaps" in v.last_error()
     assert f(A, 128, 0, 0, v.F32, 4, 64, 1e-5, A - 4 * 63, 128, 0, 0, v.F32) == v.ERR_INVALID_ARG
     assert f(A, 127, 0, 0, v.F32, 4, 64, 1e-5, A + 4 * 64, 127, 0, 0, v.F32) == v.ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+def test_data_parallel_example(v):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "data_parallel_step.py")
+    spec = importlib.util.spec_from_file_location("data_parallel_step", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    losses, grads = ex.train(steps=60)
+    assert all(np.isfinite(losses))
+    # it starts at an even guess among the tokens, or a little above, and learns the rule
+    assert abs(losses[0] - np.log(ex.VOCAB)) < 0.5 and losses[-1] < 0.5 * losses[0]
+    for u in range(1, ex.RANKS):
+        for a, b in zip(grads[0], grads[u]):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_example_gradients_against_autograd(v):
+    # the whole backward pass of one rank beside autograd on the same formulas in 64 bits: what
+    # separates them is the 8-bit form, half a step (a block's top / 254) in each normalised value
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "data_parallel_step.py")
+    spec = importlib.util.spec_from_file_location("data_parallel_step", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    g = gen(20)
+    tokens, targets = ex.batch(g)
+    params = [torch.randn(ex.VOCAB, ex.WIDTH, generator=g, device="cuda") * 0.2,
+              1 + 0.1 * torch.randn(ex.WIDTH, generator=g, device="cuda"),
+              0.1 * torch.randn(ex.WIDTH, generator=g, device="cuda")]
+    grads = [torch.empty_like(p) for p in params]
+    loss = ex.gradients(params, grads, tokens, targets)
+    table, weight, bias = (p.double().requires_grad_() for p in params)
+    t = tokens.flatten()
+    x = table[t.clamp(min=0)] * (t >= 0)[:, None] * float(np.float32(np.sqrt(ex.WIDTH)))
+    mean = x.mean(1, keepdim=True)
+    h = (x - mean) / ((x - mean).pow(2).mean(1, keepdim=True) + float(np.float32(1e-5))).sqrt()
+    p = torch.log_softmax((h * weight + bias) @ table.t(), 1)
+    valid = ((t >= 0) & (targets.flatten() >= 0))
+    want = -(p.gather(1, targets.flatten().clamp(min=0)[:, None])[:, 0] * valid).sum() / valid.sum()
+    want.backward()
+    assert abs(float(loss) - float(want)) < 1e-4 * float(want)
+    for a, b in zip(grads, (table.grad, weight.grad, bias.grad)):
+        # rounding errors of half a step at most, about a third of that on average and unrelated
+        # to one another: 1 / 254 of the top, 4 deviations, is 1.6 % of a typical value
+        assert float((a.double() - b).norm() / b.norm()) < 0.016
