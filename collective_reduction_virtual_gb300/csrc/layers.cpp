@@ -160,6 +160,20 @@ NormShape norm_shape(int64_t D, int E, bool grad) {
   return s;
 }
 
+// Lanes that take a row of D columns (norm_narrow.cuh), 0: it is too wide.
+int narrow_lanes(int64_t D, int E) { return D <= 8 * E ? 8 : D <= 16 * E ? 16 : D <= 32 * E ? 32 : 0; }
+
+// Launch of a norm_narrow.cuh kernel: as many CTAs as stay resident, at most
+// `most`.  *ctas: how many.
+int launch_norm_narrow(const void* fn, int lanes, int64_t most, NormParams* p, void* stream, int* ctas) {
+  int sms = 0, fit = 0;
+  VCOLL_TRY(device_sms(&sms));
+  VCOLL_TRY(device_residency(fn, kRowThreads, 0, &fit));
+  const int64_t need = ceil_div(p->N, (int64_t)kWarps * kNarrowRows * (32 / lanes));
+  *ctas = (int)std::min(most, std::min<int64_t>(need, (int64_t)sms * fit));
+  return launch_grid(fn, *ctas, 1, kRowThreads, 0, p, stream);
+}
+
 // Launch of a norm_rows.cuh kernel: as many CTAs as stay resident, at most
 // `most`.  *ctas: how many.
 int launch_norm_rows(const void* fn, const NormShape& s, size_t smem, int64_t most, NormParams* p,
@@ -417,6 +431,15 @@ static int norm_forward(const void* x, int64_t x_ld, const void* weight, const v
   p.eps = eps;
   p.wbf16 = weight_dtype == VCOLL_BF16;
   const int E = 16 / es;
+  int access = E, ctas;
+  for (int k = 0; k < 4; ++k) access = row_access(access, access_of(ops[k], E), dtype);
+  if (const int lanes = narrow_lanes(D, E)) {
+    // weight and bias are read once, element by element
+    access = row_access(access_of(ops[0], E), access_of(ops[3], E), dtype);
+    const void* fn = dtype == VCOLL_F32 ? norm_narrow_kernel_f32(access, lanes, false, keep)
+                                        : norm_narrow_kernel_bf16(access, lanes, false, keep);
+    return launch_norm_narrow(fn, lanes, kMaxExtent, &p, stream, &ctas);
+  }
   const NormShape s = norm_shape(D, E, false);
   if (!s.chunks) {
     int64_t grid;
@@ -424,14 +447,11 @@ static int norm_forward(const void* x, int64_t x_ld, const void* weight, const v
     return launch_grid(norm_wide_kernel(dtype), grid, 1, kRowThreads, 0, &p, stream);
   }
   p.warps = s.warps;
-  int access = E;
-  for (int k = 0; k < 4; ++k) access = row_access(access, access_of(ops[k], E), dtype);
   const void* fn = dtype == VCOLL_F32 ? norm_rows_kernel_f32(access, s.chunks, s.threads, false, keep)
                                       : norm_rows_kernel_bf16(access, s.chunks, s.threads, false, keep);
   // the ring, and two partial sums of 8 bytes a warp
   const size_t smem =
       (size_t)s.threads * 16 * s.chunks * norm_stages(s.chunks, E, false) + s.threads / 2;
-  int ctas;
   return launch_norm_rows(fn, s, smem, kMaxExtent, &p, stream, &ctas);
 }
 
@@ -483,6 +503,7 @@ static int norm_backward(const void* grad, int64_t grad_ld, const void* x, int64
   p.codes_ld = codes_ld;
   p.wbf16 = weight_dtype == VCOLL_BF16;
   const int E = 16 / es;
+  const int lanes = narrow_lanes(D, E);
   const NormShape s = norm_shape(D, E, true);
   if (!s.chunks) {
     if (dweight || dbias)
@@ -494,10 +515,16 @@ static int norm_backward(const void* grad, int64_t grad_ld, const void* x, int64
   }
   if (!dx && !dweight && !dbias) return VCOLL_OK;
   if (N) {
-    p.warps = s.warps;
     p.part = dweight || dbias ? (float*)workspace : nullptr;
     int access = E;
-    for (int k : {0, 1, 6, 7}) access = row_access(access, access_of(ops[k], E), dtype);
+    for (int k : {0, 1, 7}) access = row_access(access, access_of(ops[k], E), dtype);
+    if (lanes) {
+      const void* fn = dtype == VCOLL_F32 ? norm_narrow_kernel_f32(access, lanes, true, kept)
+                                          : norm_narrow_kernel_bf16(access, lanes, true, kept);
+      VCOLL_TRY(launch_norm_narrow(fn, lanes, kNormMaxCtas, &p, stream, &p.parts));
+    } else {
+    p.warps = s.warps;
+    access = row_access(access, access_of(ops[6], E), dtype);
     const void* fn = dtype == VCOLL_F32 ? norm_rows_kernel_f32(access, s.chunks, s.threads, true, kept)
                                         : norm_rows_kernel_bf16(access, s.chunks, s.threads, true, kept);
     const size_t smem =
@@ -505,6 +532,7 @@ static int norm_backward(const void* grad, int64_t grad_ld, const void* x, int64
                              norm_grad_smem_sums(s.chunks, E) * s.chunks * E * 4) +
         s.threads / 2;
     VCOLL_TRY(launch_norm_rows(fn, s, smem, kNormMaxCtas, &p, stream, &p.parts));
+    }
   }
   if (!dweight && !dbias) return VCOLL_OK;
   return launch_grid(norm_wsum_kernel(), ceil_div(D, 32), 2, 1024, 0, &p, stream);

@@ -91,6 +91,8 @@ struct NormParams {
   int parts;  // partial rows of the gradient (CTAs)
 };
 
+// norm_narrow.cuh: rows of a group of lanes in flight.
+constexpr int kNarrowRows = 4;
 // norm_rows.cuh: warps of a CTA of several teams, and of the largest team.
 constexpr int kNormCtaWarps = 8;
 constexpr int kNormMaxWarps = 16;
@@ -136,6 +138,8 @@ enum GradPart { GRAD_SMALL, GRAD_SUM, GRAD_SUM_BASE, GRAD_JOIN };
 const void* embed_grad_kernel(int dtype, int table_dtype, int access, GradPart part);
 const void* norm_rows_kernel_f32(int access, int chunks, int threads, bool grad, bool kept);
 const void* norm_rows_kernel_bf16(int access, int chunks, int threads, bool grad, bool kept);
+const void* norm_narrow_kernel_f32(int access, int lanes, bool grad, bool kept);
+const void* norm_narrow_kernel_bf16(int access, int lanes, bool grad, bool kept);
 const void* norm_wsum_kernel();
 const void* norm_wide_kernel(int dtype);
 const void* norm_grad_wide_kernel(int dtype);

@@ -1,4 +1,5 @@
 // Layer norm kernels for fp32 rows.
+#include "norm_narrow.cuh"
 #include "norm_rows.cuh"
 
 namespace vcoll {
@@ -7,7 +8,6 @@ namespace {
 
 template <int A, bool KEEP>
 const void* forward(int chunks, int threads) {
-  if (chunks == 1 && threads <= 256) return (const void*)&vc_norm_rows<float, A, 1, 256, KEEP>;
   if (chunks == 2 && threads <= 256) return (const void*)&vc_norm_rows<float, A, 2, 256, KEEP>;
   if (chunks == 4 && threads <= 256) return (const void*)&vc_norm_rows<float, A, 4, 256, KEEP>;
   if (chunks == 8 && threads <= 256) return (const void*)&vc_norm_rows<float, A, 8, 256, KEEP>;
@@ -16,7 +16,6 @@ const void* forward(int chunks, int threads) {
 }
 template <int A, bool KEPT>
 const void* backward(int chunks, int threads) {
-  if (chunks == 1 && threads <= 256) return (const void*)&vc_norm_grad_rows<float, A, 1, 256, KEPT>;
   if (chunks == 2 && threads <= 256) return (const void*)&vc_norm_grad_rows<float, A, 2, 256, KEPT>;
   if (chunks == 4 && threads <= 256) return (const void*)&vc_norm_grad_rows<float, A, 4, 256, KEPT>;
   if (chunks == 4 && threads <= 512) return (const void*)&vc_norm_grad_rows<float, A, 4, 512, KEPT>;
@@ -34,6 +33,11 @@ const void* by_pass(int chunks, int threads, bool grad, bool kept) {
 const void* norm_rows_kernel_f32(int access, int chunks, int threads, bool grad, bool kept) {
   if (access == 4) return by_pass<4>(chunks, threads, grad, kept);
   return by_pass<1>(chunks, threads, grad, kept);
+}
+
+const void* norm_narrow_kernel_f32(int access, int lanes, bool grad, bool kept) {
+  if (access == 4) return narrow_kernel<float, 4>(lanes, grad, kept);
+  return narrow_kernel<float, 1>(lanes, grad, kept);
 }
 
 }  // namespace vcoll

@@ -1,0 +1,312 @@
+// Layer norm and its gradient for narrow rows, up to 32 * E columns (256 of
+// bf16, 128 of fp32: heads, small models), instantiated in norm_f32.cu and
+// norm_bf16.cu.
+//
+// A row is taken by G lanes (8, 16 or 32), so a warp takes 32 / G rows at a
+// time, and kNarrowRows times that in one go: the loads of all of them are in
+// flight together, and their sums, a few shuffles each, overlap.  Weight and
+// bias stay in registers.  What bounds these kernels is the latency of such a
+// go; a warp of norm_rows.cuh would spend it on one row, most of its lanes idle.
+#pragma once
+
+#include "layers_internal.h"
+#include "norm_common.cuh"
+#include "row_access.cuh"
+
+namespace vcoll {
+
+namespace {
+
+// The lanes of a row: accesses of A elements side by side.
+template <typename T, int A, int G>
+struct Group {
+  static constexpr int E = kLane<T>, BYTES = Elem<T>::kBytes;
+  int sub, c;  // which of the warp's rows, first column
+  __device__ __forceinline__ Group() {
+    const int lane = threadIdx.x & 31;
+    sub = lane / G;
+    c = lane % G * A;
+  }
+  static __device__ __forceinline__ constexpr int offset(int e) { return e / A * G * A + e % A; }
+
+  __device__ __forceinline__ uint4 load(const char* row, int D, bool in) const {
+    uint32_t word[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < E; e += A) {
+      Raw<T, A> v;
+      if (in && c + offset(e) < D) v.load_stream(row + (c + offset(e)) * BYTES);
+      else v.zero();
+      v.into(word, e);
+    }
+    return make_uint4(word[0], word[1], word[2], word[3]);
+  }
+  __device__ __forceinline__ void store(char* row, int D, const float (&f)[E]) const {
+#pragma unroll
+    for (int e = 0; e < E; e += A) {
+      float g[A];
+#pragma unroll
+      for (int a = 0; a < A; ++a) g[a] = f[e + a];
+      Raw<T, A> o;
+      o.narrow(g);
+      if (c + offset(e) < D) o.store_stream(row + (c + offset(e)) * BYTES);
+    }
+  }
+  __device__ __forceinline__ void weights(const void* w, int bf16, int D, float none, float (&f)[E]) const {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      f[e] = c + offset(e) < D ? load_weight(w, bf16, c + offset(e), none) : 0.0f;
+  }
+  static __device__ __forceinline__ float sum(float v) {
+#pragma unroll
+    for (int d = G / 2; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
+    return v;
+  }
+  // Which of a row's two blocks of 128 columns element e lies in.
+  __device__ __forceinline__ int block_of(int e) const {
+    return G * E <= kBlock8 ? 0 : (c + offset(e)) / kBlock8;
+  }
+  // Keeps the row's values (0 past its end): codes and scales.  Every lane of
+  // the warp calls it; `in`: the row exists.
+  __device__ __forceinline__ void keep(const float (&f)[E], int D, bool in, int8_t* codes,
+                                       float* scales) const {
+    constexpr int B = G * E <= kBlock8 ? 1 : 2;
+    uint32_t top[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) top[b] = 0u;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+        if (block_of(e) == b) top[b] = max(top[b], magnitude_bits(f[e]));
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+#pragma unroll
+      for (int d = G / 2; d; d >>= 1) top[b] = max(top[b], __shfl_xor_sync(~0u, top[b], d));
+    Scale8 s[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) s[b] = scale8(top[b]);
+    if (!in) return;
+    const int end = (D + 15) & ~15;
+    uint32_t word[E / 4];
+#pragma unroll
+    for (int k = 0; k < E; k += 4)  // four elements lie in one block
+      word[k / 4] = code_word(f + k, s[B == 2 && block_of(k) == 1 ? B - 1 : 0]);
+#pragma unroll
+    for (int e = 0; e < E; e += A) {
+      const int at = c + offset(e);
+      if (at >= end) break;
+      if constexpr (A == 8) *reinterpret_cast<uint2*>(codes + at) = make_uint2(word[0], word[E / 4 - 1]);
+      else if constexpr (A == 4) *reinterpret_cast<uint32_t*>(codes + at) = word[e / 4];
+      else if constexpr (A == 2)
+        *reinterpret_cast<uint16_t*>(codes + at) = (uint16_t)(word[e / 4] >> (8 * (e % 4)));
+      else codes[at] = (int8_t)(word[e / 4] >> (8 * (e % 4)));
+    }
+    // rows of fewer than G * E columns may have no second block; columns from
+    // the end of the lanes' to the padded end are the first lanes'
+    if (c == 0)
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+        if (b * kBlock8 < D) scales[b] = s[b].scale;
+  }
+  // h from codes and scales
+  __device__ __forceinline__ void kept(const int8_t* codes, const float* scales, int D, bool in,
+                                       float (&h)[E]) const {
+    uint32_t word[2] = {0u, 0u};
+    float scale[E / 4];
+#pragma unroll
+    for (int e = 0; e < E; e += A) {
+      const int at = c + offset(e);
+      const bool has = in && at < D;
+      if (e % 4 == 0) scale[e / 4] = has ? scales[at / kBlock8] : 0.0f;
+      if (!has) continue;
+      if constexpr (A == 8) {
+        const uint2 v = __ldcs(reinterpret_cast<const uint2*>(codes + at));
+        word[0] = v.x;
+        word[1] = v.y;
+        scale[E / 4 - 1] = scale[0];
+      } else if constexpr (A == 4) {
+        word[e / 4] = __ldcs(reinterpret_cast<const uint32_t*>(codes + at));
+      } else {
+#pragma unroll
+        for (int a = 0; a < A; ++a)
+          word[(e + a) / 4] |= (uint32_t)(uint8_t)codes[at + a] << (8 * ((e + a) % 4));
+      }
+    }
+    if constexpr (A == 8) scale[E / 4 - 1] = scale[0];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) code_values(word[e / 4], e % 4, scale[e / 4], h[e], h[e + 1]);
+  }
+};
+
+}  // namespace
+
+template <typename T, int A, int G, bool KEEP>
+__global__ void __launch_bounds__(kRowThreads, 3) vc_norm_narrow(const __grid_constant__ NormParams p) {
+  pdl_enter();
+  using P = Group<T, A, G>;
+  constexpr int E = P::E, U = kNarrowRows, S = 32 / G;
+  const P g;
+  const int D = (int)p.D;
+  float w[E], b[E];
+  g.weights(p.weight, p.wbf16, D, 1.0f, w);
+  g.weights(p.bias, p.wbf16, D, 0.0f, b);
+  const uint32_t rows = (uint32_t)p.N, warps = gridDim.x * (kRowThreads / 32);
+  for (uint32_t unit = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); unit * (U * S) < rows; unit += warps) {
+    const uint32_t first = unit * (U * S) + g.sub;
+    uint4 raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t i = first + u * S;
+      raw[u] = g.load(elem_at<T>(p.x, i * p.x_ld), D, i < rows);
+    }
+    float f[U][E], mean[U], rstd[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      Elem<T>::widen(raw[u], f[u]);
+      float x = 0.0f, y = 0.0f;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) add2(x, y, x, y, f[u][e], f[u][e + 1]);
+      mean[u] = P::sum(x + y) / (float)D;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float x = 0.0f, y = 0.0f;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        add2(f[u][e], f[u][e + 1], f[u][e], f[u][e + 1], -mean[u], -mean[u]);
+        if (g.c + P::offset(e) >= D) f[u][e] = 0.0f;
+        if (g.c + P::offset(e + 1) >= D) f[u][e + 1] = 0.0f;
+        fma2(x, y, f[u][e], f[u][e + 1], f[u][e], f[u][e + 1], x, y);
+      }
+      rstd[u] = rsqrtf(P::sum(x + y) / (float)D + p.eps);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t i = first + u * S;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) mul2(f[u][e], f[u][e + 1], f[u][e], f[u][e + 1], rstd[u], rstd[u]);
+      if constexpr (KEEP)
+        g.keep(f[u], D, i < rows, p.codes + i * p.codes_ld, p.scales + (int64_t)i * ((D + kBlock8 - 1) / kBlock8));
+      if (i >= rows) continue;
+#pragma unroll
+      for (int e = 0; e < E; e += 2)
+        fma2(f[u][e], f[u][e + 1], f[u][e], f[u][e + 1], w[e], w[e + 1], b[e], b[e + 1]);
+      g.store(elem_at<T>(p.y, i * p.y_ld), D, f[u]);
+      if (g.c == 0) {
+        if (p.mean) p.mean[i] = mean[u];
+        if (p.rstd) p.rstd[i] = rstd[u];
+      }
+    }
+  }
+}
+
+template <typename T, int A, int G, bool KEPT>
+__global__ void __launch_bounds__(kRowThreads, 2) vc_norm_grad_narrow(const __grid_constant__ NormParams p) {
+  pdl_enter();
+  using P = Group<T, A, G>;
+  constexpr int E = P::E, U = kNarrowRows, S = 32 / G, NW = kRowThreads / 32;
+  __shared__ float sums[2][NW][G * E];
+  const P g;
+  const int D = (int)p.D, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float w[E], dw[E], db[E];
+  g.weights(p.weight, p.wbf16, D, 1.0f, w);
+#pragma unroll
+  for (int e = 0; e < E; ++e) dw[e] = db[e] = 0.0f;
+  const uint32_t rows = (uint32_t)p.N, warps = gridDim.x * NW;
+  for (uint32_t unit = blockIdx.x * NW + warp; unit * (U * S) < rows; unit += warps) {
+    const uint32_t first = unit * (U * S) + g.sub;
+    uint4 graw[U], xraw[U];
+    float h[U][E], mean[U], rstd[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t i = first + u * S;
+      const bool in = i < rows;
+      graw[u] = g.load(elem_at<T>(p.grad, i * p.grad_ld), D, in);
+      if constexpr (!KEPT) {
+        xraw[u] = g.load(elem_at<T>(p.x, i * p.x_ld), D, in);
+        mean[u] = in ? p.mean[i] : 0.0f;
+      }
+      rstd[u] = in ? p.rstd[i] : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t i = first + u * S;
+      if constexpr (KEPT) {
+        g.kept(p.codes + i * p.codes_ld, p.scales + (int64_t)i * ((D + kBlock8 - 1) / kBlock8), D, i < rows, h[u]);
+      } else {
+        Elem<T>::widen(xraw[u], h[u]);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          add2(h[u][e], h[u][e + 1], h[u][e], h[u][e + 1], -mean[u], -mean[u]);
+          mul2(h[u][e], h[u][e + 1], h[u][e], h[u][e + 1], rstd[u], rstd[u]);
+        }
+      }
+    }
+    // columns past the row's end, and rows past the last, have a gradient of 0
+    float f[U][E], s1[U], s2[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      Elem<T>::widen(graw[u], f[u]);
+      float ax = 0.0f, ay = 0.0f, bx = 0.0f, by = 0.0f;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        fma2(dw[e], dw[e + 1], f[u][e], f[u][e + 1], h[u][e], h[u][e + 1], dw[e], dw[e + 1]);
+        add2(db[e], db[e + 1], db[e], db[e + 1], f[u][e], f[u][e + 1]);
+        mul2(f[u][e], f[u][e + 1], f[u][e], f[u][e + 1], w[e], w[e + 1]);
+        add2(ax, ay, ax, ay, f[u][e], f[u][e + 1]);
+        fma2(bx, by, f[u][e], f[u][e + 1], h[u][e], h[u][e + 1], bx, by);
+      }
+      s1[u] = P::sum(ax + ay) / -(float)D;
+      s2[u] = P::sum(bx + by) / -(float)D;
+    }
+    if (!p.y) continue;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t i = first + u * S;
+      if (i >= rows) continue;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        add2(f[u][e], f[u][e + 1], f[u][e], f[u][e + 1], s1[u], s1[u]);
+        fma2(f[u][e], f[u][e + 1], h[u][e], h[u][e + 1], s2[u], s2[u], f[u][e], f[u][e + 1]);
+        mul2(f[u][e], f[u][e + 1], f[u][e], f[u][e + 1], rstd[u], rstd[u]);
+      }
+      g.store(elem_at<T>(p.y, i * p.y_ld), D, f[u]);
+    }
+  }
+  if (!p.part) return;
+  // the groups of a warp, then its warps, in order
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+#pragma unroll
+    for (int d = G; d < 32; d *= 2) {
+      dw[e] += __shfl_xor_sync(~0u, dw[e], d);
+      db[e] += __shfl_xor_sync(~0u, db[e], d);
+    }
+    if (lane < G) {
+      sums[0][warp][g.c + P::offset(e)] = dw[e];
+      sums[1][warp][g.c + P::offset(e)] = db[e];
+    }
+  }
+  __syncthreads();
+  for (int k = threadIdx.x; k < 2 * D; k += kRowThreads) {
+    const int which = k >= D, at = k - which * D;
+    float s = 0.0f;
+    for (int n = 0; n < NW; ++n) s += sums[which][n][at];
+    p.part[(size_t)(blockIdx.x * 2 + which) * D + at] = s;
+  }
+}
+
+// access: elements of an access; lanes: of a row
+template <typename T, int A, int G>
+const void* narrow_kernel(bool grad, bool kept) {
+  if (grad) return kept ? (const void*)&vc_norm_grad_narrow<T, A, G, true> : (const void*)&vc_norm_grad_narrow<T, A, G, false>;
+  return kept ? (const void*)&vc_norm_narrow<T, A, G, true> : (const void*)&vc_norm_narrow<T, A, G, false>;
+}
+template <typename T, int A>
+const void* narrow_kernel(int lanes, bool grad, bool kept) {
+  return lanes == 8    ? narrow_kernel<T, A, 8>(grad, kept)
+         : lanes == 16 ? narrow_kernel<T, A, 16>(grad, kept)
+                       : narrow_kernel<T, A, 32>(grad, kept);
+}
+
+}  // namespace vcoll
