@@ -1,6 +1,7 @@
 // Embedding lookup and its gradient.
 #include "device_common.cuh"
 #include "layers_internal.h"
+#include "norm_common.cuh"
 #include "row_access.cuh"
 
 namespace vcoll {
@@ -35,6 +36,34 @@ __global__ void __launch_bounds__(kRowThreads) vc_embed(const __grid_constant__ 
     Raw<T, A> o;
     o.narrow(f);
     o.store_stream(elem_at<T>(to, j * 32 * A));
+  }
+}
+
+// Narrow rows, kNarrowRows of each group of G lanes in flight.
+template <typename T, int A, int G>
+__global__ void __launch_bounds__(kRowThreads) vc_embed_narrow(const __grid_constant__ EmbedParams p) {
+  pdl_enter();
+  const Group<T, A, G> g;
+  constexpr int E = kLane<T>, U = kNarrowRows, S = 32 / G;
+  const int D = (int)p.D;
+  const int64_t first = ((int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * (U * S) + g.sub;
+  int64_t t[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) t[u] = first + u * S < p.N ? token_at(p.tokens, p.idx64, first + u * S) : -1;
+  uint4 raw[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const bool inside = t[u] >= 0 && t[u] < p.V;
+    raw[u] = g.load(elem_at<T>(p.table, inside ? t[u] * p.table_ld : 0), D, inside);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (first + u * S >= p.N) return;
+    float f[E];
+    Elem<T>::widen(raw[u], f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = __fmul_rn(f[e], p.scale);
+    g.store(elem_at<T>(p.out, (first + u * S) * p.out_ld), D, f);
   }
 }
 
@@ -681,6 +710,24 @@ const void* lookup_kernel(int access) {
                             : (const void*)&vc_embed<T, 1>;
 }
 }  // namespace
+namespace {
+template <typename T, int A>
+const void* lookup_narrow_kernel(int lanes) {
+  return lanes == 8    ? (const void*)&vc_embed_narrow<T, A, 8>
+         : lanes == 16 ? (const void*)&vc_embed_narrow<T, A, 16>
+                       : (const void*)&vc_embed_narrow<T, A, 32>;
+}
+template <typename T>
+const void* lookup_narrow_kernel(int access, int lanes) {
+  return access == kLane<T> ? lookup_narrow_kernel<T, kLane<T>>(lanes)
+         : access == 2      ? lookup_narrow_kernel<T, 2>(lanes)
+                            : lookup_narrow_kernel<T, 1>(lanes);
+}
+}  // namespace
+const void* embed_narrow_kernel(int dtype, int access, int lanes) {
+  return dtype == VCOLL_F32 ? lookup_narrow_kernel<float>(access, lanes)
+                            : lookup_narrow_kernel<__nv_bfloat16>(access, lanes);
+}
 const void* embed_kernel(int dtype, int access) {
   return dtype == VCOLL_F32 ? lookup_kernel<float>(access) : lookup_kernel<__nv_bfloat16>(access);
 }

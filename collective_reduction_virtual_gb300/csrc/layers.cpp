@@ -121,6 +121,15 @@ int grid_for(int64_t items, int64_t per, int waves, int64_t* grid) {
 
 constexpr int kWarps = kRowThreads / 32;
 
+// Lanes that take a row of D columns where the row is narrow, else 0.
+int narrow_lanes(int64_t D, int E) { return D <= 8 * E ? 8 : D <= 16 * E ? 16 : D <= 32 * E ? 32 : 0; }
+
+// kNarrowRows rows for each group of `lanes` lanes.
+int launch_narrow(const void* fn, int64_t N, int lanes, void* params, void* stream) {
+  return launch_grid(fn, ceil_div(N, (int64_t)kWarps * kNarrowRows * (32 / lanes)), 1, kRowThreads, 0,
+                     params, stream);
+}
+
 // A warp for each piece of each of N rows.
 int launch_pieces(const void* fn, int64_t N, int64_t pieces, void* params, void* stream) {
   const int64_t grid = ceil_div(N, kWarps) > 0x7FFFFFFF / pieces ? 0 : ceil_div(N * pieces, kWarps);
@@ -159,9 +168,6 @@ NormShape norm_shape(int64_t D, int E, bool grad) {
   s.threads = s.warps * std::max(1, kNormCtaWarps / s.warps) * 32;
   return s;
 }
-
-// Lanes that take a row of D columns (norm_narrow.cuh), 0: it is too wide.
-int narrow_lanes(int64_t D, int E) { return D <= 8 * E ? 8 : D <= 16 * E ? 16 : D <= 32 * E ? 32 : 0; }
 
 // Launch of a norm_narrow.cuh kernel: as many CTAs as stay resident, at most
 // `most`.  *ctas: how many.
@@ -263,6 +269,8 @@ int vcoll_embedding(const void* tokens, int index_type, int64_t N, const void* t
   p.scale = scale;
   p.idx64 = index_type == VCOLL_I64;
   const int E = 16 / es, access = std::min(access_of(ops[1], E), access_of(ops[2], E));
+  if (const int lanes = narrow_lanes(D, E))
+    return launch_narrow(embed_narrow_kernel(dtype, access, lanes), N, lanes, &p, stream);
   p.pieces = ceil_div(D, lookup_accesses(access, E) * 32 * access);
   return launch_pieces(embed_kernel(dtype, access), N, p.pieces, &p, stream);
 }
@@ -599,9 +607,11 @@ int vcoll_checkpoint8(const void* x, int64_t x_ld, int64_t N, int64_t D, int8_t*
   p.D = D;
   p.x_ld = x_ld;
   p.codes_ld = codes_ld;
+  const int access = row_access(access_of(ops[0], E), E, dtype);
+  if (const int lanes = narrow_lanes(D, E))
+    return launch_narrow(pack8_narrow_kernel(dtype, access, lanes, false), N, lanes, &p, stream);
   p.pieces = ceil_div(D, kPackChunks * 32 * E);
-  return launch_pieces(pack8_kernel(dtype, row_access(access_of(ops[0], E), E, dtype)), N, p.pieces,
-                       &p, stream);
+  return launch_pieces(pack8_kernel(dtype, access), N, p.pieces, &p, stream);
 }
 
 int vcoll_checkpoint8_restore(const int8_t* codes, int64_t codes_ld, const float* scales,
@@ -630,9 +640,11 @@ int vcoll_checkpoint8_restore(const int8_t* codes, int64_t codes_ld, const float
   p.x_ld = out_ld;
   p.codes_ld = codes_ld;
   p.wbf16 = weight_dtype == VCOLL_BF16;
+  int access = row_access(access_of(ops[4], E), E, dtype);
+  if (const int lanes = narrow_lanes(D, E))  // weight and bias by single elements
+    return launch_narrow(pack8_narrow_kernel(dtype, access, lanes, true), N, lanes, &p, stream);
+  for (int k : {2, 3}) access = row_access(access, access_of(ops[k], E), dtype);
   p.pieces = ceil_div(D, kPackChunks * 32 * E);
-  int access = E;
-  for (int k : {2, 3, 4}) access = row_access(access, access_of(ops[k], E), dtype);
   return launch_pieces(unpack8_kernel(dtype, access), N, p.pieces, &p, stream);
 }
 

@@ -131,6 +131,7 @@ constexpr int kPackChunks = 4;  // chunks that a warp has in flight
 
 // access: elements of an access (a whole 16 bytes of dtype, 2 or 1)
 const void* embed_kernel(int dtype, int access);
+const void* embed_narrow_kernel(int dtype, int access, int lanes);
 const void* embed_sort_kernel();
 const void* embed_count_kernel();
 const void* embed_scatter_kernel();
@@ -146,5 +147,6 @@ const void* norm_grad_wide_kernel(int dtype);
 const void* norm_wgrad_wide_kernel(int dtype);
 const void* pack8_kernel(int dtype, int access);
 const void* unpack8_kernel(int dtype, int access);
+const void* pack8_narrow_kernel(int dtype, int access, int lanes, bool unpack);
 
 }  // namespace vcoll

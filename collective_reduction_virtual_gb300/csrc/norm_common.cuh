@@ -286,6 +286,131 @@ __device__ __forceinline__ void keep8(const float (&f)[R][kLane<T>], int col, in
   }
 }
 
+// ------------------------------------------------------------ narrow rows
+// A row of up to G * E columns is taken by G lanes (8, 16 or 32), accesses of A
+// elements side by side, so that a warp takes 32 / G rows at a time.
+template <typename T, int A, int G>
+struct Group {
+  static constexpr int E = kLane<T>, BYTES = Elem<T>::kBytes;
+  int sub, c;  // which of the warp's rows, first column
+  __device__ __forceinline__ Group() {
+    const int lane = threadIdx.x & 31;
+    sub = lane / G;
+    c = lane % G * A;
+  }
+  static __device__ __forceinline__ constexpr int offset(int e) { return e / A * G * A + e % A; }
+
+  __device__ __forceinline__ uint4 load(const char* row, int D, bool in) const {
+    uint32_t word[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < E; e += A) {
+      Raw<T, A> v;
+      if (in && c + offset(e) < D) v.load_stream(row + (c + offset(e)) * BYTES);
+      else v.zero();
+      v.into(word, e);
+    }
+    return make_uint4(word[0], word[1], word[2], word[3]);
+  }
+  __device__ __forceinline__ void store(char* row, int D, const float (&f)[E]) const {
+#pragma unroll
+    for (int e = 0; e < E; e += A) {
+      float g[A];
+#pragma unroll
+      for (int a = 0; a < A; ++a) g[a] = f[e + a];
+      Raw<T, A> o;
+      o.narrow(g);
+      if (c + offset(e) < D) o.store_stream(row + (c + offset(e)) * BYTES);
+    }
+  }
+  __device__ __forceinline__ void weights(const void* w, int bf16, int D, float none, float (&f)[E]) const {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      f[e] = c + offset(e) < D ? load_weight(w, bf16, c + offset(e), none) : 0.0f;
+  }
+  static __device__ __forceinline__ float sum(float v) {
+#pragma unroll
+    for (int d = G / 2; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
+    return v;
+  }
+  // Which of a row's two blocks of 128 columns element e lies in.
+  __device__ __forceinline__ int block_of(int e) const {
+    return G * E <= kBlock8 ? 0 : (c + offset(e)) / kBlock8;
+  }
+  // Keeps the row's values (0 past its end): codes and scales.  Every lane of
+  // the warp calls it; `in`: the row exists.
+  __device__ __forceinline__ void keep(const float (&f)[E], int D, bool in, int8_t* codes,
+                                       float* scales) const {
+    // whole accesses of a row of two blocks: half of its lanes have each
+    constexpr bool HALVES = G * E > kBlock8 && A == E;
+    constexpr int B = G * E <= kBlock8 || HALVES ? 1 : 2, L = HALVES ? G / 2 : G;
+    uint32_t top[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) top[b] = 0u;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+        if (B == 1 || block_of(e) == b) top[b] = max(top[b], magnitude_bits(f[e]));
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+#pragma unroll
+      for (int d = L / 2; d; d >>= 1) top[b] = max(top[b], __shfl_xor_sync(~0u, top[b], d));
+    Scale8 s[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) s[b] = scale8(top[b]);
+    if (!in) return;
+    const int end = (D + 15) & ~15;
+    uint32_t word[E / 4];
+#pragma unroll
+    for (int k = 0; k < E; k += 4)  // four elements lie in one block
+      word[k / 4] = code_word(f + k, s[B == 2 && block_of(k) == 1 ? B - 1 : 0]);
+#pragma unroll
+    for (int e = 0; e < E; e += A) {
+      const int at = c + offset(e);
+      if (at >= end) break;
+      if constexpr (A == 8) *reinterpret_cast<uint2*>(codes + at) = make_uint2(word[0], word[E / 4 - 1]);
+      else if constexpr (A == 4) *reinterpret_cast<uint32_t*>(codes + at) = word[e / 4];
+      else if constexpr (A == 2)
+        *reinterpret_cast<uint16_t*>(codes + at) = (uint16_t)(word[e / 4] >> (8 * (e % 4)));
+      else codes[at] = (int8_t)(word[e / 4] >> (8 * (e % 4)));
+    }
+    // rows of fewer than G * E columns may have no second block
+    if (c == 0)
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+        if (b * kBlock8 < D) scales[b] = s[b].scale;
+    if (HALVES && c == kBlock8 && c < D) scales[1] = s[0].scale;
+  }
+  // h from codes and scales
+  __device__ __forceinline__ void kept(const int8_t* codes, const float* scales, int D, bool in,
+                                       float (&h)[E]) const {
+    uint32_t word[2] = {0u, 0u};
+    float scale[E / 4];
+#pragma unroll
+    for (int e = 0; e < E; e += A) {
+      const int at = c + offset(e);
+      const bool has = in && at < D;
+      if (e % 4 == 0) scale[e / 4] = has ? scales[at / kBlock8] : 0.0f;
+      if (!has) continue;
+      if constexpr (A == 8) {
+        const uint2 v = __ldcs(reinterpret_cast<const uint2*>(codes + at));
+        word[0] = v.x;
+        word[1] = v.y;
+        scale[E / 4 - 1] = scale[0];
+      } else if constexpr (A == 4) {
+        word[e / 4] = __ldcs(reinterpret_cast<const uint32_t*>(codes + at));
+      } else {
+#pragma unroll
+        for (int a = 0; a < A; ++a)
+          word[(e + a) / 4] |= (uint32_t)(uint8_t)codes[at + a] << (8 * ((e + a) % 4));
+      }
+    }
+    if constexpr (A == 8) scale[E / 4 - 1] = scale[0];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) code_values(word[e / 4], e % 4, scale[e / 4], h[e], h[e + 1]);
+  }
+};
+
 }  // namespace
 
 }  // namespace vcoll

@@ -250,6 +250,55 @@ __global__ void __launch_bounds__(kRowThreads) vc_unpack8(const __grid_constant_
   else group(Bool<false>());
 }
 
+// Narrow rows, kNarrowRows of each group of G lanes in flight.
+template <typename T, int A, int G>
+__global__ void __launch_bounds__(kRowThreads) vc_pack8_narrow(const __grid_constant__ PackParams p) {
+  pdl_enter();
+  const Group<T, A, G> g;
+  constexpr int E = kLane<T>, U = kNarrowRows, S = 32 / G;
+  const int D = (int)p.D;
+  const int64_t first = ((int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * (U * S) + g.sub;
+  uint4 raw[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t i = first + u * S;
+    raw[u] = g.load(elem_at<T>(p.x, i * p.x_ld), D, i < p.N);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t i = first + u * S;
+    float f[E];
+    Elem<T>::widen(raw[u], f);
+    g.keep(f, D, i < p.N, p.codes + i * p.codes_ld, p.scales + i * ((D + kBlock8 - 1) / kBlock8));
+  }
+}
+template <typename T, int A, int G>
+__global__ void __launch_bounds__(kRowThreads) vc_unpack8_narrow(const __grid_constant__ PackParams p) {
+  pdl_enter();
+  const Group<T, A, G> g;
+  constexpr int E = kLane<T>, U = kNarrowRows, S = 32 / G;
+  const int D = (int)p.D;
+  const int64_t first = ((int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * (U * S) + g.sub;
+  float f[U][E], w[E], b[E];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t i = first + u * S;
+    g.kept(p.codes + i * p.codes_ld, p.scales + i * ((D + kBlock8 - 1) / kBlock8), D, i < p.N, f[u]);
+  }
+  g.weights(p.weight, p.wbf16, D, 1.0f, w);
+  g.weights(p.bias, p.wbf16, D, 0.0f, b);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t i = first + u * S;
+    if (i >= p.N) return;
+    if (p.weight || p.bias)
+#pragma unroll
+      for (int e = 0; e < E; e += 2)
+        fma2(f[u][e], f[u][e + 1], f[u][e], f[u][e + 1], w[e], w[e + 1], b[e], b[e + 1]);
+    g.store(elem_at<T>(p.out, i * p.x_ld), D, f[u]);
+  }
+}
+
 #define VCOLL_BY_TYPE(fn) \
   (dtype == VCOLL_F32 ? (const void*)&fn<float> : (const void*)&fn<__nv_bfloat16>)
 #define VCOLL_BY_ACCESS(fn)                                                                \
@@ -263,6 +312,21 @@ const void* norm_wgrad_wide_kernel(int dtype) { return VCOLL_BY_TYPE(vc_norm_wgr
 const void* norm_wsum_kernel() { return (const void*)&vc_norm_wsum; }
 const void* pack8_kernel(int dtype, int access) { return VCOLL_BY_ACCESS(vc_pack8); }
 const void* unpack8_kernel(int dtype, int access) { return VCOLL_BY_ACCESS(vc_unpack8); }
+
+namespace {
+template <typename T, int A>
+const void* narrow(int lanes, bool unpack) {
+  if (lanes == 8) return unpack ? (const void*)&vc_unpack8_narrow<T, A, 8> : (const void*)&vc_pack8_narrow<T, A, 8>;
+  if (lanes == 16) return unpack ? (const void*)&vc_unpack8_narrow<T, A, 16> : (const void*)&vc_pack8_narrow<T, A, 16>;
+  return unpack ? (const void*)&vc_unpack8_narrow<T, A, 32> : (const void*)&vc_pack8_narrow<T, A, 32>;
+}
+}  // namespace
+const void* pack8_narrow_kernel(int dtype, int access, int lanes, bool unpack) {
+  if (dtype == VCOLL_F32) return access == 4 ? narrow<float, 4>(lanes, unpack) : narrow<float, 1>(lanes, unpack);
+  return access == 8   ? narrow<__nv_bfloat16, 8>(lanes, unpack)
+         : access == 2 ? narrow<__nv_bfloat16, 2>(lanes, unpack)
+                       : narrow<__nv_bfloat16, 1>(lanes, unpack);
+}
 #undef VCOLL_BY_TYPE
 #undef VCOLL_BY_ACCESS
 
