@@ -27,7 +27,8 @@ int fail(int status, const char* fmt, ...) {
     if (rc_) return rc_;  \
   } while (0)
 
-constexpr int64_t kMaxExtent = 0x7FFFFFFE;
+constexpr int64_t kMaxExtent = 0x7FFFFFFE;  // rows; tokens of a table
+constexpr int64_t kMaxWidth = 1 << 30;      // columns: a chunk past the last fits 32 bits
 
 int elem_size(int dtype) { return dtype == VCOLL_F32 ? 4 : dtype == VCOLL_BF16 ? 2 : 0; }
 
@@ -36,11 +37,11 @@ int check_type(int dtype, const char* what) {
   return VCOLL_OK;
 }
 
-int check_extent(int64_t v, const char* what) {
+int check_extent(int64_t v, const char* what, int64_t most = kMaxExtent) {
   if (v < 0) return fail(VCOLL_ERR_INVALID_ARG, "%s = %lld < 0", what, (long long)v);
-  if (v > kMaxExtent)
+  if (v > most)
     return fail(VCOLL_ERR_UNSUPPORTED, "%s = %lld is above %lld", what, (long long)v,
-                (long long)kMaxExtent);
+                (long long)most);
   return VCOLL_OK;
 }
 
@@ -249,7 +250,7 @@ int vcoll_embedding(const void* tokens, int index_type, int64_t N, const void* t
     return fail(VCOLL_ERR_INVALID_TYPE, "unknown index type %d", index_type);
   VCOLL_TRY(check_extent(N, "N"));
   VCOLL_TRY(check_extent(V, "V"));
-  VCOLL_TRY(check_extent(D, "D"));
+  VCOLL_TRY(check_extent(D, "D", kMaxWidth));
   const int es = elem_size(dtype);
   const Operand ops[] = {
       {"tokens", tokens, D ? N : 0, 1, 1, index_type == VCOLL_I64 ? 8 : 4, false, nullptr},
@@ -276,7 +277,7 @@ int vcoll_embedding(const void* tokens, int index_type, int64_t N, const void* t
 }
 
 size_t vcoll_embedding_backward_workspace_bytes(int64_t N, int64_t V, int64_t D) {
-  if (N <= kSmallTokens || V <= 0 || D <= 0 || N > kMaxExtent || V > kMaxExtent || D > kMaxExtent)
+  if (N <= kSmallTokens || V <= 0 || D <= 0 || N > kMaxExtent || V > kMaxExtent || D > kMaxWidth)
     return 0;
   return grad_layout(N, V, D).bytes;
 }
@@ -292,7 +293,7 @@ int vcoll_embedding_backward(const void* grad, int64_t grad_ld, int dtype, const
     return fail(VCOLL_ERR_INVALID_TYPE, "unknown index type %d", index_type);
   VCOLL_TRY(check_extent(N, "N"));
   VCOLL_TRY(check_extent(V, "V"));
-  VCOLL_TRY(check_extent(D, "D"));
+  VCOLL_TRY(check_extent(D, "D", kMaxWidth));
   const int es = elem_size(dtype), ts = elem_size(table_dtype);
   const size_t need = vcoll_embedding_backward_workspace_bytes(N, V, D);
   const Operand ops[] = {
@@ -390,7 +391,7 @@ static int norm_checks(int64_t N, int64_t D, int dtype, int weight_dtype) {
   VCOLL_TRY(check_type(dtype, "dtype"));
   VCOLL_TRY(check_type(weight_dtype, "weight dtype"));
   VCOLL_TRY(check_extent(N, "N"));
-  return check_extent(D, "D");
+  return check_extent(D, "D", kMaxWidth);
 }
 
 static int check_codes(const void* codes, int64_t codes_ld, int64_t N, int64_t D) {
@@ -531,15 +532,16 @@ static int norm_backward(const void* grad, int64_t grad_ld, const void* x, int64
                                           : norm_narrow_kernel_bf16(access, lanes, true, kept);
       VCOLL_TRY(launch_norm_narrow(fn, lanes, kNormMaxCtas, &p, stream, &p.parts));
     } else {
-    p.warps = s.warps;
-    access = row_access(access, access_of(ops[6], E), dtype);
-    const void* fn = dtype == VCOLL_F32 ? norm_rows_kernel_f32(access, s.chunks, s.threads, true, kept)
-                                        : norm_rows_kernel_bf16(access, s.chunks, s.threads, true, kept);
-    const size_t smem =
-        (size_t)s.threads * (norm_stages(s.chunks, E, true) * norm_grad_slot_bytes(s.chunks, E, kept) +
-                             norm_grad_smem_sums(s.chunks, E) * s.chunks * E * 4) +
-        s.threads / 2;
-    VCOLL_TRY(launch_norm_rows(fn, s, smem, kNormMaxCtas, &p, stream, &p.parts));
+      p.warps = s.warps;
+      access = row_access(access, access_of(ops[6], E), dtype);
+      const void* fn = dtype == VCOLL_F32
+                           ? norm_rows_kernel_f32(access, s.chunks, s.threads, true, kept)
+                           : norm_rows_kernel_bf16(access, s.chunks, s.threads, true, kept);
+      const size_t smem =
+          (size_t)s.threads * (norm_stages(s.chunks, E, true) * norm_grad_slot_bytes(s.chunks, E, kept) +
+                               norm_grad_smem_sums(s.chunks, E) * s.chunks * E * 4) +
+          s.threads / 2;
+      VCOLL_TRY(launch_norm_rows(fn, s, smem, kNormMaxCtas, &p, stream, &p.parts));
     }
   }
   if (!dweight && !dbias) return VCOLL_OK;

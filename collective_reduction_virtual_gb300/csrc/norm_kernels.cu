@@ -144,7 +144,8 @@ __global__ void __launch_bounds__(kRowThreads) vc_norm_wgrad_wide(const __grid_c
 // ------------------------------------------ the gradient's sum over the CTAs
 
 // part[cta][2][D] summed over the CTAs: a CTA per 32 columns of one of the
-// two; its warps take every 32nd row, and the first one adds up their sums.
+// two; its warps take every 32nd row, and each adds up one column's sums.  304
+// rows of 4096 columns: 5 us, from L2.
 __global__ void __launch_bounds__(1024) vc_norm_wsum(const __grid_constant__ NormParams p) {
   pdl_enter();
   __shared__ float sum[32][33];
@@ -169,7 +170,8 @@ __global__ void __launch_bounds__(1024) vc_norm_wsum(const __grid_constant__ Nor
 
 // ------------------------------------------------------- 8-bit activations
 // A warp takes kPackChunks chunks of 32 * E columns of a row, all of their
-// loads in flight.
+// loads in flight.  Bound by HBM: 9001 x 2052 fp32 kept and restored in 30 us,
+// 6.3 TB/s; 32768 x 4096 bf16 67 and 65 us, 6.0 and 6.2 TB/s.
 
 template <typename T, int A>
 __global__ void __launch_bounds__(kRowThreads) vc_pack8(const __grid_constant__ PackParams p) {
@@ -250,7 +252,8 @@ __global__ void __launch_bounds__(kRowThreads) vc_unpack8(const __grid_constant_
   else group(Bool<false>());
 }
 
-// Narrow rows, kNarrowRows of each group of G lanes in flight.
+// Narrow rows, kNarrowRows of each group of G lanes in flight (100000 x 64 bf16:
+// 5.5 and 5.6 us; a warp per row took 34 and 39).
 template <typename T, int A, int G>
 __global__ void __launch_bounds__(kRowThreads) vc_pack8_narrow(const __grid_constant__ PackParams p) {
   pdl_enter();

@@ -6,7 +6,9 @@
 // time, and kNarrowRows times that in one go: the loads of all of them are in
 // flight together, and their sums, a few shuffles each, overlap.  Weight and
 // bias stay in registers.  What bounds these kernels is the latency of such a
-// go; a warp of norm_rows.cuh would spend it on one row, most of its lanes idle.
+// go; a warp of norm_rows.cuh would spend it on one row, most of its lanes idle
+// (100000 x 64 bf16: 25.7 us forward and 30.0 backward; here 7.1 and 10.7).
+// 200000 x 128 bf16: 22 us forward, 4.7 TB/s, and 30 backward, 5.2 TB/s.
 #pragma once
 
 #include "layers_internal.h"

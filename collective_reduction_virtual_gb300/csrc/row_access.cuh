@@ -176,10 +176,10 @@ __device__ __forceinline__ void fetch_async(void* slot, const void* from) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at), "l"(from) : "memory");
   else if constexpr (BYTES == 4)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at), "l"(from) : "memory");
-  else if constexpr (BYTES == 2)  // below the smallest asynchronous copy
+  else {  // below the smallest asynchronous copy
+    static_assert(BYTES == 2, "");
     *static_cast<uint16_t*>(slot) = *static_cast<const uint16_t*>(from);
-  else
-    *static_cast<uint8_t*>(slot) = *static_cast<const uint8_t*>(from);
+  }
 }
 __device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>

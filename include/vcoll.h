@@ -341,7 +341,7 @@ int vcoll_sparse_allreduce_noalloc(const void* const* in, void* const* out, void
  * hold, and in addition:
  *  - A matrix of N rows and D columns is a pointer and a row stride `*_ld`
  *    in elements (>= D; rows may be parts of wider rows); its columns are
- *    adjacent.  N, D, V up to 2^31 - 2 each; offsets are 64-bit.
+ *    adjacent.  N and V up to 2^31 - 2, D up to 2^30; offsets are 64-bit.
  *  - Buffers of one call may not overlap, except where a call names an
  *    in-place form; matrices that are different column ranges of the same
  *    wider rows (equal row strides in bytes) do not overlap.
