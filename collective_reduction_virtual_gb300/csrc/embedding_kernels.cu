@@ -598,12 +598,12 @@ __global__ void __launch_bounds__(kRowThreads) vc_embed_join(const __grid_consta
 }
 
 // ------------------------------------------------------------- short lists
-// Up to kSmallTokens tokens one launch does all, without a sort.  A warp per
+// A short list is not sorted, one launch does all.  A warp per
 // (place, tile of columns) reads the list: if an earlier place holds its token
 // it has nothing to do, else it sums the rows of the places that hold it, in
 // order.  Tokens of more than kSmallAlone places are summed by all warps of the
 // CTA, an eighth of the list each, and joined in order.  CTAs behind these fill
-// the rows of absent tokens, a row a warp.
+// the rows of absent tokens, p.fill_each a CTA.
 
 namespace {
 
@@ -648,22 +648,23 @@ __global__ void __launch_bounds__(kRowThreads) vc_embed_grad_small(const __grid_
   pdl_enter();
   constexpr int E = kLane<T>, NW = kRowThreads / 32;
   __shared__ int32_t list[kSmallTokens];  // -1: outside the table
-  __shared__ uint32_t met;  // of the CTA's rows, those whose tokens occur
+  __shared__ uint32_t met[2];  // of the CTA's rows, those whose tokens occur
   __shared__ int32_t shared_token[NW];  // -1: nothing left for the CTA to do
   __shared__ float part[NW][32 * E];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = (int)p.N;
   const bool fills = (int64_t)blockIdx.x >= p.sum_ctas;
-  const int64_t first = ((int64_t)blockIdx.x - p.sum_ctas) * NW;
-  if (threadIdx.x == 0) met = 0u;
+  const int64_t first = ((int64_t)blockIdx.x - p.sum_ctas) * p.fill_each;
+  if (threadIdx.x < 2) met[threadIdx.x] = 0u;
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += kRowThreads) {
     const int64_t t = token_at(p.tokens, p.idx64, i);
     list[i] = t >= 0 && t < p.V ? (int32_t)t : -1;
-    if (fills && t >= first && t < first + NW) atomicOr(&met, 1u << (t - first));
+    if (fills && t >= first && t < first + p.fill_each) atomicOr(&met[(t - first) >> 5], 1u << ((t - first) & 31));
   }
   __syncthreads();
   if (fills) {
-    if (first + warp < p.V && !(met >> warp & 1)) fill_row(p, first + warp);
+    for (int r = warp; r < p.fill_each && first + r < p.V; r += NW)
+      if (!(met[r >> 5] >> (r & 31) & 1)) fill_row(p, first + r);
     return;
   }
   // units a CTA apart: the tiles of a frequent token's place go to different

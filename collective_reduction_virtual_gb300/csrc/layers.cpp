@@ -209,6 +209,12 @@ constexpr int64_t kSortOneCta = 2048;
 // what is written in the time that a pass takes.
 constexpr int64_t kFillPassBytes = 48 << 20;
 
+// Whether the list of the embedding's gradient is short enough not to be sorted:
+// a warp for each place and tile reads it.
+bool grad_is_short(int64_t N, int64_t D) {
+  return N <= kSmallTokens && N * N * ceil_div(D, 256) <= kSmallWork;
+}
+
 // The workspace of the embedding's gradient.
 struct GradLayout {
   int passes, bits;            // of the sort
@@ -277,7 +283,8 @@ int vcoll_embedding(const void* tokens, int index_type, int64_t N, const void* t
 }
 
 size_t vcoll_embedding_backward_workspace_bytes(int64_t N, int64_t V, int64_t D) {
-  if (N <= kSmallTokens || V <= 0 || D <= 0 || N > kMaxExtent || V > kMaxExtent || D > kMaxWidth)
+  if (N <= 0 || V <= 0 || D <= 0 || N > kMaxExtent || V > kMaxExtent || D > kMaxWidth ||
+      grad_is_short(N, D))
     return 0;
   return grad_layout(N, V, D).bytes;
 }
@@ -330,9 +337,11 @@ int vcoll_embedding_backward(const void* grad, int64_t grad_ld, int dtype, const
   for (const Operand* o = ops + 1; o < ops + 4; ++o) access = std::min(access, access_of(*o, E));
   p.tiles = ceil_div(D, 32 * E);
   auto kernel = [&](GradPart part) { return embed_grad_kernel(dtype, table_dtype, access, part); };
-  if (N <= kSmallTokens) {
+  if (grad_is_short(N, D)) {
     p.sum_ctas = ceil_div(N * p.tiles, kWarps);
-    return launch_grid(kernel(GRAD_SMALL), p.sum_ctas + (in_place ? 0 : ceil_div(V, kWarps)), 1,
+    // a row for each warp, or eight where there are rows for all SMs
+    p.fill_each = ceil_div(V, 8 * kWarps) >= 608 ? 8 * kWarps : kWarps;
+    return launch_grid(kernel(GRAD_SMALL), p.sum_ctas + (in_place ? 0 : ceil_div(V, p.fill_each)), 1,
                        kRowThreads, 0, &p, stream);
   }
   const GradLayout L = grad_layout(N, V, D);

@@ -39,10 +39,14 @@ constexpr int64_t kSortFineTile = 1024, kSortFineMost = 32768;
 constexpr int64_t kSortMinTile = 2048;
 constexpr int kSortMaxTiles = 128;
 constexpr int64_t kFillRows = 2;  // adjacent rows that a warp fills
-// Tokens up to which the list is not sorted.  Spread as in text, 4096 bf16
-// columns: 512 take 13 us without the sort and 19 us with it; at twice as many
-// the two meet (reading the list for each place grows with its square).
-constexpr int kSmallTokens = 512;
+// Lists that are not sorted: up to kSmallTokens tokens and, since a warp for each
+// place and 256 columns reads the list, kSmallWork of tokens squared times these
+// tiles.  In place, spread as in text, without and with the sort: 512 tokens of
+// 4096 columns 15 and 19 us, 1024 of 1024 14 and 20, 2048 of 256 17 and 23; past
+// it 768 of 4096 25 and 20, 2048 of 1024 28 and 22.  One token alone, the worst
+// for it: 2048 of 256 28 and 16.
+constexpr int kSmallTokens = 2048;
+constexpr int64_t kSmallWork = (int64_t)1 << 22;
 constexpr int kSmallAlone = 32;    // places of a token that one warp sums alone
 constexpr int64_t kJoinAlone = 16;  // partial rows that one warp adds up alone
 struct EmbedGradParams {
@@ -62,6 +66,7 @@ struct EmbedGradParams {
   int64_t tiles;      // column tiles
   int64_t sum_ctas;   // CTAs that sum
   int64_t fill_begin, fill_end;  // rows that a launch fills where their tokens are absent
+  int fill_each;      // rows of absent tokens that a CTA of the short lists looks after
   int fill_bytes;     // of an access of these: 16, 4 or 2
   int table_es;       // bytes of an element of the table
   int sort_tiles;

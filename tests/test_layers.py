@@ -116,6 +116,8 @@ def test_embedding_shapes_extreme_tokens_and_an_empty_table(v):
     (512, 300, 72, "one", "odd"), (512, 2000, 258, "skewed", "dense"), (513, 2000, 258, "one", "dense"),
     (4096, 9000, 24, "skewed", "dense"), (4097, 65, 24, "any", "slice"), (6000, 3, 1000, "any", "dense"),
     (5000, 40, 129, "none", "dense"), (70000, 513, 16, "skewed", "dense"),
+    (2048, 30, 256, "one", "dense"), (2048, 9000, 200, "skewed", "odd"), (2049, 300, 40, "any", "dense"),
+    (1500, 70000, 12, "skewed", "dense"), (1800, 500, 1030, "skewed", "dense"), (900, 12, 700, "skewed", "slice"),
 ])
 def test_embedding_backward(v, dtype, table_dtype, n, V, d, kind, layout):
     g = gen(n + V + d)
