@@ -360,9 +360,8 @@ __global__ void __launch_bounds__(kSortThreads)
 // that began in an earlier chunk goes to the chunk's first partial row (fp32),
 // of one that goes on in the next to its second, and vc_embed_join adds these
 // up in order.  The work is even however the tokens are spread.  Bound by HBM:
-// 262144 rows of 4096 bf16 into 128000, spread as in text, 489 us, 5.9 TB/s with
-// the fill; 16384 rows of 2048 into 32000 of fp32, 41 us, 5 TB/s; rows of odd
-// width, in 4-byte accesses, 4 TB/s.
+// 262144 rows of 4096 bf16 into 128000, spread as in text, 480 us, 5.9 TB/s with
+// the fill; rows of odd width, in 4-byte accesses, 4 to 5 TB/s.
 
 namespace {
 

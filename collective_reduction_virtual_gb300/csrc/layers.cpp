@@ -205,9 +205,10 @@ int row_access(int a, int b, int dtype) {
 // less than many CTAs take).
 constexpr int64_t kSortOneCta = 2048;
 
-// Bytes of absent rows that are filled beside each pass of the sort, about
-// what is written in the time that a pass takes.
-constexpr int64_t kFillPassBytes = 48 << 20;
+// Bytes that are moved for absent rows beside each pass of the sort and beside
+// the join, about what the time that these take allows (16384 tokens into 32000
+// x 2048 fp32: 70 us with 64 MB, 74 with 48, 77 with 96).
+constexpr int64_t kFillPassBytes = 64 << 20;
 
 // Whether the list of the embedding's gradient is short enough not to be sorted:
 // a warp for each place and tile reads it.
@@ -230,9 +231,9 @@ GradLayout grad_layout(int64_t N, int64_t V, int64_t D) {
   L.sort_tile = std::max(N <= kSortFineMost ? kSortFineTile : kSortMinTile,
                          ceil_div(ceil_div(N, kSortMaxTiles), 32) * 32);
   // Places per warp: enough chunks for two waves of 32 warps on 152 SMs, each
-  // of 32 places at least (partial rows are traffic) and 256 at most.
+  // of 16 places at least (partial rows are traffic) and 256 at most.
   const int64_t tiles = ceil_div(D, 256);
-  L.chunk = std::min<int64_t>(256, std::max<int64_t>(1, ceil_div(N * tiles, 2 * 32 * 152 * 32)) * 32);
+  L.chunk = std::min<int64_t>(256, std::max<int64_t>(1, ceil_div(N * tiles, 2 * 32 * 152 * 16)) * 16);
   L.list = align256((size_t)N * sizeof(uint32_t));
   L.cnt = 4 * L.list;
   L.stamp = L.cnt;
@@ -361,13 +362,12 @@ int vcoll_embedding_backward(const void* grad, int64_t grad_ld, int dtype, const
   if (p.sum_ctas + ceil_div(V, kWarps * kFillRows) > 0x7FFFFFFF)
     return fail(VCOLL_ERR_UNSUPPORTED, "%lld rows of %lld columns are too many", (long long)N,
                 (long long)D);
-  // Rows of absent tokens are filled beside the sort's passes, kFillPassBytes
-  // each, and beside the join, half as many; the others beside the sums.  In
-  // place all of them stay.
+  // Rows of absent tokens are filled beside the sort's passes and the join,
+  // kFillPassBytes each, the others beside the sums.  In place all of them stay.
   const bool join = N > p.chunk;  // a token may reach a second chunk
-  const int64_t share = std::max<int64_t>(1, kFillPassBytes / (D * ts));
+  const int64_t share = std::max<int64_t>(1, kFillPassBytes / (D * ts * (base ? 2 : 1)));
   const int64_t early = N <= kSortOneCta ? 0 : std::min(V, p.passes * share);
-  const int64_t last = in_place || !join ? V : V - std::min(V - early, share / 2);  // the join's first
+  const int64_t last = in_place || !join ? V : V - std::min(V - early, share);  // the join's first
   p.fill_end = in_place ? V : 0;  // rows filled so far
   // the next `count` rows, and CTAs of `warps` warps for them
   auto take = [&](int64_t count, int64_t end, int64_t warps) {
