@@ -29,7 +29,6 @@ struct EmbedParams {
 // radix sort; tokens outside [0, V) sort as V, behind all others.
 constexpr int kSortThreads = 1024;
 constexpr int kSortMaxBits = 9;  // digit width
-constexpr int kSortMaxPasses = 4;
 // Keys of a CTA where several sort: short lists are cut finer (8192 keys of
 // 128000 tokens: 26.5 us a call with tiles of 1024, 27.1 of 2048, 33.0 of 4096;
 // 105491 keys: 43.8, 42.7 and 48.8), long ones into no more than 128 tiles,

@@ -801,3 +801,90 @@ def test_example_gradients_against_autograd(v):
         # rounding errors of half a step at most, about a third of that on average and unrelated
         # to one another: 1 / 254 of the top, 4 deviations, is 1.6 % of a typical value
         assert float((a.double() - b).norm() / b.norm()) < 0.016
+
+
+def _spot(r, t):
+    """A copy of a matrix at a random alignment and row stride."""
+    n, d = t.shape
+    pad, at = int(r.choice([0, 0, 0, 1, 2, 8, 24])), int(r.choice([0, 0, 1, 2, 3, 4, 8]))
+    flat = torch.empty(n * (d + pad) + at, dtype=t.dtype, device="cuda")
+    return flat[at:].view(n, d + pad)[:, :d].copy_(t)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("seed", range(60))
+def test_random_layer_norms(v, seed):
+    r = np.random.default_rng(seed)
+    g = gen(seed)
+    d = int(round(np.exp(r.uniform(0, np.log(20000)))))
+    n = int(min(round(np.exp(r.uniform(0, np.log(20000)))), max(1, 4_000_000 // d)))
+    dtype, wtype = TYPES[r.integers(2)], TYPES[r.integers(2)]
+    x = _spot(r, matrix(g, n, d, dtype, "dense", 2.0, float(r.choice([0.0, 1.0, -30.0]))))
+    grad = _spot(r, matrix(g, n, d, dtype))
+    w, b = (t if t is None or r.integers(2) else torch.cat([t[:1], t])[1:]
+            for t in weights(g, d, wtype, r.choice(["both", "both", "weight", "bias", "none"])))
+    w64 = w.double() if w is not None else torch.ones(d, device="cuda", dtype=torch.float64)
+    b64 = b.double() if b is not None else torch.zeros(d, device="cuda", dtype=torch.float64)
+    wy, wm, wr, h, bm, br, dh, by = R.norm(x.double(), w64, b64, float(np.float32(1e-5)))
+    y, mean, rstd = v.layer_norm(x, w, b, out=_spot(r, x))
+    close(mean, wm, bm + R.U * wm.abs(), torch.float32)
+    close(rstd, wr, wr * br, torch.float32)
+    close(y, wy, by, dtype)
+    y, rstd8, k = v.layer_norm_checkpoint8(x, w, b, out=_spot(r, x))
+    close(y, wy, by, dtype)
+    step = k.scales.double().repeat_interleave(128, 1)[:, :d]
+    kept = k.codes[:, :d].double() * step
+    assert ((kept - h).abs() <= 0.5 * step * (1 + 300 * R.U) + dh).all()
+    assert not k.codes[:, d:].any()
+    back = v.checkpoint8_restore(k, w, b, out=_spot(r, x))
+    close(back, kept * w64 + b64, 3 * R.U * ((kept * w64).abs() + b64.abs()), dtype)
+    wtype = w.dtype if w is not None else torch.float32
+    hx = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    for kept_form in (False, True):
+        want = R.norm_grad(grad.double(), kept if kept_form else hx,
+                           (rstd8 if kept_form else rstd).double(), w64)
+        if kept_form:
+            got = v.layer_norm_backward_checkpoint8(grad, k, rstd8, w, dx=_spot(r, x))
+        else:
+            got = v.layer_norm_backward(grad, x, mean, rstd, w, dx=_spot(r, x))
+        for a, c, e, t in zip(got, want[:3], want[3:], (dtype, wtype, wtype)):
+            close(a, c, e, t)
+    codes, scales = R.pack8(R.f64(x))
+    k = v.checkpoint8(x)
+    assert np.array_equal(k.codes[:, :d].cpu().numpy(), codes) and not k.codes[:, d:].any()
+    assert np.array_equal(k.scales.cpu().numpy(), scales)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("seed", range(60))
+def test_random_embeddings(v, seed):
+    r = np.random.default_rng(1000 + seed)
+    g = gen(1000 + seed)
+    d = int(round(np.exp(r.uniform(0, np.log(6000)))))
+    n = int(min(round(np.exp(r.uniform(0, np.log(60000)))), max(1, 4_000_000 // d)))
+    V = int(min(round(np.exp(r.uniform(0, np.log(300000)))), max(1, 6_000_000 // d)))
+    dtype, ttype = TYPES[r.integers(2)], TYPES[r.integers(2)]
+    tokens = tokens_of(g, n, V, str(r.choice(["any", "skewed", "skewed", "one", "none"])),
+                       torch.int32 if r.integers(2) else torch.int64)
+    scale = float(r.choice([1.0, 0.37, 45.25]))
+    t, s = tokens.long(), float(np.float32(scale))
+    inside = (t >= 0) & (t < V)
+    table = _spot(r, matrix(g, V, d, dtype))
+    out = v.embedding(tokens, table, scale=scale, out=_spot(r, torch.empty(n, d, dtype=dtype, device="cuda")))
+    want = table.double()[t.clamp(0, V - 1)] * s * inside[:, None]
+    assert torch.equal(out, want.float().to(dtype))
+    grad = _spot(r, matrix(g, n, d, dtype))
+    grad[~inside] = float("nan")  # rows of padding hold anything
+    base = _spot(r, matrix(g, V, d, ttype, "dense", 3.0)) if r.integers(3) else None
+    rows, g64 = t[inside], grad[inside].double()
+    total = torch.zeros(V, d, dtype=torch.float64, device="cuda").index_add_(0, rows, g64) * s
+    size = torch.zeros(V, d, dtype=torch.float64, device="cuda").index_add_(0, rows, g64.abs()) * abs(s)
+    count = torch.bincount(rows, minlength=V)[:, None].double()
+    want = total if base is None else base.double() + total
+    bound = (count + 4) * R.U * size + 2 * R.U * want.abs()
+    if base is not None and r.integers(2):
+        got = v.embedding_backward(grad, tokens, V, scale=scale, base=base, out=base)
+    else:
+        got = v.embedding_backward(grad, tokens, V, scale=scale, base=base,
+                                   out=_spot(r, torch.empty(V, d, dtype=ttype, device="cuda")))
+    close(got, want, bound, ttype)
