@@ -16,6 +16,7 @@ runs on.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple
 
 import torch
@@ -127,6 +128,10 @@ def vcoll_layer_norm_backward_checkpoint8(grad, grad_ld, codes, codes_ld, scales
 _TYPES = {torch.float32: F32, torch.bfloat16: BF16}
 _INDEX = {torch.int32: I32, torch.int64: I64}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# torch.empty without the dispatcher: after a launch it takes the host 1.5 us
+# where torch.empty takes 5.7 (a GB300's Grace CPU); absent, torch.empty it is
+_new_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None),
+                    "_empty_strided_cuda", None)
 
 
 def _refuse(message, status=ERR_INVALID_ARG):
@@ -141,12 +146,35 @@ def _handle(stream, device):
     return torch.cuda.current_stream().cuda_stream
 
 
+def _strides(shape):
+    strides, step = [], 1
+    for size in reversed(shape):
+        strides.append(step)
+        step *= size if size > 1 else 1
+    return tuple(reversed(strides))
+
+
 def _empty(shape, dtype, stream):
-    """A tensor allocated on the stream that the call runs on."""
-    if stream is None:
+    """A contiguous tensor allocated on the stream that the call runs on."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device="cuda")
+    if _new_cuda is None:
         return torch.empty(shape, dtype=dtype, device="cuda")
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device="cuda")
+    shape = tuple(shape)
+    n = len(shape)
+    return _new_cuda(shape, (1,) if n == 1 else (shape[1], 1) if n == 2 and shape[1] else
+                     _strides(shape), dtype)
+
+
+@functools.lru_cache(maxsize=256)
+def _embedding_need(N, vocab, D):
+    return _fn("vcoll_embedding_backward_workspace_bytes")(N, vocab, D)
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_need(N, D):
+    return _fn("vcoll_layer_norm_workspace_bytes")(N, D)
 
 
 def _dtype(t, what):
@@ -217,7 +245,7 @@ def _workspace(given, need, device, stream):
     if given is None:
         if not need:
             return 0, 0, None
-        given = _empty(need, torch.uint8, stream)
+        given = _empty((need,), torch.uint8, stream)
         return given.data_ptr(), need, given
     if given.get_device() != device:
         _place(given, "workspace", device)
@@ -263,6 +291,7 @@ def embedding_backward(grad, tokens, vocab, scale=1.0, base=None, out=None, dtyp
     grad's).  workspace: a uint8 CUDA tensor of embedding_workspace_bytes(N,
     vocab, D) bytes, allocated here when omitted."""
     device = torch.cuda.current_device()
+    vocab = int(vocab)
     index = _tokens(tokens, device)
     code = _dtype(grad, "grad")
     N, D, grad_ld = _rows(grad, "grad", device, None, tokens.numel())
@@ -282,7 +311,7 @@ def embedding_backward(grad, tokens, vocab, scale=1.0, base=None, out=None, dtyp
     table_code = _dtype(out, "out")
     if base is not None and base.dtype != out.dtype:
         _refuse(f"base is {base.dtype}, out {out.dtype}", ERR_INVALID_TYPE)
-    need = _fn("vcoll_embedding_backward_workspace_bytes")(N, vocab, D)
+    need = _embedding_need(N, vocab, D)
     ws, ws_bytes, _hold = _workspace(workspace, need, device, stream)
     rc = _fn("vcoll_embedding_backward")(grad.data_ptr(), grad_ld, code, tokens.data_ptr(), index,
                                          N, vocab, D, scale, base_ptr, base_ld, out.data_ptr(),
@@ -344,12 +373,12 @@ def _gradients(grad, weight, dx, dweight, dbias, weight_grads, N, D, device, str
     if dweight is not None:
         pw = _vector(dweight, "dweight", device, D, wtype)
     elif weight_grads:
-        dweight = _empty(D, wtype, stream)
+        dweight = _empty((D,), wtype, stream)
         pw = dweight.data_ptr()
     if dbias is not None:
         pb = _vector(dbias, "dbias", device, D, wtype)
     elif weight_grads:
-        dbias = _empty(D, wtype, stream)
+        dbias = _empty((D,), wtype, stream)
         pb = dbias.data_ptr()
     return w, wcode, dx, dx_ld, dweight, dbias, pw, pb
 
@@ -371,7 +400,7 @@ def layer_norm_backward(grad, x, mean, rstd, weight=None, dx=None, dweight=None,
     pr = _vector(rstd, "rstd", device, N, torch.float32)
     w, wcode, dx, dx_ld, dweight, dbias, pw, pb = _gradients(
         grad, weight, dx, dweight, dbias, weight_grads, N, D, device, stream)
-    need = _fn("vcoll_layer_norm_workspace_bytes")(N, D)
+    need = _norm_need(N, D)
     ws, ws_bytes, _hold = _workspace(workspace, need, device, stream)
     rc = _fn("vcoll_layer_norm_backward")(grad.data_ptr(), grad_ld, x.data_ptr(), x_ld, pm, pr, w,
                                           wcode, N, D, dx.data_ptr(), dx_ld, pw, pb, code, ws,
@@ -480,7 +509,7 @@ def layer_norm_backward_checkpoint8(grad, kept, rstd, weight=None, dx=None, dwei
     pr = _vector(rstd, "rstd", device, N, torch.float32)
     w, wcode, dx, dx_ld, dweight, dbias, pw, pb = _gradients(
         grad, weight, dx, dweight, dbias, weight_grads, N, D, device, stream)
-    need = _fn("vcoll_layer_norm_workspace_bytes")(N, D)
+    need = _norm_need(N, D)
     ws, ws_bytes, _hold = _workspace(workspace, need, device, stream)
     rc = _fn("vcoll_layer_norm_backward_checkpoint8")(
         grad.data_ptr(), grad_ld, codes, codes_ld, scales, pr, w, wcode, N, D, dx.data_ptr(),
