@@ -264,15 +264,34 @@ __global__ void __launch_bounds__(kSortThreads) vc_embed_sort(const __grid_const
   }
 }
 
+// Rows of the gradient on their way to L2 while the sort takes its time: every
+// row is read by the sums that follow.  A lane asks for kPrefetchLines lines of
+// 128 bytes, those of p.row_lines a row.
+__device__ __forceinline__ void prefetch_rows(const EmbedGradParams& p, int64_t cta) {
+  const int64_t first = p.line_begin + cta * (kSortThreads * kPrefetchLines) + threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < kPrefetchLines; ++k) {
+    const int64_t line = first + k * kSortThreads;
+    if (line >= p.line_end) return;
+    const RowPiece at(line, p.row_lines);
+    const int64_t byte = min(at.piece * 128, p.D * p.grad_es - 1);
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p.grad) + at.row * p.grad_ld * p.grad_es + byte));
+  }
+}
+
 // The sort in one launch per pass, a CTA per tile, after one that counts the
 // first digit.  cnt[pass][tile][digit] are the tiles' counts.
 __global__ void __launch_bounds__(kSortThreads) vc_embed_count(const __grid_constant__ EmbedGradParams p) {
   pdl_enter();
   extern __shared__ uint32_t count[];
   const int bins = 1 << p.bits;
+  if ((int)blockIdx.x >= p.sort_tiles) {
+    prefetch_rows(p, (int64_t)blockIdx.x - p.sort_tiles);
+    return;
+  }
   const int64_t lo = (int64_t)blockIdx.x * p.sort_tile;
   const int64_t hi = lo + p.sort_tile < p.N ? lo + p.sort_tile : p.N;
-  const size_t matrix = (size_t)gridDim.x * bins;
+  const size_t matrix = (size_t)p.sort_tiles * bins;
   for (int b = threadIdx.x; b < bins * (p.passes - 1); b += kSortThreads)
     p.cnt[(size_t)(1 + b / bins) * matrix + (size_t)blockIdx.x * bins + b % bins] = 0;
   // one stamp for each token of a tile's piece: as many stores to a frequent
@@ -307,7 +326,7 @@ __global__ void __launch_bounds__(kSortThreads) vc_embed_count(const __grid_cons
 // itself (it is read from L2), which saves a launch; the next pass's counts
 // are collected on the way, each pair's at the tile where it lands.  A pass
 // takes a few microseconds and hardly any bandwidth, so CTAs behind the tiles'
-// fill rows of absent tokens meanwhile.
+// fill rows of absent tokens meanwhile, or fetch rows of the gradient to L2.
 __global__ void __launch_bounds__(kSortThreads)
     vc_embed_scatter(const __grid_constant__ EmbedGradParams p) {
   pdl_enter();
@@ -315,6 +334,10 @@ __global__ void __launch_bounds__(kSortThreads)
   __shared__ uint32_t wsum[kSortWarps];
   __shared__ uint32_t sall[kSortThreads], sbefore[kSortThreads];
   const int pass = p.pass, bins = 1 << p.bits, tiles = p.sort_tiles;
+  if ((int)blockIdx.x >= tiles + p.fill_ctas) {
+    prefetch_rows(p, (int64_t)blockIdx.x - tiles - p.fill_ctas);
+    return;
+  }
   if ((int)blockIdx.x >= tiles) {
     fill_rows(p, p.fill_begin + ((int64_t)(blockIdx.x - tiles) * kSortWarps + (threadIdx.x >> 5)) * kFillRows);
     return;

@@ -209,6 +209,12 @@ constexpr int64_t kSortOneCta = 2048;
 // the join, about what the time that these take allows (16384 tokens into 32000
 // x 2048 fp32: 70 us with 64 MB, 74 with 48, 77 with 96).
 constexpr int64_t kFillPassBytes = 64 << 20;
+// Bytes of the gradient that are fetched to L2 (129 MB) meanwhile, at most, where
+// its rows have kPrefetchRow bytes or more: 65536 x 2048 bf16 into 8000 rows 94
+// us without, 90 with 32 MB, 87 with 64 and 89 with 96; 100000 rows of 512 bytes,
+// whose sums wait for other things, 45 without and 46 with any.
+constexpr int64_t kPrefetchBytes = 64 << 20;
+constexpr int64_t kPrefetchRow = 1024;
 
 // Whether the list of the embedding's gradient is short enough not to be sorted:
 // a warp for each place and tile reads it.
@@ -380,11 +386,22 @@ int vcoll_embedding_backward(const void* grad, int64_t grad_ld, int dtype, const
     VCOLL_TRY(launch_grid(embed_sort_kernel(), 1, 1, kSortThreads, smem, &p, stream));
   } else {
     p.sort_tiles = (int)ceil_div(N, L.sort_tile);
-    VCOLL_TRY(launch_grid(embed_count_kernel(), p.sort_tiles, 1, kSortThreads, smem, &p, stream));
+    // where there are no rows left to fill, rows of the gradient go to L2
+    p.grad_es = es;
+    p.row_lines = ceil_div(D * es, 128);
+    const int64_t lines = D * es < kPrefetchRow ? 0 : std::min(N * p.row_lines, kPrefetchBytes / 128);
+    auto fetch = [&](int64_t bytes) {
+      p.line_begin = p.line_end;
+      p.line_end = std::min(lines, p.line_begin + std::max<int64_t>(0, bytes) / 128);
+      return ceil_div(p.line_end - p.line_begin, kSortThreads * kPrefetchLines);
+    };
+    int64_t ahead = in_place || V < share ? fetch(kFillPassBytes / 2) : 0;
+    VCOLL_TRY(launch_grid(embed_count_kernel(), p.sort_tiles + ahead, 1, kSortThreads, smem, &p, stream));
     for (p.pass = 0; p.pass < p.passes; ++p.pass) {
-      const int64_t fill = take(share, last, kSortThreads / 32);
-      VCOLL_TRY(launch_grid(embed_scatter_kernel(), p.sort_tiles + fill, 1, kSortThreads, smem, &p,
-                            stream));
+      p.fill_ctas = (int)take(share, last, kSortThreads / 32);
+      ahead = fetch((share - (p.fill_end - p.fill_begin)) * D * ts);
+      VCOLL_TRY(launch_grid(embed_scatter_kernel(), p.sort_tiles + p.fill_ctas + ahead, 1,
+                            kSortThreads, smem, &p, stream));
     }
   }
   const int64_t fill = take(V, last, kWarps);

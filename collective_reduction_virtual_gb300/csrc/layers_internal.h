@@ -37,6 +37,7 @@ constexpr int kSortMaxBits = 9;  // digit width
 constexpr int64_t kSortFineTile = 1024, kSortFineMost = 32768;
 constexpr int64_t kSortMinTile = 2048;
 constexpr int kSortMaxTiles = 128;
+constexpr int kPrefetchLines = 4;  // that a lane fetches to L2
 constexpr int64_t kFillRows = 2;  // adjacent rows that a warp fills
 // Lists that are not sorted: up to kSmallTokens tokens and, since a warp for each
 // place and 256 columns reads the list, kSmallWork of tokens squared times these
@@ -68,7 +69,10 @@ struct EmbedGradParams {
   int fill_each;      // rows of absent tokens that a CTA of the short lists looks after
   int fill_bytes;     // of an access of these: 16, 4 or 2
   int table_es;       // bytes of an element of the table
-  int sort_tiles;
+  int sort_tiles, fill_ctas;  // CTAs of a pass that sort, and that fill
+  int64_t row_lines;             // lines of 128 bytes of a row of the gradient
+  int64_t line_begin, line_end;  // those that a launch fetches to L2
+  int grad_es;
   float scale;
   int idx64;
   int passes, bits, pass;
