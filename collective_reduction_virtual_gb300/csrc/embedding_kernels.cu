@@ -81,15 +81,15 @@ __device__ __forceinline__ void put_stamp(const EmbedGradParams& p, uint32_t key
   if (key < (uint32_t)p.V) p.stamp[key] = i;
 }
 
-// One warp writes base or zeros to those of kFillRows adjacent rows whose
-// tokens do not occur, eight accesses per lane in flight.  BYTES: of an access.
+// One warp writes base or zeros to the bytes begin .. end - 1 of those of
+// kFillRows adjacent rows whose tokens do not occur, eight accesses per lane in
+// flight.  BYTES: of an access.
 template <int BYTES>
-__device__ __forceinline__ void fill_pieces(const EmbedGradParams& p, int64_t v) {
+__device__ __forceinline__ void fill_pieces(const EmbedGradParams& p, int64_t v, int64_t begin, int64_t end) {
   using P = Raw<float, BYTES / 4>;
   const char* from = static_cast<const char*>(p.base) + v * p.base_ld * p.table_es;
   char* to = static_cast<char*>(p.out) + v * p.out_ld * p.table_es;
-  const int64_t end = p.D * p.table_es;
-  for (int64_t c0 = (threadIdx.x & 31) * BYTES; c0 < end; c0 += 8 * 32 * BYTES) {
+  for (int64_t c0 = begin + (threadIdx.x & 31) * BYTES; c0 < end; c0 += 8 * 32 * BYTES) {
     P r[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k)
@@ -101,37 +101,41 @@ __device__ __forceinline__ void fill_pieces(const EmbedGradParams& p, int64_t v)
   }
 }
 // two-byte pieces: rows of bf16 at odd places
-__device__ __forceinline__ void fill_halves(const EmbedGradParams& p, int64_t v) {
+__device__ __forceinline__ void fill_halves(const EmbedGradParams& p, int64_t v, int64_t begin, int64_t end) {
   using P = Raw<__nv_bfloat16, 1>;
   const char* from = elem_at<__nv_bfloat16>(p.base, v * p.base_ld);
   char* to = elem_at<__nv_bfloat16>(p.out, v * p.out_ld);
-  for (int64_t c0 = threadIdx.x & 31; c0 < p.D; c0 += 8 * 32) {
+  for (int64_t c0 = begin + (threadIdx.x & 31) * 2; c0 < end; c0 += 8 * 32 * 2) {
     P r[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (p.base && c0 + k * 32 < p.D) r[k].load_stream(from + (c0 + k * 32) * 2);
+      if (p.base && c0 + k * 64 < end) r[k].load_stream(from + c0 + k * 64);
       else r[k].zero();
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (c0 + k * 32 < p.D) r[k].store_stream(to + (c0 + k * 32) * 2);
+      if (c0 + k * 64 < end) r[k].store_stream(to + c0 + k * 64);
   }
 }
 
-__device__ __forceinline__ void fill_row(const EmbedGradParams& p, int64_t row) {
-  if (p.fill_bytes == 16) fill_pieces<16>(p, row);
-  else if (p.fill_bytes == 4) fill_pieces<4>(p, row);
-  else fill_halves(p, row);
+__device__ __forceinline__ void fill_row(const EmbedGradParams& p, int64_t row, int64_t begin, int64_t end) {
+  if (p.fill_bytes == 16) fill_pieces<16>(p, row, begin, end);
+  else if (p.fill_bytes == 4) fill_pieces<4>(p, row, begin, end);
+  else fill_halves(p, row, begin, end);
 }
 
-__device__ __forceinline__ void fill_rows(const EmbedGradParams& p, int64_t first) {
+// Unit: p.fill_piece bytes of kFillRows rows from p.fill_begin on.
+__device__ __forceinline__ void fill_rows(const EmbedGradParams& p, int64_t unit) {
   const int lane = threadIdx.x & 31;
+  const RowPiece at(unit, p.fill_pieces);
+  const int64_t first = p.fill_begin + at.row * kFillRows, begin = at.piece * p.fill_piece;
+  const int64_t end = min(begin + p.fill_piece, p.D * p.table_es);
   const int64_t v = first + lane;
   bool gone = lane < kFillRows && v < p.fill_end;
   if (gone && p.N) {
     const uint32_t i = p.stamp[v];
     gone = (int64_t)i >= p.N || token_at(p.tokens, p.idx64, i) != v;
   }
-  for (uint32_t m = __ballot_sync(~0u, gone); m; m &= m - 1) fill_row(p, first + __ffs(m) - 1);
+  for (uint32_t m = __ballot_sync(~0u, gone); m; m &= m - 1) fill_row(p, first + __ffs(m) - 1, begin, end);
 }
 
 }  // namespace
@@ -339,7 +343,7 @@ __global__ void __launch_bounds__(kSortThreads)
     return;
   }
   if ((int)blockIdx.x >= tiles) {
-    fill_rows(p, p.fill_begin + ((int64_t)(blockIdx.x - tiles) * kSortWarps + (threadIdx.x >> 5)) * kFillRows);
+    fill_rows(p, (int64_t)(blockIdx.x - tiles) * kSortWarps + (threadIdx.x >> 5));
     return;
   }
   const uint32_t* cnt = p.cnt + (size_t)pass * tiles * bins;
@@ -457,7 +461,7 @@ __global__ void __launch_bounds__(kRowThreads, A == kLane<T> ? 3 : 4)
   const int64_t fills = (int64_t)gridDim.x - p.sum_ctas;
   const int64_t fill = (int64_t)blockIdx.x * fills / gridDim.x;
   if (((int64_t)blockIdx.x + 1) * fills / gridDim.x != fill) {
-    fill_rows(p, p.fill_begin + (fill * (kRowThreads / 32) + (threadIdx.x >> 5)) * kFillRows);
+    fill_rows(p, fill * (kRowThreads / 32) + (threadIdx.x >> 5));
     return;
   }
   const int64_t unit = ((int64_t)blockIdx.x - fill) * (kRowThreads / 32) + (threadIdx.x >> 5);
@@ -550,7 +554,7 @@ __global__ void __launch_bounds__(kRowThreads) vc_embed_join(const __grid_consta
   const uint32_t* key = p.key[(p.passes + 1) & 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if ((int64_t)blockIdx.x >= p.sum_ctas) {  // hardly any bandwidth is used here either
-    fill_rows(p, p.fill_begin + (((int64_t)blockIdx.x - p.sum_ctas) * NW + warp) * kFillRows);
+    fill_rows(p, ((int64_t)blockIdx.x - p.sum_ctas) * NW + warp);
     return;
   }
   // units a CTA apart: those of one chunk, which a long token makes long, go to
@@ -686,7 +690,7 @@ __global__ void __launch_bounds__(kRowThreads) vc_embed_grad_small(const __grid_
   __syncthreads();
   if (fills) {
     for (int r = warp; r < p.fill_each && first + r < p.V; r += NW)
-      if (!(met[r >> 5] >> (r & 31) & 1)) fill_row(p, first + r);
+      if (!(met[r >> 5] >> (r & 31) & 1)) fill_row(p, first + r, 0, p.D * p.table_es);
     return;
   }
   // units a CTA apart: the tiles of a frequent token's place go to different

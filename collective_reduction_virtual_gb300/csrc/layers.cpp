@@ -209,6 +209,11 @@ constexpr int64_t kSortOneCta = 2048;
 // the join, about what the time that these take allows (16384 tokens into 32000
 // x 2048 fp32: 70 us with 64 MB, 74 with 48, 77 with 96).
 constexpr int64_t kFillPassBytes = 64 << 20;
+// Bytes of a row that a warp fills there, where few CTAs have little time, and
+// beside the sums (4096 tokens into 32000 x 5120 fp32: 120 us with 4096 and
+// 16384, 125 with 8192, 152 with whole rows; 262144 tokens into 128000 x 4096,
+// whose sums do most of the filling: 692 us, and 706 with 4096 there, too).
+constexpr int64_t kFillPiece = 4096, kFillPieceSums = 16384;
 // Bytes of the gradient that are fetched to L2 (129 MB) meanwhile, at most, where
 // its rows have kPrefetchRow bytes or more: 65536 x 2048 bf16 into 8000 rows 94
 // us without, 90 with 32 MB, 87 with 64 and 89 with 96; 100000 rows of 512 bytes,
@@ -365,7 +370,7 @@ int vcoll_embedding_backward(const void* grad, int64_t grad_ld, int dtype, const
   p.sort_tile = L.sort_tile;
   p.chunk = L.chunk;
   p.sum_ctas = ceil_div(ceil_div(N, p.chunk) * p.tiles, kWarps);
-  if (p.sum_ctas + ceil_div(V, kWarps * kFillRows) > 0x7FFFFFFF)
+  if (p.sum_ctas + ceil_div(ceil_div(V, kFillRows) * ceil_div(D * ts, kFillPiece), kWarps) > 0x7FFFFFFF)
     return fail(VCOLL_ERR_UNSUPPORTED, "%lld rows of %lld columns are too many", (long long)N,
                 (long long)D);
   // Rows of absent tokens are filled beside the sort's passes and the join,
@@ -376,10 +381,12 @@ int vcoll_embedding_backward(const void* grad, int64_t grad_ld, int dtype, const
   const int64_t last = in_place || !join ? V : V - std::min(V - early, share);  // the join's first
   p.fill_end = in_place ? V : 0;  // rows filled so far
   // the next `count` rows, and CTAs of `warps` warps for them
-  auto take = [&](int64_t count, int64_t end, int64_t warps) {
+  auto take = [&](int64_t count, int64_t end, int64_t warps, int64_t piece) {
+    p.fill_piece = piece;
+    p.fill_pieces = ceil_div(D * ts, piece);
     p.fill_begin = p.fill_end;
     p.fill_end = std::min(end, p.fill_begin + count);
-    return ceil_div(p.fill_end - p.fill_begin, warps * kFillRows);
+    return ceil_div(ceil_div(p.fill_end - p.fill_begin, kFillRows) * p.fill_pieces, warps);
   };
   const size_t smem = ((size_t)1 << kSortMaxBits) * (kSortThreads / 32) * sizeof(uint32_t);
   if (N <= kSortOneCta) {
@@ -398,17 +405,17 @@ int vcoll_embedding_backward(const void* grad, int64_t grad_ld, int dtype, const
     int64_t ahead = in_place || V < share ? fetch(kFillPassBytes / 2) : 0;
     VCOLL_TRY(launch_grid(embed_count_kernel(), p.sort_tiles + ahead, 1, kSortThreads, smem, &p, stream));
     for (p.pass = 0; p.pass < p.passes; ++p.pass) {
-      p.fill_ctas = (int)take(share, last, kSortThreads / 32);
+      p.fill_ctas = (int)take(share, last, kSortThreads / 32, kFillPiece);
       ahead = fetch((share - (p.fill_end - p.fill_begin)) * D * ts);
       VCOLL_TRY(launch_grid(embed_scatter_kernel(), p.sort_tiles + p.fill_ctas + ahead, 1,
                             kSortThreads, smem, &p, stream));
     }
   }
-  const int64_t fill = take(V, last, kWarps);
+  const int64_t fill = take(V, last, kWarps, kFillPieceSums);
   VCOLL_TRY(launch_grid(kernel(base ? GRAD_SUM_BASE : GRAD_SUM), p.sum_ctas + fill, 1, kRowThreads,
                         0, &p, stream));
   if (!join) return VCOLL_OK;
-  const int64_t rest = take(V, V, kWarps);
+  const int64_t rest = take(V, V, kWarps, kFillPiece);
   return launch_grid(kernel(GRAD_JOIN), p.sum_ctas + rest, 1, kRowThreads, 0, &p, stream);
 }
 

@@ -66,6 +66,7 @@ struct EmbedGradParams {
   int64_t tiles;      // column tiles
   int64_t sum_ctas;   // CTAs that sum
   int64_t fill_begin, fill_end;  // rows that a launch fills where their tokens are absent
+  int64_t fill_piece, fill_pieces;  // bytes of a row that a warp fills, and their number
   int fill_each;      // rows of absent tokens that a CTA of the short lists looks after
   int fill_bytes;     // of an access of these: 16, 4 or 2
   int table_es;       // bytes of an element of the table

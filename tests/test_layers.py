@@ -888,3 +888,26 @@ def test_random_embeddings(v, seed):
         got = v.embedding_backward(grad, tokens, V, scale=scale, base=base,
                                    out=_spot(r, torch.empty(V, d, dtype=ttype, device="cuda")))
     close(got, want, bound, ttype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ttype", TYPES)
+@pytest.mark.parametrize("n,V,d,layout", [
+    (2300, 400, 4097, "odd"), (2300, 700, 8200, "dense"), (2100, 300, 9001, "dense"),
+    (4200, 5000, 2050, "slice"), (2060, 1500, 17000, "dense"), (1500, 900, 6001, "odd"),
+])
+def test_absent_rows_of_wide_tables(v, ttype, n, V, d, layout):
+    """Rows that several warps fill, before, beside and after the sums."""
+    g = gen(n + V + d)
+    grad = matrix(g, n, d, torch.bfloat16)
+    base = matrix(g, V, d, ttype, layout, 3.0)
+    tokens = tokens_of(g, n, V, "skewed")
+    absent = torch.ones(V, dtype=torch.bool, device="cuda")
+    absent[tokens[(tokens >= 0) & (tokens < V)]] = False
+    assert absent.any()
+    for b in (None, base):
+        out = like(torch.full((V, d), float("nan"), dtype=ttype, device="cuda"), layout)
+        out.fill_(float("nan"))
+        assert v.embedding_backward(grad, tokens, V, base=b, out=out) is out
+        assert torch.equal(out[absent], base[absent] if b is not None else torch.zeros_like(base[absent]))
+        assert out.isfinite().all()
