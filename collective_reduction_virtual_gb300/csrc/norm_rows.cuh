@@ -18,7 +18,7 @@
 // the workspace (vc_norm_wsum adds these up).
 //
 // Measured: 32768 x 8192 bf16 forward 177 us, 6.1 TB/s, of which the measured
-// copy does 6.7; 32768 x 4096 bf16 backward 136 us and 5 for vc_norm_wsum, 5.9
+// copy does 6.7; 32768 x 4096 bf16 backward 134 us and 5 for vc_norm_wsum, 5.9
 // TB/s.  With the 8-bit form, 16384 x 4096 bf16, 62 and 75 us (5.4 and 4.5
 // TB/s): there the instructions that pack and unpack share the bound.  Two CTAs
 // of 256 threads are on an SM, held by 128 registers; at 80 both spill.
@@ -61,6 +61,14 @@ struct Team {
     b = warp_sum(o.y);
   }
 };
+
+// V adjacent sums, one store.
+template <int V>
+__device__ __forceinline__ void put_sums(float* to, const float* v) {
+  if constexpr (V == 4) *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
+  else if constexpr (V == 2) *reinterpret_cast<float2*>(to) = make_float2(v[0], v[1]);
+  else *to = *v;
+}
 
 // The ring starts as zeros: columns past a row's end are never fetched and
 // stay so.
@@ -358,16 +366,20 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
   if (col + P::kColumns <= D) work(Bool<true>());
   else work(Bool<false>());
   if (!p.part) return;
+  // rows of partial sums: stores of V adjacent columns (4096 x 4096 bf16: 24 us,
+  // and 31 with single ones, of which a warp's lie 32 bytes apart)
+  constexpr int V = A < 4 ? A : 4;
+  float* part = p.part + (size_t)blockIdx.x * 2 * D;
   if constexpr (SUMS) {  // one team, each thread its own columns
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
+      for (int e = 0; e < E; e += V) {
         const int at = c + P::offset(r, e);
         const float* own = reinterpret_cast<const float*>(sums + (r * E + e) / 4 * threads) + e % 4;
         if (at < D) {
-          p.part[(size_t)blockIdx.x * 2 * D + at] = *own;
-          p.part[(size_t)(blockIdx.x * 2 + 1) * D + at] = BOTH ? own[R * E * threads] : db[r][e];
+          put_sums<V>(part + at, own);
+          put_sums<V>(part + D + at, BOTH ? own + R * E * threads : &db[r][e]);
         }
       }
     return;
@@ -393,12 +405,17 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
         if (k + 1 < count) {
           *a = dw[r][e];
           *b = db[r][e];
-        } else {
-          const int at = c + P::offset(r, e);
-          if (at < D) {
-            p.part[(size_t)blockIdx.x * 2 * D + at] = dw[r][e];
-            p.part[(size_t)(blockIdx.x * 2 + 1) * D + at] = db[r][e];
-          }
+        }
+      }
+    if (k + 1 < count) continue;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < E; e += V) {
+        const int at = c + P::offset(r, e);
+        if (at < D) {
+          put_sums<V>(part + at, &dw[r][e]);
+          put_sums<V>(part + D + at, &db[r][e]);
         }
       }
   }
