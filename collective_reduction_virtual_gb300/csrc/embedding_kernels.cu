@@ -401,12 +401,33 @@ struct GradTile {
 
   __device__ __forceinline__ int64_t col(int j) const { return col0 + (j * 32 + lane) * A; }
 
+  // The lane's columns of the row at element `at` of a matrix.  Two-byte pieces,
+  // of which there are eight, are loaded without branches: past the row's end a
+  // lane takes the last column, whose sum it drops (50021 x 1001 bf16 in place in
+  // 49999 rows: 124 us, 226 with branches).
+  template <typename M>
+  __device__ __forceinline__ void load(const void* rows, int64_t at, Raw<M, A> (&r)[E / A]) const {
+    if constexpr (E / A == 8) {
+      const int64_t c = min(col(0), p.D - 1);
+      const int left = (int)min(p.D - 1 - c, (int64_t)(7 * 32));
+      const char* from = elem_at<M>(rows, at + c);
+#pragma unroll
+      for (int j = 0; j < E / A; ++j) r[j].load_stream(from + min(j * 32, left) * Elem<M>::kBytes);
+    } else {
+#pragma unroll
+      for (int j = 0; j < E / A; ++j) {
+        if (col(j) < p.D) r[j].load_stream(elem_at<M>(rows, at + col(j)));
+        else r[j].zero();
+      }
+    }
+  }
   // base[v] of the lane's columns, zeros where there is no base
   __device__ __forceinline__ void load_base(int64_t v, Raw<TO, A> (&b)[E / A]) const {
+    if (p.base) {
+      load<TO>(p.base, v * p.base_ld, b);
+    } else {
 #pragma unroll
-    for (int j = 0; j < E / A; ++j) {
-      if (p.base && col(j) < p.D) b[j].load_stream(elem_at<TO>(p.base, v * p.base_ld + col(j)));
-      else b[j].zero();
+      for (int j = 0; j < E / A; ++j) b[j].zero();
     }
   }
   // table_grad[v] = base[v] + scale * sum
@@ -446,10 +467,14 @@ struct GradTile {
 
 }  // namespace
 
+// CTAs that stay on an SM: rows of 16-byte accesses and of two-byte ones take
+// more registers (the latter 142 us with four, spilled, 124 with three).
+constexpr int grad_ctas(int A, int E) { return A == E || E / A == 8 ? 3 : 4; }
+
 // BASE: there is a base, whose rows are fetched with the rows that end a
 // token's sum; half as many rows are in flight then.
 template <typename T, typename TO, int A, bool BASE>
-__global__ void __launch_bounds__(kRowThreads, A == kLane<T> ? 3 : 4)
+__global__ void __launch_bounds__(kRowThreads, grad_ctas(A, kLane<T>))
     vc_embed_grad(const __grid_constant__ EmbedGradParams p) {
   pdl_enter();
   constexpr int E = kLane<T>;
@@ -500,10 +525,11 @@ __global__ void __launch_bounds__(kRowThreads, A == kLane<T> ? 3 : 4)
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t row = (int64_t)__shfl_sync(~0u, from, s + u) * p.grad_ld;
+        if (s + u < n) {
+          g.template load<T>(p.grad, row, r[u]);
+        } else {
 #pragma unroll
-        for (int j = 0; j < E / A; ++j) {
-          if (s + u < n && g.col(j) < p.D) r[u][j].load_stream(elem_at<T>(p.grad, row + g.col(j)));
-          else r[u][j].zero();
+          for (int j = 0; j < E / A; ++j) r[u][j].zero();
         }
       }
       if constexpr (BASE) {
@@ -646,11 +672,11 @@ __device__ __forceinline__ void sum_places(const GradTile<T, TO, A>& g, const in
       Raw<T, A> r[U][E / A];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t row = (int64_t)(i + __ffs(same) - 1) * g.p.grad_ld;
+        if (same) {
+          g.template load<T>(g.p.grad, (int64_t)(i + __ffs(same) - 1) * g.p.grad_ld, r[u]);
+        } else {
 #pragma unroll
-        for (int j = 0; j < E / A; ++j) {
-          if (same && g.col(j) < g.p.D) r[u][j].load_stream(elem_at<T>(g.p.grad, row + g.col(j)));
-          else r[u][j].zero();
+          for (int j = 0; j < E / A; ++j) r[u][j].zero();
         }
         same &= same - 1;
       }

@@ -29,9 +29,7 @@ struct Raw {
   // read once: evict first
   __device__ __forceinline__ void load_stream(const void* p) {
     if constexpr (kBytes == 2) {
-      uint16_t h;
-      asm volatile("ld.global.cs.u16 %0, [%1];" : "=h"(h) : "l"(p));
-      w[0] = h;
+      asm volatile("ld.global.cs.u16 %0, [%1];" : "=r"(w[0]) : "l"(p));  // zeros above
     } else if constexpr (kBytes == 4) {
       asm volatile("ld.global.cs.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
     } else if constexpr (kBytes == 8) {
