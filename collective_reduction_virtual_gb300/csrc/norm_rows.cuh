@@ -19,7 +19,7 @@
 //
 // Measured: 32768 x 8192 bf16 forward 177 us, 6.1 TB/s, of which the measured
 // copy does 6.7; 32768 x 4096 bf16 backward 131 us and 5 for vc_norm_wsum, 6.1
-// TB/s.  With the 8-bit form, 16384 x 4096 bf16, 62 and 68 us (5.4 and 4.9
+// TB/s.  With the 8-bit form, 16384 x 4096 bf16, 62 and 74 us (5.4 and 4.6
 // TB/s): there the instructions that pack and unpack share the bound.  Two CTAs
 // of 256 threads are on an SM, held by 128 registers; at 80 both spill.
 #pragma once
