@@ -343,6 +343,7 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
           fma2(s2x, s2y, f[r][e], f[r][e + 1], h[r][e], h[r][e + 1], s2x, s2y);
         }
       float s1 = warp_sum(s1x + s1y), s2 = warp_sum(s2x + s2y);
+      if constexpr (KEPT && A < E) __syncwarp();  // codes that other lanes have read
       fetch(s);  // the slot has been read
       s = s + 1 == S ? 0 : s + 1;
       if (!p.y) continue;
