@@ -222,8 +222,11 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
             const int from = col + (r * 32 + t.lane) * E;
             if (FULL || from < D) {
               // beside rows of single bf16 elements, which are copied at once, the
-              // codes are, too: an asynchronous copy behind those copies was lost
-              // in one build of this kernel
+              // codes are, too.  As asynchronous copies behind the others, four chunks
+              // a warp, the last chunk's landed in the slot of the second or the third
+              // (nvcc 13.0.88; other warps from run to run, with nothing else in
+              // flight), though two copies of 4 bytes, or the codes first, landed where
+              // they should: not a matter of the source's order
               if constexpr (P::BYTES < 4)
                 *reinterpret_cast<uint2*>(xslot + at + r * threads * E) =
                     *reinterpret_cast<const uint2*>(x + from);

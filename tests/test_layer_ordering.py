@@ -41,3 +41,30 @@ def test_every_row_meets_its_own_codes(dtype, ld, n, d):
         _, dw, db = vc.layer_norm_backward_checkpoint8(grad, kept, rstd)
         assert torch.equal(dw.double(), codes[:, :d].double().sum(0))
         assert (db == n).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,pad,at", [(torch.bfloat16, 0, 0), (torch.bfloat16, 2, 2), (torch.bfloat16, 1, 1),
+                                          (torch.float32, 0, 0), (torch.float32, 1, 1)])
+@pytest.mark.parametrize("d", [64, 128, 256, 512, 1024, 2048, 4096, 8192, 8704, 12288, 16384])
+def test_copies_land_in_their_own_slots(dtype, pad, at, d):
+    # codes and gradients that name their place among the columns that a warp copies: a copy that
+    # landed in another slot would bring another column's number
+    from collective_reduction_virtual_gb300 import build
+    build.build()
+    import collective_reduction_virtual_gb300 as vc
+    n = 3
+    col = torch.arange(d, device="cuda")
+    for code in (col // 8 % 128, col // 1024 % 128, (col + col // 128) % 113):
+        codes = code.to(torch.int8).repeat(n, 1)
+        kept = vc.Checkpoint8(codes, torch.ones(n, -(-d // 128), device="cuda"), torch.Size((n, d)))
+        flat = torch.zeros(n * (d + pad) + at, dtype=dtype, device="cuda")
+        grad = flat[at:].view(n, d + pad)[:, :d]
+        grad.copy_(1 + (col // 32 % 64) + torch.arange(n, device="cuda")[:, None])
+        x = flat.clone()[at:].view(n, d + pad)[:, :d]
+        x.copy_(code)
+        mean, rstd = torch.zeros(n, device="cuda"), torch.ones(n, device="cuda")
+        total, want = grad.double().sum(0), (grad.double() * code).sum(0)
+        for got in (vc.layer_norm_backward_checkpoint8(grad, kept, rstd),
+                    vc.layer_norm_backward(grad, x, mean, rstd)):
+            assert torch.equal(got[1].double(), want) and torch.equal(got[2].double(), total)
