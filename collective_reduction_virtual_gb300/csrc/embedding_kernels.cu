@@ -18,6 +18,7 @@ __global__ void __launch_bounds__(kRowThreads) vc_embed(const __grid_constant__ 
   if (piece.row >= p.N) return;
   const int64_t t = token_at(p.tokens, p.idx64, piece.row);
   const bool inside = t >= 0 && t < p.V;
+  const float scale = inside ? p.scale : 0.0f;  // zeros whatever p.scale is
   const int64_t c0 = piece.piece * (G * 32 * A) + (threadIdx.x & 31) * A;
   const char* from = elem_at<T>(p.table, (inside ? t * p.table_ld : 0) + c0);
   char* to = elem_at<T>(p.out, piece.row * p.out_ld + c0);
@@ -33,7 +34,7 @@ __global__ void __launch_bounds__(kRowThreads) vc_embed(const __grid_constant__ 
     float f[A];
     r[j].widen(f);
 #pragma unroll
-    for (int a = 0; a < A; ++a) f[a] = __fmul_rn(f[a], p.scale);
+    for (int a = 0; a < A; ++a) f[a] = __fmul_rn(f[a], scale);
     Raw<T, A> o;
     o.narrow(f);
     o.store_stream(elem_at<T>(to, j * 32 * A));
@@ -61,10 +62,11 @@ __global__ void __launch_bounds__(kRowThreads) vc_embed_narrow(const __grid_cons
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (first + u * S >= p.N) return;
+    const float scale = t[u] >= 0 && t[u] < p.V ? p.scale : 0.0f;  // zeros whatever p.scale is
     float f[E];
     Elem<T>::widen(raw[u], f);
 #pragma unroll
-    for (int e = 0; e < E; ++e) f[e] = __fmul_rn(f[e], p.scale);
+    for (int e = 0; e < E; ++e) f[e] = __fmul_rn(f[e], scale);
     g.store(elem_at<T>(p.out, (first + u * S) * p.out_ld), D, f);
   }
 }
