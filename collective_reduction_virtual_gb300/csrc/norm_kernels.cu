@@ -11,6 +11,34 @@ namespace vcoll {
 
 namespace {
 
+template <int K>
+struct Sums {
+  float v[K];
+  __device__ __forceinline__ Sums() {
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = 0.0f;
+  }
+};
+// each(i, part) for i = first, first + step, ... below end, kTerms of them with
+// the same part, whose sums it adds to and which are then added up in sum: n terms
+// in one chain are off by up to n u of the sum of their magnitudes, these by
+// kTerms + n / kTerms (u = 2^-24).  Eight terms' loads go out together: 20000 x
+// 16400 fp32 650 us forward and 1146 backward (one chain: 620 and 1575).
+template <int K, typename F>
+__device__ __forceinline__ Sums<K> long_sums(int64_t first, int64_t end, int step, F each) {
+  constexpr int kTerms = 64;
+  Sums<K> sum;
+  for (int64_t i = first; i < end;) {
+    Sums<K> part;
+    const int64_t stop = min(end, i + (int64_t)kTerms * step);
+#pragma unroll 8
+    for (; i < stop; i += step) each(i, part.v);
+#pragma unroll
+    for (int k = 0; k < K; ++k) sum.v[k] += part.v[k];
+  }
+  return sum;
+}
+
 // Sum over the CTA, the same in every thread.
 __device__ __forceinline__ float block_sum(float v, float* red) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -46,15 +74,14 @@ __global__ void __launch_bounds__(kRowThreads) vc_norm_wide(const __grid_constan
   __shared__ float red[kRowThreads / 32];
   for (int64_t i = blockIdx.x; i < p.N; i += gridDim.x) {
     const int64_t at = i * p.x_ld;
-    float sum = 0.0f;
-    for (int64_t c = threadIdx.x; c < p.D; c += kRowThreads) sum += load1<T>(p.x, at + c);
-    const float mean = block_sum(sum, red) / (float)p.D;
-    float sq = 0.0f;
-    for (int64_t c = threadIdx.x; c < p.D; c += kRowThreads) {
+    const Sums<1> sum = long_sums<1>(threadIdx.x, p.D, kRowThreads,
+                                     [&](int64_t c, float* s) { *s += load1<T>(p.x, at + c); });
+    const float mean = block_sum(sum.v[0], red) / (float)p.D;
+    const Sums<1> sq = long_sums<1>(threadIdx.x, p.D, kRowThreads, [&](int64_t c, float* s) {
       const float d = load1<T>(p.x, at + c) - mean;
-      sq += d * d;
-    }
-    const float rstd = rsqrtf(block_sum(sq, red) / (float)p.D + p.eps);
+      *s += d * d;
+    });
+    const float rstd = rsqrtf(block_sum(sq.v[0], red) / (float)p.D + p.eps);
     if (p.codes) {
       const int64_t blocks = (p.D + kBlock8 - 1) / kBlock8;
       for (int64_t b = threadIdx.x >> 5; b < blocks; b += kRowThreads / 32)
@@ -92,14 +119,13 @@ __global__ void __launch_bounds__(kRowThreads) vc_norm_grad_wide(const __grid_co
   __shared__ float red[kRowThreads / 32];
   for (int64_t i = blockIdx.x; i < p.N; i += gridDim.x) {
     const float mean = p.x ? p.mean[i] : 0.0f, rstd = p.rstd[i];
-    float s1 = 0.0f, s2 = 0.0f;
-    for (int64_t c = threadIdx.x; c < p.D; c += kRowThreads) {
+    const Sums<2> sum = long_sums<2>(threadIdx.x, p.D, kRowThreads, [&](int64_t c, float* s) {
       const float g = load1<T>(p.grad, i * p.grad_ld + c) * load_weight(p.weight, p.wbf16, c, 1.0f);
-      s1 += g;
-      s2 += g * normal_at<T>(p, i, c, mean, rstd);
-    }
-    s1 = block_sum(s1, red) / (float)p.D;
-    s2 = block_sum(s2, red) / (float)p.D;
+      s[0] += g;
+      s[1] += g * normal_at<T>(p, i, c, mean, rstd);
+    });
+    const float s1 = block_sum(sum.v[0], red) / (float)p.D;
+    const float s2 = block_sum(sum.v[1], red) / (float)p.D;
     for (int64_t c = threadIdx.x; c < p.D; c += kRowThreads) {
       const float g = load1<T>(p.grad, i * p.grad_ld + c) * load_weight(p.weight, p.wbf16, c, 1.0f);
       store1<T>(p.y, i * p.y_ld + c, (g - s1 - normal_at<T>(p, i, c, mean, rstd) * s2) * rstd);
@@ -116,18 +142,16 @@ __global__ void __launch_bounds__(kRowThreads) vc_norm_wgrad_wide(const __grid_c
   __shared__ float sw[NW][32], sb[NW][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
-  float dw = 0.0f, db = 0.0f;
-  if (c < p.D)
-    for (int64_t i = warp; i < p.N; i += NW) {
-      const float g = load1<T>(p.grad, i * p.grad_ld + c);
-      dw += g * normal_at<T>(p, i, c, p.x ? p.mean[i] : 0.0f, p.rstd[i]);
-      db += g;
-    }
-  sw[warp][lane] = dw;
-  sb[warp][lane] = db;
+  const Sums<2> sum = long_sums<2>(warp, c < p.D ? p.N : 0, NW, [&](int64_t i, float* s) {
+    const float g = load1<T>(p.grad, i * p.grad_ld + c);
+    s[0] += g * normal_at<T>(p, i, c, p.x ? p.mean[i] : 0.0f, p.rstd[i]);
+    s[1] += g;
+  });
+  sw[warp][lane] = sum.v[0];
+  sb[warp][lane] = sum.v[1];
   __syncthreads();
   if (warp || c >= p.D) return;
-  dw = db = 0.0f;
+  float dw = 0.0f, db = 0.0f;
   for (int k = 0; k < NW; ++k) {
     dw += sw[k][lane];
     db += sb[k][lane];

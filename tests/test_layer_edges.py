@@ -32,3 +32,47 @@ def test_padding_is_zero_whatever_the_scale(v, dtype, d, layout, scale):
     assert torch.equal(torch.nan_to_num(out[inside], 7.0), torch.nan_to_num(want, 7.0))
     bits = out[[1, 3, 5]].contiguous().view(torch.int32 if dtype == torch.float32 else torch.int16)
     assert not bits.any()  # +0
+
+
+# One value whose last bits a sum of many equal terms drops at every addition: the errors of a
+# chain all have the same sign, and grow with its length.  Sums in parts of 64 terms, m terms a
+# thread, are off by (64 + m / 64) u, and a few more where threads and warps are joined.
+BIASED = float(np.float32(1.0 + 0.99 * 2.0 ** -14))
+
+
+def test_one_chain_of_biased_terms_would_not_do():
+    terms = np.full(2500, BIASED, np.float32)
+    chain = np.cumsum(terms, dtype=np.float32)[-1]
+    parts = np.add.reduce([np.cumsum(terms[a:a + 64], dtype=np.float32)[-1] for a in range(0, 2500, 64)])
+    exact, bound = 2500 * BIASED, (64 + 2500 / 64 + 16) * R.U * 2500 * BIASED
+    assert abs(float(chain) - exact) > 2 * bound and abs(float(parts) - exact) <= bound
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [20000, 4001])
+def test_weight_gradients_of_wide_rows_over_many_rows(v, n):
+    d = 16400  # above what a team of warps holds
+    grad = torch.full((n, d), BIASED, device="cuda")
+    x = torch.ones(n, d, device="cuda")
+    x[:, 1::2] = -1.0
+    mean, rstd = torch.zeros(n, device="cuda"), torch.ones(n, device="cuda")
+    _, dw, db = v.layer_norm_backward(grad, x, mean, rstd, dx=grad)
+    bound = (64 + n / 8 / 64 + 16) * R.U * n * BIASED
+    assert ((db.double() - n * BIASED).abs() <= bound).all()
+    assert ((dw.double() - n * BIASED * x[0].double()).abs() <= bound).all()
+
+
+@pytest.mark.gpu
+def test_statistics_of_rows_of_millions(v):
+    n, d = 2, 2 ** 22
+    x = torch.full((n, d), BIASED, device="cuda")
+    bound = (64 + d / 256 / 64 + 24) * R.U * BIASED
+    _, mean, rstd = v.layer_norm(x)
+    assert ((mean.double() - BIASED).abs() <= bound).all()
+    # the gradient of equal values, with h = 0: what is left is the error of their mean
+    dx, _, _ = v.layer_norm_backward(x, torch.zeros_like(x), mean * 0, mean * 0 + 1)
+    assert (dx.double().abs() <= bound + 2 * R.U * BIASED).all()
+    # and of their squares: x of +-c has the variance c^2
+    x[:, 1::2] *= -1.0
+    _, _, rstd = v.layer_norm(x, eps=0.0)
+    assert ((rstd.double() * BIASED - 1.0).abs() <= 0.5 * (64 + d / 256 / 64 + 24) * R.U + 2.0 ** -22 + 4 * R.U).all()
