@@ -249,6 +249,8 @@ def _workspace(given, need, device, stream):
         return given.data_ptr(), need, given
     if given.get_device() != device:
         _place(given, "workspace", device)
+    if not given.is_contiguous():
+        _refuse("workspace is not contiguous")
     return given.data_ptr(), given.numel() * given.element_size(), given
 
 

@@ -76,3 +76,16 @@ def test_statistics_of_rows_of_millions(v):
     x[:, 1::2] *= -1.0
     _, _, rstd = v.layer_norm(x, eps=0.0)
     assert ((rstd.double() * BIASED - 1.0).abs() <= 0.5 * (64 + d / 256 / 64 + 24) * R.U + 2.0 ** -22 + 4 * R.U).all()
+
+
+def test_a_workspace_without_memory_of_its_own_is_refused(v):
+    # one byte seen many times, or bytes with gaps between them: its elements times their size say
+    # nothing about the memory behind it
+    from collective_reduction_virtual_gb300 import layers
+    host = -1  # get_device() of a host tensor
+    one = torch.empty(1, dtype=torch.uint8)
+    for given in (one.expand(4096), torch.empty(64, 64, dtype=torch.uint8)[:, ::2], torch.empty(8, 8).t()):
+        with pytest.raises(v.VcollError):
+            layers._workspace(given, 1024, host, None)
+    given = torch.empty(2048, dtype=torch.uint8)
+    assert layers._workspace(given, 1024, host, None)[:2] == (given.data_ptr(), 2048)
