@@ -117,6 +117,13 @@ __global__ void __launch_bounds__(kRowThreads, 2) vc_norm_grad_narrow(const __gr
           add2(h[u][e], h[u][e + 1], h[u][e], h[u][e + 1], -mean[u], -mean[u]);
           mul2(h[u][e], h[u][e + 1], h[u][e], h[u][e + 1], rstd[u], rstd[u]);
         }
+        // past the row's end h is -mean * rstd: where that is no finite number, 0
+        // times it would reach the row's sum
+        if (D < G * E && !isfinite(mean[u] * rstd[u])) {
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (g.c + P::offset(e) >= D) h[u][e] = 0.0f;
+        }
       }
     }
     // columns past the row's end, and rows past the last, have a gradient of 0

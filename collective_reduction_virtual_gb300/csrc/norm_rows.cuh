@@ -336,6 +336,18 @@ __global__ void __launch_bounds__(MT, MT == 256 ? 2 : 1)
           for (int e = 0; e < E; e += 2) add2(db[r][e], db[r][e + 1], db[r][e], db[r][e + 1], f[r][e], f[r][e + 1]);
         }
       }
+      if constexpr (!KEPT && !FULL) {
+        // past the row's end h is -mean * rstd: where that is no finite number, 0
+        // times it would reach the row's sum (one test a row: 8000 x 9001 fp32
+        // 280 us, 366 with a selection for each value)
+        if (!isfinite(mean * rstd)) {
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              if (!P::template inside<FULL>(r, e, c, D)) h[r][e] = 0.0f;
+        }
+      }
       P::template affine<FULL>(p.weight, nullptr, p.wbf16, c, D, f);  // g
       float s1x = 0.0f, s1y = 0.0f, s2x = 0.0f, s2y = 0.0f;
 #pragma unroll

@@ -89,3 +89,28 @@ def test_a_workspace_without_memory_of_its_own_is_refused(v):
             layers._workspace(given, 1024, host, None)
     given = torch.empty(2048, dtype=torch.uint8)
     assert layers._workspace(given, 1024, host, None)[:2] == (given.data_ptr(), 2048)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d,value,eps", [(100, 2.0 ** 120, 1e-5), (249, 2.0 ** 119, 1e-5), (24, -2.0 ** 121, 1e-5),
+                                         (300, 2.0 ** 112, 1e-12), (1001, 2.0 ** 112, 1e-12),
+                                         (1002, -2.0 ** 112, 1e-12), (2056, 2.0 ** 112, 1e-12),
+                                         (9001, 2.0 ** 110, 1e-12), (20001, 2.0 ** 110, 1e-12)])
+def test_gradient_of_rows_of_one_large_value(v, dtype, d, value, eps):
+    # h is 0 throughout, though mean * rstd is above the largest fp32: what a lane holds past the
+    # row's end, (0 - mean) * rstd, may not reach the sums
+    g = L.gen(d)
+    n = 5
+    x = torch.full((n, d), value, device="cuda", dtype=dtype)
+    x[3] = torch.randn(d, generator=g, device="cuda").to(dtype)
+    grad = L.matrix(g, n, d, dtype)
+    y, mean, rstd = v.layer_norm(x, eps=eps)
+    rows = [0, 1, 2, 4]
+    assert (mean[rows] == value).all() and not y[rows].any() and torch.isfinite(rstd).all()
+    dx, dw, db = v.layer_norm_backward(grad, x, mean, rstd)
+    h = torch.zeros(n, d, dtype=torch.float64, device="cuda")
+    h[3] = (x[3].double() - mean[3].double()) * rstd[3].double()
+    want = R.norm_grad(grad.double(), h, rstd.double(), torch.ones(d, dtype=torch.float64, device="cuda"))
+    for got, w, b, t in zip((dx, dw, db), want[:3], want[3:], (dtype, torch.float32, torch.float32)):
+        assert ((got.double() - w).abs() <= 1.01 * b + R.out_unit(t) * (w.abs() + b)).all()
