@@ -129,9 +129,25 @@ _TYPES = {torch.float32: F32, torch.bfloat16: BF16}
 _INDEX = {torch.int32: I32, torch.int64: I64}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 # torch.empty without the dispatcher: after a launch it takes the host 1.5 us
-# where torch.empty takes 5.7 (a GB300's Grace CPU); absent, torch.empty it is
+# where torch.empty takes 5.7 (a GB300's Grace CPU).  It is torch's own and may
+# change, so it is tried once before it is used (_sound), and torch.empty takes
+# its place where it is absent or does something else, and while a dispatch mode
+# is on, which has to see what is allocated.
 _new_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None),
                     "_empty_strided_cuda", None)
+_modes = getattr(torch._C, "_len_torch_dispatch_stack", None)
+_tried = False
+
+
+def _sound(new):
+    """Whether new(shape, strides, dtype) allocates what _empty needs."""
+    try:
+        t = new((2, 3), (3, 1), torch.bfloat16)
+        return (type(t) is torch.Tensor and t.shape == (2, 3) and t.stride() == (3, 1) and
+                t.dtype == torch.bfloat16 and t.is_cuda and
+                t.get_device() == torch.cuda.current_device() and not t.requires_grad)
+    except Exception:
+        return False
 
 
 def _refuse(message, status=ERR_INVALID_ARG):
@@ -159,7 +175,12 @@ def _empty(shape, dtype, stream):
     if stream is not None:
         with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device="cuda")
-    if _new_cuda is None:
+    global _new_cuda, _tried
+    if not _tried:
+        _tried = True
+        if _modes is None or (_new_cuda is not None and not _sound(_new_cuda)):
+            _new_cuda = None
+    if _new_cuda is None or _modes():
         return torch.empty(shape, dtype=dtype, device="cuda")
     shape = tuple(shape)
     n = len(shape)

@@ -114,3 +114,51 @@ def test_gradient_of_rows_of_one_large_value(v, dtype, d, value, eps):
     want = R.norm_grad(grad.double(), h, rstd.double(), torch.ones(d, dtype=torch.float64, device="cuda"))
     for got, w, b, t in zip((dx, dw, db), want[:3], want[3:], (dtype, torch.float32, torch.float32)):
         assert ((got.double() - w).abs() <= 1.01 * b + R.out_unit(t) * (w.abs() + b)).all()
+
+
+@pytest.mark.gpu
+def test_outputs_are_seen_by_a_dispatch_mode(v):
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    class Allocations(TorchDispatchMode):
+        def __init__(self):
+            super().__init__()
+            self.shapes = []
+
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            out = func(*args, **(kwargs or {}))
+            if "empty" in func.name():
+                self.shapes.append(tuple(out.shape))
+            return out
+
+    x = torch.randn(6, 96, device="cuda")
+    want = v.layer_norm(x)
+    with Allocations() as seen:
+        got = v.layer_norm(x)
+    assert sorted(seen.shapes) == [(6,), (6,), (6, 96)]
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_an_allocator_that_does_something_else_is_not_used(v):
+    from collective_reduction_virtual_gb300 import layers
+
+    def refuses(*args):
+        raise TypeError("three arguments")
+
+    # on the host, or nothing, or not as asked for
+    for new in (refuses, lambda s, t, d: None, lambda s, t, d: torch.empty(s, dtype=d),
+                lambda s, t, d: torch.empty(0)):
+        assert not layers._sound(new)
+
+
+@pytest.mark.gpu
+def test_the_allocator_is_tried(v):
+    from collective_reduction_virtual_gb300 import layers
+
+    def new(shape, strides, dtype, device="cuda"):
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+
+    assert layers._sound(new)
+    for other in (lambda s, t, d: new(s, (1, 2), d), lambda s, t, d: new(s, t, torch.float32),
+                  lambda s, t, d: new((3, 2), (2, 1), d), lambda s, t, d: new(s, t, d, "cpu")):
+        assert not layers._sound(other)
