@@ -347,8 +347,12 @@ int vcoll_sparse_allreduce_noalloc(const void* const* in, void* const* out, void
  *    wider rows (equal row strides in bytes) do not overlap.
  *  - Sums, means and statistics are fp32; a bf16 output is rounded once (a
  *    computed NaN is the canonical one of the conversion).
- *    The order of every sum is fixed by the sizes, the tokens and the GPU, so
- *    a call repeated on the same inputs gives the same bits.
+ *    The order of every sum is fixed by the sizes, the tokens and the GPU, in
+ *    the layer norms also by the alignment and the row strides of the operands
+ *    (weight and bias among them), which decide what columns a thread holds.
+ *    So a call repeated on the same buffers gives the same bits, but a layer
+ *    norm of the same values placed otherwise may differ in the last ones; the
+ *    lookup, its gradient and the 8-bit form alone do not.
  *  - `workspace`: device memory of the size the *_workspace_bytes function
  *    gives, 256-byte aligned, contents neither expected nor kept; calls that
  *    share one must not overlap.

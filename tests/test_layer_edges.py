@@ -162,3 +162,43 @@ def test_the_allocator_is_tried(v):
     for other in (lambda s, t, d: new(s, (1, 2), d), lambda s, t, d: new(s, t, torch.float32),
                   lambda s, t, d: new((3, 2), (2, 1), d), lambda s, t, d: new(s, t, d, "cpu")):
         assert not layers._sound(other)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,V,d", [(700, 90, 256), (5000, 300, 512), (40000, 9000, 64), (2100, 17, 1000)])
+def test_where_buffers_lie_does_not_change_lookups_and_codes(v, dtype, n, V, d):
+    g = L.gen(n + d)
+    tokens = L.tokens_of(g, n, V, "skewed")
+    grad, base, table = L.matrix(g, n, d, dtype), L.matrix(g, V, d, torch.float32), L.matrix(g, V, d, dtype)
+    k = v.checkpoint8(grad)
+    want = [v.embedding(tokens, table, 1.3), v.embedding_backward(grad, tokens, V, 0.7, base=base), k.codes, k.scales]
+    for layout in ("slice", "odd"):
+        def moved(t):
+            return L.like(t, layout).copy_(t)
+        gm, bm = moved(grad), moved(base)
+        k = v.checkpoint8(gm)
+        got = [v.embedding(tokens, moved(table), 1.3, out=L.like(want[0], layout)),
+               v.embedding_backward(gm, tokens, V, 0.7, base=bm, out=bm), k.codes, k.scales]
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [100, 1024, 1001, 9000, 40000])
+def test_layer_norms_repeat_their_bits_on_the_same_buffers(v, dtype, d):
+    g = L.gen(d)
+    x, grad = L.matrix(g, 300, d, dtype, "slice"), L.matrix(g, 300, d, dtype, "odd")
+    w, b = L.weights(g, d, dtype)
+
+    def run():
+        y, mean, rstd = v.layer_norm(x, w, b)
+        y8, rstd8, k = v.layer_norm_checkpoint8(x, w, b)
+        return [y, mean, rstd, y8, rstd8, k.codes, k.scales, *v.layer_norm_backward(grad, x, mean, rstd, w),
+                *v.layer_norm_backward_checkpoint8(grad, k, rstd8, w), v.checkpoint8_restore(k, w, b)]
+
+    want = run()
+    for _ in range(3):
+        for a, c in zip(run(), want):
+            assert torch.equal(a, c)
