@@ -470,7 +470,9 @@ struct GradTile {
 }  // namespace
 
 // CTAs that stay on an SM: rows of 16-byte accesses and of two-byte ones take
-// more registers (the latter 142 us with four, spilled, 124 with three).
+// more registers (the latter 142 us with four, 124 with three).  With a base,
+// whose rows are in flight as well, two-byte ones spill at three, too (about 280
+// bytes a thread), and bf16 pairs into fp32 at four (144).
 constexpr int grad_ctas(int A, int E) { return A == E || E / A == 8 ? 3 : 4; }
 
 // BASE: there is a base, whose rows are fetched with the rows that end a

@@ -20,8 +20,12 @@
 // Measured: 32768 x 8192 bf16 forward 177 us, 6.1 TB/s, of which the measured
 // copy does 6.7; 32768 x 4096 bf16 backward 131 us and 5 for vc_norm_wsum, 6.1
 // TB/s.  With the 8-bit form, 16384 x 4096 bf16, 62 and 74 us (5.4 and 4.6
-// TB/s): there the instructions that pack and unpack share the bound.  Two CTAs
-// of 256 threads are on an SM, held by 128 registers; at 80 both spill.
+// TB/s), issue at 57 and 51 %.  Two CTAs of 256 threads are on an SM, held by 128
+// registers; at 80 both spill.  Rows of 8 chunks a warp spill at 128, most of all
+// the fp32 gradient from 8 bits above 8192 columns (300 bytes a thread: 10007 x
+// 12288 314 us, 274 without the 8 bits).  Rows of single bf16 elements are copied
+// to the ring synchronously and wait for it: 100003 x 1001 192 us forward and 430
+// backward, three to five times what their bytes take.
 #pragma once
 
 #include "layers_internal.h"

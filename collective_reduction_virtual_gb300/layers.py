@@ -12,6 +12,11 @@ before it are its rows, which may be parts of wider rows (a column slice of a
 matrix is taken as it is, without a copy).  Outputs, and the workspaces that a
 call takes when it is given none, are allocated on the stream that the call
 runs on.
+
+As with the collectives, autograd does not see these calls: a tensor that
+requires grad is taken for its values, what comes back has no history, and an
+in-place output's version is not counted up.  The gradients are the ``*_backward``
+functions' to compute.
 """
 from __future__ import annotations
 
