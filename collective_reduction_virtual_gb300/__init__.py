@@ -604,9 +604,21 @@ _LAYERS = {"Checkpoint8", "checkpoint8", "checkpoint8_restore", "embedding", "em
            "CHECKPOINT8_BLOCK"}
 
 
+_PRODUCTS = {"cross_entropy", "cross_entropy_backward", "cross_entropy_backward_workspace_bytes",
+             "cross_entropy_workspace_bytes", "gated_ff", "gated_ff_backward",
+             "gated_ff_backward_workspace_bytes", "gated_ff_workspace_bytes",
+             "vcoll_cross_entropy", "vcoll_cross_entropy_backward",
+             "vcoll_cross_entropy_backward_workspace_bytes", "vcoll_cross_entropy_workspace_bytes",
+             "vcoll_gated_ff", "vcoll_gated_ff_backward", "vcoll_gated_ff_backward_workspace_bytes",
+             "vcoll_gated_ff_workspace_bytes", "SILU", "GELU", "GELU_TANH"}
+
+
 def __getattr__(name):
-    if name not in _LAYERS:
+    if name in _PRODUCTS:
+        from . import products as module
+    elif name in _LAYERS:
+        from . import layers as module
+    else:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import layers
-    value = globals()[name] = getattr(layers, name)
+    value = globals()[name] = getattr(module, name)
     return value

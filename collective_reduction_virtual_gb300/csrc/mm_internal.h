@@ -1,0 +1,122 @@
+// Products of two matrices with the element-wise part of an operator as their
+// epilogue (the loss against a vocabulary, the gated feed-forward block):
+// parameters shared by the host entry points (products.cpp) and the kernels.
+// Not part of the public ABI.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include "vcoll_internal.h"
+
+namespace vcoll {
+
+// What a tile of a product becomes.
+enum MmEpilogue : int {
+  MM_OUT = 0,    // stored, after what it is added to and its scale
+  MM_LSE = 1,    // each row's maximum and sum of exponentials, and its target's logit
+  MM_ERROR = 2,  // softmax minus one at the target, as bf16 parts
+  MM_GATED = 3,  // act(gate) * up, and where they are kept gate and up
+};
+
+// An operand in bf16: rows x cols, cols adjacent, rows ld apart.  fp32 values
+// stand as three such matrices ("parts", plane elements apart) that add up to
+// them.  The product sums over the columns of an operand, or over its rows
+// where it is taken transposed.
+struct MmOperand {
+  const void* p;
+  int64_t rows, cols, ld, plane;
+};
+
+struct MmParams {
+  MmOperand a, b[2];
+  int64_t M, N;   // of a tile space: rows and columns of the result
+  int64_t K;      // length of the sum
+  int64_t K1;     // the sum's places from here on take b[1] (K: none)
+  int parts;      // 1, or 3: six products of the parts
+  int b_halves;   // the tile's columns are half b[0]'s and half b[1]'s (MM_GATED)
+  int tn;         // columns of a tile
+  int64_t tiles_m, tiles_n;
+  // MM_OUT
+  void* out;
+  int64_t out_ld;
+  const float* accum_in;  // fp32 sums so far, accum_ld apart
+  float* accum_out;       // instead of out
+  int64_t accum_ld;
+  const float* scale;     // one value, or NULL
+  const void* base;       // of out's type and stride base_ld
+  int64_t base_ld;
+  int out_f32;
+  // MM_LSE, MM_ERROR: column j is token token0 + j of V
+  const void* targets;
+  const float* dloss;
+  int64_t dloss_step;  // 0 or 1
+  const float* lse;
+  float2* part;        // tiles_n x M
+  float* picked;       // M: the target's logit
+  int64_t token0, V;
+  int idx64;
+  // MM_ERROR: bf16 parts; MM_GATED: out is h
+  void* error;
+  int64_t error_ld, error_plane;
+  void *gate, *up;
+  int64_t gate_ld, up_ld;
+  int act;
+};
+
+// The six products of three parts that reach an fp32 result's precision, the
+// small ones first: parts 0 and 2, 2 and 0, 1 and 1, 0 and 1, 1 and 0, 0 and 0.
+VCOLL_HD constexpr int mm_pairs(int parts) { return parts == 1 ? 1 : 6; }
+VCOLL_HD constexpr int mm_pair_a(int pairs, int q) { return pairs == 1 ? 0 : (0x010120 >> (4 * q)) & 15; }
+VCOLL_HD constexpr int mm_pair_b(int pairs, int q) { return pairs == 1 ? 0 : (0x001102 >> (4 * q)) & 15; }
+
+constexpr int kMmTileM = 128;
+constexpr int kMmSimpleTileN = 64;
+constexpr int kMmSimpleThreads = 256;
+
+// Rows as bf16 parts, masked rows as zeros.
+struct MmPackParams {
+  const void* src;
+  void* dst;
+  const void* targets;  // NULL: no row is masked
+  int64_t rows, cols, src_ld, dst_ld, plane;
+  int64_t V;
+  int idx64, src_f32, parts;
+};
+
+// Joins the tiles' maxima and sums of a piece of the vocabulary to those of
+// the pieces before, and after the last gives the loss.
+struct MmJoinParams {
+  const float2* part;  // tiles x N
+  float2* state;       // N: of the pieces before
+  const void* targets;
+  float *loss, *lse;
+  int64_t tiles, N, V;
+  int idx64, first, last;
+};
+
+// The largest magnitude of the loss's gradient over the rows that count.
+struct MmScaleParams {
+  const float* dloss;
+  const void* targets;
+  float* scale;
+  int64_t N, V, step;
+  int idx64;
+};
+
+// The gradients of gate and up, as bf16 parts beside each other.
+struct MmGatedGradParams {
+  const void *dh, *gate, *up;
+  void* dst;
+  int64_t N, F, dh_ld, gate_ld, up_ld;
+  int64_t dst_ld, half, plane;  // gate's at 0, up's at half
+  int f32, parts, act;
+};
+
+const void* mm_simple_kernel(int epilogue, bool a_mn);  // MM_OUT: b is taken transposed
+const void* mm_pack_kernel();
+const void* mm_join_kernel();
+const void* mm_scale_kernel();
+const void* mm_gated_grad_kernel();
+
+}  // namespace vcoll

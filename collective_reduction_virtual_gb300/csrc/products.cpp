@@ -1,0 +1,526 @@
+// Host side of the products declared in include/vcoll.h (the loss against a
+// vocabulary, the gated feed-forward block): argument checks, the workspace's
+// layout, pieces of the vocabulary, and launches.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "layer_checks.h"
+#include "mm_internal.h"
+
+using namespace vcoll;
+
+namespace {
+
+constexpr int64_t kPackBytes = 256 << 20;   // of a piece of the table, laid out
+constexpr int64_t kErrorBytes = 256 << 20;  // of the gradient's e for a piece
+constexpr int64_t kPartBytes = 128 << 20;   // of the loss's tiles of a piece
+constexpr int kPassThreads = 256;           // of the kernels of mm_parts.cu
+
+int64_t round_up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
+int parts_of(int dtype) { return dtype == VCOLL_F32 ? 3 : 1; }
+
+// Regions of a workspace, one after the other.
+struct Regions {
+  size_t bytes = 0;
+  size_t take(int64_t n) {
+    const size_t at = bytes;
+    bytes += align256((size_t)n);
+    return at;
+  }
+};
+
+// A matrix laid out as parts: rows of a multiple of 8 values.
+int64_t packed_bytes(int64_t rows, int64_t cols, int parts) {
+  return rows * round_up(cols, 8) * 2 * parts;
+}
+
+// Columns of a piece of the vocabulary: `fit` at most, whole tiles.
+int64_t piece_of(int64_t V, int64_t fit) {
+  return std::min(V, std::max<int64_t>(2048, fit / 256 * 256));
+}
+
+struct LossLayout {
+  int64_t piece, pieces;
+  size_t x, table, part, state, bytes;
+};
+LossLayout loss_layout(int64_t N, int64_t V, int64_t D, int dtype, bool direct) {
+  const int parts = parts_of(dtype);
+  LossLayout L;
+  int64_t fit = kPartBytes / (8 * std::max<int64_t>(N, 1)) * 256;
+  if (!direct) fit = std::min(fit, kPackBytes / std::max<int64_t>(1, packed_bytes(1, D, parts)));
+  L.piece = piece_of(V, fit);
+  L.pieces = std::max<int64_t>(1, L.piece ? ceil_div(V, L.piece) : 1);
+  Regions r;
+  L.x = r.take(direct ? 0 : packed_bytes(N, D, parts));
+  L.table = r.take(direct ? 0 : packed_bytes(L.piece, D, parts));
+  L.part = r.take(ceil_div(L.piece, kMmSimpleTileN) * N * (int64_t)sizeof(float2));
+  L.state = r.take(L.pieces > 1 ? N * (int64_t)sizeof(float2) : 0);
+  L.bytes = r.bytes;
+  return L;
+}
+
+struct LossGradLayout {
+  int64_t piece, pieces, error_ld;
+  size_t scale, x, table, error, accum, bytes;
+};
+LossGradLayout loss_grad_layout(int64_t N, int64_t V, int64_t D, int dtype, bool direct) {
+  const int parts = parts_of(dtype);
+  LossGradLayout L;
+  int64_t fit = kErrorBytes / (2 * parts * std::max<int64_t>(N, 1));
+  if (!direct) fit = std::min(fit, kPackBytes / std::max<int64_t>(1, packed_bytes(1, D, parts)));
+  L.piece = piece_of(V, fit);
+  L.pieces = std::max<int64_t>(1, L.piece ? ceil_div(V, L.piece) : 1);
+  L.error_ld = round_up(L.piece, 8);
+  Regions r;
+  L.scale = r.take(sizeof(float));
+  L.x = r.take(packed_bytes(N, D, parts));
+  L.table = r.take(direct ? 0 : packed_bytes(L.piece, D, parts));
+  L.error = r.take(N * L.error_ld * 2 * parts);
+  L.accum = r.take(L.pieces > 1 ? N * D * 4 : 0);
+  L.bytes = r.bytes;
+  return L;
+}
+
+struct GatedLayout {
+  int64_t half;  // backward: gate's columns, a whole number of tiles
+  size_t x, w_gate, w_up, grads, bytes;
+};
+GatedLayout gated_layout(int64_t N, int64_t D, int64_t F, int dtype, bool direct, bool backward) {
+  const int parts = parts_of(dtype);
+  GatedLayout L;
+  L.half = round_up(F, kMmTileM);
+  Regions r;
+  L.x = r.take(direct ? 0 : packed_bytes(N, D, parts));
+  L.w_gate = r.take(direct ? 0 : packed_bytes(F, D, parts));
+  L.w_up = r.take(direct ? 0 : packed_bytes(F, D, parts));
+  L.grads = r.take(backward ? packed_bytes(N, 2 * L.half, parts) : 0);
+  L.bytes = r.bytes;
+  return L;
+}
+
+// Whether the products can read the matrix where it lies.
+bool lies_direct(const void* p, int64_t rows, int64_t cols, int64_t ld, int dtype) {
+  if (!rows || !cols) return true;
+  if (dtype != VCOLL_BF16 || (uint64_t)p % 16 || (rows > 1 && ld % 8)) return false;
+  cudaPointerAttributes a;
+  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return false;
+  }
+  return a.type == cudaMemoryTypeDevice;
+}
+
+MmOperand operand(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t plane = 0) {
+  return {p, rows, cols, rows > 1 ? ld : round_up(std::max<int64_t>(cols, 1), 8), plane};
+}
+
+// Lays a matrix out as parts at `to`; rows whose target is outside [0, V) as
+// zeros where targets are given.
+int pack(const void* src, int64_t rows, int64_t cols, int64_t ld, int dtype, void* to,
+         const void* targets, int64_t V, int idx64, MmOperand* o, void* stream) {
+  MmPackParams p = {};
+  p.src = src;
+  p.dst = to;
+  p.targets = targets;
+  p.rows = rows;
+  p.cols = cols;
+  p.src_ld = ld;
+  p.dst_ld = round_up(cols, 8);
+  p.plane = rows * p.dst_ld;
+  p.V = V;
+  p.idx64 = idx64;
+  p.src_f32 = dtype == VCOLL_F32;
+  p.parts = parts_of(dtype);
+  *o = operand(to, rows, cols, p.dst_ld, p.plane);
+  if (!rows || !cols) return VCOLL_OK;
+  int sms = 0;
+  VCOLL_TRY(device_sms(&sms));
+  const int64_t grid = std::min<int64_t>(ceil_div(rows * ceil_div(cols, 4), kPassThreads), (int64_t)sms * 8);
+  return launch_grid(mm_pack_kernel(), grid, 1, kPassThreads, 0, &p, stream);
+}
+
+// The matrix where it lies, or laid out at `to`.
+int lay(const void* src, int64_t rows, int64_t cols, int64_t ld, int dtype, bool direct, void* to,
+        MmOperand* o, void* stream) {
+  if (!direct) return pack(src, rows, cols, ld, dtype, to, nullptr, 0, 0, o, stream);
+  *o = operand(src, rows, cols, ld);
+  return VCOLL_OK;
+}
+
+// out[i][j] = sum over k < K of a and b.
+int product(MmEpilogue epilogue, bool a_mn, MmParams* p, void* stream) {
+  p->tn = kMmSimpleTileN;
+  p->tiles_m = ceil_div(p->M, kMmTileM);
+  p->tiles_n = ceil_div(p->N, p->b_halves ? p->tn / 2 : p->tn);
+  if (!p->K1) p->K1 = p->K;
+  if (!p->tiles_m || !p->tiles_n) return VCOLL_OK;
+  if (p->tiles_m > 0x7FFFFFFF / p->tiles_n)
+    return fail(VCOLL_ERR_UNSUPPORTED, "%lld x %lld tiles are too many", (long long)p->tiles_m,
+                (long long)p->tiles_n);
+  return launch_grid(mm_simple_kernel(epilogue, a_mn), p->tiles_m * p->tiles_n, 1, kMmSimpleThreads,
+                     0, p, stream);
+}
+
+// Matrices of more values than any memory holds: their bytes fit 64 bits.
+constexpr double kMaxValues = 1125899906842624.0;  // 2^50
+int check_area(int64_t rows, int64_t cols, const char* what) {
+  if ((double)rows * (double)cols > kMaxValues)
+    return fail(VCOLL_ERR_UNSUPPORTED, "%s: %lld x %lld values are too many", what, (long long)rows,
+                (long long)cols);
+  return VCOLL_OK;
+}
+
+int check_loss(int dtype, int index_type, int64_t N, int64_t V, int64_t D) {
+  VCOLL_TRY(check_type(dtype, "dtype"));
+  if (index_type != VCOLL_I32 && index_type != VCOLL_I64)
+    return fail(VCOLL_ERR_INVALID_TYPE, "unknown index type %d", index_type);
+  VCOLL_TRY(check_extent(N, "N"));
+  VCOLL_TRY(check_extent(V, "V"));
+  VCOLL_TRY(check_extent(D, "D", kMaxWidth));
+  VCOLL_TRY(check_area(N, D, "x"));
+  return check_area(V, D, "table");
+}
+
+int check_gated(int dtype, int activation, int64_t N, int64_t D, int64_t F) {
+  VCOLL_TRY(check_type(dtype, "dtype"));
+  if (activation != VCOLL_SILU && activation != VCOLL_GELU && activation != VCOLL_GELU_TANH)
+    return fail(VCOLL_ERR_INVALID_OP, "unknown activation %d", activation);
+  VCOLL_TRY(check_extent(N, "N"));
+  VCOLL_TRY(check_extent(D, "D", kMaxWidth));
+  VCOLL_TRY(check_extent(F, "F", kMaxWidth));
+  VCOLL_TRY(check_area(N, D, "x"));
+  VCOLL_TRY(check_area(N, F, "h"));
+  return check_area(F, D, "w_gate");
+}
+
+// The workspace is there, is device memory, and overlaps no operand.
+int check_room(Operand* ops, int n, void* workspace, size_t bytes, size_t need) {
+  VCOLL_TRY(check_operands(ops, n));
+  VCOLL_TRY(check_workspace(workspace, bytes, need));
+  ops[n] = {"workspace", workspace, need ? 1 : 0, (int64_t)need, (int64_t)need, 1, true, nullptr};
+  VCOLL_TRY(check_operands(ops, n + 1));
+  if (!need) return VCOLL_OK;
+  cudaPointerAttributes a;
+  if (cudaPointerGetAttributes(&a, workspace) != cudaSuccess) {
+    (void)cudaGetLastError();
+    a.type = cudaMemoryTypeUnregistered;
+  }
+  if (a.type != cudaMemoryTypeDevice)
+    return fail(VCOLL_ERR_INVALID_ARG, "the workspace is not device memory");
+  return VCOLL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t vcoll_cross_entropy_workspace_bytes(int64_t N, int64_t V, int64_t D, int dtype, int direct) {
+  if (check_loss(dtype, VCOLL_I32, N, V, D) || !N) return 0;
+  const size_t least = dtype == VCOLL_F32 ? 0 : loss_layout(N, V, D, dtype, true).bytes;
+  return dtype == VCOLL_BF16 && direct ? least : std::max(least, loss_layout(N, V, D, dtype, false).bytes);
+}
+
+int vcoll_cross_entropy(const void* x, int64_t x_ld, const void* table, int64_t table_ld,
+                        const void* targets, int index_type, int64_t N, int64_t V, int64_t D,
+                        float* loss, float* lse, int dtype, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  VCOLL_TRY(check_loss(dtype, index_type, N, V, D));
+  const int es = elem_size(dtype);
+  Operand ops[6] = {{"x", x, N, D, x_ld, es, false, nullptr},
+                    {"table", table, N ? V : 0, D, table_ld, es, false, nullptr},
+                    {"targets", targets, N, 1, 1, index_type == VCOLL_I64 ? 8 : 4, false, nullptr},
+                    {"loss", loss, N ? 1 : 0, N, N, 4, true, nullptr},
+                    {"lse", lse, N ? 1 : 0, N, N, 4, true, nullptr}};
+  VCOLL_TRY(check_operands(ops, 5));
+  if (!N) return VCOLL_OK;
+  const bool x_direct = lies_direct(x, N, D, x_ld, dtype), t_direct = lies_direct(table, V, D, table_ld, dtype);
+  const LossLayout L = loss_layout(N, V, D, dtype, x_direct && t_direct);
+  VCOLL_TRY(check_room(ops, 5, workspace, workspace_bytes, L.bytes));
+  char* ws = (char*)workspace;
+  MmParams p = {};
+  VCOLL_TRY(lay(x, N, D, x_ld, dtype, x_direct, ws + L.x, &p.a, stream));
+  p.M = N;
+  p.K = D;
+  p.parts = parts_of(dtype);
+  p.targets = targets;
+  p.idx64 = index_type == VCOLL_I64;
+  p.V = V;
+  p.part = (float2*)(ws + L.part);
+  p.picked = loss;
+  MmJoinParams j = {};
+  j.part = p.part;
+  j.state = (float2*)(ws + L.state);
+  j.targets = targets;
+  j.idx64 = p.idx64;
+  j.loss = loss;
+  j.lse = lse;
+  j.N = N;
+  j.V = V;
+  for (int64_t i = 0; i < L.pieces; ++i) {
+    p.token0 = i * L.piece;
+    p.N = std::min(L.piece, V - p.token0);
+    VCOLL_TRY(lay((const char*)table + p.token0 * table_ld * es, p.N, D, table_ld, dtype, t_direct,
+                  ws + L.table, &p.b[0], stream));
+    VCOLL_TRY(product(MM_LSE, false, &p, stream));
+    j.tiles = p.tiles_n;
+    j.first = i == 0;
+    j.last = i == L.pieces - 1;
+    VCOLL_TRY(launch_grid(mm_join_kernel(), ceil_div(N, 32), 1, kPassThreads, 0, &j, stream));
+  }
+  return VCOLL_OK;
+}
+
+size_t vcoll_cross_entropy_backward_workspace_bytes(int64_t N, int64_t V, int64_t D, int dtype,
+                                                    int direct) {
+  if (check_loss(dtype, VCOLL_I32, N, V, D)) return 0;
+  const size_t least = dtype == VCOLL_F32 ? 0 : loss_grad_layout(N, V, D, dtype, true).bytes;
+  return dtype == VCOLL_BF16 && direct ? least
+                                       : std::max(least, loss_grad_layout(N, V, D, dtype, false).bytes);
+}
+
+int vcoll_cross_entropy_backward(const float* dloss, int64_t dloss_count, const void* x,
+                                 int64_t x_ld, const void* table, int64_t table_ld,
+                                 const void* targets, int index_type, const float* lse, int64_t N,
+                                 int64_t V, int64_t D, void* dx, int64_t dx_ld, const void* base,
+                                 int64_t base_ld, void* dtable, int64_t dtable_ld, int dtype,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  VCOLL_TRY(check_loss(dtype, index_type, N, V, D));
+  if (dloss_count != N && dloss_count != 1)
+    return fail(VCOLL_ERR_INVALID_ARG, "dloss_count = %lld is neither 1 nor N", (long long)dloss_count);
+  const int es = elem_size(dtype);
+  Operand ops[9] = {{"x", x, N, D, x_ld, es, false, nullptr},
+                    {"table", table, N ? V : 0, D, table_ld, es, false, nullptr},
+                    {"targets", targets, N, 1, 1, index_type == VCOLL_I64 ? 8 : 4, false, nullptr},
+                    {"dloss", dloss, N ? 1 : 0, dloss_count, dloss_count, 4, false, nullptr},
+                    {"lse", lse, N ? 1 : 0, N, N, 4, false, nullptr},
+                    {"base", base, base && dtable ? V : 0, D, base_ld, es, false, nullptr},
+                    {"dx", dx, dx ? N : 0, D, dx_ld, es, true, x},
+                    {"dtable", dtable, dtable ? V : 0, D, dtable_ld, es, true, base}};
+  VCOLL_TRY(check_operands(ops, 8));
+  if (!D || (!dx && !dtable)) return VCOLL_OK;
+  if (!N && base && base == dtable) return VCOLL_OK;
+  const bool direct = lies_direct(table, N ? V : 0, D, table_ld, dtype);
+  const LossGradLayout L = loss_grad_layout(N, V, D, dtype, direct);
+  VCOLL_TRY(check_room(ops, 8, workspace, workspace_bytes, L.bytes));
+  char* ws = (char*)workspace;
+  const int parts = parts_of(dtype), idx64 = index_type == VCOLL_I64;
+  float* scale = (float*)(ws + L.scale);
+  MmScaleParams s = {};
+  s.dloss = dloss;
+  s.targets = targets;
+  s.scale = scale;
+  s.N = N;
+  s.V = V;
+  s.step = dloss_count == 1 ? 0 : 1;
+  s.idx64 = idx64;
+  VCOLL_TRY(launch_grid(mm_scale_kernel(), 1, 1, 1024, 0, &s, stream));
+  MmOperand rows;  // x without the rows that do not count
+  VCOLL_TRY(pack(x, N, D, x_ld, dtype, ws + L.x, targets, V, idx64, &rows, stream));
+  for (int64_t i = 0; i < L.pieces; ++i) {
+    const int64_t v0 = i * L.piece, width = std::min(L.piece, V - v0);
+    MmOperand tokens = operand(table, 0, D, table_ld);
+    if (N)
+      VCOLL_TRY(lay((const char*)table + v0 * table_ld * es, width, D, table_ld, dtype, direct,
+                    ws + L.table, &tokens, stream));
+    const MmOperand error = operand(ws + L.error, N, width, L.error_ld, N * L.error_ld);
+    MmParams p = {};
+    p.a = rows;
+    p.b[0] = tokens;
+    p.M = N;
+    p.N = width;
+    p.K = D;
+    p.parts = parts;
+    p.targets = targets;
+    p.idx64 = idx64;
+    p.V = V;
+    p.token0 = v0;
+    p.dloss = dloss;
+    p.dloss_step = s.step;
+    p.lse = lse;
+    p.scale = scale;
+    p.error = ws + L.error;
+    p.error_ld = L.error_ld;
+    p.error_plane = N * L.error_ld;
+    VCOLL_TRY(product(MM_ERROR, false, &p, stream));
+    if (dx) {
+      MmParams q = {};
+      q.a = error;
+      q.b[0] = tokens;
+      q.M = N;
+      q.N = D;
+      q.K = width;
+      q.parts = parts;
+      q.scale = scale;
+      q.out = dx;
+      q.out_ld = dx_ld;
+      q.out_f32 = dtype == VCOLL_F32;
+      q.accum_ld = D;
+      if (i > 0) q.accum_in = (float*)(ws + L.accum);
+      if (i < L.pieces - 1) q.accum_out = (float*)(ws + L.accum);
+      VCOLL_TRY(product(MM_OUT, false, &q, stream));
+    }
+    if (dtable) {
+      MmParams q = {};
+      q.a = error;
+      q.b[0] = rows;
+      q.M = width;
+      q.N = D;
+      q.K = N;
+      q.parts = parts;
+      q.scale = scale;
+      q.out = (char*)dtable + v0 * dtable_ld * es;
+      q.out_ld = dtable_ld;
+      q.out_f32 = dtype == VCOLL_F32;
+      q.base = base ? (const char*)base + v0 * base_ld * es : nullptr;
+      q.base_ld = base_ld;
+      VCOLL_TRY(product(MM_OUT, true, &q, stream));
+    }
+  }
+  return VCOLL_OK;
+}
+
+size_t vcoll_gated_ff_workspace_bytes(int64_t N, int64_t D, int64_t F, int dtype, int direct) {
+  if (check_gated(dtype, VCOLL_SILU, N, D, F)) return 0;
+  return gated_layout(N, D, F, dtype, dtype == VCOLL_BF16 && direct, false).bytes;
+}
+
+int vcoll_gated_ff(const void* x, int64_t x_ld, const void* w_gate, int64_t w_gate_ld,
+                   const void* w_up, int64_t w_up_ld, int activation, int64_t N, int64_t D,
+                   int64_t F, void* h, int64_t h_ld, void* gate, int64_t gate_ld, void* up,
+                   int64_t up_ld, int dtype, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+  VCOLL_TRY(check_gated(dtype, activation, N, D, F));
+  const int es = elem_size(dtype);
+  const int64_t W = N ? F : 0;
+  Operand ops[7] = {{"x", x, F ? N : 0, D, x_ld, es, false, nullptr},
+                    {"w_gate", w_gate, W, D, w_gate_ld, es, false, nullptr},
+                    {"w_up", w_up, W, D, w_up_ld, es, false, nullptr},
+                    {"h", h, N, F, h_ld, es, true, nullptr},
+                    {"gate", gate, gate ? N : 0, F, gate_ld, es, true, nullptr},
+                    {"up", up, up ? N : 0, F, up_ld, es, true, nullptr}};
+  VCOLL_TRY(check_operands(ops, 6));
+  if (!N || !F) return VCOLL_OK;
+  const bool x_direct = lies_direct(x, N, D, x_ld, dtype), g_direct = lies_direct(w_gate, F, D, w_gate_ld, dtype),
+             u_direct = lies_direct(w_up, F, D, w_up_ld, dtype);
+  const GatedLayout L = gated_layout(N, D, F, dtype, x_direct && g_direct && u_direct, false);
+  VCOLL_TRY(check_room(ops, 6, workspace, workspace_bytes, L.bytes));
+  char* ws = (char*)workspace;
+  MmParams p = {};
+  VCOLL_TRY(lay(x, N, D, x_ld, dtype, x_direct, ws + L.x, &p.a, stream));
+  VCOLL_TRY(lay(w_gate, F, D, w_gate_ld, dtype, g_direct, ws + L.w_gate, &p.b[0], stream));
+  VCOLL_TRY(lay(w_up, F, D, w_up_ld, dtype, u_direct, ws + L.w_up, &p.b[1], stream));
+  p.M = N;
+  p.N = F;
+  p.K = D;
+  p.parts = parts_of(dtype);
+  p.b_halves = 1;
+  p.out = h;
+  p.out_ld = h_ld;
+  p.out_f32 = dtype == VCOLL_F32;
+  p.gate = gate;
+  p.gate_ld = gate_ld;
+  p.up = up;
+  p.up_ld = up_ld;
+  p.act = activation;
+  return product(MM_GATED, false, &p, stream);
+}
+
+size_t vcoll_gated_ff_backward_workspace_bytes(int64_t N, int64_t D, int64_t F, int dtype,
+                                               int direct) {
+  if (check_gated(dtype, VCOLL_SILU, N, D, F)) return 0;
+  return gated_layout(N, D, F, dtype, dtype == VCOLL_BF16 && direct, true).bytes;
+}
+
+int vcoll_gated_ff_backward(const void* dh, int64_t dh_ld, const void* x, int64_t x_ld,
+                            const void* w_gate, int64_t w_gate_ld, const void* w_up,
+                            int64_t w_up_ld, const void* gate, int64_t gate_ld, const void* up,
+                            int64_t up_ld, int activation, int64_t N, int64_t D, int64_t F,
+                            void* dx, int64_t dx_ld, void* dw_gate, int64_t dw_gate_ld,
+                            void* dw_up, int64_t dw_up_ld, int dtype, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  VCOLL_TRY(check_gated(dtype, activation, N, D, F));
+  const int es = elem_size(dtype);
+  const bool weights = dw_gate || dw_up;
+  Operand ops[10] = {{"dh", dh, N, F, dh_ld, es, false, nullptr},
+                     {"x", x, weights && F ? N : 0, D, x_ld, es, false, nullptr},
+                     {"w_gate", w_gate, dx && N ? F : 0, D, w_gate_ld, es, false, nullptr},
+                     {"w_up", w_up, dx && N ? F : 0, D, w_up_ld, es, false, nullptr},
+                     {"gate", gate, N, F, gate_ld, es, false, nullptr},
+                     {"up", up, N, F, up_ld, es, false, nullptr},
+                     {"dx", dx, dx ? N : 0, D, dx_ld, es, true, nullptr},
+                     {"dw_gate", dw_gate, dw_gate ? F : 0, D, dw_gate_ld, es, true, nullptr},
+                     {"dw_up", dw_up, dw_up ? F : 0, D, dw_up_ld, es, true, nullptr}};
+  VCOLL_TRY(check_operands(ops, 9));
+  if (!D || (!dx && !weights)) return VCOLL_OK;
+  const bool x_direct = !weights || lies_direct(x, F ? N : 0, D, x_ld, dtype),
+             g_direct = !dx || lies_direct(w_gate, N ? F : 0, D, w_gate_ld, dtype),
+             u_direct = !dx || lies_direct(w_up, N ? F : 0, D, w_up_ld, dtype);
+  const GatedLayout L = gated_layout(N, D, F, dtype, x_direct && g_direct && u_direct, true);
+  VCOLL_TRY(check_room(ops, 9, workspace, workspace_bytes, L.bytes));
+  char* ws = (char*)workspace;
+  const int parts = parts_of(dtype);
+  if (N && F) {
+    MmGatedGradParams g = {};
+    g.dh = dh;
+    g.gate = gate;
+    g.up = up;
+    g.dst = ws + L.grads;
+    g.N = N;
+    g.F = F;
+    g.dh_ld = dh_ld;
+    g.gate_ld = gate_ld;
+    g.up_ld = up_ld;
+    g.dst_ld = 2 * L.half;
+    g.half = L.half;
+    g.plane = N * 2 * L.half;
+    g.f32 = dtype == VCOLL_F32;
+    g.parts = parts;
+    g.act = activation;
+    int sms = 0;
+    VCOLL_TRY(device_sms(&sms));
+    VCOLL_TRY(launch_grid(mm_gated_grad_kernel(),
+                          std::min<int64_t>(ceil_div(N * L.half, kPassThreads), (int64_t)sms * 8), 1,
+                          kPassThreads, 0, &g, stream));
+  }
+  const MmOperand grads = operand(ws + L.grads, N, 2 * L.half, 2 * L.half, N * 2 * L.half);
+  if (dx) {
+    MmParams p = {};
+    p.a = grads;
+    VCOLL_TRY(lay(w_gate, N ? F : 0, D, w_gate_ld, dtype, g_direct, ws + L.w_gate, &p.b[0], stream));
+    VCOLL_TRY(lay(w_up, N ? F : 0, D, w_up_ld, dtype, u_direct, ws + L.w_up, &p.b[1], stream));
+    p.M = N;
+    p.N = D;
+    p.K = 2 * L.half;
+    p.K1 = L.half;
+    p.parts = parts;
+    p.out = dx;
+    p.out_ld = dx_ld;
+    p.out_f32 = dtype == VCOLL_F32;
+    VCOLL_TRY(product(MM_OUT, false, &p, stream));
+  }
+  if (weights) {
+    MmOperand rows;
+    VCOLL_TRY(lay(x, F ? N : 0, D, x_ld, dtype, x_direct, ws + L.x, &rows, stream));
+    for (int k = 0; k < 2; ++k) {
+      void* out = k ? dw_up : dw_gate;
+      if (!out) continue;
+      MmParams p = {};
+      p.a = grads;
+      p.a.p = ws + L.grads + (size_t)k * L.half * 2;
+      p.a.cols = F;
+      p.b[0] = rows;
+      p.M = F;
+      p.N = D;
+      p.K = N;
+      p.parts = parts;
+      p.out = out;
+      p.out_ld = k ? dw_up_ld : dw_gate_ld;
+      p.out_f32 = dtype == VCOLL_F32;
+      VCOLL_TRY(product(MM_OUT, true, &p, stream));
+    }
+  }
+  return VCOLL_OK;
+}
+
+}  // extern "C"

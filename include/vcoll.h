@@ -465,6 +465,91 @@ int vcoll_layer_norm_backward_checkpoint8(const void* grad, int64_t grad_ld, con
                                           void* dweight, void* dbias, int dtype, void* workspace,
                                           size_t workspace_bytes, void* stream);
 
+/*
+ * Products of a rank's rows with weights, with the element-wise part of the
+ * operator in the product's epilogue: the loss against a vocabulary and the
+ * gated feed-forward block.  The conventions of the layer operators hold, and
+ * in addition:
+ *  - bf16 products are exact and summed in fp32.  fp32 operands are taken as
+ *    three bf16 parts each, which together hold their 24 bits, in six products
+ *    summed in fp32; an infinite fp32 operand gives NaN.
+ *  - A bf16 matrix in device memory that starts at a 16-byte boundary, with a
+ *    row stride that is a multiple of 8, is read where it lies; any other, and
+ *    every fp32 one, is laid out in the workspace first.
+ *  - The *_workspace_bytes functions take `direct`: 1 where all the matrices
+ *    that the products read (x, table, w_gate, w_up) lie so; 0 always suffices.
+ *    The workspace is device memory.
+ *  - The order of a sum is fixed by the sizes, the type and the GPU.  Other
+ *    rows than a row's own do not touch its results.
+ */
+
+/*
+ * Softmax cross entropy of N rows against a table of V tokens, without keeping
+ * the logits z = x * table^T: lse[i] = log(sum over v of exp(z[i][v])), loss[i]
+ * = lse[i] - z[i][targets[i]].  A target outside [0, V) -- padding -- has loss
+ * 0.  x: N x D, table: V x D, both of dtype; loss, lse: N fp32.  V == 0: lse is
+ * -infinity.  D == 0: the logits are zeros.
+ */
+size_t vcoll_cross_entropy_workspace_bytes(int64_t N, int64_t V, int64_t D, int dtype, int direct);
+int vcoll_cross_entropy(const void* x, int64_t x_ld, const void* table, int64_t table_ld,
+                        const void* targets, int index_type, int64_t N, int64_t V, int64_t D,
+                        float* loss, float* lse, int dtype, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * Its gradient.  With e[i][v] = dloss[i] * (exp(z[i][v] - lse[i]) - (v ==
+ * targets[i])), and e[i] zeros where the target is outside [0, V) (whatever
+ * that row of x, its dloss and its lse hold): dx = e * table, dtable = base +
+ * e^T * x.  The logits are computed again, a piece of the vocabulary at a time.
+ * dloss: N fp32, or one for all rows (dloss_count N or 1).  base (V x D of
+ * dtype) may be NULL (zeros), or dtable itself with the same row stride; dx may
+ * be x with the same row stride.  dx and dtable may each be NULL (not wanted).
+ * With bf16 operands e is rounded to bf16 for the products, relative to the
+ * largest magnitude of dloss over the rows that count.
+ */
+size_t vcoll_cross_entropy_backward_workspace_bytes(int64_t N, int64_t V, int64_t D, int dtype,
+                                                    int direct);
+int vcoll_cross_entropy_backward(const float* dloss, int64_t dloss_count, const void* x,
+                                 int64_t x_ld, const void* table, int64_t table_ld,
+                                 const void* targets, int index_type, const float* lse, int64_t N,
+                                 int64_t V, int64_t D, void* dx, int64_t dx_ld, const void* base,
+                                 int64_t base_ld, void* dtable, int64_t dtable_ld, int dtype,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* Activation of a gated block: g / (1 + exp(-g)); g * Phi(g) with the normal
+ * distribution function Phi; g * (1 + tanh(sqrt(2 / pi) * (g + 0.044715 *
+ * g^3))) / 2. */
+typedef enum { VCOLL_SILU = 0, VCOLL_GELU = 1, VCOLL_GELU_TANH = 2 } vcoll_activation_t;
+
+/*
+ * Gated feed-forward block: gate = x * w_gate^T, up = x * w_up^T, h =
+ * act(gate) * up, computed from the unrounded gate and up.  x: N x D, w_gate,
+ * w_up: F x D, h, gate, up: N x F, all of dtype.  gate and up are kept for the
+ * backward pass; either may be NULL.  D == 0: zeros.
+ */
+size_t vcoll_gated_ff_workspace_bytes(int64_t N, int64_t D, int64_t F, int dtype, int direct);
+int vcoll_gated_ff(const void* x, int64_t x_ld, const void* w_gate, int64_t w_gate_ld,
+                   const void* w_up, int64_t w_up_ld, int activation, int64_t N, int64_t D,
+                   int64_t F, void* h, int64_t h_ld, void* gate, int64_t gate_ld, void* up,
+                   int64_t up_ld, int dtype, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/*
+ * Its gradient from the kept gate and up: dgate = dh * up * act'(gate), dup =
+ * dh * act(gate), dx = dgate * w_gate + dup * w_up, dw_gate = dgate^T * x,
+ * dw_up = dup^T * x.  With bf16 operands dgate and dup are rounded to bf16 for
+ * the products.  dx, dw_gate and dw_up may each be NULL (not wanted).
+ */
+size_t vcoll_gated_ff_backward_workspace_bytes(int64_t N, int64_t D, int64_t F, int dtype,
+                                               int direct);
+int vcoll_gated_ff_backward(const void* dh, int64_t dh_ld, const void* x, int64_t x_ld,
+                            const void* w_gate, int64_t w_gate_ld, const void* w_up,
+                            int64_t w_up_ld, const void* gate, int64_t gate_ld, const void* up,
+                            int64_t up_ld, int activation, int64_t N, int64_t D, int64_t F,
+                            void* dx, int64_t dx_ld, void* dw_gate, int64_t dw_gate_ld,
+                            void* dw_up, int64_t dw_up_ld, int dtype, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
 /* Device-side error bits, OR-ed into one word per device by the kernels.
  * The staged kernels bound every wait on their shared-memory barriers (2 s of
  * wall-clock time); a wait that gives up records VCOLL_DEVICE_ERR_TIMEOUT and
