@@ -16,7 +16,7 @@
 #include <mutex>
 #include <vector>
 
-#include "vcoll_internal.h"
+#include "mm_internal.h"
 
 using namespace vcoll;
 
@@ -1294,6 +1294,20 @@ int launch_grid(const void* fn, int64_t gx, int64_t gy, int threads, size_t smem
   }
   const cudaError_t e = launch_pdl(fn, dim3((unsigned)gx, (unsigned)gy), dim3((unsigned)threads),
                                    args, smem, (cudaStream_t)stream);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return cuda_fail(e, "kernel launch");
+  }
+  return VCOLL_OK;
+}
+
+int launch_tiles(const void* fn, int64_t grid, int threads, size_t smem, void* params,
+                 void* stream) {
+  void* args[] = {params};
+  int rc = allow_dynamic_smem(fn, smem);
+  if (rc) return rc;
+  const cudaError_t e = launch_pdl(fn, dim3((unsigned)grid), dim3((unsigned)threads), args, smem,
+                                   (cudaStream_t)stream);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return cuda_fail(e, "kernel launch");

@@ -11,8 +11,7 @@
 
 namespace vcoll {
 
-constexpr int kMmStagePitch = 33;
-constexpr int kMmStageWords = 32 * kMmStagePitch;  // fp32 words of a warp's block
+constexpr int kMmPitch = 33;
 
 __device__ __forceinline__ float mm_exp(float x) {  // e^x, to 2 ulp; 0 below 2^-126
   float y;
@@ -67,16 +66,20 @@ __device__ __forceinline__ void mm_act(int act, float g, float& s, float& ds) {
   }
 }
 
+__device__ __forceinline__ void mm_to_block(float* stage, int lane, const float (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) stage[lane * kMmPitch + j] = v[j];
+}
+
 // f(r, value) for the rows r < rows of the warp's block, lane = column.
 template <class F>
 __device__ __forceinline__ void mm_by_rows(float* stage, int lane, const float (&v)[32], int rows,
                                            bool mine, F f) {
-#pragma unroll
-  for (int j = 0; j < 32; ++j) stage[lane * kMmStagePitch + j] = v[j];
+  mm_to_block(stage, lane, v);
   __syncwarp();
   if (mine) {
 #pragma unroll 8
-    for (int r = 0; r < rows; ++r) f(r, stage[r * kMmStagePitch + lane]);
+    for (int r = 0; r < rows; ++r) f(r, stage[r * kMmPitch + lane]);
   }
   __syncwarp();
 }
@@ -164,26 +167,28 @@ __device__ __forceinline__ void mm_epilogue(const MmParams& p, int64_t row0, int
       });
     }
   } else {
+    // in the layout by rows, so that a single row keeps all lanes busy
     const int half = p.tn / 2;
-    float u[32];
+    float* other = stage + kMmBlockWords;
     for (int c = 0; c < half; c += 32) {
       const int64_t col = tile_n * half + c + lane;
       src(c, v);
-      src(half + c, u);
-      if (p.gate)
-        mm_by_rows(stage, lane, v, rows, col < p.N,
-                   [&](int r, float x) { mm_store(p.gate, p.out_f32, (row0 + r) * p.gate_ld + col, x); });
-      if (p.up)
-        mm_by_rows(stage, lane, u, rows, col < p.N,
-                   [&](int r, float x) { mm_store(p.up, p.out_f32, (row0 + r) * p.up_ld + col, x); });
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        float s, ds;
-        mm_act(p.act, v[j], s, ds);
-        v[j] = v[j] * s * u[j];
+      mm_to_block(stage, lane, v);
+      src(half + c, v);
+      mm_to_block(other, lane, v);
+      __syncwarp();
+      if (col < p.N) {
+#pragma unroll 4
+        for (int r = 0; r < rows; ++r) {
+          const float g = stage[r * kMmPitch + lane], u = other[r * kMmPitch + lane];
+          float s, ds;
+          mm_act(p.act, g, s, ds);
+          if (p.gate) mm_store(p.gate, p.out_f32, (row0 + r) * p.gate_ld + col, g);
+          if (p.up) mm_store(p.up, p.out_f32, (row0 + r) * p.up_ld + col, u);
+          mm_store(p.out, p.out_f32, (row0 + r) * p.out_ld + col, g * s * u);
+        }
       }
-      mm_by_rows(stage, lane, v, rows, col < p.N,
-                 [&](int r, float x) { mm_store(p.out, p.out_f32, (row0 + r) * p.out_ld + col, x); });
+      __syncwarp();
     }
   }
 }

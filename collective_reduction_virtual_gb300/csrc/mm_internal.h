@@ -4,6 +4,9 @@
 // Not part of the public ABI.
 #pragma once
 
+#include <cuda.h>
+#include <cuda_runtime.h>
+
 #include <cstddef>
 #include <cstdint>
 
@@ -29,6 +32,7 @@ struct MmOperand {
 };
 
 struct MmParams {
+  CUtensorMap map_a, map_b[2];  // of a and b: columns, rows, parts
   MmOperand a, b[2];
   int64_t M, N;   // of a tile space: rows and columns of the result
   int64_t K;      // length of the sum
@@ -37,6 +41,9 @@ struct MmParams {
   int b_halves;   // the tile's columns are half b[0]'s and half b[1]'s (MM_GATED)
   int tn;         // columns of a tile
   int64_t tiles_m, tiles_n;
+  int splits;         // that a tile's sum is cut into
+  float* partial;     // of splits: tiles x splits x min(M, 128) x tn
+  unsigned* error_word;
   // MM_OUT
   void* out;
   int64_t out_ld;
@@ -70,9 +77,19 @@ VCOLL_HD constexpr int mm_pairs(int parts) { return parts == 1 ? 1 : 6; }
 VCOLL_HD constexpr int mm_pair_a(int pairs, int q) { return pairs == 1 ? 0 : (0x010120 >> (4 * q)) & 15; }
 VCOLL_HD constexpr int mm_pair_b(int pairs, int q) { return pairs == 1 ? 0 : (0x001102 >> (4 * q)) & 15; }
 
+// Geometry of the tiles: 128 rows, and tn <= 256 columns; 64 places of the sum
+// (128 bytes of a row) at a time, in stages.
 constexpr int kMmTileM = 128;
-constexpr int kMmSimpleTileN = 64;
-constexpr int kMmSimpleThreads = 256;
+constexpr int kMmTileN = 256;
+constexpr int kMmDepth = 64;
+constexpr int kMmStages = 4;
+constexpr int kMmStageA = kMmTileM * kMmDepth * 2;
+constexpr int kMmStageB = kMmTileN * kMmDepth * 2;
+constexpr int kMmEpilogueWarps = 4;
+constexpr int kMmThreads = (kMmEpilogueWarps + 2) * 32;
+constexpr int kMmBlockWords = 32 * 33;   // a warp's block of 32 x 32 values
+constexpr int kMmEpilogueBytes = kMmEpilogueWarps * 2 * kMmBlockWords * 4;
+constexpr int kMmSmem = kMmStages * (kMmStageA + kMmStageB) + kMmEpilogueBytes + 256 + 1024;
 
 // Rows as bf16 parts, masked rows as zeros.
 struct MmPackParams {
@@ -113,10 +130,15 @@ struct MmGatedGradParams {
   int f32, parts, act;
 };
 
-const void* mm_simple_kernel(int epilogue, bool a_mn);  // MM_OUT: b is taken transposed
+// MM_OUT takes b transposed, and a where a_mn is set
+const void* mm_kernel(MmEpilogue epilogue, bool a_mn);
+const void* mm_join_splits_kernel(MmEpilogue epilogue);
 const void* mm_pack_kernel();
 const void* mm_join_kernel();
 const void* mm_scale_kernel();
 const void* mm_gated_grad_kernel();
+
+// Launch of one CTA per SM that takes nearly all of its shared memory.
+int launch_tiles(const void* fn, int64_t grid, int threads, size_t smem, void* params, void* stream);
 
 }  // namespace vcoll

@@ -1,0 +1,151 @@
+// The instructions that the tiled products are made of: TMA tile loads,
+// mbarriers with bounded waits, and the 5th-generation tensor cores (tcgen05)
+// with their accumulators in tensor memory.
+#pragma once
+
+#include <cuda.h>
+#include <stdint.h>
+
+#include "device_common.cuh"
+#include "vcoll_internal.h"
+
+namespace vcoll {
+
+constexpr uint64_t kMmWaitNs = 2000000000ull;    // a wait gives up after 2 s
+constexpr uint64_t kMmDrainNs = 20000000000ull;  // for copies that are on their way
+
+__device__ __forceinline__ uint32_t mm_smem(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+__device__ __forceinline__ void mm_bar_init(uint32_t bar, unsigned count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mm_bar_expect(uint32_t bar, unsigned bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mm_bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mm_bar_try(uint32_t bar, unsigned parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// What a CTA's waits share: where a wait that gives up is recorded, and that
+// the CTA's other waits need not be waited for any more.
+struct MmAbort {
+  volatile int* flag;    // in shared memory
+  unsigned* error_word;  // VCOLL_DEVICE_ERR_*
+};
+
+__device__ __noinline__ bool mm_bar_wait_long(uint32_t bar, unsigned parity, const MmAbort& a, uint64_t limit) {
+  uint64_t t0, t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+  while (!mm_bar_try(bar, parity)) {
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    if (t - t0 > limit) {
+      atomicOr(a.error_word, (unsigned)VCOLL_DEVICE_ERR_TIMEOUT);
+      *a.flag = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+// False where the phase did not complete in time, or another wait of the CTA
+// had given up before.
+__device__ __forceinline__ bool mm_bar_wait(uint32_t bar, unsigned parity, const MmAbort& a,
+                                            uint64_t limit = kMmWaitNs) {
+  if (mm_bar_try(bar, parity)) return true;
+  return mm_bar_wait_long(bar, parity, a, limit);
+}
+
+// A box of a tensor map into shared memory; its bytes count on `bar`.
+__device__ __forceinline__ void mm_load_box(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+          "r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void mm_prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// ------------------------------------------------------------ tensor memory
+
+template <int COLS>
+__device__ __forceinline__ void mm_tmem_alloc(uint32_t where) {  // a whole warp
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(where), "n"(COLS) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+template <int COLS>
+__device__ __forceinline__ void mm_tmem_free(uint32_t at) {  // the same warp
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "n"(COLS) : "memory");
+}
+
+__device__ __forceinline__ void mm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void mm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 32 columns of this warp's 32 lanes: lane i gets row i.
+__device__ __forceinline__ void mm_tmem_load(uint32_t at, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+}
+
+// ------------------------------------------------------------------ products
+
+// Shared-memory descriptor of an operand tile in 128-byte swizzle atoms (8 rows
+// of 128 bytes).  Along the sum (64 values a row): atoms of 8 rows 1024 bytes
+// apart.  Taken transposed, 64 rows of the sum with 64 values each form a chunk:
+// groups of 8 rows are 1024 bytes apart, and the next 64 values a chunk (8192
+// bytes) away.
+__device__ __forceinline__ uint64_t mm_desc(uint32_t addr, bool mn) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(mn ? 512 : 1) << 16 | (uint64_t)64 << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// the descriptor's step for 16 places of the sum: 32 bytes of a row, or 16 rows
+__device__ __forceinline__ constexpr uint64_t mm_desc_step(bool mn) { return mn ? 128 : 2; }
+
+// Instruction descriptor: bf16 operands, fp32 accumulators, 128 x n.
+__device__ __forceinline__ uint32_t mm_idesc(bool a_mn, bool b_mn, int m, int n) {
+  return 1u << 4 | 1u << 7 | 1u << 10 | (a_mn ? 1u << 15 : 0) | (b_mn ? 1u << 16 : 0) | (uint32_t)(n >> 3) << 17 |
+         (uint32_t)(m >> 4) << 24;
+}
+
+__device__ __forceinline__ void mm_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+
+// `bar` is arrived at when the products issued so far are done.
+__device__ __forceinline__ void mm_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+}  // namespace vcoll

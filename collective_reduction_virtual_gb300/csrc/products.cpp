@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <array>
 
 #include "layer_checks.h"
 #include "mm_internal.h"
@@ -16,6 +17,10 @@ constexpr int64_t kPackBytes = 256 << 20;   // of a piece of the table, laid out
 constexpr int64_t kErrorBytes = 256 << 20;  // of the gradient's e for a piece
 constexpr int64_t kPartBytes = 128 << 20;   // of the loss's tiles of a piece
 constexpr int kPassThreads = 256;           // of the kernels of mm_parts.cu
+
+// SMs that tiles and splits are planned for: a plan (and with it a workspace and
+// the order of the sums) depends on the sizes alone.
+constexpr int64_t kPlanSms = 152;
 
 int64_t round_up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
 int parts_of(int dtype) { return dtype == VCOLL_F32 ? 3 : 1; }
@@ -35,14 +40,55 @@ int64_t packed_bytes(int64_t rows, int64_t cols, int parts) {
   return rows * round_up(cols, 8) * 2 * parts;
 }
 
+// How a product is cut: columns of a tile, and splits of a tile's sum.
+struct Plan {
+  int tn = 256, splits = 1;
+  int64_t tiles = 0;
+  size_t bytes = 0;  // of the splits' sums
+};
+// The cheapest by a model of cycles: a step of 64 places takes the tensor cores 2
+// tn, and its operands arrive at about 24 bytes a cycle and SM from memory or 45
+// from L2 where rows of tiles share them.
+Plan plan_of(int64_t M, int64_t N, int64_t K, int parts, bool halves) {
+  Plan best;
+  double least = 0;
+  const int64_t steps = mm_pairs(parts) * ceil_div(K, kMmDepth), tiles_m = ceil_div(M, kMmTileM);
+  for (int tn : {256, 192, 128, 64}) {
+    if (halves && tn == 192) continue;
+    const int64_t cols = halves ? tn / 2 : tn;
+    const double tiles = (double)tiles_m * (double)ceil_div(N, cols);
+    for (int s = 1; s <= 16; ++s) {
+      if (s > 1 && (steps / s < 4 || tiles * s > 8 * kPlanSms)) break;
+      const double units = tiles * s, waves = (double)(int64_t)((units + kPlanSms - 1) / kPlanSms);
+      const double bytes = 128.0 * (double)(std::min<int64_t>(M, kMmTileM) + tn);
+      const double step = std::max(2.0 * tn, bytes / (tiles_m > 1 ? 45 : 24));
+      double cost = waves * ((double)ceil_div(steps, s) * step + 2500);
+      if (s > 1) cost += 4000 + units * (double)std::min<int64_t>(M, kMmTileM) * tn * 8 / (24.0 * kPlanSms);
+      if (least == 0 || cost < least) {
+        least = cost;
+        best.tn = tn;
+        best.splits = s;
+        best.tiles = tiles < 1e15 ? (int64_t)tiles : 0;
+        best.bytes = s == 1 ? 0 : (size_t)units * (size_t)std::min<int64_t>(M, kMmTileM) * tn * sizeof(float);
+      }
+    }
+  }
+  return best;
+}
+
 // Columns of a piece of the vocabulary: `fit` at most, whole tiles.
 int64_t piece_of(int64_t V, int64_t fit) {
   return std::min(V, std::max<int64_t>(2048, fit / 256 * 256));
 }
 
+// The widths of a vocabulary's pieces: all but the last are alike.
+std::array<int64_t, 2> piece_widths(int64_t V, int64_t piece) {
+  return {piece, piece ? V - (V - 1) / piece * piece : 0};
+}
+
 struct LossLayout {
   int64_t piece, pieces;
-  size_t x, table, part, state, bytes;
+  size_t x, table, part, state, splits, bytes;
 };
 LossLayout loss_layout(int64_t N, int64_t V, int64_t D, int dtype, bool direct) {
   const int parts = parts_of(dtype);
@@ -54,7 +100,15 @@ LossLayout loss_layout(int64_t N, int64_t V, int64_t D, int dtype, bool direct) 
   Regions r;
   L.x = r.take(direct ? 0 : packed_bytes(N, D, parts));
   L.table = r.take(direct ? 0 : packed_bytes(L.piece, D, parts));
-  L.part = r.take(ceil_div(L.piece, kMmSimpleTileN) * N * (int64_t)sizeof(float2));
+  size_t splits = 0;
+  int64_t tiles = 0;
+  for (int64_t w : piece_widths(V, L.piece)) {
+    const Plan plan = plan_of(N, w, D, parts, false);
+    splits = std::max(splits, plan.bytes);
+    tiles = std::max(tiles, ceil_div(w, plan.tn));
+  }
+  L.part = r.take(tiles * N * (int64_t)sizeof(float2));
+  L.splits = r.take((int64_t)splits);
   L.state = r.take(L.pieces > 1 ? N * (int64_t)sizeof(float2) : 0);
   L.bytes = r.bytes;
   return L;
@@ -62,7 +116,7 @@ LossLayout loss_layout(int64_t N, int64_t V, int64_t D, int dtype, bool direct) 
 
 struct LossGradLayout {
   int64_t piece, pieces, error_ld;
-  size_t scale, x, table, error, accum, bytes;
+  size_t scale, x, table, error, accum, splits, bytes;
 };
 LossGradLayout loss_grad_layout(int64_t N, int64_t V, int64_t D, int dtype, bool direct) {
   const int parts = parts_of(dtype);
@@ -78,13 +132,19 @@ LossGradLayout loss_grad_layout(int64_t N, int64_t V, int64_t D, int dtype, bool
   L.table = r.take(direct ? 0 : packed_bytes(L.piece, D, parts));
   L.error = r.take(N * L.error_ld * 2 * parts);
   L.accum = r.take(L.pieces > 1 ? N * D * 4 : 0);
+  size_t splits = 0;
+  for (int64_t w : piece_widths(V, L.piece))
+    for (const Plan& plan : {plan_of(N, w, D, parts, false), plan_of(N, D, w, parts, false),
+                             plan_of(w, D, N, parts, false)})
+      splits = std::max(splits, plan.bytes);
+  L.splits = r.take((int64_t)splits);
   L.bytes = r.bytes;
   return L;
 }
 
 struct GatedLayout {
   int64_t half;  // backward: gate's columns, a whole number of tiles
-  size_t x, w_gate, w_up, grads, bytes;
+  size_t x, w_gate, w_up, grads, splits, bytes;
 };
 GatedLayout gated_layout(int64_t N, int64_t D, int64_t F, int dtype, bool direct, bool backward) {
   const int parts = parts_of(dtype);
@@ -95,14 +155,20 @@ GatedLayout gated_layout(int64_t N, int64_t D, int64_t F, int dtype, bool direct
   L.w_gate = r.take(direct ? 0 : packed_bytes(F, D, parts));
   L.w_up = r.take(direct ? 0 : packed_bytes(F, D, parts));
   L.grads = r.take(backward ? packed_bytes(N, 2 * L.half, parts) : 0);
+  L.splits = r.take((int64_t)(backward ? std::max(plan_of(N, D, 2 * L.half, parts, false).bytes,
+                                                  plan_of(F, D, N, parts, false).bytes)
+                                       : plan_of(N, F, D, parts, true).bytes));
   L.bytes = r.bytes;
   return L;
 }
 
+constexpr int64_t kMaxStride = (int64_t)1 << 38;  // a tensor map's is below 2^40 bytes
+
 // Whether the products can read the matrix where it lies.
 bool lies_direct(const void* p, int64_t rows, int64_t cols, int64_t ld, int dtype) {
   if (!rows || !cols) return true;
-  if (dtype != VCOLL_BF16 || (uint64_t)p % 16 || (rows > 1 && ld % 8)) return false;
+  if (dtype != VCOLL_BF16 || (uint64_t)p % 16 || (rows > 1 && (ld % 8 || ld >= kMaxStride)))
+    return false;
   cudaPointerAttributes a;
   if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
     (void)cudaGetLastError();
@@ -148,18 +214,66 @@ int lay(const void* src, int64_t rows, int64_t cols, int64_t ld, int dtype, bool
   return VCOLL_OK;
 }
 
-// out[i][j] = sum over k < K of a and b.
-int product(MmEpilogue epilogue, bool a_mn, MmParams* p, void* stream) {
-  p->tn = kMmSimpleTileN;
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                                CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                CUtensorMapFloatOOBfill);
+
+// A tensor map of an operand (columns, rows, parts) with boxes of 64 columns and
+// `box` rows; what a box reaches outside is read as zeros.
+int encode(CUtensorMap* map, const MmOperand& o, int parts, int box) {
+  static const EncodeTiled fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess) {
+      (void)cudaGetLastError();
+      f = nullptr;
+    }
+    return (EncodeTiled)f;
+  }();
+  if (!fn) return fail(VCOLL_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
+  const cuuint64_t dims[3] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows, (cuuint64_t)parts};
+  const cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2, (cuuint64_t)(parts > 1 ? o.plane : o.ld) * 2};
+  const cuuint32_t boxes[3] = {kMmDepth, (cuuint32_t)box, 1}, steps[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.p), dims, strides,
+                        boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(VCOLL_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", (int)r);
+  return VCOLL_OK;
+}
+
+// The tiles of a product, and its epilogue.  b is taken transposed by MM_OUT, a
+// where a_mn is set.  partial: the room that plan_of's splits need.
+int product(MmEpilogue epilogue, bool a_mn, MmParams* p, void* partial, void* stream) {
+  const bool b_mn = epilogue == MM_OUT;
+  const Plan plan = plan_of(p->M, p->N, p->K, p->parts, p->b_halves);
+  p->tn = plan.tn;
+  p->splits = plan.splits;
+  p->partial = (float*)partial;
   p->tiles_m = ceil_div(p->M, kMmTileM);
   p->tiles_n = ceil_div(p->N, p->b_halves ? p->tn / 2 : p->tn);
-  if (!p->K1) p->K1 = p->K;
+  const bool second = p->b[1].p && !p->b_halves;
+  if (!second) p->K1 = round_up(p->K, kMmDepth);
   if (!p->tiles_m || !p->tiles_n) return VCOLL_OK;
   if (p->tiles_m > 0x7FFFFFFF / p->tiles_n)
     return fail(VCOLL_ERR_UNSUPPORTED, "%lld x %lld tiles are too many", (long long)p->tiles_m,
                 (long long)p->tiles_n);
-  return launch_grid(mm_simple_kernel(epilogue, a_mn), p->tiles_m * p->tiles_n, 1, kMmSimpleThreads,
-                     0, p, stream);
+  if (p->K) {
+    VCOLL_TRY(encode(&p->map_a, p->a, p->parts, a_mn ? kMmDepth : kMmTileM));
+    const int box = b_mn ? kMmDepth : p->b_halves ? p->tn / 2 : p->tn;
+    VCOLL_TRY(encode(&p->map_b[0], p->b[0], p->parts, box));
+    if (second || p->b_halves) VCOLL_TRY(encode(&p->map_b[1], p->b[1], p->parts, box));
+  }
+  p->error_word = device_error_symbol();
+  if (!p->error_word) return fail(VCOLL_ERR_CUDA, "the device error word has no address");
+  int sms = 0;
+  VCOLL_TRY(device_sms(&sms));
+  VCOLL_TRY(launch_tiles(mm_kernel(epilogue, a_mn), std::min<int64_t>(sms, p->tiles_m * p->tiles_n * p->splits),
+                         kMmThreads, kMmSmem, p, stream));
+  if (p->splits == 1) return VCOLL_OK;
+  return launch_grid(mm_join_splits_kernel(epilogue), p->tiles_m * p->tiles_n, 1, kMmEpilogueWarps * 32, 0, p,
+                     stream);
 }
 
 // Matrices of more values than any memory holds: their bytes fit 64 bits.
@@ -262,7 +376,7 @@ int vcoll_cross_entropy(const void* x, int64_t x_ld, const void* table, int64_t 
     p.N = std::min(L.piece, V - p.token0);
     VCOLL_TRY(lay((const char*)table + p.token0 * table_ld * es, p.N, D, table_ld, dtype, t_direct,
                   ws + L.table, &p.b[0], stream));
-    VCOLL_TRY(product(MM_LSE, false, &p, stream));
+    VCOLL_TRY(product(MM_LSE, false, &p, ws + L.splits, stream));
     j.tiles = p.tiles_n;
     j.first = i == 0;
     j.last = i == L.pieces - 1;
@@ -342,7 +456,7 @@ int vcoll_cross_entropy_backward(const float* dloss, int64_t dloss_count, const 
     p.error = ws + L.error;
     p.error_ld = L.error_ld;
     p.error_plane = N * L.error_ld;
-    VCOLL_TRY(product(MM_ERROR, false, &p, stream));
+    VCOLL_TRY(product(MM_ERROR, false, &p, ws + L.splits, stream));
     if (dx) {
       MmParams q = {};
       q.a = error;
@@ -358,7 +472,7 @@ int vcoll_cross_entropy_backward(const float* dloss, int64_t dloss_count, const 
       q.accum_ld = D;
       if (i > 0) q.accum_in = (float*)(ws + L.accum);
       if (i < L.pieces - 1) q.accum_out = (float*)(ws + L.accum);
-      VCOLL_TRY(product(MM_OUT, false, &q, stream));
+      VCOLL_TRY(product(MM_OUT, false, &q, ws + L.splits, stream));
     }
     if (dtable) {
       MmParams q = {};
@@ -374,7 +488,7 @@ int vcoll_cross_entropy_backward(const float* dloss, int64_t dloss_count, const 
       q.out_f32 = dtype == VCOLL_F32;
       q.base = base ? (const char*)base + v0 * base_ld * es : nullptr;
       q.base_ld = base_ld;
-      VCOLL_TRY(product(MM_OUT, true, &q, stream));
+      VCOLL_TRY(product(MM_OUT, true, &q, ws + L.splits, stream));
     }
   }
   return VCOLL_OK;
@@ -423,7 +537,7 @@ int vcoll_gated_ff(const void* x, int64_t x_ld, const void* w_gate, int64_t w_ga
   p.up = up;
   p.up_ld = up_ld;
   p.act = activation;
-  return product(MM_GATED, false, &p, stream);
+  return product(MM_GATED, false, &p, ws + L.splits, stream);
 }
 
 size_t vcoll_gated_ff_backward_workspace_bytes(int64_t N, int64_t D, int64_t F, int dtype,
@@ -497,7 +611,7 @@ int vcoll_gated_ff_backward(const void* dh, int64_t dh_ld, const void* x, int64_
     p.out = dx;
     p.out_ld = dx_ld;
     p.out_f32 = dtype == VCOLL_F32;
-    VCOLL_TRY(product(MM_OUT, false, &p, stream));
+    VCOLL_TRY(product(MM_OUT, false, &p, ws + L.splits, stream));
   }
   if (weights) {
     MmOperand rows;
@@ -517,7 +631,7 @@ int vcoll_gated_ff_backward(const void* dh, int64_t dh_ld, const void* x, int64_
       p.out = out;
       p.out_ld = k ? dw_up_ld : dw_gate_ld;
       p.out_f32 = dtype == VCOLL_F32;
-      VCOLL_TRY(product(MM_OUT, true, &p, stream));
+      VCOLL_TRY(product(MM_OUT, true, &p, ws + L.splits, stream));
     }
   }
   return VCOLL_OK;
