@@ -1301,13 +1301,25 @@ int launch_grid(const void* fn, int64_t gx, int64_t gy, int threads, size_t smem
   return VCOLL_OK;
 }
 
-int launch_tiles(const void* fn, int64_t grid, int threads, size_t smem, void* params,
+int launch_tiles(const void* fn, int64_t grid, int cluster, int threads, size_t smem, void* params,
                  void* stream) {
   void* args[] = {params};
   int rc = allow_dynamic_smem(fn, smem);
   if (rc) return rc;
-  const cudaError_t e = launch_pdl(fn, dim3((unsigned)grid), dim3((unsigned)threads), args, smem,
-                                   (cudaStream_t)stream);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = (cudaStream_t)stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return cuda_fail(e, "kernel launch");

@@ -41,12 +41,17 @@ struct MmParams {
   int b_halves;   // the tile's columns are half b[0]'s and half b[1]'s (MM_GATED)
   int tn;         // columns of a tile
   int64_t tiles_m, tiles_n;
+  int tile_rows;      // 128, or 256 of a pair of CTAs
+  int a_rows;         // of a stage's a: 128, or fewer where M is smaller
+  int stages, stage_bytes;
   int splits;         // that a tile's sum is cut into
-  float* partial;     // of splits: tiles x splits x min(M, 128) x tn
+  float* partial;     // of splits: tiles x splits x min(M, rows of a tile) x tn
   unsigned* error_word;
   // MM_OUT
   void* out;
   int64_t out_ld;
+  void* out2;             // of the rows from M1 on (M1 = 0: none), M2 in each half
+  int64_t out2_ld, M1, M2;
   const float* accum_in;  // fp32 sums so far, accum_ld apart
   float* accum_out;       // instead of out
   int64_t accum_ld;
@@ -54,6 +59,7 @@ struct MmParams {
   const void* base;       // of out's type and stride base_ld
   int64_t base_ld;
   int out_f32;
+  int out_pairs;          // two bf16 columns can be stored at once
   // MM_LSE, MM_ERROR: column j is token token0 + j of V
   const void* targets;
   const float* dloss;
@@ -77,27 +83,40 @@ VCOLL_HD constexpr int mm_pairs(int parts) { return parts == 1 ? 1 : 6; }
 VCOLL_HD constexpr int mm_pair_a(int pairs, int q) { return pairs == 1 ? 0 : (0x010120 >> (4 * q)) & 15; }
 VCOLL_HD constexpr int mm_pair_b(int pairs, int q) { return pairs == 1 ? 0 : (0x001102 >> (4 * q)) & 15; }
 
-// Geometry of the tiles: 128 rows, and tn <= 256 columns; 64 places of the sum
-// (128 bytes of a row) at a time, in stages.
-constexpr int kMmTileM = 128;
+// Geometry of the tiles.  A CTA has 128 rows of a tile and at most 256 columns;
+// one CTA, or two that share their columns' operand, take a tile.  64 places of
+// the sum (128 bytes of a row) at a time, in stages of shared memory.
+constexpr int kMmRows = 128;
 constexpr int kMmTileN = 256;
 constexpr int kMmDepth = 64;
-constexpr int kMmStages = 4;
-constexpr int kMmStageA = kMmTileM * kMmDepth * 2;
-constexpr int kMmStageB = kMmTileN * kMmDepth * 2;
+constexpr int kMmStageRoom = 192 * 1024;
+constexpr int kMmMaxStages = 12;
 constexpr int kMmEpilogueWarps = 4;
 constexpr int kMmThreads = (kMmEpilogueWarps + 2) * 32;
-constexpr int kMmBlockWords = 32 * 33;   // a warp's block of 32 x 32 values
-constexpr int kMmEpilogueBytes = kMmEpilogueWarps * 2 * kMmBlockWords * 4;
-constexpr int kMmSmem = kMmStages * (kMmStageA + kMmStageB) + kMmEpilogueBytes + 256 + 1024;
+constexpr int kMmPitch = 33;  // words of a row of a warp's block of 32 x 32
+constexpr int kMmBlockWords = 32 * kMmPitch;
+constexpr int kMmEpilogueBytes = kMmEpilogueWarps * kMmBlockWords * 4;
+constexpr int kMmSmem = kMmStageRoom + kMmEpilogueBytes + 512 + 1024;
 
-// Rows as bf16 parts, masked rows as zeros.
-struct MmPackParams {
+// A matrix laid out as bf16 parts, masked rows as zeros.
+struct MmPackJob {
   const void* src;
   void* dst;
-  const void* targets;  // NULL: no row is masked
   int64_t rows, cols, src_ld, dst_ld, plane;
-  int64_t V;
+  int64_t first_block, blocks;
+  int masked;
+  int load16;  // rows start at 16-byte boundaries
+};
+// Up to three matrices; and where targets are given the largest magnitude of
+// dloss over the rows that count (block 0).
+constexpr int kMmPackJobs = 3;
+struct MmPackParams {
+  MmPackJob job[kMmPackJobs];
+  const void* targets;
+  const float* dloss;
+  int64_t dloss_step;
+  float* scale;  // NULL: not wanted
+  int64_t N, V;
   int idx64, src_f32, parts;
 };
 
@@ -111,15 +130,7 @@ struct MmJoinParams {
   int64_t tiles, N, V;
   int idx64, first, last;
 };
-
-// The largest magnitude of the loss's gradient over the rows that count.
-struct MmScaleParams {
-  const float* dloss;
-  const void* targets;
-  float* scale;
-  int64_t N, V, step;
-  int idx64;
-};
+constexpr int kMmJoinThreads = 1024;
 
 // The gradients of gate and up, as bf16 parts beside each other.
 struct MmGatedGradParams {
@@ -128,17 +139,19 @@ struct MmGatedGradParams {
   int64_t N, F, dh_ld, gate_ld, up_ld;
   int64_t dst_ld, half, plane;  // gate's at 0, up's at half
   int f32, parts, act;
+  int load16;  // the rows of dh, gate and up start at 16-byte boundaries
 };
 
-// MM_OUT takes b transposed, and a where a_mn is set
-const void* mm_kernel(MmEpilogue epilogue, bool a_mn);
+// MM_OUT takes b transposed, and a where a_mn is set; ctas that share a tile: 1 or 2
+const void* mm_kernel(MmEpilogue epilogue, bool a_mn, int ctas);
 const void* mm_join_splits_kernel(MmEpilogue epilogue);
 const void* mm_pack_kernel();
 const void* mm_join_kernel();
-const void* mm_scale_kernel();
 const void* mm_gated_grad_kernel();
 
-// Launch of one CTA per SM that takes nearly all of its shared memory.
-int launch_tiles(const void* fn, int64_t grid, int threads, size_t smem, void* params, void* stream);
+// Launch of clusters of `cluster` CTAs, one CTA per SM, that take nearly all of
+// its shared memory.
+int launch_tiles(const void* fn, int64_t grid, int cluster, int threads, size_t smem, void* params,
+                 void* stream);
 
 }  // namespace vcoll

@@ -1,43 +1,133 @@
 // The passes around the products of mm_kernels.cu: operands laid out as bf16
-// parts, the join of the loss's tiles, the scale of the loss's gradient, and the
-// element-wise gradient of a gated block.
+// parts, the join of the loss's tiles, and the element-wise gradient of a gated
+// block.  All are bound by memory: each value is read and written once, eight
+// adjacent ones a thread.
 #include "mm_epilogue.cuh"
 
 namespace vcoll {
 
 namespace {
-constexpr int kThreads = 256;
-}
 
-// dst[part][i][j]: the parts of src[i][j], a thread for 4 columns.  Reads 2 or 4
-// bytes a value and writes 2 or 6: bound by memory.
-__global__ void __launch_bounds__(kThreads) vc_mm_pack(const __grid_constant__ MmPackParams p) {
-  pdl_enter();
-  const int64_t quads = (p.cols + 3) / 4;
-  for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < p.rows * quads;
-       e += (int64_t)gridDim.x * kThreads) {
-    const int64_t i = e / quads, j0 = e % quads * 4;
-    bool keep = true;
-    if (p.targets) {
-      const int64_t t = mm_token(p.targets, p.idx64, i);
-      keep = t >= 0 && t < p.V;
-    }
-    uint16_t q[4][3];
-    for (int j = 0; j < 4; ++j) {
-      const bool read = keep && j0 + j < p.cols;
-      const float x = read ? mm_load(p.src, p.src_f32, i * p.src_ld + j0 + j) : 0.0f;
-      mm_parts(x, q[j]);
-    }
-    for (int k = 0; k < p.parts; ++k)  // rows are padded to 8 values
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.dst) + k * p.plane + i * p.dst_ld + j0) =
-          make_uint2(q[0][k] | (uint32_t)q[1][k] << 16, q[2][k] | (uint32_t)q[3][k] << 16);
+constexpr int kThreads = 256;
+
+// row and group of eight columns of item e; 64-bit division only where needed
+__device__ __forceinline__ void item_at(int64_t e, int64_t groups, int64_t& row, int64_t& group) {
+  if ((uint64_t)e <= 0xFFFFFFFFull && (uint64_t)groups <= 0xFFFFFFFFull) {
+    row = (uint32_t)e / (uint32_t)groups;
+    group = (uint32_t)e - (uint32_t)row * (uint32_t)groups;
+  } else {
+    row = e / groups;
+    group = e - row * groups;
   }
 }
 
-// A CTA for 32 rows, a warp for every eighth tile of them.
-__global__ void __launch_bounds__(kThreads) vc_mm_join(const __grid_constant__ MmJoinParams p) {
+// Values i .. i + 7 of a matrix of fp32 or bf16, those from `count` on as zeros.
+__device__ __forceinline__ void load8(const void* p, int f32, bool load16, int64_t i, int64_t count,
+                                      float (&v)[8]) {
+  if (f32) {
+    const float* q = static_cast<const float*>(p) + i;
+    if (load16 && count >= 8) {
+      const uint4 a = ld_stream(q), b = ld_stream(q + 4);
+      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = j < count ? q[j] : 0.0f;
+    }
+    return;
+  }
+  const uint16_t* q = static_cast<const uint16_t*>(p) + i;
+  if (count >= 8) {
+    uint32_t w[4];
+    if (load16) {
+      const uint4 a = ld_stream(q);
+      w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+    } else {
+      // the words that hold them: each holds at least one of the values
+      const uint32_t* x = reinterpret_cast<const uint32_t*>((uintptr_t)q & ~(uintptr_t)3);
+      const bool odd = (uintptr_t)q & 2;
+      const uint32_t y[5] = {x[0], x[1], x[2], x[3], odd ? x[4] : 0};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = odd ? __funnelshift_r(y[j], y[j + 1], 16) : y[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) Elem<__nv_bfloat16>::widen2(w[j], v[2 * j], v[2 * j + 1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < count ? Elem<__nv_bfloat16>::widen1(q[j]) : 0.0f;
+  }
+}
+
+// The parts of eight values, 16 bytes each.  One part alone is the value rounded.
+__device__ __forceinline__ void store8(void* dst, int64_t i, int64_t plane, int parts, const float (&v)[8]) {
+  uint16_t* to = static_cast<uint16_t*>(dst) + i;
+  if (parts == 1) {
+    *reinterpret_cast<uint4*>(to) = make_uint4(mm_narrow2(v[0], v[1]), mm_narrow2(v[2], v[3]),
+                                               mm_narrow2(v[4], v[5]), mm_narrow2(v[6], v[7]));
+    return;
+  }
+  uint16_t q[8][3];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) mm_parts(v[j], q[j]);
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    *reinterpret_cast<uint4*>(to + k * plane) =
+        make_uint4(q[0][k] | (uint32_t)q[1][k] << 16, q[2][k] | (uint32_t)q[3][k] << 16,
+                   q[4][k] | (uint32_t)q[5][k] << 16, q[6][k] | (uint32_t)q[7][k] << 16);
+}
+
+// The largest magnitude of dloss over the rows that count, by one CTA; 1 where it
+// is zero or not finite.
+__device__ __forceinline__ void largest(const MmPackParams& p) {
+  __shared__ float part[kThreads / 32];
+  float top = 0.0f;
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < p.N; i += kThreads) {
+    const int64_t t = mm_token(p.targets, p.idx64, i);
+    const float g = fabsf(p.dloss[i * p.dloss_step]);
+    if (t >= 0 && t < p.V && g > top) top = g;
+  }
+  for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = top;
+  __syncthreads();
+  if (threadIdx.x) return;
+  for (int w = 1; w < kThreads / 32; ++w) top = fmaxf(top, part[w]);
+  *p.scale = top > 0.0f && top < INFINITY ? top : 1.0f;
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kThreads) vc_mm_pack(const __grid_constant__ MmPackParams p) {
   pdl_enter();
-  __shared__ float2 part[kThreads];
+  int64_t block = blockIdx.x;
+  if (p.scale && block-- == 0) {
+    largest(p);
+    return;
+  }
+  int which = 0;
+  while (which + 1 < kMmPackJobs && block >= p.job[which + 1].first_block) ++which;
+  const MmPackJob& j = p.job[which];
+  const int64_t groups = (j.cols + 7) / 8;
+  for (int64_t e = (block - j.first_block) * kThreads + threadIdx.x; e < j.rows * groups; e += j.blocks * kThreads) {
+    int64_t row, group;
+    item_at(e, groups, row, group);
+    bool keep = true;
+    if (j.masked) {
+      const int64_t t = mm_token(p.targets, p.idx64, row);
+      keep = t >= 0 && t < p.V;
+    }
+    float v[8];
+    load8(j.src, p.src_f32, j.load16, row * j.src_ld + group * 8, keep ? j.cols - group * 8 : 0, v);
+    store8(j.dst, row * j.dst_ld + group * 8, j.plane, p.parts, v);
+  }
+}
+
+// A CTA for 32 rows, a warp for every 32nd tile of them.  The maxima are to base 2.
+__global__ void __launch_bounds__(kMmJoinThreads) vc_mm_join(const __grid_constant__ MmJoinParams p) {
+  pdl_enter();
+  constexpr int WARPS = kMmJoinThreads / 32;
+  __shared__ float2 part[kMmJoinThreads];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int64_t row = (int64_t)blockIdx.x * 32 + lane;
   float m = -INFINITY, s = 0.0f;
@@ -47,78 +137,55 @@ __global__ void __launch_bounds__(kThreads) vc_mm_join(const __grid_constant__ M
       s += q.y;
       return;
     }
-    s = s * mm_exp(m - top) + q.y * mm_exp(q.x - top);
+    s = s * mm_exp2(m - top) + q.y * mm_exp2(q.x - top);
     m = top;
   };
   if (row < p.N) {
     if (warp == 0 && !p.first) add(p.state[row]);
-    for (int64_t t = warp; t < p.tiles; t += kThreads / 32) add(p.part[t * p.N + row]);
+#pragma unroll 4
+    for (int64_t t = warp; t < p.tiles; t += WARPS) add(p.part[t * p.N + row]);
   }
   part[threadIdx.x] = make_float2(m, s);
   __syncthreads();
   if (warp || row >= p.N) return;
-  for (int w = 1; w < kThreads / 32; ++w) add(part[w * 32 + lane]);
+  for (int w = 1; w < WARPS; ++w) add(part[w * 32 + lane]);
   if (!p.last) {
     p.state[row] = make_float2(m, s);
     return;
   }
   const int64_t t = mm_token(p.targets, p.idx64, row);
-  const float lse = m + logf(s);  // no token at all: log 0
+  const float lse = (m + log2f(s)) * 0.69314718055994531f;  // no token at all: log 0
   p.lse[row] = lse;
   p.loss[row] = t >= 0 && t < p.V ? lse - p.loss[row] : 0.0f;
-}
-
-// One CTA.  1 where the largest magnitude is zero or not finite.
-__global__ void __launch_bounds__(1024) vc_mm_scale(const __grid_constant__ MmScaleParams p) {
-  pdl_enter();
-  __shared__ float part[32];
-  float top = 0.0f;
-  for (int64_t i = threadIdx.x; i < p.N; i += 1024) {
-    const int64_t t = mm_token(p.targets, p.idx64, i);
-    const float g = fabsf(p.dloss[i * p.step]);
-    if (t >= 0 && t < p.V && g > top) top = g;
-  }
-  for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = top;
-  __syncthreads();
-  if (threadIdx.x) return;
-  for (int w = 1; w < 32; ++w) top = fmaxf(top, part[w]);
-  *p.scale = top > 0.0f && top < INFINITY ? top : 1.0f;
 }
 
 // dgate = dh * up * act'(gate), dup = dh * act(gate).
 __global__ void __launch_bounds__(kThreads) vc_mm_gated_grad(const __grid_constant__ MmGatedGradParams p) {
   pdl_enter();
-  uint16_t* dst = static_cast<uint16_t*>(p.dst);
-  for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < p.N * p.half;
+  const int64_t groups = p.half / 8;
+  for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < p.N * groups;
        e += (int64_t)gridDim.x * kThreads) {
-    const int64_t i = e / p.half, j = e % p.half;
-    float dg = 0.0f, du = 0.0f;
-    if (j < p.F) {  // what pads a row stands in the sum of dx
-      const float dh = mm_load(p.dh, p.f32, i * p.dh_ld + j), g = mm_load(p.gate, p.f32, i * p.gate_ld + j);
+    int64_t row, group;
+    item_at(e, groups, row, group);
+    const int64_t col = group * 8, left = p.F - col;  // what pads a row is zeros: it stands in the sum of dx
+    float dh[8], g[8], u[8];
+    load8(p.dh, p.f32, p.load16, row * p.dh_ld + col, left, dh);
+    load8(p.gate, p.f32, p.load16, row * p.gate_ld + col, left, g);
+    load8(p.up, p.f32, p.load16, row * p.up_ld + col, left, u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
       float s, ds;
-      mm_act(p.act, g, s, ds);
-      dg = dh * mm_load(p.up, p.f32, i * p.up_ld + j) * (s + g * ds);
-      du = dh * (g * s);
+      mm_act(p.act, g[j], s, ds);
+      u[j] = dh[j] * u[j] * (s + g[j] * ds);
+      dh[j] = dh[j] * (g[j] * s);
     }
-    if (p.parts == 1) {  // rounded for the product, as its other operand is
-      dst[i * p.dst_ld + j] = Elem<__nv_bfloat16>::narrow1(dg);
-      dst[i * p.dst_ld + p.half + j] = Elem<__nv_bfloat16>::narrow1(du);
-      continue;
-    }
-    uint16_t qg[3], qu[3];
-    mm_parts(dg, qg);
-    mm_parts(du, qu);
-    for (int k = 0; k < p.parts; ++k) {
-      dst[k * p.plane + i * p.dst_ld + j] = qg[k];
-      dst[k * p.plane + i * p.dst_ld + p.half + j] = qu[k];
-    }
+    store8(p.dst, row * p.dst_ld + col, p.plane, p.parts, u);
+    store8(p.dst, row * p.dst_ld + p.half + col, p.plane, p.parts, dh);
   }
 }
 
 const void* mm_pack_kernel() { return (const void*)vc_mm_pack; }
 const void* mm_join_kernel() { return (const void*)vc_mm_join; }
-const void* mm_scale_kernel() { return (const void*)vc_mm_scale; }
 const void* mm_gated_grad_kernel() { return (const void*)vc_mm_gated_grad; }
 
 }  // namespace vcoll

@@ -40,36 +40,42 @@ int64_t packed_bytes(int64_t rows, int64_t cols, int parts) {
   return rows * round_up(cols, 8) * 2 * parts;
 }
 
-// How a product is cut: columns of a tile, and splits of a tile's sum.
+// How a product is cut: CTAs that share a tile, its columns, and splits of its sum.
 struct Plan {
-  int tn = 256, splits = 1;
-  int64_t tiles = 0;
+  int ctas = 1, tn = 256, splits = 1;
   size_t bytes = 0;  // of the splits' sums
 };
-// The cheapest by a model of cycles: a step of 64 places takes the tensor cores 2
-// tn, and its operands arrive at about 24 bytes a cycle and SM from memory or 45
-// from L2 where rows of tiles share them.
+// The cheapest by a model of cycles.  A step of 64 places takes the tensor cores 2
+// tn, or as long as the step's operands take to arrive: at 24 bytes a cycle and SM
+// from memory where one row of tiles takes each column once, at 80 from L2 where
+// rows of tiles share them.  A tile's epilogue goes beside the next tile's sum, but
+// for the last one's.
 Plan plan_of(int64_t M, int64_t N, int64_t K, int parts, bool halves) {
   Plan best;
   double least = 0;
-  const int64_t steps = mm_pairs(parts) * ceil_div(K, kMmDepth), tiles_m = ceil_div(M, kMmTileM);
-  for (int tn : {256, 192, 128, 64}) {
-    if (halves && tn == 192) continue;
-    const int64_t cols = halves ? tn / 2 : tn;
-    const double tiles = (double)tiles_m * (double)ceil_div(N, cols);
-    for (int s = 1; s <= 16; ++s) {
-      if (s > 1 && (steps / s < 4 || tiles * s > 8 * kPlanSms)) break;
-      const double units = tiles * s, waves = (double)(int64_t)((units + kPlanSms - 1) / kPlanSms);
-      const double bytes = 128.0 * (double)(std::min<int64_t>(M, kMmTileM) + tn);
-      const double step = std::max(2.0 * tn, bytes / (tiles_m > 1 ? 45 : 24));
-      double cost = waves * ((double)ceil_div(steps, s) * step + 2500);
-      if (s > 1) cost += 4000 + units * (double)std::min<int64_t>(M, kMmTileM) * tn * 8 / (24.0 * kPlanSms);
-      if (least == 0 || cost < least) {
-        least = cost;
-        best.tn = tn;
-        best.splits = s;
-        best.tiles = tiles < 1e15 ? (int64_t)tiles : 0;
-        best.bytes = s == 1 ? 0 : (size_t)units * (size_t)std::min<int64_t>(M, kMmTileM) * tn * sizeof(float);
+  const int64_t steps = mm_pairs(parts) * ceil_div(K, kMmDepth);
+  for (int ctas : {2, 1}) {
+    if (ctas == 2 && M <= kMmRows) continue;
+    const int64_t tile_rows = kMmRows * ctas, rows = std::min<int64_t>(M, tile_rows), slots = kPlanSms / ctas;
+    const int64_t tiles_m = ceil_div(M, tile_rows);
+    for (int tn : {256, 128, 64}) {
+      if (tn == 64 && (halves || ctas == 2)) continue;
+      const int64_t cols = halves ? tn / 2 : tn;
+      const double tiles = (double)tiles_m * (double)ceil_div(N, cols);
+      const double bytes = 128.0 * (double)(std::min<int64_t>(M, kMmRows) + tn / ctas);
+      const double step = std::max(2.0 * tn, bytes / (tiles_m > 1 ? 80 : 24)), tail = 10.0 * tn + 1000;
+      for (int s = 1; s <= 16; ++s) {
+        if (s > 1 && (steps / s < 4 || tiles * s > 8 * kPlanSms)) break;
+        const double units = tiles * s, waves = (double)(int64_t)((units + slots - 1) / slots);
+        double cost = waves * ((double)ceil_div(steps, s) * step + 200) + tail;
+        if (s > 1) cost += 3000 + units * (double)rows * tn * 8 / (24.0 * kPlanSms);
+        if (least == 0 || cost < least) {
+          least = cost;
+          best.ctas = ctas;
+          best.tn = tn;
+          best.splits = s;
+          best.bytes = s == 1 ? 0 : (size_t)units * (size_t)rows * tn * sizeof(float);
+        }
       }
     }
   }
@@ -149,14 +155,15 @@ struct GatedLayout {
 GatedLayout gated_layout(int64_t N, int64_t D, int64_t F, int dtype, bool direct, bool backward) {
   const int parts = parts_of(dtype);
   GatedLayout L;
-  L.half = round_up(F, kMmTileM);
+  L.half = round_up(F, kMmRows);
   Regions r;
   L.x = r.take(direct ? 0 : packed_bytes(N, D, parts));
   L.w_gate = r.take(direct ? 0 : packed_bytes(F, D, parts));
   L.w_up = r.take(direct ? 0 : packed_bytes(F, D, parts));
   L.grads = r.take(backward ? packed_bytes(N, 2 * L.half, parts) : 0);
   L.splits = r.take((int64_t)(backward ? std::max(plan_of(N, D, 2 * L.half, parts, false).bytes,
-                                                  plan_of(F, D, N, parts, false).bytes)
+                                                  std::max(plan_of(F, D, N, parts, false).bytes,
+                                                           plan_of(2 * L.half, D, N, parts, false).bytes))
                                        : plan_of(N, F, D, parts, true).bytes));
   L.bytes = r.bytes;
   return L;
@@ -181,38 +188,56 @@ MmOperand operand(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t
   return {p, rows, cols, rows > 1 ? ld : round_up(std::max<int64_t>(cols, 1), 8), plane};
 }
 
-// Lays a matrix out as parts at `to`; rows whose target is outside [0, V) as
-// zeros where targets are given.
-int pack(const void* src, int64_t rows, int64_t cols, int64_t ld, int dtype, void* to,
-         const void* targets, int64_t V, int idx64, MmOperand* o, void* stream) {
-  MmPackParams p = {};
-  p.src = src;
-  p.dst = to;
-  p.targets = targets;
-  p.rows = rows;
-  p.cols = cols;
-  p.src_ld = ld;
-  p.dst_ld = round_up(cols, 8);
-  p.plane = rows * p.dst_ld;
-  p.V = V;
-  p.idx64 = idx64;
-  p.src_f32 = dtype == VCOLL_F32;
-  p.parts = parts_of(dtype);
-  *o = operand(to, rows, cols, p.dst_ld, p.plane);
-  if (!rows || !cols) return VCOLL_OK;
-  int sms = 0;
-  VCOLL_TRY(device_sms(&sms));
-  const int64_t grid = std::min<int64_t>(ceil_div(rows * ceil_div(cols, 4), kPassThreads), (int64_t)sms * 8);
-  return launch_grid(mm_pack_kernel(), grid, 1, kPassThreads, 0, &p, stream);
+bool rows_at_16(const void* p, int64_t rows, int64_t ld, int es) {
+  return (uint64_t)p % 16 == 0 && (rows <= 1 || ld * es % 16 == 0);
 }
 
-// The matrix where it lies, or laid out at `to`.
-int lay(const void* src, int64_t rows, int64_t cols, int64_t ld, int dtype, bool direct, void* to,
-        MmOperand* o, void* stream) {
-  if (!direct) return pack(src, rows, cols, ld, dtype, to, nullptr, 0, 0, o, stream);
-  *o = operand(src, rows, cols, ld);
-  return VCOLL_OK;
-}
+// Matrices that are laid out as parts by one launch.
+struct Packer {
+  MmPackParams p = {};
+  int jobs = 0;
+  int64_t blocks = 0;
+
+  Packer(int dtype) {
+    p.src_f32 = dtype == VCOLL_F32;
+    p.parts = parts_of(dtype);
+  }
+  // The matrix where it lies, or laid out at `to`.  masked: rows whose target is
+  // outside [0, V) as zeros.
+  int add(const void* src, int64_t rows, int64_t cols, int64_t ld, bool direct, void* to, bool masked,
+          MmOperand* o) {
+    if (direct) {
+      *o = operand(src, rows, cols, ld);
+      return VCOLL_OK;
+    }
+    MmPackJob& j = p.job[jobs];
+    j.src = src;
+    j.dst = to;
+    j.rows = rows;
+    j.cols = cols;
+    j.src_ld = ld;
+    j.dst_ld = round_up(cols, 8);
+    j.plane = rows * j.dst_ld;
+    j.masked = masked;
+    j.load16 = rows_at_16(src, rows, ld, p.src_f32 ? 4 : 2);
+    *o = operand(to, rows, cols, j.dst_ld, j.plane);
+    if (!rows || !cols) return VCOLL_OK;
+    int sms = 0;
+    VCOLL_TRY(device_sms(&sms));
+    j.first_block = blocks;
+    j.blocks = std::min<int64_t>(ceil_div(rows * ceil_div(cols, 8), kPassThreads), (int64_t)sms * 8);
+    blocks += j.blocks;
+    ++jobs;
+    return VCOLL_OK;
+  }
+  int run(void* stream) {
+    const int64_t all = blocks + (p.scale ? 1 : 0);
+    if (!all) return VCOLL_OK;
+    for (int i = jobs; i < kMmPackJobs; ++i) p.job[i].first_block = INT64_MAX;
+    if (!jobs) p.job[0].blocks = 1;
+    return launch_grid(mm_pack_kernel(), all, 1, kPassThreads, 0, &p, stream);
+  }
+};
 
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
@@ -251,8 +276,12 @@ int product(MmEpilogue epilogue, bool a_mn, MmParams* p, void* partial, void* st
   p->tn = plan.tn;
   p->splits = plan.splits;
   p->partial = (float*)partial;
-  p->tiles_m = ceil_div(p->M, kMmTileM);
+  p->tile_rows = kMmRows * plan.ctas;
+  p->tiles_m = ceil_div(p->M, p->tile_rows);
   p->tiles_n = ceil_div(p->N, p->b_halves ? p->tn / 2 : p->tn);
+  p->a_rows = a_mn ? kMmRows : (int)std::min<int64_t>(kMmRows, round_up(p->M, 8));
+  p->stage_bytes = (p->a_rows + p->tn / plan.ctas) * kMmDepth * 2;
+  p->stages = std::min(kMmMaxStages, kMmStageRoom / p->stage_bytes);
   const bool second = p->b[1].p && !p->b_halves;
   if (!second) p->K1 = round_up(p->K, kMmDepth);
   if (!p->tiles_m || !p->tiles_n) return VCOLL_OK;
@@ -260,8 +289,8 @@ int product(MmEpilogue epilogue, bool a_mn, MmParams* p, void* partial, void* st
     return fail(VCOLL_ERR_UNSUPPORTED, "%lld x %lld tiles are too many", (long long)p->tiles_m,
                 (long long)p->tiles_n);
   if (p->K) {
-    VCOLL_TRY(encode(&p->map_a, p->a, p->parts, a_mn ? kMmDepth : kMmTileM));
-    const int box = b_mn ? kMmDepth : p->b_halves ? p->tn / 2 : p->tn;
+    VCOLL_TRY(encode(&p->map_a, p->a, p->parts, a_mn ? kMmDepth : p->a_rows));
+    const int box = b_mn ? kMmDepth : p->b_halves ? p->tn / 2 : p->tn / plan.ctas;
     VCOLL_TRY(encode(&p->map_b[0], p->b[0], p->parts, box));
     if (second || p->b_halves) VCOLL_TRY(encode(&p->map_b[1], p->b[1], p->parts, box));
   }
@@ -269,11 +298,19 @@ int product(MmEpilogue epilogue, bool a_mn, MmParams* p, void* partial, void* st
   if (!p->error_word) return fail(VCOLL_ERR_CUDA, "the device error word has no address");
   int sms = 0;
   VCOLL_TRY(device_sms(&sms));
-  VCOLL_TRY(launch_tiles(mm_kernel(epilogue, a_mn), std::min<int64_t>(sms, p->tiles_m * p->tiles_n * p->splits),
+  const int64_t tiles = p->tiles_m * p->tiles_n;
+  VCOLL_TRY(launch_tiles(mm_kernel(epilogue, a_mn, plan.ctas),
+                         plan.ctas * std::min<int64_t>(sms / plan.ctas, tiles * p->splits), plan.ctas,
                          kMmThreads, kMmSmem, p, stream));
   if (p->splits == 1) return VCOLL_OK;
-  return launch_grid(mm_join_splits_kernel(epilogue), p->tiles_m * p->tiles_n, 1, kMmEpilogueWarps * 32, 0, p,
-                     stream);
+  const int64_t chunks = epilogue == MM_LSE ? 1 : (p->b_halves ? p->tn / 2 : p->tn) / 32;
+  const int64_t warps = tiles * std::min<int64_t>(p->M, p->tile_rows) * chunks;
+  return launch_grid(mm_join_splits_kernel(epilogue), ceil_div(warps, 8), 1, 256, 0, p, stream);
+}
+
+// Whether every row of a bf16 matrix allows 4-byte stores of two columns.
+bool in_pairs(const void* p, int64_t rows, int64_t ld, int dtype) {
+  return dtype == VCOLL_BF16 && (uint64_t)p % 4 == 0 && (rows <= 1 || ld % 2 == 0);
 }
 
 // Matrices of more values than any memory holds: their bytes fit 64 bits.
@@ -353,7 +390,6 @@ int vcoll_cross_entropy(const void* x, int64_t x_ld, const void* table, int64_t 
   VCOLL_TRY(check_room(ops, 5, workspace, workspace_bytes, L.bytes));
   char* ws = (char*)workspace;
   MmParams p = {};
-  VCOLL_TRY(lay(x, N, D, x_ld, dtype, x_direct, ws + L.x, &p.a, stream));
   p.M = N;
   p.K = D;
   p.parts = parts_of(dtype);
@@ -374,13 +410,16 @@ int vcoll_cross_entropy(const void* x, int64_t x_ld, const void* table, int64_t 
   for (int64_t i = 0; i < L.pieces; ++i) {
     p.token0 = i * L.piece;
     p.N = std::min(L.piece, V - p.token0);
-    VCOLL_TRY(lay((const char*)table + p.token0 * table_ld * es, p.N, D, table_ld, dtype, t_direct,
-                  ws + L.table, &p.b[0], stream));
+    Packer pack(dtype);
+    if (i == 0) VCOLL_TRY(pack.add(x, N, D, x_ld, x_direct, ws + L.x, false, &p.a));
+    VCOLL_TRY(pack.add((const char*)table + p.token0 * table_ld * es, p.N, D, table_ld, t_direct,
+                       ws + L.table, false, &p.b[0]));
+    VCOLL_TRY(pack.run(stream));
     VCOLL_TRY(product(MM_LSE, false, &p, ws + L.splits, stream));
     j.tiles = p.tiles_n;
     j.first = i == 0;
     j.last = i == L.pieces - 1;
-    VCOLL_TRY(launch_grid(mm_join_kernel(), ceil_div(N, 32), 1, kPassThreads, 0, &j, stream));
+    VCOLL_TRY(launch_grid(mm_join_kernel(), ceil_div(N, 32), 1, kMmJoinThreads, 0, &j, stream));
   }
   return VCOLL_OK;
 }
@@ -420,23 +459,25 @@ int vcoll_cross_entropy_backward(const float* dloss, int64_t dloss_count, const 
   char* ws = (char*)workspace;
   const int parts = parts_of(dtype), idx64 = index_type == VCOLL_I64;
   float* scale = (float*)(ws + L.scale);
-  MmScaleParams s = {};
-  s.dloss = dloss;
-  s.targets = targets;
-  s.scale = scale;
-  s.N = N;
-  s.V = V;
-  s.step = dloss_count == 1 ? 0 : 1;
-  s.idx64 = idx64;
-  VCOLL_TRY(launch_grid(mm_scale_kernel(), 1, 1, 1024, 0, &s, stream));
+  const int64_t dloss_step = dloss_count == 1 ? 0 : 1;
   MmOperand rows;  // x without the rows that do not count
-  VCOLL_TRY(pack(x, N, D, x_ld, dtype, ws + L.x, targets, V, idx64, &rows, stream));
   for (int64_t i = 0; i < L.pieces; ++i) {
     const int64_t v0 = i * L.piece, width = std::min(L.piece, V - v0);
-    MmOperand tokens = operand(table, 0, D, table_ld);
-    if (N)
-      VCOLL_TRY(lay((const char*)table + v0 * table_ld * es, width, D, table_ld, dtype, direct,
-                    ws + L.table, &tokens, stream));
+    MmOperand tokens;
+    Packer pack(dtype);
+    pack.p.targets = targets;
+    pack.p.idx64 = idx64;
+    pack.p.V = V;
+    if (i == 0) {
+      pack.p.dloss = dloss;
+      pack.p.dloss_step = dloss_step;
+      pack.p.scale = scale;
+      pack.p.N = N;
+      VCOLL_TRY(pack.add(x, N, D, x_ld, false, ws + L.x, true, &rows));
+    }
+    VCOLL_TRY(pack.add((const char*)table + v0 * table_ld * es, N ? width : 0, D, table_ld, direct, ws + L.table,
+                       false, &tokens));
+    VCOLL_TRY(pack.run(stream));
     const MmOperand error = operand(ws + L.error, N, width, L.error_ld, N * L.error_ld);
     MmParams p = {};
     p.a = rows;
@@ -450,7 +491,7 @@ int vcoll_cross_entropy_backward(const float* dloss, int64_t dloss_count, const 
     p.V = V;
     p.token0 = v0;
     p.dloss = dloss;
-    p.dloss_step = s.step;
+    p.dloss_step = dloss_step;
     p.lse = lse;
     p.scale = scale;
     p.error = ws + L.error;
@@ -467,6 +508,7 @@ int vcoll_cross_entropy_backward(const float* dloss, int64_t dloss_count, const 
       q.parts = parts;
       q.scale = scale;
       q.out = dx;
+      q.out_pairs = in_pairs(dx, N, dx_ld, dtype);
       q.out_ld = dx_ld;
       q.out_f32 = dtype == VCOLL_F32;
       q.accum_ld = D;
@@ -485,6 +527,7 @@ int vcoll_cross_entropy_backward(const float* dloss, int64_t dloss_count, const 
       q.scale = scale;
       q.out = (char*)dtable + v0 * dtable_ld * es;
       q.out_ld = dtable_ld;
+      q.out_pairs = in_pairs(q.out, V, dtable_ld, dtype);
       q.out_f32 = dtype == VCOLL_F32;
       q.base = base ? (const char*)base + v0 * base_ld * es : nullptr;
       q.base_ld = base_ld;
@@ -521,9 +564,11 @@ int vcoll_gated_ff(const void* x, int64_t x_ld, const void* w_gate, int64_t w_ga
   VCOLL_TRY(check_room(ops, 6, workspace, workspace_bytes, L.bytes));
   char* ws = (char*)workspace;
   MmParams p = {};
-  VCOLL_TRY(lay(x, N, D, x_ld, dtype, x_direct, ws + L.x, &p.a, stream));
-  VCOLL_TRY(lay(w_gate, F, D, w_gate_ld, dtype, g_direct, ws + L.w_gate, &p.b[0], stream));
-  VCOLL_TRY(lay(w_up, F, D, w_up_ld, dtype, u_direct, ws + L.w_up, &p.b[1], stream));
+  Packer pack(dtype);
+  VCOLL_TRY(pack.add(x, N, D, x_ld, x_direct, ws + L.x, false, &p.a));
+  VCOLL_TRY(pack.add(w_gate, F, D, w_gate_ld, g_direct, ws + L.w_gate, false, &p.b[0]));
+  VCOLL_TRY(pack.add(w_up, F, D, w_up_ld, u_direct, ws + L.w_up, false, &p.b[1]));
+  VCOLL_TRY(pack.run(stream));
   p.M = N;
   p.N = F;
   p.K = D;
@@ -537,6 +582,8 @@ int vcoll_gated_ff(const void* x, int64_t x_ld, const void* w_gate, int64_t w_ga
   p.up = up;
   p.up_ld = up_ld;
   p.act = activation;
+  p.out_pairs = in_pairs(h, N, h_ld, dtype) && (!gate || in_pairs(gate, N, gate_ld, dtype)) &&
+                (!up || in_pairs(up, N, up_ld, dtype));
   return product(MM_GATED, false, &p, ws + L.splits, stream);
 }
 
@@ -591,18 +638,27 @@ int vcoll_gated_ff_backward(const void* dh, int64_t dh_ld, const void* x, int64_
     g.f32 = dtype == VCOLL_F32;
     g.parts = parts;
     g.act = activation;
+    g.load16 = rows_at_16(dh, N, dh_ld, es) && rows_at_16(gate, N, gate_ld, es) && rows_at_16(up, N, up_ld, es);
     int sms = 0;
     VCOLL_TRY(device_sms(&sms));
     VCOLL_TRY(launch_grid(mm_gated_grad_kernel(),
-                          std::min<int64_t>(ceil_div(N * L.half, kPassThreads), (int64_t)sms * 8), 1,
+                          std::min<int64_t>(ceil_div(N * (L.half / 8), kPassThreads), (int64_t)sms * 8), 1,
                           kPassThreads, 0, &g, stream));
   }
   const MmOperand grads = operand(ws + L.grads, N, 2 * L.half, 2 * L.half, N * 2 * L.half);
+  MmOperand rows, gates, ups;
+  Packer pack(dtype);
+  if (weights) VCOLL_TRY(pack.add(x, F ? N : 0, D, x_ld, x_direct, ws + L.x, false, &rows));
+  if (dx) {
+    VCOLL_TRY(pack.add(w_gate, N ? F : 0, D, w_gate_ld, g_direct, ws + L.w_gate, false, &gates));
+    VCOLL_TRY(pack.add(w_up, N ? F : 0, D, w_up_ld, u_direct, ws + L.w_up, false, &ups));
+  }
+  VCOLL_TRY(pack.run(stream));
   if (dx) {
     MmParams p = {};
     p.a = grads;
-    VCOLL_TRY(lay(w_gate, N ? F : 0, D, w_gate_ld, dtype, g_direct, ws + L.w_gate, &p.b[0], stream));
-    VCOLL_TRY(lay(w_up, N ? F : 0, D, w_up_ld, dtype, u_direct, ws + L.w_up, &p.b[1], stream));
+    p.b[0] = gates;
+    p.b[1] = ups;
     p.M = N;
     p.N = D;
     p.K = 2 * L.half;
@@ -611,28 +667,34 @@ int vcoll_gated_ff_backward(const void* dh, int64_t dh_ld, const void* x, int64_
     p.out = dx;
     p.out_ld = dx_ld;
     p.out_f32 = dtype == VCOLL_F32;
+    p.out_pairs = in_pairs(dx, N, dx_ld, dtype);
     VCOLL_TRY(product(MM_OUT, false, &p, ws + L.splits, stream));
   }
-  if (weights) {
-    MmOperand rows;
-    VCOLL_TRY(lay(x, F ? N : 0, D, x_ld, dtype, x_direct, ws + L.x, &rows, stream));
-    for (int k = 0; k < 2; ++k) {
-      void* out = k ? dw_up : dw_gate;
-      if (!out) continue;
-      MmParams p = {};
-      p.a = grads;
-      p.a.p = ws + L.grads + (size_t)k * L.half * 2;
-      p.a.cols = F;
-      p.b[0] = rows;
-      p.M = F;
-      p.N = D;
-      p.K = N;
-      p.parts = parts;
-      p.out = out;
-      p.out_ld = k ? dw_up_ld : dw_gate_ld;
-      p.out_f32 = dtype == VCOLL_F32;
-      VCOLL_TRY(product(MM_OUT, true, &p, ws + L.splits, stream));
+  if (weights) {  // both as one product, or the one that is wanted
+    const bool both = dw_gate && dw_up;
+    MmParams p = {};
+    p.a = grads;
+    if (!both) {
+      p.a.p = ws + L.grads + (dw_gate ? 0 : (size_t)L.half * 2);
+      p.a.cols = L.half;
     }
+    p.b[0] = rows;
+    p.M = both ? 2 * L.half : F;
+    p.N = D;
+    p.K = N;
+    p.parts = parts;
+    p.out = dw_gate ? dw_gate : dw_up;
+    p.out_ld = dw_gate ? dw_gate_ld : dw_up_ld;
+    p.out_f32 = dtype == VCOLL_F32;
+    p.out_pairs = in_pairs(p.out, F, p.out_ld, dtype);
+    if (both) {
+      p.out2 = dw_up;
+      p.out2_ld = dw_up_ld;
+      p.M1 = L.half;
+      p.M2 = F;
+      p.out_pairs = p.out_pairs && in_pairs(dw_up, F, dw_up_ld, dtype);
+    }
+    VCOLL_TRY(product(MM_OUT, true, &p, ws + L.splits, stream));
   }
   return VCOLL_OK;
 }
