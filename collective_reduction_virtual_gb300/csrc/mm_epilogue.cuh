@@ -1,10 +1,12 @@
 // What becomes of a tile of a product (MmEpilogue), a warp for 32 of its rows.
 //
 // The accumulators arrive as the tensor cores leave them: a lane holds a row,
-// 32 columns at a time.  What goes along a row (exponentials, activations, a
-// row's maximum and sum) is done there, in registers.  What is stored goes
-// through a 32 x 33 block of shared memory, so that a warp writes 128 adjacent
-// bytes of one row after the other.
+// 32 columns at a time.  What goes along a row (its maximum and sum, what its
+// target decides) is done there, in registers.  What is stored goes through a 32
+// x 33 block of shared memory, after which a lane holds two adjacent columns of
+// every second row: a warp's stores are 64 or 128 adjacent bytes of two rows.
+// The loops are kept short rather than unrolled: a tile's first pass through
+// them waits for instructions (4000 of them took longer than a small product).
 #pragma once
 
 #include "device_common.cuh"
@@ -81,16 +83,6 @@ __device__ __forceinline__ void mm_act(int act, float g, float& s, float& ds) {
   }
 }
 
-template <int ACT>
-__device__ __forceinline__ void mm_gate(float (&g)[32], const float (&u)[32]) {
-#pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    float s, ds;
-    mm_act(ACT, g[j], s, ds);
-    g[j] *= s * u[j];
-  }
-}
-
 // Where a row of the result goes.
 struct MmOutRow {
   void* out;
@@ -106,120 +98,144 @@ __device__ __forceinline__ int mm_rows(const MmParams& p, int64_t row0) {
   return (int)(end - row0 < 32 ? end - row0 : 32);
 }
 
-// A warp's block by rows: for the rows r < rows, x = load(r, word) eight at a
-// time, then store(r, x).
-template <class Load, class Store>
-__device__ __forceinline__ void mm_by_rows(const uint32_t* block, int lane, int rows, bool mine, Load load,
-                                           Store store) {
-  __syncwarp();
-  if (mine) {
-    for (int r = 0; r < rows; r += 8) {
-      float x[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (r + i < rows) x[i] = load(r + i, block[(r + i) * kMmPitch + lane]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (r + i < rows) store(r + i, x[i]);
-    }
+// Two adjacent values of a row: at most `left` of them are the result's.  wide:
+// they can be moved at once.
+__device__ __forceinline__ void mm_store2(void* p, int f32, int wide, int64_t i, int64_t left, float x, float y) {
+  if (wide && left > 1) {
+    if (f32)
+      *reinterpret_cast<float2*>(static_cast<float*>(p) + i) = make_float2(x, y);
+    else
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p) + i) = mm_narrow2(x, y);
+  } else {
+    if (left > 0) mm_store(p, f32, i, x);
+    if (left > 1) mm_store(p, f32, i + 1, y);
   }
+}
+__device__ __forceinline__ float2 mm_load2(const void* p, int f32, int wide, int64_t i, int64_t left) {
+  float2 v = make_float2(0.0f, 0.0f);
+  if (wide && left > 1) {
+    if (f32)
+      v = *reinterpret_cast<const float2*>(static_cast<const float*>(p) + i);
+    else
+      Elem<__nv_bfloat16>::widen2(*reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + i), v.x, v.y);
+  } else {
+    if (left > 0) v.x = mm_load(p, f32, i);
+    if (left > 1) v.y = mm_load(p, f32, i + 1);
+  }
+  return v;
+}
+
+__device__ __forceinline__ void mm_to_block(float* block, int lane, const float (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) block[lane * kMmPitch + j] = v[j];
   __syncwarp();
 }
 
-// 64 columns of bf16, two to a word, into rows that allow 4-byte stores.
-__device__ __forceinline__ void mm_store_pairs(uint32_t* block, int lane, const float (&a)[32],
-                                               const float (&b)[32], int rows, uint16_t* to, int64_t ld,
-                                               int64_t left) {
+// 64 columns as bf16, two to a word: a warp's stores are 128 adjacent bytes of a
+// row (with 64 bytes of two rows the block's training batch took 4 % longer).
+__device__ __forceinline__ void mm_store_64(float* block, int lane, const float (&a)[32], const float (&b)[32],
+                                            int rows, uint16_t* to, int64_t ld, int64_t left) {
+  uint32_t* words = reinterpret_cast<uint32_t*>(block);
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    block[lane * kMmPitch + j] = mm_narrow2(a[2 * j], a[2 * j + 1]);
-    block[lane * kMmPitch + 16 + j] = mm_narrow2(b[2 * j], b[2 * j + 1]);
+    words[lane * kMmPitch + j] = mm_narrow2(a[2 * j], a[2 * j + 1]);
+    words[lane * kMmPitch + 16 + j] = mm_narrow2(b[2 * j], b[2 * j + 1]);
   }
   __syncwarp();
-  uint16_t* at = to + 2 * lane;
+  to += 2 * lane;
   if (2 * lane + 1 < left) {
-    if (rows >= 32) {
-#pragma unroll
-      for (int r = 0; r < 32; ++r)
-        *reinterpret_cast<uint32_t*>(at + r * ld) = block[r * kMmPitch + lane];
-    } else {
-      for (int r = 0; r < rows; ++r)
-        *reinterpret_cast<uint32_t*>(at + r * ld) = block[r * kMmPitch + lane];
-    }
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r, to += ld) *reinterpret_cast<uint32_t*>(to) = words[r * kMmPitch + lane];
   } else if (2 * lane < left) {
-    for (int r = 0; r < rows; ++r) at[r * ld] = (uint16_t)block[r * kMmPitch + lane];
+    for (int r = 0; r < rows; ++r, to += ld) *to = (uint16_t)words[r * kMmPitch + lane];
   }
   __syncwarp();
 }
 
-// 32 columns, a store for each value.
-__device__ __forceinline__ void mm_store_each(uint32_t* block, int lane, const float (&v)[32], int rows,
-                                              void* to, int f32, int64_t at, int64_t ld, int64_t left) {
+template <int ACT>
+__device__ __forceinline__ void mm_gate(float (&g)[32], const float (&u)[32]) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) block[lane * kMmPitch + j] = __float_as_uint(v[j]);
-  mm_by_rows(
-      block, lane, rows, lane < left, [](int, uint32_t w) { return __uint_as_float(w); },
-      [&](int r, float x) { mm_store(to, f32, at + r * ld + lane, x); });
-}
-
-// 64 columns of a matrix of the operator's type.
-__device__ __forceinline__ void mm_store_64(uint32_t* block, int lane, const float (&a)[32], const float (&b)[32],
-                                            int rows, void* to, int f32, int pairs, int64_t row, int64_t ld,
-                                            int64_t col, int64_t cols) {
-  const int64_t at = row * ld + col;
-  if (pairs) {
-    mm_store_pairs(block, lane, a, b, rows, static_cast<uint16_t*>(to) + at, ld, cols - col);
-  } else {
-    mm_store_each(block, lane, a, rows, to, f32, at, ld, cols - col);
-    mm_store_each(block, lane, b, rows, to, f32, at + 32, ld, cols - col - 32);
+  for (int j = 0; j < 32; ++j) {
+    float s, ds;
+    mm_act(ACT, g[j], s, ds);
+    g[j] *= s * u[j];
   }
 }
 
-// src(c0, c1, a, b): columns c0 .. c0 + 31 and c1 .. c1 + 31 of this lane's row of
-// the tile, called by the whole warp.  row0: the warp's first row of the result.
+// src(c, v): columns c .. c + 31 of this lane's row of the tile, called by the
+// whole warp; columns c0 .. c1 - 1 are this warp's.  row0: its first row of the
+// result.  In the block a lane takes two adjacent columns of every second row.
 template <int EPI, class Source>
-__device__ __forceinline__ void mm_epilogue(const MmParams& p, int64_t row0, int64_t tile_n, int lane,
-                                            uint32_t* block, Source src) {
+__device__ __forceinline__ void mm_epilogue(const MmParams& p, int64_t row0, int64_t tile_n, int c0, int c1,
+                                            int lane, float* block, Source src) {
   const int64_t row = row0 + lane;
   const int rows = mm_rows(p, row0);  // < 1: only src is called
-  float a[32], b[32];
+  const int pair = (lane & 15) * 2, odd = lane >> 4;
+  float v[32];
   if constexpr (EPI == MM_OUT) {
     const float scale = p.scale ? *p.scale : 1.0f;
     const MmOutRow to = mm_out_row(p, row0);
-    for (int c = 0; c < p.tn; c += 64) {
-      const int64_t col = tile_n * p.tn + c;
-      src(c, c + 32, a, b);
-      if (col >= p.N) continue;
-      if (!p.accum_in && !p.accum_out && !p.base) {
+    const bool add = p.accum_in || p.accum_out || p.base;
+    if (!add && !p.out_f32 && p.out_pairs) {
+      float w[32];
+      for (int c = c0; c < c1; c += 64) {
+        const int64_t col = tile_n * p.tn + c;
+        src(c, v);
+        src(c + 32, w);
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          a[j] *= scale;
-          b[j] *= scale;
+          v[j] *= scale;
+          w[j] *= scale;
         }
-        mm_store_64(block, lane, a, b, rows, to.out, p.out_f32, p.out_pairs, to.row, to.ld, col, p.N);
-        continue;
+        mm_store_64(block, lane, v, w, rows, static_cast<uint16_t*>(to.out) + to.row * to.ld + col, to.ld, p.N - col);
       }
+      return;
+    }
+    for (int c = c0; c < c1; c += 32) {
+      const int64_t col = tile_n * p.tn + c + pair, left = p.N - col;
+      src(c, v);
+      mm_to_block(block, lane, v);
+      if (!add) {
+#pragma unroll 4
+        for (int r = odd; r < rows; r += 2)
+          mm_store2(to.out, p.out_f32, p.out_pairs, (to.row + r) * to.ld + col, left,
+                    block[r * kMmPitch + pair] * scale, block[r * kMmPitch + pair + 1] * scale);
+      } else {
+        // what is added is fetched eight rows at a time: a load waits longer than
+        // all else here takes
+        for (int r = odd; r < rows; r += 16) {
+          float2 x[8];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+          for (int i = 0; i < 8; ++i) {
+            x[i] = make_float2(0.0f, 0.0f);
+            if (r + 2 * i < rows) {
+              if (p.accum_in)
+                x[i] = mm_load2(p.accum_in, 1, 1, (row0 + r + 2 * i) * p.accum_ld + col, left);
+              else if (p.base)
+                x[i] = mm_load2(p.base, p.out_f32, p.out_pairs, (to.row + r + 2 * i) * p.base_ld + col, left);
+            }
+          }
 #pragma unroll
-        for (int j = 0; j < 32; ++j) block[lane * kMmPitch + j] = __float_as_uint(h ? b[j] : a[j]);
-        const int64_t at = col + 32 * h + lane;
-        mm_by_rows(
-            block, lane, rows, at < p.N,
-            [&](int r, uint32_t w) {
-              float x = __uint_as_float(w);
-              if (p.accum_in) x += p.accum_in[(row0 + r) * p.accum_ld + at];
-              if (!p.accum_out) x *= scale;
-              if (p.base) x += mm_load(p.base, p.out_f32, (to.row + r) * p.base_ld + at);
-              return x;
-            },
-            [&](int r, float x) {
-              if (p.accum_out)
-                p.accum_out[(row0 + r) * p.accum_ld + at] = x;
-              else
-                mm_store(to.out, p.out_f32, (to.row + r) * to.ld + at, x);
-            });
+          for (int i = 0; i < 8; ++i) {
+            const int at = r + 2 * i;
+            if (at >= rows) break;
+            float2 y = make_float2(block[at * kMmPitch + pair], block[at * kMmPitch + pair + 1]);
+            if (p.base) {
+              y.x = y.x * scale + x[i].x;
+              y.y = y.y * scale + x[i].y;
+            } else {
+              const float s = p.accum_out ? 1.0f : scale;
+              y.x = (x[i].x + y.x) * s;
+              y.y = (x[i].y + y.y) * s;
+            }
+            if (p.accum_out)
+              mm_store2(p.accum_out, 1, 1, (row0 + at) * p.accum_ld + col, left, y.x, y.y);
+            else
+              mm_store2(to.out, p.out_f32, p.out_pairs, (to.row + at) * to.ld + col, left, y.x, y.y);
+          }
+        }
       }
+      __syncwarp();
     }
   } else if constexpr (EPI == MM_LSE) {
     // exponentials to base 2 of z log2(e), relative to a row's largest so far
@@ -227,41 +243,34 @@ __device__ __forceinline__ void mm_epilogue(const MmParams& p, int64_t row0, int
     if (lane < rows) t = mm_token(p.targets, p.idx64, row);
     const int64_t hit = t >= 0 && t < p.V ? t - p.token0 - tile_n * p.tn : -1;
     float m = -INFINITY, s = 0.0f;
-    for (int c = 0; c < p.tn; c += 64) {
-      src(c, c + 32, a, b);
+    for (int c = c0; c < c1; c += 32) {
+      src(c, v);
       const int64_t left = p.N - tile_n * p.tn - c;
-      if (hit >= c && hit < c + 64) {
+      if (hit >= c && hit < c + 32) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          if (hit == c + j) p.picked[row] = a[j];
-          if (hit == c + 32 + j) p.picked[row] = b[j];
-        }
+        for (int j = 0; j < 32; ++j)
+          if (hit == c + j) p.picked[row] = v[j];
       }
-      if (left < 64) {
+      if (left < 32) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          if (j >= left) a[j] = -INFINITY;
-          if (j + 32 >= left) b[j] = -INFINITY;
-        }
+        for (int j = 0; j < 32; ++j)
+          if (j >= left) v[j] = -INFINITY;
       }
-      float top = fmaxf(a[0], b[0]);
+      float top = v[0];
 #pragma unroll
-      for (int j = 1; j < 32; ++j) top = fmaxf(top, fmaxf(a[j], b[j]));
+      for (int j = 1; j < 32; ++j) top = fmaxf(top, v[j]);
       top *= kMmLog2e;
       if (top > m) {
         s *= mm_exp2(m - top);
         m = top;
       }
       const float ref = m == -INFINITY ? 0.0f : m;  // no difference of infinities
-      float sa = 0.0f, sb = 0.0f;
+      float part[4] = {};
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        sa += mm_exp2(fmaf(a[j], kMmLog2e, -ref));
-        sb += mm_exp2(fmaf(b[j], kMmLog2e, -ref));
-      }
-      s += sa + sb;
+      for (int j = 0; j < 32; ++j) part[j % 4] += mm_exp2(fmaf(v[j], kMmLog2e, -ref));
+      s += (part[0] + part[1]) + (part[2] + part[3]);
     }
-    if (lane < rows) p.part[tile_n * p.M + row] = make_float2(m, s);
+    if (lane < rows && c0 < c1) p.part[(tile_n * (p.tn / (c1 - c0)) + (c0 ? 1 : 0)) * p.M + row] = make_float2(m, s);
   } else if constexpr (EPI == MM_ERROR) {
     int64_t hit = -1;
     float lse = 0.0f, w = 0.0f;  // of a masked row, whose logits are zeros
@@ -273,60 +282,85 @@ __device__ __forceinline__ void mm_epilogue(const MmParams& p, int64_t row0, int
         w = p.dloss[row * p.dloss_step] / *p.scale;
       }
     }
-    for (int c = 0; c < p.tn; c += 64) {
+    float x[32];
+    for (int c = c0; c < c1; c += 64) {
       const int64_t col = tile_n * p.tn + c;
-      src(c, c + 32, a, b);
-      if (col >= p.N) continue;
+      src(c, v);
+      src(c + 32, x);
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
-        a[j] = mm_exp(a[j] - lse);
-        b[j] = mm_exp(b[j] - lse);
+        v[j] = mm_exp(v[j] - lse);
+        x[j] = mm_exp(x[j] - lse);
       }
       if (hit >= c && hit < c + 64) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          if (hit == c + j) a[j] -= 1.0f;
-          if (hit == c + 32 + j) b[j] -= 1.0f;
+          if (hit == c + j) v[j] -= 1.0f;
+          if (hit == c + 32 + j) x[j] -= 1.0f;
         }
       }
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
-        a[j] *= w;
-        b[j] *= w;
+        v[j] *= w;
+        x[j] *= w;
       }
-      for (int k = 0; k < p.parts; ++k) {
-        mm_store_pairs(block, lane, a, b, rows, static_cast<uint16_t*>(p.error) + k * p.error_plane + row0 * p.error_ld + col,
-                       p.error_ld, p.N - col);
-        if (k + 1 < p.parts) {  // what is left for the next part
+      for (int k = 0; k < p.parts; ++k) {  // a part, and what it leaves for the next
+        mm_store_64(block, lane, v, x, rows,
+                    static_cast<uint16_t*>(p.error) + k * p.error_plane + row0 * p.error_ld + col, p.error_ld,
+                    p.N - col);
+        if (k + 1 < p.parts) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            a[j] -= Elem<__nv_bfloat16>::widen1(mm_narrow(a[j]));
-            b[j] -= Elem<__nv_bfloat16>::widen1(mm_narrow(b[j]));
+            v[j] -= Elem<__nv_bfloat16>::widen1(mm_narrow(v[j]));
+            x[j] -= Elem<__nv_bfloat16>::widen1(mm_narrow(x[j]));
           }
         }
       }
     }
-  } else {
+  } else if (!p.out_f32 && p.out_pairs && p.act != VCOLL_GELU) {
     const int half = p.tn / 2;
-    for (int c = 0; c < half; c += 64) {
-      const int64_t col = tile_n * half + c;
-      float d[32], e[32];
-      src(c, half + c, a, b);
-      src(c + 32, half + c + 32, d, e);
-      if (col >= p.N) continue;
-      if (p.gate) mm_store_64(block, lane, a, d, rows, p.gate, p.out_f32, p.out_pairs, row0, p.gate_ld, col, p.N);
-      if (p.up) mm_store_64(block, lane, b, e, rows, p.up, p.out_f32, p.out_pairs, row0, p.up_ld, col, p.N);
-      if (p.act == VCOLL_SILU) {
-        mm_gate<VCOLL_SILU>(a, b);
-        mm_gate<VCOLL_SILU>(d, e);
-      } else if (p.act == VCOLL_GELU) {
-        mm_gate<VCOLL_GELU>(a, b);
-        mm_gate<VCOLL_GELU>(d, e);
-      } else {
-        mm_gate<VCOLL_GELU_TANH>(a, b);
-        mm_gate<VCOLL_GELU_TANH>(d, e);
+    float w[32], u[32];
+    for (int c = c0 / 2; c < c1 / 2; c += 64) {
+      const int64_t col = tile_n * half + c, left = p.N - col;
+      for (int k = 0; k < 2; ++k) {  // tensor memory is read again rather than held
+        uint16_t* to = static_cast<uint16_t*>(k ? p.up : p.gate);
+        const int64_t ld = k ? p.up_ld : p.gate_ld;
+        if (!to) continue;
+        src(k * half + c, v);
+        src(k * half + c + 32, w);
+        mm_store_64(block, lane, v, w, rows, to + row0 * ld + col, ld, left);
       }
-      mm_store_64(block, lane, a, d, rows, p.out, p.out_f32, p.out_pairs, row0, p.out_ld, col, p.N);
+      src(c, v);
+      src(half + c, u);
+      if (p.act == VCOLL_SILU) mm_gate<VCOLL_SILU>(v, u);
+      else mm_gate<VCOLL_GELU_TANH>(v, u);
+      src(c + 32, w);
+      src(half + c + 32, u);
+      if (p.act == VCOLL_SILU) mm_gate<VCOLL_SILU>(w, u);
+      else mm_gate<VCOLL_GELU_TANH>(w, u);
+      mm_store_64(block, lane, v, w, rows, static_cast<uint16_t*>(p.out) + row0 * p.out_ld + col, p.out_ld, left);
+    }
+  } else {
+    // (the exact gelu's code is too long to be repeated for 64 columns)
+    // 16 columns of gate and the same of up beside each other; a lane takes two
+    // of them in every fourth row
+    const int half = p.tn / 2, two = (lane & 7) * 2, quarter = lane >> 3;
+    for (int c = c0 / 2; c < c1 / 2; c += 16) {
+      const int64_t col = tile_n * half + c + two, left = p.N - col;
+      src(c, half + c, v);
+      mm_to_block(block, lane, v);
+#pragma unroll 2
+      for (int r = quarter; r < rows; r += 4) {
+        const float* at = block + r * kMmPitch + two;
+        const float g0 = at[0], g1 = at[1], u0 = at[16], u1 = at[17];
+        float s0, s1, ds;
+        mm_act(p.act, g0, s0, ds);
+        mm_act(p.act, g1, s1, ds);
+        if (p.gate) mm_store2(p.gate, p.out_f32, p.out_pairs, (row0 + r) * p.gate_ld + col, left, g0, g1);
+        if (p.up) mm_store2(p.up, p.out_f32, p.out_pairs, (row0 + r) * p.up_ld + col, left, u0, u1);
+        mm_store2(p.out, p.out_f32, p.out_pairs, (row0 + r) * p.out_ld + col, left, g0 * (s0 * u0), g1 * (s1 * u1));
+      }
+      __syncwarp();
     }
   }
 }

@@ -38,15 +38,16 @@ struct MmParams {
   int64_t K;      // length of the sum
   int64_t K1;     // the sum's places from here on take b[1] (K: none)
   int parts;      // 1, or 3: six products of the parts
+  uint32_t depth;  // steps of kMmDepth places
   int b_halves;   // the tile's columns are half b[0]'s and half b[1]'s (MM_GATED)
   int tn;         // columns of a tile
-  int64_t tiles_m, tiles_n;
+  uint32_t tiles_m, tiles_n;
   int tile_rows;      // 128, or 256 of a pair of CTAs
   int a_rows;         // of a stage's a: 128, or fewer where M is smaller
-  int stages, stage_bytes;
-  int splits;         // that a tile's sum is cut into
+  uint32_t splits;      // that a tile's sum is cut into
+  uint32_t units;       // tiles times splits
+  uint32_t join_blocks;  // CTAs of the splits' join
   float* partial;     // of splits: tiles x splits x min(M, rows of a tile) x tn
-  unsigned* error_word;
   // MM_OUT
   void* out;
   int64_t out_ld;
@@ -59,13 +60,13 @@ struct MmParams {
   const void* base;       // of out's type and stride base_ld
   int64_t base_ld;
   int out_f32;
-  int out_pairs;          // two bf16 columns can be stored at once
+  int out_pairs;          // two adjacent columns can be moved at once
   // MM_LSE, MM_ERROR: column j is token token0 + j of V
   const void* targets;
   const float* dloss;
   int64_t dloss_step;  // 0 or 1
   const float* lse;
-  float2* part;        // tiles_n x M
+  float2* part;        // 2 tiles_n x M: of each half of a tile's columns
   float* picked;       // M: the target's logit
   int64_t token0, V;
   int idx64;
@@ -75,6 +76,18 @@ struct MmParams {
   void *gate, *up;
   int64_t gate_ld, up_ld;
   int act;
+};
+
+// One launch.  p[0]: the product.  With MM_OUT, which takes b transposed, p[1] is
+// another, independent one, which takes a transposed too, and the tiles of both
+// fill the GPU together; either may be absent (units 0).  The CTAs (or pairs) take
+// p[0]'s units in turn; those that have one fewer of them take `ahead` of p[1]'s
+// before all take the rest in turn.
+struct MmLaunch {
+  MmParams p[2];
+  int stages, stage_bytes;
+  uint32_t ahead;
+  unsigned* error_word;
 };
 
 // The six products of three parts that reach an fp32 result's precision, the
@@ -91,7 +104,7 @@ constexpr int kMmTileN = 256;
 constexpr int kMmDepth = 64;
 constexpr int kMmStageRoom = 192 * 1024;
 constexpr int kMmMaxStages = 12;
-constexpr int kMmEpilogueWarps = 4;
+constexpr int kMmEpilogueWarps = 8;  // four for the 128 rows, twice: each takes half of the columns
 constexpr int kMmThreads = (kMmEpilogueWarps + 2) * 32;
 constexpr int kMmPitch = 33;  // words of a row of a warp's block of 32 x 32
 constexpr int kMmBlockWords = 32 * kMmPitch;
@@ -142,8 +155,8 @@ struct MmGatedGradParams {
   int load16;  // the rows of dh, gate and up start at 16-byte boundaries
 };
 
-// MM_OUT takes b transposed, and a where a_mn is set; ctas that share a tile: 1 or 2
-const void* mm_kernel(MmEpilogue epilogue, bool a_mn, int ctas);
+// ctas that share a tile: 1 or 2
+const void* mm_kernel(MmEpilogue epilogue, int ctas);
 const void* mm_join_splits_kernel(MmEpilogue epilogue);
 const void* mm_pack_kernel();
 const void* mm_join_kernel();

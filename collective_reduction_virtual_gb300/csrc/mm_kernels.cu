@@ -5,7 +5,7 @@
 // and up to 256 columns.  A warp's lane fills stages of shared memory by TMA, 64
 // places of the sum at a time; a lane of another warp (of a pair: of its first
 // CTA) issues the tcgen05 products of the stages that have arrived, with the
-// accumulators in tensor memory; four more warps take a finished tile from there
+// accumulators in tensor memory; eight more warps take a finished tile from there
 // (mm_epilogue.cuh) while the next one is being summed into the other half of
 // the 512 columns.  Each CTA of a pair holds half of the columns' operand, which
 // the products of both read: that takes a third less from L2 and shared memory.
@@ -22,40 +22,243 @@ namespace {
 
 // Tiles in groups of 2048 rows: the tiles that are in flight together share their
 // operands through the L2.
-__device__ __forceinline__ void tile_at(const MmParams& p, int tile_rows, int64_t tile, int64_t& m, int64_t& n) {
-  const int64_t group = 2048 / tile_rows, per = group * p.tiles_n;
-  const int64_t g = tile / per, in = tile % per;
-  const int64_t rows = p.tiles_m - g * group < group ? p.tiles_m - g * group : group;
-  m = g * group + in % rows;
+__device__ __forceinline__ void tile_at(const MmParams& p, int tile_rows, uint32_t tile, uint32_t& m, uint32_t& n) {
+  const uint32_t group = 2048 / tile_rows, per = group * p.tiles_n;
+  const uint32_t g = tile / per, in = tile - g * per;
+  const uint32_t rows = p.tiles_m - g * group < group ? p.tiles_m - g * group : group;
   n = in / rows;
+  m = g * group + in - n * rows;
+}
+
+// What a CTA (or pair) does n-th: a unit of one of the launch's products.
+struct Unit {
+  bool second;
+  uint32_t at;
+};
+template <bool TWO>
+__device__ __forceinline__ bool unit_at(const MmLaunch& all, uint32_t me, uint32_t of, uint32_t n, Unit& u) {
+  const uint32_t units = all.p[0].units;
+  if (!TWO) {
+    u = {false, n * of + me};
+    return u.at < units;
+  }
+  const uint32_t more = units % of, mine = units / of + (me < more);
+  if (n < mine) {
+    u = {false, n * of + me};
+    return true;
+  }
+  n -= mine;
+  u.second = true;
+  if (me >= more && n < all.ahead) {
+    u.at = n * (of - more) + me - more;
+  } else {
+    if (me >= more) n -= all.ahead;
+    u.at = all.ahead * (of - more) + n * of + me;
+  }
+  return u.at < all.p[1].units;
+}
+
+// The steps of a unit, a split of a tile: every pair of parts has `depth` of them.
+__device__ __forceinline__ void steps_of(const MmParams& p, uint32_t unit, uint32_t& tile, uint32_t& begin,
+                                         uint32_t& end) {
+  const uint32_t steps = mm_pairs(p.parts) * p.depth;
+  tile = unit;
+  begin = 0;
+  end = steps;
+  if (p.splits > 1) {
+    tile = unit / p.splits;
+    const uint32_t split = unit - tile * p.splits;  // 16 at most, of steps below 2^28
+    begin = steps * split / p.splits;
+    end = steps * (split + 1) / p.splits;
+  }
+}
+
+// Where a CTA's parts lie in shared memory, and its place in a pair.
+struct Place {
+  uint32_t stage0, full, empty, acc_full, acc_empty, drained;
+  uint32_t rank, tmem;
+  int stages, stage_bytes;
+  MmAbort guard;
+};
+struct Ring {
+  int stage = 0;
+  uint32_t round = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++stage == stages) {
+      stage = 0;
+      ++round;
+    }
+  }
+};
+
+// A unit's copies into the ring; the number of stages that were filled.
+template <int EPI, int CTAS, bool A_MN>
+__device__ __forceinline__ uint32_t load_unit(const MmParams& p, uint32_t unit, const Place& at, Ring& ring) {
+  constexpr int TILE_ROWS = kMmRows * CTAS;
+  constexpr bool B_MN = EPI == MM_OUT;
+  const int cols = p.tn / CTAS;  // of b that this CTA holds
+  const int stage_a = p.a_rows * kMmDepth * 2;
+  const uint32_t bytes = (uint32_t)CTAS * (stage_a + cols * kMmDepth * 2);
+  const int pairs = mm_pairs(p.parts);
+  const uint32_t depth = p.depth, second = (uint32_t)(p.K1 / kMmDepth);  // the first step that takes map_b[1]
+  uint32_t tile, tm, tn, begin, end;
+  steps_of(p, unit, tile, begin, end);
+  tile_at(p, TILE_ROWS, tile, tm, tn);
+  int q = pairs > 1 ? (int)(begin / depth) : 0;
+  uint32_t k = begin - q * depth;
+  const int row = (int)(tm * TILE_ROWS + at.rank * kMmRows);
+  const int col = EPI == MM_GATED ? (int)(tn * (p.tn / 2)) : (int)(tn * p.tn + at.rank * cols);
+  for (uint32_t i = begin; i < end; ++i) {
+    if (ring.round && !mm_bar_wait(at.empty + 8 * ring.stage, (ring.round - 1) & 1, at.guard)) return i - begin;
+    const uint32_t a = at.stage0 + ring.stage * at.stage_bytes, b = a + stage_a;
+    uint32_t bar = at.full + 8 * ring.stage;
+    if (at.rank == 0) mm_bar_expect(bar, bytes);
+    if (CTAS > 1) bar = mm_of_first(bar);
+    const int pa = mm_pair_a(pairs, q), pb = mm_pair_b(pairs, q);
+    const int kk = (int)(k * kMmDepth);
+    if (A_MN) {
+#pragma unroll
+      for (int c = 0; c < kMmRows / 64; ++c)
+        mm_load_box<CTAS>(a + c * 8192, &p.map_a, row + 64 * c, kk, pa, bar);
+    } else {
+      mm_load_box<CTAS>(a, &p.map_a, kk, row, pa, bar);
+    }
+    if (EPI == MM_GATED && CTAS == 2) {
+      mm_load_box<CTAS>(b, at.rank ? &p.map_b[1] : &p.map_b[0], kk, col, pb, bar);
+    } else if (EPI == MM_GATED) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        mm_load_box<CTAS>(b + h * (p.tn / 2) * kMmDepth * 2, &p.map_b[h], kk, col, pb, bar);
+    } else if (B_MN) {
+      const bool other = k >= second;
+      const CUtensorMap* map = other ? &p.map_b[1] : &p.map_b[0];
+      const int kb = other ? kk - (int)p.K1 : kk;
+#pragma unroll
+      for (int c = 0; c < kMmTileN / CTAS / 64; ++c)
+        if (64 * c < cols) mm_load_box<CTAS>(b + c * 8192, map, col + 64 * c, kb, pb, bar);
+    } else {
+      mm_load_box<CTAS>(b, &p.map_b[0], kk, col, pb, bar);
+    }
+    if (++k == depth) {
+      k = 0;
+      ++q;
+    }
+    ring.next(at.stages);
+  }
+  return end - begin;
+}
+
+// A unit's products into the accumulators `acc`; false where a wait gave up.
+template <int EPI, int CTAS, bool A_MN>
+__device__ __forceinline__ bool multiply_unit(const MmParams& p, uint32_t unit, const Place& at, Ring& ring, int acc) {
+  constexpr bool B_MN = EPI == MM_OUT;
+  const uint32_t idesc = mm_idesc(A_MN, B_MN, kMmRows * CTAS, p.tn);
+  const int stage_a = p.a_rows * kMmDepth * 2;
+  const uint32_t d = at.tmem + acc * kMmTileN;
+  uint32_t tile, begin, end;
+  steps_of(p, unit, tile, begin, end);
+  for (uint32_t i = begin; i < end; ++i) {
+    if (!mm_bar_wait(at.full + 8 * ring.stage, ring.round & 1, at.guard)) return false;
+    mm_fence_after();
+    const uint32_t a = at.stage0 + ring.stage * at.stage_bytes;
+    const uint64_t da = mm_desc(a, A_MN), db = mm_desc(a + stage_a, B_MN);
+#pragma unroll
+    for (int j = 0; j < kMmDepth / 16; ++j)
+      mm_mma<CTAS>(d, da + j * mm_desc_step(A_MN), db + j * mm_desc_step(B_MN), idesc, i > begin || j > 0);
+    mm_commit<CTAS>(at.empty + 8 * ring.stage);
+    ring.next(at.stages);
+  }
+  mm_commit<CTAS>(at.acc_full + 8 * acc);
+  return true;
+}
+
+// A warp's accumulators in tensor memory; zeros where nothing was summed.
+struct TmemSource {
+  uint32_t at;
+  bool any;
+
+  __device__ __forceinline__ void give(const uint32_t (&r)[32], float (&v)[32]) const {
+    mm_tmem_wait();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = any ? __uint_as_float(r[j]) : 0.0f;
+  }
+  __device__ __forceinline__ void operator()(int c, float (&v)[32]) const {
+    uint32_t r[32];
+    mm_tmem_load(at + c, r);
+    give(r, v);
+  }
+  // 16 columns from c, and 16 from d
+  __device__ __forceinline__ void operator()(int c, int d, float (&v)[32]) const {
+    uint32_t r[32];
+    mm_tmem_load16(at + c, r);
+    mm_tmem_load16(at + d, r + 16);
+    give(r, v);
+  }
+};
+
+// A finished unit: its epilogue, or its sums left for the join.  A warp has 32 rows
+// and half of the columns, where a half has 64 of them.
+template <int EPI, int CTAS>
+__device__ __forceinline__ void finish_unit(const MmParams& p, uint32_t unit, const Place& at, int acc, int warp, int lane,
+                                            float* block) {
+  constexpr int TILE_ROWS = kMmRows * CTAS;
+  const int width = p.tn >= (EPI == MM_GATED ? 256 : 128) ? p.tn / 2 : p.tn;
+  const int c0 = warp / 4 * width, c1 = c0 < p.tn ? c0 + width : c0;
+  const int quarter = warp % 4;  // of tensor memory's lanes, which this warp can read
+  uint32_t tile = unit, tm, tn;
+  if (p.splits > 1) tile = unit / p.splits;
+  tile_at(p, TILE_ROWS, tile, tm, tn);
+  const TmemSource src = {at.tmem + ((uint32_t)(quarter * 32) << 16) + acc * kMmTileN, p.depth != 0};
+  const int in_tile = (int)at.rank * kMmRows + quarter * 32;
+  const int64_t row0 = (int64_t)tm * TILE_ROWS + in_tile;
+  if (p.splits == 1) {
+    mm_epilogue<EPI>(p, row0, tn, c0, c1, lane, block, src);
+    return;
+  }
+  const int64_t rows = p.M < TILE_ROWS ? p.M : TILE_ROWS;
+  float4* to = reinterpret_cast<float4*>(p.partial + (unit * rows + in_tile + lane) * p.tn);
+  for (int c = c0; c < c1; c += 32) {
+    float x[32];
+    src(c, x);
+    if (row0 + lane < p.M) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) to[c / 4 + j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+    }
+  }
 }
 
 }  // namespace
 
-template <int EPI, bool A_MN, bool B_MN, int CTAS>
-__global__ void __launch_bounds__(kMmThreads, 1) vc_mm(const __grid_constant__ MmParams p) {
+template <int EPI, int CTAS>
+__global__ void __launch_bounds__(kMmThreads, 1) vc_mm(const __grid_constant__ MmLaunch all) {
   pdl_enter();
   extern __shared__ unsigned char raw[];
   __shared__ volatile int gave_up;
   __shared__ uint32_t tmem_at;
-  constexpr int TILE_ROWS = kMmRows * CTAS;
-  const uint32_t stage0 = (mm_smem(raw) + 1023) & ~1023u;  // of 128-byte swizzle atoms
-  const uint32_t blocks = stage0 + kMmStageRoom, bars = blocks + kMmEpilogueBytes;
-  const uint32_t full = bars, empty = bars + 8 * kMmMaxStages, acc_full = empty + 8 * kMmMaxStages,
-                 acc_empty = acc_full + 16, drained = acc_empty + 16;
+  constexpr bool TWO = EPI == MM_OUT;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t rank = CTAS == 1 ? 0 : mm_rank();
-  const MmAbort guard = {&gave_up, p.error_word};
+  Place at;
+  at.stage0 = (mm_smem(raw) + 1023) & ~1023u;  // of 128-byte swizzle atoms
+  const uint32_t blocks = at.stage0 + kMmStageRoom;
+  at.full = blocks + kMmEpilogueBytes;
+  at.empty = at.full + 8 * kMmMaxStages;
+  at.acc_full = at.empty + 8 * kMmMaxStages;
+  at.acc_empty = at.acc_full + 16;
+  at.drained = at.acc_empty + 16;
+  at.rank = CTAS == 1 ? 0 : mm_rank();
+  at.stages = all.stages;
+  at.stage_bytes = all.stage_bytes;
+  at.guard = {&gave_up, all.error_word};
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMmMaxStages; ++s) {
-      mm_bar_init(full + 8 * s, 1);
-      mm_bar_init(empty + 8 * s, 1);
+      mm_bar_init(at.full + 8 * s, 1);
+      mm_bar_init(at.empty + 8 * s, 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mm_bar_init(acc_full + 8 * s, 1);
-      mm_bar_init(acc_empty + 8 * s, kMmEpilogueWarps * CTAS);
+      mm_bar_init(at.acc_full + 8 * s, 1);
+      mm_bar_init(at.acc_empty + 8 * s, kMmEpilogueWarps * CTAS);
     }
-    mm_bar_init(drained, 1);
+    mm_bar_init(at.drained, 1);
     gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -64,156 +267,54 @@ __global__ void __launch_bounds__(kMmThreads, 1) vc_mm(const __grid_constant__ M
   __syncthreads();
   if (CTAS > 1) mm_cluster_sync();
   mm_fence_after();
-  const uint32_t tmem = tmem_at;
+  at.tmem = tmem_at;
 
-  const int64_t units = p.tiles_m * p.tiles_n * p.splits;
-  const int64_t first = blockIdx.x / CTAS, stride = gridDim.x / CTAS;
-  const int64_t depth = (p.K + kMmDepth - 1) / kMmDepth;  // steps of a sum
-  const int pairs = mm_pairs(p.parts);
-  const int64_t steps = pairs * depth;
-  const int stages = p.stages;
-  const int stage_a = p.a_rows * kMmDepth * 2;
-
+  const uint32_t me = blockIdx.x / CTAS, of = gridDim.x / CTAS;
+  Unit u;
   if (warp == kMmEpilogueWarps) {
     if (lane == 0) {
-      const int64_t second = p.K1 / kMmDepth;  // the first step that takes map_b[1]
-      const int cols = p.tn / CTAS;            // of b that this CTA holds
-      const uint32_t bytes = (uint32_t)CTAS * (stage_a + cols * kMmDepth * 2);
+      Ring ring;
       int64_t issued = 0;
-      int st = 0, round = 0;
-      for (int64_t u = first; u < units && !gave_up; u += stride) {
-        int64_t tm, tn;
-        tile_at(p, TILE_ROWS, u / p.splits, tm, tn);
-        const int64_t s = u % p.splits;
-        const int64_t begin = steps * s / p.splits, end = steps * (s + 1) / p.splits;
-        int q = depth ? (int)(begin / depth) : 0;
-        int64_t k = begin - q * depth;
-        const int row = (int)(tm * TILE_ROWS) + (int)rank * kMmRows;
-        const int col = EPI == MM_GATED ? (int)(tn * (p.tn / 2)) : (int)(tn * p.tn) + (int)rank * cols;
-        for (int64_t i = begin; i < end; ++i, ++issued) {
-          if (round && !mm_bar_wait(empty + 8 * st, (round - 1) & 1, guard)) break;
-          const uint32_t a = stage0 + st * p.stage_bytes, b = a + stage_a;
-          uint32_t bar = full + 8 * st;
-          if (rank == 0) mm_bar_expect(bar, bytes);
-          if (CTAS > 1) bar = mm_of_first(bar);
-          const int pa = mm_pair_a(pairs, q), pb = mm_pair_b(pairs, q);
-          const int kk = (int)(k * kMmDepth);
-          if (A_MN) {
-            for (int c = 0; c < kMmRows / 64; ++c)
-              mm_load_box<CTAS>(a + c * 8192, &p.map_a, row + 64 * c, kk, pa, bar);
-          } else {
-            mm_load_box<CTAS>(a, &p.map_a, kk, row, pa, bar);
-          }
-          if (EPI == MM_GATED && CTAS == 2) {
-            mm_load_box<CTAS>(b, &p.map_b[rank], kk, col, pb, bar);
-          } else if (EPI == MM_GATED) {
-            for (int h = 0; h < 2; ++h)
-              mm_load_box<CTAS>(b + h * (p.tn / 2) * kMmDepth * 2, &p.map_b[h], kk, col, pb, bar);
-          } else if (B_MN) {
-            const CUtensorMap* map = &p.map_b[k >= second];
-            const int kb = kk - (k >= second ? (int)p.K1 : 0);
-            for (int c = 0; c < cols / 64; ++c)
-              mm_load_box<CTAS>(b + c * 8192, map, col + 64 * c, kb, pb, bar);
-          } else {
-            mm_load_box<CTAS>(b, &p.map_b[0], kk, col, pb, bar);
-          }
-          if (++k == depth) {
-            k = 0;
-            ++q;
-          }
-          if (++st == stages) {
-            st = 0;
-            ++round;
-          }
-        }
-      }
-      if (gave_up && rank == 0)  // copies cannot be called back: their memory has to stay until they have landed
-        for (int64_t i = issued < stages ? 0 : issued - stages; i < issued; ++i)
-          mm_bar_wait(full + 8 * (i % stages), (i / stages) & 1, guard, kMmDrainNs);
+      for (uint32_t n = 0; !gave_up && unit_at<TWO>(all, me, of, n, u); ++n)
+        issued += TWO && u.second ? load_unit<EPI, CTAS, true>(all.p[1], u.at, at, ring)
+                                  : load_unit<EPI, CTAS, false>(all.p[0], u.at, at, ring);
+      if (gave_up && at.rank == 0)  // copies cannot be called back: their memory has to stay until they have landed
+        for (int64_t i = issued < at.stages ? 0 : issued - at.stages; i < issued; ++i)
+          mm_bar_wait(at.full + 8 * (i % at.stages), (i / at.stages) & 1, at.guard, kMmDrainNs);
     }
   } else if (warp == kMmEpilogueWarps + 1) {
-    if (lane == 0 && rank == 0) {
-      const uint32_t idesc = mm_idesc(A_MN, B_MN, TILE_ROWS, p.tn);
-      int64_t it = 0;
-      int st = 0, round = 0;
-      for (int64_t u = first; u < units && !gave_up; u += stride, ++it) {
-        const int64_t s = u % p.splits;
-        const int64_t count = steps * (s + 1) / p.splits - steps * s / p.splits;
-        const int acc = it & 1;
-        if (!mm_bar_wait(acc_empty + 8 * acc, ((it >> 1) & 1) ^ 1, guard)) break;
+    if (lane == 0 && at.rank == 0) {
+      Ring ring;
+      for (uint32_t n = 0; !gave_up && unit_at<TWO>(all, me, of, n, u); ++n) {
+        const int acc = n & 1;
+        if (!mm_bar_wait(at.acc_empty + 8 * acc, ((n >> 1) & 1) ^ 1, at.guard)) break;
         mm_fence_after();
-        const uint32_t d = tmem + acc * kMmTileN;
-        bool ok = true;
-        for (int64_t i = 0; i < count; ++i) {
-          ok = mm_bar_wait(full + 8 * st, round & 1, guard);
-          if (!ok) break;
-          mm_fence_after();
-          const uint32_t a = stage0 + st * p.stage_bytes;
-          const uint64_t da = mm_desc(a, A_MN), db = mm_desc(a + stage_a, B_MN);
-#pragma unroll
-          for (int j = 0; j < kMmDepth / 16; ++j)
-            mm_mma<CTAS>(d, da + j * mm_desc_step(A_MN), db + j * mm_desc_step(B_MN), idesc, i > 0 || j > 0);
-          mm_commit<CTAS>(empty + 8 * st);
-          if (++st == stages) {
-            st = 0;
-            ++round;
-          }
-        }
+        const bool ok = TWO && u.second ? multiply_unit<EPI, CTAS, true>(all.p[1], u.at, at, ring, acc)
+                                        : multiply_unit<EPI, CTAS, false>(all.p[0], u.at, at, ring, acc);
         if (!ok) break;
-        mm_commit<CTAS>(acc_full + 8 * acc);
       }
       if (gave_up) {
-        mm_commit<CTAS>(drained);
-        mm_bar_wait(drained, 0, guard, kMmDrainNs);
+        mm_commit<CTAS>(at.drained);
+        mm_bar_wait(at.drained, 0, at.guard, kMmDrainNs);
       }
     }
   } else {
-    uint32_t* block = reinterpret_cast<uint32_t*>(raw + (blocks - mm_smem(raw))) + warp * kMmBlockWords;
-    int64_t it = 0;
-    for (int64_t u = first; u < units; u += stride, ++it) {
-      const int acc = it & 1;
-      if (!__all_sync(~0u, mm_bar_wait(acc_full + 8 * acc, (it >> 1) & 1, guard))) break;
+    float* block = reinterpret_cast<float*>(raw + (blocks - mm_smem(raw))) + warp * kMmBlockWords;
+    for (uint32_t n = 0; unit_at<TWO>(all, me, of, n, u); ++n) {
+      const int acc = n & 1;
+      if (!__all_sync(~0u, mm_bar_wait(at.acc_full + 8 * acc, (n >> 1) & 1, at.guard))) break;
       mm_fence_after();
-      int64_t tm, tn;
-      tile_at(p, TILE_ROWS, u / p.splits, tm, tn);
-      const uint32_t d = tmem + ((uint32_t)(warp * 32) << 16) + acc * kMmTileN;
-      auto src = [&](int c0, int c1, float (&x)[32], float (&y)[32]) {
-        uint32_t r0[32], r1[32];
-        mm_tmem_load(d + c0, r0);
-        mm_tmem_load(d + c1, r1);
-        mm_tmem_wait();
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          x[j] = steps ? __uint_as_float(r0[j]) : 0.0f;  // nothing was summed
-          y[j] = steps ? __uint_as_float(r1[j]) : 0.0f;
-        }
-      };
-      const int in_tile = (int)rank * kMmRows + warp * 32;
-      const int64_t row0 = tm * TILE_ROWS + in_tile;
-      if (p.splits == 1) {
-        mm_epilogue<EPI>(p, row0, tn, lane, block, src);
-      } else {
-        const int64_t rows = p.M < TILE_ROWS ? p.M : TILE_ROWS;
-        float4* to = reinterpret_cast<float4*>(p.partial + (u * rows + in_tile + lane) * p.tn);
-        for (int c = 0; c < p.tn; c += 64) {
-          float x[32], y[32];
-          src(c, c + 32, x, y);
-          if (row0 + lane < p.M) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              to[c / 4 + j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-              to[c / 4 + 8 + j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
-            }
-          }
-        }
-      }
+      if (TWO)
+        finish_unit<EPI, CTAS>(all.p[u.second], u.at, at, acc, warp, lane, block);
+      else
+        finish_unit<EPI, CTAS>(all.p[0], u.at, at, acc, warp, lane, block);
       mm_fence_before();
       __syncwarp();
       if (lane == 0) {
         if (CTAS == 1)
-          mm_bar_arrive(acc_empty + 8 * acc);
+          mm_bar_arrive(at.acc_empty + 8 * acc);
         else
-          mm_bar_arrive_at(mm_of_first(acc_empty + 8 * acc));
+          mm_bar_arrive_at(mm_of_first(at.acc_empty + 8 * acc));
       }
     }
   }
@@ -221,25 +322,27 @@ __global__ void __launch_bounds__(kMmThreads, 1) vc_mm(const __grid_constant__ M
   mm_fence_before();
   __syncthreads();
   if (CTAS > 1) mm_cluster_sync();  // the other CTA's copies and products reach into this one's memory
-  if (warp == kMmEpilogueWarps + 1) mm_tmem_free<CTAS>(tmem);
+  if (warp == kMmEpilogueWarps + 1) mm_tmem_free<CTAS>(at.tmem);
 }
 
 // The epilogue of tiles whose sums were cut: the splits' sums added in order, a
 // warp for 32 columns of a row (MM_LSE: for a tile's).
 template <int EPI>
-__global__ void __launch_bounds__(256) vc_mm_join_splits(const __grid_constant__ MmParams p) {
+__global__ void __launch_bounds__(256) vc_mm_join_splits(const __grid_constant__ MmLaunch all) {
   pdl_enter();
+  const bool second = blockIdx.x >= all.p[0].join_blocks;  // CTAs of p[0]'s come first
+  const MmParams& p = all.p[second];
   const int lane = threadIdx.x % 32;
   const int tile_rows = p.tile_rows;
   const int64_t rows = p.M < tile_rows ? p.M : tile_rows;
   const int width = EPI == MM_GATED ? p.tn / 2 : p.tn, chunks = EPI == MM_LSE ? 1 : width / 32;
-  const int64_t w = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+  const int64_t w = (int64_t)(blockIdx.x - (second ? all.p[0].join_blocks : 0)) * 8 + threadIdx.x / 32;
   const int chunk = (int)(w % chunks);
   const int64_t r = w / chunks % rows, tile = w / chunks / rows;
-  if (tile >= p.tiles_m * p.tiles_n) return;
-  int64_t tm, tn;
-  tile_at(p, tile_rows, tile, tm, tn);
-  const int64_t row = tm * tile_rows + r;
+  if (tile >= (int64_t)p.tiles_m * p.tiles_n) return;
+  uint32_t tm, tn;
+  tile_at(p, tile_rows, (uint32_t)tile, tm, tn);
+  const int64_t row = (int64_t)tm * tile_rows + r;
   if (row >= p.M) return;
   const float* from = p.partial + (tile * p.splits * rows + r) * p.tn;
   auto sum = [&](int c) {
@@ -249,7 +352,7 @@ __global__ void __launch_bounds__(256) vc_mm_join_splits(const __grid_constant__
     return x;
   };
   const int c = chunk * 32 + lane;
-  const int64_t col = tn * width + c;
+  const int64_t col = (int64_t)tn * width + c;
   if constexpr (EPI == MM_OUT) {
     const MmOutRow to = mm_out_row(p, row);
     if (col >= p.N || to.row >= (p.M1 ? p.M2 : p.M)) return;
@@ -268,7 +371,7 @@ __global__ void __launch_bounds__(256) vc_mm_join_splits(const __grid_constant__
     float v[kMmTileN / 32], top = -INFINITY, s = 0.0f;
 #pragma unroll
     for (int i = 0; i < kMmTileN / 32; ++i) {
-      const int64_t at = tn * p.tn + i * 32 + lane;
+      const int64_t at = (int64_t)tn * p.tn + i * 32 + lane;
       const bool in = i * 32 < p.tn && at < p.N;
       v[i] = in ? sum(i * 32 + lane) : -INFINITY;
       if (in && at == hit) p.picked[row] = v[i];
@@ -280,7 +383,7 @@ __global__ void __launch_bounds__(256) vc_mm_join_splits(const __grid_constant__
 #pragma unroll
     for (int i = 0; i < kMmTileN / 32; ++i) s += mm_exp2(fmaf(v[i], kMmLog2e, -ref));
     for (int d = 16; d; d /= 2) s += __shfl_xor_sync(~0u, s, d);
-    if (lane == 0) p.part[tn * p.M + row] = make_float2(top, s);
+    if (lane == 0) p.part[(int64_t)tn * p.M + row] = make_float2(top, s);  // of the whole tile
   } else if constexpr (EPI == MM_ERROR) {
     if (col >= p.N) return;
     const int64_t t = mm_token(p.targets, p.idx64, row);
@@ -307,21 +410,21 @@ __global__ void __launch_bounds__(256) vc_mm_join_splits(const __grid_constant__
 }
 
 template <int CTAS>
-static const void* kernel_of(MmEpilogue epilogue, bool a_mn) {
+static const void* kernel_of(MmEpilogue epilogue) {
   switch (epilogue) {
     case MM_LSE:
-      return (const void*)vc_mm<MM_LSE, false, false, CTAS>;
+      return (const void*)vc_mm<MM_LSE, CTAS>;
     case MM_ERROR:
-      return (const void*)vc_mm<MM_ERROR, false, false, CTAS>;
+      return (const void*)vc_mm<MM_ERROR, CTAS>;
     case MM_GATED:
-      return (const void*)vc_mm<MM_GATED, false, false, CTAS>;
+      return (const void*)vc_mm<MM_GATED, CTAS>;
     default:
-      return a_mn ? (const void*)vc_mm<MM_OUT, true, true, CTAS> : (const void*)vc_mm<MM_OUT, false, true, CTAS>;
+      return (const void*)vc_mm<MM_OUT, CTAS>;
   }
 }
 
-const void* mm_kernel(MmEpilogue epilogue, bool a_mn, int ctas) {
-  return ctas == 2 ? kernel_of<2>(epilogue, a_mn) : kernel_of<1>(epilogue, a_mn);
+const void* mm_kernel(MmEpilogue epilogue, int ctas) {
+  return ctas == 2 ? kernel_of<2>(epilogue) : kernel_of<1>(epilogue);
 }
 
 const void* mm_join_splits_kernel(MmEpilogue epilogue) {

@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <array>
+#include <cmath>
 
 #include "layer_checks.h"
 #include "mm_internal.h"
@@ -40,47 +41,111 @@ int64_t packed_bytes(int64_t rows, int64_t cols, int parts) {
   return rows * round_up(cols, 8) * 2 * parts;
 }
 
-// How a product is cut: CTAs that share a tile, its columns, and splits of its sum.
-struct Plan {
-  int ctas = 1, tn = 256, splits = 1;
-  size_t bytes = 0;  // of the splits' sums
+// A product to be planned.
+struct Shape {
+  int64_t M, N, K;
+  int parts;
+  bool halves;
 };
+
+// How a launch's products are cut: CTAs that share a tile, and for each product the
+// tile's columns, the splits of its sum, and a unit's cycles.
+struct Plan {
+  int ctas = 1;
+  struct {
+    int tn = 256, splits = 1;
+    double unit = 0;
+    size_t bytes = 0;  // of the splits' sums
+  } of[2];
+  size_t bytes() const { return align256(of[0].bytes) + align256(of[1].bytes); }
+};
+
 // The cheapest by a model of cycles.  A step of 64 places takes the tensor cores 2
 // tn, or as long as the step's operands take to arrive: at 24 bytes a cycle and SM
 // from memory where one row of tiles takes each column once, at 80 from L2 where
 // rows of tiles share them.  A tile's epilogue goes beside the next tile's sum, but
-// for the last one's.
-Plan plan_of(int64_t M, int64_t N, int64_t K, int parts, bool halves) {
+// for the last one's.  Alone, a product takes whole waves of units; two fill each
+// other's last waves to within a unit.
+Plan search_plan(const Shape* shape, int count) {
   Plan best;
-  double least = 0;
-  const int64_t steps = mm_pairs(parts) * ceil_div(K, kMmDepth);
+  double least = -1;
   for (int ctas : {2, 1}) {
-    if (ctas == 2 && M <= kMmRows) continue;
-    const int64_t tile_rows = kMmRows * ctas, rows = std::min<int64_t>(M, tile_rows), slots = kPlanSms / ctas;
-    const int64_t tiles_m = ceil_div(M, tile_rows);
-    for (int tn : {256, 128, 64}) {
-      if (tn == 64 && (halves || ctas == 2)) continue;
-      const int64_t cols = halves ? tn / 2 : tn;
-      const double tiles = (double)tiles_m * (double)ceil_div(N, cols);
-      const double bytes = 128.0 * (double)(std::min<int64_t>(M, kMmRows) + tn / ctas);
-      const double step = std::max(2.0 * tn, bytes / (tiles_m > 1 ? 80 : 24)), tail = 10.0 * tn + 1000;
-      for (int s = 1; s <= 16; ++s) {
-        if (s > 1 && (steps / s < 4 || tiles * s > 8 * kPlanSms)) break;
-        const double units = tiles * s, waves = (double)(int64_t)((units + slots - 1) / slots);
-        double cost = waves * ((double)ceil_div(steps, s) * step + 200) + tail;
-        if (s > 1) cost += 3000 + units * (double)rows * tn * 8 / (24.0 * kPlanSms);
-        if (least == 0 || cost < least) {
-          least = cost;
-          best.ctas = ctas;
-          best.tn = tn;
-          best.splits = s;
-          best.bytes = s == 1 ? 0 : (size_t)units * (size_t)rows * tn * sizeof(float);
+    if (ctas == 2 && shape[0].M <= kMmRows && (count == 1 || shape[1].M <= kMmRows)) continue;
+    const double slots = kPlanSms / ctas;
+    struct Choice {
+      int tn, splits;
+      double units, unit, join, tail;
+      size_t bytes;
+    } choice[2][48];
+    int choices[2] = {0, 0};
+    for (int i = 0; i < count; ++i) {
+      const Shape& s = shape[i];
+      const int64_t tile_rows = kMmRows * ctas, rows = std::min<int64_t>(s.M, tile_rows);
+      const int64_t steps = mm_pairs(s.parts) * ceil_div(s.K, kMmDepth), tiles_m = ceil_div(s.M, tile_rows);
+      for (int tn : {256, 128, 64}) {
+        if (tn == 64 && (s.halves || ctas == 2)) continue;
+        const double tiles = (double)tiles_m * (double)ceil_div(s.N, s.halves ? tn / 2 : tn);
+        const double bytes = 128.0 * (double)(std::min<int64_t>(s.M, kMmRows) + tn / ctas);
+        const double step = std::max(2.0 * tn, bytes / (tiles_m > 1 ? 80 : 24));
+        for (int k : {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16}) {
+          if (k > 1 && (steps / k < 4 || tiles * k > 8 * kPlanSms)) break;
+          const double units = tiles * k;
+          Choice& c = choice[i][choices[i]++];
+          c = {tn, k, units, (double)ceil_div(steps, k) * step + 200, 0.0, 10.0 * tn + 1000, 0};
+          if (k > 1) {
+            c.bytes = (size_t)units * (size_t)rows * tn * sizeof(float);
+            c.join = 2500 + (double)c.bytes * 2 / (10.0 * kPlanSms);
+          }
         }
+      }
+    }
+    for (int i = 0; i < choices[0]; ++i) {
+      const Choice& a = choice[0][i];
+      auto consider = [&](double cost, const Choice* b) {
+        if (least >= 0 && cost >= least) return;
+        least = cost;
+        best.ctas = ctas;
+        best.of[0] = {a.tn, a.splits, a.unit, a.bytes};
+        if (b) best.of[1] = {b->tn, b->splits, b->unit, b->bytes};
+      };
+      if (count == 1) {
+        consider(std::ceil(a.units / slots) * a.unit + a.tail + a.join, nullptr);
+        continue;
+      }
+      for (int j = 0; j < choices[1]; ++j) {
+        const Choice& b = choice[1][j];
+        const double work = (a.units * a.unit + b.units * b.unit) / slots;
+        consider(std::max(work + 0.5 * std::min(a.unit, b.unit), std::max(a.unit, b.unit)) + std::max(a.tail, b.tail) +
+                     std::max(a.join, b.join),
+                 &b);
       }
     }
   }
   return best;
 }
+
+// A program repeats the sizes of its calls: each thread keeps its last plans.
+Plan make_plan(const Shape* shape, int count) {
+  struct Kept {
+    Shape shape[2];
+    int count = 0;
+    Plan plan;
+  };
+  static thread_local Kept kept[32];
+  static thread_local int next = 0;
+  auto same = [](const Shape& a, const Shape& b) {
+    return a.M == b.M && a.N == b.N && a.K == b.K && a.parts == b.parts && a.halves == b.halves;
+  };
+  for (const Kept& k : kept)
+    if (k.count == count && same(k.shape[0], shape[0]) && (count == 1 || same(k.shape[1], shape[1]))) return k.plan;
+  Kept& k = kept[next++ % 32];
+  for (int i = 0; i < count; ++i) k.shape[i] = shape[i];
+  k.plan = search_plan(shape, count);
+  k.count = count;
+  return k.plan;
+}
+
+Plan plan_of(const Shape& a) { return make_plan(&a, 1); }
 
 // Columns of a piece of the vocabulary: `fit` at most, whole tiles.
 int64_t piece_of(int64_t V, int64_t fit) {
@@ -109,11 +174,11 @@ LossLayout loss_layout(int64_t N, int64_t V, int64_t D, int dtype, bool direct) 
   size_t splits = 0;
   int64_t tiles = 0;
   for (int64_t w : piece_widths(V, L.piece)) {
-    const Plan plan = plan_of(N, w, D, parts, false);
-    splits = std::max(splits, plan.bytes);
-    tiles = std::max(tiles, ceil_div(w, plan.tn));
+    const Plan plan = plan_of({N, w, D, parts, false});
+    splits = std::max(splits, plan.bytes());
+    tiles = std::max(tiles, ceil_div(w, plan.of[0].tn));
   }
-  L.part = r.take(tiles * N * (int64_t)sizeof(float2));
+  L.part = r.take(2 * tiles * N * (int64_t)sizeof(float2));
   L.splits = r.take((int64_t)splits);
   L.state = r.take(L.pieces > 1 ? N * (int64_t)sizeof(float2) : 0);
   L.bytes = r.bytes;
@@ -131,18 +196,19 @@ LossGradLayout loss_grad_layout(int64_t N, int64_t V, int64_t D, int dtype, bool
   if (!direct) fit = std::min(fit, kPackBytes / std::max<int64_t>(1, packed_bytes(1, D, parts)));
   L.piece = piece_of(V, fit);
   L.pieces = std::max<int64_t>(1, L.piece ? ceil_div(V, L.piece) : 1);
-  L.error_ld = round_up(L.piece, 8);
+  L.error_ld = round_up(L.piece, 64);  // rows of whole 128-byte lines
   Regions r;
   L.scale = r.take(sizeof(float));
   L.x = r.take(packed_bytes(N, D, parts));
   L.table = r.take(direct ? 0 : packed_bytes(L.piece, D, parts));
   L.error = r.take(N * L.error_ld * 2 * parts);
-  L.accum = r.take(L.pieces > 1 ? N * D * 4 : 0);
+  L.accum = r.take(L.pieces > 1 ? N * round_up(D, 2) * 4 : 0);
   size_t splits = 0;
-  for (int64_t w : piece_widths(V, L.piece))
-    for (const Plan& plan : {plan_of(N, w, D, parts, false), plan_of(N, D, w, parts, false),
-                             plan_of(w, D, N, parts, false)})
-      splits = std::max(splits, plan.bytes);
+  for (int64_t w : piece_widths(V, L.piece)) {
+    const Shape s[3] = {{N, w, D, parts, false}, {N, D, w, parts, false}, {w, D, N, parts, false}};
+    splits = std::max({splits, plan_of(s[0]).bytes(), plan_of(s[1]).bytes(), plan_of(s[2]).bytes(),
+                       make_plan(s + 1, 2).bytes()});
+  }
   L.splits = r.take((int64_t)splits);
   L.bytes = r.bytes;
   return L;
@@ -161,10 +227,16 @@ GatedLayout gated_layout(int64_t N, int64_t D, int64_t F, int dtype, bool direct
   L.w_gate = r.take(direct ? 0 : packed_bytes(F, D, parts));
   L.w_up = r.take(direct ? 0 : packed_bytes(F, D, parts));
   L.grads = r.take(backward ? packed_bytes(N, 2 * L.half, parts) : 0);
-  L.splits = r.take((int64_t)(backward ? std::max(plan_of(N, D, 2 * L.half, parts, false).bytes,
-                                                  std::max(plan_of(F, D, N, parts, false).bytes,
-                                                           plan_of(2 * L.half, D, N, parts, false).bytes))
-                                       : plan_of(N, F, D, parts, true).bytes));
+  size_t splits = 0;
+  if (backward) {  // dx; one weight's gradient; both
+    const Shape s[3] = {{N, D, 2 * L.half, parts, false}, {F, D, N, parts, false}, {2 * L.half, D, N, parts, false}};
+    const Shape one[2] = {s[0], s[1]}, both[2] = {s[0], s[2]};
+    splits = std::max({plan_of(s[0]).bytes(), plan_of(s[1]).bytes(), plan_of(s[2]).bytes(), make_plan(one, 2).bytes(),
+                       make_plan(both, 2).bytes()});
+  } else {
+    splits = plan_of({N, F, D, parts, true}).bytes();
+  }
+  L.splits = r.take((int64_t)splits);
   L.bytes = r.bytes;
   return L;
 }
@@ -268,49 +340,71 @@ int encode(CUtensorMap* map, const MmOperand& o, int parts, int box) {
   return VCOLL_OK;
 }
 
-// The tiles of a product, and its epilogue.  b is taken transposed by MM_OUT, a
-// where a_mn is set.  partial: the room that plan_of's splits need.
-int product(MmEpilogue epilogue, bool a_mn, MmParams* p, void* partial, void* stream) {
+// The launch's tiles and their epilogues; partial: the room that the plan's splits
+// need.
+int products(MmEpilogue epilogue, MmLaunch* all, void* partial, void* stream) {
   const bool b_mn = epilogue == MM_OUT;
-  const Plan plan = plan_of(p->M, p->N, p->K, p->parts, p->b_halves);
-  p->tn = plan.tn;
-  p->splits = plan.splits;
-  p->partial = (float*)partial;
-  p->tile_rows = kMmRows * plan.ctas;
-  p->tiles_m = ceil_div(p->M, p->tile_rows);
-  p->tiles_n = ceil_div(p->N, p->b_halves ? p->tn / 2 : p->tn);
-  p->a_rows = a_mn ? kMmRows : (int)std::min<int64_t>(kMmRows, round_up(p->M, 8));
-  p->stage_bytes = (p->a_rows + p->tn / plan.ctas) * kMmDepth * 2;
-  p->stages = std::min(kMmMaxStages, kMmStageRoom / p->stage_bytes);
-  const bool second = p->b[1].p && !p->b_halves;
-  if (!second) p->K1 = round_up(p->K, kMmDepth);
-  if (!p->tiles_m || !p->tiles_n) return VCOLL_OK;
-  if (p->tiles_m > 0x7FFFFFFF / p->tiles_n)
-    return fail(VCOLL_ERR_UNSUPPORTED, "%lld x %lld tiles are too many", (long long)p->tiles_m,
-                (long long)p->tiles_n);
-  if (p->K) {
-    VCOLL_TRY(encode(&p->map_a, p->a, p->parts, a_mn ? kMmDepth : p->a_rows));
-    const int box = b_mn ? kMmDepth : p->b_halves ? p->tn / 2 : p->tn / plan.ctas;
-    VCOLL_TRY(encode(&p->map_b[0], p->b[0], p->parts, box));
-    if (second || p->b_halves) VCOLL_TRY(encode(&p->map_b[1], p->b[1], p->parts, box));
+  Shape shape[2];
+  int which[2], count = 0;
+  for (int i = 0; i < 2; ++i) {
+    const MmParams& p = all->p[i];
+    if (p.M && p.N) {
+      shape[count] = {p.M, p.N, p.K, p.parts, p.b_halves != 0};
+      which[count++] = i;
+    }
   }
-  p->error_word = device_error_symbol();
-  if (!p->error_word) return fail(VCOLL_ERR_CUDA, "the device error word has no address");
+  if (!count) return VCOLL_OK;
+  const Plan plan = make_plan(shape, count);
+  all->error_word = device_error_symbol();
+  if (!all->error_word) return fail(VCOLL_ERR_CUDA, "the device error word has no address");
+  int64_t units = 0, join_blocks = 0;
+  for (int i = 0; i < count; ++i) {
+    MmParams* p = &all->p[which[i]];
+    const bool a_mn = which[i] == 1;
+    p->tn = plan.of[i].tn;
+    p->splits = plan.of[i].splits;
+    p->partial = (float*)((char*)partial + (i ? align256(plan.of[0].bytes) : 0));
+    p->tile_rows = kMmRows * plan.ctas;
+    const int64_t tiles_m = ceil_div(p->M, p->tile_rows), tiles_n = ceil_div(p->N, p->b_halves ? p->tn / 2 : p->tn);
+    if (tiles_m > 0x3FFFFFFF / tiles_n)
+      return fail(VCOLL_ERR_UNSUPPORTED, "%lld x %lld tiles are too many", (long long)tiles_m, (long long)tiles_n);
+    p->tiles_m = (uint32_t)tiles_m;
+    p->tiles_n = (uint32_t)tiles_n;
+    p->units = (uint32_t)(tiles_m * tiles_n) * p->splits;
+    units += p->units;
+    p->depth = (uint32_t)ceil_div(p->K, kMmDepth);
+    p->a_rows = a_mn || plan.ctas == 2 ? kMmRows : (int)std::min<int64_t>(kMmRows, round_up(p->M, 8));
+    all->stage_bytes = std::max(all->stage_bytes, (p->a_rows + p->tn / plan.ctas) * kMmDepth * 2);
+    const bool second = p->b[1].p && !p->b_halves;
+    if (!second) p->K1 = round_up(p->K, kMmDepth);
+    if (p->K) {
+      VCOLL_TRY(encode(&p->map_a, p->a, p->parts, a_mn ? kMmDepth : p->a_rows));
+      const int box = b_mn ? kMmDepth : p->b_halves ? p->tn / 2 : p->tn / plan.ctas;
+      VCOLL_TRY(encode(&p->map_b[0], p->b[0], p->parts, box));
+      if (second || p->b_halves) VCOLL_TRY(encode(&p->map_b[1], p->b[1], p->parts, box));
+    }
+    if (p->splits > 1) {
+      const int64_t chunks = epilogue == MM_LSE ? 1 : (p->b_halves ? p->tn / 2 : p->tn) / 32;
+      p->join_blocks = (uint32_t)ceil_div(tiles_m * tiles_n * std::min<int64_t>(p->M, p->tile_rows) * chunks, 8);
+      join_blocks += p->join_blocks;
+    }
+  }
+  all->stages = std::min(kMmMaxStages, kMmStageRoom / all->stage_bytes);
   int sms = 0;
   VCOLL_TRY(device_sms(&sms));
-  const int64_t tiles = p->tiles_m * p->tiles_n;
-  VCOLL_TRY(launch_tiles(mm_kernel(epilogue, a_mn, plan.ctas),
-                         plan.ctas * std::min<int64_t>(sms / plan.ctas, tiles * p->splits), plan.ctas,
-                         kMmThreads, kMmSmem, p, stream));
-  if (p->splits == 1) return VCOLL_OK;
-  const int64_t chunks = epilogue == MM_LSE ? 1 : (p->b_halves ? p->tn / 2 : p->tn) / 32;
-  const int64_t warps = tiles * std::min<int64_t>(p->M, p->tile_rows) * chunks;
-  return launch_grid(mm_join_splits_kernel(epilogue), ceil_div(warps, 8), 1, 256, 0, p, stream);
+  const uint32_t slots = (uint32_t)std::min<int64_t>(sms / plan.ctas, units), last = all->p[0].units % slots;
+  if (count == 2 && last)
+    all->ahead = std::min<uint32_t>((uint32_t)std::llround(plan.of[0].unit / plan.of[1].unit),
+                                    all->p[1].units / (slots - last));
+  VCOLL_TRY(launch_tiles(mm_kernel(epilogue, plan.ctas), (int64_t)plan.ctas * slots, plan.ctas, kMmThreads, kMmSmem,
+                         all, stream));
+  if (!join_blocks) return VCOLL_OK;
+  return launch_grid(mm_join_splits_kernel(epilogue), join_blocks, 1, 256, 0, all, stream);
 }
 
-// Whether every row of a bf16 matrix allows 4-byte stores of two columns.
+// Whether two adjacent columns of every row can be moved at once.
 bool in_pairs(const void* p, int64_t rows, int64_t ld, int dtype) {
-  return dtype == VCOLL_BF16 && (uint64_t)p % 4 == 0 && (rows <= 1 || ld % 2 == 0);
+  return (uint64_t)p % (2 * elem_size(dtype)) == 0 && (rows <= 1 || ld % 2 == 0);
 }
 
 // Matrices of more values than any memory holds: their bytes fit 64 bits.
@@ -389,7 +483,8 @@ int vcoll_cross_entropy(const void* x, int64_t x_ld, const void* table, int64_t 
   const LossLayout L = loss_layout(N, V, D, dtype, x_direct && t_direct);
   VCOLL_TRY(check_room(ops, 5, workspace, workspace_bytes, L.bytes));
   char* ws = (char*)workspace;
-  MmParams p = {};
+  MmLaunch all = {};
+  MmParams& p = all.p[0];
   p.M = N;
   p.K = D;
   p.parts = parts_of(dtype);
@@ -415,8 +510,10 @@ int vcoll_cross_entropy(const void* x, int64_t x_ld, const void* table, int64_t 
     VCOLL_TRY(pack.add((const char*)table + p.token0 * table_ld * es, p.N, D, table_ld, t_direct,
                        ws + L.table, false, &p.b[0]));
     VCOLL_TRY(pack.run(stream));
-    VCOLL_TRY(product(MM_LSE, false, &p, ws + L.splits, stream));
-    j.tiles = p.tiles_n;
+    VCOLL_TRY(products(MM_LSE, &all, ws + L.splits, stream));
+    j.tiles = (int64_t)p.tiles_n * (p.splits > 1 || p.tn < 128 ? 1 : 2);
+    p.join_blocks = 0;
+    all.stage_bytes = 0;
     j.first = i == 0;
     j.last = i == L.pieces - 1;
     VCOLL_TRY(launch_grid(mm_join_kernel(), ceil_div(N, 32), 1, kMmJoinThreads, 0, &j, stream));
@@ -479,7 +576,8 @@ int vcoll_cross_entropy_backward(const float* dloss, int64_t dloss_count, const 
                        false, &tokens));
     VCOLL_TRY(pack.run(stream));
     const MmOperand error = operand(ws + L.error, N, width, L.error_ld, N * L.error_ld);
-    MmParams p = {};
+    MmLaunch all = {};
+    MmParams& p = all.p[0];
     p.a = rows;
     p.b[0] = tokens;
     p.M = N;
@@ -497,9 +595,10 @@ int vcoll_cross_entropy_backward(const float* dloss, int64_t dloss_count, const 
     p.error = ws + L.error;
     p.error_ld = L.error_ld;
     p.error_plane = N * L.error_ld;
-    VCOLL_TRY(product(MM_ERROR, false, &p, ws + L.splits, stream));
+    VCOLL_TRY(products(MM_ERROR, &all, ws + L.splits, stream));
+    MmLaunch grads = {};  // of x and of the table
     if (dx) {
-      MmParams q = {};
+      MmParams& q = grads.p[0];
       q.a = error;
       q.b[0] = tokens;
       q.M = N;
@@ -511,13 +610,12 @@ int vcoll_cross_entropy_backward(const float* dloss, int64_t dloss_count, const 
       q.out_pairs = in_pairs(dx, N, dx_ld, dtype);
       q.out_ld = dx_ld;
       q.out_f32 = dtype == VCOLL_F32;
-      q.accum_ld = D;
+      q.accum_ld = round_up(D, 2);
       if (i > 0) q.accum_in = (float*)(ws + L.accum);
       if (i < L.pieces - 1) q.accum_out = (float*)(ws + L.accum);
-      VCOLL_TRY(product(MM_OUT, false, &q, ws + L.splits, stream));
     }
     if (dtable) {
-      MmParams q = {};
+      MmParams& q = grads.p[1];
       q.a = error;
       q.b[0] = rows;
       q.M = width;
@@ -531,8 +629,9 @@ int vcoll_cross_entropy_backward(const float* dloss, int64_t dloss_count, const 
       q.out_f32 = dtype == VCOLL_F32;
       q.base = base ? (const char*)base + v0 * base_ld * es : nullptr;
       q.base_ld = base_ld;
-      VCOLL_TRY(product(MM_OUT, true, &q, ws + L.splits, stream));
+      if (base) q.out_pairs = q.out_pairs && in_pairs(q.base, V, base_ld, dtype);
     }
+    VCOLL_TRY(products(MM_OUT, &grads, ws + L.splits, stream));
   }
   return VCOLL_OK;
 }
@@ -563,7 +662,8 @@ int vcoll_gated_ff(const void* x, int64_t x_ld, const void* w_gate, int64_t w_ga
   const GatedLayout L = gated_layout(N, D, F, dtype, x_direct && g_direct && u_direct, false);
   VCOLL_TRY(check_room(ops, 6, workspace, workspace_bytes, L.bytes));
   char* ws = (char*)workspace;
-  MmParams p = {};
+  MmLaunch all = {};
+  MmParams& p = all.p[0];
   Packer pack(dtype);
   VCOLL_TRY(pack.add(x, N, D, x_ld, x_direct, ws + L.x, false, &p.a));
   VCOLL_TRY(pack.add(w_gate, F, D, w_gate_ld, g_direct, ws + L.w_gate, false, &p.b[0]));
@@ -584,7 +684,7 @@ int vcoll_gated_ff(const void* x, int64_t x_ld, const void* w_gate, int64_t w_ga
   p.act = activation;
   p.out_pairs = in_pairs(h, N, h_ld, dtype) && (!gate || in_pairs(gate, N, gate_ld, dtype)) &&
                 (!up || in_pairs(up, N, up_ld, dtype));
-  return product(MM_GATED, false, &p, ws + L.splits, stream);
+  return products(MM_GATED, &all, ws + L.splits, stream);
 }
 
 size_t vcoll_gated_ff_backward_workspace_bytes(int64_t N, int64_t D, int64_t F, int dtype,
@@ -654,8 +754,9 @@ int vcoll_gated_ff_backward(const void* dh, int64_t dh_ld, const void* x, int64_
     VCOLL_TRY(pack.add(w_up, N ? F : 0, D, w_up_ld, u_direct, ws + L.w_up, false, &ups));
   }
   VCOLL_TRY(pack.run(stream));
+  MmLaunch all = {};  // dx and the weights' gradients
   if (dx) {
-    MmParams p = {};
+    MmParams& p = all.p[0];
     p.a = grads;
     p.b[0] = gates;
     p.b[1] = ups;
@@ -668,11 +769,10 @@ int vcoll_gated_ff_backward(const void* dh, int64_t dh_ld, const void* x, int64_
     p.out_ld = dx_ld;
     p.out_f32 = dtype == VCOLL_F32;
     p.out_pairs = in_pairs(dx, N, dx_ld, dtype);
-    VCOLL_TRY(product(MM_OUT, false, &p, ws + L.splits, stream));
   }
   if (weights) {  // both as one product, or the one that is wanted
     const bool both = dw_gate && dw_up;
-    MmParams p = {};
+    MmParams& p = all.p[1];
     p.a = grads;
     if (!both) {
       p.a.p = ws + L.grads + (dw_gate ? 0 : (size_t)L.half * 2);
@@ -694,9 +794,8 @@ int vcoll_gated_ff_backward(const void* dh, int64_t dh_ld, const void* x, int64_
       p.M2 = F;
       p.out_pairs = p.out_pairs && in_pairs(dw_up, F, dw_up_ld, dtype);
     }
-    VCOLL_TRY(product(MM_OUT, true, &p, ws + L.splits, stream));
   }
-  return VCOLL_OK;
+  return products(MM_OUT, &all, ws + L.splits, stream);
 }
 
 }  // extern "C"
