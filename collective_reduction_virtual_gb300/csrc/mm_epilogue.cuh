@@ -111,18 +111,63 @@ __device__ __forceinline__ void mm_store2(void* p, int f32, int wide, int64_t i,
     if (left > 1) mm_store(p, f32, i + 1, y);
   }
 }
-__device__ __forceinline__ float2 mm_load2(const void* p, int f32, int wide, int64_t i, int64_t left) {
-  float2 v = make_float2(0.0f, 0.0f);
-  if (wide && left > 1) {
-    if (f32)
-      v = *reinterpret_cast<const float2*>(static_cast<const float*>(p) + i);
-    else
-      Elem<__nv_bfloat16>::widen2(*reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + i), v.x, v.y);
-  } else {
-    if (left > 0) v.x = mm_load(p, f32, i);
-    if (left > 1) v.y = mm_load(p, f32, i + 1);
+// x = (in + first * x) * then, for a block of 32 columns of which a lane has two in
+// every second row.  in may be NULL.  The loads of eight rows are issued at once,
+// from places within the matrix whatever the row and column: a load waits longer
+// than all else takes.
+struct MmAdd {
+  const void* in;
+  int64_t in_at, in_ld;
+  void* out;
+  int64_t out_at, out_ld;
+  float first, then;
+};
+template <bool IN32, bool OUT32, bool WIDE>
+__device__ __forceinline__ void mm_add_block(const MmAdd& h, const float* block, int rows, int pair, int odd, int64_t col,
+                                          int64_t left) {
+  // left + pair: columns from the block's first on
+  if (left + pair <= 0) return;
+  const int64_t c0 = left > 0 ? col : col + left - 1, c1 = left > 1 ? c0 + 1 : c0;
+  for (int r = odd; r < rows; r += 16) {
+    float2 x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = r + 2 * i < rows ? r + 2 * i : rows - 1;
+      const int64_t from = h.in_at + at * h.in_ld;
+      x[i] = make_float2(0.0f, 0.0f);
+      if (!h.in) continue;
+      if (IN32) {
+        x[i].x = static_cast<const float*>(h.in)[from + c0];
+        x[i].y = static_cast<const float*>(h.in)[from + c1];
+      } else {
+        x[i].x = Elem<__nv_bfloat16>::widen1(static_cast<const uint16_t*>(h.in)[from + c0]);
+        x[i].y = Elem<__nv_bfloat16>::widen1(static_cast<const uint16_t*>(h.in)[from + c1]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = r + 2 * i;
+      if (at >= rows) break;
+      const float y0 = (x[i].x + h.first * block[at * kMmPitch + pair]) * h.then,
+                  y1 = (x[i].y + h.first * block[at * kMmPitch + pair + 1]) * h.then;
+      mm_store2(h.out, OUT32, WIDE, h.out_at + at * h.out_ld + col, left, y0, y1);
+    }
   }
-  return v;
+}
+
+// What a unit's epilogue will add, fetched to L2 while the unit is being summed:
+// a lane a row of the warp's 32.
+__device__ __forceinline__ void mm_prefetch_added(const MmParams& p, int64_t row0, int64_t tile_n, int c0, int c1, int lane) {
+  if (!p.accum_in && !p.base) return;
+  const int rows = mm_rows(p, row0);
+  const int64_t col = tile_n * p.tn + c0, end = p.N < tile_n * p.tn + c1 ? p.N : tile_n * p.tn + c1;
+  if (lane >= rows || col >= end) return;
+  const int es = p.accum_in || p.out_f32 ? 4 : 2;
+  const int64_t at = p.accum_in ? (row0 + lane) * p.accum_ld : (mm_out_row(p, row0).row + lane) * p.base_ld;
+  const char* first = static_cast<const char*>(p.accum_in ? (const void*)p.accum_in : p.base) + (at + col) * es;
+  const char* last = first + (end - col) * es - 1;
+  for (uintptr_t line = (uintptr_t)first & ~(uintptr_t)127; line <= (uintptr_t)last; line += 128)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
 }
 
 __device__ __forceinline__ void mm_to_block(float* block, int lane, const float (&v)[32]) {
@@ -201,39 +246,22 @@ __device__ __forceinline__ void mm_epilogue(const MmParams& p, int64_t row0, int
           mm_store2(to.out, p.out_f32, p.out_pairs, (to.row + r) * to.ld + col, left,
                     block[r * kMmPitch + pair] * scale, block[r * kMmPitch + pair + 1] * scale);
       } else {
-        // what is added is fetched eight rows at a time: a load waits longer than
-        // all else here takes
-        for (int r = odd; r < rows; r += 16) {
-          float2 x[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[i] = make_float2(0.0f, 0.0f);
-            if (r + 2 * i < rows) {
-              if (p.accum_in)
-                x[i] = mm_load2(p.accum_in, 1, 1, (row0 + r + 2 * i) * p.accum_ld + col, left);
-              else if (p.base)
-                x[i] = mm_load2(p.base, p.out_f32, p.out_pairs, (to.row + r + 2 * i) * p.base_ld + col, left);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int at = r + 2 * i;
-            if (at >= rows) break;
-            float2 y = make_float2(block[at * kMmPitch + pair], block[at * kMmPitch + pair + 1]);
-            if (p.base) {
-              y.x = y.x * scale + x[i].x;
-              y.y = y.y * scale + x[i].y;
-            } else {
-              const float s = p.accum_out ? 1.0f : scale;
-              y.x = (x[i].x + y.x) * s;
-              y.y = (x[i].y + y.y) * s;
-            }
-            if (p.accum_out)
-              mm_store2(p.accum_out, 1, 1, (row0 + at) * p.accum_ld + col, left, y.x, y.y);
-            else
-              mm_store2(to.out, p.out_f32, p.out_pairs, (to.row + at) * to.ld + col, left, y.x, y.y);
-          }
-        }
+        const MmAdd how = {p.accum_in ? (const void*)p.accum_in : p.base,
+                           p.accum_in ? row0 * p.accum_ld : to.row * p.base_ld, p.accum_in ? p.accum_ld : p.base_ld,
+                           p.accum_out ? (void*)p.accum_out : to.out,
+                           p.accum_out ? row0 * p.accum_ld : to.row * to.ld, p.accum_out ? p.accum_ld : to.ld,
+                           p.base ? scale : 1.0f, p.base || p.accum_out ? 1.0f : scale};
+        const bool out32 = p.accum_out || p.out_f32, in32 = p.accum_in || out32;
+        if (in32 && out32 && (p.out_pairs || (p.accum_in && p.accum_out)))
+          mm_add_block<true, true, true>(how, block, rows, pair, odd, col, left);
+        else if (in32 && out32)
+          mm_add_block<true, true, false>(how, block, rows, pair, odd, col, left);
+        else if (in32)
+          mm_add_block<true, false, false>(how, block, rows, pair, odd, col, left);
+        else if (p.out_pairs)
+          mm_add_block<false, false, true>(how, block, rows, pair, odd, col, left);
+        else
+          mm_add_block<false, false, false>(how, block, rows, pair, odd, col, left);
       }
       __syncwarp();
     }

@@ -58,19 +58,17 @@ __device__ __forceinline__ bool unit_at(const MmLaunch& all, uint32_t me, uint32
   return u.at < all.p[1].units;
 }
 
-// The steps of a unit, a split of a tile: every pair of parts has `depth` of them.
-__device__ __forceinline__ void steps_of(const MmParams& p, uint32_t unit, uint32_t& tile, uint32_t& begin,
-                                         uint32_t& end) {
+// A unit's tile, and its steps: of every pair of parts' `depth` steps a split takes
+// every splits-th, so that the splits of a tile, which run side by side, read
+// memory that lies side by side.
+__device__ __forceinline__ uint32_t steps_of(const MmParams& p, uint32_t unit, uint32_t& tile, uint32_t& split) {
   const uint32_t steps = mm_pairs(p.parts) * p.depth;
   tile = unit;
-  begin = 0;
-  end = steps;
-  if (p.splits > 1) {
-    tile = unit / p.splits;
-    const uint32_t split = unit - tile * p.splits;  // 16 at most, of steps below 2^28
-    begin = steps * split / p.splits;
-    end = steps * (split + 1) / p.splits;
-  }
+  split = 0;
+  if (p.splits == 1) return steps;
+  tile = unit / p.splits;
+  split = unit - tile * p.splits;
+  return (steps - split + p.splits - 1) / p.splits;
 }
 
 // Where a CTA's parts lie in shared memory, and its place in a pair.
@@ -91,61 +89,57 @@ struct Ring {
   }
 };
 
-// A unit's copies into the ring; the number of stages that were filled.
+// A unit's copies into the ring; the number of stages that were filled.  One lane
+// has a few hundred cycles for a step: what does not change is outside the loop.
 template <int EPI, int CTAS, bool A_MN>
 __device__ __forceinline__ uint32_t load_unit(const MmParams& p, uint32_t unit, const Place& at, Ring& ring) {
   constexpr int TILE_ROWS = kMmRows * CTAS;
   constexpr bool B_MN = EPI == MM_OUT;
   const int cols = p.tn / CTAS;  // of b that this CTA holds
-  const int stage_a = p.a_rows * kMmDepth * 2;
+  const int stage_a = p.a_rows * kMmDepth * 2, half_b = p.tn / 2 * kMmDepth * 2;
   const uint32_t bytes = (uint32_t)CTAS * (stage_a + cols * kMmDepth * 2);
   const int pairs = mm_pairs(p.parts);
-  const uint32_t depth = p.depth, second = (uint32_t)(p.K1 / kMmDepth);  // the first step that takes map_b[1]
-  uint32_t tile, tm, tn, begin, end;
-  steps_of(p, unit, tile, begin, end);
+  const uint32_t depth = p.depth, stride = p.splits;
+  const uint32_t second = B_MN ? (uint32_t)(p.K1 / kMmDepth) : 0;  // the first step that takes map_b[1]
+  uint32_t tile, tm, tn, k, done = 0;
+  steps_of(p, unit, tile, k);
   tile_at(p, TILE_ROWS, tile, tm, tn);
-  int q = pairs > 1 ? (int)(begin / depth) : 0;
-  uint32_t k = begin - q * depth;
   const int row = (int)(tm * TILE_ROWS + at.rank * kMmRows);
   const int col = EPI == MM_GATED ? (int)(tn * (p.tn / 2)) : (int)(tn * p.tn + at.rank * cols);
-  for (uint32_t i = begin; i < end; ++i) {
-    if (ring.round && !mm_bar_wait(at.empty + 8 * ring.stage, (ring.round - 1) & 1, at.guard)) return i - begin;
-    const uint32_t a = at.stage0 + ring.stage * at.stage_bytes, b = a + stage_a;
-    uint32_t bar = at.full + 8 * ring.stage;
-    if (at.rank == 0) mm_bar_expect(bar, bytes);
-    if (CTAS > 1) bar = mm_of_first(bar);
+  const CUtensorMap *map_a = &p.map_a, *map_b = EPI == MM_GATED && CTAS == 2 && at.rank ? &p.map_b[1] : &p.map_b[0];
+  const uint32_t signal = CTAS > 1 ? mm_of_first(at.full) : at.full;
+  for (int q = 0; q < pairs; ++q, k -= depth) {
     const int pa = mm_pair_a(pairs, q), pb = mm_pair_b(pairs, q);
-    const int kk = (int)(k * kMmDepth);
-    if (A_MN) {
+    for (; k < depth; k += stride, ++done) {
+      // an empty stage's barrier was never used: the phase before its first is over
+      if (!mm_bar_wait(at.empty + 8 * ring.stage, (ring.round & 1) ^ 1, at.guard)) return done;
+      const uint32_t a = at.stage0 + ring.stage * at.stage_bytes, b = a + stage_a, bar = signal + 8 * ring.stage;
+      if (CTAS == 1 || at.rank == 0) mm_bar_expect(at.full + 8 * ring.stage, bytes);
+      const int kk = (int)(k * kMmDepth);
+      if (A_MN) {
 #pragma unroll
-      for (int c = 0; c < kMmRows / 64; ++c)
-        mm_load_box<CTAS>(a + c * 8192, &p.map_a, row + 64 * c, kk, pa, bar);
-    } else {
-      mm_load_box<CTAS>(a, &p.map_a, kk, row, pa, bar);
-    }
-    if (EPI == MM_GATED && CTAS == 2) {
-      mm_load_box<CTAS>(b, at.rank ? &p.map_b[1] : &p.map_b[0], kk, col, pb, bar);
-    } else if (EPI == MM_GATED) {
+        for (int c = 0; c < kMmRows / 64; ++c) mm_load_box<CTAS>(a + c * 8192, map_a, row + 64 * c, kk, pa, bar);
+      } else {
+        mm_load_box<CTAS>(a, map_a, kk, row, pa, bar);
+      }
+      if (EPI == MM_GATED && CTAS == 1) {
+        mm_load_box<CTAS>(b, &p.map_b[0], kk, col, pb, bar);
+        mm_load_box<CTAS>(b + half_b, &p.map_b[1], kk, col, pb, bar);
+      } else if (B_MN) {
+        const bool other = !A_MN && k >= second;  // of dx, which sums over both weights
+        const CUtensorMap* map = other ? &p.map_b[1] : map_b;
+        const int kb = other ? kk - (int)p.K1 : kk;
+        mm_load_box<CTAS>(b, map, col, kb, pb, bar);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        mm_load_box<CTAS>(b + h * (p.tn / 2) * kMmDepth * 2, &p.map_b[h], kk, col, pb, bar);
-    } else if (B_MN) {
-      const bool other = k >= second;
-      const CUtensorMap* map = other ? &p.map_b[1] : &p.map_b[0];
-      const int kb = other ? kk - (int)p.K1 : kk;
-#pragma unroll
-      for (int c = 0; c < kMmTileN / CTAS / 64; ++c)
-        if (64 * c < cols) mm_load_box<CTAS>(b + c * 8192, map, col + 64 * c, kb, pb, bar);
-    } else {
-      mm_load_box<CTAS>(b, &p.map_b[0], kk, col, pb, bar);
+        for (int c = 1; c < kMmTileN / CTAS / 64; ++c)
+          if (64 * c < cols) mm_load_box<CTAS>(b + c * 8192, map, col + 64 * c, kb, pb, bar);
+      } else {
+        mm_load_box<CTAS>(b, map_b, kk, col, pb, bar);
+      }
+      ring.next(at.stages);
     }
-    if (++k == depth) {
-      k = 0;
-      ++q;
-    }
-    ring.next(at.stages);
   }
-  return end - begin;
+  return done;
 }
 
 // A unit's products into the accumulators `acc`; false where a wait gave up.
@@ -155,16 +149,16 @@ __device__ __forceinline__ bool multiply_unit(const MmParams& p, uint32_t unit, 
   const uint32_t idesc = mm_idesc(A_MN, B_MN, kMmRows * CTAS, p.tn);
   const int stage_a = p.a_rows * kMmDepth * 2;
   const uint32_t d = at.tmem + acc * kMmTileN;
-  uint32_t tile, begin, end;
-  steps_of(p, unit, tile, begin, end);
-  for (uint32_t i = begin; i < end; ++i) {
+  uint32_t tile, split;
+  const uint32_t steps = steps_of(p, unit, tile, split);
+  for (uint32_t i = 0; i < steps; ++i) {
     if (!mm_bar_wait(at.full + 8 * ring.stage, ring.round & 1, at.guard)) return false;
     mm_fence_after();
     const uint32_t a = at.stage0 + ring.stage * at.stage_bytes;
     const uint64_t da = mm_desc(a, A_MN), db = mm_desc(a + stage_a, B_MN);
 #pragma unroll
     for (int j = 0; j < kMmDepth / 16; ++j)
-      mm_mma<CTAS>(d, da + j * mm_desc_step(A_MN), db + j * mm_desc_step(B_MN), idesc, i > begin || j > 0);
+      mm_mma<CTAS>(d, da + j * mm_desc_step(A_MN), db + j * mm_desc_step(B_MN), idesc, i > 0 || j > 0);
     mm_commit<CTAS>(at.empty + 8 * ring.stage);
     ring.next(at.stages);
   }
@@ -196,11 +190,12 @@ struct TmemSource {
   }
 };
 
-// A finished unit: its epilogue, or its sums left for the join.  A warp has 32 rows
+// A unit's epilogue once it is summed, or its sums left for the join; false where
+// the wait gave up.  A warp has 32 rows
 // and half of the columns, where a half has 64 of them.
 template <int EPI, int CTAS>
-__device__ __forceinline__ void finish_unit(const MmParams& p, uint32_t unit, const Place& at, int acc, int warp, int lane,
-                                            float* block) {
+__device__ __forceinline__ bool finish_unit(const MmParams& p, uint32_t unit, const Place& at, int acc, uint32_t parity,
+                                            int warp, int lane, float* block) {
   constexpr int TILE_ROWS = kMmRows * CTAS;
   const int width = p.tn >= (EPI == MM_GATED ? 256 : 128) ? p.tn / 2 : p.tn;
   const int c0 = warp / 4 * width, c1 = c0 < p.tn ? c0 + width : c0;
@@ -211,9 +206,12 @@ __device__ __forceinline__ void finish_unit(const MmParams& p, uint32_t unit, co
   const TmemSource src = {at.tmem + ((uint32_t)(quarter * 32) << 16) + acc * kMmTileN, p.depth != 0};
   const int in_tile = (int)at.rank * kMmRows + quarter * 32;
   const int64_t row0 = (int64_t)tm * TILE_ROWS + in_tile;
+  if (EPI == MM_OUT && p.splits == 1) mm_prefetch_added(p, row0, tn, c0, c1, lane);
+  if (!__all_sync(~0u, mm_bar_wait(at.acc_full + 8 * acc, parity, at.guard))) return false;
+  mm_fence_after();
   if (p.splits == 1) {
     mm_epilogue<EPI>(p, row0, tn, c0, c1, lane, block, src);
-    return;
+    return true;
   }
   const int64_t rows = p.M < TILE_ROWS ? p.M : TILE_ROWS;
   float4* to = reinterpret_cast<float4*>(p.partial + (unit * rows + in_tile + lane) * p.tn);
@@ -225,6 +223,7 @@ __device__ __forceinline__ void finish_unit(const MmParams& p, uint32_t unit, co
       for (int j = 0; j < 8; ++j) to[c / 4 + j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
     }
   }
+  return true;
 }
 
 }  // namespace
@@ -302,12 +301,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) vc_mm(const __grid_constant__ M
     float* block = reinterpret_cast<float*>(raw + (blocks - mm_smem(raw))) + warp * kMmBlockWords;
     for (uint32_t n = 0; unit_at<TWO>(all, me, of, n, u); ++n) {
       const int acc = n & 1;
-      if (!__all_sync(~0u, mm_bar_wait(at.acc_full + 8 * acc, (n >> 1) & 1, at.guard))) break;
-      mm_fence_after();
-      if (TWO)
-        finish_unit<EPI, CTAS>(all.p[u.second], u.at, at, acc, warp, lane, block);
-      else
-        finish_unit<EPI, CTAS>(all.p[0], u.at, at, acc, warp, lane, block);
+      if (!finish_unit<EPI, CTAS>(all.p[TWO && u.second], u.at, at, acc, (n >> 1) & 1, warp, lane, block)) break;
       mm_fence_before();
       __syncwarp();
       if (lane == 0) {

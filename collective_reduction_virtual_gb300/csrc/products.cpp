@@ -61,9 +61,9 @@ struct Plan {
 };
 
 // The cheapest by a model of cycles.  A step of 64 places takes the tensor cores 2
-// tn, or as long as the step's operands take to arrive: at 24 bytes a cycle and SM
-// from memory where one row of tiles takes each column once, at 80 from L2 where
-// rows of tiles share them.  A tile's epilogue goes beside the next tile's sum, but
+// tn, or as long as the step's operands take to arrive, at 45 bytes a cycle and SM
+// from memory where one row of tiles takes each column once, 3600 for all SMs, and
+// at 80 from L2 where rows of tiles share them.  A tile's epilogue goes beside the next tile's sum, but
 // for the last one's.  Alone, a product takes whole waves of units; two fill each
 // other's last waves to within a unit.
 Plan search_plan(const Shape* shape, int count) {
@@ -86,10 +86,10 @@ Plan search_plan(const Shape* shape, int count) {
         if (tn == 64 && (s.halves || ctas == 2)) continue;
         const double tiles = (double)tiles_m * (double)ceil_div(s.N, s.halves ? tn / 2 : tn);
         const double bytes = 128.0 * (double)(std::min<int64_t>(s.M, kMmRows) + tn / ctas);
-        const double step = std::max(2.0 * tn, bytes / (tiles_m > 1 ? 80 : 24));
         for (int k : {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16}) {
           if (k > 1 && (steps / k < 4 || tiles * k > 8 * kPlanSms)) break;
-          const double units = tiles * k;
+          const double units = tiles * k, rate = tiles_m > 1 ? 80 : std::min(45.0, 3600 / std::min(units, slots));
+          const double step = std::max(2.0 * tn, bytes / rate);
           Choice& c = choice[i][choices[i]++];
           c = {tn, k, units, (double)ceil_div(steps, k) * step + 200, 0.0, 10.0 * tn + 1000, 0};
           if (k > 1) {
@@ -354,7 +354,20 @@ int products(MmEpilogue epilogue, MmLaunch* all, void* partial, void* stream) {
     }
   }
   if (!count) return VCOLL_OK;
-  const Plan plan = make_plan(shape, count);
+  Plan plan = make_plan(shape, count);
+#ifdef MM_DEBUG
+  if (const char* e = getenv("MM_PLAN")) {
+    int tn = 0, sp = 0;
+    if (sscanf(e, "%d,%d", &tn, &sp) == 2 && count == 1) {
+      plan.of[0].tn = tn;
+      plan.of[0].splits = sp;
+    }
+  }
+  if (getenv("MM_SHOW"))
+    for (int i = 0; i < count; ++i)
+      fprintf(stderr, "epi %d M %ld N %ld K %ld parts %d: ctas %d tn %d splits %d\n", (int)epilogue, shape[i].M, shape[i].N, shape[i].K,
+              shape[i].parts, plan.ctas, plan.of[i].tn, plan.of[i].splits);
+#endif
   all->error_word = device_error_symbol();
   if (!all->error_word) return fail(VCOLL_ERR_CUDA, "the device error word has no address");
   int64_t units = 0, join_blocks = 0;
