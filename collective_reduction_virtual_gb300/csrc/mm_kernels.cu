@@ -89,8 +89,9 @@ struct Ring {
   }
 };
 
-// A unit's copies into the ring; the number of stages that were filled.  One lane
-// has a few hundred cycles for a step: what does not change is outside the loop.
+// A unit's copies into the ring, by a whole warp of which one lane issues them; the
+// number of stages that were filled.  A step has 256 cycles: what does not change
+// is outside the loop.
 template <int EPI, int CTAS, bool A_MN>
 __device__ __forceinline__ uint32_t load_unit(const MmParams& p, uint32_t unit, const Place& at, Ring& ring) {
   constexpr int TILE_ROWS = kMmRows * CTAS;
@@ -112,10 +113,13 @@ __device__ __forceinline__ uint32_t load_unit(const MmParams& p, uint32_t unit, 
     const int pa = mm_pair_a(pairs, q), pb = mm_pair_b(pairs, q);
     for (; k < depth; k += stride, ++done) {
       // an empty stage's barrier was never used: the phase before its first is over
-      if (!mm_bar_wait(at.empty + 8 * ring.stage, (ring.round & 1) ^ 1, at.guard)) return done;
+      if (!mm_warp_wait(at.empty + 8 * ring.stage, (ring.round & 1) ^ 1, at.guard)) return done;
       const uint32_t a = at.stage0 + ring.stage * at.stage_bytes, b = a + stage_a, bar = signal + 8 * ring.stage;
-      if (CTAS == 1 || at.rank == 0) mm_bar_expect(at.full + 8 * ring.stage, bytes);
+      const uint32_t mine = at.full + 8 * ring.stage;
+      ring.next(at.stages);
       const int kk = (int)(k * kMmDepth);
+      if (!mm_elect()) continue;
+      if (CTAS == 1 || at.rank == 0) mm_bar_expect(mine, bytes);
       if (A_MN) {
 #pragma unroll
         for (int c = 0; c < kMmRows / 64; ++c) mm_load_box<CTAS>(a + c * 8192, map_a, row + 64 * c, kk, pa, bar);
@@ -136,13 +140,13 @@ __device__ __forceinline__ uint32_t load_unit(const MmParams& p, uint32_t unit, 
       } else {
         mm_load_box<CTAS>(b, map_b, kk, col, pb, bar);
       }
-      ring.next(at.stages);
     }
   }
   return done;
 }
 
-// A unit's products into the accumulators `acc`; false where a wait gave up.
+// A unit's products into the accumulators `acc`, by a whole warp of which one lane
+// issues them; false where a wait gave up.
 template <int EPI, int CTAS, bool A_MN>
 __device__ __forceinline__ bool multiply_unit(const MmParams& p, uint32_t unit, const Place& at, Ring& ring, int acc) {
   constexpr bool B_MN = EPI == MM_OUT;
@@ -152,17 +156,18 @@ __device__ __forceinline__ bool multiply_unit(const MmParams& p, uint32_t unit, 
   uint32_t tile, split;
   const uint32_t steps = steps_of(p, unit, tile, split);
   for (uint32_t i = 0; i < steps; ++i) {
-    if (!mm_bar_wait(at.full + 8 * ring.stage, ring.round & 1, at.guard)) return false;
+    if (!mm_warp_wait(at.full + 8 * ring.stage, ring.round & 1, at.guard)) return false;
     mm_fence_after();
-    const uint32_t a = at.stage0 + ring.stage * at.stage_bytes;
+    const uint32_t a = at.stage0 + ring.stage * at.stage_bytes, free = at.empty + 8 * ring.stage;
+    ring.next(at.stages);
     const uint64_t da = mm_desc(a, A_MN), db = mm_desc(a + stage_a, B_MN);
+    if (!mm_elect()) continue;
 #pragma unroll
     for (int j = 0; j < kMmDepth / 16; ++j)
       mm_mma<CTAS>(d, da + j * mm_desc_step(A_MN), db + j * mm_desc_step(B_MN), idesc, i > 0 || j > 0);
-    mm_commit<CTAS>(at.empty + 8 * ring.stage);
-    ring.next(at.stages);
+    mm_commit<CTAS>(free);
   }
-  mm_commit<CTAS>(at.acc_full + 8 * acc);
+  if (mm_elect()) mm_commit<CTAS>(at.acc_full + 8 * acc);
   return true;
 }
 
@@ -207,7 +212,7 @@ __device__ __forceinline__ bool finish_unit(const MmParams& p, uint32_t unit, co
   const int in_tile = (int)at.rank * kMmRows + quarter * 32;
   const int64_t row0 = (int64_t)tm * TILE_ROWS + in_tile;
   if (EPI == MM_OUT && p.splits == 1) mm_prefetch_added(p, row0, tn, c0, c1, lane);
-  if (!__all_sync(~0u, mm_bar_wait(at.acc_full + 8 * acc, parity, at.guard))) return false;
+  if (!mm_warp_wait(at.acc_full + 8 * acc, parity, at.guard)) return false;
   mm_fence_after();
   if (p.splits == 1) {
     mm_epilogue<EPI>(p, row0, tn, c0, c1, lane, block, src);
@@ -235,7 +240,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) vc_mm(const __grid_constant__ M
   __shared__ volatile int gave_up;
   __shared__ uint32_t tmem_at;
   constexpr bool TWO = EPI == MM_OUT;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x % 32;  // the warp's, as the compiler sees it
   Place at;
   at.stage0 = (mm_smem(raw) + 1023) & ~1023u;  // of 128-byte swizzle atoms
   const uint32_t blocks = at.stage0 + kMmStageRoom;
@@ -266,35 +271,34 @@ __global__ void __launch_bounds__(kMmThreads, 1) vc_mm(const __grid_constant__ M
   __syncthreads();
   if (CTAS > 1) mm_cluster_sync();
   mm_fence_after();
-  at.tmem = tmem_at;
+  at.tmem = __shfl_sync(~0u, tmem_at, 0);
 
   const uint32_t me = blockIdx.x / CTAS, of = gridDim.x / CTAS;
   Unit u;
+  auto go_on = [&] { return !__any_sync(~0u, gave_up); };
   if (warp == kMmEpilogueWarps) {
-    if (lane == 0) {
-      Ring ring;
-      int64_t issued = 0;
-      for (uint32_t n = 0; !gave_up && unit_at<TWO>(all, me, of, n, u); ++n)
-        issued += TWO && u.second ? load_unit<EPI, CTAS, true>(all.p[1], u.at, at, ring)
-                                  : load_unit<EPI, CTAS, false>(all.p[0], u.at, at, ring);
-      if (gave_up && at.rank == 0)  // copies cannot be called back: their memory has to stay until they have landed
-        for (int64_t i = issued < at.stages ? 0 : issued - at.stages; i < issued; ++i)
-          mm_bar_wait(at.full + 8 * (i % at.stages), (i / at.stages) & 1, at.guard, kMmDrainNs);
-    }
+    Ring ring;
+    int64_t issued = 0;
+    for (uint32_t n = 0; go_on() && unit_at<TWO>(all, me, of, n, u); ++n)
+      issued += TWO && u.second ? load_unit<EPI, CTAS, true>(all.p[1], u.at, at, ring)
+                                : load_unit<EPI, CTAS, false>(all.p[0], u.at, at, ring);
+    if (!go_on() && at.rank == 0)  // copies cannot be called back: their memory has to stay until they have landed
+      for (int64_t i = issued < at.stages ? 0 : issued - at.stages; i < issued; ++i)
+        mm_warp_wait(at.full + 8 * (i % at.stages), (i / at.stages) & 1, at.guard, kMmDrainNs);
   } else if (warp == kMmEpilogueWarps + 1) {
-    if (lane == 0 && at.rank == 0) {
+    if (at.rank == 0) {
       Ring ring;
-      for (uint32_t n = 0; !gave_up && unit_at<TWO>(all, me, of, n, u); ++n) {
+      for (uint32_t n = 0; go_on() && unit_at<TWO>(all, me, of, n, u); ++n) {
         const int acc = n & 1;
-        if (!mm_bar_wait(at.acc_empty + 8 * acc, ((n >> 1) & 1) ^ 1, at.guard)) break;
+        if (!mm_warp_wait(at.acc_empty + 8 * acc, ((n >> 1) & 1) ^ 1, at.guard)) break;
         mm_fence_after();
         const bool ok = TWO && u.second ? multiply_unit<EPI, CTAS, true>(all.p[1], u.at, at, ring, acc)
                                         : multiply_unit<EPI, CTAS, false>(all.p[0], u.at, at, ring, acc);
         if (!ok) break;
       }
-      if (gave_up) {
-        mm_commit<CTAS>(at.drained);
-        mm_bar_wait(at.drained, 0, at.guard, kMmDrainNs);
+      if (!go_on()) {
+        if (mm_elect()) mm_commit<CTAS>(at.drained);
+        mm_warp_wait(at.drained, 0, at.guard, kMmDrainNs);
       }
     }
   } else {

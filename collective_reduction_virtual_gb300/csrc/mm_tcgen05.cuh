@@ -39,6 +39,18 @@ __device__ __forceinline__ bool mm_bar_try(uint32_t bar, unsigned parity) {
   return done != 0;
 }
 
+// One lane of a whole warp, always the same: what it issues has operands that the
+// compiler knows to be the warp's.
+__device__ __forceinline__ bool mm_elect() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(yes));
+  return yes != 0;
+}
+
 // What a CTA's waits share: where a wait that gives up is recorded, and that
 // the CTA's other waits need not be waited for any more.
 struct MmAbort {
@@ -84,6 +96,12 @@ __device__ __forceinline__ uint32_t mm_rank() {
 }
 __device__ __forceinline__ void mm_cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// For a whole warp: whether all of its lanes' waits came to their end.
+__device__ __forceinline__ bool mm_warp_wait(uint32_t bar, unsigned parity, const MmAbort& a,
+                                             uint64_t limit = kMmWaitNs) {
+  return __all_sync(~0u, mm_bar_wait(bar, parity, a, limit));
 }
 
 // A box of a tensor map into this CTA's shared memory; its bytes count on `bar`
