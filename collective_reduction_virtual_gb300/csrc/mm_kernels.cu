@@ -71,6 +71,12 @@ __device__ __forceinline__ uint32_t steps_of(const MmParams& p, uint32_t unit, u
   return (steps - split + p.splits - 1) / p.splits;
 }
 
+// Steps of a unit's first chunk: the small ones of the parts' products together.
+__device__ __forceinline__ uint32_t first_chunk(const MmParams& p, uint32_t split) {
+  if (p.parts == 1) return p.chunk;
+  return ((mm_pairs(p.parts) - 1) * p.depth - split + p.splits - 1) / p.splits;
+}
+
 // Where a CTA's parts lie in shared memory, and its place in a pair.
 struct Place {
   uint32_t stage0, full, empty, acc_full, acc_empty, drained;
@@ -145,30 +151,50 @@ __device__ __forceinline__ uint32_t load_unit(const MmParams& p, uint32_t unit, 
   return done;
 }
 
-// A unit's products into the accumulators `acc`, by a whole warp of which one lane
-// issues them; false where a wait gave up.
+// A unit's products into the accumulators, by a whole warp of which one lane issues
+// them: `chunk` steps into one half of them, the next into the other.  turn counts
+// the chunks.  False where a wait gave up.
 template <int EPI, int CTAS, bool A_MN>
-__device__ __forceinline__ bool multiply_unit(const MmParams& p, uint32_t unit, const Place& at, Ring& ring, int acc) {
+__device__ __forceinline__ bool multiply_unit(const MmParams& p, uint32_t unit, const Place& at, Ring& ring,
+                                              uint32_t& turn) {
   constexpr bool B_MN = EPI == MM_OUT;
   const uint32_t idesc = mm_idesc(A_MN, B_MN, kMmRows * CTAS, p.tn);
   const int stage_a = p.a_rows * kMmDepth * 2;
-  const uint32_t d = at.tmem + acc * kMmTileN;
-  uint32_t tile, split;
-  const uint32_t steps = steps_of(p, unit, tile, split);
-  for (uint32_t i = 0; i < steps; ++i) {
-    if (!mm_warp_wait(at.full + 8 * ring.stage, ring.round & 1, at.guard)) return false;
+  uint32_t tile, split, left = steps_of(p, unit, tile, split), chunk = first_chunk(p, split);
+  do {
+    const uint32_t acc = turn & 1, d = at.tmem + acc * kMmTileN;
+    if (!mm_warp_wait(at.acc_empty + 8 * acc, ((turn >> 1) & 1) ^ 1, at.guard)) return false;
     mm_fence_after();
-    const uint32_t a = at.stage0 + ring.stage * at.stage_bytes, free = at.empty + 8 * ring.stage;
-    ring.next(at.stages);
-    const uint64_t da = mm_desc(a, A_MN), db = mm_desc(a + stage_a, B_MN);
-    if (!mm_elect()) continue;
+    const uint32_t steps = left < chunk ? left : chunk;
+    for (uint32_t i = 0; i < steps; ++i) {
+      if (!mm_warp_wait(at.full + 8 * ring.stage, ring.round & 1, at.guard)) return false;
+      mm_fence_after();
+      const uint32_t a = at.stage0 + ring.stage * at.stage_bytes, free = at.empty + 8 * ring.stage;
+      ring.next(at.stages);
+      const uint64_t da = mm_desc(a, A_MN), db = mm_desc(a + stage_a, B_MN);
+      if (!mm_elect()) continue;
 #pragma unroll
-    for (int j = 0; j < kMmDepth / 16; ++j)
-      mm_mma<CTAS>(d, da + j * mm_desc_step(A_MN), db + j * mm_desc_step(B_MN), idesc, i > 0 || j > 0);
-    mm_commit<CTAS>(free);
-  }
-  if (mm_elect()) mm_commit<CTAS>(at.acc_full + 8 * acc);
+      for (int j = 0; j < kMmDepth / 16; ++j)
+        mm_mma<CTAS>(d, da + j * mm_desc_step(A_MN), db + j * mm_desc_step(B_MN), idesc, i > 0 || j > 0);
+      mm_commit<CTAS>(free);
+    }
+    if (mm_elect()) mm_commit<CTAS>(at.acc_full + 8 * acc);
+    ++turn;
+    left -= steps;
+    chunk = p.chunk;
+  } while (left);
   return true;
+}
+
+// The accumulators of a turn may be summed into again, as far as this warp goes.
+template <int CTAS>
+__device__ __forceinline__ void release(const Place& at, uint32_t turn) {
+  const uint32_t bar = at.acc_empty + 8 * (turn & 1);
+  if (!mm_elect()) return;
+  if (CTAS == 1)
+    mm_bar_arrive(bar);
+  else
+    mm_bar_arrive_at(mm_of_first(bar));
 }
 
 // A warp's accumulators in tensor memory; zeros where nothing was summed.
@@ -176,8 +202,8 @@ struct TmemSource {
   uint32_t at;
   bool any;
 
-  __device__ __forceinline__ void give(const uint32_t (&r)[32], float (&v)[32]) const {
-    mm_tmem_wait();
+  __device__ __forceinline__ void give(uint32_t (&r)[32], float (&v)[32]) const {
+    mm_tmem_wait32(r);
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = any ? __uint_as_float(r[j]) : 0.0f;
   }
@@ -195,27 +221,73 @@ struct TmemSource {
   }
 };
 
+// Chunks of a sum, added in registers.  The last one is not waited for here; the
+// sum of the others is added to it in tensor memory by `finish`.  A warp's columns
+// are two runs of 16 `groups` / 2 of them.
+struct ChunkSum {
+  float sum[8][16];
+
+  // add: this chunk to the sum; else the sum to this chunk, in tensor memory
+  template <bool ADD>
+  __device__ __forceinline__ void take(uint32_t tmem, int run0, int run1, int groups) {
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      if (g >= groups) break;
+      const uint32_t col = tmem + (g < groups / 2 ? run0 + 16 * g : run1 + 16 * (g - groups / 2));
+      uint32_t r[16];
+      mm_tmem_load16(col, r);
+      mm_tmem_wait16(r);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) sum[g][j] += __uint_as_float(r[j]);
+      if (!ADD) mm_tmem_store16(col, sum[g]);
+    }
+    if (!ADD) mm_tmem_stored();
+  }
+};
+
 // A unit's epilogue once it is summed, or its sums left for the join; false where
-// the wait gave up.  A warp has 32 rows
-// and half of the columns, where a half has 64 of them.
+// the wait gave up.  A warp has 32 rows and half of the columns, where a half has 64
+// of them.
 template <int EPI, int CTAS>
-__device__ __forceinline__ bool finish_unit(const MmParams& p, uint32_t unit, const Place& at, int acc, uint32_t parity,
-                                            int warp, int lane, float* block) {
+__device__ __forceinline__ bool finish_unit(const MmParams& p, uint32_t unit, const Place& at, uint32_t& turn, int warp,
+                                            int lane, float* block) {
   constexpr int TILE_ROWS = kMmRows * CTAS;
   const int width = p.tn >= (EPI == MM_GATED ? 256 : 128) ? p.tn / 2 : p.tn;
   const int c0 = warp / 4 * width, c1 = c0 < p.tn ? c0 + width : c0;
   const int quarter = warp % 4;  // of tensor memory's lanes, which this warp can read
-  uint32_t tile = unit, tm, tn;
-  if (p.splits > 1) tile = unit / p.splits;
+  const uint32_t lanes = at.tmem + ((uint32_t)(quarter * 32) << 16);
+  uint32_t tile, tm, tn, split;
+  uint32_t left = steps_of(p, unit, tile, split);
   tile_at(p, TILE_ROWS, tile, tm, tn);
-  const TmemSource src = {at.tmem + ((uint32_t)(quarter * 32) << 16) + acc * kMmTileN, p.depth != 0};
   const int in_tile = (int)at.rank * kMmRows + quarter * 32;
   const int64_t row0 = (int64_t)tm * TILE_ROWS + in_tile;
   if (EPI == MM_OUT && p.splits == 1) mm_prefetch_added(p, row0, tn, c0, c1, lane);
-  if (!mm_warp_wait(at.acc_full + 8 * acc, parity, at.guard)) return false;
-  mm_fence_after();
+  uint32_t chunk = first_chunk(p, split);
+  if (left > chunk) {
+    ChunkSum s = {};
+    // in a gated tile a warp's columns are as many of gate's and of up's
+    const int run0 = EPI == MM_GATED ? c0 / 2 : c0, run1 = EPI == MM_GATED ? p.tn / 2 + c0 / 2 : c0 + (c1 - c0) / 2;
+    for (; left > chunk; left -= chunk, chunk = p.chunk, ++turn) {
+      if (!mm_warp_wait(at.acc_full + 8 * (turn & 1), (turn >> 1) & 1, at.guard)) return false;
+      mm_fence_after();
+      s.take<true>(lanes + (turn & 1) * kMmTileN, run0, run1, (c1 - c0) / 16);
+      mm_fence_before();
+      __syncwarp();
+      release<CTAS>(at, turn);
+    }
+    if (!mm_warp_wait(at.acc_full + 8 * (turn & 1), (turn >> 1) & 1, at.guard)) return false;
+    mm_fence_after();
+    s.take<false>(lanes + (turn & 1) * kMmTileN, run0, run1, (c1 - c0) / 16);
+  } else {
+    if (!mm_warp_wait(at.acc_full + 8 * (turn & 1), (turn >> 1) & 1, at.guard)) return false;
+    mm_fence_after();
+  }
+  const TmemSource src = {lanes + (turn & 1) * kMmTileN, p.depth != 0};
   if (p.splits == 1) {
     mm_epilogue<EPI>(p, row0, tn, c0, c1, lane, block, src);
+    mm_fence_before();
+    __syncwarp();
+    release<CTAS>(at, turn++);
     return true;
   }
   const int64_t rows = p.M < TILE_ROWS ? p.M : TILE_ROWS;
@@ -228,6 +300,9 @@ __device__ __forceinline__ bool finish_unit(const MmParams& p, uint32_t unit, co
       for (int j = 0; j < 8; ++j) to[c / 4 + j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
     }
   }
+  mm_fence_before();
+  __syncwarp();
+  release<CTAS>(at, turn++);
   return true;
 }
 
@@ -288,14 +363,11 @@ __global__ void __launch_bounds__(kMmThreads, 1) vc_mm(const __grid_constant__ M
   } else if (warp == kMmEpilogueWarps + 1) {
     if (at.rank == 0) {
       Ring ring;
-      for (uint32_t n = 0; go_on() && unit_at<TWO>(all, me, of, n, u); ++n) {
-        const int acc = n & 1;
-        if (!mm_warp_wait(at.acc_empty + 8 * acc, ((n >> 1) & 1) ^ 1, at.guard)) break;
-        mm_fence_after();
-        const bool ok = TWO && u.second ? multiply_unit<EPI, CTAS, true>(all.p[1], u.at, at, ring, acc)
-                                        : multiply_unit<EPI, CTAS, false>(all.p[0], u.at, at, ring, acc);
-        if (!ok) break;
-      }
+      uint32_t turn = 0;
+      bool ok = true;
+      for (uint32_t n = 0; ok && go_on() && unit_at<TWO>(all, me, of, n, u); ++n)
+        ok = TWO && u.second ? multiply_unit<EPI, CTAS, true>(all.p[1], u.at, at, ring, turn)
+                             : multiply_unit<EPI, CTAS, false>(all.p[0], u.at, at, ring, turn);
       if (!go_on()) {
         if (mm_elect()) mm_commit<CTAS>(at.drained);
         mm_warp_wait(at.drained, 0, at.guard, kMmDrainNs);
@@ -303,18 +375,9 @@ __global__ void __launch_bounds__(kMmThreads, 1) vc_mm(const __grid_constant__ M
     }
   } else {
     float* block = reinterpret_cast<float*>(raw + (blocks - mm_smem(raw))) + warp * kMmBlockWords;
-    for (uint32_t n = 0; unit_at<TWO>(all, me, of, n, u); ++n) {
-      const int acc = n & 1;
-      if (!finish_unit<EPI, CTAS>(all.p[TWO && u.second], u.at, at, acc, (n >> 1) & 1, warp, lane, block)) break;
-      mm_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (CTAS == 1)
-          mm_bar_arrive(at.acc_empty + 8 * acc);
-        else
-          mm_bar_arrive_at(mm_of_first(at.acc_empty + 8 * acc));
-      }
-    }
+    uint32_t turn = 0;
+    for (uint32_t n = 0; unit_at<TWO>(all, me, of, n, u); ++n)
+      if (!finish_unit<EPI, CTAS>(all.p[TWO && u.second], u.at, at, turn, warp, lane, block)) break;
   }
   __syncwarp();
   mm_fence_before();

@@ -264,6 +264,11 @@ bool rows_at_16(const void* p, int64_t rows, int64_t ld, int es) {
   return (uint64_t)p % 16 == 0 && (rows <= 1 || ld * es % 16 == 0);
 }
 
+// CTAs of a pass of mm_parts.cu over so many groups of eight values, one a thread:
+// CTAs in order keep what is in flight close together in memory (16384 x 11008
+// gradients: xx us, and 390 with eight CTAs per SM that go around).
+int64_t pass_blocks(int64_t groups) { return std::min<int64_t>(ceil_div(groups, kPassThreads), 1 << 28); }
+
 // Matrices that are laid out as parts by one launch.
 struct Packer {
   MmPackParams p = {};
@@ -294,10 +299,8 @@ struct Packer {
     j.load16 = rows_at_16(src, rows, ld, p.src_f32 ? 4 : 2);
     *o = operand(to, rows, cols, j.dst_ld, j.plane);
     if (!rows || !cols) return VCOLL_OK;
-    int sms = 0;
-    VCOLL_TRY(device_sms(&sms));
     j.first_block = blocks;
-    j.blocks = std::min<int64_t>(ceil_div(rows * ceil_div(cols, 8), kPassThreads), (int64_t)sms * 8);
+    j.blocks = pass_blocks(rows * ceil_div(cols, 8));
     blocks += j.blocks;
     ++jobs;
     return VCOLL_OK;
@@ -386,6 +389,7 @@ int products(MmEpilogue epilogue, MmLaunch* all, void* partial, void* stream) {
     p->units = (uint32_t)(tiles_m * tiles_n) * p->splits;
     units += p->units;
     p->depth = (uint32_t)ceil_div(p->K, kMmDepth);
+    p->chunk = p->parts > 1 ? kMmChunkParts : epilogue == MM_LSE ? kMmChunkLoss : kMmChunkBf16;
     p->a_rows = a_mn || plan.ctas == 2 ? kMmRows : (int)std::min<int64_t>(kMmRows, round_up(p->M, 8));
     all->stage_bytes = std::max(all->stage_bytes, (p->a_rows + p->tn / plan.ctas) * kMmDepth * 2);
     const bool second = p->b[1].p && !p->b_halves;
@@ -752,11 +756,7 @@ int vcoll_gated_ff_backward(const void* dh, int64_t dh_ld, const void* x, int64_
     g.parts = parts;
     g.act = activation;
     g.load16 = rows_at_16(dh, N, dh_ld, es) && rows_at_16(gate, N, gate_ld, es) && rows_at_16(up, N, up_ld, es);
-    int sms = 0;
-    VCOLL_TRY(device_sms(&sms));
-    VCOLL_TRY(launch_grid(mm_gated_grad_kernel(),
-                          std::min<int64_t>(ceil_div(N * (L.half / 8), kPassThreads), (int64_t)sms * 8), 1,
-                          kPassThreads, 0, &g, stream));
+    VCOLL_TRY(launch_grid(mm_gated_grad_kernel(), pass_blocks(N * (L.half / 8)), 1, kPassThreads, 0, &g, stream));
   }
   const MmOperand grads = operand(ws + L.grads, N, 2 * L.half, 2 * L.half, N * 2 * L.half);
   MmOperand rows, gates, ups;
