@@ -126,37 +126,35 @@ template <bool IN32, bool OUT32, bool WIDE>
 __device__ __forceinline__ void mm_add_block(const MmAdd& h, const float* block, int rows, int pair, int odd, int64_t col,
                                           int64_t left) {
   // left + pair: columns from the block's first on
-  if (left + pair <= 0) return;
+  if (left + pair <= 0 || rows <= 0) return;
   const int64_t c0 = left > 0 ? col : col + left - 1, c1 = left > 1 ? c0 + 1 : c0;
-  for (int r = odd; r < rows; r += 16) {
-    float2 x[8];
+  float2 x[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int at = r + 2 * i < rows ? r + 2 * i : rows - 1;
-      const int64_t from = h.in_at + at * h.in_ld;
-      x[i] = make_float2(0.0f, 0.0f);
-      if (!h.in) continue;
-      if (IN32) {
-        x[i].x = static_cast<const float*>(h.in)[from + c0];
-        x[i].y = static_cast<const float*>(h.in)[from + c1];
-      } else {
-        x[i].x = Elem<__nv_bfloat16>::widen1(static_cast<const uint16_t*>(h.in)[from + c0]);
-        x[i].y = Elem<__nv_bfloat16>::widen1(static_cast<const uint16_t*>(h.in)[from + c1]);
-      }
+  for (int i = 0; i < 16; ++i) {
+    const int r = 2 * i + odd < rows ? 2 * i + odd : rows - 1;
+    const int64_t from = h.in_at + r * h.in_ld;
+    x[i] = make_float2(0.0f, 0.0f);
+    if (!h.in) continue;
+    if (IN32) {
+      x[i].x = static_cast<const float*>(h.in)[from + c0];
+      x[i].y = static_cast<const float*>(h.in)[from + c1];
+    } else {
+      x[i].x = Elem<__nv_bfloat16>::widen1(static_cast<const uint16_t*>(h.in)[from + c0]);
+      x[i].y = Elem<__nv_bfloat16>::widen1(static_cast<const uint16_t*>(h.in)[from + c1]);
     }
+  }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int at = r + 2 * i;
-      if (at >= rows) break;
-      const float y0 = (x[i].x + h.first * block[at * kMmPitch + pair]) * h.then,
-                  y1 = (x[i].y + h.first * block[at * kMmPitch + pair + 1]) * h.then;
-      mm_store2(h.out, OUT32, WIDE, h.out_at + at * h.out_ld + col, left, y0, y1);
-    }
+  for (int i = 0; i < 16; ++i) {
+    const int r = 2 * i + odd;
+    if (r >= rows) break;
+    const float y0 = (x[i].x + h.first * block[r * kMmPitch + pair]) * h.then,
+                y1 = (x[i].y + h.first * block[r * kMmPitch + pair + 1]) * h.then;
+    mm_store2(h.out, OUT32, WIDE, h.out_at + r * h.out_ld + col, left, y0, y1);
   }
 }
 
-// What a unit's epilogue will add, fetched to L2 while the unit is being summed:
-// a lane a row of the warp's 32.
+// What an epilogue will add, fetched to L2 a unit ahead: a lane a row of the warp's
+// 32.
 __device__ __forceinline__ void mm_prefetch_added(const MmParams& p, int64_t row0, int64_t tile_n, int c0, int c1, int lane) {
   if (!p.accum_in && !p.base) return;
   const int rows = mm_rows(p, row0);

@@ -245,23 +245,38 @@ struct ChunkSum {
   }
 };
 
+// What a warp has of a unit: 32 rows, and half of the columns, where a half has 64 of
+// them.
+struct Share {
+  uint32_t tn, split, steps;
+  int c0, c1, in_tile;
+  int64_t row0;
+};
+template <int EPI, int CTAS>
+__device__ __forceinline__ Share share_of(const MmParams& p, uint32_t unit, const Place& at, int warp) {
+  Share s;
+  const int width = p.tn >= (EPI == MM_GATED ? 256 : 128) ? p.tn / 2 : p.tn;
+  s.c0 = warp / 4 * width;
+  s.c1 = s.c0 < p.tn ? s.c0 + width : s.c0;
+  uint32_t tile, tm;
+  s.steps = steps_of(p, unit, tile, s.split);
+  tile_at(p, kMmRows * CTAS, tile, tm, s.tn);
+  s.in_tile = (int)at.rank * kMmRows + warp % 4 * 32;  // of tensor memory a warp reads a quarter
+  s.row0 = (int64_t)tm * kMmRows * CTAS + s.in_tile;
+  return s;
+}
+
 // A unit's epilogue once it is summed, or its sums left for the join; false where
-// the wait gave up.  A warp has 32 rows and half of the columns, where a half has 64
-// of them.
+// the wait gave up.
 template <int EPI, int CTAS>
 __device__ __forceinline__ bool finish_unit(const MmParams& p, uint32_t unit, const Place& at, uint32_t& turn, int warp,
                                             int lane, float* block) {
   constexpr int TILE_ROWS = kMmRows * CTAS;
-  const int width = p.tn >= (EPI == MM_GATED ? 256 : 128) ? p.tn / 2 : p.tn;
-  const int c0 = warp / 4 * width, c1 = c0 < p.tn ? c0 + width : c0;
-  const int quarter = warp % 4;  // of tensor memory's lanes, which this warp can read
-  const uint32_t lanes = at.tmem + ((uint32_t)(quarter * 32) << 16);
-  uint32_t tile, tm, tn, split;
-  uint32_t left = steps_of(p, unit, tile, split);
-  tile_at(p, TILE_ROWS, tile, tm, tn);
-  const int in_tile = (int)at.rank * kMmRows + quarter * 32;
-  const int64_t row0 = (int64_t)tm * TILE_ROWS + in_tile;
-  if (EPI == MM_OUT && p.splits == 1) mm_prefetch_added(p, row0, tn, c0, c1, lane);
+  const Share mine = share_of<EPI, CTAS>(p, unit, at, warp);
+  const int c0 = mine.c0, c1 = mine.c1, in_tile = mine.in_tile;
+  const int64_t row0 = mine.row0;
+  const uint32_t split = mine.split, tn = mine.tn, lanes = at.tmem + ((uint32_t)(warp % 4 * 32) << 16);
+  uint32_t left = mine.steps;
   uint32_t chunk = first_chunk(p, split);
   if (left > chunk) {
     ChunkSum s = {};
@@ -376,8 +391,17 @@ __global__ void __launch_bounds__(kMmThreads, 1) vc_mm(const __grid_constant__ M
   } else {
     float* block = reinterpret_cast<float*>(raw + (blocks - mm_smem(raw))) + warp * kMmBlockWords;
     uint32_t turn = 0;
-    for (uint32_t n = 0; unit_at<TWO>(all, me, of, n, u); ++n)
+    for (uint32_t n = 0; unit_at<TWO>(all, me, of, n, u); ++n) {
+      Unit next;
+      if (EPI == MM_OUT)
+        for (uint32_t ahead = n ? 1 : 0; ahead < 2 && unit_at<TWO>(all, me, of, n + ahead, next); ++ahead) {
+          const MmParams& p = all.p[next.second];
+          if (p.splits > 1 || (!p.accum_in && !p.base)) continue;
+          const Share s = share_of<EPI, CTAS>(p, next.at, at, warp);
+          mm_prefetch_added(p, s.row0, s.tn, s.c0, s.c1, lane);
+        }
       if (!finish_unit<EPI, CTAS>(all.p[TWO && u.second], u.at, at, turn, warp, lane, block)) break;
+    }
   }
   __syncwarp();
   mm_fence_before();
