@@ -122,27 +122,45 @@ struct MmAdd {
   int64_t out_at, out_ld;
   float first, then;
 };
-template <bool IN32, bool OUT32, bool WIDE>
-__device__ __forceinline__ void mm_add_block(const MmAdd& h, const float* block, int rows, int pair, int odd, int64_t col,
-                                          int64_t left) {
-  // left + pair: columns from the block's first on
-  if (left + pair <= 0 || rows <= 0) return;
-  const int64_t c0 = left > 0 ? col : col + left - 1, c1 = left > 1 ? c0 + 1 : c0;
-  float2 x[16];
+template <bool IN32, bool WIDE>
+__device__ __forceinline__ void mm_add_load(const MmAdd& h, float2 (&x)[16], int rows, int pair, int odd, int64_t col,
+                                            int64_t left) {
+  // left + pair, the same for all lanes: columns from the block's first on.  No
+  // condition stands between the loads, which would wait for each other.
+  if (!h.in || rows <= 0 || left + pair <= 0) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int r = 2 * i + odd < rows ? 2 * i + odd : rows - 1;
-    const int64_t from = h.in_at + r * h.in_ld;
-    x[i] = make_float2(0.0f, 0.0f);
-    if (!h.in) continue;
-    if (IN32) {
-      x[i].x = static_cast<const float*>(h.in)[from + c0];
-      x[i].y = static_cast<const float*>(h.in)[from + c1];
-    } else {
-      x[i].x = Elem<__nv_bfloat16>::widen1(static_cast<const uint16_t*>(h.in)[from + c0]);
-      x[i].y = Elem<__nv_bfloat16>::widen1(static_cast<const uint16_t*>(h.in)[from + c1]);
+    for (int i = 0; i < 16; ++i) x[i] = make_float2(0.0f, 0.0f);
+  } else if (WIDE && left + pair >= 32) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int64_t at = h.in_at + (2 * i + odd < rows ? 2 * i + odd : rows - 1) * h.in_ld + col;
+      if (IN32)
+        x[i] = *reinterpret_cast<const float2*>(static_cast<const float*>(h.in) + at);
+      else
+        x[i].x = __uint_as_float(*reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(h.in) + at));
+    }
+    if (!IN32) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) Elem<__nv_bfloat16>::widen2(__float_as_uint(x[i].x), x[i].x, x[i].y);
+    }
+  } else {
+    const int64_t c0 = left > 0 ? col : col + left - 1, c1 = left > 1 ? c0 + 1 : c0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int64_t at = h.in_at + (2 * i + odd < rows ? 2 * i + odd : rows - 1) * h.in_ld;
+      if (IN32) {
+        x[i].x = static_cast<const float*>(h.in)[at + c0];
+        x[i].y = static_cast<const float*>(h.in)[at + c1];
+      } else {
+        x[i].x = __uint_as_float((uint32_t)static_cast<const uint16_t*>(h.in)[at + c0] << 16);
+        x[i].y = __uint_as_float((uint32_t)static_cast<const uint16_t*>(h.in)[at + c1] << 16);
+      }
     }
   }
+}
+template <bool OUT32, bool WIDE>
+__device__ __forceinline__ void mm_add_store(const MmAdd& h, const float2 (&x)[16], const float* block, int rows,
+                                             int pair, int odd, int64_t col, int64_t left) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const int r = 2 * i + odd;
@@ -234,33 +252,47 @@ __device__ __forceinline__ void mm_epilogue(const MmParams& p, int64_t row0, int
       }
       return;
     }
+    if (add) {
+      const MmAdd how = {p.accum_in ? (const void*)p.accum_in : p.base,
+                         p.accum_in ? row0 * p.accum_ld : to.row * p.base_ld, p.accum_in ? p.accum_ld : p.base_ld,
+                         p.accum_out ? (void*)p.accum_out : to.out,
+                         p.accum_out ? row0 * p.accum_ld : to.row * to.ld, p.accum_out ? p.accum_ld : to.ld,
+                         p.base ? scale : 1.0f, p.base || p.accum_out ? 1.0f : scale};
+      const bool out32 = p.accum_out || p.out_f32, in32 = p.accum_in || out32;
+      const bool in_wide = p.accum_in || p.out_pairs, out_wide = p.accum_out || p.out_pairs;
+      for (int c = c0; c < c1; c += 32) {
+        const int64_t col = tile_n * p.tn + c + pair, left = p.N - col;
+        float2 x[16];
+        if (in32 && in_wide)
+          mm_add_load<true, true>(how, x, rows, pair, odd, col, left);
+        else if (in32)
+          mm_add_load<true, false>(how, x, rows, pair, odd, col, left);
+        else if (in_wide)
+          mm_add_load<false, true>(how, x, rows, pair, odd, col, left);
+        else
+          mm_add_load<false, false>(how, x, rows, pair, odd, col, left);
+        src(c, v);
+        mm_to_block(block, lane, v);
+        if (out32 && out_wide)
+          mm_add_store<true, true>(how, x, block, rows, pair, odd, col, left);
+        else if (out32)
+          mm_add_store<true, false>(how, x, block, rows, pair, odd, col, left);
+        else if (out_wide)
+          mm_add_store<false, true>(how, x, block, rows, pair, odd, col, left);
+        else
+          mm_add_store<false, false>(how, x, block, rows, pair, odd, col, left);
+        __syncwarp();
+      }
+      return;
+    }
     for (int c = c0; c < c1; c += 32) {
       const int64_t col = tile_n * p.tn + c + pair, left = p.N - col;
       src(c, v);
       mm_to_block(block, lane, v);
-      if (!add) {
 #pragma unroll 4
-        for (int r = odd; r < rows; r += 2)
-          mm_store2(to.out, p.out_f32, p.out_pairs, (to.row + r) * to.ld + col, left,
-                    block[r * kMmPitch + pair] * scale, block[r * kMmPitch + pair + 1] * scale);
-      } else {
-        const MmAdd how = {p.accum_in ? (const void*)p.accum_in : p.base,
-                           p.accum_in ? row0 * p.accum_ld : to.row * p.base_ld, p.accum_in ? p.accum_ld : p.base_ld,
-                           p.accum_out ? (void*)p.accum_out : to.out,
-                           p.accum_out ? row0 * p.accum_ld : to.row * to.ld, p.accum_out ? p.accum_ld : to.ld,
-                           p.base ? scale : 1.0f, p.base || p.accum_out ? 1.0f : scale};
-        const bool out32 = p.accum_out || p.out_f32, in32 = p.accum_in || out32;
-        if (in32 && out32 && (p.out_pairs || (p.accum_in && p.accum_out)))
-          mm_add_block<true, true, true>(how, block, rows, pair, odd, col, left);
-        else if (in32 && out32)
-          mm_add_block<true, true, false>(how, block, rows, pair, odd, col, left);
-        else if (in32)
-          mm_add_block<true, false, false>(how, block, rows, pair, odd, col, left);
-        else if (p.out_pairs)
-          mm_add_block<false, false, true>(how, block, rows, pair, odd, col, left);
-        else
-          mm_add_block<false, false, false>(how, block, rows, pair, odd, col, left);
-      }
+      for (int r = odd; r < rows; r += 2)
+        mm_store2(to.out, p.out_f32, p.out_pairs, (to.row + r) * to.ld + col, left,
+                  block[r * kMmPitch + pair] * scale, block[r * kMmPitch + pair + 1] * scale);
       __syncwarp();
     }
   } else if constexpr (EPI == MM_LSE) {

@@ -46,7 +46,11 @@ struct Shape {
   int64_t M, N, K;
   int parts;
   bool halves;
+  int epilogue;  // cycles that it takes for a column of a tile
 };
+// Measured on tiles of little depth: 64 columns of bf16 at once, 32 of fp32 (or its
+// parts), and those whose rows something is added to, which is waited for.
+int epilogue_cycles(int parts, bool add = false) { return add ? 40 : parts > 1 ? 40 : 12; }
 
 // How a launch's products are cut: CTAs that share a tile, and for each product the
 // tile's columns, the splits of its sum, and a unit's cycles.
@@ -91,7 +95,8 @@ Plan search_plan(const Shape* shape, int count) {
           const double units = tiles * k, rate = tiles_m > 1 ? 80 : std::min(45.0, 3600 / std::min(units, slots));
           const double step = std::max(2.0 * tn, bytes / rate);
           Choice& c = choice[i][choices[i]++];
-          c = {tn, k, units, (double)ceil_div(steps, k) * step + 200, 0.0, 10.0 * tn + 1000, 0};
+          const double tail = (double)s.epilogue * tn + 1000;
+          c = {tn, k, units, std::max((double)ceil_div(steps, k) * step, k > 1 ? 12.0 * tn : tail) + 200, 0.0, tail, 0};
           if (k > 1) {
             c.bytes = (size_t)units * (size_t)rows * tn * sizeof(float);
             c.join = 2500 + (double)c.bytes * 2 / (10.0 * kPlanSms);
@@ -134,7 +139,8 @@ Plan make_plan(const Shape* shape, int count) {
   static thread_local Kept kept[32];
   static thread_local int next = 0;
   auto same = [](const Shape& a, const Shape& b) {
-    return a.M == b.M && a.N == b.N && a.K == b.K && a.parts == b.parts && a.halves == b.halves;
+    return a.M == b.M && a.N == b.N && a.K == b.K && a.parts == b.parts && a.halves == b.halves &&
+           a.epilogue == b.epilogue;
   };
   for (const Kept& k : kept)
     if (k.count == count && same(k.shape[0], shape[0]) && (count == 1 || same(k.shape[1], shape[1]))) return k.plan;
@@ -174,7 +180,7 @@ LossLayout loss_layout(int64_t N, int64_t V, int64_t D, int dtype, bool direct) 
   size_t splits = 0;
   int64_t tiles = 0;
   for (int64_t w : piece_widths(V, L.piece)) {
-    const Plan plan = plan_of({N, w, D, parts, false});
+    const Plan plan = plan_of({N, w, D, parts, false, epilogue_cycles(1)});
     splits = std::max(splits, plan.bytes());
     tiles = std::max(tiles, ceil_div(w, plan.of[0].tn));
   }
@@ -205,9 +211,13 @@ LossGradLayout loss_grad_layout(int64_t N, int64_t V, int64_t D, int dtype, bool
   L.accum = r.take(L.pieces > 1 ? N * round_up(D, 2) * 4 : 0);
   size_t splits = 0;
   for (int64_t w : piece_widths(V, L.piece)) {
-    const Shape s[3] = {{N, w, D, parts, false}, {N, D, w, parts, false}, {w, D, N, parts, false}};
-    splits = std::max({splits, plan_of(s[0]).bytes(), plan_of(s[1]).bytes(), plan_of(s[2]).bytes(),
-                       make_plan(s + 1, 2).bytes()});
+    const Shape error = {N, w, D, parts, false, epilogue_cycles(parts)};
+    splits = std::max(splits, plan_of(error).bytes());
+    for (const bool base : {false, true}) {  // dx, dtable, and both
+      const Shape s[2] = {{N, D, w, parts, false, epilogue_cycles(parts, L.pieces > 1)},
+                          {w, D, N, parts, false, epilogue_cycles(parts, base)}};
+      splits = std::max({splits, plan_of(s[0]).bytes(), plan_of(s[1]).bytes(), make_plan(s, 2).bytes()});
+    }
   }
   L.splits = r.take((int64_t)splits);
   L.bytes = r.bytes;
@@ -228,13 +238,16 @@ GatedLayout gated_layout(int64_t N, int64_t D, int64_t F, int dtype, bool direct
   L.w_up = r.take(direct ? 0 : packed_bytes(F, D, parts));
   L.grads = r.take(backward ? packed_bytes(N, 2 * L.half, parts) : 0);
   size_t splits = 0;
+  const int cycles = epilogue_cycles(parts);
   if (backward) {  // dx; one weight's gradient; both
-    const Shape s[3] = {{N, D, 2 * L.half, parts, false}, {F, D, N, parts, false}, {2 * L.half, D, N, parts, false}};
+    const Shape s[3] = {{N, D, 2 * L.half, parts, false, cycles},
+                        {F, D, N, parts, false, cycles},
+                        {2 * L.half, D, N, parts, false, cycles}};
     const Shape one[2] = {s[0], s[1]}, both[2] = {s[0], s[2]};
     splits = std::max({plan_of(s[0]).bytes(), plan_of(s[1]).bytes(), plan_of(s[2]).bytes(), make_plan(one, 2).bytes(),
                        make_plan(both, 2).bytes()});
   } else {
-    splits = plan_of({N, F, D, parts, true}).bytes();
+    splits = plan_of({N, F, D, parts, true, cycles}).bytes();
   }
   L.splits = r.take((int64_t)splits);
   L.bytes = r.bytes;
@@ -352,7 +365,9 @@ int products(MmEpilogue epilogue, MmLaunch* all, void* partial, void* stream) {
   for (int i = 0; i < 2; ++i) {
     const MmParams& p = all->p[i];
     if (p.M && p.N) {
-      shape[count] = {p.M, p.N, p.K, p.parts, p.b_halves != 0};
+      const int cycles = epilogue == MM_LSE ? epilogue_cycles(1)
+                                            : epilogue_cycles(p.parts, p.accum_in || p.accum_out || p.base);
+      shape[count] = {p.M, p.N, p.K, p.parts, p.b_halves != 0, cycles};
       which[count++] = i;
     }
   }
