@@ -92,10 +92,10 @@ __device__ __forceinline__ MmOutRow mm_out_row(const MmParams& p, int64_t row) {
   const bool second = p.M1 && row >= p.M1;
   return {second ? p.out2 : p.out, second ? p.out2_ld : p.out_ld, second ? row - p.M1 : row};
 }
-// of 32 rows from row0 on: those that are the result's
+// of a warp's rows from row0 on: those that are the result's
 __device__ __forceinline__ int mm_rows(const MmParams& p, int64_t row0) {
   const int64_t end = !p.M1 ? p.M : row0 >= p.M1 ? p.M1 + p.M2 : p.M2;
-  return (int)(end - row0 < 32 ? end - row0 : 32);
+  return (int)(end - row0 < p.warp_rows ? end - row0 : p.warp_rows);
 }
 
 // Two adjacent values of a row: at most `left` of them are the result's.  wide:

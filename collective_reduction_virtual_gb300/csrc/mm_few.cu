@@ -1,0 +1,299 @@
+// Products of a few fp32 rows, on the fp32 units.
+//
+// The tensor cores take fp32 operands as three bf16 parts, and laying a weight out
+// as parts reads 4 bytes a value and writes 6 that are then read six times.  Where
+// a weight meets a few rows only, reading it once bounds the product, and the
+// fp32 units keep up with that to 16 rows (two operations a row for 4 bytes: 54
+// TFLOP/s at 6.8 TB/s).  The small operand is in parts already, and is put
+// together again in shared memory; the weight is read where it lies.
+#include "mm_epilogue.cuh"
+
+namespace vcoll {
+
+namespace {
+
+constexpr int kThreads = kMmFewThreads, kWarps = kThreads / 32;
+constexpr int kChunk = 512;  // places of a sum whose small operand is in shared memory
+
+// Eight values of an operand in parts, from a multiple of 8 on; rows are as long.
+__device__ __forceinline__ void from_parts(const MmOperand& o, int64_t row, int64_t col, float (&v)[8]) {
+  const uint16_t* p = static_cast<const uint16_t*>(o.p) + row * o.ld + col;
+  float q[3][8];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) Elem<__nv_bfloat16>::widen(*reinterpret_cast<const uint4*>(p + k * o.plane), q[k]);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = q[0][j] + (q[1][j] + q[2][j]);
+}
+
+// Four values of a row, of which `count` from its first on are there: those from
+// `at` on, 16 bytes at once, or without WIDE every 32nd from there, so that a warp
+// reads 128 bytes in a row.  The others are zeros; the row's first value is read in
+// their place, since loads behind a condition would wait for each other.
+template <bool WIDE>
+__device__ __forceinline__ float4 load4(const float* row, int64_t at, int64_t count) {
+  float4 v;
+  if (WIDE) {
+    const bool in = at < count;
+    const uint4 q = ld_stream(in ? row + at : row);
+    v = make_float4(__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z), __uint_as_float(q.w));
+    if (!in) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  } else {
+    const bool x = at < count, y = at + 32 < count, z = at + 64 < count, w = at + 96 < count;
+    v.x = __ldg(x ? row + at : row);
+    v.y = __ldg(y ? row + at + 32 : row);
+    v.z = __ldg(z ? row + at + 64 : row);
+    v.w = __ldg(w ? row + at + 96 : row);
+    v.x = x ? v.x : 0.0f;
+    v.y = y ? v.y : 0.0f;
+    v.z = z ? v.z : 0.0f;
+    v.w = w ? v.w : 0.0f;
+  }
+  return v;
+}
+
+// The warp's sums of N values: those from lane * (N / 32) on, N / 32 of them, in the
+// lane's first.  In each step a lane gives half of what it has to the lane S away.
+template <int S, int LEFT, int N>
+__device__ __forceinline__ void scatter_sums(float (&v)[N], int lane) {
+  const bool upper = lane & S;
+#pragma unroll
+  for (int j = 0; j < LEFT / 2; ++j) {
+    const float give = upper ? v[j] : v[LEFT / 2 + j], keep = upper ? v[LEFT / 2 + j] : v[j];
+    v[j] = keep + __shfl_xor_sync(~0u, give, S);
+  }
+  if constexpr (S > 1) scatter_sums<S / 2, LEFT / 2>(v, lane);
+}
+
+// A row of a tile's sums in shared memory.
+struct FewSource {
+  const float* row;
+  __device__ __forceinline__ void operator()(int c, float (&v)[32]) const {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = row[c + j];
+  }
+  __device__ __forceinline__ void operator()(int c, int d, float (&v)[32]) const {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      v[j] = row[c + j];
+      v[16 + j] = row[d + j];
+    }
+  }
+};
+
+}  // namespace
+
+// Rows of the small operand a times rows of the weight b: a CTA for all of a,
+// ROWS at most, and 64 rows of b, eight a warp, whose lanes go along the sum.
+template <int EPI, int ROWS, bool WIDE>
+__global__ void __launch_bounds__(kThreads) vc_mm_few_rows(const __grid_constant__ MmLaunch all) {
+  pdl_enter();
+  const MmParams& p = all.p[0];
+  __shared__ __align__(16) float xs[ROWS][kChunk];
+  __shared__ float sums[32 * 65];
+  __shared__ float block[kMmBlockWords];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t tile_n = blockIdx.x;
+  const bool second = EPI == MM_GATED && warp >= kWarps / 2;  // gate's rows, then as many of up's
+  const MmOperand& b = p.b[second];
+  const int64_t first = EPI == MM_GATED ? tile_n * 32 + warp % (kWarps / 2) * 8 : tile_n * 64 + warp * 8;
+  const float* w[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r)  // rows past the end give columns that are not stored
+    w[r] = static_cast<const float*>(b.p) + (first + r < b.rows ? first + r : b.rows - 1) * b.ld;
+  float acc[8 * ROWS] = {};
+  constexpr int FIRST = WIDE ? 4 : 1, NEXT = WIDE ? 1 : 32;  // places between lanes, and between a lane's four
+  for (int64_t k0 = 0; k0 < p.K; k0 += kChunk) {
+    for (int e = threadIdx.x; e < ROWS * (kChunk / 8); e += kThreads) {
+      const int m = e / (kChunk / 8), k = e % (kChunk / 8) * 8;
+      float v[8] = {};
+      if (m < p.M && k0 + k < p.K) from_parts(p.a, m, k0 + k, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) xs[m][k + j] = k0 + k + j < p.K ? v[j] : 0.0f;
+    }
+    __syncthreads();
+    constexpr int STEPS = ROWS == 4 ? 2 : 1;  // loads in flight: as many as there are registers
+    for (int k = 0; k < kChunk && k0 + k < p.K; k += 128 * STEPS) {
+      float4 v[STEPS][8];
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+        for (int r = 0; r < 8; ++r) v[s][r] = load4<WIDE>(w[r], k0 + k + 128 * s + lane * FIRST, p.K);
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+        for (int m = 0; m < ROWS; ++m) {
+          const float* at = &xs[m][k + 128 * s + lane * FIRST];
+          const float4 x = WIDE ? *reinterpret_cast<const float4*>(at)
+                                : make_float4(at[0], at[NEXT], at[2 * NEXT], at[3 * NEXT]);
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const float4 y = v[s][r];
+            acc[r * ROWS + m] += (y.x * x.x + y.y * x.y) + (y.z * x.z + y.w * x.w);
+          }
+        }
+    }
+    __syncthreads();
+  }
+  scatter_sums<16, 8 * ROWS>(acc, lane);
+#pragma unroll
+  for (int j = 0; j < 8 * ROWS / 32; ++j) {
+    const int at = lane * (8 * ROWS / 32) + j;  // r * ROWS + m
+    sums[at % ROWS * 65 + warp * 8 + at / ROWS] = acc[j];
+  }
+  __syncthreads();
+  if (warp) return;
+  const FewSource src = {sums + lane * 65};
+  mm_epilogue<EPI>(p, 0, tile_n, 0, p.tn, lane, block, src);
+}
+
+// The small operand a times the weight b, which is taken transposed: a CTA for all
+// rows, ROWS at most, 128 columns, four a lane, and a split of the sum, which its warps share.
+template <int ROWS, bool WIDE>
+__global__ void __launch_bounds__(kThreads) vc_mm_few_cols(const __grid_constant__ MmLaunch all) {
+  pdl_enter();
+  const MmParams& p = all.p[0];
+  constexpr int CHUNK = 4096 / ROWS, FIRST = WIDE ? 4 : 1, NEXT = WIDE ? 1 : 32;
+  __shared__ float xs[CHUNK][ROWS];
+  __shared__ float sums[ROWS][128];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const uint32_t split = blockIdx.y;
+  const int64_t col = (int64_t)blockIdx.x * 128 + lane * FIRST;
+  const int64_t begin = p.K * split / p.splits & ~(int64_t)7;
+  const int64_t end = split + 1 == p.splits ? p.K : p.K * (split + 1) / p.splits & ~(int64_t)7;
+  const float *w0 = static_cast<const float*>(p.b[0].p), *w1 = static_cast<const float*>(p.b[1].p);
+  const int64_t rows0 = p.b[0].rows, rows1 = p.b[1].rows, ld0 = p.b[0].ld, ld1 = p.b[1].ld;
+  float acc[ROWS][4] = {};
+  for (int64_t k0 = begin; k0 < end; k0 += CHUNK) {
+    for (int e = threadIdx.x; e < ROWS * (CHUNK / 8); e += kThreads) {
+      const int m = e % ROWS, k = e / ROWS * 8;
+      float v[8] = {};
+      if (m < p.M && k0 + k < end) from_parts(p.a, m, k0 + k, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) xs[k + j][m] = k0 + k + j < end ? v[j] : 0.0f;
+    }
+    __syncthreads();
+    for (int k = warp * 8; k < CHUNK && k0 + k < end; k += kWarps * 8) {
+      float4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool second = k0 + k + i >= p.K1;
+        const int64_t r = second ? k0 + k + i - p.K1 : k0 + k + i, rows = second ? rows1 : rows0;
+        const bool in = r < rows && k0 + k + i < end;  // or it pads a's first half
+        const float* w = !in ? w0 : second ? w1 + r * ld1 : w0 + r * ld0;  // w1 may be absent
+        v[i] = load4<WIDE>(w, col, in ? p.N : 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int m = 0; m < ROWS; ++m) {
+          const float x = xs[k + i][m];
+          acc[m][0] += x * v[i].x;
+          acc[m][1] += x * v[i].y;
+          acc[m][2] += x * v[i].z;
+          acc[m][3] += x * v[i].w;
+        }
+    }
+    __syncthreads();
+  }
+  for (int q = 0; q < kWarps; ++q) {  // one warp after the other: a fixed order
+    if (warp == q) {
+#pragma unroll
+      for (int m = 0; m < ROWS; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float* at = &sums[m][lane * FIRST + j * NEXT];
+          *at = q ? *at + acc[m][j] : acc[m][j];
+        }
+    }
+    __syncthreads();
+  }
+  float* to = p.partial + ((int64_t)blockIdx.x * p.splits + split) * p.M * p.tn;
+  for (int e = threadIdx.x; e < p.M * 128; e += kThreads) to[e] = sums[0][e];
+}
+
+// The products of the columns of two small operands of a few rows: a CTA for
+// 64 x 128 of the result, which it writes (and adds to base): bound by that.
+__global__ void __launch_bounds__(kThreads) vc_mm_few_outer(const __grid_constant__ MmLaunch all) {
+  pdl_enter();
+  const MmParams& p = all.p[1];
+  __shared__ __align__(16) float es[kMmFewRows][64];
+  __shared__ __align__(16) float xs[kMmFewRows][128];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t tiles = (p.N + 127) / 128;
+  const int64_t row0 = blockIdx.x / tiles * 64, col0 = blockIdx.x % tiles * 128;
+  const int K = (int)p.K;
+  for (int e = threadIdx.x; e < K * 24; e += kThreads) {
+    const int k = e / 24, i = e % 24 * 8;  // 64 of es and 128 of xs; what is past their ends is not stored
+    float v[8] = {};
+    if (i < 64) {
+      if (row0 + i < p.a.cols) from_parts(p.a, k, row0 + i, v);
+    } else if (col0 + i - 64 < p.N) {
+      from_parts(p.b[0], k, col0 + i - 64, v);
+    }
+    float* to = i < 64 ? &es[k][i] : &xs[k][i - 64];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) to[j] = v[j];
+  }
+  __syncthreads();
+  float acc[8][4] = {};
+#pragma unroll 2
+  for (int k = 0; k < K; ++k) {
+    const float4 x = *reinterpret_cast<const float4*>(&xs[k][lane * 4]);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const float e = es[k][warp * 8 + r];
+      acc[r][0] += e * x.x;
+      acc[r][1] += e * x.y;
+      acc[r][2] += e * x.z;
+      acc[r][3] += e * x.w;
+    }
+  }
+  const float scale = p.scale ? *p.scale : 1.0f;
+  const int64_t col = col0 + lane * 4, left = p.N - col;
+  const MmOutRow to = mm_out_row(p, row0);
+  const int64_t end = p.M1 ? p.M2 : p.M;
+  const bool whole = all.wide && left >= 4;
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    const int64_t row = to.row + warp * 8 + r;
+    if (row >= end) break;
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = acc[r][j] * scale;
+    float* out = static_cast<float*>(to.out) + row * to.ld + col;
+    const float* base = static_cast<const float*>(p.base) + row * p.base_ld + col;
+    if (whole) {
+      if (p.base) {
+        const float4 x = *reinterpret_cast<const float4*>(base);
+        v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+      }
+      *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < left) out[j] = p.base ? base[j] + v[j] : v[j];
+    }
+  }
+}
+
+template <int ROWS, bool WIDE>
+static const void* rows_kernel(MmEpilogue epilogue) {
+  switch (epilogue) {
+    case MM_LSE:
+      return (const void*)vc_mm_few_rows<MM_LSE, ROWS, WIDE>;
+    case MM_ERROR:
+      return (const void*)vc_mm_few_rows<MM_ERROR, ROWS, WIDE>;
+    case MM_GATED:
+      return (const void*)vc_mm_few_rows<MM_GATED, ROWS, WIDE>;
+    default:
+      return (const void*)vc_mm_few_cols<ROWS, WIDE>;
+  }
+}
+const void* mm_few_kernel(MmEpilogue epilogue, int rows, bool wide) {
+  if (rows <= 4) return wide ? rows_kernel<4, true>(epilogue) : rows_kernel<4, false>(epilogue);
+  if (rows <= 8) return wide ? rows_kernel<8, true>(epilogue) : rows_kernel<8, false>(epilogue);
+  return wide ? rows_kernel<16, true>(epilogue) : rows_kernel<16, false>(epilogue);
+}
+const void* mm_few_outer_kernel() { return (const void*)vc_mm_few_outer; }
+
+}  // namespace vcoll

@@ -43,6 +43,7 @@ struct MmParams {
   int tn;         // columns of a tile
   uint32_t tiles_m, tiles_n;
   int tile_rows;      // 128, or 256 of a pair of CTAs
+  int warp_rows;      // that a warp's epilogue has at most: 32
   int a_rows;         // of a stage's a: 128, or fewer where M is smaller
   uint32_t chunk;       // steps that the tensor cores sum before the sum is added in registers
   uint32_t splits;      // that a tile's sum is cut into
@@ -89,6 +90,7 @@ struct MmLaunch {
   int stages, stage_bytes;
   uint32_t ahead;
   unsigned* error_word;
+  int wide;  // mm_few.cu: the result's matrices allow accesses of 16 bytes
 };
 
 // The six products of three parts that reach an fp32 result's precision, the
@@ -164,9 +166,15 @@ struct MmGatedGradParams {
   int load16;  // the rows of dh, gate and up start at 16-byte boundaries
 };
 
+// mm_few.cu: fp32 rows that it takes at most.
+constexpr int kMmFewRows = 16;
+constexpr int kMmFewThreads = 256;
+
 // ctas that share a tile: 1 or 2
 const void* mm_kernel(MmEpilogue epilogue, int ctas);
 const void* mm_join_splits_kernel(MmEpilogue epilogue);
+const void* mm_few_kernel(MmEpilogue epilogue, int rows, bool wide);  // MM_OUT: sums for the join
+const void* mm_few_outer_kernel();
 const void* mm_pack_kernel();
 const void* mm_join_kernel();
 const void* mm_gated_grad_kernel();

@@ -153,6 +153,19 @@ Plan make_plan(const Shape* shape, int count) {
 
 Plan plan_of(const Shape& a) { return make_plan(&a, 1); }
 
+// Whether the products are those of mm_few.cu, which read fp32 weights where they
+// lie.
+bool few_rows(int64_t N, int dtype) { return dtype == VCOLL_F32 && N <= kMmFewRows; }
+// Splits of the sum of a product with a weight that is taken transposed: two CTAs
+// per SM, of 256 places at least; the join adds them one after the other.
+int64_t few_splits(int64_t N, int64_t K) {
+  const int64_t fill = ceil_div(2 * kPlanSms, std::max<int64_t>(1, ceil_div(N, 128)));
+  return std::max<int64_t>(1, std::min<int64_t>({fill, K / 256, 64}));
+}
+size_t few_bytes(int64_t M, int64_t N, int64_t K) {
+  return (size_t)(ceil_div(N, 128) * few_splits(N, K) * M * 128) * sizeof(float);
+}
+
 // Columns of a piece of the vocabulary: `fit` at most, whole tiles.
 int64_t piece_of(int64_t V, int64_t fit) {
   return std::min(V, std::max<int64_t>(2048, fit / 256 * 256));
@@ -170,19 +183,24 @@ struct LossLayout {
 LossLayout loss_layout(int64_t N, int64_t V, int64_t D, int dtype, bool direct) {
   const int parts = parts_of(dtype);
   LossLayout L;
+  const bool few = few_rows(N, dtype);
   int64_t fit = kPartBytes / (8 * std::max<int64_t>(N, 1)) * 256;
-  if (!direct) fit = std::min(fit, kPackBytes / std::max<int64_t>(1, packed_bytes(1, D, parts)));
+  if (!direct && !few) fit = std::min(fit, kPackBytes / std::max<int64_t>(1, packed_bytes(1, D, parts)));
   L.piece = piece_of(V, fit);
   L.pieces = std::max<int64_t>(1, L.piece ? ceil_div(V, L.piece) : 1);
   Regions r;
   L.x = r.take(direct ? 0 : packed_bytes(N, D, parts));
-  L.table = r.take(direct ? 0 : packed_bytes(L.piece, D, parts));
+  L.table = r.take(direct || few ? 0 : packed_bytes(L.piece, D, parts));
   size_t splits = 0;
   int64_t tiles = 0;
-  for (int64_t w : piece_widths(V, L.piece)) {
-    const Plan plan = plan_of({N, w, D, parts, false, epilogue_cycles(1)});
-    splits = std::max(splits, plan.bytes());
-    tiles = std::max(tiles, ceil_div(w, plan.of[0].tn));
+  if (few) {
+    tiles = ceil_div(L.piece, 64);
+  } else {
+    for (int64_t w : piece_widths(V, L.piece)) {
+      const Plan plan = plan_of({N, w, D, parts, false, epilogue_cycles(1)});
+      splits = std::max(splits, plan.bytes());
+      tiles = std::max(tiles, ceil_div(w, plan.of[0].tn));
+    }
   }
   L.part = r.take(2 * tiles * N * (int64_t)sizeof(float2));
   L.splits = r.take((int64_t)splits);
@@ -198,25 +216,30 @@ struct LossGradLayout {
 LossGradLayout loss_grad_layout(int64_t N, int64_t V, int64_t D, int dtype, bool direct) {
   const int parts = parts_of(dtype);
   LossGradLayout L;
+  const bool few = few_rows(N, dtype);
   int64_t fit = kErrorBytes / (2 * parts * std::max<int64_t>(N, 1));
-  if (!direct) fit = std::min(fit, kPackBytes / std::max<int64_t>(1, packed_bytes(1, D, parts)));
+  if (!direct && !few) fit = std::min(fit, kPackBytes / std::max<int64_t>(1, packed_bytes(1, D, parts)));
   L.piece = piece_of(V, fit);
   L.pieces = std::max<int64_t>(1, L.piece ? ceil_div(V, L.piece) : 1);
   L.error_ld = round_up(L.piece, 64);  // rows of whole 128-byte lines
   Regions r;
   L.scale = r.take(sizeof(float));
   L.x = r.take(packed_bytes(N, D, parts));
-  L.table = r.take(direct ? 0 : packed_bytes(L.piece, D, parts));
+  L.table = r.take(direct || few ? 0 : packed_bytes(L.piece, D, parts));
   L.error = r.take(N * L.error_ld * 2 * parts);
   L.accum = r.take(L.pieces > 1 ? N * round_up(D, 2) * 4 : 0);
   size_t splits = 0;
-  for (int64_t w : piece_widths(V, L.piece)) {
-    const Shape error = {N, w, D, parts, false, epilogue_cycles(parts)};
-    splits = std::max(splits, plan_of(error).bytes());
-    for (const bool base : {false, true}) {  // dx, dtable, and both
-      const Shape s[2] = {{N, D, w, parts, false, epilogue_cycles(parts, L.pieces > 1)},
-                          {w, D, N, parts, false, epilogue_cycles(parts, base)}};
-      splits = std::max({splits, plan_of(s[0]).bytes(), plan_of(s[1]).bytes(), make_plan(s, 2).bytes()});
+  if (few) {
+    splits = few_bytes(N, D, L.piece);
+  } else {
+    for (int64_t w : piece_widths(V, L.piece)) {
+      const Shape error = {N, w, D, parts, false, epilogue_cycles(parts)};
+      splits = std::max(splits, plan_of(error).bytes());
+      for (const bool base : {false, true}) {  // dx, dtable, and both
+        const Shape s[2] = {{N, D, w, parts, false, epilogue_cycles(parts, L.pieces > 1)},
+                            {w, D, N, parts, false, epilogue_cycles(parts, base)}};
+        splits = std::max({splits, plan_of(s[0]).bytes(), plan_of(s[1]).bytes(), make_plan(s, 2).bytes()});
+      }
     }
   }
   L.splits = r.take((int64_t)splits);
@@ -234,12 +257,15 @@ GatedLayout gated_layout(int64_t N, int64_t D, int64_t F, int dtype, bool direct
   L.half = round_up(F, kMmRows);
   Regions r;
   L.x = r.take(direct ? 0 : packed_bytes(N, D, parts));
-  L.w_gate = r.take(direct ? 0 : packed_bytes(F, D, parts));
-  L.w_up = r.take(direct ? 0 : packed_bytes(F, D, parts));
+  const bool few = few_rows(N, dtype);
+  L.w_gate = r.take(direct || few ? 0 : packed_bytes(F, D, parts));
+  L.w_up = r.take(direct || few ? 0 : packed_bytes(F, D, parts));
   L.grads = r.take(backward ? packed_bytes(N, 2 * L.half, parts) : 0);
   size_t splits = 0;
   const int cycles = epilogue_cycles(parts);
-  if (backward) {  // dx; one weight's gradient; both
+  if (few) {
+    splits = backward ? few_bytes(N, D, 2 * L.half) : 0;
+  } else if (backward) {  // dx; one weight's gradient; both
     const Shape s[3] = {{N, D, 2 * L.half, parts, false, cycles},
                         {F, D, N, parts, false, cycles},
                         {2 * L.half, D, N, parts, false, cycles}};
@@ -403,6 +429,7 @@ int products(MmEpilogue epilogue, MmLaunch* all, void* partial, void* stream) {
     p->tiles_n = (uint32_t)tiles_n;
     p->units = (uint32_t)(tiles_m * tiles_n) * p->splits;
     units += p->units;
+    p->warp_rows = 32;
     p->depth = (uint32_t)ceil_div(p->K, kMmDepth);
     p->chunk = p->parts > 1 ? kMmChunkParts : epilogue == MM_LSE ? kMmChunkLoss : kMmChunkBf16;
     p->a_rows = a_mn || plan.ctas == 2 ? kMmRows : (int)std::min<int64_t>(kMmRows, round_up(p->M, 8));
@@ -432,6 +459,56 @@ int products(MmEpilogue epilogue, MmLaunch* all, void* partial, void* stream) {
                          all, stream));
   if (!join_blocks) return VCOLL_OK;
   return launch_grid(mm_join_splits_kernel(epilogue), join_blocks, 1, 256, 0, all, stream);
+}
+
+// Products of a few fp32 rows (mm_few.cu); b: fp32 where it lies.
+bool wide_rows(const void* p, int64_t rows, int64_t cols, int64_t ld) {
+  return cols % 4 == 0 && rows_at_16(p, rows, ld, 4);
+}
+
+int few_product(MmEpilogue epilogue, MmLaunch* all, void* partial, void* stream) {
+  MmParams* p = &all->p[0];
+  if (!p->M || !p->N) return VCOLL_OK;
+  const int rows = (int)p->M;
+  p->warp_rows = rows;
+  const bool second = p->b[1].p != nullptr;
+  const bool wide = wide_rows(p->b[0].p, p->b[0].rows, p->b[0].cols, p->b[0].ld) &&
+                    (!second || wide_rows(p->b[1].p, p->b[1].rows, p->b[1].cols, p->b[1].ld));
+  const void* fn = mm_few_kernel(epilogue, rows, wide);
+  if (epilogue != MM_OUT) {
+    p->tn = 64;
+    p->splits = 1;
+    p->tiles_n = (uint32_t)ceil_div(p->N, epilogue == MM_GATED ? 32 : 64);
+    return launch_grid(fn, p->tiles_n, 1, kMmFewThreads, 0, all, stream);
+  }
+  if (!second) p->K1 = p->K;
+  p->tn = 128;
+  p->splits = (uint32_t)few_splits(p->N, p->K);
+  p->partial = (float*)partial;
+  p->tile_rows = kMmRows;
+  p->tiles_m = 1;
+  p->tiles_n = (uint32_t)ceil_div(p->N, 128);
+  p->join_blocks = (uint32_t)ceil_div((int64_t)p->tiles_n * p->M * 4, 8);
+  VCOLL_TRY(launch_grid(fn, p->tiles_n, p->splits, kMmFewThreads, 0, all, stream));
+  return launch_grid(mm_join_splits_kernel(MM_OUT), p->join_blocks, 1, 256, 0, all, stream);
+}
+
+int few_outer(MmLaunch* all, void* stream) {
+  MmParams* p = &all->p[1];
+  const int64_t tiles = ceil_div(p->M, 64) * ceil_div(p->N, 128);
+  if (!tiles) return VCOLL_OK;
+  if (tiles > 0x7FFFFFFF) return fail(VCOLL_ERR_UNSUPPORTED, "%lld tiles are too many", (long long)tiles);
+  const int64_t rows = p->M1 ? p->M2 : p->M;
+  all->wide = wide_rows(p->out, rows, p->N, p->out_ld) && (!p->out2 || wide_rows(p->out2, rows, p->N, p->out2_ld)) &&
+              (!p->base || wide_rows(p->base, rows, p->N, p->base_ld));
+  return launch_grid(mm_few_outer_kernel(), tiles, 1, kMmFewThreads, 0, all, stream);
+}
+
+// The launch's products on the units that suit them.
+int run(MmEpilogue epilogue, bool few, MmLaunch* all, void* partial, void* stream) {
+  if (!few) return products(epilogue, all, partial, stream);
+  VCOLL_TRY(few_product(epilogue, all, partial, stream));
+  return few_outer(all, stream);
 }
 
 // Whether two adjacent columns of every row can be moved at once.
@@ -515,6 +592,7 @@ int vcoll_cross_entropy(const void* x, int64_t x_ld, const void* table, int64_t 
   const LossLayout L = loss_layout(N, V, D, dtype, x_direct && t_direct);
   VCOLL_TRY(check_room(ops, 5, workspace, workspace_bytes, L.bytes));
   char* ws = (char*)workspace;
+  const bool few = few_rows(N, dtype);
   MmLaunch all = {};
   MmParams& p = all.p[0];
   p.M = N;
@@ -539,11 +617,11 @@ int vcoll_cross_entropy(const void* x, int64_t x_ld, const void* table, int64_t 
     p.N = std::min(L.piece, V - p.token0);
     Packer pack(dtype);
     if (i == 0) VCOLL_TRY(pack.add(x, N, D, x_ld, x_direct, ws + L.x, false, &p.a));
-    VCOLL_TRY(pack.add((const char*)table + p.token0 * table_ld * es, p.N, D, table_ld, t_direct,
+    VCOLL_TRY(pack.add((const char*)table + p.token0 * table_ld * es, p.N, D, table_ld, t_direct || few,
                        ws + L.table, false, &p.b[0]));
     VCOLL_TRY(pack.run(stream));
-    VCOLL_TRY(products(MM_LSE, &all, ws + L.splits, stream));
-    j.tiles = (int64_t)p.tiles_n * (p.splits > 1 || p.tn < 128 ? 1 : 2);
+    VCOLL_TRY(run(MM_LSE, few, &all, ws + L.splits, stream));
+    j.tiles = (int64_t)p.tiles_n * (few || p.splits > 1 || p.tn < 128 ? 1 : 2);
     p.join_blocks = 0;
     all.stage_bytes = 0;
     j.first = i == 0;
@@ -587,6 +665,7 @@ int vcoll_cross_entropy_backward(const float* dloss, int64_t dloss_count, const 
   VCOLL_TRY(check_room(ops, 8, workspace, workspace_bytes, L.bytes));
   char* ws = (char*)workspace;
   const int parts = parts_of(dtype), idx64 = index_type == VCOLL_I64;
+  const bool few = few_rows(N, dtype);
   float* scale = (float*)(ws + L.scale);
   const int64_t dloss_step = dloss_count == 1 ? 0 : 1;
   MmOperand rows;  // x without the rows that do not count
@@ -604,7 +683,7 @@ int vcoll_cross_entropy_backward(const float* dloss, int64_t dloss_count, const 
       pack.p.N = N;
       VCOLL_TRY(pack.add(x, N, D, x_ld, false, ws + L.x, true, &rows));
     }
-    VCOLL_TRY(pack.add((const char*)table + v0 * table_ld * es, N ? width : 0, D, table_ld, direct, ws + L.table,
+    VCOLL_TRY(pack.add((const char*)table + v0 * table_ld * es, N ? width : 0, D, table_ld, direct || few, ws + L.table,
                        false, &tokens));
     VCOLL_TRY(pack.run(stream));
     const MmOperand error = operand(ws + L.error, N, width, L.error_ld, N * L.error_ld);
@@ -627,7 +706,7 @@ int vcoll_cross_entropy_backward(const float* dloss, int64_t dloss_count, const 
     p.error = ws + L.error;
     p.error_ld = L.error_ld;
     p.error_plane = N * L.error_ld;
-    VCOLL_TRY(products(MM_ERROR, &all, ws + L.splits, stream));
+    VCOLL_TRY(run(MM_ERROR, few, &all, ws + L.splits, stream));
     MmLaunch grads = {};  // of x and of the table
     if (dx) {
       MmParams& q = grads.p[0];
@@ -663,7 +742,7 @@ int vcoll_cross_entropy_backward(const float* dloss, int64_t dloss_count, const 
       q.base_ld = base_ld;
       if (base) q.out_pairs = q.out_pairs && in_pairs(q.base, V, base_ld, dtype);
     }
-    VCOLL_TRY(products(MM_OUT, &grads, ws + L.splits, stream));
+    VCOLL_TRY(run(MM_OUT, few, &grads, ws + L.splits, stream));
   }
   return VCOLL_OK;
 }
@@ -698,8 +777,9 @@ int vcoll_gated_ff(const void* x, int64_t x_ld, const void* w_gate, int64_t w_ga
   MmParams& p = all.p[0];
   Packer pack(dtype);
   VCOLL_TRY(pack.add(x, N, D, x_ld, x_direct, ws + L.x, false, &p.a));
-  VCOLL_TRY(pack.add(w_gate, F, D, w_gate_ld, g_direct, ws + L.w_gate, false, &p.b[0]));
-  VCOLL_TRY(pack.add(w_up, F, D, w_up_ld, u_direct, ws + L.w_up, false, &p.b[1]));
+  const bool few = few_rows(N, dtype);
+  VCOLL_TRY(pack.add(w_gate, F, D, w_gate_ld, g_direct || few, ws + L.w_gate, false, &p.b[0]));
+  VCOLL_TRY(pack.add(w_up, F, D, w_up_ld, u_direct || few, ws + L.w_up, false, &p.b[1]));
   VCOLL_TRY(pack.run(stream));
   p.M = N;
   p.N = F;
@@ -716,7 +796,7 @@ int vcoll_gated_ff(const void* x, int64_t x_ld, const void* w_gate, int64_t w_ga
   p.act = activation;
   p.out_pairs = in_pairs(h, N, h_ld, dtype) && (!gate || in_pairs(gate, N, gate_ld, dtype)) &&
                 (!up || in_pairs(up, N, up_ld, dtype));
-  return products(MM_GATED, &all, ws + L.splits, stream);
+  return run(MM_GATED, few, &all, ws + L.splits, stream);
 }
 
 size_t vcoll_gated_ff_backward_workspace_bytes(int64_t N, int64_t D, int64_t F, int dtype,
@@ -774,12 +854,13 @@ int vcoll_gated_ff_backward(const void* dh, int64_t dh_ld, const void* x, int64_
     VCOLL_TRY(launch_grid(mm_gated_grad_kernel(), pass_blocks(N * (L.half / 8)), 1, kPassThreads, 0, &g, stream));
   }
   const MmOperand grads = operand(ws + L.grads, N, 2 * L.half, 2 * L.half, N * 2 * L.half);
+  const bool few = few_rows(N, dtype);
   MmOperand rows, gates, ups;
   Packer pack(dtype);
   if (weights) VCOLL_TRY(pack.add(x, F ? N : 0, D, x_ld, x_direct, ws + L.x, false, &rows));
   if (dx) {
-    VCOLL_TRY(pack.add(w_gate, N ? F : 0, D, w_gate_ld, g_direct, ws + L.w_gate, false, &gates));
-    VCOLL_TRY(pack.add(w_up, N ? F : 0, D, w_up_ld, u_direct, ws + L.w_up, false, &ups));
+    VCOLL_TRY(pack.add(w_gate, N ? F : 0, D, w_gate_ld, g_direct || few, ws + L.w_gate, false, &gates));
+    VCOLL_TRY(pack.add(w_up, N ? F : 0, D, w_up_ld, u_direct || few, ws + L.w_up, false, &ups));
   }
   VCOLL_TRY(pack.run(stream));
   MmLaunch all = {};  // dx and the weights' gradients
@@ -823,7 +904,7 @@ int vcoll_gated_ff_backward(const void* dh, int64_t dh_ld, const void* x, int64_
       p.out_pairs = p.out_pairs && in_pairs(dw_up, F, dw_up_ld, dtype);
     }
   }
-  return products(MM_OUT, &all, ws + L.splits, stream);
+  return run(MM_OUT, few, &all, ws + L.splits, stream);
 }
 
 }  // extern "C"
