@@ -98,23 +98,27 @@ __device__ __forceinline__ int mm_rows(const MmParams& p, int64_t row0) {
   return (int)(end - row0 < p.warp_rows ? end - row0 : p.warp_rows);
 }
 
-// Two adjacent values of a row: at most `left` of them are the result's.  wide:
-// they can be moved at once.
-__device__ __forceinline__ void mm_store2(void* p, int f32, int wide, int64_t i, int64_t left, float x, float y) {
-  if (wide && left > 1) {
-    if (f32)
-      *reinterpret_cast<float2*>(static_cast<float*>(p) + i) = make_float2(x, y);
-    else
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p) + i) = mm_narrow2(x, y);
-  } else {
-    if (left > 0) mm_store(p, f32, i, x);
-    if (left > 1) mm_store(p, f32, i + 1, y);
+// A warp's block of 32 rows and 32 columns of the result, as its lanes take it: two
+// adjacent columns in every second row where two can be moved at once (WIDE), else a
+// column of every row, so that a warp's access is one piece of two rows or of one.
+template <bool WIDE>
+struct MmBlock {
+  int rows;       // of the result in it
+  int64_t col;    // this lane's first column
+  int64_t left;   // columns from there on that are the result's
+  int row, at;    // this lane's first row, and its place in the block
+  static constexpr int STEP = WIDE ? 2 : 1, COUNT = WIDE ? 16 : 32;
+
+  __device__ __forceinline__ MmBlock(int rows_, int64_t col0, int64_t cols, int lane) : rows(rows_) {
+    const int c = WIDE ? (lane & 15) * 2 : lane;
+    row = WIDE ? lane >> 4 : 0;
+    at = row * kMmPitch + c;
+    col = col0 + c;
+    left = cols - col;
   }
-}
-// x = (in + first * x) * then, for a block of 32 columns of which a lane has two in
-// every second row.  in may be NULL.  The loads of eight rows are issued at once,
-// from places within the matrix whatever the row and column: a load waits longer
-// than all else takes.
+};
+
+// x = (in + first * x) * then.  in may be NULL.
 struct MmAdd {
   const void* in;
   int64_t in_at, in_ld;
@@ -122,52 +126,75 @@ struct MmAdd {
   int64_t out_at, out_ld;
   float first, then;
 };
+// What is added to a block.  All loads are issued at once, from places within the
+// matrix whatever the row and column, and without a condition between them, which
+// they would wait for: a load waits longer than all else takes.
 template <bool IN32, bool WIDE>
-__device__ __forceinline__ void mm_add_load(const MmAdd& h, float2 (&x)[16], int rows, int pair, int odd, int64_t col,
-                                            int64_t left) {
-  // left + pair, the same for all lanes: columns from the block's first on.  No
-  // condition stands between the loads, which would wait for each other.
-  if (!h.in || rows <= 0 || left + pair <= 0) {
+__device__ __forceinline__ void mm_add_load(const MmAdd& h, const MmBlock<WIDE>& b, float (&x)[32]) {
+  using Block = MmBlock<WIDE>;
+  if (!h.in || b.rows <= 0 || !__any_sync(~0u, b.left > 0)) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = make_float2(0.0f, 0.0f);
-  } else if (WIDE && left + pair >= 32) {
+    for (int i = 0; i < 32; ++i) x[i] = 0.0f;
+    return;
+  }
+  const int64_t col = b.left > 0 ? b.col : b.col + b.left - Block::STEP;  // the last there are
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int64_t at = h.in_at + (2 * i + odd < rows ? 2 * i + odd : rows - 1) * h.in_ld + col;
-      if (IN32)
-        x[i] = *reinterpret_cast<const float2*>(static_cast<const float*>(h.in) + at);
-      else
-        x[i].x = __uint_as_float(*reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(h.in) + at));
+  for (int i = 0; i < Block::COUNT; ++i) {
+    const int r = b.row + i * Block::STEP < b.rows ? b.row + i * Block::STEP : b.rows - 1;
+    const int64_t at = h.in_at + r * h.in_ld + col;
+    if (WIDE && IN32) {
+      const float2 v = *reinterpret_cast<const float2*>(static_cast<const float*>(h.in) + at);
+      x[2 * i] = v.x;
+      x[2 * i + 1] = v.y;
+    } else if (WIDE) {
+      x[2 * i] = __uint_as_float(*reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(h.in) + at));
+    } else if (IN32) {
+      x[i] = static_cast<const float*>(h.in)[at];
+    } else {
+      x[i] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(h.in)[at] << 16);
     }
-    if (!IN32) {
+  }
+  if (WIDE && !IN32) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) Elem<__nv_bfloat16>::widen2(__float_as_uint(x[i].x), x[i].x, x[i].y);
-    }
-  } else {
-    const int64_t c0 = left > 0 ? col : col + left - 1, c1 = left > 1 ? c0 + 1 : c0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int64_t at = h.in_at + (2 * i + odd < rows ? 2 * i + odd : rows - 1) * h.in_ld;
-      if (IN32) {
-        x[i].x = static_cast<const float*>(h.in)[at + c0];
-        x[i].y = static_cast<const float*>(h.in)[at + c1];
-      } else {
-        x[i].x = __uint_as_float((uint32_t)static_cast<const uint16_t*>(h.in)[at + c0] << 16);
-        x[i].y = __uint_as_float((uint32_t)static_cast<const uint16_t*>(h.in)[at + c1] << 16);
-      }
-    }
+    for (int i = 0; i < Block::COUNT; ++i)
+      Elem<__nv_bfloat16>::widen2(__float_as_uint(x[2 * i]), x[2 * i], x[2 * i + 1]);
   }
 }
 template <bool OUT32, bool WIDE>
-__device__ __forceinline__ void mm_add_store(const MmAdd& h, const float2 (&x)[16], const float* block, int rows,
-                                             int pair, int odd, int64_t col, int64_t left) {
+__device__ __forceinline__ void mm_add_store(const MmAdd& h, const MmBlock<WIDE>& b, const float (&x)[32],
+                                             const float* block) {
+  using Block = MmBlock<WIDE>;
+  if (b.left <= 0) return;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int r = 2 * i + odd;
-    if (r >= rows) break;
-    const float y0 = (x[i].x + h.first * block[r * kMmPitch + pair]) * h.then,
-                y1 = (x[i].y + h.first * block[r * kMmPitch + pair + 1]) * h.then;
-    mm_store2(h.out, OUT32, WIDE, h.out_at + r * h.out_ld + col, left, y0, y1);
+  for (int i = 0; i < Block::COUNT; ++i) {
+    const int r = i * Block::STEP;
+    if (b.row + r >= b.rows) break;
+    const float* from = block + b.at + r * kMmPitch;
+    const int64_t at = h.out_at + (b.row + r) * h.out_ld + b.col;
+    if (WIDE) {
+      const float y = (x[2 * i] + h.first * from[0]) * h.then, z = (x[2 * i + 1] + h.first * from[1]) * h.then;
+      if (OUT32)
+        *reinterpret_cast<float2*>(static_cast<float*>(h.out) + at) = make_float2(y, z);
+      else
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(h.out) + at) = mm_narrow2(y, z);
+    } else {
+      mm_store(h.out, OUT32, at, (x[i] + h.first * from[0]) * h.then);
+    }
+  }
+}
+// A block of fp32, or of bf16 whose rows do not allow 4-byte accesses.
+template <bool WIDE>
+__device__ __forceinline__ void mm_store_block(const MmBlock<WIDE>& b, const float* block, float scale, void* out, int f32,
+                                               int64_t at, int64_t ld) {
+  if (b.left <= 0) return;
+#pragma unroll 4
+  for (int r = b.row; r < b.rows; r += MmBlock<WIDE>::STEP) {
+    const float* from = block + b.at + (r - b.row) * kMmPitch;
+    const int64_t to = at + r * ld + b.col;
+    if (WIDE)
+      *reinterpret_cast<float2*>(static_cast<float*>(out) + to) = make_float2(from[0] * scale, from[1] * scale);
+    else
+      mm_store(out, f32, to, from[0] * scale);
   }
 }
 
@@ -190,6 +217,20 @@ __device__ __forceinline__ void mm_to_block(float* block, int lane, const float 
 #pragma unroll
   for (int j = 0; j < 32; ++j) block[lane * kMmPitch + j] = v[j];
   __syncwarp();
+}
+
+template <bool IN32, bool OUT32, bool WIDE, class Source>
+__device__ __forceinline__ void mm_add_blocks(const MmAdd& h, int rows, int64_t col0, int64_t cols, int c0, int c1,
+                                              int lane, float* block, Source src) {
+  for (int c = c0; c < c1; c += 32) {
+    const MmBlock<WIDE> b(rows, col0 + c, cols, lane);
+    float x[32];
+    src(c, x);
+    mm_to_block(block, lane, x);
+    mm_add_load<IN32>(h, b, x);
+    mm_add_store<OUT32>(h, b, x, block);
+    __syncwarp();
+  }
 }
 
 // 64 columns as bf16, two to a word: a warp's stores are 128 adjacent bytes of a
@@ -223,18 +264,43 @@ __device__ __forceinline__ void mm_gate(float (&g)[32], const float (&u)[32]) {
   }
 }
 
+// What a lane's row brings besides its sums, loaded before they are waited for.
+struct MmRow {
+  float scale;  // MM_OUT
+  int64_t hit;  // the tile's column of the row's target, or one that it has not
+  float lse, w;  // of a masked row, whose logits are zeros: 0
+};
+template <int EPI>
+__device__ __forceinline__ MmRow mm_row(const MmParams& p, int64_t row0, int64_t tile_n, int lane) {
+  MmRow r = {1.0f, -1, 0.0f, 0.0f};
+  if constexpr (EPI == MM_OUT) {
+    if (p.scale) r.scale = *p.scale;
+  } else if constexpr (EPI == MM_LSE || EPI == MM_ERROR) {
+    if (lane < mm_rows(p, row0)) {
+      const int64_t t = mm_token(p.targets, p.idx64, row0 + lane);
+      const bool inside = t >= 0 && t < p.V;
+      if (inside) r.hit = t - p.token0 - tile_n * p.tn;
+      if (EPI == MM_ERROR) {
+        const float lse = p.lse[row0 + lane], w = p.dloss[(row0 + lane) * p.dloss_step] / *p.scale;
+        r.lse = inside ? lse : 0.0f;
+        r.w = inside ? w : 0.0f;
+      }
+    }
+  }
+  return r;
+}
+
 // src(c, v): columns c .. c + 31 of this lane's row of the tile, called by the
 // whole warp; columns c0 .. c1 - 1 are this warp's.  row0: its first row of the
-// result.  In the block a lane takes two adjacent columns of every second row.
+// result.
 template <int EPI, class Source>
 __device__ __forceinline__ void mm_epilogue(const MmParams& p, int64_t row0, int64_t tile_n, int c0, int c1,
-                                            int lane, float* block, Source src) {
+                                            const MmRow& mine, int lane, float* block, Source src) {
   const int64_t row = row0 + lane;
   const int rows = mm_rows(p, row0);  // < 1: only src is called
-  const int pair = (lane & 15) * 2, odd = lane >> 4;
   float v[32];
   if constexpr (EPI == MM_OUT) {
-    const float scale = p.scale ? *p.scale : 1.0f;
+    const float scale = mine.scale;
     const MmOutRow to = mm_out_row(p, row0);
     const bool add = p.accum_in || p.accum_out || p.base;
     if (!add && !p.out_f32 && p.out_pairs) {
@@ -259,47 +325,34 @@ __device__ __forceinline__ void mm_epilogue(const MmParams& p, int64_t row0, int
                          p.accum_out ? row0 * p.accum_ld : to.row * to.ld, p.accum_out ? p.accum_ld : to.ld,
                          p.base ? scale : 1.0f, p.base || p.accum_out ? 1.0f : scale};
       const bool out32 = p.accum_out || p.out_f32, in32 = p.accum_in || out32;
-      const bool in_wide = p.accum_in || p.out_pairs, out_wide = p.accum_out || p.out_pairs;
-      for (int c = c0; c < c1; c += 32) {
-        const int64_t col = tile_n * p.tn + c + pair, left = p.N - col;
-        float2 x[16];
-        if (in32 && in_wide)
-          mm_add_load<true, true>(how, x, rows, pair, odd, col, left);
-        else if (in32)
-          mm_add_load<true, false>(how, x, rows, pair, odd, col, left);
-        else if (in_wide)
-          mm_add_load<false, true>(how, x, rows, pair, odd, col, left);
-        else
-          mm_add_load<false, false>(how, x, rows, pair, odd, col, left);
-        src(c, v);
-        mm_to_block(block, lane, v);
-        if (out32 && out_wide)
-          mm_add_store<true, true>(how, x, block, rows, pair, odd, col, left);
-        else if (out32)
-          mm_add_store<true, false>(how, x, block, rows, pair, odd, col, left);
-        else if (out_wide)
-          mm_add_store<false, true>(how, x, block, rows, pair, odd, col, left);
-        else
-          mm_add_store<false, false>(how, x, block, rows, pair, odd, col, left);
-        __syncwarp();
-      }
+      // pairs of columns do not reach past the last one
+      const bool wide = p.N % 2 == 0 && (p.accum_in || !p.base || p.out_pairs) && (p.accum_out || p.out_pairs);
+      const int64_t col0 = tile_n * p.tn;
+      if (in32 && out32 && wide)
+        mm_add_blocks<true, true, true>(how, rows, col0, p.N, c0, c1, lane, block, src);
+      else if (in32 && out32)
+        mm_add_blocks<true, true, false>(how, rows, col0, p.N, c0, c1, lane, block, src);
+      else if (in32)
+        mm_add_blocks<true, false, false>(how, rows, col0, p.N, c0, c1, lane, block, src);
+      else if (wide)
+        mm_add_blocks<false, false, true>(how, rows, col0, p.N, c0, c1, lane, block, src);
+      else
+        mm_add_blocks<false, false, false>(how, rows, col0, p.N, c0, c1, lane, block, src);
       return;
     }
     for (int c = c0; c < c1; c += 32) {
-      const int64_t col = tile_n * p.tn + c + pair, left = p.N - col;
       src(c, v);
       mm_to_block(block, lane, v);
-#pragma unroll 4
-      for (int r = odd; r < rows; r += 2)
-        mm_store2(to.out, p.out_f32, p.out_pairs, (to.row + r) * to.ld + col, left,
-                  block[r * kMmPitch + pair] * scale, block[r * kMmPitch + pair + 1] * scale);
+      if (p.out_f32 && p.out_pairs && p.N % 2 == 0)
+        mm_store_block(MmBlock<true>(rows, tile_n * p.tn + c, p.N, lane), block, scale, to.out, 1, to.row * to.ld, to.ld);
+      else
+        mm_store_block(MmBlock<false>(rows, tile_n * p.tn + c, p.N, lane), block, scale, to.out, p.out_f32,
+                       to.row * to.ld, to.ld);
       __syncwarp();
     }
   } else if constexpr (EPI == MM_LSE) {
     // exponentials to base 2 of z log2(e), relative to a row's largest so far
-    int64_t t = -1;
-    if (lane < rows) t = mm_token(p.targets, p.idx64, row);
-    const int64_t hit = t >= 0 && t < p.V ? t - p.token0 - tile_n * p.tn : -1;
+    const int64_t hit = mine.hit;
     float m = -INFINITY, s = 0.0f;
     for (int c = c0; c < c1; c += 32) {
       src(c, v);
@@ -330,16 +383,8 @@ __device__ __forceinline__ void mm_epilogue(const MmParams& p, int64_t row0, int
     }
     if (lane < rows && c0 < c1) p.part[(tile_n * (p.tn / (c1 - c0)) + (c0 ? 1 : 0)) * p.M + row] = make_float2(m, s);
   } else if constexpr (EPI == MM_ERROR) {
-    int64_t hit = -1;
-    float lse = 0.0f, w = 0.0f;  // of a masked row, whose logits are zeros
-    if (lane < rows) {
-      const int64_t t = mm_token(p.targets, p.idx64, row);
-      if (t >= 0 && t < p.V) {
-        hit = t - p.token0 - tile_n * p.tn;
-        lse = p.lse[row];
-        w = p.dloss[row * p.dloss_step] / *p.scale;
-      }
-    }
+    const int64_t hit = mine.hit;
+    const float lse = mine.lse, w = mine.w;
     float x[32];
     for (int c = c0; c < c1; c += 64) {
       const int64_t col = tile_n * p.tn + c;
@@ -400,23 +445,23 @@ __device__ __forceinline__ void mm_epilogue(const MmParams& p, int64_t row0, int
     }
   } else {
     // (the exact gelu's code is too long to be repeated for 64 columns)
-    // 16 columns of gate and the same of up beside each other; a lane takes two
-    // of them in every fourth row
-    const int half = p.tn / 2, two = (lane & 7) * 2, quarter = lane >> 3;
+    // 16 columns of gate and the same of up beside each other; a lane takes one of
+    // them in every second row
+    const int half = p.tn / 2, at = lane & 15;
     for (int c = c0 / 2; c < c1 / 2; c += 16) {
-      const int64_t col = tile_n * half + c + two, left = p.N - col;
+      const int64_t col = tile_n * half + c + at;
       src(c, half + c, v);
       mm_to_block(block, lane, v);
-#pragma unroll 2
-      for (int r = quarter; r < rows; r += 4) {
-        const float* at = block + r * kMmPitch + two;
-        const float g0 = at[0], g1 = at[1], u0 = at[16], u1 = at[17];
-        float s0, s1, ds;
-        mm_act(p.act, g0, s0, ds);
-        mm_act(p.act, g1, s1, ds);
-        if (p.gate) mm_store2(p.gate, p.out_f32, p.out_pairs, (row0 + r) * p.gate_ld + col, left, g0, g1);
-        if (p.up) mm_store2(p.up, p.out_f32, p.out_pairs, (row0 + r) * p.up_ld + col, left, u0, u1);
-        mm_store2(p.out, p.out_f32, p.out_pairs, (row0 + r) * p.out_ld + col, left, g0 * (s0 * u0), g1 * (s1 * u1));
+      if (col < p.N) {
+#pragma unroll 4
+        for (int r = lane >> 4; r < rows; r += 2) {
+          const float g = block[r * kMmPitch + at], u = block[r * kMmPitch + at + 16];
+          float s, ds;
+          mm_act(p.act, g, s, ds);
+          if (p.gate) mm_store(p.gate, p.out_f32, (row0 + r) * p.gate_ld + col, g);
+          if (p.up) mm_store(p.up, p.out_f32, (row0 + r) * p.up_ld + col, u);
+          mm_store(p.out, p.out_f32, (row0 + r) * p.out_ld + col, g * (s * u));
+        }
       }
       __syncwarp();
     }

@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) vc_mm_few_rows(const __grid_constant
   __syncthreads();
   if (warp) return;
   const FewSource src = {sums + lane * 65};
-  mm_epilogue<EPI>(p, 0, tile_n, 0, p.tn, lane, block, src);
+  mm_epilogue<EPI>(p, 0, tile_n, 0, p.tn, mm_row<EPI>(p, 0, tile_n, lane), lane, block, src);
 }
 
 // The small operand a times the weight b, which is taken transposed: a CTA for all

@@ -111,6 +111,7 @@ constexpr int kMmRows = 128;
 // What is rounded to bf16 in the end drifts by less than that rounding's 1 % in
 // 32768 places.
 constexpr uint32_t kMmChunkLoss = 16, kMmChunkParts = 8, kMmChunkBf16 = 512;
+constexpr uint32_t kMmChunkMost = 1 << 16;  // some 20 ms, far below what a wait may take
 constexpr int kMmTileN = 256;
 constexpr int kMmDepth = 64;
 constexpr int kMmStageRoom = 192 * 1024;
@@ -162,7 +163,7 @@ struct MmGatedGradParams {
   void* dst;
   int64_t N, F, dh_ld, gate_ld, up_ld;
   int64_t dst_ld, half, plane;  // gate's at 0, up's at half
-  int f32, parts, act;
+  int f32, parts;
   int load16;  // the rows of dh, gate and up start at 16-byte boundaries
 };
 
@@ -177,7 +178,7 @@ const void* mm_few_kernel(MmEpilogue epilogue, int rows, bool wide);  // MM_OUT:
 const void* mm_few_outer_kernel();
 const void* mm_pack_kernel();
 const void* mm_join_kernel();
-const void* mm_gated_grad_kernel();
+const void* mm_gated_grad_kernel(int act);
 
 // Launch of clusters of `cluster` CTAs, one CTA per SM, that take nearly all of
 // its shared memory.

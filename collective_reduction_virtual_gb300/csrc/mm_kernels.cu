@@ -74,7 +74,8 @@ __device__ __forceinline__ uint32_t steps_of(const MmParams& p, uint32_t unit, u
 // Steps of a unit's first chunk: the small ones of the parts' products together.
 __device__ __forceinline__ uint32_t first_chunk(const MmParams& p, uint32_t split) {
   if (p.parts == 1) return p.chunk;
-  return ((mm_pairs(p.parts) - 1) * p.depth - split + p.splits - 1) / p.splits;
+  const uint32_t small = ((mm_pairs(p.parts) - 1) * p.depth - split + p.splits - 1) / p.splits;
+  return small < kMmChunkMost ? small : kMmChunkMost;
 }
 
 // Where a CTA's parts lie in shared memory, and its place in a pair.
@@ -277,6 +278,7 @@ __device__ __forceinline__ bool finish_unit(const MmParams& p, uint32_t unit, co
   const int64_t row0 = mine.row0;
   const uint32_t split = mine.split, tn = mine.tn, lanes = at.tmem + ((uint32_t)(warp % 4 * 32) << 16);
   uint32_t left = mine.steps;
+  const MmRow row = mm_row<EPI>(p, row0, tn, lane);
   uint32_t chunk = first_chunk(p, split);
   if (left > chunk) {
     ChunkSum s = {};
@@ -299,7 +301,7 @@ __device__ __forceinline__ bool finish_unit(const MmParams& p, uint32_t unit, co
   }
   const TmemSource src = {lanes + (turn & 1) * kMmTileN, p.depth != 0};
   if (p.splits == 1) {
-    mm_epilogue<EPI>(p, row0, tn, c0, c1, lane, block, src);
+    mm_epilogue<EPI>(p, row0, tn, c0, c1, row, lane, block, src);
     mm_fence_before();
     __syncwarp();
     release<CTAS>(at, turn++);

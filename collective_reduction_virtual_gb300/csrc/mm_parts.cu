@@ -145,10 +145,12 @@ __global__ void __launch_bounds__(kMmJoinThreads) vc_mm_join(const __grid_consta
 #pragma unroll 4
     for (int64_t t = warp; t < p.tiles; t += WARPS) add(p.part[t * p.N + row]);
   }
-  part[threadIdx.x] = make_float2(m, s);
-  __syncthreads();
+  for (int half = WARPS / 2; half; half /= 2) {
+    if (warp >= half && warp < 2 * half) part[threadIdx.x] = make_float2(m, s);
+    __syncthreads();
+    if (warp < half) add(part[threadIdx.x + half * 32]);
+  }
   if (warp || row >= p.N) return;
-  for (int w = 1; w < WARPS; ++w) add(part[w * 32 + lane]);
   if (!p.last) {
     p.state[row] = make_float2(m, s);
     return;
@@ -160,6 +162,7 @@ __global__ void __launch_bounds__(kMmJoinThreads) vc_mm_join(const __grid_consta
 }
 
 // dgate = dh * up * act'(gate), dup = dh * act(gate).
+template <int ACT>
 __global__ void __launch_bounds__(kThreads) vc_mm_gated_grad(const __grid_constant__ MmGatedGradParams p) {
   pdl_enter();
   const int64_t groups = p.half / 8;
@@ -175,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) vc_mm_gated_grad(const __grid_consta
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       float s, ds;
-      mm_act(p.act, g[j], s, ds);
+      mm_act(ACT, g[j], s, ds);
       u[j] = dh[j] * u[j] * (s + g[j] * ds);
       dh[j] = dh[j] * (g[j] * s);
     }
@@ -186,6 +189,10 @@ __global__ void __launch_bounds__(kThreads) vc_mm_gated_grad(const __grid_consta
 
 const void* mm_pack_kernel() { return (const void*)vc_mm_pack; }
 const void* mm_join_kernel() { return (const void*)vc_mm_join; }
-const void* mm_gated_grad_kernel() { return (const void*)vc_mm_gated_grad; }
+const void* mm_gated_grad_kernel(int act) {
+  return act == VCOLL_SILU   ? (const void*)vc_mm_gated_grad<VCOLL_SILU>
+         : act == VCOLL_GELU ? (const void*)vc_mm_gated_grad<VCOLL_GELU>
+                             : (const void*)vc_mm_gated_grad<VCOLL_GELU_TANH>;
+}
 
 }  // namespace vcoll

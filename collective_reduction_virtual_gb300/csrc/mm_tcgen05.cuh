@@ -86,8 +86,9 @@ __device__ __forceinline__ uint32_t mm_of_first(uint32_t bar) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(bar));
   return at;
 }
+// Relaxed: a release would wait for the stores to global memory before it.
 __device__ __forceinline__ void mm_bar_arrive_at(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 __device__ __forceinline__ uint32_t mm_rank() {
   uint32_t r;

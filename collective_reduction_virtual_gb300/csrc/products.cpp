@@ -64,10 +64,19 @@ struct Plan {
   size_t bytes() const { return align256(of[0].bytes) + align256(of[1].bytes); }
 };
 
-// The cheapest by a model of cycles.  A step of 64 places takes the tensor cores 2
-// tn, or as long as the step's operands take to arrive, at 45 bytes a cycle and SM
-// from memory where one row of tiles takes each column once, 3600 for all SMs, and
-// at 80 from L2 where rows of tiles share them.  A tile's epilogue goes beside the next tile's sum, but
+// Cycles of a step of 64 places: a pair of CTAs sums 256 columns at the tensor
+// cores' rate, fewer or one CTA's less well (4096 x 16384 x 2048, bf16: 1930 TFLOP/s
+// with 256 columns and 1780 with 128, and 1750, 1520 and 860 by one CTA with 256, 128
+// and 64).
+double step_cycles(int ctas, int tn) {
+  if (ctas == 2) return tn == 256 ? 512 : 280;
+  return tn == 256 ? 565 : tn == 128 ? 325 : 290;
+}
+
+// The cheapest by a model of cycles.  A step takes the tensor cores' time, or as long
+// as its operands take to arrive, at 45 bytes a cycle and SM from memory where one
+// row of tiles takes each column once, 3600 for all SMs, and at 80 from L2 where rows
+// of tiles share them.  A tile's epilogue goes beside the next tile's sum, but
 // for the last one's.  Alone, a product takes whole waves of units; two fill each
 // other's last waves to within a unit.
 Plan search_plan(const Shape* shape, int count) {
@@ -93,7 +102,7 @@ Plan search_plan(const Shape* shape, int count) {
         for (int k : {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16}) {
           if (k > 1 && (steps / k < 4 || tiles * k > 8 * kPlanSms)) break;
           const double units = tiles * k, rate = tiles_m > 1 ? 80 : std::min(45.0, 3600 / std::min(units, slots));
-          const double step = std::max(2.0 * tn, bytes / rate);
+          const double step = std::max(step_cycles(ctas, tn), bytes / rate);
           Choice& c = choice[i][choices[i]++];
           const double tail = (double)s.epilogue * tn + 1000;
           c = {tn, k, units, std::max((double)ceil_div(steps, k) * step, k > 1 ? 12.0 * tn : tail) + 200, 0.0, tail, 0};
@@ -160,7 +169,7 @@ bool few_rows(int64_t N, int dtype) { return dtype == VCOLL_F32 && N <= kMmFewRo
 // per SM, of 256 places at least; the join adds them one after the other.
 int64_t few_splits(int64_t N, int64_t K) {
   const int64_t fill = ceil_div(2 * kPlanSms, std::max<int64_t>(1, ceil_div(N, 128)));
-  return std::max<int64_t>(1, std::min<int64_t>({fill, K / 256, 64}));
+  return std::max<int64_t>(1, std::min<int64_t>({fill, K / 256, 128}));
 }
 size_t few_bytes(int64_t M, int64_t N, int64_t K) {
   return (size_t)(ceil_div(N, 128) * few_splits(N, K) * M * 128) * sizeof(float);
@@ -398,20 +407,7 @@ int products(MmEpilogue epilogue, MmLaunch* all, void* partial, void* stream) {
     }
   }
   if (!count) return VCOLL_OK;
-  Plan plan = make_plan(shape, count);
-#ifdef MM_DEBUG
-  if (const char* e = getenv("MM_PLAN")) {
-    int tn = 0, sp = 0;
-    if (sscanf(e, "%d,%d", &tn, &sp) == 2 && count == 1) {
-      plan.of[0].tn = tn;
-      plan.of[0].splits = sp;
-    }
-  }
-  if (getenv("MM_SHOW"))
-    for (int i = 0; i < count; ++i)
-      fprintf(stderr, "epi %d M %ld N %ld K %ld parts %d: ctas %d tn %d splits %d\n", (int)epilogue, shape[i].M, shape[i].N, shape[i].K,
-              shape[i].parts, plan.ctas, plan.of[i].tn, plan.of[i].splits);
-#endif
+  const Plan plan = make_plan(shape, count);
   all->error_word = device_error_symbol();
   if (!all->error_word) return fail(VCOLL_ERR_CUDA, "the device error word has no address");
   int64_t units = 0, join_blocks = 0;
@@ -849,9 +845,8 @@ int vcoll_gated_ff_backward(const void* dh, int64_t dh_ld, const void* x, int64_
     g.plane = N * 2 * L.half;
     g.f32 = dtype == VCOLL_F32;
     g.parts = parts;
-    g.act = activation;
     g.load16 = rows_at_16(dh, N, dh_ld, es) && rows_at_16(gate, N, gate_ld, es) && rows_at_16(up, N, up_ld, es);
-    VCOLL_TRY(launch_grid(mm_gated_grad_kernel(), pass_blocks(N * (L.half / 8)), 1, kPassThreads, 0, &g, stream));
+    VCOLL_TRY(launch_grid(mm_gated_grad_kernel(activation), pass_blocks(N * (L.half / 8)), 1, kPassThreads, 0, &g, stream));
   }
   const MmOperand grads = operand(ws + L.grads, N, 2 * L.half, 2 * L.half, N * 2 * L.half);
   const bool few = few_rows(N, dtype);
