@@ -2,12 +2,15 @@
 
 Each rank looks its tokens up (``embedding``), normalises the rows keeping 8
 bits of them (``layer_norm_checkpoint8``), and predicts every next token with
-the table itself.  For the backward pass the normalised rows are taken back
-from the kept form (``checkpoint8_restore``); the table's gradient from the
+the table itself (``cross_entropy``, which keeps no logits; padding has targets
+outside the table).  The loss's gradient follows at once
+(``cross_entropy_backward``), so that the normalised rows themselves need not be
+kept: the layer norm's gradient takes their 8-bit form
+(``layer_norm_backward_checkpoint8``), its weight and bias gradients going
+straight into the rank's gradient tensors.  The table's gradient from the
 projection is the base that the lookup's gradient is added to in place
-(``embedding_backward``), and the layer norm's weight and bias gradients
-(``layer_norm_backward_checkpoint8``) go straight into the rank's gradient
-tensors, which one ``FusionPlan`` averages over the ranks.
+(``embedding_backward``), and one ``FusionPlan`` averages everything over the
+ranks.
 
     python examples/data_parallel_step.py [steps]
 """
@@ -42,24 +45,16 @@ def gradients(params, grads, tokens, targets):
     scale = math.sqrt(WIDTH)
     x = vc.embedding(tokens, table, scale=scale)
     y, rstd, kept = vc.layer_norm_checkpoint8(x, weight, bias)
-    logits = y.flatten(0, 1) @ table.t()
-    del x, y  # the kept form is all that the backward pass needs of them
-    p = torch.log_softmax(logits, 1)
-    valid = (tokens >= 0) & (targets >= 0)
-    picked = targets.clamp(min=0).flatten()[:, None]
-    count = valid.sum()
-    loss = -(p.gather(1, picked)[:, 0] * valid.flatten()).sum() / count
-
-    dlogits = p.exp_()
-    dlogits.scatter_add_(1, picked, torch.full_like(picked, -1.0, dtype=dlogits.dtype))
-    dlogits *= valid.flatten()[:, None] / count
-    y = vc.checkpoint8_restore(kept, weight, bias, dtype=table.dtype).flatten(0, 1)
-    torch.mm(dlogits.t(), y, out=grads[0])
-    dy = (dlogits @ table).view(*tokens.shape, WIDTH)
+    del x
+    counted = torch.where(tokens >= 0, targets, -1)
+    share = 1.0 / ((counted >= 0).sum())
+    losses, lse = vc.cross_entropy(y, table, counted)
+    dy, _ = vc.cross_entropy_backward(share, y, table, counted, lse, dtable=grads[0])
+    del y  # the kept form is all that the rest of the backward pass needs of it
     dx, _, _ = vc.layer_norm_backward_checkpoint8(dy, kept, rstd, weight, dx=dy, dweight=grads[1],
                                                   dbias=grads[2])
     vc.embedding_backward(dx, tokens, VOCAB, scale=scale, base=grads[0], out=grads[0])
-    return loss
+    return losses.sum() * share
 
 
 def train(steps=60, rate=0.5):

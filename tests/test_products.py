@@ -3,6 +3,9 @@ gradients, against 64-bit definitions (products_ref.py): types, strides, sizes
 from nothing to several tiles, masks, pieces of the vocabulary, captured calls
 and other streams; and their refusals.  Every tolerance is the bound that
 products_ref.py derives for the inputs."""
+import math
+
+import numpy as np
 import pytest
 import torch
 
@@ -455,6 +458,163 @@ def test_repeated_calls_give_the_same_bits(v):
             assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
             for a, b in zip(grads, v.cross_entropy_backward(one, x, table, t, lse)):
                 assert torch.equal(a, b)
+
+
+def spot(r, t):
+    """A copy of a matrix at a random alignment and row stride."""
+    n, d = t.shape
+    pad, at = int(r.choice([0, 0, 0, 1, 2, 8, 24])), int(r.choice([0, 0, 1, 2, 3, 4, 8]))
+    flat = torch.empty(n * (d + pad) + at, dtype=t.dtype, device="cuda")
+    return flat[at:].view(n, d + pad)[:, :d].copy_(t)
+
+
+def size(r, lo, hi):
+    return int(round(np.exp(r.uniform(np.log(lo), np.log(hi)))))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("seed", range(60))
+def test_random_losses(v, seed):
+    r, g = np.random.default_rng(seed), gen(seed)
+    n, V, D = size(r, 1, 1500), size(r, 1, 6000), size(r, 1, 1500)
+    dtype = TYPES[r.integers(2)]
+    x, table, t = loss_case(g, n, V, D, dtype, kind=["all", "some", "some", "none"][r.integers(4)],
+                            index=[torch.int32, torch.int64][r.integers(2)])
+    x, table = spot(r, x), spot(r, table)
+    loss, lse = v.cross_entropy(x, table, t)
+    want, wlse, bound, blse = R.loss(x, table, t)
+    near(loss, want, bound)
+    near(lse, wlse, blse)
+    gloss = torch.randn(n if r.integers(2) else 1, generator=g, device="cuda")
+    base = spot(r, matrix(g, V, D, dtype)) if r.integers(2) else None
+    want = R.loss_grad(gloss, x, table, t, lse, base, dtype)
+    which = r.integers(4)  # both, or one alone
+    dx, dt = v.cross_entropy_backward(gloss, x, table, t, lse, base=base,
+                                      dx=filled(spot(r, x)) if which != 1 else None,
+                                      dtable=filled(spot(r, table)) if which != 2 else None,
+                                      x_grad=which != 1, table_grad=which != 2)
+    if which != 1:
+        near(dx, want[0], want[2], dtype)
+    if which != 2:
+        near(dt, want[1], want[3], dtype)
+    assert v.device_errors() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("seed", range(60))
+def test_random_gated_blocks(v, seed):
+    r, g = np.random.default_rng(seed + 1000), gen(seed + 1000)
+    n, D, F = size(r, 1, 1500), size(r, 1, 1500), size(r, 1, 3000)
+    dtype, act = TYPES[r.integers(2)], ["silu", "gelu", "gelu_tanh"][r.integers(3)]
+    x, wg, wu = (spot(r, t) for t in gated_case(g, n, D, F, dtype, "dense"))
+    keep = bool(r.integers(2))
+    h = v.gated_ff(x, wg, wu, activation=act, keep=keep, out=filled(spot(r, torch.empty(n, F, dtype=dtype, device="cuda"))))
+    want = R.gated(x, wg, wu, act)
+    for got, w, b in zip(h if keep else (h,), want[:3], want[3:]):
+        near(got, w, b, dtype)
+    gate, up, dh = (spot(r, matrix(g, n, F, dtype, "dense", s)) for s in (2.0, 1.0, 1e-2))
+    which = r.integers(4)
+    got = v.gated_ff_backward(dh, x, wg, wu, gate, up, activation=act, x_grad=which != 1, weight_grads=which != 2,
+                              dw_gate=filled(spot(r, wg)) if which == 3 else None)
+    want = R.gated_grad(dh, x, wg, wu, gate, up, act, dtype)
+    assert (got[0] is None) == (which == 1) and (got[2] is None) == (which == 2)
+    for t, w, b in zip(got, want[:3], want[3:]):
+        if t is not None:
+            near(t, w, b, dtype)
+    assert v.device_errors() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [3, 4, 5, 8, 9, 15, 16, 17, 33])
+@pytest.mark.parametrize("D,V", [(512, 1000), (1028, 333), (4099, 66), (130, 2049), (2, 9)])
+def test_few_rows_in_full_precision(v, n, D, V):
+    # up to 16 rows go another way than more, and rows of whole 16 bytes another than others
+    g = gen(n * D + V)
+    x, table, t = loss_case(g, n, V, D, torch.float32, kind="some")
+    loss, lse = v.cross_entropy(x, table, t)
+    want, wlse, bound, blse = R.loss(x, table, t)
+    near(loss, want, bound)
+    near(lse, wlse, blse)
+    gloss = torch.randn(n, generator=g, device="cuda")
+    base = matrix(g, V, D, torch.float32)
+    want = R.loss_grad(gloss, x, table, t, lse, base, torch.float32)
+    dx, dt = v.cross_entropy_backward(gloss, x, table, t, lse, base=base)
+    near(dx, want[0], want[2])
+    near(dt, want[1], want[3])
+    _, wg, wu = gated_case(g, 1, D, V, torch.float32, "dense")
+    h, gate, up = v.gated_ff(x, wg, wu, activation="gelu", keep=True)
+    want = R.gated(x, wg, wu, "gelu")
+    for got, w, b in zip((h, gate, up), want[:3], want[3:]):
+        near(got, w, b)
+    got = v.gated_ff_backward(h, x, wg, wu, gate, up, activation="gelu")
+    want = R.gated_grad(h, x, wg, wu, gate, up, "gelu", torch.float32)
+    for a, w, b in zip(got, want[:3], want[3:]):
+        near(a, w, b)
+
+
+@pytest.mark.gpu
+def test_a_table_past_32_bit_offsets(v):
+    g = gen(16)
+    V, D, n = 2_100_013, 2048, 5
+    assert V * D > 2 ** 32
+    table = torch.randn(V, D, generator=g, device="cuda", dtype=torch.bfloat16).mul_(0.02)
+    x = matrix(g, n, D, torch.bfloat16)
+    t = torch.tensor([0, V - 1, V - 2, V // 2, V], device="cuda")
+    loss, lse = v.cross_entropy(x, table, t)
+    parts = [R.product(x.double(), table[a:a + 65536].double().t()) for a in range(0, V, 65536)]
+    z, dz = (torch.cat([p[k] for p in parts], 1) for k in range(2))
+    wlse = torch.logsumexp(z, 1)
+    # the bound of a vocabulary that products_ref.loss has, written for rows already multiplied
+    p = torch.exp(z - wlse[:, None])
+    blse = (p * (dz + 4 * R.U * (2 + 2 * (z - z.amax(1, keepdim=True)).abs()))).sum(1) + (320 + V / 256) * R.U
+    blse = blse + 4 * R.U * (wlse.abs() + z.amax(1).abs() + math.log(V) + 1)
+    near(lse, wlse, blse)
+    at = t[:4, None]
+    near(loss[:4], wlse[:4] - z[:4].gather(1, at)[:, 0], blse[:4] + dz[:4].gather(1, at)[:, 0] + 8 * R.U * wlse[:4])
+    assert loss[4] == 0
+    dx, dt = v.cross_entropy_backward(torch.ones(1, device="cuda"), x, table, t, lse)
+    # the rows at both ends of the table's gradient, and between
+    for a in (0, V // 2 - 32, V - 64):
+        rows = slice(a, a + 64)
+        e = torch.exp(z[:4, rows] - lse[:4, None].double())
+        size_e = e.clone()
+        for i in range(4):
+            if a <= int(t[i]) < a + 64:
+                e[i, int(t[i]) - a] -= 1.0
+                size_e[i, int(t[i]) - a] += 1.0
+        want = e.t() @ x[:4].double()
+        bound = (size_e * (dz[:4, rows] + 2.0 ** -20 * (2 + z[:4, rows].abs())) + R.BF16 * 1.01 * e.abs()).t() @ x[:4].double().abs()
+        near(dt[rows], want, bound + 64 * R.U * (e.abs().t() @ x[:4].double().abs()), torch.bfloat16)
+    want = sum(p[:4, a:a + 65536] @ table[a:a + 65536].double() for a in range(0, V, 65536))
+    want = want - table[t[:4]].double()
+    size_w = sum(p[:4, a:a + 65536] @ table[a:a + 65536].double().abs() for a in range(0, V, 65536)) + table[t[:4]].double().abs()
+    near(dx[:4], want, size_w * (R.BF16 * 1.01 + 1e-3), torch.bfloat16)
+    assert not dx[4].any()
+
+
+@pytest.mark.gpu
+def test_two_graphs_in_turn(v):
+    g = gen(17)
+    cases = [loss_case(g, n, V, 64, torch.bfloat16) for n, V in ((300, 900), (40, 5000))]
+    one = torch.ones(1, device="cuda")
+    graphs, outs = [], []
+    for x, table, t in cases:
+        lse = v.cross_entropy(x, table, t)[1]
+        v.cross_entropy_backward(one, x, table, t, lse)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            loss, lse = v.cross_entropy(x, table, t)
+            outs.append((loss, lse, *v.cross_entropy_backward(one, x, table, t, lse)))
+        graphs.append(graph)
+    for _ in range(3):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for (x, table, t), out in zip(cases, outs):
+        loss, lse = v.cross_entropy(x, table, t)
+        for a, b in zip(out, (loss, lse, *v.cross_entropy_backward(one, x, table, t, lse))):
+            assert torch.equal(a, b)
 
 
 @pytest.mark.gpu
