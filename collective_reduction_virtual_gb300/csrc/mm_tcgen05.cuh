@@ -51,8 +51,8 @@ __device__ __forceinline__ bool mm_elect() {
   return yes != 0;
 }
 
-// What a CTA's waits share: where a wait that gives up is recorded, and that
-// the CTA's other waits need not be waited for any more.
+// Where a wait that gives up is recorded: for the CTA's other roles, which begin
+// nothing more, and for the host.
 struct MmAbort {
   volatile int* flag;    // in shared memory
   unsigned* error_word;  // VCOLL_DEVICE_ERR_*
@@ -72,8 +72,7 @@ __device__ __noinline__ bool mm_bar_wait_long(uint32_t bar, unsigned parity, con
   return true;
 }
 
-// False where the phase did not complete in time, or another wait of the CTA
-// had given up before.
+// False where the phase did not complete in time.
 __device__ __forceinline__ bool mm_bar_wait(uint32_t bar, unsigned parity, const MmAbort& a,
                                             uint64_t limit = kMmWaitNs) {
   if (mm_bar_try(bar, parity)) return true;
@@ -122,10 +121,6 @@ __device__ __forceinline__ void mm_load_box(uint32_t dst, const CUtensorMap* map
             "r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
-}
-
-__device__ __forceinline__ void mm_prefetch_map(const CUtensorMap* map) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 // ------------------------------------------------------------ tensor memory

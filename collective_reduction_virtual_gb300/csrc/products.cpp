@@ -138,25 +138,29 @@ Plan search_plan(const Shape* shape, int count) {
   return best;
 }
 
-// A program repeats the sizes of its calls: each thread keeps its last plans.
+// A program repeats the sizes of its calls: each thread keeps plans, one in a place
+// that the sizes decide.
 Plan make_plan(const Shape* shape, int count) {
   struct Kept {
     Shape shape[2];
     int count = 0;
     Plan plan;
   };
-  static thread_local Kept kept[32];
-  static thread_local int next = 0;
+  static thread_local Kept kept[256];
   auto same = [](const Shape& a, const Shape& b) {
     return a.M == b.M && a.N == b.N && a.K == b.K && a.parts == b.parts && a.halves == b.halves &&
            a.epilogue == b.epilogue;
   };
-  for (const Kept& k : kept)
-    if (k.count == count && same(k.shape[0], shape[0]) && (count == 1 || same(k.shape[1], shape[1]))) return k.plan;
-  Kept& k = kept[next++ % 32];
-  for (int i = 0; i < count; ++i) k.shape[i] = shape[i];
-  k.plan = search_plan(shape, count);
-  k.count = count;
+  uint64_t place = (uint64_t)count;
+  for (int i = 0; i < count; ++i)
+    for (const int64_t v : {shape[i].M, shape[i].N, shape[i].K, (int64_t)shape[i].parts + 4 * shape[i].epilogue})
+      place = (place ^ (uint64_t)v) * 0x9E3779B97F4A7C15ull;
+  Kept& k = kept[place >> 56];
+  if (k.count != count || !same(k.shape[0], shape[0]) || (count > 1 && !same(k.shape[1], shape[1]))) {
+    for (int i = 0; i < count; ++i) k.shape[i] = shape[i];
+    k.plan = search_plan(shape, count);
+    k.count = count;
+  }
   return k.plan;
 }
 

@@ -472,15 +472,17 @@ int vcoll_layer_norm_backward_checkpoint8(const void* grad, int64_t grad_ld, con
  * in addition:
  *  - bf16 products are exact and summed in fp32.  fp32 operands are taken as
  *    three bf16 parts each, which together hold their 24 bits, in six products
- *    summed in fp32; an infinite fp32 operand gives NaN.
+ *    summed in fp32 (weights that meet 16 rows or fewer as they are); an infinite
+ *    fp32 operand may give NaN.
  *  - A bf16 matrix in device memory that starts at a 16-byte boundary, with a
  *    row stride that is a multiple of 8, is read where it lies; any other, and
  *    every fp32 one, is laid out in the workspace first.
  *  - The *_workspace_bytes functions take `direct`: 1 where all the matrices
  *    that the products read (x, table, w_gate, w_up) lie so; 0 always suffices.
  *    The workspace is device memory.
- *  - The order of a sum is fixed by the sizes, the type and the GPU.  Other
- *    rows than a row's own do not touch its results.
+ *  - The order of a sum is fixed by the sizes, the type, the GPU and, of 16 fp32
+ *    rows or fewer, whether the weights' rows are whole 16-byte pieces.  A call
+ *    repeated on the same buffers gives the same bits.
  */
 
 /*
@@ -551,9 +553,10 @@ int vcoll_gated_ff_backward(const void* dh, int64_t dh_ld, const void* x, int64_
                             size_t workspace_bytes, void* stream);
 
 /* Device-side error bits, OR-ed into one word per device by the kernels.
- * The staged kernels bound every wait on their shared-memory barriers (2 s of
- * wall-clock time); a wait that gives up records VCOLL_DEVICE_ERR_TIMEOUT and
- * the kernel returns early (its outputs are then incomplete). */
+ * The staged kernels and the products bound every wait on their shared-memory
+ * barriers (2 s of wall-clock time); a wait that gives up records
+ * VCOLL_DEVICE_ERR_TIMEOUT and the kernel returns early (its outputs are then
+ * incomplete). */
 #define VCOLL_DEVICE_ERR_TIMEOUT 0x1u
 
 /* Reads the current device's error word into *flags (and resets it when
