@@ -36,9 +36,11 @@ struct Regions {
   }
 };
 
-// A matrix laid out as parts: rows of a multiple of 8 values.
+// A matrix laid out as parts: rows of whole 128-byte lines, which a step of a
+// product reads one of.
+constexpr int64_t kPackedCols = 64;
 int64_t packed_bytes(int64_t rows, int64_t cols, int parts) {
-  return rows * round_up(cols, 8) * 2 * parts;
+  return rows * round_up(cols, kPackedCols) * 2 * parts;
 }
 
 // A product to be planned.
@@ -234,7 +236,7 @@ LossGradLayout loss_grad_layout(int64_t N, int64_t V, int64_t D, int dtype, bool
   if (!direct && !few) fit = std::min(fit, kPackBytes / std::max<int64_t>(1, packed_bytes(1, D, parts)));
   L.piece = piece_of(V, fit);
   L.pieces = std::max<int64_t>(1, L.piece ? ceil_div(V, L.piece) : 1);
-  L.error_ld = round_up(L.piece, 64);  // rows of whole 128-byte lines
+  L.error_ld = round_up(L.piece, kPackedCols);
   Regions r;
   L.scale = r.take(sizeof(float));
   L.x = r.take(packed_bytes(N, D, parts));
@@ -345,7 +347,7 @@ struct Packer {
     j.rows = rows;
     j.cols = cols;
     j.src_ld = ld;
-    j.dst_ld = round_up(cols, 8);
+    j.dst_ld = round_up(cols, kPackedCols);
     j.plane = rows * j.dst_ld;
     j.masked = masked;
     j.load16 = rows_at_16(src, rows, ld, p.src_f32 ? 4 : 2);
