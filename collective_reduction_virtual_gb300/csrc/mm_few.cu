@@ -13,7 +13,9 @@ namespace vcoll {
 namespace {
 
 constexpr int kThreads = kMmFewThreads, kWarps = kThreads / 32;
+constexpr int kColThreads = kMmFewColThreads, kColWarps = kColThreads / 32;
 constexpr int kChunk = 512;  // places of a sum whose small operand is in shared memory
+constexpr int kRows = 4;     // of the weight that a warp has in flight, and again as many
 
 // Eight values of an operand in parts, from a multiple of 8 on; rows are as long.
 __device__ __forceinline__ void from_parts(const MmOperand& o, int64_t row, int64_t col, float (&v)[8]) {
@@ -25,37 +27,33 @@ __device__ __forceinline__ void from_parts(const MmOperand& o, int64_t row, int6
   for (int j = 0; j < 8; ++j) v[j] = q[0][j] + (q[1][j] + q[2][j]);
 }
 
-// Four values of a row, of which `count` from its first on are there: those from
-// `at` on, 16 bytes at once, or without WIDE every 32nd from there, so that a warp
-// reads 128 bytes in a row.  The others are zeros; the row's first value is read in
-// their place, since loads behind a condition would wait for each other.
+// A lane's four values: adjacent ones, 16 bytes at once, or without WIDE every 32nd,
+// so that a warp reads 128 bytes in a row.
 template <bool WIDE>
-__device__ __forceinline__ float4 load4(const float* row, int64_t at, int64_t count) {
-  float4 v;
-  if (WIDE) {
-    const bool in = at < count;
-    const uint4 q = ld_stream(in ? row + at : row);
-    v = make_float4(__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z), __uint_as_float(q.w));
-    if (!in) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  } else {
-    const bool x = at < count, y = at + 32 < count, z = at + 64 < count, w = at + 96 < count;
-    v.x = __ldg(x ? row + at : row);
-    v.y = __ldg(y ? row + at + 32 : row);
-    v.z = __ldg(z ? row + at + 64 : row);
-    v.w = __ldg(w ? row + at + 96 : row);
-    v.x = x ? v.x : 0.0f;
-    v.y = y ? v.y : 0.0f;
-    v.z = z ? v.z : 0.0f;
-    v.w = w ? v.w : 0.0f;
-  }
-  return v;
+constexpr int kFirst = WIDE ? 4 : 1;  // places between lanes
+template <bool WIDE>
+constexpr int kNext = WIDE ? 1 : 32;  // and between a lane's four
+template <bool WIDE>
+__device__ __forceinline__ float4 load4(const float* p) {
+  if (!WIDE) return make_float4(__ldg(p), __ldg(p + 32), __ldg(p + 64), __ldg(p + 96));
+  const uint4 q = ld_stream(p);
+  return make_float4(__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z), __uint_as_float(q.w));
+}
+// The same from place `at` of a row of `count` values, zeros past its end.
+template <bool WIDE>
+__device__ __forceinline__ float4 load4_end(const float* row, int64_t at, int64_t count) {
+  if (WIDE) return at < count ? load4<true>(row + at) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  return make_float4(at < count ? __ldg(row + at) : 0.0f, at + 32 < count ? __ldg(row + at + 32) : 0.0f,
+                     at + 64 < count ? __ldg(row + at + 64) : 0.0f, at + 96 < count ? __ldg(row + at + 96) : 0.0f);
 }
 
-// The warp's sums of N values: those from lane * (N / 32) on, N / 32 of them, in the
-// lane's first.  In each step a lane gives half of what it has to the lane S away.
+// The warp's sums of N values: those from lane * N / 32 on, N / 32 of them but one at
+// least, in the lane's first.  In each step a lane gives half of what it has to the
+// lane S away.
 template <int S, int LEFT, int N>
 __device__ __forceinline__ void scatter_sums(float (&v)[N], int lane) {
   const bool upper = lane & S;
+  if constexpr (LEFT == 1) v[0] += __shfl_xor_sync(~0u, v[0], S);
 #pragma unroll
   for (int j = 0; j < LEFT / 2; ++j) {
     const float give = upper ? v[j] : v[LEFT / 2 + j], keep = upper ? v[LEFT / 2 + j] : v[j];
@@ -82,8 +80,9 @@ struct FewSource {
 
 }  // namespace
 
-// Rows of the small operand a times rows of the weight b: a CTA for all of a,
-// ROWS at most, and 64 rows of b, eight a warp, whose lanes go along the sum.
+// Rows of the small operand a times rows of the weight b: a CTA for all of a, ROWS
+// at most, and 64 rows of b, four a warp, whose lanes go along the sum.  A warp's
+// next loads are under way while it multiplies.
 template <int EPI, int ROWS, bool WIDE>
 __global__ void __launch_bounds__(kThreads) vc_mm_few_rows(const __grid_constant__ MmLaunch all) {
   pdl_enter();
@@ -95,13 +94,38 @@ __global__ void __launch_bounds__(kThreads) vc_mm_few_rows(const __grid_constant
   const int64_t tile_n = blockIdx.x;
   const bool second = EPI == MM_GATED && warp >= kWarps / 2;  // gate's rows, then as many of up's
   const MmOperand& b = p.b[second];
-  const int64_t first = EPI == MM_GATED ? tile_n * 32 + warp % (kWarps / 2) * 8 : tile_n * 64 + warp * 8;
-  const float* w[8];
+  const int64_t first = EPI == MM_GATED ? tile_n * 32 + warp % (kWarps / 2) * kRows : tile_n * 64 + warp * kRows;
+  const float* w[kRows];
 #pragma unroll
-  for (int r = 0; r < 8; ++r)  // rows past the end give columns that are not stored
+  for (int r = 0; r < kRows; ++r)  // rows past the end give columns that are not stored
     w[r] = static_cast<const float*>(b.p) + (first + r < b.rows ? first + r : b.rows - 1) * b.ld;
-  float acc[8 * ROWS] = {};
-  constexpr int FIRST = WIDE ? 4 : 1, NEXT = WIDE ? 1 : 32;  // places between lanes, and between a lane's four
+  constexpr int FIRST = kFirst<WIDE>, NEXT = kNext<WIDE>;
+  float acc[kRows * ROWS] = {};
+  float4 now[kRows], next[kRows];
+  // a row's values from place k on, zeros past its end: its first one is read in their
+  // place, since a load behind a condition would wait for the one before
+  auto fetch = [&](const float* row, int64_t k) {
+    const int64_t at = k + lane * FIRST;
+    float4 v;
+    if (WIDE) {
+      const bool in = at < p.K;
+      v = load4<true>(in ? row + at : row);
+      if (!in) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    } else {
+      const bool x = at < p.K, y = at + 32 < p.K, z = at + 64 < p.K, u = at + 96 < p.K;
+      v = make_float4(__ldg(x ? row + at : row), __ldg(y ? row + at + 32 : row), __ldg(z ? row + at + 64 : row),
+                      __ldg(u ? row + at + 96 : row));
+      v.x = x ? v.x : 0.0f;
+      v.y = y ? v.y : 0.0f;
+      v.z = z ? v.z : 0.0f;
+      v.w = u ? v.w : 0.0f;
+    }
+    return v;
+  };
+  if (p.K) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) next[r] = fetch(w[r], 0);
+  }
   for (int64_t k0 = 0; k0 < p.K; k0 += kChunk) {
     for (int e = threadIdx.x; e < ROWS * (kChunk / 8); e += kThreads) {
       const int m = e / (kChunk / 8), k = e % (kChunk / 8) * 8;
@@ -111,34 +135,30 @@ __global__ void __launch_bounds__(kThreads) vc_mm_few_rows(const __grid_constant
       for (int j = 0; j < 8; ++j) xs[m][k + j] = k0 + k + j < p.K ? v[j] : 0.0f;
     }
     __syncthreads();
-    constexpr int STEPS = ROWS == 4 ? 2 : 1;  // loads in flight: as many as there are registers
-    for (int k = 0; k < kChunk && k0 + k < p.K; k += 128 * STEPS) {
-      float4 v[STEPS][8];
+    for (int k = 0; k < kChunk && k0 + k < p.K; k += 128) {
 #pragma unroll
-      for (int s = 0; s < STEPS; ++s)
+      for (int r = 0; r < kRows; ++r) {
+        now[r] = next[r];
+        next[r] = fetch(w[r], k0 + k + 128);
+      }
 #pragma unroll
-        for (int r = 0; r < 8; ++r) v[s][r] = load4<WIDE>(w[r], k0 + k + 128 * s + lane * FIRST, p.K);
+      for (int m = 0; m < ROWS; ++m) {
+        const float* at = &xs[m][k + lane * FIRST];
+        const float4 x = WIDE ? *reinterpret_cast<const float4*>(at)
+                              : make_float4(at[0], at[NEXT], at[2 * NEXT], at[3 * NEXT]);
 #pragma unroll
-      for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-        for (int m = 0; m < ROWS; ++m) {
-          const float* at = &xs[m][k + 128 * s + lane * FIRST];
-          const float4 x = WIDE ? *reinterpret_cast<const float4*>(at)
-                                : make_float4(at[0], at[NEXT], at[2 * NEXT], at[3 * NEXT]);
-#pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            const float4 y = v[s][r];
-            acc[r * ROWS + m] += (y.x * x.x + y.y * x.y) + (y.z * x.z + y.w * x.w);
-          }
-        }
+        for (int r = 0; r < kRows; ++r)
+          acc[r * ROWS + m] += (now[r].x * x.x + now[r].y * x.y) + (now[r].z * x.z + now[r].w * x.w);
+      }
     }
     __syncthreads();
   }
-  scatter_sums<16, 8 * ROWS>(acc, lane);
+  constexpr int EACH = kRows * ROWS / 32 > 0 ? kRows * ROWS / 32 : 1;
+  scatter_sums<16, kRows * ROWS>(acc, lane);
 #pragma unroll
-  for (int j = 0; j < 8 * ROWS / 32; ++j) {
-    const int at = lane * (8 * ROWS / 32) + j;  // r * ROWS + m
-    sums[at % ROWS * 65 + warp * 8 + at / ROWS] = acc[j];
+  for (int j = 0; j < EACH; ++j) {
+    const int at = (lane * kRows * ROWS >> 5) + j;  // r * ROWS + m
+    sums[at % ROWS * 65 + warp * kRows + at / ROWS] = acc[j];
   }
   __syncthreads();
   if (warp) return;
@@ -149,10 +169,11 @@ __global__ void __launch_bounds__(kThreads) vc_mm_few_rows(const __grid_constant
 // The small operand a times the weight b, which is taken transposed: a CTA for all
 // rows, ROWS at most, 128 columns, four a lane, and a split of the sum, which its warps share.
 template <int ROWS, bool WIDE>
-__global__ void __launch_bounds__(kThreads) vc_mm_few_cols(const __grid_constant__ MmLaunch all) {
+__global__ void __launch_bounds__(kColThreads, 2) vc_mm_few_cols(const __grid_constant__ MmLaunch all) {
   pdl_enter();
   const MmParams& p = all.p[0];
-  constexpr int CHUNK = 4096 / ROWS, FIRST = WIDE ? 4 : 1, NEXT = WIDE ? 1 : 32;
+  constexpr int FLIGHT = ROWS == 16 ? 4 : 8;  // of the weight's rows that a warp has in flight, and again as many
+  constexpr int CHUNK = 4096 / ROWS, FIRST = kFirst<WIDE>, NEXT = kNext<WIDE>;
   __shared__ float xs[CHUNK][ROWS];
   __shared__ float sums[ROWS][128];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -162,9 +183,33 @@ __global__ void __launch_bounds__(kThreads) vc_mm_few_cols(const __grid_constant
   const int64_t end = split + 1 == p.splits ? p.K : p.K * (split + 1) / p.splits & ~(int64_t)7;
   const float *w0 = static_cast<const float*>(p.b[0].p), *w1 = static_cast<const float*>(p.b[1].p);
   const int64_t rows0 = p.b[0].rows, rows1 = p.b[1].rows, ld0 = p.b[0].ld, ld1 = p.b[1].ld;
+  // the weight's rows at places k .. of the sum.  Columns past the end are not stored:
+  // the last ones stand in for them, so that there is no condition between the loads.
+  int64_t from[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) from[j] = WIDE ? (col < p.N ? col : p.N - 4) : col + 32 * j < p.N ? col + 32 * j : p.N - 1;
+  float4 now[FLIGHT], next[FLIGHT];
+  auto fetch = [&](int64_t k) {
+    const bool second = k >= p.K1;
+    const int64_t r = second ? k - p.K1 : k, rows = second ? rows1 : rows0, ld = second ? ld1 : ld0;
+    const float* w = (second ? w1 : w0) + r * ld;
+    if (k + FLIGHT <= end && r + FLIGHT <= rows) {
+#pragma unroll
+      for (int i = 0; i < FLIGHT; ++i) {
+        const float* q = w + i * ld;
+        next[i] = WIDE ? load4<true>(q + from[0])
+                       : make_float4(__ldg(q + from[0]), __ldg(q + from[1]), __ldg(q + from[2]), __ldg(q + from[3]));
+      }
+    } else {  // what pads a's first half has no row
+#pragma unroll
+      for (int i = 0; i < FLIGHT; ++i)
+        next[i] = load4_end<WIDE>(w + i * ld, col, k + i < end && r + i < rows ? p.N : 0);
+    }
+  };
   float acc[ROWS][4] = {};
+  fetch(begin + warp * FLIGHT);
   for (int64_t k0 = begin; k0 < end; k0 += CHUNK) {
-    for (int e = threadIdx.x; e < ROWS * (CHUNK / 8); e += kThreads) {
+    for (int e = threadIdx.x; e < ROWS * (CHUNK / 8); e += kColThreads) {
       const int m = e % ROWS, k = e / ROWS * 8;
       float v[8] = {};
       if (m < p.M && k0 + k < end) from_parts(p.a, m, k0 + k, v);
@@ -172,30 +217,26 @@ __global__ void __launch_bounds__(kThreads) vc_mm_few_cols(const __grid_constant
       for (int j = 0; j < 8; ++j) xs[k + j][m] = k0 + k + j < end ? v[j] : 0.0f;
     }
     __syncthreads();
-    for (int k = warp * 8; k < CHUNK && k0 + k < end; k += kWarps * 8) {
-      float4 v[8];
+    for (int k = warp * FLIGHT; k < CHUNK && k0 + k < end; k += kColWarps * FLIGHT) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool second = k0 + k + i >= p.K1;
-        const int64_t r = second ? k0 + k + i - p.K1 : k0 + k + i, rows = second ? rows1 : rows0;
-        const bool in = r < rows && k0 + k + i < end;  // or it pads a's first half
-        const float* w = !in ? w0 : second ? w1 + r * ld1 : w0 + r * ld0;  // w1 may be absent
-        v[i] = load4<WIDE>(w, col, in ? p.N : 0);
-      }
+      for (int i = 0; i < FLIGHT; ++i) now[i] = next[i];
+      // this warp's next rows: of this chunk, or its first of the next one
+      const int64_t then = k0 + (k + kColWarps * FLIGHT < CHUNK ? k + kColWarps * FLIGHT : CHUNK + warp * FLIGHT);
+      fetch(then);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < FLIGHT; ++i)
 #pragma unroll
         for (int m = 0; m < ROWS; ++m) {
           const float x = xs[k + i][m];
-          acc[m][0] += x * v[i].x;
-          acc[m][1] += x * v[i].y;
-          acc[m][2] += x * v[i].z;
-          acc[m][3] += x * v[i].w;
+          acc[m][0] += x * now[i].x;
+          acc[m][1] += x * now[i].y;
+          acc[m][2] += x * now[i].z;
+          acc[m][3] += x * now[i].w;
         }
     }
     __syncthreads();
   }
-  for (int q = 0; q < kWarps; ++q) {  // one warp after the other: a fixed order
+  for (int q = 0; q < kColWarps; ++q) {  // one warp after the other: a fixed order
     if (warp == q) {
 #pragma unroll
       for (int m = 0; m < ROWS; ++m)
@@ -208,12 +249,13 @@ __global__ void __launch_bounds__(kThreads) vc_mm_few_cols(const __grid_constant
     __syncthreads();
   }
   float* to = p.partial + ((int64_t)blockIdx.x * p.splits + split) * p.M * p.tn;
-  for (int e = threadIdx.x; e < p.M * 128; e += kThreads) to[e] = sums[0][e];
+  for (int e = threadIdx.x; e < p.M * 128; e += kColThreads) to[e] = sums[0][e];
 }
 
 // The products of the columns of two small operands of a few rows: a CTA for
 // 64 x 128 of the result, which it writes (and adds to base): bound by that.
-__global__ void __launch_bounds__(kThreads) vc_mm_few_outer(const __grid_constant__ MmLaunch all) {
+template <bool WIDE>
+__global__ void __launch_bounds__(kColThreads) vc_mm_few_outer(const __grid_constant__ MmLaunch all) {
   pdl_enter();
   const MmParams& p = all.p[1];
   __shared__ __align__(16) float es[kMmFewRows][64];
@@ -222,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) vc_mm_few_outer(const __grid_constan
   const int64_t tiles = (p.N + 127) / 128;
   const int64_t row0 = blockIdx.x / tiles * 64, col0 = blockIdx.x % tiles * 128;
   const int K = (int)p.K;
-  for (int e = threadIdx.x; e < K * 24; e += kThreads) {
+  for (int e = threadIdx.x; e < K * 24; e += kColThreads) {
     const int k = e / 24, i = e % 24 * 8;  // 64 of es and 128 of xs; what is past their ends is not stored
     float v[8] = {};
     if (i < 64) {
@@ -238,7 +280,8 @@ __global__ void __launch_bounds__(kThreads) vc_mm_few_outer(const __grid_constan
   float acc[8][4] = {};
 #pragma unroll 2
   for (int k = 0; k < K; ++k) {
-    const float4 x = *reinterpret_cast<const float4*>(&xs[k][lane * 4]);
+    const float4 x = WIDE ? *reinterpret_cast<const float4*>(&xs[k][lane * 4])
+                          : make_float4(xs[k][lane], xs[k][lane + 32], xs[k][lane + 64], xs[k][lane + 96]);
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       const float e = es[k][warp * 8 + r];
@@ -249,29 +292,34 @@ __global__ void __launch_bounds__(kThreads) vc_mm_few_outer(const __grid_constan
     }
   }
   const float scale = p.scale ? *p.scale : 1.0f;
-  const int64_t col = col0 + lane * 4, left = p.N - col;
+  const int64_t col = col0 + (WIDE ? lane * 4 : lane);
   const MmOutRow to = mm_out_row(p, row0);
-  const int64_t end = p.M1 ? p.M2 : p.M;
-  const bool whole = all.wide && left >= 4;
+  const int64_t first = to.row + warp * 8, end = p.M1 ? p.M2 : p.M;
+  float4 x[8];  // of base, all loads at once
+#pragma unroll
+  for (int r = 0; r < 8; ++r) x[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const float* base = static_cast<const float*>(p.base);
+  if (base && first + 8 <= end && col0 + 128 <= p.N) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) x[r] = load4<WIDE>(base + (first + r) * p.base_ld + col);
+  } else if (base && first < end) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+      x[r] = load4_end<WIDE>(base + (first + r < end ? first + r : first) * p.base_ld, col, p.N);
+  }
 #pragma unroll
   for (int r = 0; r < 8; ++r) {
-    const int64_t row = to.row + warp * 8 + r;
-    if (row >= end) break;
-    float v[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = acc[r][j] * scale;
-    float* out = static_cast<float*>(to.out) + row * to.ld + col;
-    const float* base = static_cast<const float*>(p.base) + row * p.base_ld + col;
-    if (whole) {
-      if (p.base) {
-        const float4 x = *reinterpret_cast<const float4*>(base);
-        v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-      }
-      *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
+    if (first + r >= end) break;
+    float* out = static_cast<float*>(to.out) + (first + r) * to.ld + col;
+    const float4 y = make_float4(x[r].x + acc[r][0] * scale, x[r].y + acc[r][1] * scale, x[r].z + acc[r][2] * scale,
+                                 x[r].w + acc[r][3] * scale);
+    if (WIDE) {
+      if (col < p.N) *reinterpret_cast<float4*>(out) = y;
     } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j < left) out[j] = p.base ? base[j] + v[j] : v[j];
+      if (col < p.N) out[0] = y.x;
+      if (col + 32 < p.N) out[32] = y.y;
+      if (col + 64 < p.N) out[64] = y.z;
+      if (col + 96 < p.N) out[96] = y.w;
     }
   }
 }
@@ -294,6 +342,8 @@ const void* mm_few_kernel(MmEpilogue epilogue, int rows, bool wide) {
   if (rows <= 8) return wide ? rows_kernel<8, true>(epilogue) : rows_kernel<8, false>(epilogue);
   return wide ? rows_kernel<16, true>(epilogue) : rows_kernel<16, false>(epilogue);
 }
-const void* mm_few_outer_kernel() { return (const void*)vc_mm_few_outer; }
+const void* mm_few_outer_kernel(bool wide) {
+  return wide ? (const void*)vc_mm_few_outer<true> : (const void*)vc_mm_few_outer<false>;
+}
 
 }  // namespace vcoll

@@ -90,7 +90,6 @@ struct MmLaunch {
   int stages, stage_bytes;
   uint32_t ahead;
   unsigned* error_word;
-  int wide;  // mm_few.cu: the result's matrices allow accesses of 16 bytes
 };
 
 // The six products of three parts that reach an fp32 result's precision, the
@@ -169,13 +168,14 @@ struct MmGatedGradParams {
 
 // mm_few.cu: fp32 rows that it takes at most.
 constexpr int kMmFewRows = 16;
-constexpr int kMmFewThreads = 256;
+constexpr int kMmFewThreads = 512;
+constexpr int kMmFewColThreads = 256;
 
 // ctas that share a tile: 1 or 2
 const void* mm_kernel(MmEpilogue epilogue, int ctas);
 const void* mm_join_splits_kernel(MmEpilogue epilogue);
 const void* mm_few_kernel(MmEpilogue epilogue, int rows, bool wide);  // MM_OUT: sums for the join
-const void* mm_few_outer_kernel();
+const void* mm_few_outer_kernel(bool wide);
 const void* mm_pack_kernel();
 const void* mm_join_kernel();
 const void* mm_gated_grad_kernel(int act);

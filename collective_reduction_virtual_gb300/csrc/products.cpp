@@ -171,10 +171,10 @@ Plan plan_of(const Shape& a) { return make_plan(&a, 1); }
 // Whether the products are those of mm_few.cu, which read fp32 weights where they
 // lie.
 bool few_rows(int64_t N, int dtype) { return dtype == VCOLL_F32 && N <= kMmFewRows; }
-// Splits of the sum of a product with a weight that is taken transposed: two CTAs
-// per SM, of 256 places at least; the join adds them one after the other.
+// Splits of the sum of a product with a weight that is taken transposed: one wave of
+// two CTAs per SM, of 256 places at least; the join adds them one after the other.
 int64_t few_splits(int64_t N, int64_t K) {
-  const int64_t fill = ceil_div(2 * kPlanSms, std::max<int64_t>(1, ceil_div(N, 128)));
+  const int64_t fill = 2 * kPlanSms / std::max<int64_t>(1, ceil_div(N, 128));
   return std::max<int64_t>(1, std::min<int64_t>({fill, K / 256, 128}));
 }
 size_t few_bytes(int64_t M, int64_t N, int64_t K) {
@@ -491,7 +491,7 @@ int few_product(MmEpilogue epilogue, MmLaunch* all, void* partial, void* stream)
   p->tiles_m = 1;
   p->tiles_n = (uint32_t)ceil_div(p->N, 128);
   p->join_blocks = (uint32_t)ceil_div((int64_t)p->tiles_n * p->M * 4, 8);
-  VCOLL_TRY(launch_grid(fn, p->tiles_n, p->splits, kMmFewThreads, 0, all, stream));
+  VCOLL_TRY(launch_grid(fn, p->tiles_n, p->splits, kMmFewColThreads, 0, all, stream));
   return launch_grid(mm_join_splits_kernel(MM_OUT), p->join_blocks, 1, 256, 0, all, stream);
 }
 
@@ -501,9 +501,9 @@ int few_outer(MmLaunch* all, void* stream) {
   if (!tiles) return VCOLL_OK;
   if (tiles > 0x7FFFFFFF) return fail(VCOLL_ERR_UNSUPPORTED, "%lld tiles are too many", (long long)tiles);
   const int64_t rows = p->M1 ? p->M2 : p->M;
-  all->wide = wide_rows(p->out, rows, p->N, p->out_ld) && (!p->out2 || wide_rows(p->out2, rows, p->N, p->out2_ld)) &&
-              (!p->base || wide_rows(p->base, rows, p->N, p->base_ld));
-  return launch_grid(mm_few_outer_kernel(), tiles, 1, kMmFewThreads, 0, all, stream);
+  const bool wide = wide_rows(p->out, rows, p->N, p->out_ld) && (!p->out2 || wide_rows(p->out2, rows, p->N, p->out2_ld)) &&
+                    (!p->base || wide_rows(p->base, rows, p->N, p->base_ld));
+  return launch_grid(mm_few_outer_kernel(wide), tiles, 1, kMmFewColThreads, 0, all, stream);
 }
 
 // The launch's products on the units that suit them.
