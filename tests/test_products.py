@@ -425,6 +425,36 @@ def test_captured_calls_replay_on_new_inputs(v, dtype):
 
 
 @pytest.mark.gpu
+def test_a_process_may_capture_its_first_calls():
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+import collective_reduction_virtual_gb300 as vc
+x, w = torch.randn(200, 256, device="cuda").bfloat16(), torch.randn(512, 256, device="cuda").bfloat16()
+t = torch.randint(0, 512, (200,), device="cuda")
+one = torch.ones(1, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    loss, lse = vc.cross_entropy(x, w, t)
+    grads = vc.cross_entropy_backward(one, x, w, t, lse)
+    h, gate, up = vc.gated_ff(x, w, w, keep=True)
+    more = vc.gated_ff_backward(h, x, w, w, gate, up)
+graph.replay()
+torch.cuda.synchronize()
+again = vc.cross_entropy(x, w, t)
+assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
+for a, b in zip((*grads, *more), (*vc.cross_entropy_backward(one, x, w, t, lse), *vc.gated_ff_backward(h, x, w, w, gate, up))):
+    assert torch.equal(a, b)
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.gpu
 def test_calls_on_two_streams_at_once(v):
     g = gen(11)
     cases = [loss_case(g, 400, 3000, 256, torch.bfloat16) for _ in range(2)]
