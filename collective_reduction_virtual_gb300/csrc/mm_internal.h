@@ -43,7 +43,7 @@ struct MmParams {
   int tn;         // columns of a tile
   uint32_t tiles_m, tiles_n;
   int tile_rows;      // 128, or 256 of a pair of CTAs
-  int warp_rows;      // that a warp's epilogue has at most: 32
+  int warp_rows;      // that a warp's epilogue has at most: 32, or all of a few
   int a_rows;         // of a stage's a: 128, or fewer where M is smaller
   uint32_t chunk;       // steps that the tensor cores sum before the sum is added in registers
   uint32_t splits;      // that a tile's sum is cut into
@@ -164,6 +164,8 @@ struct MmGatedGradParams {
   int64_t dst_ld, half, plane;  // gate's at 0, up's at half
   int f32, parts;
   int load16;  // the rows of dh, gate and up start at 16-byte boundaries
+  int64_t blocks;     // CTAs; those after them lay out matrices
+  MmPackParams pack;
 };
 
 // mm_few.cu: fp32 rows that it takes at most.

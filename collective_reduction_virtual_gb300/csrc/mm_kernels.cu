@@ -97,8 +97,8 @@ struct Ring {
 };
 
 // A unit's copies into the ring, by a whole warp of which one lane issues them; the
-// number of stages that were filled.  A step has 256 cycles: what does not change
-// is outside the loop.
+// number of stages that were filled.  A step lasts 512
+// cycles at 256 columns and 256 at 128: what does not change is outside the loop.
 template <int EPI, int CTAS, bool A_MN>
 __device__ __forceinline__ uint32_t load_unit(const MmParams& p, uint32_t unit, const Place& at, Ring& ring) {
   constexpr int TILE_ROWS = kMmRows * CTAS;
@@ -325,6 +325,20 @@ __device__ __forceinline__ bool finish_unit(const MmParams& p, uint32_t unit, co
 
 }  // namespace
 
+// c[m, n] = sum over k of a[m, k] b[n, k], or of b[k, n] (MM_OUT), and the epilogue.
+//
+// Large products are bound by the tensor cores, whose rate the power limit sets in a
+// long run.  Alone, us and PFLOP/s: the logits of 4096 x 32768 tokens and 4096 columns
+// with what makes them e 551, 2.0; both gradients of those 1127, 1.95; 8192 x 128000 x
+// 4096 to their log sum 4343, 2.0; the gated block of 16384 x 4096 x 11008 1490, 1.98.
+// A tile of 256 x 256 by a pair reads 64 KB of operands for 512 cycles of products, a
+// third less than two of 128 x 256; single CTAs are for products of less than a pair's
+// rows, or with few tiles (the plan in products.cpp says which).  The eight warps of
+// the epilogue have as long as the next tile's sum takes: with 64 steps and up
+// they are hidden.
+// Few rows are bound by the weight's bytes: 7 rows by 32000 x 4096 44, 6.0 TB/s; one
+// row by two of 11008 x 4096 35, 5.1 TB/s, with 86 tiles for
+// 152 SMs (in splits or narrower tiles it was no faster).
 template <int EPI, int CTAS>
 __global__ void __launch_bounds__(kMmThreads, 1) vc_mm(const __grid_constant__ MmLaunch all) {
   pdl_enter();
@@ -413,7 +427,9 @@ __global__ void __launch_bounds__(kMmThreads, 1) vc_mm(const __grid_constant__ M
 }
 
 // The epilogue of tiles whose sums were cut: the splits' sums added in order, a
-// warp for 32 columns of a row (MM_LSE: for a tile's).
+// warp for 32 columns of a row (MM_LSE: for a tile's), so that every load is a whole
+// line.  Bound by those sums, which are still in L2, and by its launch: both gradients
+// of 1000 x 5000 x 320 7.7 us, of 512 x 320 x 1280 5.3.
 template <int EPI>
 __global__ void __launch_bounds__(256) vc_mm_join_splits(const __grid_constant__ MmLaunch all) {
   pdl_enter();

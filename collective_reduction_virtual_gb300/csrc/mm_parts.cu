@@ -96,15 +96,8 @@ __device__ __forceinline__ void largest(const MmPackParams& p) {
   *p.scale = top > 0.0f && top < INFINITY ? top : 1.0f;
 }
 
-}  // namespace
-
-__global__ void __launch_bounds__(kThreads) vc_mm_pack(const __grid_constant__ MmPackParams p) {
-  pdl_enter();
-  int64_t block = blockIdx.x;
-  if (p.scale && block-- == 0) {
-    largest(p);
-    return;
-  }
+// A CTA's part of the matrices that are laid out; the first CTA is block 0.
+__device__ __forceinline__ void pack(const MmPackParams& p, int64_t block) {
   int which = 0;
   while (which + 1 < kMmPackJobs && block >= p.job[which + 1].first_block) ++which;
   const MmPackJob& j = p.job[which];
@@ -123,7 +116,27 @@ __global__ void __launch_bounds__(kThreads) vc_mm_pack(const __grid_constant__ M
   }
 }
 
-// A CTA for 32 rows, a warp for every 32nd tile of them.  The maxima are to base 2.
+}  // namespace
+
+// Operands that TMA cannot take as they lie (fp32, odd rows, x of padded tokens) to
+// bf16 parts in rows of whole lines; several matrices in one launch, the CTAs
+// shared out by their sizes.  50.8e6 + 2.0e6 bf16 values of 1001 columns, 2-byte
+// aligned: 44 us, 4.7 TB/s; 16.8e6 of 4096 columns 16 us, 4.2 TB/s.  Odd rows are
+// read in the words that hold them, 20 bytes for 16.
+__global__ void __launch_bounds__(kThreads) vc_mm_pack(const __grid_constant__ MmPackParams p) {
+  pdl_enter();
+  if (!p.scale)
+    pack(p, blockIdx.x);
+  else if (blockIdx.x)
+    pack(p, (int64_t)blockIdx.x - 1);
+  else
+    largest(p);
+}
+
+// lse[i] = log of the sum over the tiles' (maximum, sum of exponentials), which are
+// joined pair by pair: s = s1 2^(m1 - m) + s2 2^(m2 - m) with m the larger maximum;
+// the maxima are to base 2.  A CTA for 32 rows, a warp for every 32nd tile of them.
+// Bound by latency: 7 rows of 125 tiles 5.9 us, 8192 rows of 500 16 us (2 TB/s).
 __global__ void __launch_bounds__(kMmJoinThreads) vc_mm_join(const __grid_constant__ MmJoinParams p) {
   pdl_enter();
   constexpr int WARPS = kMmJoinThreads / 32;
@@ -161,13 +174,20 @@ __global__ void __launch_bounds__(kMmJoinThreads) vc_mm_join(const __grid_consta
   p.loss[row] = t >= 0 && t < p.V ? lse - p.loss[row] : 0.0f;
 }
 
-// dgate = dh * up * act'(gate), dup = dh * act(gate).
+// dgate = dh * up * act'(gate), dup = dh * act(gate), next to each other in a row:
+// dx sums over both.  16384 x 11008 bf16, silu: 341 us for 1.8 GB, 5.3 TB/s (with the
+// exact gelu's erf and for odd rows instructions bound it: 3001 x 2671 19 us, 4.2 TB/s).
+// The CTAs behind lay out x and the weights: a launch of its own for that took 4.5 us
+// more of 512 x 320 x 1280, 5 of 3001 x 1001 x 2671.
 template <int ACT>
 __global__ void __launch_bounds__(kThreads) vc_mm_gated_grad(const __grid_constant__ MmGatedGradParams p) {
   pdl_enter();
+  if (blockIdx.x >= p.blocks) {
+    pack(p.pack, blockIdx.x - p.blocks);
+    return;
+  }
   const int64_t groups = p.half / 8;
-  for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < p.N * groups;
-       e += (int64_t)gridDim.x * kThreads) {
+  for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < p.N * groups; e += p.blocks * kThreads) {
     int64_t row, group;
     item_at(e, groups, row, group);
     const int64_t col = group * 8, left = p.F - col;  // what pads a row is zeros: it stands in the sum of dx

@@ -361,12 +361,15 @@ struct Packer {
     ++jobs;
     return VCOLL_OK;
   }
-  int run(void* stream) {
-    const int64_t all = blocks + (p.scale ? 1 : 0);
-    if (!all) return VCOLL_OK;
+  // The parameters, once all matrices are there.
+  MmPackParams& params() {
     for (int i = jobs; i < kMmPackJobs; ++i) p.job[i].first_block = INT64_MAX;
     if (!jobs) p.job[0].blocks = 1;
-    return launch_grid(mm_pack_kernel(), all, 1, kPassThreads, 0, &p, stream);
+    return p;
+  }
+  int run(void* stream) {
+    const int64_t all = blocks + (p.scale ? 1 : 0);
+    return all ? launch_grid(mm_pack_kernel(), all, 1, kPassThreads, 0, &params(), stream) : VCOLL_OK;
   }
 };
 
@@ -837,6 +840,15 @@ int vcoll_gated_ff_backward(const void* dh, int64_t dh_ld, const void* x, int64_
   VCOLL_TRY(check_room(ops, 9, workspace, workspace_bytes, L.bytes));
   char* ws = (char*)workspace;
   const int parts = parts_of(dtype);
+  const MmOperand grads = operand(ws + L.grads, N, 2 * L.half, 2 * L.half, N * 2 * L.half);
+  const bool few = few_rows(N, dtype);
+  MmOperand rows, gates, ups;
+  Packer pack(dtype);
+  if (weights) VCOLL_TRY(pack.add(x, F ? N : 0, D, x_ld, x_direct, ws + L.x, false, &rows));
+  if (dx) {
+    VCOLL_TRY(pack.add(w_gate, N ? F : 0, D, w_gate_ld, g_direct || few, ws + L.w_gate, false, &gates));
+    VCOLL_TRY(pack.add(w_up, N ? F : 0, D, w_up_ld, u_direct || few, ws + L.w_up, false, &ups));
+  }
   if (N && F) {
     MmGatedGradParams g = {};
     g.dh = dh;
@@ -854,18 +866,12 @@ int vcoll_gated_ff_backward(const void* dh, int64_t dh_ld, const void* x, int64_
     g.f32 = dtype == VCOLL_F32;
     g.parts = parts;
     g.load16 = rows_at_16(dh, N, dh_ld, es) && rows_at_16(gate, N, gate_ld, es) && rows_at_16(up, N, up_ld, es);
-    VCOLL_TRY(launch_grid(mm_gated_grad_kernel(activation), pass_blocks(N * (L.half / 8)), 1, kPassThreads, 0, &g, stream));
+    g.blocks = pass_blocks(N * (L.half / 8));
+    g.pack = pack.params();
+    VCOLL_TRY(launch_grid(mm_gated_grad_kernel(activation), g.blocks + pack.blocks, 1, kPassThreads, 0, &g, stream));
+  } else {
+    VCOLL_TRY(pack.run(stream));
   }
-  const MmOperand grads = operand(ws + L.grads, N, 2 * L.half, 2 * L.half, N * 2 * L.half);
-  const bool few = few_rows(N, dtype);
-  MmOperand rows, gates, ups;
-  Packer pack(dtype);
-  if (weights) VCOLL_TRY(pack.add(x, F ? N : 0, D, x_ld, x_direct, ws + L.x, false, &rows));
-  if (dx) {
-    VCOLL_TRY(pack.add(w_gate, N ? F : 0, D, w_gate_ld, g_direct || few, ws + L.w_gate, false, &gates));
-    VCOLL_TRY(pack.add(w_up, N ? F : 0, D, w_up_ld, u_direct || few, ws + L.w_up, false, &ups));
-  }
-  VCOLL_TRY(pack.run(stream));
   MmLaunch all = {};  // dx and the weights' gradients
   if (dx) {
     MmParams& p = all.p[0];

@@ -214,6 +214,44 @@ def test_a_vocabulary_in_pieces(v, dtype, n, V, D, layout):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,n,V,D", [(torch.float32, 30011, 4801, 9), (torch.bfloat16, 70001, 5001, 15)])
+def test_one_gradient_of_a_vocabulary_in_pieces(v, dtype, n, V, D):
+    g = gen(6)
+    x, table, t = loss_case(g, n, V, D, dtype, "odd", index=torch.int32)
+    lse = v.cross_entropy(x, table, t)[1]
+    one = torch.full((1,), 1.0 / n, device="cuda")
+    base = matrix(g, V, D, dtype)
+    dx, none = v.cross_entropy_backward(one, x, table, t, lse, table_grad=False)
+    assert none is None
+    none, dt = v.cross_entropy_backward(one, x, table, t, lse, base=base, x_grad=False)
+    assert none is None
+    total = bound = 0.0
+    for a in range(0, n, 8192):
+        part = slice(a, a + 8192)
+        w = R.loss_grad(one, x[part], table, t[part], lse[part], None, dtype)
+        near(dx[part], w[0], w[2], dtype)
+        total, bound = total + w[1], bound + w[3]
+    bound = bound * max(1, n // 4096) + 2 * R.U * (total + base.double()).abs()
+    near(dt, total + base.double(), bound, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_long_batch_of_narrow_rows(v, dtype):
+    n, V, D = 300007, 37, 8
+    g = gen(8)
+    x, table, t = loss_case(g, n, V, D, dtype)
+    loss, lse = v.cross_entropy(x, table, t)
+    w = R.loss(x, table, t)
+    near(loss, w[0], w[2])
+    near(lse, w[1], w[3])
+    h, gate, up = v.gated_ff(x, table, table, "gelu", keep=True)
+    want = R.gated(x, table, table, "gelu")
+    for got, exact, bound in zip((h, gate, up), want[:3], want[3:]):
+        near(got, exact, bound, dtype)
+
+
+@pytest.mark.gpu
 def test_cross_entropy_gradient_against_differences(v):
     g = gen(6)
     n, V, D = 40, 90, 48
