@@ -42,6 +42,7 @@ struct MmParams {
   int b_halves;   // the tile's columns are half b[0]'s and half b[1]'s (MM_GATED)
   int tn;         // columns of a tile
   uint32_t tiles_m, tiles_n;
+  uint32_t group;     // rows of tiles that are taken column after column
   int tile_rows;      // 128, or 256 of a pair of CTAs
   int warp_rows;      // that a warp's epilogue has at most: 32, or all of a few
   int a_rows;         // of a stage's a: 128, or fewer where M is smaller

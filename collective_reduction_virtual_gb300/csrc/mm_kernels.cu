@@ -20,10 +20,10 @@ namespace vcoll {
 
 namespace {
 
-// Tiles in groups of 2048 rows: the tiles that are in flight together share their
-// operands through the L2.
-__device__ __forceinline__ void tile_at(const MmParams& p, int tile_rows, uint32_t tile, uint32_t& m, uint32_t& n) {
-  const uint32_t group = 2048 / tile_rows, per = group * p.tiles_n;
+// Tiles in groups of rows, column after column: the tiles that are in flight together
+// share their operands through the L2.
+__device__ __forceinline__ void tile_at(const MmParams& p, uint32_t tile, uint32_t& m, uint32_t& n) {
+  const uint32_t group = p.group, per = group * p.tiles_n;
   const uint32_t g = tile / per, in = tile - g * per;
   const uint32_t rows = p.tiles_m - g * group < group ? p.tiles_m - g * group : group;
   n = in / rows;
@@ -111,7 +111,7 @@ __device__ __forceinline__ uint32_t load_unit(const MmParams& p, uint32_t unit, 
   const uint32_t second = B_MN ? (uint32_t)(p.K1 / kMmDepth) : 0;  // the first step that takes map_b[1]
   uint32_t tile, tm, tn, k, done = 0;
   steps_of(p, unit, tile, k);
-  tile_at(p, TILE_ROWS, tile, tm, tn);
+  tile_at(p, tile, tm, tn);
   const int row = (int)(tm * TILE_ROWS + at.rank * kMmRows);
   const int col = EPI == MM_GATED ? (int)(tn * (p.tn / 2)) : (int)(tn * p.tn + at.rank * cols);
   const CUtensorMap *map_a = &p.map_a, *map_b = EPI == MM_GATED && CTAS == 2 && at.rank ? &p.map_b[1] : &p.map_b[0];
@@ -261,7 +261,7 @@ __device__ __forceinline__ Share share_of(const MmParams& p, uint32_t unit, cons
   s.c1 = s.c0 < p.tn ? s.c0 + width : s.c0;
   uint32_t tile, tm;
   s.steps = steps_of(p, unit, tile, s.split);
-  tile_at(p, kMmRows * CTAS, tile, tm, s.tn);
+  tile_at(p, tile, tm, s.tn);
   s.in_tile = (int)at.rank * kMmRows + warp % 4 * 32;  // of tensor memory a warp reads a quarter
   s.row0 = (int64_t)tm * kMmRows * CTAS + s.in_tile;
   return s;
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(256) vc_mm_join_splits(const __grid_constant__
   const int64_t r = w / chunks % rows, tile = w / chunks / rows;
   if (tile >= (int64_t)p.tiles_m * p.tiles_n) return;
   uint32_t tm, tn;
-  tile_at(p, tile_rows, (uint32_t)tile, tm, tn);
+  tile_at(p, (uint32_t)tile, tm, tn);
   const int64_t row = (int64_t)tm * tile_rows + r;
   if (row >= p.M) return;
   const float* from = p.partial + (tile * p.splits * rows + r) * p.tn;

@@ -402,6 +402,32 @@ int encode(CUtensorMap* map, const MmOperand& o, int parts, int box) {
   return VCOLL_OK;
 }
 
+// Rows that tiles are taken by, column after column: as many as stay in L2 meanwhile
+// (kGroupBytes of a), so that b is read once for each group of them.  Where the sums
+// are too long for that, 2048 rows make what is in flight about as high as wide.
+// 8192 x 128000 x 4096 to the loss, us: 4930 with 1024 rows, 4735 with 2048, 4650 with
+// 4096 (this rule's) and 4815 with 8192; sums of 16384 and 22016 places (the block's
+// gradient): 3870, 3805 and 3930 with 1024, 2048 and 4096.
+constexpr int64_t kGroupBytes = 40 << 20;
+int64_t group_rows(int64_t K, int parts) {
+  int64_t rows = 2048;
+  while (rows < 8192 && 2 * rows * K * 2 * parts <= kGroupBytes) rows *= 2;
+  return rows;
+}
+
+// Two products fill each other's last waves in one launch.  But their tiles then do
+// not run in step, and where both sums are long, more of their operands lies between
+// them than L2 holds (12.3 GB read from memory instead of 8.1 with 16384 rows): those
+// take a launch each, where each has a wave of tiles at least.  The block's gradient,
+// us in one launch and in two, N x D, F: 16384 x 4096, 11008 4000 and 3795; 12288 x
+// 8192, 16384 8830 and 8340; 9000 x 1024, 8500 521 and 514; with shorter sums, 4096 x
+// 4096, 11008 930 and 964.
+constexpr int64_t kLongSums = 8192;
+bool apart(const MmParams& a, const MmParams& b) {
+  const int64_t wave = kPlanSms / 2 * kMmTileN * 2 * kMmRows;
+  return std::min(a.K, b.K) >= kLongSums && std::min(a.M * a.N, b.M * b.N) >= wave;
+}
+
 // The launch's tiles and their epilogues; partial: the room that the plan's splits
 // need.
 int products(MmEpilogue epilogue, MmLaunch* all, void* partial, void* stream) {
@@ -429,6 +455,7 @@ int products(MmEpilogue epilogue, MmLaunch* all, void* partial, void* stream) {
     p->splits = plan.of[i].splits;
     p->partial = (float*)((char*)partial + (i ? align256(plan.of[0].bytes) : 0));
     p->tile_rows = kMmRows * plan.ctas;
+    p->group = (uint32_t)(group_rows(p->K, p->parts) / p->tile_rows);
     const int64_t tiles_m = ceil_div(p->M, p->tile_rows), tiles_n = ceil_div(p->N, p->b_halves ? p->tn / 2 : p->tn);
     if (tiles_m > 0x3FFFFFFF / tiles_n)
       return fail(VCOLL_ERR_UNSUPPORTED, "%lld x %lld tiles are too many", (long long)tiles_m, (long long)tiles_n);
@@ -493,7 +520,7 @@ int few_product(MmEpilogue epilogue, MmLaunch* all, void* partial, void* stream)
   p->splits = (uint32_t)few_splits(p->N, p->K);
   p->partial = (float*)partial;
   p->tile_rows = kMmRows;
-  p->tiles_m = 1;
+  p->tiles_m = p->group = 1;
   p->tiles_n = (uint32_t)ceil_div(p->N, 128);
   p->join_blocks = (uint32_t)ceil_div((int64_t)p->tiles_n * p->M * 4, 8);
   VCOLL_TRY(launch_grid(fn, p->tiles_n, p->splits, kMmFewColThreads, 0, all, stream));
@@ -513,6 +540,12 @@ int few_outer(MmLaunch* all, void* stream) {
 
 // The launch's products on the units that suit them.
 int run(MmEpilogue epilogue, bool few, MmLaunch* all, void* partial, void* stream) {
+  if (!few && apart(all->p[0], all->p[1])) {
+    MmLaunch first = *all;
+    first.p[1].M = 0;
+    all->p[0].M = 0;
+    VCOLL_TRY(products(epilogue, &first, partial, stream));
+  }
   if (!few) return products(epilogue, all, partial, stream);
   VCOLL_TRY(few_product(epilogue, all, partial, stream));
   return few_outer(all, stream);
