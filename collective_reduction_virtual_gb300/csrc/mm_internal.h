@@ -37,7 +37,7 @@ struct MmParams {
   int64_t M, N;   // of a tile space: rows and columns of the result
   int64_t K;      // length of the sum
   int64_t K1;     // the sum's places from here on take b[1] (K: none)
-  int parts;      // 1, or 3: six products of the parts
+  int parts;      // of each operand: 1, or 3 in six products; 2: of a alone
   uint32_t depth;  // steps of kMmDepth places
   int b_halves;   // the tile's columns are half b[0]'s and half b[1]'s (MM_GATED)
   int tn;         // columns of a tile
@@ -95,9 +95,9 @@ struct MmLaunch {
 
 // The six products of three parts that reach an fp32 result's precision, the
 // small ones first: parts 0 and 2, 2 and 0, 1 and 1, 0 and 1, 1 and 0, 0 and 0.
-VCOLL_HD constexpr int mm_pairs(int parts) { return parts == 1 ? 1 : 6; }
-VCOLL_HD constexpr int mm_pair_a(int pairs, int q) { return pairs == 1 ? 0 : (0x010120 >> (4 * q)) & 15; }
-VCOLL_HD constexpr int mm_pair_b(int pairs, int q) { return pairs == 1 ? 0 : (0x001102 >> (4 * q)) & 15; }
+VCOLL_HD constexpr int mm_pairs(int parts) { return parts == 3 ? 6 : parts; }
+VCOLL_HD constexpr int mm_pair_a(int pairs, int q) { return pairs < 6 ? pairs - 1 - q : (0x010120 >> (4 * q)) & 15; }
+VCOLL_HD constexpr int mm_pair_b(int pairs, int q) { return pairs < 6 ? 0 : (0x001102 >> (4 * q)) & 15; }
 
 // Geometry of the tiles.  A CTA has 128 rows of a tile and at most 256 columns;
 // one CTA, or two that share their columns' operand, take a tile.  64 places of
@@ -110,7 +110,8 @@ constexpr int kMmRows = 128;
 // fp32 adders 6.6e-7.  Of three parts' products only the last and largest is cut.
 // What is rounded to bf16 in the end may drift by 3e-5 in 32768 places, a hundredth
 // of that rounding.
-constexpr uint32_t kMmChunkLoss = 16, kMmChunkParts = 8, kMmChunkBf16 = 512;
+// Rows of one tile wait for memory anyway: their loss takes chunks of 256 places.
+constexpr uint32_t kMmChunkLoss = 16, kMmChunkFew = 4, kMmChunkParts = 8, kMmChunkBf16 = 512;
 constexpr uint32_t kMmChunkMost = 1 << 16;  // some 20 ms, far below what a wait may take
 constexpr int kMmTileN = 256;
 constexpr int kMmDepth = 64;

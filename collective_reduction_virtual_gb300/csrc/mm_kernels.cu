@@ -73,7 +73,7 @@ __device__ __forceinline__ uint32_t steps_of(const MmParams& p, uint32_t unit, u
 
 // Steps of a unit's first chunk: the small ones of the parts' products together.
 __device__ __forceinline__ uint32_t first_chunk(const MmParams& p, uint32_t split) {
-  if (p.parts == 1) return p.chunk;
+  if (p.parts < 3) return p.chunk;
   const uint32_t small = ((mm_pairs(p.parts) - 1) * p.depth - split + p.splits - 1) / p.splits;
   return small < kMmChunkMost ? small : kMmChunkMost;
 }

@@ -27,6 +27,12 @@ constexpr int64_t kPlanSms = 152;
 
 int64_t round_up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
 int parts_of(int dtype) { return dtype == VCOLL_F32 ? 3 : 1; }
+// Of the gradients of gate and up.  Rounded to one bf16 they make bf16 results off by
+// 1.4 times their own rounding, and where there are few of them, by chance by up to 1.6
+// times: those take two parts, which costs nothing there (1 x 1024, 4096: 29 us either
+// way; with 1 x 4096, 11008 it would be 97 and 152).
+constexpr int64_t kFineValues = 8192;
+int grad_parts(int64_t N, int64_t F, int dtype) { return dtype == VCOLL_F32 ? 3 : N * F <= kFineValues ? 2 : 1; }
 
 // Regions of a workspace, one after the other.
 struct Regions {
@@ -54,7 +60,7 @@ struct Shape {
 };
 // Measured on tiles of little depth: 64 columns of bf16 at once, 32 of fp32 (or its
 // parts), and those whose rows something is added to, which is waited for.
-int epilogue_cycles(int parts, bool add = false) { return add ? 40 : parts > 1 ? 40 : 12; }
+int epilogue_cycles(int parts, bool add = false) { return add ? 40 : parts > 2 ? 40 : 12; }
 
 // How a launch's products are cut: CTAs that share a tile, and for each product the
 // tile's columns, the splits of its sum, and a unit's cycles.
@@ -277,15 +283,16 @@ GatedLayout gated_layout(int64_t N, int64_t D, int64_t F, int dtype, bool direct
   const bool few = few_rows(N, dtype);
   L.w_gate = r.take(direct || few ? 0 : packed_bytes(F, D, parts));
   L.w_up = r.take(direct || few ? 0 : packed_bytes(F, D, parts));
-  L.grads = r.take(backward ? packed_bytes(N, 2 * L.half, parts) : 0);
+  const int fine = grad_parts(N, F, dtype);
+  L.grads = r.take(backward ? packed_bytes(N, 2 * L.half, fine) : 0);
   size_t splits = 0;
   const int cycles = epilogue_cycles(parts);
   if (few) {
     splits = backward ? few_bytes(N, D, 2 * L.half) : 0;
   } else if (backward) {  // dx; one weight's gradient; both
-    const Shape s[3] = {{N, D, 2 * L.half, parts, false, cycles},
-                        {F, D, N, parts, false, cycles},
-                        {2 * L.half, D, N, parts, false, cycles}};
+    const Shape s[3] = {{N, D, 2 * L.half, fine, false, cycles},
+                        {F, D, N, fine, false, cycles},
+                        {2 * L.half, D, N, fine, false, cycles}};
     const Shape one[2] = {s[0], s[1]}, both[2] = {s[0], s[2]};
     splits = std::max({plan_of(s[0]).bytes(), plan_of(s[1]).bytes(), plan_of(s[2]).bytes(), make_plan(one, 2).bytes(),
                        make_plan(both, 2).bytes()});
@@ -465,7 +472,7 @@ int products(MmEpilogue epilogue, MmLaunch* all, void* partial, void* stream) {
     units += p->units;
     p->warp_rows = 32;
     p->depth = (uint32_t)ceil_div(p->K, kMmDepth);
-    p->chunk = p->parts > 1 ? kMmChunkParts : epilogue == MM_LSE ? kMmChunkLoss : kMmChunkBf16;
+    p->chunk = p->parts > 2 ? kMmChunkParts : epilogue == MM_LSE ? (p->M > kMmRows ? kMmChunkLoss : kMmChunkFew) : kMmChunkBf16;
     p->a_rows = a_mn || plan.ctas == 2 ? kMmRows : (int)std::min<int64_t>(kMmRows, round_up(p->M, 8));
     all->stage_bytes = std::max(all->stage_bytes, (p->a_rows + p->tn / plan.ctas) * kMmDepth * 2);
     const bool second = p->b[1].p && !p->b_halves;
@@ -473,8 +480,9 @@ int products(MmEpilogue epilogue, MmLaunch* all, void* partial, void* stream) {
     if (p->K) {
       VCOLL_TRY(encode(&p->map_a, p->a, p->parts, a_mn ? kMmDepth : p->a_rows));
       const int box = b_mn ? kMmDepth : p->b_halves ? p->tn / 2 : p->tn / plan.ctas;
-      VCOLL_TRY(encode(&p->map_b[0], p->b[0], p->parts, box));
-      if (second || p->b_halves) VCOLL_TRY(encode(&p->map_b[1], p->b[1], p->parts, box));
+      const int parts = p->parts == 3 ? 3 : 1;
+      VCOLL_TRY(encode(&p->map_b[0], p->b[0], parts, box));
+      if (second || p->b_halves) VCOLL_TRY(encode(&p->map_b[1], p->b[1], parts, box));
     }
     if (p->splits > 1) {
       const int64_t chunks = epilogue == MM_LSE ? 1 : (p->b_halves ? p->tn / 2 : p->tn) / 32;
@@ -872,7 +880,7 @@ int vcoll_gated_ff_backward(const void* dh, int64_t dh_ld, const void* x, int64_
   const GatedLayout L = gated_layout(N, D, F, dtype, x_direct && g_direct && u_direct, true);
   VCOLL_TRY(check_room(ops, 9, workspace, workspace_bytes, L.bytes));
   char* ws = (char*)workspace;
-  const int parts = parts_of(dtype);
+  const int parts = grad_parts(N, F, dtype);
   const MmOperand grads = operand(ws + L.grads, N, 2 * L.half, 2 * L.half, N * 2 * L.half);
   const bool few = few_rows(N, dtype);
   MmOperand rows, gates, ups;

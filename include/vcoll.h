@@ -540,7 +540,7 @@ int vcoll_gated_ff(const void* x, int64_t x_ld, const void* w_gate, int64_t w_ga
  * Its gradient from the kept gate and up: dgate = dh * up * act'(gate), dup =
  * dh * act(gate), dx = dgate * w_gate + dup * w_up, dw_gate = dgate^T * x,
  * dw_up = dup^T * x.  With bf16 operands dgate and dup are rounded to bf16 for
- * the products.  dx, dw_gate and dw_up may each be NULL (not wanted).
+ * the products, or where N * F is 8192 or less to twice its bits.  dx, dw_gate and dw_up may each be NULL (not wanted).
  */
 size_t vcoll_gated_ff_backward_workspace_bytes(int64_t N, int64_t D, int64_t F, int dtype,
                                                int direct);

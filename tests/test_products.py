@@ -327,6 +327,27 @@ def test_gated_ff_backward(v, dtype, n, D, F, layout, act):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 2, 7])
+@pytest.mark.parametrize("D,F,layout", [(72, 200, "dense"), (129, 67, "odd"), (640, 1030, "slice")])
+def test_gradients_of_a_few_bf16_rows_round_once(v, n, D, F, layout):
+    # dgate and dup hold 16 bits: what they lose is 2^-8 of a rounding to bf16
+    bf = torch.bfloat16
+    g = gen(n + D)
+    x, wg, wu = gated_case(g, n, D, F, bf, layout)
+    dh, gate, up = (matrix(g, n, F, bf, layout) for _ in range(3))
+    got = v.gated_ff_backward(dh, x, wg, wu, gate, up, "silu")
+    exact = R.gated_grad(dh, x, wg, wu, gate, up, "silu", torch.float32)
+    rounded = R.gated_grad(dh, x, wg, wu, gate, up, "silu", bf)
+    for one, want, fine, coarse in zip(got, exact[:3], exact[3:], rounded[3:]):
+        near(one, want, fine + (coarse - fine) * 2.0 ** -8, bf)
+    for skip in ({"x_grad": False}, {"weight_grads": False}):
+        for one, want, fine, coarse in zip(v.gated_ff_backward(dh, x, wg, wu, gate, up, "silu", **skip),
+                                           exact[:3], exact[3:], rounded[3:]):
+            if one is not None:
+                near(one, want, fine + (coarse - fine) * 2.0 ** -8, bf)
+
+
+@pytest.mark.gpu
 def test_gated_ff_of_nothing(v):
     for dtype in TYPES:
         x, wg, wu = gated_case(gen(7), 6, 40, 50, dtype, "dense")
