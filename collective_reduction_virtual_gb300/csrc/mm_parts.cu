@@ -71,12 +71,10 @@ __device__ __forceinline__ void store8(void* dst, int64_t i, int64_t plane, int 
 #pragma unroll
   for (int j = 0; j < 8; ++j) mm_parts(v[j], q[j]);
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    if (k == parts) break;
+  for (int k = 0; k < 3; ++k)
     *reinterpret_cast<uint4*>(to + k * plane) =
         make_uint4(q[0][k] | (uint32_t)q[1][k] << 16, q[2][k] | (uint32_t)q[3][k] << 16,
                    q[4][k] | (uint32_t)q[5][k] << 16, q[6][k] | (uint32_t)q[7][k] << 16);
-  }
 }
 
 // The largest magnitude of dloss over the rows that count, by one CTA; 1 where it

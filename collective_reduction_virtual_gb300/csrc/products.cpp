@@ -284,7 +284,7 @@ GatedLayout gated_layout(int64_t N, int64_t D, int64_t F, int dtype, bool direct
   L.w_gate = r.take(direct || few ? 0 : packed_bytes(F, D, parts));
   L.w_up = r.take(direct || few ? 0 : packed_bytes(F, D, parts));
   const int fine = grad_parts(N, F, dtype);
-  L.grads = r.take(backward ? packed_bytes(N, 2 * L.half, fine) : 0);
+  L.grads = r.take(backward ? packed_bytes(N, 2 * L.half, fine > 1 ? 3 : 1) : 0);  // two parts are laid out as three
   size_t splits = 0;
   const int cycles = epilogue_cycles(parts);
   if (few) {
