@@ -247,10 +247,14 @@ struct ChunkSum {
 };
 
 // What a warp has of a unit: 32 rows, and half of the columns, where a half has 64 of
-// them.
+// them.  In tensor memory these lie as two runs of `run` columns: of a gated tile,
+// whose first half is gate's and whose second is up's, as many of each.  What the
+// unit's sums go through in tensor memory is the warp's own runs and nothing else,
+// since no barrier is between the warps.
 struct Share {
   uint32_t tn, split, steps;
   int c0, c1, in_tile;
+  int run0, run1, run;
   int64_t row0;
 };
 template <int EPI, int CTAS>
@@ -259,6 +263,9 @@ __device__ __forceinline__ Share share_of(const MmParams& p, uint32_t unit, cons
   const int width = p.tn >= (EPI == MM_GATED ? 256 : 128) ? p.tn / 2 : p.tn;
   s.c0 = warp / 4 * width;
   s.c1 = s.c0 < p.tn ? s.c0 + width : s.c0;
+  s.run = (s.c1 - s.c0) / 2;
+  s.run0 = EPI == MM_GATED ? s.c0 / 2 : s.c0;
+  s.run1 = EPI == MM_GATED ? p.tn / 2 + s.c0 / 2 : s.c0 + s.run;
   uint32_t tile, tm;
   s.steps = steps_of(p, unit, tile, s.split);
   tile_at(p, tile, tm, s.tn);
@@ -282,19 +289,17 @@ __device__ __forceinline__ bool finish_unit(const MmParams& p, uint32_t unit, co
   uint32_t chunk = first_chunk(p, split);
   if (left > chunk) {
     ChunkSum s = {};
-    // in a gated tile a warp's columns are as many of gate's and of up's
-    const int run0 = EPI == MM_GATED ? c0 / 2 : c0, run1 = EPI == MM_GATED ? p.tn / 2 + c0 / 2 : c0 + (c1 - c0) / 2;
     for (; left > chunk; left -= chunk, chunk = p.chunk, ++turn) {
       if (!mm_warp_wait(at.acc_full + 8 * (turn & 1), (turn >> 1) & 1, at.guard)) return false;
       mm_fence_after();
-      s.take<true>(lanes + (turn & 1) * kMmTileN, run0, run1, (c1 - c0) / 16);
+      s.take<true>(lanes + (turn & 1) * kMmTileN, mine.run0, mine.run1, mine.run / 8);
       mm_fence_before();
       __syncwarp();
       release<CTAS>(at, turn);
     }
     if (!mm_warp_wait(at.acc_full + 8 * (turn & 1), (turn >> 1) & 1, at.guard)) return false;
     mm_fence_after();
-    s.take<false>(lanes + (turn & 1) * kMmTileN, run0, run1, (c1 - c0) / 16);
+    s.take<false>(lanes + (turn & 1) * kMmTileN, mine.run0, mine.run1, mine.run / 8);
   } else {
     if (!mm_warp_wait(at.acc_full + 8 * (turn & 1), (turn >> 1) & 1, at.guard)) return false;
     mm_fence_after();
@@ -309,7 +314,8 @@ __device__ __forceinline__ bool finish_unit(const MmParams& p, uint32_t unit, co
   }
   const int64_t rows = p.M < TILE_ROWS ? p.M : TILE_ROWS;
   float4* to = reinterpret_cast<float4*>(p.partial + (unit * rows + in_tile + lane) * p.tn);
-  for (int c = c0; c < c1; c += 32) {
+  for (int i = 0; i < 2 * mine.run; i += 32) {
+    const int c = i < mine.run ? mine.run0 + i : mine.run1 + i - mine.run;
     float x[32];
     src(c, x);
     if (row0 + lane < p.M) {
