@@ -33,18 +33,25 @@ template <bool WIDE>
 constexpr int kFirst = WIDE ? 4 : 1;  // places between lanes
 template <bool WIDE>
 constexpr int kNext = WIDE ? 1 : 32;  // and between a lane's four
-template <bool WIDE>
+// A value of what nothing writes meanwhile (FIXED: the weights), or of what the same
+// kernel may write in place (base).
+template <bool FIXED>
+__device__ __forceinline__ float load1(const float* p) {
+  return FIXED ? __ldg(p) : *p;
+}
+template <bool WIDE, bool FIXED>
 __device__ __forceinline__ float4 load4(const float* p) {
-  if (!WIDE) return make_float4(__ldg(p), __ldg(p + 32), __ldg(p + 64), __ldg(p + 96));
+  if (!WIDE) return make_float4(load1<FIXED>(p), load1<FIXED>(p + 32), load1<FIXED>(p + 64), load1<FIXED>(p + 96));
   const uint4 q = ld_stream(p);
   return make_float4(__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z), __uint_as_float(q.w));
 }
 // The same from place `at` of a row of `count` values, zeros past its end.
-template <bool WIDE>
+template <bool WIDE, bool FIXED>
 __device__ __forceinline__ float4 load4_end(const float* row, int64_t at, int64_t count) {
-  if (WIDE) return at < count ? load4<true>(row + at) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  return make_float4(at < count ? __ldg(row + at) : 0.0f, at + 32 < count ? __ldg(row + at + 32) : 0.0f,
-                     at + 64 < count ? __ldg(row + at + 64) : 0.0f, at + 96 < count ? __ldg(row + at + 96) : 0.0f);
+  if (WIDE) return at < count ? load4<true, FIXED>(row + at) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  return make_float4(at < count ? load1<FIXED>(row + at) : 0.0f, at + 32 < count ? load1<FIXED>(row + at + 32) : 0.0f,
+                     at + 64 < count ? load1<FIXED>(row + at + 64) : 0.0f,
+                     at + 96 < count ? load1<FIXED>(row + at + 96) : 0.0f);
 }
 
 // The warp's sums of N values: those from lane * N / 32 on, N / 32 of them but one at
@@ -112,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) vc_mm_few_rows(const __grid_constant
     float4 v;
     if (WIDE) {
       const bool in = at < p.K;
-      v = load4<true>(in ? row + at : row);
+      v = load4<true, true>(in ? row + at : row);
       if (!in) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     } else {
       const bool x = at < p.K, y = at + 32 < p.K, z = at + 64 < p.K, u = at + 96 < p.K;
@@ -202,13 +209,13 @@ __global__ void __launch_bounds__(kColThreads, 2) vc_mm_few_cols(const __grid_co
 #pragma unroll
       for (int i = 0; i < FLIGHT; ++i) {
         const float* q = w + i * ld;
-        next[i] = WIDE ? load4<true>(q + from[0])
+        next[i] = WIDE ? load4<true, true>(q + from[0])
                        : make_float4(__ldg(q + from[0]), __ldg(q + from[1]), __ldg(q + from[2]), __ldg(q + from[3]));
       }
     } else {  // what pads a's first half has no row
 #pragma unroll
       for (int i = 0; i < FLIGHT; ++i)
-        next[i] = load4_end<WIDE>(w + i * ld, col, k + i < end && r + i < rows ? p.N : 0);
+        next[i] = load4_end<WIDE, true>(w + i * ld, col, k + i < end && r + i < rows ? p.N : 0);
     }
   };
   float acc[ROWS][4] = {};
@@ -307,11 +314,11 @@ __global__ void __launch_bounds__(kColThreads) vc_mm_few_outer(const __grid_cons
   const float* base = static_cast<const float*>(p.base);
   if (base && first + 8 <= end && col0 + 128 <= p.N) {
 #pragma unroll
-    for (int r = 0; r < 8; ++r) x[r] = load4<WIDE>(base + (first + r) * p.base_ld + col);
+    for (int r = 0; r < 8; ++r) x[r] = load4<WIDE, false>(base + (first + r) * p.base_ld + col);
   } else if (base && first < end) {
 #pragma unroll
     for (int r = 0; r < 8; ++r)
-      x[r] = load4_end<WIDE>(base + (first + r < end ? first + r : first) * p.base_ld, col, p.N);
+      x[r] = load4_end<WIDE, false>(base + (first + r < end ? first + r : first) * p.base_ld, col, p.N);
   }
 #pragma unroll
   for (int r = 0; r < 8; ++r) {

@@ -38,3 +38,13 @@ def test_launches_go_through_the_dependent_launch_helper():
     src = open(os.path.join(CSRC, "api.cpp")).read()
     plain = [ln.strip() for ln in src.splitlines() if "cudaLaunchKernel(" in ln]
     assert len(plain) == 1 and "selftest_timeout_kernel" in plain[0], plain
+
+
+def test_what_may_be_the_result_itself_is_not_read_as_constant():
+    # base may be dtable: the loads of it promise nothing about who writes it
+    src = open(os.path.join(CSRC, "mm_few.cu")).read()
+    start = src.index("vc_mm_few_outer(")
+    body = src[start:src.index("\n}\n", start)]
+    loads = re.findall(r"(__ldg|load\w*(?:<[^>]*>)?)\(", body)
+    loads = [name for name in loads if name.startswith(("__ldg", "load"))]
+    assert loads and all(name.endswith("false>") for name in loads), loads
