@@ -67,8 +67,9 @@ __device__ __forceinline__ void mm_parts(float x, uint16_t (&q)[3]) {
 }
 
 // The activations, g times a factor, and the factor's part in the derivative:
-// act = g * s, act' = s + g * ds.  The exact gelu takes erfcf where g < 0, since
-// 1 + erf loses the bits of a small result.
+// act = g * s, act' = s + g * ds, with what mm_low and mm_finite make of an infinite g.
+// The exact gelu takes erfcf where g < 0, since 1 + erf loses the bits of a small
+// result.  Where a factor has come to 0 or 1, ds is 0 whatever g * g is.
 __device__ __forceinline__ void mm_act(int act, float g, float& s, float& ds) {
   if (act == VCOLL_SILU) {
     s = mm_rcp(1.0f + mm_exp(-g));
@@ -79,9 +80,15 @@ __device__ __forceinline__ void mm_act(int act, float g, float& s, float& ds) {
   } else {  // (1 + tanh(t)) / 2 = 1 / (1 + e^(-2 t))
     const float c = 1.5957691216057308f;  // 2 sqrt(2 / pi)
     s = mm_rcp(1.0f + mm_exp(-c * (g + 0.044715f * g * g * g)));
-    ds = s * (1.0f - s) * c * (1.0f + 0.134145f * g * g);
+    const float both = s * (1.0f - s);
+    ds = both == 0.0f ? 0.0f : both * c * (1.0f + 0.134145f * g * g);
   }
 }
+// The limits at infinity: act(-inf) = -0, act'(inf) = 1, act'(-inf) = 0, where the
+// factor 0 must not meet an infinite g.  A NaN stays one.
+constexpr float kMmHighest = 3.402823466e38f;
+__device__ __forceinline__ float mm_low(float g) { return g < -kMmHighest ? -kMmHighest : g; }
+__device__ __forceinline__ float mm_finite(float g) { return g > kMmHighest ? kMmHighest : mm_low(g); }
 
 // Where a row of the result goes.
 struct MmOutRow {
@@ -260,7 +267,7 @@ __device__ __forceinline__ void mm_gate(float (&g)[32], const float (&u)[32]) {
   for (int j = 0; j < 32; ++j) {
     float s, ds;
     mm_act(ACT, g[j], s, ds);
-    g[j] *= s * u[j];
+    g[j] = mm_low(g[j]) * (s * u[j]);
   }
 }
 
@@ -460,7 +467,7 @@ __device__ __forceinline__ void mm_epilogue(const MmParams& p, int64_t row0, int
           mm_act(p.act, g, s, ds);
           if (p.gate) mm_store(p.gate, p.out_f32, (row0 + r) * p.gate_ld + col, g);
           if (p.up) mm_store(p.up, p.out_f32, (row0 + r) * p.up_ld + col, u);
-          mm_store(p.out, p.out_f32, (row0 + r) * p.out_ld + col, g * (s * u));
+          mm_store(p.out, p.out_f32, (row0 + r) * p.out_ld + col, mm_low(g) * (s * u));
         }
       }
       __syncwarp();

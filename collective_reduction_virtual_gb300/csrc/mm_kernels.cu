@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(256) vc_mm_join_splits(const __grid_constant__
     mm_act(p.act, g, s, ds);
     if (p.gate) mm_store(p.gate, p.out_f32, row * p.gate_ld + col, g);
     if (p.up) mm_store(p.up, p.out_f32, row * p.up_ld + col, u);
-    mm_store(p.out, p.out_f32, row * p.out_ld + col, g * (s * u));
+    mm_store(p.out, p.out_f32, row * p.out_ld + col, mm_low(g) * (s * u));
   }
 }
 

@@ -199,8 +199,8 @@ __global__ void __launch_bounds__(kThreads) vc_mm_gated_grad(const __grid_consta
     for (int j = 0; j < 8; ++j) {
       float s, ds;
       mm_act(ACT, g[j], s, ds);
-      u[j] = dh[j] * u[j] * (s + g[j] * ds);
-      dh[j] = dh[j] * (g[j] * s);
+      u[j] = dh[j] * u[j] * (s + mm_finite(g[j]) * ds);
+      dh[j] = dh[j] * (mm_low(g[j]) * s);
     }
     store8(p.dst, row * p.dst_ld + col, p.plane, p.parts, u);
     store8(p.dst, row * p.dst_ld + p.half + col, p.plane, p.parts, dh);

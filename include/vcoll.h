@@ -520,7 +520,8 @@ int vcoll_cross_entropy_backward(const float* dloss, int64_t dloss_count, const 
 
 /* Activation of a gated block: g / (1 + exp(-g)); g * Phi(g) with the normal
  * distribution function Phi; g * (1 + tanh(sqrt(2 / pi) * (g + 0.044715 *
- * g^3))) / 2. */
+ * g^3))) / 2.  At an infinite g the activation and its derivative are their
+ * limits. */
 typedef enum { VCOLL_SILU = 0, VCOLL_GELU = 1, VCOLL_GELU_TANH = 2 } vcoll_activation_t;
 
 /*

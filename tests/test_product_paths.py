@@ -55,3 +55,56 @@ def test_splits_of_a_gated_block_in_chunks(v, dtype, n, D, F):
         for got, again in zip(out, v.gated_ff(x, wg, wu, activation="silu", keep=True)):
             assert torch.equal(got, again)
     assert v.device_errors() == 0
+
+
+# ------------------------------------------------- operands at their range's ends
+
+INF = float("inf")
+FAR = [200.0, 1e4, 1e13, 1e20, 3e38]
+
+
+def same(got, want, rel):
+    """got is want to a relative bound, with its infinities and NaN."""
+    want = want.double()
+    far = want.abs() > torch.finfo(got.dtype).max  # rounds to infinity
+    want = torch.where(far, torch.copysign(torch.full_like(want, INF), want), want)
+    got = got.double()
+    ok = (got == want) | ((got - want).abs() <= rel * want.abs()) | (got.isnan() & want.isnan())
+    assert ok.all(), (got[~ok], want[~ok])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("copies", [1, 30])  # a few fp32 rows, and tiles
+def test_activations_far_out(v, dtype, act, copies):
+    # gate is x's first value (or ten times it, which overflows at the last), up is 2;
+    # so far out each activation is its argument or zero, and its slope one or zero
+    ends = torch.tensor(FAR + [-e for e in FAR], device="cuda").to(dtype).repeat(copies)
+    n = len(ends)
+    x = torch.stack([ends, torch.ones_like(ends)], 1)
+    wg = torch.tensor([[1.0, 0.0], [10.0, 0.0]] * 40, device="cuda").to(dtype)
+    wu = torch.tensor([[0.0, 2.0]] * 80, device="cuda").to(dtype)
+    h, gate, up = v.gated_ff(x, wg, wu, act, keep=True)
+    # an fp32 value of three parts is put together by fp32 additions that may cut a bit off each
+    rel = 2.0 ** -21 if dtype == torch.float32 else 2.0 ** -8
+    exact = (ends.double()[:, None] * torch.tensor([1.0, 10.0], device="cuda").double()).repeat(1, 40)
+    same(gate, exact, rel)
+    same(up, torch.full_like(exact, 2.0), rel)
+    same(h, 2.0 * exact.clamp(min=0.0), rel)
+
+    # the slopes of these and of infinite ones: x is one row's one, so that a weight's gradient is a row's
+    gate = torch.cat([ends, torch.tensor([INF, -INF, float("nan")], device="cuda").to(dtype)])
+    n = len(gate)
+    pick = torch.eye(n, device="cuda").to(dtype)
+    w = torch.zeros(1, n, device="cuda").to(dtype)
+    one = torch.ones(n, 1, device="cuda").to(dtype)
+    slope = torch.where(gate.isnan(), gate.double(), (gate > 0).double())
+    dg = v.gated_ff_backward(one[:-1], pick[:-1], w, w, gate[:-1, None], one[:-1], act, x_grad=False)[1]
+    same(dg[0, :-1], slope[:-1], rel)
+    dg, du = v.gated_ff_backward(one[:-3], pick[:-3], w, w, gate[:-3, None], one[:-3], act, x_grad=False)[1:]
+    same(du[0, :-3], gate[:-3].double().clamp(min=0.0), rel)
+    # one row of them all
+    dg, du = v.gated_ff_backward(one.t(), one[:1], one, one, gate[None], one.t(), act, x_grad=False)[1:]
+    same(dg[:, 0], slope, rel)
+    same(du[:, 0], torch.where(gate.isnan(), gate.double(), gate.double().clamp(min=0.0)), rel)
