@@ -20,6 +20,9 @@ __device__ __forceinline__ float mm_exp2(float x) {  // 2 ulp; 0 below 2^-126
   return y;
 }
 constexpr float kMmLog2e = 1.4426950408889634f;
+// e^x: off by 2 ulp and by |x| 2^-23, since x log2(e) is rounded (and log2(e) itself).
+// Where |x| is large the value is small beside those it is added to: of a softmax's
+// sum, whose largest term is 1; of 1 + e^-g; of a density.
 __device__ __forceinline__ float mm_exp(float x) { return mm_exp2(x * kMmLog2e); }
 __device__ __forceinline__ float mm_rcp(float x) {  // 1 ulp
   float y;
@@ -358,7 +361,8 @@ __device__ __forceinline__ void mm_epilogue(const MmParams& p, int64_t row0, int
       __syncwarp();
     }
   } else if constexpr (EPI == MM_LSE) {
-    // exponentials to base 2 of z log2(e), relative to a row's largest so far
+    // exponentials relative to a row's largest logit so far, which is kept as it is: its
+    // own exponential is exactly 1, and it meets a rounding only in the sum that is lse
     const int64_t hit = mine.hit;
     float m = -INFINITY, s = 0.0f;
     for (int c = c0; c < c1; c += 32) {
@@ -377,15 +381,14 @@ __device__ __forceinline__ void mm_epilogue(const MmParams& p, int64_t row0, int
       float top = v[0];
 #pragma unroll
       for (int j = 1; j < 32; ++j) top = fmaxf(top, v[j]);
-      top *= kMmLog2e;
       if (top > m) {
-        s *= mm_exp2(m - top);
+        s *= mm_exp(m - top);
         m = top;
       }
       const float ref = m == -INFINITY ? 0.0f : m;  // no difference of infinities
       float part[4] = {};
 #pragma unroll
-      for (int j = 0; j < 32; ++j) part[j % 4] += mm_exp2(fmaf(v[j], kMmLog2e, -ref));
+      for (int j = 0; j < 32; ++j) part[j % 4] += mm_exp(v[j] - ref);
       s += (part[0] + part[1]) + (part[2] + part[3]);
     }
     if (lane < rows && c0 < c1) p.part[(tile_n * (p.tn / (c1 - c0)) + (c0 ? 1 : 0)) * p.M + row] = make_float2(m, s);

@@ -487,10 +487,9 @@ __global__ void __launch_bounds__(256) vc_mm_join_splits(const __grid_constant__
       top = fmaxf(top, v[i]);
     }
     for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-    top *= kMmLog2e;
     const float ref = top == -INFINITY ? 0.0f : top;
 #pragma unroll
-    for (int i = 0; i < kMmTileN / 32; ++i) s += mm_exp2(fmaf(v[i], kMmLog2e, -ref));
+    for (int i = 0; i < kMmTileN / 32; ++i) s += mm_exp(v[i] - ref);
     for (int d = 16; d; d /= 2) s += __shfl_xor_sync(~0u, s, d);
     if (lane == 0) p.part[(int64_t)tn * p.M + row] = make_float2(top, s);  // of the whole tile
   } else if constexpr (EPI == MM_ERROR) {

@@ -108,3 +108,26 @@ def test_activations_far_out(v, dtype, act, copies):
     dg, du = v.gated_ff_backward(one.t(), one[:1], one, one, gate[None], one.t(), act, x_grad=False)[1:]
     same(dg[:, 0], slope, rel)
     same(du[:, 0], torch.where(gate.isnan(), gate.double(), gate.double().clamp(min=0.0)), rel)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,V,D", [(7, 1000, 2), (40, 1000, 2), (300, 5000, 8), (3, 40000, 640), (20, 130, 4000)])
+def test_loss_of_sure_rows_is_exact(v, dtype, n, V, D):
+    # one logit stands 500 above the others: lse is that logit, and the loss of its token zero
+    g = gen(n + V)
+    x = torch.zeros(n, D, device="cuda", dtype=dtype)
+    x[:, 0] = (torch.rand(n, generator=g, device="cuda") * 2000 - 1000).to(dtype)
+    x[:, 1] = 1.0
+    table = torch.zeros(V, D, device="cuda", dtype=dtype)
+    table[:, 0] = 1.0
+    sure = V // 3
+    table[:, 1] = -500.0
+    table[sure, 1] = 0.0
+    t = torch.full((n,), sure, device="cuda")
+    t[1::2] = V - 1
+    loss, lse = v.cross_entropy(x, table, t)
+    assert torch.equal(lse, x[:, 0].float())
+    assert not loss[::2].any()
+    # the other logits: a sum of two terms below 1500, cut off at most twice
+    assert ((loss[1::2] - 500.0).abs() <= 4 * 2.0 ** -24 * 1500).all()
