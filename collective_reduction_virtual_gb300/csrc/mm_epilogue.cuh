@@ -274,6 +274,11 @@ __device__ __forceinline__ void mm_gate(float (&g)[32], const float (&u)[32]) {
   }
 }
 
+// What a row's exponentials are relative to: its largest logit so far, or where that is
+// infinite zero, since infinities have no difference.  A logit of +infinity then makes
+// the sum infinite, and with it lse.
+__device__ __forceinline__ float mm_ref(float top) { return fabsf(top) == INFINITY ? 0.0f : top; }
+
 // What a lane's row brings besides its sums, loaded before they are waited for.
 struct MmRow {
   float scale;  // MM_OUT
@@ -385,7 +390,7 @@ __device__ __forceinline__ void mm_epilogue(const MmParams& p, int64_t row0, int
         s *= mm_exp(m - top);
         m = top;
       }
-      const float ref = m == -INFINITY ? 0.0f : m;  // no difference of infinities
+      const float ref = mm_ref(m);
       float part[4] = {};
 #pragma unroll
       for (int j = 0; j < 32; ++j) part[j % 4] += mm_exp(v[j] - ref);

@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(256) vc_mm_join_splits(const __grid_constant__
       top = fmaxf(top, v[i]);
     }
     for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-    const float ref = top == -INFINITY ? 0.0f : top;
+    const float ref = mm_ref(top);
 #pragma unroll
     for (int i = 0; i < kMmTileN / 32; ++i) s += mm_exp(v[i] - ref);
     for (int d = 16; d; d /= 2) s += __shfl_xor_sync(~0u, s, d);

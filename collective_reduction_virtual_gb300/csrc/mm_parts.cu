@@ -146,11 +146,10 @@ __global__ void __launch_bounds__(kMmJoinThreads) vc_mm_join(const __grid_consta
   float m = -INFINITY, s = 0.0f;
   auto add = [&](float2 q) {
     const float top = fmaxf(m, q.x);
-    if (top == -INFINITY) {  // nothing yet but what has no exponential, or NaN
+    if (fabsf(top) == INFINITY)  // nothing yet but what has no exponential, or NaN; or lse is infinite
       s += q.y;
-      return;
-    }
-    s = s * mm_exp(m - top) + q.y * mm_exp(q.x - top);
+    else
+      s = s * mm_exp(m - top) + q.y * mm_exp(q.x - top);
     m = top;
   };
   if (row < p.N) {

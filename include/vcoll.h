@@ -490,7 +490,8 @@ int vcoll_layer_norm_backward_checkpoint8(const void* grad, int64_t grad_ld, con
  * the logits z = x * table^T: lse[i] = log(sum over v of exp(z[i][v])), loss[i]
  * = lse[i] - z[i][targets[i]].  A target outside [0, V) -- padding -- has loss
  * 0.  x: N x D, table: V x D, both of dtype; loss, lse: N fp32.  V == 0: lse is
- * -infinity.  D == 0: the logits are zeros.
+ * -infinity.  D == 0: the logits are zeros.  A logit that overflows to +infinity
+ * gives lse +infinity, and the loss +infinity to other targets of its row.
  */
 size_t vcoll_cross_entropy_workspace_bytes(int64_t N, int64_t V, int64_t D, int dtype, int direct);
 int vcoll_cross_entropy(const void* x, int64_t x_ld, const void* table, int64_t table_ld,

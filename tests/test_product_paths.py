@@ -131,3 +131,46 @@ def test_loss_of_sure_rows_is_exact(v, dtype, n, V, D):
     assert not loss[::2].any()
     # the other logits: a sum of two terms below 1500, cut off at most twice
     assert ((loss[1::2] - 500.0).abs() <= 4 * 2.0 ** -24 * 1500).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,V,D", [(5, 700, 16), (40, 700, 16), (300, 3000, 64), (6, 40000, 640), (20, 130, 4000)])
+def test_infinite_logits(v, dtype, n, V, D):
+    # rows 0, 3, ...: one token's logit overflows; rows 1, 4, ...: many do, to both sides; the others are finite
+    g = gen(n * V)
+    x = (torch.rand(n, D, generator=g, device="cuda") + 0.5).to(dtype)
+    table = (torch.randn(V, D, generator=g, device="cuda") * 0.1).to(dtype)
+    table[:, :2] = 0.0
+    table[V - 2, 0] = 10.0
+    table[::7, 1], table[1::7, 1] = 10.0, -10.0
+    x[:, :2] = 0.0
+    x[::3, 0] = 3e38
+    x[1::3, 1] = 3e38
+    t = torch.full((n,), 3, device="cuda")  # of a finite logit in every row
+    t[-1] = -1
+    loss, lse = v.cross_entropy(x, table, t)
+    over = torch.arange(n, device="cuda") % 3 < 2
+    assert (lse[over] == INF).all()
+    want, wlse, bound, blse = R.loss(x[~over], table, t[~over])
+    near(loss[~over], want, bound)
+    near(lse[~over], wlse, blse)
+    assert loss[-1] == 0
+    over[-1] = False
+    assert (loss[over] == INF).all()
+    # the token whose own logit is infinite has no loss: inf - inf
+    t[0] = V - 2
+    assert v.cross_entropy(x, table, t)[0][0].isnan()
+
+
+@pytest.mark.gpu
+def test_infinite_bf16_operands(v):
+    g = gen(31)
+    for n, V in ((5, 700), (200, 3000)):
+        x = torch.randn(n, 64, generator=g, device="cuda").bfloat16()
+        table = torch.randn(V, 64, generator=g, device="cuda").bfloat16()
+        table[:, 0] = table[:, 0].abs() + 1.0
+        x[0, 0], x[1, 0], x[2, 0] = INF, -INF, float("nan")
+        t = torch.full((n,), 1, device="cuda")
+        lse = v.cross_entropy(x, table, t)[1]
+        assert lse[0] == INF and lse[1] == -INF and lse[2].isnan() and lse[3:].isfinite().all()
