@@ -174,3 +174,141 @@ def test_infinite_bf16_operands(v):
         t = torch.full((n,), 1, device="cuda")
         lse = v.cross_entropy(x, table, t)[1]
         assert lse[0] == INF and lse[1] == -INF and lse[2].isnan() and lse[3:].isfinite().all()
+
+
+# --------------------------------------------------------- long and separate sums
+
+@pytest.mark.gpu
+def test_gated_sums_longer_than_a_chunk(v):
+    # bf16 sums of more than 32768 places leave the tensor cores in two pieces, and no tile is split
+    dtype, n, D, F = torch.bfloat16, 513, 33000, 4864
+    assert splits_room(v, n, D, F, dtype) == 0
+    g = gen(21)
+    x, wg, wu = (matrix(g, r, D, dtype, scale=s).abs_() for r, s in ((n, 1.0), (F, 1e-3), (F, 1e-3)))
+    wg[1::2] *= -1  # gates of both signs, each a sum of one sign
+    want = R.gated(x, wg, wu, "gelu_tanh")
+    for got, w, b in zip(v.gated_ff(x, wg, wu, "gelu_tanh", keep=True), want[:3], want[3:]):
+        near(got, w, b, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+def test_gated_gradients_in_a_launch_each(v, dtype):
+    # both sums of 8192 places and more, and a wave of tiles in each product
+    n, D, F = 8200, 616, 4200
+    g = gen(22)
+    x, wg, wu = matrix(g, n, D, dtype), matrix(g, F, D, dtype, scale=0.05), matrix(g, F, D, dtype, scale=0.05)
+    dh, gate, up = (matrix(g, n, F, dtype) for _ in range(3))
+    want = R.gated_grad(dh, x, wg, wu, gate, up, "silu", dtype)
+    got = v.gated_ff_backward(dh, x, wg, wu, gate, up, "silu")
+    for t, w, b in zip(got, want[:3], want[3:]):
+        near(t, w, b, dtype)
+    for t, again in zip(got, v.gated_ff_backward(dh, x, wg, wu, gate, up, "silu")):
+        assert torch.equal(t, again)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("with_base", [False, True])
+def test_loss_gradients_in_a_launch_each(v, dtype, with_base):
+    n, V, D = 8200, 8300, 616
+    g = gen(23)
+    x, table = matrix(g, n, D, dtype), matrix(g, V, D, dtype, scale=0.08)
+    t = torch.randint(-200, V, (n,), generator=g, device="cuda")
+    base = matrix(g, V, D, dtype) if with_base else None
+    gloss = torch.randn(n, generator=g, device="cuda")
+    lse = v.cross_entropy(x, table, t)[1]
+    dx, dt = v.cross_entropy_backward(gloss, x, table, t, lse, base=base)
+    want = R.loss_grad(gloss, x, table, t, lse, base, dtype)
+    near(dx, want[0], want[2], dtype)
+    near(dt, want[1], want[3], dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,D,F,layout", [(1, 64, 100, "dense"), (9, 129, 67, "odd"), (16, 320, 1030, "slice"),
+                                          (17, 33, 5, "odd"), (300, 200, 500, "dense"), (700, 1001, 259, "odd")])
+@pytest.mark.parametrize("which", ["gate", "up"])
+@pytest.mark.parametrize("x_grad", [False, True])
+def test_one_weights_gradient_alone(v, dtype, n, D, F, layout, which, x_grad):
+    g = gen(n + D + F)
+    x, wg, wu = (matrix(g, r, D, dtype, layout) for r in (n, F, F))
+    dh, gate, up = (matrix(g, n, F, dtype, layout) for _ in range(3))
+    out = matrix(g, F, D, dtype, layout).fill_(float("nan"))
+    got = v.gated_ff_backward(dh, x, wg, wu, gate, up, "gelu", x_grad=x_grad, weight_grads=False, **{"dw_" + which: out})
+    want = R.gated_grad(dh, x, wg, wu, gate, up, "gelu", dtype)
+    at = 1 if which == "gate" else 2
+    assert got[at] is out and got[3 - at] is None and (got[0] is not None) == x_grad
+    near(out, want[at], want[3 + at], dtype)
+    if x_grad:
+        near(got[0], want[0], want[3], dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,n,V,D", [(torch.float32, 40000, 5001, 24), (torch.bfloat16, 70001, 5001, 16)])
+def test_table_gradient_of_tokens_that_no_row_aims_at(v, dtype, n, V, D):
+    # A vocabulary in pieces.  With rows, weights and e of one sign a sum's bound is a small share of it.
+    # The sum over all rows is off by 2 n u of its terms, beside what products_ref has for each part of them.
+    g = gen(24)
+    x, table = matrix(g, n, D, dtype).abs_(), matrix(g, V, D, dtype, scale=0.5)
+    t = torch.randint(-50, V // 2, (n,), generator=g, device="cuda")
+    gloss = torch.rand(n, generator=g, device="cuda") + 0.5
+    lse = v.cross_entropy(x, table, t)[1]
+    dt = v.cross_entropy_backward(gloss, x, table, t, lse, x_grad=False)[1]
+    total = bound = 0.0
+    for a in range(0, n, 8192):
+        part = slice(a, a + 8192)
+        w = R.loss_grad(gloss[part], x[part], table, t[part], lse[part], None, dtype)
+        total, bound = total + w[1], bound + w[3]
+    free = slice(V // 2, V)
+    bound = bound[free] + 2 * n * R.U * total[free]
+    assert (bound <= 0.02 * total[free]).all()
+    near(dt[free], total[free], bound, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+def test_products_repeat_their_bits(v, dtype):
+    g = gen(25)
+    for n, D, F in ((5, 700, 900), (40, 1024, 3000), (300, 2048, 1000), (1000, 320, 1280)):
+        x, w, u = (matrix(g, r, D, dtype) for r in (n, F, F))
+        t = torch.randint(-3, F, (n,), generator=g, device="cuda")
+        one = torch.ones(1, device="cuda")
+
+        def calls():
+            loss, lse = v.cross_entropy(x, w, t)
+            h, gate, up = v.gated_ff(x, w, u, keep=True)
+            return (loss, lse, *v.cross_entropy_backward(one, x, w, t, lse, base=u), h, gate, up,
+                    *v.gated_ff_backward(h, x, w, u, gate, up))
+
+        first = calls()
+        for _ in range(5):
+            assert all(torch.equal(a, b) for a, b in zip(first, calls()))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,D,F", [(1, 8, 3), (7, 130, 1000), (16, 513, 77), (100, 1024, 4096), (513, 320, 1280), (33, 1001, 2671)])
+def test_workspaces_are_not_left(v, dtype, n, D, F):
+    # each call has exactly the bytes that it asks for, between others that it leaves alone
+    g = gen(n + D + F + 2)
+    x, w, u = (matrix(g, r, D, dtype) for r in (n, F, F))
+    dh = matrix(g, n, F, dtype)
+    t = torch.randint(-1, F, (n,), generator=g, device="cuda")
+    one = torch.ones(1, device="cuda")
+    def inside(need, call):
+        room = torch.full((need + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+        out = call(room[4096:4096 + need])
+        assert (room[:4096] == 0xA5).all() and (room[4096 + need:] == 0xA5).all()
+        return out
+
+    loss, lse = inside(v.cross_entropy_workspace_bytes(n, F, D, dtype), lambda ws: v.cross_entropy(x, w, t, workspace=ws))
+    grads = inside(v.cross_entropy_backward_workspace_bytes(n, F, D, dtype),
+                   lambda ws: v.cross_entropy_backward(one, x, w, t, lse, base=u, workspace=ws))
+    h, gate, up = inside(v.gated_ff_workspace_bytes(n, D, F, dtype), lambda ws: v.gated_ff(x, w, u, keep=True, workspace=ws))
+    more = inside(v.gated_ff_backward_workspace_bytes(n, D, F, dtype),
+                  lambda ws: v.gated_ff_backward(dh, x, w, u, gate, up, workspace=ws))
+    for got, again in zip((loss, lse, *grads, h, gate, up, *more),
+                          (*v.cross_entropy(x, w, t), *v.cross_entropy_backward(one, x, w, t, lse, base=u),
+                           *v.gated_ff(x, w, u, keep=True), *v.gated_ff_backward(dh, x, w, u, gate, up))):
+        assert torch.equal(got, again)
