@@ -338,7 +338,8 @@ __device__ __forceinline__ void mm_epilogue(const MmParams& p, int64_t row0, int
                          p.accum_in ? row0 * p.accum_ld : to.row * p.base_ld, p.accum_in ? p.accum_ld : p.base_ld,
                          p.accum_out ? (void*)p.accum_out : to.out,
                          p.accum_out ? row0 * p.accum_ld : to.row * to.ld, p.accum_out ? p.accum_ld : to.ld,
-                         p.base ? scale : 1.0f, p.base || p.accum_out ? 1.0f : scale};
+                         p.base || p.accum_scaled ? scale : 1.0f,
+                         p.base || p.accum_scaled || p.accum_out ? 1.0f : scale};
       const bool out32 = p.accum_out || p.out_f32, in32 = p.accum_in || out32;
       // pairs of columns do not reach past the last one
       const bool wide = p.N % 2 == 0 && (p.accum_in || !p.base || p.out_pairs) && (p.accum_out || p.out_pairs);

@@ -59,6 +59,7 @@ struct MmParams {
   const float* accum_in;  // fp32 sums so far, accum_ld apart
   float* accum_out;       // instead of out
   int64_t accum_ld;
+  int accum_scaled;       // the sums so far hold scale (else out applies it); what is added to base begins with it
   const float* scale;     // one value, or NULL
   const void* base;       // of out's type and stride base_ld
   int64_t base_ld;
@@ -146,6 +147,16 @@ struct MmPackParams {
   int idx64, src_f32, parts;
 };
 
+// A matrix widened to fp32, its rows dst_ld apart.
+struct MmWidenParams {
+  const void* src;
+  float* dst;
+  int64_t rows, cols, src_ld, dst_ld;
+  int src_f32;
+  int load16;  // rows start at 16-byte boundaries
+  int64_t blocks;
+};
+
 // Joins the tiles' maxima and sums of a piece of the vocabulary to those of
 // the pieces before, and after the last gives the loss.
 struct MmJoinParams {
@@ -181,6 +192,7 @@ const void* mm_join_splits_kernel(MmEpilogue epilogue);
 const void* mm_few_kernel(MmEpilogue epilogue, int rows, bool wide);  // MM_OUT: sums for the join
 const void* mm_few_outer_kernel(bool wide);
 const void* mm_pack_kernel();
+const void* mm_widen_kernel();
 const void* mm_join_kernel();
 const void* mm_gated_grad_kernel(int act);
 

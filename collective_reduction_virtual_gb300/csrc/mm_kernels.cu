@@ -466,12 +466,14 @@ __global__ void __launch_bounds__(256) vc_mm_join_splits(const __grid_constant__
     const MmOutRow to = mm_out_row(p, row);
     if (col >= p.N || to.row >= (p.M1 ? p.M2 : p.M)) return;
     float x = sum(c);
+    const float scale = p.scale ? *p.scale : 1.0f;
+    if (p.accum_scaled) x *= scale;
     if (p.accum_in) x += p.accum_in[row * p.accum_ld + col];
     if (p.accum_out) {
       p.accum_out[row * p.accum_ld + col] = x;
       return;
     }
-    if (p.scale) x *= *p.scale;
+    if (!p.accum_scaled) x *= scale;
     if (p.base) x += mm_load(p.base, p.out_f32, to.row * p.base_ld + col);
     mm_store(to.out, p.out_f32, to.row * to.ld + col, x);
   } else if constexpr (EPI == MM_LSE) {

@@ -133,6 +133,23 @@ __global__ void __launch_bounds__(kThreads) vc_mm_pack(const __grid_constant__ M
     largest(p);
 }
 
+// What a table's gradient is added to, as the first of the fp32 sums that its blocks
+// of rows add to.  Once for a piece of the vocabulary: a thousandth of its products.
+__global__ void __launch_bounds__(kThreads) vc_mm_widen(const __grid_constant__ MmWidenParams p) {
+  pdl_enter();
+  const int64_t groups = (p.cols + 7) / 8;
+  for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < p.rows * groups; e += p.blocks * kThreads) {
+    int64_t row, group;
+    item_at(e, groups, row, group);
+    float v[8];
+    load8(p.src, p.src_f32, p.load16, row * p.src_ld + group * 8, p.cols - group * 8, v);
+    float* to = p.dst + row * p.dst_ld + group * 8;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (group * 8 + j < p.cols) to[j] = v[j];
+  }
+}
+
 // lse[i] = log of the sum over the tiles' (maximum, sum of exponentials), which are
 // joined pair by pair: s = s1 e^(m1 - m) + s2 e^(m2 - m) with m the larger maximum.
 // A CTA for 32 rows, a warp for every 32nd tile of them.
@@ -207,6 +224,7 @@ __global__ void __launch_bounds__(kThreads) vc_mm_gated_grad(const __grid_consta
 }
 
 const void* mm_pack_kernel() { return (const void*)vc_mm_pack; }
+const void* mm_widen_kernel() { return (const void*)vc_mm_widen; }
 const void* mm_join_kernel() { return (const void*)vc_mm_join; }
 const void* mm_gated_grad_kernel(int act) {
   return act == VCOLL_SILU   ? (const void*)vc_mm_gated_grad<VCOLL_SILU>

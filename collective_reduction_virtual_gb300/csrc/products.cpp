@@ -18,6 +18,12 @@ constexpr int64_t kPackBytes = 256 << 20;   // of a piece of the table, laid out
 // of the gradient's e for a piece (4096 x 128000 x 4096 bf16: 7.63 ms with 64 MB, 7.39
 // with 128, 7.26 with 256 and 7.20 with 512)
 constexpr int64_t kErrorBytes = 256 << 20;
+// and, where the rows are so many that the narrowest piece of e takes more, of e for a
+// block of rows: half of a million fp32 rows of 64 columns would take 6.4 GB at once.
+// Blocks of a quarter of this (65536 rows of bf16) cost up to 12 % (65536 x 8000 x 512
+// fp32 6.7 ms with all rows at once, 7.5 with four blocks; 131072 x 32000 x 4096 bf16
+// 68.1 and 68.4 with two).
+constexpr int64_t kBlockBytes = 1 << 30;
 constexpr int64_t kPartBytes = 128 << 20;   // of the loss's tiles of a piece
 constexpr int kPassThreads = 256;           // of the kernels of mm_parts.cu
 
@@ -189,14 +195,16 @@ size_t few_bytes(int64_t M, int64_t N, int64_t K) {
   return (size_t)(ceil_div(N, 128) * few_splits(N, K) * M * 128) * sizeof(float);
 }
 
-// Columns of a piece of the vocabulary: `fit` at most, whole tiles.
+// Columns of a piece of the vocabulary: `fit` at most, whole tiles, but not fewer than
+// a product with them needs to be worth its launches.
+constexpr int64_t kLeastPiece = 2048;
 int64_t piece_of(int64_t V, int64_t fit) {
-  return std::min(V, std::max<int64_t>(2048, fit / 256 * 256));
+  return std::min(V, std::max<int64_t>(kLeastPiece, fit / 256 * 256));
 }
 
-// The widths of a vocabulary's pieces: all but the last are alike.
-std::array<int64_t, 2> piece_widths(int64_t V, int64_t piece) {
-  return {piece, piece ? V - (V - 1) / piece * piece : 0};
+// The sizes of the pieces that `all` are cut into: all but the last are alike.
+std::array<int64_t, 2> widths_of(int64_t all, int64_t piece) {
+  return {piece, piece ? all - (all - 1) / piece * piece : 0};
 }
 
 struct LossLayout {
@@ -219,7 +227,7 @@ LossLayout loss_layout(int64_t N, int64_t V, int64_t D, int dtype, bool direct) 
   if (few) {
     tiles = ceil_div(L.piece, 64);
   } else {
-    for (int64_t w : piece_widths(V, L.piece)) {
+    for (int64_t w : widths_of(V, L.piece)) {
       const Plan plan = plan_of({N, w, D, parts, false, epilogue_cycles(1)});
       splits = std::max(splits, plan.bytes());
       tiles = std::max(tiles, ceil_div(w, plan.of[0].tn));
@@ -232,15 +240,22 @@ LossLayout loss_layout(int64_t N, int64_t V, int64_t D, int dtype, bool direct) 
   return L;
 }
 
+// The gradient's e exists for a piece of the vocabulary and a block of rows at a time.
+// A block has all rows, or where 2048 columns of them are more than kBlockBytes as many
+// as fit: the table's gradient of a piece is then summed over the blocks in fp32.
 struct LossGradLayout {
-  int64_t piece, pieces, error_ld;
-  size_t scale, x, table, error, accum, splits, bytes;
+  int64_t piece, pieces, rows, blocks, error_ld;
+  size_t scale, x, table, error, accum, table_accum, splits, bytes;
 };
 LossGradLayout loss_grad_layout(int64_t N, int64_t V, int64_t D, int dtype, bool direct) {
   const int parts = parts_of(dtype);
   LossGradLayout L;
   const bool few = few_rows(N, dtype);
-  int64_t fit = kErrorBytes / (2 * parts * std::max<int64_t>(N, 1));
+  const int64_t least = std::min<int64_t>(std::max<int64_t>(round_up(V, kPackedCols), 1), kLeastPiece);
+  const int64_t most = kBlockBytes / (2 * parts * least) / 256 * 256;
+  L.blocks = std::max<int64_t>(1, ceil_div(N, most));
+  L.rows = L.blocks > 1 ? round_up(ceil_div(N, L.blocks), 256) : N;
+  int64_t fit = kErrorBytes / (2 * parts * std::max<int64_t>(L.rows, 1));
   if (!direct && !few) fit = std::min(fit, kPackBytes / std::max<int64_t>(1, packed_bytes(1, D, parts)));
   L.piece = piece_of(V, fit);
   L.pieces = std::max<int64_t>(1, L.piece ? ceil_div(V, L.piece) : 1);
@@ -249,21 +264,23 @@ LossGradLayout loss_grad_layout(int64_t N, int64_t V, int64_t D, int dtype, bool
   L.scale = r.take(sizeof(float));
   L.x = r.take(packed_bytes(N, D, parts));
   L.table = r.take(direct || few ? 0 : packed_bytes(L.piece, D, parts));
-  L.error = r.take(N * L.error_ld * 2 * parts);
+  L.error = r.take(L.rows * L.error_ld * 2 * parts);
   L.accum = r.take(L.pieces > 1 ? N * round_up(D, 2) * 4 : 0);
+  L.table_accum = r.take(L.blocks > 1 ? L.piece * round_up(D, 2) * 4 : 0);
   size_t splits = 0;
   if (few) {
     splits = few_bytes(N, D, L.piece);
   } else {
-    for (int64_t w : piece_widths(V, L.piece)) {
-      const Shape error = {N, w, D, parts, false, epilogue_cycles(parts)};
-      splits = std::max(splits, plan_of(error).bytes());
-      for (const bool base : {false, true}) {  // dx, dtable, and both
-        const Shape s[2] = {{N, D, w, parts, false, epilogue_cycles(parts, L.pieces > 1)},
-                            {w, D, N, parts, false, epilogue_cycles(parts, base)}};
-        splits = std::max({splits, plan_of(s[0]).bytes(), plan_of(s[1]).bytes(), make_plan(s, 2).bytes()});
+    for (int64_t w : widths_of(V, L.piece))
+      for (int64_t n : widths_of(N, L.rows)) {
+        const Shape error = {n, w, D, parts, false, epilogue_cycles(parts)};
+        splits = std::max(splits, plan_of(error).bytes());
+        for (const bool add : {false, true}) {  // dx, dtable, and both
+          const Shape s[2] = {{n, D, w, parts, false, epilogue_cycles(parts, L.pieces > 1)},
+                              {w, D, n, parts, false, epilogue_cycles(parts, add)}};
+          splits = std::max({splits, plan_of(s[0]).bytes(), plan_of(s[1]).bytes(), make_plan(s, 2).bytes()});
+        }
       }
-    }
   }
   L.splits = r.take((int64_t)splits);
   L.bytes = r.bytes;
@@ -715,8 +732,8 @@ int vcoll_cross_entropy_backward(const float* dloss, int64_t dloss_count, const 
   const int parts = parts_of(dtype), idx64 = index_type == VCOLL_I64;
   const bool few = few_rows(N, dtype);
   float* scale = (float*)(ws + L.scale);
-  const int64_t dloss_step = dloss_count == 1 ? 0 : 1;
-  MmOperand rows;  // x without the rows that do not count
+  const int64_t dloss_step = dloss_count == 1 ? 0 : 1, index_bytes = idx64 ? 8 : 4;
+  MmOperand all_rows;  // x without the rows that do not count
   for (int64_t i = 0; i < L.pieces; ++i) {
     const int64_t v0 = i * L.piece, width = std::min(L.piece, V - v0);
     MmOperand tokens;
@@ -729,68 +746,97 @@ int vcoll_cross_entropy_backward(const float* dloss, int64_t dloss_count, const 
       pack.p.dloss_step = dloss_step;
       pack.p.scale = scale;
       pack.p.N = N;
-      VCOLL_TRY(pack.add(x, N, D, x_ld, false, ws + L.x, true, &rows));
+      VCOLL_TRY(pack.add(x, N, D, x_ld, false, ws + L.x, true, &all_rows));
     }
     VCOLL_TRY(pack.add((const char*)table + v0 * table_ld * es, N ? width : 0, D, table_ld, direct || few, ws + L.table,
                        false, &tokens));
     VCOLL_TRY(pack.run(stream));
-    const MmOperand error = operand(ws + L.error, N, width, L.error_ld, N * L.error_ld);
-    MmLaunch all = {};
-    MmParams& p = all.p[0];
-    p.a = rows;
-    p.b[0] = tokens;
-    p.M = N;
-    p.N = width;
-    p.K = D;
-    p.parts = parts;
-    p.targets = targets;
-    p.idx64 = idx64;
-    p.V = V;
-    p.token0 = v0;
-    p.dloss = dloss;
-    p.dloss_step = dloss_step;
-    p.lse = lse;
-    p.scale = scale;
-    p.error = ws + L.error;
-    p.error_ld = L.error_ld;
-    p.error_plane = N * L.error_ld;
-    VCOLL_TRY(run(MM_ERROR, few, &all, ws + L.splits, stream));
-    MmLaunch grads = {};  // of x and of the table
-    if (dx) {
-      MmParams& q = grads.p[0];
-      q.a = error;
-      q.b[0] = tokens;
-      q.M = N;
-      q.N = D;
-      q.K = width;
-      q.parts = parts;
-      q.scale = scale;
-      q.out = dx;
-      q.out_pairs = in_pairs(dx, N, dx_ld, dtype);
-      q.out_ld = dx_ld;
-      q.out_f32 = dtype == VCOLL_F32;
-      q.accum_ld = round_up(D, 2);
-      if (i > 0) q.accum_in = (float*)(ws + L.accum);
-      if (i < L.pieces - 1) q.accum_out = (float*)(ws + L.accum);
+    float* sums = (float*)(ws + L.table_accum);
+    if (L.blocks > 1 && base && dtable) {
+      MmWidenParams w = {};
+      w.src = (const char*)base + v0 * base_ld * es;
+      w.dst = sums;
+      w.rows = width;
+      w.cols = D;
+      w.src_ld = base_ld;
+      w.dst_ld = round_up(D, 2);
+      w.src_f32 = dtype == VCOLL_F32;
+      w.load16 = rows_at_16(w.src, width, base_ld, es);
+      w.blocks = pass_blocks(width * ceil_div(D, 8));
+      if (width) VCOLL_TRY(launch_grid(mm_widen_kernel(), w.blocks, 1, kPassThreads, 0, &w, stream));
     }
-    if (dtable) {
-      MmParams& q = grads.p[1];
-      q.a = error;
-      q.b[0] = rows;
-      q.M = width;
-      q.N = D;
-      q.K = N;
-      q.parts = parts;
-      q.scale = scale;
-      q.out = (char*)dtable + v0 * dtable_ld * es;
-      q.out_ld = dtable_ld;
-      q.out_pairs = in_pairs(q.out, V, dtable_ld, dtype);
-      q.out_f32 = dtype == VCOLL_F32;
-      q.base = base ? (const char*)base + v0 * base_ld * es : nullptr;
-      q.base_ld = base_ld;
-      if (base) q.out_pairs = q.out_pairs && in_pairs(q.base, V, base_ld, dtype);
+    for (int64_t b = 0; b < L.blocks; ++b) {
+      const int64_t n0 = b * L.rows, n = std::min(L.rows, N - n0);
+      const MmOperand error = operand(ws + L.error, n, width, L.error_ld, L.rows * L.error_ld);
+      MmOperand rows = all_rows;
+      rows.p = (const char*)rows.p + n0 * rows.ld * 2;
+      rows.rows = n;
+      MmLaunch all = {};
+      MmParams& p = all.p[0];
+      p.a = rows;
+      p.b[0] = tokens;
+      p.M = n;
+      p.N = width;
+      p.K = D;
+      p.parts = parts;
+      p.targets = (const char*)targets + n0 * index_bytes;
+      p.idx64 = idx64;
+      p.V = V;
+      p.token0 = v0;
+      p.dloss = dloss + n0 * dloss_step;
+      p.dloss_step = dloss_step;
+      p.lse = lse + n0;
+      p.scale = scale;
+      p.error = ws + L.error;
+      p.error_ld = L.error_ld;
+      p.error_plane = L.rows * L.error_ld;
+      VCOLL_TRY(run(MM_ERROR, few, &all, ws + L.splits, stream));
+      MmLaunch grads = {};  // of x and of the table
+      if (dx) {
+        MmParams& q = grads.p[0];
+        q.a = error;
+        q.b[0] = tokens;
+        q.M = n;
+        q.N = D;
+        q.K = width;
+        q.parts = parts;
+        q.scale = scale;
+        q.out = (char*)dx + n0 * dx_ld * es;
+        q.out_pairs = in_pairs(q.out, N, dx_ld, dtype);
+        q.out_ld = dx_ld;
+        q.out_f32 = dtype == VCOLL_F32;
+        q.accum_ld = round_up(D, 2);
+        float* so_far = (float*)(ws + L.accum) + n0 * q.accum_ld;
+        if (i > 0) q.accum_in = so_far;
+        if (i < L.pieces - 1) q.accum_out = so_far;
+      }
+      if (dtable) {
+        MmParams& q = grads.p[1];
+        q.a = error;
+        q.b[0] = rows;
+        q.M = width;
+        q.N = D;
+        q.K = n;
+        q.parts = parts;
+        q.scale = scale;
+        q.out = (char*)dtable + v0 * dtable_ld * es;
+        q.out_ld = dtable_ld;
+        q.out_pairs = in_pairs(q.out, V, dtable_ld, dtype);
+        q.out_f32 = dtype == VCOLL_F32;
+        if (L.blocks == 1 && base) {
+          q.base = (const char*)base + v0 * base_ld * es;
+          q.base_ld = base_ld;
+          q.out_pairs = q.out_pairs && in_pairs(q.base, V, base_ld, dtype);
+        }
+        if (L.blocks > 1) {
+          q.accum_ld = round_up(D, 2);
+          q.accum_scaled = 1;
+          if (b > 0 || base) q.accum_in = sums;
+          if (b < L.blocks - 1) q.accum_out = sums;
+        }
+      }
+      VCOLL_TRY(run(MM_OUT, few, &grads, ws + L.splits, stream));
     }
-    VCOLL_TRY(run(MM_OUT, few, &grads, ws + L.splits, stream));
   }
   return VCOLL_OK;
 }

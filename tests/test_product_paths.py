@@ -312,3 +312,61 @@ def test_workspaces_are_not_left(v, dtype, n, D, F):
                           (*v.cross_entropy(x, w, t), *v.cross_entropy_backward(one, x, w, t, lse, base=u),
                            *v.gated_ff(x, w, u, keep=True), *v.gated_ff_backward(dh, x, w, u, gate, up))):
         assert torch.equal(got, again)
+
+
+# ----------------------------------------------------- many rows, block by block
+
+def test_the_loss_gradients_workspace_is_bounded(v):
+    # 1 GB of e at most (256 MB where that has 2048 columns) beside what has the rows' own size: x laid out
+    # and dx's sums so far
+    for n, V, D, dtype, e in ((65536, 128000, 64, torch.bfloat16, 1 << 28), (21000, 128000, 64, torch.float32, 1 << 28),
+                              (1 << 19, 128000, 64, torch.float32, 1 << 30), (1 << 20, 128000, 64, torch.float32, 1 << 30),
+                              (1 << 20, 50000, 1, torch.bfloat16, 1 << 30)):
+        parts = 3 if dtype == torch.float32 else 1
+        wide = (D + 63) // 64 * 64
+        rows = n * (wide * 2 * parts + (D + 1) // 2 * 2 * 4)
+        table = 2 * V * wide * 2 * parts  # a piece laid out and its gradient's sums, and splits of these
+        assert v.cross_entropy_backward_workspace_bytes(n, V, D, dtype) <= e + rows + table + (64 << 20), (n, V, D)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,n,V,D,index", [
+    (torch.bfloat16, 270000, 2100, 40, torch.int32), (torch.bfloat16, 530001, 2049, 7, torch.int64),
+    (torch.float32, 88000, 4100, 33, torch.int64), (torch.float32, 174081, 2500, 16, torch.int32),
+    (torch.bfloat16, 524289, 2500, 8, torch.int64)])
+@pytest.mark.parametrize("form", ["dense", "odd", "one"])
+def test_a_loss_gradient_in_blocks_of_rows(v, dtype, n, V, D, index, form):
+    g = gen(n + V)
+    layout = "odd" if form == "odd" else "dense"
+    x, table = matrix(g, n, D, dtype, layout).abs_(), matrix(g, V, D, dtype, layout, scale=0.5)
+    t = torch.randint(-500, V // 2, (n,), generator=g, device="cuda").to(index)
+    t[-1], t[n // 2] = V // 2, -1
+    gloss = torch.rand(1 if form == "one" else n, generator=g, device="cuda") + 0.5
+    base = matrix(g, V, D, dtype, layout)
+    lse = v.cross_entropy(x, table, t)[1]
+    plain = v.cross_entropy_backward(gloss, x, table, t, lse)
+    kept = base.clone()
+    dx, dt = v.cross_entropy_backward(gloss, x.clone(), table, t, lse, base=base, dtable=base)
+    assert dt is base and torch.equal(dx, plain[0])
+    total = bound = 0.0
+    wants = []
+    for a in range(0, n, 8192):
+        part = slice(a, a + 8192)
+        w = R.loss_grad(gloss[part] if form != "one" else gloss, x[part], table, t[part], lse[part], None, dtype)
+        wants.append((part, w[0], w[2]))
+        near(dx[part], w[0], w[2], dtype)
+        total, bound = total + w[1], bound + w[3]
+    # The sum over all rows is off by 2 n u of its terms' magnitudes, beside what each part's is.  These are
+    # g p x, which the total has, and g x of the rows that aim at the token, which it has the other way round.
+    inside = (t >= 0).nonzero().flatten()
+    aimed = torch.zeros_like(total).index_add_(0, t[inside].long(), x[inside].double() * gloss.expand(n)[inside, None])
+    bound = bound + 2 * n * R.U * (total + 2 * aimed)
+    near(plain[1], total, bound, dtype)
+    added = bound + 8 * R.U * (total.abs() + 2 * aimed + kept.double().abs())
+    near(dt, total + kept.double(), added, dtype)
+    # each gradient alone
+    near(v.cross_entropy_backward(gloss, x, table, t, lse, base=kept, x_grad=False)[1], total + kept.double(), added, dtype)
+    dx = v.cross_entropy_backward(gloss, x, table, t, lse, dx=x, table_grad=False)[0]
+    assert dx is x
+    for part, w, b in wants:
+        near(dx[part], w, b, dtype)
