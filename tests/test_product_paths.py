@@ -370,3 +370,20 @@ def test_a_loss_gradient_in_blocks_of_rows(v, dtype, n, V, D, index, form):
     assert dx is x
     for part, w, b in wants:
         near(dx[part], w, b, dtype)
+
+
+# ------------------------------------------------------------------- precision
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,D,F", [(300, 512, 400), (700, 448, 1000), (300, 1500, 400), (40, 1500, 2000)])
+def test_fp32_sums_are_as_close_as_fp32_adders(v, n, D, F):
+    # against adders that round to nearest after each of the terms in turn
+    g = gen(26)
+    x, wg, wu = matrix(g, n, D, torch.float32), matrix(g, F, D, torch.float32), matrix(g, F, D, torch.float32)
+    _, gate, up = v.gated_ff(x, wg, wu, keep=True)
+    for got, w in ((gate, wg), (up, wu)):
+        exact = x.double() @ w.double().t()
+        adders = torch.zeros_like(got)
+        for k in range(D):
+            adders += x[:, k, None] * w[None, :, k]
+        assert (got.double() - exact).norm() <= (adders.double() - exact).norm()
