@@ -399,6 +399,10 @@ __device__ __forceinline__ void mm_epilogue(const MmParams& p, int64_t row0, int
     }
     if (lane < rows && c0 < c1) p.part[(tile_n * (p.tn / (c1 - c0)) + (c0 ? 1 : 0)) * p.M + row] = make_float2(m, s);
   } else if constexpr (EPI == MM_ERROR) {
+    // e, the one matrix that has to exist: of bf16 operands in one bf16, half a step of 2^-8
+    // off, as a program holds it that keeps its logits' gradient (results of bf16 are then off
+    // by 1.14 to 1.16 times their own rounding; two parts would double both products' work);
+    // of fp32 operands in three, which hold its 24 bits
     const int64_t hit = mine.hit;
     const float lse = mine.lse, w = mine.w;
     float x[32];

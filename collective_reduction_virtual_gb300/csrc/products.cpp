@@ -34,9 +34,13 @@ constexpr int64_t kPlanSms = 152;
 int64_t round_up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
 int parts_of(int dtype) { return dtype == VCOLL_F32 ? 3 : 1; }
 // Of the gradients of gate and up.  Rounded to one bf16 they make bf16 results off by
-// 1.4 times their own rounding, and where there are few of them, by chance by up to 1.6
-// times: those take two parts, which costs nothing there (1 x 1024, 4096: 29 us either
-// way; with 1 x 4096, 11008 it would be 97 and 152).
+// sqrt(2) times their own rounding (measured 1.37 to 1.43), as those of a program are
+// that keeps them in bf16.  That is a mean over n roundings, which chance moves by some
+// 1 / sqrt(n): over a hundred by 10 % and more (1.6 was seen), over 8192 by 1 %.  Up to
+// there they take two parts and results are off by their own rounding alone (1.00).
+// N x D, F in us with two parts and with one: 1 x 1024, 4096 29 and 29; 8 x 1024, 1024
+// 27 and 29; 1 x 4096, 8192 102 and 77.  Of more values they would cost 1 x 4096, 11008
+// 128 instead of 98, 3001 x 1001, 2671 117 instead of 70.
 constexpr int64_t kFineValues = 8192;
 int grad_parts(int64_t N, int64_t F, int dtype) { return dtype == VCOLL_F32 ? 3 : N * F <= kFineValues ? 2 : 1; }
 
