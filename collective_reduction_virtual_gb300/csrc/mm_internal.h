@@ -109,14 +109,15 @@ constexpr int kMmRows = 128;
 // and added in registers.  Relative errors of the loss over 4096 columns: 2.9e-6
 // without, 6.9e-7 in chunks of 1024 places, 3.2e-7 of 512, which took 5 % longer; of
 // fp32 adders 6.6e-7.
-// Rows of one tile wait for memory anyway: their loss takes chunks of 256 places.
+// Rows of one tile wait for memory anyway: their loss takes chunks of 128 places (7 rows
+// of 32000 x 4096: 5.3e-8 off in 48 us, 1.2e-7 in chunks of 256, 49.4 us in chunks of 64).
 // Of three parts' products only the last and largest is cut, after 256 places: 777 x
 // 1001 x 2671 is off by 2.3e-7 (fp32 adders 5.7e-7), after 512 by 4.7e-7 and after 128 by
 // 1.3e-7; the smallest gradient of the loss took 87 us, 85.5 and 89, others the same.
 // What is rounded to bf16 in the end may drift by 3e-5 in 32768 places, a hundredth
 // of that rounding (the gated block of 4096 columns by 4e-6: of its results one in 400
 // is rounded to the other neighbour).
-constexpr uint32_t kMmChunkLoss = 16, kMmChunkFew = 4, kMmChunkParts = 4, kMmChunkBf16 = 512;
+constexpr uint32_t kMmChunkLoss = 16, kMmChunkFew = 2, kMmChunkParts = 4, kMmChunkBf16 = 512;
 constexpr uint32_t kMmChunkMost = 1 << 16;  // some 20 ms, far below what a wait may take
 constexpr int kMmTileN = 256;
 constexpr int kMmDepth = 64;
