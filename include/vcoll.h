@@ -480,9 +480,12 @@ int vcoll_layer_norm_backward_checkpoint8(const void* grad, int64_t grad_ld, con
  *  - The *_workspace_bytes functions take `direct`: 1 where all the matrices
  *    that the products read (x, table, w_gate, w_up) lie so; 0 always suffices.
  *    The workspace is device memory.
- *  - The order of a sum is fixed by the sizes, the type, the GPU and, of 16 fp32
- *    rows or fewer, whether the weights' rows are whole 16-byte pieces.  A call
- *    repeated on the same buffers gives the same bits.
+ *  - The order of a sum is fixed by the sizes, the type, the results that are
+ *    wanted (dx with or without dtable), whether there is a base, whether the
+ *    matrices lie as `direct` says and, of 16 fp32 rows or fewer, whether the
+ *    weights' rows are whole 16-byte pieces.  A call repeated on the same
+ *    buffers gives the same bits; a call that differs in one of these may
+ *    differ in a result's last bits.
  */
 
 /*
@@ -542,7 +545,8 @@ int vcoll_gated_ff(const void* x, int64_t x_ld, const void* w_gate, int64_t w_ga
  * Its gradient from the kept gate and up: dgate = dh * up * act'(gate), dup =
  * dh * act(gate), dx = dgate * w_gate + dup * w_up, dw_gate = dgate^T * x,
  * dw_up = dup^T * x.  With bf16 operands dgate and dup are rounded to bf16 for
- * the products, or where N * F is 8192 or less to twice its bits.  dx, dw_gate and dw_up may each be NULL (not wanted).
+ * the products, or where N * F is 8192 or less to twice its bits.  dx, dw_gate
+ * and dw_up may each be NULL (not wanted).
  */
 size_t vcoll_gated_ff_backward_workspace_bytes(int64_t N, int64_t D, int64_t F, int dtype,
                                                int direct);
